@@ -15,4 +15,9 @@ from ._lib import (  # noqa: F401
     expert_linear64, expert_linear64_workspace_size,
     DecodeBuffers, alloc_decode_workspace, make_decode_args, text_decode_attention,
     text_decode_workspace_init, text_decode_workspace_size,
+    Mxfp4Cache, alloc_mxfp4_cache, Mxfp4Rows, make_rows_args, expert_attn_write_mxfp4, expert_attn_read_mxfp4,
+    DecodeMxfp4Buffers, alloc_decode_mxfp4_workspace, make_decode_mxfp4_args, text_decode_attention_mxfp4,
+    text_decode_mxfp4_workspace_size,
+    LayerMxfp4Buffers, alloc_mxfp4_workspace, make_mxfp4_args, expert_attn_layers_mxfp4,
+    expert_attn_mxfp4_workspace_size,
 )

@@ -39,6 +39,16 @@ class EaDecodeArgs(ctypes.Structure):
         "q_raw", "k_raw", "v_raw", "q_gamma", "k_gamma", "k_cache", "v_cache", "out")]
 
 
+class EaMxfp4Rows(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_codes", "k_scales", "v_codes", "v_scales")]
+
+
+class EaAttnMxfp4Args(ctypes.Structure):  # ea_decode_mxfp4_args and ea_layer_mxfp4_args
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "q_raw", "k_raw", "v_raw", "q_gamma", "k_gamma", "k_codes", "k_scales", "v_codes", "v_scales",
+        "out", "k_new", "v_new")]
+
+
 _lib_handle = None
 
 
@@ -51,6 +61,7 @@ def lib() -> ctypes.CDLL:
                                "`python -m gqa_attention_long_gb300.build` (needs nvcc 13)")
         h = ctypes.CDLL(LIB_PATH)
         P, I, S, V = ctypes.POINTER(EaLayerArgs), ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p
+        R, M, L = ctypes.POINTER(EaMxfp4Rows), ctypes.POINTER(EaAttnMxfp4Args), ctypes.c_int64
         sig = {
             "expert_attn_workspace_size": (S, [I, I, I]),
             "expert_attn_workspace_init": (I, [V, S, V]),
@@ -71,6 +82,12 @@ def lib() -> ctypes.CDLL:
             "text_decode_workspace_size": (S, [I]),
             "text_decode_workspace_init": (I, [V, S, V]),
             "text_decode_attention": (I, [ctypes.POINTER(EaDecodeArgs), I, I, I, I, V, S, V]),
+            "expert_attn_write_mxfp4": (I, [R, I, I, I, I, I, L, L, V]),
+            "expert_attn_read_mxfp4": (I, [R, I, I, I, I, I, L, L, V]),
+            "text_decode_mxfp4_workspace_size": (S, [I]),
+            "text_decode_attention_mxfp4": (I, [M, I, I, I, I, V, S, V]),
+            "expert_attn_mxfp4_workspace_size": (S, [I]),
+            "expert_attn_layers_mxfp4": (I, [M, I, I, I, I, V, S, V]),
         }
         for name, (res, args) in sig.items():
             f = getattr(h, name)
@@ -408,3 +425,203 @@ def text_decode_attention(layers: list[DecodeBuffers], pos: int, Smax: int, rope
     p, n = _ws(ws)
     _check("text_decode_attention", lib().text_decode_attention(arr, len(arr), int(pos), int(Smax),
                                                                 int(rope_delta), p, n, _stream(stream)))
+
+
+# ------------------------------------------------------------------------- 4-bit cache (MXFP4)
+@dataclass
+class Mxfp4Cache:
+    """One layer's 4-bit K and V caches (include/expert_attn.h): packed E2M1 codes and scale bytes."""
+    k_codes: torch.Tensor   # uint8 [8, Smax, 64]
+    k_scales: torch.Tensor  # uint8 [8, Smax, 4]
+    v_codes: torch.Tensor
+    v_scales: torch.Tensor
+
+
+def alloc_mxfp4_cache(Smax: int, device="cuda") -> Mxfp4Cache:
+    """A zero-filled 4-bit cache of Smax rows."""
+    z = lambda w: torch.zeros(8, Smax, w, dtype=torch.uint8, device=device)  # noqa: E731
+    return Mxfp4Cache(z(64), z(4), z(64), z(4))
+
+
+class _Arr:
+    """A marshalled argument array, the device its tensors are on, and (rows) their type and strides."""
+
+    def __init__(self, arr, device, dtype=None, strides=(0, 0), n_rows=0, Smax=0):
+        self.arr, self.n, self.device, self.dtype, self.strides = arr, len(arr), device, dtype, strides
+        self.n_rows, self.Smax = n_rows, Smax
+
+
+def _one_device(tensors, what: str) -> int:
+    devices = {t.device.index for t in tensors if t is not None}
+    if len(devices) != 1:
+        raise ValueError(f"{what}: all tensors must be on one device")
+    return devices.pop()
+
+
+def _current(a: _Arr, Smax: int, ws: torch.Tensor | None = None) -> None:
+    if a.device != torch.cuda.current_device() or (ws is not None and ws.device.index != a.device):
+        raise ValueError(f"the tensors are on cuda:{a.device}, which must be the current device (and the workspace's)")
+    if a.Smax != Smax:
+        raise ValueError(f"the arguments were made for caches of {a.Smax} rows, not {Smax}")
+
+
+def _mx_cache(a, c: Mxfp4Cache, Smax: int) -> None:
+    u8 = torch.uint8
+    a.k_codes, a.v_codes = _ptr(c.k_codes, "k_codes", u8, 8 * Smax * 64), _ptr(c.v_codes, "v_codes", u8, 8 * Smax * 64)
+    a.k_scales, a.v_scales = _ptr(c.k_scales, "k_scales", u8, 8 * Smax * 4), _ptr(c.v_scales, "v_scales", u8, 8 * Smax * 4)
+
+
+@dataclass
+class Mxfp4Rows:
+    """Rows of one layer's K and V beside the 4-bit cache they go to or come from."""
+    k: torch.Tensor  # [8, n, 128] bf16, fp16 or fp32; any head and row strides, channels contiguous
+    v: torch.Tensor  # the same shape, type and strides
+    cache: Mxfp4Cache
+
+
+_ROWS_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def make_rows_args(layers: list[Mxfp4Rows], Smax: int) -> _Arr:
+    """Marshalled arguments of expert_attn_write_mxfp4 and expert_attn_read_mxfp4."""
+    if not layers:
+        raise ValueError("no layers")
+    arr, first = (EaMxfp4Rows * len(layers))(), layers[0].k
+    for a, L in zip(arr, layers):
+        for name, t in (("k", L.k), ("v", L.v)):
+            if not isinstance(t, torch.Tensor) or not t.is_cuda:
+                raise TypeError(f"{name} must be a CUDA tensor")
+            if t.dtype not in _ROWS_DTYPES or t.dtype != first.dtype:
+                raise TypeError(f"{name} has dtype {t.dtype}: bf16, fp16 or fp32 is expected, the same in every layer")
+            if t.dim() != 3 or t.shape[0] != 8 or t.shape[2] != 128 or t.shape != first.shape:
+                raise ValueError(f"{name} has shape {tuple(t.shape)}: [8, rows, 128] is expected, the same in every layer")
+            if t.shape[1] and (t.stride(2) != 1 or t.stride(0) != first.stride(0) or
+                               (t.shape[1] > 1 and t.stride(1) != first.stride(1))):
+                raise ValueError(f"{name} has strides {t.stride()}: contiguous channels and the same strides in every "
+                                 "layer are expected")
+        a.k, a.v = L.k.data_ptr(), L.v.data_ptr()
+        _mx_cache(a, L.cache, Smax)
+    dev = _one_device([t for L in layers for t in (L.k, L.v, *L.cache.__dict__.values())], "rows")
+    return _Arr(arr, dev, _ROWS_DTYPES[first.dtype], (first.stride(0), first.stride(1)), first.shape[1], Smax)
+
+
+def _rows_call(fn: str, layers, row0: int, n_rows: int, Smax: int, stream, a: _Arr | None) -> None:
+    a = a if a is not None else make_rows_args(layers, Smax)
+    _current(a, Smax)
+    if n_rows > a.n_rows:
+        raise ValueError(f"k and v have {a.n_rows} rows, {n_rows} are asked for")
+    if n_rows == 0:
+        return
+    _check(fn, getattr(lib(), fn)(a.arr, a.n, int(row0), int(n_rows), int(Smax), a.dtype, a.strides[0], a.strides[1],
+                                  _stream(stream)))
+
+
+def expert_attn_write_mxfp4(layers: list[Mxfp4Rows], row0: int, n_rows: int, Smax: int, stream=None, _arr=None) -> None:
+    """Quantises the first n_rows rows of every layer's k and v into its cache's rows [row0, row0 + n_rows)."""
+    _rows_call("expert_attn_write_mxfp4", layers, row0, n_rows, Smax, stream, _arr)
+
+
+def expert_attn_read_mxfp4(layers: list[Mxfp4Rows], row0: int, n_rows: int, Smax: int, stream=None, _arr=None) -> None:
+    """Fills the first n_rows rows of every layer's k and v with the values of its cache's rows [row0, row0 + n_rows)."""
+    _rows_call("expert_attn_read_mxfp4", layers, row0, n_rows, Smax, stream, _arr)
+
+
+@dataclass
+class DecodeMxfp4Buffers:
+    """One layer's device tensors for text_decode_attention_mxfp4 (include/expert_attn.h)."""
+    q_raw: torch.Tensor    # bf16 [64, 128]
+    k_raw: torch.Tensor    # bf16 [8, 128]
+    v_raw: torch.Tensor    # bf16 [8, 128]
+    q_gamma: torch.Tensor  # bf16 [128]
+    k_gamma: torch.Tensor  # bf16 [128]
+    cache: Mxfp4Cache
+    out: torch.Tensor      # bf16 [64, 128]
+    k_new: torch.Tensor | None = None  # optional bf16 [8, 128]: the new row's stored values
+    v_new: torch.Tensor | None = None
+
+
+@dataclass
+class LayerMxfp4Buffers:
+    """One layer's device tensors for expert_attn_layers_mxfp4 (include/expert_attn.h)."""
+    q_raw: torch.Tensor    # bf16 [16, 64, 128]
+    k_raw: torch.Tensor    # bf16 [8, 64, 128]
+    v_raw: torch.Tensor    # bf16 [8, 64, 128]
+    q_gamma: torch.Tensor  # bf16 [128]
+    k_gamma: torch.Tensor  # bf16 [128]
+    cache: Mxfp4Cache
+    out: torch.Tensor      # bf16 [16, 64, 128]
+    k_new: torch.Tensor | None = None  # optional bf16 [8, 64, 128]: the own rows' stored values
+    v_new: torch.Tensor | None = None
+
+
+def _mx_attn_args(layers, Smax: int, hq: int, tok: int) -> _Arr:
+    if not layers:
+        raise ValueError("no layers")
+    arr, bf = (EaAttnMxfp4Args * len(layers))(), torch.bfloat16
+    for a, L in zip(arr, layers):
+        for name, n in (("q_raw", hq * tok), ("k_raw", 8 * tok), ("v_raw", 8 * tok), ("q_gamma", 1), ("k_gamma", 1),
+                        ("out", hq * tok), ("k_new", 8 * tok), ("v_new", 8 * tok)):
+            setattr(a, name, _ptr(getattr(L, name), name, bf, n * 128))
+        _mx_cache(a, L.cache, Smax)
+    dev = _one_device([t for L in layers for t in (L.q_raw, L.k_raw, L.v_raw, L.q_gamma, L.k_gamma, L.out, L.k_new, L.v_new,
+                                                   *L.cache.__dict__.values())], "layers")
+    return _Arr(arr, dev, Smax=Smax)
+
+
+def make_decode_mxfp4_args(layers: list[DecodeMxfp4Buffers], Smax: int) -> _Arr:
+    """Marshalled arguments of text_decode_attention_mxfp4, for loops that call it often."""
+    return _mx_attn_args(layers, Smax, 64, 1)
+
+
+def make_mxfp4_args(layers: list[LayerMxfp4Buffers], Smax: int) -> _Arr:
+    """Marshalled arguments of expert_attn_layers_mxfp4, for loops that call it often."""
+    return _mx_attn_args(layers, Smax, 16, 64)
+
+
+def text_decode_mxfp4_workspace_size(n_layers: int) -> int:
+    return int(lib().text_decode_mxfp4_workspace_size(int(n_layers)))
+
+
+def expert_attn_mxfp4_workspace_size(n_layers: int) -> int:
+    return int(lib().expert_attn_mxfp4_workspace_size(int(n_layers)))
+
+
+def _mx_workspace(n: int, what: str, init, device) -> torch.Tensor:
+    if n == 0:
+        raise RuntimeError(f"{what} returned 0: no sm_103 GPU available")
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    init(ws)
+    return ws
+
+
+def alloc_decode_mxfp4_workspace(n_layers: int, device="cuda") -> torch.Tensor:
+    """A cleared workspace for text_decode_attention_mxfp4 (torch-allocated)."""
+    return _mx_workspace(text_decode_mxfp4_workspace_size(n_layers), "text_decode_mxfp4_workspace_size",
+                         text_decode_workspace_init, device)
+
+
+def alloc_mxfp4_workspace(n_layers: int, device="cuda") -> torch.Tensor:
+    """A cleared workspace for expert_attn_layers_mxfp4 (torch-allocated)."""
+    return _mx_workspace(expert_attn_mxfp4_workspace_size(n_layers), "expert_attn_mxfp4_workspace_size",
+                         expert_attn_workspace_init, device)
+
+
+def text_decode_attention_mxfp4(layers: list[DecodeMxfp4Buffers], pos: int, Smax: int, rope_delta: int, ws: torch.Tensor,
+                                stream=None, _arr=None) -> None:
+    """One decode step over 4-bit caches: the new row quantised into row pos, then attention over rows [0, pos]."""
+    a = _arr if _arr is not None else make_decode_mxfp4_args(layers, Smax)
+    _current(a, Smax, ws)
+    p, n = _ws(ws)
+    _check("text_decode_attention_mxfp4", lib().text_decode_attention_mxfp4(
+        a.arr, a.n, int(pos), int(Smax), int(rope_delta), p, n, _stream(stream)))
+
+
+def expert_attn_layers_mxfp4(layers: list[LayerMxfp4Buffers], S: int, Smax: int, rope_delta: int, ws: torch.Tensor,
+                             stream=None, _arr=None) -> None:
+    """The expert's attention over 4-bit caches: the own rows quantised into rows [Smax-64, Smax), then attention
+    over rows [0, S) and the own rows."""
+    a = _arr if _arr is not None else make_mxfp4_args(layers, Smax)
+    _current(a, Smax, ws)
+    p, n = _ws(ws)
+    _check("expert_attn_layers_mxfp4", lib().expert_attn_layers_mxfp4(
+        a.arr, a.n, int(S), int(Smax), int(rope_delta), p, n, _stream(stream)))

@@ -1092,3 +1092,223 @@ int text_decode_attention(const ea_decode_args* layers, int n_layers, int pos, i
 }
 
 }  // extern "C"
+
+// ------------------------------------------------------------------------------ 4-bit cache
+// Host side of the 4-bit cache's writer, reader and attentions.
+namespace ea {
+cudaError_t launch_mxfp4_rows(const MxRowsParams& p, int n_layers, int dtype, bool write, cudaLaunchConfig_t cfg);
+cudaError_t launch_mxfp4_attention(const MxAttnParams& p, int n_layers, cudaLaunchConfig_t cfg);
+}  // namespace ea
+
+namespace {
+
+int validate_mx_cache(const void* kc, const void* ks, const void* vc, const void* vs) {
+  const void* req[] = {kc, ks, vc, vs};
+  for (const void* p : req) {
+    if (p == nullptr) return EA_ERR_INVALID_ARG;
+    if (!aligned16(p)) return EA_ERR_MISALIGNED;
+  }
+  return EA_OK;
+}
+
+// No two of the caches that one call writes may be the same: their rows would be written twice.
+template <class A>
+bool mx_caches_distinct(const A* a, int n) {
+  for (int i = 0; i < n; ++i) {
+    if (a[i].k_codes == a[i].v_codes) return false;
+    for (int j = 0; j < i; ++j)
+      if (a[i].k_codes == a[j].k_codes || a[i].v_codes == a[j].v_codes || a[i].k_codes == a[j].v_codes ||
+          a[i].v_codes == a[j].k_codes)
+        return false;
+  }
+  return true;
+}
+
+int run_mx_rows(const ea_mxfp4_rows* a, int n_layers, int row0, int n_rows, int Smax, int dtype,
+                int64_t head_stride, int64_t row_stride, bool write, ea_stream_t stream) {
+  if (a == nullptr || n_layers < 1) return EA_ERR_INVALID_ARG;
+  if (Smax < 1 || Smax > (1 << 22) || row0 < 0 || n_rows < 0 || n_rows > Smax - row0) return EA_ERR_INVALID_ARG;
+  if (dtype != EA_ROWS_BF16 && dtype != EA_ROWS_FP16 && dtype != EA_ROWS_FP32) return EA_ERR_INVALID_ARG;
+  constexpr int64_t kMaxStride = 1LL << 40;
+  if (head_stride < 0 || row_stride < 0 || head_stride > kMaxStride || row_stride > kMaxStride) return EA_ERR_INVALID_ARG;
+  const int64_t esz = dtype == EA_ROWS_FP32 ? 4 : 2;
+  if (head_stride * esz % 16 != 0 || (n_rows > 1 && row_stride * esz % 16 != 0)) return EA_ERR_MISALIGNED;
+  // rows that are written must not overlap
+  if (!write && (head_stride < kD || (n_rows > 1 && (row_stride < kD || (head_stride < (n_rows - 1) * row_stride + kD &&
+                                                                        row_stride < (kHkv - 1) * head_stride + kD)))))
+    return EA_ERR_INVALID_ARG;
+  for (int l = 0; l < n_layers; ++l) {
+    if (a[l].k == nullptr || a[l].v == nullptr) return EA_ERR_INVALID_ARG;
+    if (!aligned16(a[l].k) || !aligned16(a[l].v)) return EA_ERR_MISALIGNED;
+    const int rc = validate_mx_cache(a[l].k_codes, a[l].k_scales, a[l].v_codes, a[l].v_scales);
+    if (rc != EA_OK) return rc;
+  }
+  if (write && !mx_caches_distinct(a, n_layers)) return EA_ERR_INVALID_ARG;
+  int dev;
+  DeviceInfo di;
+  if (!device_info(&dev, &di)) return EA_ERR_UNSUPPORTED;
+  if (n_rows == 0) return EA_OK;
+  MxRowsParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.head_stride = head_stride;
+  p.row_stride = n_rows > 1 ? row_stride : 0;
+  p.row0 = row0;
+  p.n_rows = n_rows;
+  p.Smax = Smax;
+  cudaLaunchAttribute attr[1];
+  for (int l0 = 0; l0 < n_layers; l0 += kMaxLayersPerLaunch) {
+    const int n = n_layers - l0 < kMaxLayersPerLaunch ? n_layers - l0 : kMaxLayersPerLaunch;
+    for (int l = 0; l < n; ++l) {
+      const ea_mxfp4_rows& x = a[l0 + l];
+      p.layer[l] = {x.k, x.v, static_cast<uint8_t*>(x.k_codes), static_cast<uint8_t*>(x.k_scales),
+                    static_cast<uint8_t*>(x.v_codes), static_cast<uint8_t*>(x.v_scales)};
+    }
+    if (launch_mxfp4_rows(p, n, dtype, write, launch_config(static_cast<cudaStream_t>(stream), attr, true)) !=
+        cudaSuccess) {
+      cudaGetLastError();
+      return EA_ERR_CUDA;
+    }
+  }
+  return EA_OK;
+}
+
+// Rotations of positions p0 + t, t < 64 (see MxAttnParams): rot_a[i] at p0 + 8 i, rot_b[i] at i, in
+// 64 bits (a far position's angle needs them), split into fp32 pairs. The angles of i and 8 i are
+// formed once per process.
+void mx_rotations(long long p0, int tok, MxAttnParams* p) {
+  struct Steps {
+    double f[kD / 2], c8[kTok / 8][kD / 2], s8[kTok / 8][kD / 2];
+    float4 b[8][kD / 2];
+  };
+  static Steps st;
+  static std::once_flag once;
+  auto split = [](double c, double s) {
+    const float ch = static_cast<float>(c), sh = static_cast<float>(s);
+    return make_float4(ch, static_cast<float>(c - ch), sh, static_cast<float>(s - sh));
+  };
+  std::call_once(once, [&] {
+    for (int j = 0; j < kD / 2; ++j) {
+      st.f[j] = std::pow(5.0e6, -static_cast<double>(j) / (kD / 2));
+      for (int i = 0; i < 8; ++i) {
+        st.c8[i][j] = std::cos(8 * i * st.f[j]);
+        st.s8[i][j] = std::sin(8 * i * st.f[j]);
+        st.b[i][j] = split(std::cos(i * st.f[j]), std::sin(i * st.f[j]));
+      }
+    }
+  });
+  for (int j = 0; j < kD / 2; ++j) {
+    const double a = static_cast<double>(p0) * st.f[j], c = std::cos(a), s = std::sin(a);
+    for (int i = 0; 8 * i < tok; ++i)
+      p->rot_a[i][j] = split(c * st.c8[i][j] - s * st.s8[i][j], s * st.c8[i][j] + c * st.s8[i][j]);
+  }
+  std::memcpy(p->rot_b, st.b, sizeof(st.b));
+}
+
+template <class A>
+int validate_mx_attn(const A* a, int n_layers, long long p0, int tok, const void* ws) {
+  if (a == nullptr || n_layers < 1 || ws == nullptr) return EA_ERR_INVALID_ARG;
+  if (p0 <= -(1LL << 24) || p0 + tok >= (1LL << 24)) return EA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return EA_ERR_MISALIGNED;
+  for (int l = 0; l < n_layers; ++l) {
+    const A& x = a[l];
+    const void* req[] = {x.q_raw, x.k_raw, x.v_raw, x.q_gamma, x.k_gamma, x.out};
+    for (const void* q : req) {
+      if (q == nullptr) return EA_ERR_INVALID_ARG;
+      if (!aligned16(q)) return EA_ERR_MISALIGNED;
+    }
+    if (!aligned16(x.k_new) || !aligned16(x.v_new)) return EA_ERR_MISALIGNED;  // (null is aligned)
+    const int rc = validate_mx_cache(x.k_codes, x.k_scales, x.v_codes, x.v_scales);
+    if (rc != EA_OK) return rc;
+  }
+  return mx_caches_distinct(a, n_layers) ? EA_OK : EA_ERR_INVALID_ARG;
+}
+
+size_t mx_ws_bytes(int n_layers, int rq) {
+  const int per = n_layers < kMaxLayersPerLaunch ? n_layers : kMaxLayersPerLaunch;
+  return 1024 + static_cast<size_t>(per) * kHkv * rq * kD * sizeof(float);
+}
+
+template <class A>
+int run_mx_attn(const A* a, int n_layers, int rep, int tok, int first, int new_row0, int Smax, long long p0,
+                void* workspace, size_t ws_bytes, ea_stream_t stream) {
+  int dev;
+  DeviceInfo di;
+  if (!device_info(&dev, &di)) return EA_ERR_UNSUPPORTED;
+  if (ws_bytes < mx_ws_bytes(n_layers, rep * tok)) return EA_ERR_WORKSPACE;
+  MxAttnParams p;
+  std::memset(&p, 0, sizeof(p));
+  mx_rotations(p0, tok, &p);
+  p.status = static_cast<uint32_t*>(workspace);
+  p.q_ws = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 1024);
+  p.rep = rep;
+  p.tok = tok;
+  p.first = first;
+  p.new_row0 = new_row0;
+  p.Smax = Smax;
+  p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(kD)));
+  cudaLaunchAttribute attr[1];
+  for (int l0 = 0; l0 < n_layers; l0 += kMaxLayersPerLaunch) {
+    const int n = n_layers - l0 < kMaxLayersPerLaunch ? n_layers - l0 : kMaxLayersPerLaunch;
+    for (int l = 0; l < n; ++l) {
+      const A& x = a[l0 + l];
+      auto bf = [](const void* q) { return static_cast<const __nv_bfloat16*>(q); };
+      auto u8 = [](void* q) { return static_cast<uint8_t*>(q); };
+      p.layer[l] = {bf(x.q_raw), bf(x.k_raw), bf(x.v_raw), bf(x.q_gamma), bf(x.k_gamma), u8(x.k_codes),
+                    u8(x.k_scales), u8(x.v_codes), u8(x.v_scales), static_cast<__nv_bfloat16*>(x.out),
+                    static_cast<__nv_bfloat16*>(x.k_new), static_cast<__nv_bfloat16*>(x.v_new)};
+    }
+    if (launch_mxfp4_attention(p, n, launch_config(static_cast<cudaStream_t>(stream), attr, true)) != cudaSuccess) {
+      cudaGetLastError();
+      return EA_ERR_CUDA;
+    }
+  }
+  return EA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int expert_attn_write_mxfp4(const ea_mxfp4_rows* layers, int n_layers, int row0, int n_rows, int Smax, int dtype,
+                            int64_t head_stride, int64_t row_stride, ea_stream_t stream) {
+  return run_mx_rows(layers, n_layers, row0, n_rows, Smax, dtype, head_stride, row_stride, true, stream);
+}
+
+int expert_attn_read_mxfp4(const ea_mxfp4_rows* layers, int n_layers, int row0, int n_rows, int Smax, int dtype,
+                           int64_t head_stride, int64_t row_stride, ea_stream_t stream) {
+  return run_mx_rows(layers, n_layers, row0, n_rows, Smax, dtype, head_stride, row_stride, false, stream);
+}
+
+size_t text_decode_mxfp4_workspace_size(int n_layers) {
+  int dev;
+  DeviceInfo di;
+  if (n_layers < 1 || !device_info(&dev, &di)) return 0;
+  return mx_ws_bytes(n_layers, kRepText);
+}
+
+int text_decode_attention_mxfp4(const ea_decode_mxfp4_args* layers, int n_layers, int pos, int Smax, int rope_delta,
+                                void* workspace, size_t ws_bytes, ea_stream_t stream) {
+  const long long p0 = static_cast<long long>(pos) + rope_delta;
+  if (Smax < kKeyTile || Smax % kTok != 0 || Smax > (1 << 22) || pos < 0 || pos >= Smax) return EA_ERR_INVALID_ARG;
+  const int rc = validate_mx_attn(layers, n_layers, p0, 1, workspace);
+  if (rc != EA_OK) return rc;
+  return run_mx_attn(layers, n_layers, kRepText, 1, pos, pos, Smax, p0, workspace, ws_bytes, stream);
+}
+
+size_t expert_attn_mxfp4_workspace_size(int n_layers) {
+  int dev;
+  DeviceInfo di;
+  if (n_layers < 1 || !device_info(&dev, &di)) return 0;
+  return mx_ws_bytes(n_layers, kRows);
+}
+
+int expert_attn_layers_mxfp4(const ea_layer_mxfp4_args* layers, int n_layers, int S, int Smax, int rope_delta,
+                             void* workspace, size_t ws_bytes, ea_stream_t stream) {
+  const long long p0 = static_cast<long long>(S) + rope_delta;
+  if (Smax < 2 * kTok || Smax % kTok != 0 || Smax > (1 << 22) || S < 0 || S > Smax - kTok) return EA_ERR_INVALID_ARG;
+  const int rc = validate_mx_attn(layers, n_layers, p0, kTok, workspace);
+  if (rc != EA_OK) return rc;
+  return run_mx_attn(layers, n_layers, kHq / kHkv, kTok, S, Smax - kTok, Smax, p0, workspace, ws_bytes, stream);
+}
+
+}  // extern "C"

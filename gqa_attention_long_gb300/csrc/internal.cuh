@@ -231,6 +231,50 @@ constexpr DecodeWs decode_ws_layout(int n_layers, int max_ctas) {
   return w;
 }
 
+// ------------------------------------------------------------------------------ 4-bit cache
+// Rows of K and V moved into or out of a 4-bit cache (one launch: <= 64 layers).
+struct MxRowsLayer {
+  void* k;      // rows [8][n_rows][128] with the launch's strides
+  void* v;
+  uint8_t* kc;  // codes [8][Smax][64], scales [8][Smax][4]
+  uint8_t* ks;
+  uint8_t* vc;
+  uint8_t* vs;
+};
+struct MxRowsParams {
+  MxRowsLayer layer[kMaxLayersPerLaunch];
+  long long head_stride, row_stride;  // of k and v, in elements
+  int row0, n_rows, Smax;
+};
+
+// Attention over 4-bit caches: the rep * tok query rows of a (layer, kv head) unit against cache rows
+// [0, first) and the tok new rows, which sit in cache rows [new_row0, new_row0 + tok).
+struct MxAttnLayer {
+  const __nv_bfloat16* q_raw;  // [8 * rep][tok][128]
+  const __nv_bfloat16* k_raw;  // [8][tok][128]
+  const __nv_bfloat16* v_raw;
+  const __nv_bfloat16* q_gamma;
+  const __nv_bfloat16* k_gamma;
+  uint8_t* kc;
+  uint8_t* ks;
+  uint8_t* vc;
+  uint8_t* vs;
+  __nv_bfloat16* out;    // [8 * rep][tok][128]
+  __nv_bfloat16* k_new;  // optional: the new rows' values as stored, [8][tok][128]
+  __nv_bfloat16* v_new;
+};
+struct MxAttnParams {
+  MxAttnLayer layer[kMaxLayersPerLaunch];
+  // rotations by position: token t sits at angle(rot_a[t / 8]) + angle(rot_b[t % 8]); each entry is
+  // the cosine (x + y) and the sine (z + w) as fp32 pairs, by frequency
+  float4 rot_a[kTok / 8][kD / 2];
+  float4 rot_b[8][kD / 2];
+  float* q_ws;  // [unit][rep * tok][128]
+  uint32_t* status;
+  int rep, tok, first, new_row0, Smax;
+  float scale_log2;  // log2(e) / sqrt(128)
+};
+
 // ------------------------------------------------------------ decoder-layer projections
 constexpr int kMaxHidden = 8192;   // widest residual stream of the decoder layer
 constexpr int kMaxInter = 32768;

@@ -1,0 +1,164 @@
+// mxfp4.cuh — the 4-bit cache format on the device: E2M1 codes (two to a byte, the lower channel in
+// the low nibble) with one power-of-two scale byte e + 127 per 32 channels of a row, its encoder
+// and decoder, and the norm and rotation of a k row that is about to be encoded.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "internal.cuh"
+#include "ptx.cuh"
+
+namespace ea {
+
+constexpr int kMxRowBytes = kD / 2;    // codes of one row
+constexpr int kMxRowScales = kD / 32;  // scale bytes of one row: one 32-bit word
+
+// ------------------------------------------------------------------------------- encoder
+// e = floor(log2(amax)) - 2, clamped to [-127, 127]; 0 for amax = 0, 127 for an infinite amax.
+__device__ __forceinline__ int mx_exponent(float amax) {
+  const int f = static_cast<int>(__float_as_uint(amax) >> 23);
+  return amax == 0.f ? 0 : f == 255 ? 127 : max(f - 129, -127);
+}
+// 2^e for e in [-127, 127] (2^-127 is a subnormal).
+__device__ __forceinline__ float mx_pow2(int e) {
+  return __uint_as_float(e == -127 ? 0x00400000u : static_cast<uint32_t>(e + 127) << 23);
+}
+// Eight values times inv = 2^-e, as E2M1 codes: nearest, ties to the even code, saturating at 6;
+// the product is exact, and a NaN becomes a zero of its sign.
+__device__ __forceinline__ uint32_t mx_pack8(const float (&x)[8], float inv) {
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = x[i] == x[i] ? x[i] * inv : copysignf(0.f, x[i]);
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(r)
+      : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
+  return r;
+}
+
+// ------------------------------------------------------------------------------- decoder
+// What a scale byte stands for: 2^(b - 127), NaN for 255 (which no encoder here writes).
+__device__ __forceinline__ float mx_scale(uint32_t b) {
+  return __uint_as_float(b == 0 ? 0x00400000u : b == 255 ? 0x7FC00000u : b << 23);
+}
+// Eight codes -> four f16 pairs (exact), channels in order.
+__device__ __forceinline__ void mx_unpack8(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+__device__ __forceinline__ void mx_values8(uint32_t w, float scale, float (&x)[8]) {
+  uint32_t h[4];
+  mx_unpack8(w, h);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = unpack_f16x2(h[i]);
+    x[2 * i] = f.x * scale;
+    x[2 * i + 1] = f.y * scale;
+  }
+}
+
+// --------------------------------------------------- norm and rotation in pairs of fp32 numbers
+// A k row is normed, rotated, rounded to fp32 and encoded. The encoder has borders (2.5 -> 2, just
+// above -> 3), so a row that is off in its last fp32 bits can land on another code than the
+// formula's. It is therefore formed as unevaluated sums h + l of two fp32 numbers (about 2^-45
+// relative), at fp32 rates; FP64 arithmetic, 1/60 of the fp32 rate here, would bound the kernel.
+struct Pair {
+  float h, l;
+};
+__device__ __forceinline__ Pair pair_fast_sum(float a, float b) {  // |a| >= |b| or a = 0
+  const float s = __fadd_rn(a, b);
+  return {s, __fadd_rn(b, -__fadd_rn(s, -a))};
+}
+__device__ __forceinline__ Pair pair_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), bb = __fadd_rn(s, -a);
+  return {s, __fadd_rn(__fadd_rn(a, -__fadd_rn(s, -bb)), __fadd_rn(b, -bb))};
+}
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
+  const Pair s = pair_sum(a.h, b.h);
+  return pair_fast_sum(s.h, __fadd_rn(s.l, __fadd_rn(a.l, b.l)));
+}
+__device__ __forceinline__ Pair operator-(Pair a) { return {-a.h, -a.l}; }
+__device__ __forceinline__ Pair operator*(Pair a, float b) {
+  const float p = __fmul_rn(a.h, b);
+  return pair_fast_sum(p, __fmaf_rn(a.l, b, __fmaf_rn(a.h, b, -p)));
+}
+__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
+  const float p = __fmul_rn(a.h, b.h);
+  return pair_fast_sum(p, __fmaf_rn(a.h, b.l, __fmaf_rn(a.l, b.h, __fmaf_rn(a.h, b.h, -p))));
+}
+
+// 1 / sqrt(mean of the row's 128 squares + 1e-6), the row held by an octet as in norm_rope
+// (lane i: channels [8i, 8i+8) and [64+8i, 64+8i+8)). A square of a bf16 number is exact in fp32.
+__device__ __forceinline__ Pair pair_inv_rms(const float (&xl)[8], const float (&xh)[8]) {
+  Pair ss = {0.f, 0.f};
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    ss = ss + Pair{__fmul_rn(xl[e], xl[e]), 0.f};
+    ss = ss + Pair{__fmul_rn(xh[e], xh[e]), 0.f};
+  }
+#pragma unroll
+  for (int m = 4; m >= 1; m >>= 1)
+    ss = ss + Pair{__shfl_xor_sync(0xffffffffu, ss.h, m), __shfl_xor_sync(0xffffffffu, ss.l, m)};
+  constexpr double kEps = 1e-6;
+  constexpr float kEpsHi = static_cast<float>(kEps), kEpsLo = static_cast<float>(kEps - kEpsHi);
+  const Pair m = Pair{ss.h * (1.0f / kD), ss.l * (1.0f / kD)} + Pair{kEpsHi, kEpsLo};
+  // one Newton step from the hardware estimate r: r (1 + e/2 + 3 e^2 / 8), e = 1 - m r^2
+  const float r = rsqrtf(m.h);
+  const Pair u = m * (Pair{r, 0.f} * r);
+  const float e = __fadd_rn(__fadd_rn(1.0f, -u.h), -u.l);
+  return pair_fast_sum(r, r * fmaf(0.375f * e, e, 0.5f * e));
+}
+
+// The normed, rotated row rounded to fp32: channels as in norm_rope; cs and sn are the eight angles'
+// cosines and sines.
+__device__ __forceinline__ void pair_norm_rope(const float (&xl)[8], const float (&xh)[8], const float (&gl)[8],
+                                               const float (&gh)[8], const Pair (&cs)[8], const Pair (&sn)[8],
+                                               float (&yl)[8], float (&yh)[8]) {
+  const Pair rs = pair_inv_rms(xl, xh);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float nl = __fmul_rn(xl[e], gl[e]), nh = __fmul_rn(xh[e], gh[e]);  // exact: 8 + 8 bits
+    yl[e] = ((cs[e] * nl + -(sn[e] * nh)) * rs).h;
+    yh[e] = ((cs[e] * nh + sn[e] * nl) * rs).h;
+  }
+}
+
+// Encodes a row held by an octet (lane i: channels [8i, 8i+8) in xl and [64+8i, ..) in xh): each
+// lane's two words of codes, and the four scale bytes of the row (the same in every lane).
+__device__ __forceinline__ void mx_encode_octet(const float (&xl)[8], const float (&xh)[8], uint32_t& cl,
+                                                uint32_t& ch, uint32_t& scales, int& el, int& eh) {
+  float al = 0.f, ah = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    al = fmaxf(al, fabsf(xl[e]));
+    ah = fmaxf(ah, fabsf(xh[e]));
+  }
+#pragma unroll
+  for (int m = 2; m >= 1; m >>= 1) {  // lanes 4 j .. 4 j + 3 of an octet hold block j and block 2 + j
+    al = fmaxf(al, __shfl_xor_sync(0xffffffffu, al, m));
+    ah = fmaxf(ah, __shfl_xor_sync(0xffffffffu, ah, m));
+  }
+  el = mx_exponent(al);
+  eh = mx_exponent(ah);
+  cl = mx_pack8(xl, mx_pow2(-el));
+  ch = mx_pack8(xh, mx_pow2(-eh));
+  const uint32_t mine = static_cast<uint32_t>(el + 127) | static_cast<uint32_t>(eh + 127) << 16;
+  const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 4);
+  const bool low = (threadIdx.x & 4) == 0;
+  scales = (low ? mine : other) | (low ? other : mine) << 8;
+}
+
+}  // namespace ea

@@ -302,6 +302,98 @@ int text_decode_workspace_init(void* workspace, size_t ws_bytes, ea_stream_t str
 int text_decode_attention(const ea_decode_args* layers, int n_layers, int pos, int Smax,
                           int rope_delta, void* workspace, size_t ws_bytes, ea_stream_t stream);
 
+/* ------------------------------------------------------------------------ 4-bit cache (MXFP4)
+ * A layer's K and V caches in the format of expert_attn_quantize_cache_mxfp4: codes uint8
+ * [8][Smax][64] and scales uint8 [8][Smax][4] each, 16-byte aligned; a row's value is
+ * code * 2^(scale - 127). The functions below write rows into such caches, read them back and
+ * attend over them. A scale byte of 255 stands for NaN: none of the library's writers stores one,
+ * and an attention that meets one in a row it reads gives undefined output.
+ * Asynchrony, ownership and errors are those of the functions above. The caches that one call
+ * writes must be distinct (else EA_ERR_INVALID_ARG). */
+
+/* The type of rows outside the cache. */
+typedef enum { EA_ROWS_BF16 = 0, EA_ROWS_FP16 = 1, EA_ROWS_FP32 = 2 } ea_rows_dtype;
+
+typedef struct {
+  void* k;        /* rows of K: element (head g, row r, channel d) at g head_stride + r row_stride + d */
+  void* v;        /* rows of V, the same strides */
+  void* k_codes;
+  void* k_scales;
+  void* v_codes;
+  void* v_scales;
+} ea_mxfp4_rows;
+
+/* Quantises n_rows rows of K and V of n_layers layers into cache rows [row0, row0 + n_rows) (layers:
+ * a HOST array). Every row has its own scales, so the other rows stay as they are. Codes and scales are
+ * those of expert_attn_quantize_cache_mxfp4 (bit for bit for bf16 rows); an infinity becomes +-6 with
+ * scale 2^127 for its block, a NaN a zero of its sign.
+ * k and v of the layers share one dtype (ea_rows_dtype) and the strides, in elements: head_stride and
+ * row_stride in [0, 2^40], each a multiple of 16 bytes (row_stride is not looked at for n_rows <= 1).
+ * k and v are 16-byte aligned. Requires 0 <= row0, 0 <= n_rows <= Smax - row0, 1 <= Smax <= 2^22.
+ * One launch per 64 layers. */
+int expert_attn_write_mxfp4(const ea_mxfp4_rows* layers, int n_layers, int row0, int n_rows, int Smax, int dtype,
+                            int64_t head_stride, int64_t row_stride, ea_stream_t stream);
+
+/* The reverse: k and v receive the values of cache rows [row0, row0 + n_rows), exactly in bf16 and fp32
+ * (up to overflow to infinity above the type's range), rounded to nearest in fp16. The caches are not
+ * written. The rows of k and v must not overlap (else EA_ERR_INVALID_ARG); the rest as above. */
+int expert_attn_read_mxfp4(const ea_mxfp4_rows* layers, int n_layers, int row0, int n_rows, int Smax, int dtype,
+                           int64_t head_stride, int64_t row_stride, ea_stream_t stream);
+
+/* text_decode_attention over 4-bit caches: the same step, with the new row stored in 4 bits:
+ * the roped k, rounded to fp32, and the raw v are quantised into cache row pos, and every query head
+ * attends to the stored values of rows [0, pos]. Rows after pos are never used and stay as they are.
+ * q_raw bf16 [64][128], k_raw and v_raw bf16 [8][128], gains bf16 [128], out bf16 [64][128]; k_new and
+ * v_new, if not NULL, bf16 [8][128], receive the new row's stored values. All pointers 16-byte aligned.
+ * 0 <= pos < Smax; Smax a multiple of 64, 128 <= Smax <= 2^22; |pos + rope_delta| < 2^24. */
+typedef struct {
+  const void* q_raw;
+  const void* k_raw;
+  const void* v_raw;
+  const void* q_gamma;
+  const void* k_gamma;
+  void* k_codes;
+  void* k_scales;
+  void* v_codes;
+  void* v_scales;
+  void* out;
+  void* k_new; /* optional */
+  void* v_new; /* optional */
+} ea_decode_mxfp4_args;
+
+/* Bytes of workspace for a call over n_layers layers on the current device (0 without a suitable one):
+ * 256-byte aligned, cleared once with text_decode_workspace_init, not shared by calls that overlap;
+ * expert_attn_read_status reads its status word. */
+size_t text_decode_mxfp4_workspace_size(int n_layers);
+int text_decode_attention_mxfp4(const ea_decode_mxfp4_args* layers, int n_layers, int pos, int Smax, int rope_delta,
+                                void* workspace, size_t ws_bytes, ea_stream_t stream);
+
+/* expert_attn_layers over 4-bit caches: the 64 own k rows (normed, roped, rounded to fp32) and raw v rows
+ * are quantised into cache rows [Smax-64, Smax), and every token attends to the stored values of rows
+ * [0, S) and of the own rows. Rows [S, Smax-64) are never used and stay as they are. q_raw bf16
+ * [16][64][128], k_raw and v_raw bf16 [8][64][128], out bf16 [16][64][128]; k_new and v_new, if not NULL,
+ * bf16 [8][64][128], receive the own rows' stored values. 0 <= S <= Smax-64, Smax a multiple of 64,
+ * 128 <= Smax <= 2^22; |S + rope_delta| + 64 < 2^24. */
+typedef struct {
+  const void* q_raw;
+  const void* k_raw;
+  const void* v_raw;
+  const void* q_gamma;
+  const void* k_gamma;
+  void* k_codes;
+  void* k_scales;
+  void* v_codes;
+  void* v_scales;
+  void* out;
+  void* k_new; /* optional */
+  void* v_new; /* optional */
+} ea_layer_mxfp4_args;
+
+/* Workspace as for the decode step above, cleared once with expert_attn_workspace_init. */
+size_t expert_attn_mxfp4_workspace_size(int n_layers);
+int expert_attn_layers_mxfp4(const ea_layer_mxfp4_args* layers, int n_layers, int S, int Smax, int rope_delta,
+                             void* workspace, size_t ws_bytes, ea_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
