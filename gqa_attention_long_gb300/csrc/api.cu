@@ -1098,6 +1098,8 @@ int text_decode_attention(const ea_decode_args* layers, int n_layers, int pos, i
 namespace ea {
 cudaError_t launch_mxfp4_rows(const MxRowsParams& p, int n_layers, int dtype, bool write, cudaLaunchConfig_t cfg);
 cudaError_t launch_mxfp4_attention(const MxAttnParams& p, int n_layers, cudaLaunchConfig_t cfg);
+cudaError_t mxfp4_decode_set_attributes();
+cudaError_t launch_mxfp4_decode(const MxDecodeParams& p, cudaLaunchConfig_t cfg);
 }  // namespace ea
 
 namespace {
@@ -1175,31 +1177,37 @@ int run_mx_rows(const ea_mxfp4_rows* a, int n_layers, int row0, int n_rows, int 
 // Rotations of positions p0 + t, t < 64 (see MxAttnParams): rot_a[i] at p0 + 8 i, rot_b[i] at i, in
 // 64 bits (a far position's angle needs them), split into fp32 pairs. The angles of i and 8 i are
 // formed once per process.
-void mx_rotations(long long p0, int tok, MxAttnParams* p) {
-  struct Steps {
-    double f[kD / 2], c8[kTok / 8][kD / 2], s8[kTok / 8][kD / 2];
-    float4 b[8][kD / 2];
-  };
-  static Steps st;
+float4 split_rotation(double c, double s) {
+  const float ch = static_cast<float>(c), sh = static_cast<float>(s);
+  return make_float4(ch, static_cast<float>(c - ch), sh, static_cast<float>(s - sh));
+}
+
+struct MxSteps {  // the frequencies 5e6^(-j/64), and the rotations by i and 8 i positions
+  double f[kD / 2], c8[kTok / 8][kD / 2], s8[kTok / 8][kD / 2];
+  float4 b[8][kD / 2];
+};
+const MxSteps& mx_steps() {
+  static MxSteps st;
   static std::once_flag once;
-  auto split = [](double c, double s) {
-    const float ch = static_cast<float>(c), sh = static_cast<float>(s);
-    return make_float4(ch, static_cast<float>(c - ch), sh, static_cast<float>(s - sh));
-  };
-  std::call_once(once, [&] {
+  std::call_once(once, [] {
     for (int j = 0; j < kD / 2; ++j) {
       st.f[j] = std::pow(5.0e6, -static_cast<double>(j) / (kD / 2));
       for (int i = 0; i < 8; ++i) {
         st.c8[i][j] = std::cos(8 * i * st.f[j]);
         st.s8[i][j] = std::sin(8 * i * st.f[j]);
-        st.b[i][j] = split(std::cos(i * st.f[j]), std::sin(i * st.f[j]));
+        st.b[i][j] = split_rotation(std::cos(i * st.f[j]), std::sin(i * st.f[j]));
       }
     }
   });
+  return st;
+}
+
+void mx_rotations(long long p0, MxAttnParams* p) {
+  const MxSteps& st = mx_steps();
   for (int j = 0; j < kD / 2; ++j) {
     const double a = static_cast<double>(p0) * st.f[j], c = std::cos(a), s = std::sin(a);
-    for (int i = 0; 8 * i < tok; ++i)
-      p->rot_a[i][j] = split(c * st.c8[i][j] - s * st.s8[i][j], s * st.c8[i][j] + c * st.s8[i][j]);
+    for (int i = 0; i < kTok / 8; ++i)
+      p->rot_a[i][j] = split_rotation(c * st.c8[i][j] - s * st.s8[i][j], s * st.c8[i][j] + c * st.s8[i][j]);
   }
   std::memcpy(p->rot_b, st.b, sizeof(st.b));
 }
@@ -1228,6 +1236,74 @@ size_t mx_ws_bytes(int n_layers, int rq) {
   return 1024 + static_cast<size_t>(per) * kHkv * rq * kD * sizeof(float);
 }
 
+// layer l of a call as the kernels take it
+template <class A>
+MxAttnLayer mx_layer(const A& x) {
+  auto bf = [](const void* q) { return static_cast<const __nv_bfloat16*>(q); };
+  auto u8 = [](void* q) { return static_cast<uint8_t*>(q); };
+  return {bf(x.q_raw), bf(x.k_raw), bf(x.v_raw), bf(x.q_gamma), bf(x.k_gamma), u8(x.k_codes),
+          u8(x.k_scales), u8(x.v_codes), u8(x.v_scales), static_cast<__nv_bfloat16*>(x.out),
+          static_cast<__nv_bfloat16*>(x.k_new), static_cast<__nv_bfloat16*>(x.v_new)};
+}
+
+bool mx_decode_attrs_ready() {
+  static std::once_flag once;
+  static bool ok = false;
+  std::call_once(once, [] {
+    ok = mxfp4_decode_set_attributes() == cudaSuccess;
+    cudaGetLastError();
+  });
+  return ok;
+}
+
+int run_mx_decode(const ea_decode_mxfp4_args* a, int n_layers, int pos, int Smax, long long p0, void* workspace,
+                  size_t ws_bytes, ea_stream_t stream) {
+  int dev;
+  DeviceInfo di;
+  if (!device_info(&dev, &di) || !mx_decode_attrs_ready()) return EA_ERR_UNSUPPORTED;
+  const int per = n_layers < kMaxLayersPerLaunch ? n_layers : kMaxLayersPerLaunch;
+  const DecodeWs wl = decode_ws_layout(per, di.sm_count);
+  if (ws_bytes < wl.total) return EA_ERR_WORKSPACE;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  MxDecodeParams p;
+  std::memset(&p, 0, sizeof(p));
+  for (int j = 0; j < kD / 2; ++j) {
+    const double x = static_cast<double>(p0) * mx_steps().f[j];
+    p.rot[j] = split_rotation(std::cos(x), std::sin(x));
+  }
+  p.part_o = reinterpret_cast<float*>(ws + wl.part_o_off);
+  p.part_lse = reinterpret_cast<float*>(ws + wl.part_ml_off);
+  p.unit_cnt = reinterpret_cast<uint32_t*>(ws + wl.cnt_off);
+  p.T = static_cast<uint32_t>(pos / kMxDecodeKeys + 1);
+  p.pos = pos;
+  p.Smax = Smax;
+  p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(kD)));
+  cudaLaunchAttribute attr[1];
+  for (int l0 = 0; l0 < n_layers; l0 += per) {
+    const int n = n_layers - l0 < per ? n_layers - l0 : per;
+    for (int l = 0; l < n; ++l) p.layer[l] = mx_layer(a[l0 + l]);
+    const uint32_t units = static_cast<uint32_t>(n) * kHkv, sms = static_cast<uint32_t>(di.sm_count);
+    const uint32_t W = units * p.T, full = (p.T + 7) / 8;  // parts of at most eight chunks: one per warp
+    uint32_t grid;
+    if (units <= sms && (units * full <= sms || sms / units * units * 20 >= sms * 19)) {
+      p.parts = full < sms / units ? full : sms / units;
+      grid = units * p.parts;
+    } else {
+      grid = sms < W ? sms : W;
+      p.parts = 0;
+      p.per_cta = W / grid;
+      p.extra = W % grid;
+    }
+    cudaLaunchConfig_t cfg = launch_config(static_cast<cudaStream_t>(stream), attr, true);
+    cfg.gridDim = dim3(grid);
+    if (launch_mxfp4_decode(p, cfg) != cudaSuccess) {
+      cudaGetLastError();
+      return EA_ERR_CUDA;
+    }
+  }
+  return EA_OK;
+}
+
 template <class A>
 int run_mx_attn(const A* a, int n_layers, int rep, int tok, int first, int new_row0, int Smax, long long p0,
                 void* workspace, size_t ws_bytes, ea_stream_t stream) {
@@ -1237,7 +1313,7 @@ int run_mx_attn(const A* a, int n_layers, int rep, int tok, int first, int new_r
   if (ws_bytes < mx_ws_bytes(n_layers, rep * tok)) return EA_ERR_WORKSPACE;
   MxAttnParams p;
   std::memset(&p, 0, sizeof(p));
-  mx_rotations(p0, tok, &p);
+  mx_rotations(p0, &p);
   p.status = static_cast<uint32_t*>(workspace);
   p.q_ws = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 1024);
   p.rep = rep;
@@ -1250,12 +1326,7 @@ int run_mx_attn(const A* a, int n_layers, int rep, int tok, int first, int new_r
   for (int l0 = 0; l0 < n_layers; l0 += kMaxLayersPerLaunch) {
     const int n = n_layers - l0 < kMaxLayersPerLaunch ? n_layers - l0 : kMaxLayersPerLaunch;
     for (int l = 0; l < n; ++l) {
-      const A& x = a[l0 + l];
-      auto bf = [](const void* q) { return static_cast<const __nv_bfloat16*>(q); };
-      auto u8 = [](void* q) { return static_cast<uint8_t*>(q); };
-      p.layer[l] = {bf(x.q_raw), bf(x.k_raw), bf(x.v_raw), bf(x.q_gamma), bf(x.k_gamma), u8(x.k_codes),
-                    u8(x.k_scales), u8(x.v_codes), u8(x.v_scales), static_cast<__nv_bfloat16*>(x.out),
-                    static_cast<__nv_bfloat16*>(x.k_new), static_cast<__nv_bfloat16*>(x.v_new)};
+      p.layer[l] = mx_layer(a[l0 + l]);
     }
     if (launch_mxfp4_attention(p, n, launch_config(static_cast<cudaStream_t>(stream), attr, true)) != cudaSuccess) {
       cudaGetLastError();
@@ -1283,7 +1354,7 @@ size_t text_decode_mxfp4_workspace_size(int n_layers) {
   int dev;
   DeviceInfo di;
   if (n_layers < 1 || !device_info(&dev, &di)) return 0;
-  return mx_ws_bytes(n_layers, kRepText);
+  return decode_ws_layout(n_layers < kMaxLayersPerLaunch ? n_layers : kMaxLayersPerLaunch, di.sm_count).total;
 }
 
 int text_decode_attention_mxfp4(const ea_decode_mxfp4_args* layers, int n_layers, int pos, int Smax, int rope_delta,
@@ -1292,7 +1363,7 @@ int text_decode_attention_mxfp4(const ea_decode_mxfp4_args* layers, int n_layers
   if (Smax < kKeyTile || Smax % kTok != 0 || Smax > (1 << 22) || pos < 0 || pos >= Smax) return EA_ERR_INVALID_ARG;
   const int rc = validate_mx_attn(layers, n_layers, p0, 1, workspace);
   if (rc != EA_OK) return rc;
-  return run_mx_attn(layers, n_layers, kRepText, 1, pos, pos, Smax, p0, workspace, ws_bytes, stream);
+  return run_mx_decode(layers, n_layers, pos, Smax, p0, workspace, ws_bytes, stream);
 }
 
 size_t expert_attn_mxfp4_workspace_size(int n_layers) {

@@ -263,6 +263,21 @@ struct MxAttnLayer {
   __nv_bfloat16* k_new;  // optional: the new rows' values as stored, [8][tok][128]
   __nv_bfloat16* v_new;
 };
+// One decode step over 4-bit caches (mxfp4_decode.cu).
+struct MxDecodeParams {
+  MxAttnLayer layer[kMaxLayersPerLaunch];
+  float4 rot[kD / 2];   // the token's rotation by frequency: cosine x + y, sine z + w
+  float* part_o;        // [n_ctas][2 slots][8 heads][128]: a part's normalised output
+  float* part_lse;      // [n_ctas][2 slots][8 heads]: its log2-sum-exp
+  uint32_t* unit_cnt;   // [unit]: parts that have written their partial (zero between calls)
+  uint32_t T;           // chunks of 32 keys per unit: pos / 32 + 1
+  uint32_t parts;       // > 0: CTAs per unit, each with its share of the unit's chunks
+  uint32_t per_cta, extra;  // else: CTA c owns per_cta chunks, one more for c < extra
+  int pos, Smax;
+  float scale_log2;     // log2(e) / sqrt(128)
+};
+constexpr int kMxDecodeKeys = 32;
+
 struct MxAttnParams {
   MxAttnLayer layer[kMaxLayersPerLaunch];
   // rotations by position: token t sits at angle(rot_a[t / 8]) + angle(rot_b[t % 8]); each entry is

@@ -1,0 +1,556 @@
+// mxfp4_decode.cu — one token's attention over 4-bit caches.
+//
+// Per (layer, kv head) unit, with the 8 query heads q_h of the GQA group (normed and roped):
+//   the new k (normed, roped) and v rows encoded into cache row pos;
+//   s[key][h] = sum_b 2^ek[key][b] (codes of block b . q_h)    over the four 32-channel blocks b
+//   out[h][d] = sum_key P[key][h] 2^ev[key][b(d)] code[key][d] / sum_key P[key][h],  P = 2^(s - m)
+//
+// What bounds it: HBM, 136 bytes a key and head for 4 x 8 x 128 flops. The codes have to be widened on the
+// way to the tensor core, and through shared memory they would cost more than the read itself: 16-bit
+// tiles are 64 KB written and 64 KB read per 128 keys (1,000 cycles at 128 bytes a cycle) where HBM
+// takes 700. So the operands are formed in registers (mma.sync fragments straight from the packed
+// codes), shared memory holds codes only, and every warp runs by itself: its own ring, its own keys, its
+// own running maximum, no barrier until a unit ends.
+//   K: a 16-byte block of a row is one matrix row of ldmatrix; a thread's word holds eight codes of one
+//      key, cvt turns each byte into an f16 pair, and one accumulator per block b takes the two
+//      k = 16 steps of its 32 channels (A = 16 keys, B = the 8 heads). The blocks' scales multiply the
+//      four sums in fp32, so that K is exact at any scale.
+//   V: ldmatrix.trans gives a thread four codes of key 2t (low half) and of key 2t + 1 (high half);
+//      exchanging nibbles pairs the two keys in a byte, and cvt gives the f16 pair along the keys
+//      that V^T (A = 16 channels, K = 16 keys) needs. V's scales go into P instead, once per block of
+//      channels: 8 products of f16 pairs a step in place of 32.
+// P 2^(ev - R) is held in f16: R is a running reference of the warp, the largest scale of a block that
+// is not all zeros (as of the last time it was exceeded by 2^3), put at 2^8, so that weights times
+// scales keep 11 bits down to 2^-22 of the largest. m is raised only when a score passes it by
+// 4 (P <= 2^4), so that both rescalings are rare.
+//
+// Work decomposition: the units' keys in chunks of 32, unit-major, one contiguous range per CTA; a CTA's
+// eight compute warps take its chunks in turn. At the end of a unit the warps' partials meet in
+// shared memory; a unit cut over several CTAs is merged by the part that finishes last. Three further
+// warps prepare the next unit's q rows and encode the new rows.
+#include "mxfp4.cuh"
+#include "rope.cuh"
+
+namespace ea {
+namespace mxd {
+
+constexpr int kWarps = 8;                    // compute warps
+constexpr int kCompute = 32 * kWarps;
+constexpr int kPrep = 96;                    // 12 octets: 8 q rows, the k row, the v row
+constexpr int kThreads = kCompute + kPrep;
+constexpr int kKeys = 32;                    // keys per chunk
+constexpr int kStages = 5;
+constexpr uint32_t kCodes = kKeys * kMxRowBytes, kScales = kKeys * kMxRowScales;
+constexpr uint32_t kStageBytes = 2 * kCodes + 2 * kScales;  // K codes, V codes, K scales, V scales
+constexpr uint32_t SM_RING = 0;
+constexpr uint32_t SM_PART = SM_RING + kWarps * kStages * kStageBytes;  // [warp][head][132] fp32
+constexpr uint32_t kPartRow = 132;           // 128 channels + 4 words: heads 2 apart fall in other banks
+constexpr uint32_t SM_ML = SM_PART + kWarps * kRepText * kPartRow * 4;  // [warp][head] (m, l)
+constexpr uint32_t SM_R = SM_ML + kWarps * kRepText * 8;                // [warp] reference scale byte
+constexpr uint32_t SM_Q = SM_R + kWarps * 4;                            // 2 x [8 heads][128] f16
+constexpr uint32_t SM_QF = SM_Q + 2 * kRepText * kD * 2;                // 2 x [8 heads] score factor
+constexpr uint32_t kNewBytes = 2 * kMxRowBytes + 8;
+constexpr uint32_t SM_NEW = SM_QF + 2 * kRepText * 4;                   // 2 x (K codes, V codes, scale words)
+constexpr uint32_t SM_FLAG = SM_NEW + 2 * 144;
+constexpr uint32_t kSmemBytes = SM_FLAG + 16;
+static_assert(kNewBytes <= 144 && kSmemBytes <= 232448, "shared memory budget of one sm_103 CTA");
+
+// P 2^(ev - R): a block at the reference has factor 2^8 (f16 exponent field 23); fields above 26 only
+// occur for all-zero blocks and are cut there, so that P <= 2^4 times the factor stays finite.
+constexpr int kRefField = 23, kMaxField = 26;
+constexpr float kLazy = 4.0f;
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldm4(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void ldm4t(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 ld_shared_v2(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+// (a & m) | (b & ~m)
+__device__ __forceinline__ uint32_t select_bits(uint32_t a, uint32_t b, uint32_t m) { return (a & m) | (b & ~m); }
+
+// CTA c's first chunk: parts > 0: the unit's chunks in that many ranges; else all chunks in ranges whose
+// lengths differ by at most one.
+__device__ __forceinline__ uint32_t cta_start(const MxDecodeParams& p, uint32_t c) {
+  if (p.parts > 0) return c / p.parts * p.T + c % p.parts * p.T / p.parts;
+  return c * p.per_cta + min(c, p.extra);
+}
+__device__ __forceinline__ uint32_t cta_of(const MxDecodeParams& p, uint32_t x) {
+  if (p.parts > 0) {  // x is a unit's first or last chunk
+    return x / p.T * p.parts + (x % p.T == 0 ? 0 : p.parts - 1);
+  }
+  const uint32_t split = p.extra * (p.per_cta + 1);
+  return x < split ? x / (p.per_cta + 1) : p.extra + (x - split) / p.per_cta;
+}
+
+// ------------------------------------------------------------------------------ chunk loads
+// Chunk f: rows [32 j, 32 j + 32) of unit u that lie before pos (the rest arrives as zeros; row pos is put
+// in by the warp itself). Block b of row r goes to 16-byte slot b ^ (r / 2 % 4) of its row, so that the
+// eight rows of an ldmatrix phase fall in different banks.
+__device__ __forceinline__ void load_chunk(const MxDecodeParams& p, uint32_t dst, uint32_t f, int lane) {
+  const uint32_t u = f / p.T, j = f - u * p.T;
+  const MxAttnLayer& L = p.layer[u / kHkv];
+  const int row0 = static_cast<int>(j) * kKeys, valid = min(kKeys, p.pos - row0);
+  const size_t base = static_cast<size_t>(u % kHkv) * p.Smax + row0;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int r = 8 * q + (lane >> 2), b = lane & 3;
+    const bool live = r < valid;
+    const size_t off = (base + (live ? r : 0)) * kMxRowBytes + 16 * b;
+    const uint32_t to = dst + r * kMxRowBytes + ((b ^ ((r >> 1) & 3)) << 4);
+    cp16(to, L.kc + off, live ? 16 : 0);
+    cp16(to + kCodes, L.vc + off, live ? 16 : 0);
+  }
+  if (lane < 16) {
+    const int q = lane & 7;
+    const int bytes = max(0, min(16, 4 * valid - 16 * q));
+    cp16(dst + 2 * kCodes + (lane >> 3) * kScales + 16 * q,
+         (lane < 8 ? L.ks : L.vs) + base * kMxRowScales + (bytes > 0 ? 16 * q : 0), bytes);
+  }
+}
+
+// ------------------------------------------------------------------------------ preparation
+// Unit u's q rows (octets 0-7: normed, roped, f16 times a power of two that puts the row's largest
+// magnitude in [1, 2)), and, when the segment holds the unit's last chunk, the new k row (octet 8) and v
+// row (octet 9): into shared memory for this CTA, into the cache, and their values to the caller.
+__device__ __forceinline__ void prepare(const MxDecodeParams& p, uint8_t* smem, uint32_t u, bool last, int buf, int tid) {
+  const int oct = tid >> 3, i = tid & 7;
+  const int l = u / kHkv, g = u % kHkv;
+  if (tid >= 64 && !last) return;
+  const MxAttnLayer& L = p.layer[l];
+  const int dl = 8 * i, dh = 64 + 8 * i;
+  const int kind = oct < 8 ? 0 : oct == 8 ? 1 : 2;  // the last two octets repeat octet 9 and store nothing
+  const __nv_bfloat16* src = kind == 0 ? L.q_raw + (static_cast<size_t>(g) * kRepText + oct) * kD
+                                       : (kind == 1 ? L.k_raw : L.v_raw) + static_cast<size_t>(g) * kD;
+  const __nv_bfloat16* gam = kind == 0 ? L.q_gamma : L.k_gamma;
+  float xl[8], xh[8], gl[8], gh[8], yl[8], yh[8];
+  const uint4 r0 = *reinterpret_cast<const uint4*>(src + dl), r1 = *reinterpret_cast<const uint4*>(src + dh);
+  const uint4 r2 = *reinterpret_cast<const uint4*>(gam + dl), r3 = *reinterpret_cast<const uint4*>(gam + dh);
+  unpack_bf16x8(r0, xl);
+  unpack_bf16x8(r1, xh);
+  unpack_bf16x8(r2, gl);
+  unpack_bf16x8(r3, gh);
+  if (tid < 64) {
+    float cs[8], sn[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      cs[e] = p.rot[dl + e].x;
+      sn[e] = p.rot[dl + e].z;
+    }
+    norm_rope(xl, xh, gl, gh, cs, sn, yl, yh);
+    float amax = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fmaxf(fabsf(yl[e]), fabsf(yh[e])));
+#pragma unroll
+    for (int m = 4; m >= 1; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
+    const int e = amax == 0.f ? 0 : min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -126), 126);
+    const float inv = mx_pow2(-e);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      yl[k] *= inv;
+      yh[k] *= inv;
+    }
+    uint8_t* q = smem + SM_Q + (buf * kRepText + oct) * kD * 2;
+    *reinterpret_cast<uint4*>(q + 2 * dl) = pack8(yl, true);
+    *reinterpret_cast<uint4*>(q + 2 * dh) = pack8(yh, true);
+    if (i == 0) reinterpret_cast<float*>(smem + SM_QF)[buf * kRepText + oct] = p.scale_log2 * mx_pow2(e);
+    return;
+  }
+  Pair cs[8], sn[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float4 a = p.rot[dl + e];
+    cs[e] = {a.x, a.y};
+    sn[e] = {a.z, a.w};
+  }
+  pair_norm_rope(xl, xh, gl, gh, cs, sn, yl, yh);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    yl[e] = kind == 1 ? yl[e] : xl[e];
+    yh[e] = kind == 1 ? yh[e] : xh[e];
+  }
+  uint32_t cl, ch, sc;
+  int el, eh;
+  mx_encode_octet(yl, yh, cl, ch, sc, el, eh);
+  if (oct > 9) return;
+  uint32_t* nw = reinterpret_cast<uint32_t*>(smem + SM_NEW + buf * 144);
+  const int v = kind == 2 ? 1 : 0;
+  nw[16 * v + i] = cl;
+  nw[16 * v + 8 + i] = ch;
+  const size_t crow = static_cast<size_t>(g) * p.Smax + p.pos;
+  uint8_t* codes = (v ? L.vc : L.kc) + crow * kMxRowBytes;
+  *reinterpret_cast<uint32_t*>(codes + 4 * i) = cl;
+  *reinterpret_cast<uint32_t*>(codes + 32 + 4 * i) = ch;
+  if (i == 0) {
+    nw[32 + v] = sc;
+    *reinterpret_cast<uint32_t*>((v ? L.vs : L.ks) + crow * kMxRowScales) = sc;
+  }
+  __nv_bfloat16* val = v ? L.v_new : L.k_new;
+  if (val != nullptr) {
+    val += static_cast<size_t>(g) * kD;
+    mx_values8(cl, mx_pow2(el), xl);
+    mx_values8(ch, mx_pow2(eh), xh);
+    *reinterpret_cast<uint4*>(val + dl) = pack8(xl, false);
+    *reinterpret_cast<uint4*>(val + dh) = pack8(xh, false);
+  }
+}
+
+// --------------------------------------------------------------------------------- one chunk
+struct Warp {
+  float m[2], l[2];  // heads 2t, 2t + 1: reference maximum (log2 units); sum over this thread's keys
+  float o[8][4];     // O^T: tile 2b + h of block b, rows = channels 32 b + 4 (lane/4) + 2 h + {0, 1}
+  int ref;           // R as a scale byte
+};
+
+// Raises the reference maximum of both heads to the chunk's (x: scores in log2 units).
+__device__ __forceinline__ void raise_max(Warp& w, float x0, float x1) {
+#pragma unroll
+  for (int m = 4; m <= 16; m <<= 1) {
+    x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, m));
+    x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, m));
+  }
+  const float n0 = fmaxf(w.m[0], x0), n1 = fmaxf(w.m[1], x1);
+  const float a0 = ex2_approx(w.m[0] - n0), a1 = ex2_approx(w.m[1] - n1);
+  w.m[0] = n0;
+  w.m[1] = n1;
+  w.l[0] *= a0;
+  w.l[1] *= a1;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    w.o[i][0] *= a0;
+    w.o[i][1] *= a1;
+    w.o[i][2] *= a0;
+    w.o[i][3] *= a1;
+  }
+}
+
+// Some scale of the chunk is far above the reference: raises the reference to the largest scale of a
+// block that has a code other than zero (lane = key), if that is the case for such a block.
+__device__ __forceinline__ void raise_ref(Warp& w, uint32_t st, int lane) {
+  const uint32_t sc = ld_shared_u32(st + 2 * kCodes + kScales + 4 * lane);
+  uint32_t top = 0;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const uint4 c = ld_shared_v4(st + kCodes + lane * kMxRowBytes + ((b ^ ((lane >> 1) & 3)) << 4));
+    if (((c.x | c.y | c.z | c.w) & 0x77777777u) != 0u) top = max(top, (sc >> (8 * b)) & 255u);
+  }
+  const int t = static_cast<int>(__reduce_max_sync(0xffffffffu, top));
+  if (t <= w.ref + (kMaxField - kRefField)) return;
+  const float a = w.ref - t < -126 ? 0.f : mx_pow2(w.ref - t);
+  w.ref = t;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w.o[i][k] *= a;
+}
+
+__device__ __forceinline__ void chunk(Warp& w, const uint32_t (&q)[4][4], const float (&qf)[2], uint32_t st, int live,
+                                      int lane) {
+  const int g = lane >> 2, t = lane & 3;
+  // ldmatrix: lane i names row (i & 7) + 8 ((i >> 3) & 1) of block (i >> 4) + {0, 2}
+  const int lr = lane & 15;
+  const uint32_t lrow = st + lr * kMxRowBytes;
+  const uint32_t sw = (lr >> 1) & 3, b0 = lane >> 4;
+  const uint32_t a0 = lrow + ((b0 ^ sw) << 4), a1 = lrow + (((b0 + 2) ^ sw) << 4);
+  float x[2][4];  // [16 keys][key g: heads 2t, 2t+1; key g + 8: the same]
+#pragma unroll
+  for (int a = 0; a < 2; ++a) {
+    const uint32_t s0 = ld_shared_u32(st + 2 * kCodes + 4 * (16 * a + g)), s1 = ld_shared_u32(st + 2 * kCodes + 4 * (16 * a + g + 8));
+    uint32_t r[8];
+    ldm4(a0 + a * 16 * kMxRowBytes, *reinterpret_cast<uint32_t(*)[4]>(r));
+    ldm4(a1 + a * 16 * kMxRowBytes, *reinterpret_cast<uint32_t(*)[4]>(r + 4));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[a][k] = 0.f;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      uint32_t h0[4], h1[4];  // f16 pairs of the eight codes of keys g and g + 8
+      mx_unpack8(r[2 * b], h0);
+      mx_unpack8(r[2 * b + 1], h1);
+      float d[4] = {0.f, 0.f, 0.f, 0.f};
+      mma16816(d, {h0[0], h1[0], h0[1], h1[1]}, q[b][0], q[b][1]);
+      mma16816(d, {h0[2], h1[2], h0[3], h1[3]}, q[b][2], q[b][3]);
+      // (a scale byte of 0, 2^-127, is taken as 0 here: such a block adds nothing to a score)
+      const float f0 = __uint_as_float(b == 3 ? (s0 >> 1) & 0x7F800000u : (s0 << (23 - 8 * b)) & 0x7F800000u);
+      const float f1 = __uint_as_float(b == 3 ? (s1 >> 1) & 0x7F800000u : (s1 << (23 - 8 * b)) & 0x7F800000u);
+      x[a][0] = fmaf(f0, d[0], x[a][0]);
+      x[a][1] = fmaf(f0, d[1], x[a][1]);
+      x[a][2] = fmaf(f1, d[2], x[a][2]);
+      x[a][3] = fmaf(f1, d[3], x[a][3]);
+    }
+  }
+#pragma unroll
+  for (int a = 0; a < 2; ++a)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[a][k] *= qf[k & 1];
+  if (live < kKeys) {
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (16 * a + g + 4 * (k & 2) >= live) x[a][k] = -INFINITY;
+  }
+  const float mx0 = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
+  const float mx1 = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
+  if (__any_sync(0xffffffffu, mx0 > w.m[0] + kLazy || mx1 > w.m[1] + kLazy)) raise_max(w, mx0, mx1);
+  {
+    const uint32_t vs = ld_shared_u32(st + 2 * kCodes + kScales + 4 * lane);
+    const uint32_t mx2 = __vmaxu2(vs & 0x00FF00FFu, (vs >> 8) & 0x00FF00FFu);
+    const int top = static_cast<int>(max(mx2 & 0xFFFFu, mx2 >> 16));
+    if (__any_sync(0xffffffffu, top > w.ref + (kMaxField - kRefField))) raise_ref(w, st, lane);
+  }
+  const uint32_t add = static_cast<uint32_t>((kRefField - w.ref) & 0xFFFF) * 0x10001u;
+#pragma unroll
+  for (int a = 0; a < 2; ++a) {
+    uint32_t pb[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float p0 = ex2_approx(x[a][2 * k] - w.m[0]), p1 = ex2_approx(x[a][2 * k + 1] - w.m[1]);
+      w.l[0] += p0;
+      w.l[1] += p1;
+      pb[k] = transpose8x8(pack_f16x2(p0, p1));  // -> head lane / 4, keys 2t, 2t + 1
+    }
+    // V's scale words of keys 2t, 2t + 1 and 2t + 8, 2t + 9 of this 16-key step
+    const uint2 va = ld_shared_v2(st + 2 * kCodes + kScales + 4 * (16 * a + 2 * t));
+    const uint2 vb = ld_shared_v2(st + 2 * kCodes + kScales + 4 * (16 * a + 2 * t + 8));
+    uint32_t r[8];
+    ldm4t(a0 + kCodes + a * 16 * kMxRowBytes, *reinterpret_cast<uint32_t(*)[4]>(r));
+    ldm4t(a1 + kCodes + a * 16 * kMxRowBytes, *reinterpret_cast<uint32_t(*)[4]>(r + 4));
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      auto factor = [&](uint2 s) -> uint32_t {  // f16 pair 2^(ev - R + 8) of the two keys, block b
+        const uint32_t z = __byte_perm(s.x, s.y, b | (4 + b) << 8) & 0x00FF00FFu;
+        return __viaddmin_s16x2_relu(z, add, kMaxField * 0x10001u) << 10;
+      };
+      const uint32_t q0 = hmul2(pb[0], factor(va)), q1 = hmul2(pb[1], factor(vb));
+      const uint32_t lo = __byte_perm(r[2 * b], r[2 * b + 1], 0x5410), hi = __byte_perm(r[2 * b], r[2 * b + 1], 0x7632);
+      const uint32_t even = select_bits(lo, hi << 4, 0x0F0F0F0Fu), odd = select_bits(lo >> 4, hi, 0x0F0F0F0Fu);
+      uint32_t he[4], ho[4];  // channels 4g + {0, 2} and {1, 3}: keys (2t, 2t+1), then (2t+8, 2t+9)
+      mx_unpack8(even, he);
+      mx_unpack8(odd, ho);
+      mma16816(w.o[2 * b], {he[0], ho[0], he[2], ho[2]}, q0, q1);
+      mma16816(w.o[2 * b + 1], {he[1], ho[1], he[3], ho[3]}, q0, q1);
+    }
+  }
+}
+
+}  // namespace mxd
+
+__global__ void __launch_bounds__(mxd::kThreads, 1) mxfp4_decode_kernel(const __grid_constant__ MxDecodeParams p) {
+  using namespace mxd;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const uint32_t sbase = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t start = cta_start(p, blockIdx.x), end = cta_start(p, blockIdx.x + 1);
+  pdl_wait_primary();
+  const uint32_t ring = sbase + SM_RING + warp * kStages * kStageBytes;
+  uint32_t n = 0;  // chunks of this warp so far: chunk n is start + warp + 8 n, in slot n % kStages
+  if (warp < kWarps) {
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) {
+      const uint32_t f = start + warp + kWarps * s;
+      if (f < end) load_chunk(p, ring + s * kStageBytes, f, lane);
+      cp_commit();
+    }
+  }
+  int seg = 0;
+  for (uint32_t f0 = start; f0 < end; ++seg) {
+    const uint32_t u = f0 / p.T, u0 = u * p.T, f1 = min(end, u0 + p.T);
+    const int buf = seg & 1;
+    const bool last = f1 == u0 + p.T;
+    if (warp >= kWarps && seg == 0) prepare(p, smem, u, last, 0, tid - kCompute);
+    __syncthreads();  // this unit's q (and new row) are ready, the last unit's partials are read
+    if (warp >= kWarps) {
+      if (f1 < end) prepare(p, smem, u + 1, end >= f1 + p.T, buf ^ 1, tid - kCompute);
+      else pdl_launch_dependents();
+    } else {
+      uint32_t q[4][4];
+      float qf[2];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const uint4 v = ld_shared_v4(sbase + SM_Q + ((buf * kRepText + (lane >> 2)) * kD + 32 * b + 8 * (lane & 3)) * 2);
+        q[b][0] = v.x; q[b][1] = v.y; q[b][2] = v.z; q[b][3] = v.w;
+      }
+      const float2 fv = reinterpret_cast<const float2*>(smem + SM_QF)[(buf * kRepText >> 1) + (lane & 3)];
+      qf[0] = fv.x;
+      qf[1] = fv.y;
+      Warp w;
+      w.m[0] = w.m[1] = -INFINITY;
+      w.l[0] = w.l[1] = 0.f;
+      w.ref = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w.o[i][k] = 0.f;
+      for (uint32_t f = start + warp + kWarps * n; f < f1; f += kWarps, ++n) {
+        const uint32_t st = ring + (n % kStages) * kStageBytes;
+        cp_wait<kStages - 2>();
+        __syncwarp();  // the chunk has landed for every lane, and every lane has left the slot that is refilled
+        const uint32_t fn = f + kWarps * (kStages - 1);
+        if (fn < end) load_chunk(p, ring + ((n + kStages - 1) % kStages) * kStageBytes, fn, lane);
+        cp_commit();
+        const int row0 = static_cast<int>(f - u0) * kKeys;
+        const int rr = p.pos - row0;  // the new row's place in this chunk
+        if (rr < kKeys) {
+          const uint8_t* nw = smem + SM_NEW + buf * 144;
+          if (lane < 8) {
+            const uint4 v = *reinterpret_cast<const uint4*>(nw + 16 * lane);
+            st_shared_v4(st + (lane >> 2) * kCodes + rr * kMxRowBytes + (((lane & 3) ^ ((rr >> 1) & 3)) << 4), v.x, v.y, v.z, v.w);
+          } else if (lane < 10) {
+            *reinterpret_cast<uint32_t*>(smem + (st - sbase) + 2 * kCodes + (lane - 8) * kScales + 4 * rr) =
+                *reinterpret_cast<const uint32_t*>(nw + 128 + 4 * (lane - 8));
+          }
+          __syncwarp();
+        }
+        chunk(w, q, qf, st, rr + 1, lane);
+      }
+      // this warp's partial: O in units of 2^(m + R - 8), m, l, R
+#pragma unroll
+      for (int m = 4; m <= 16; m <<= 1) {
+        w.l[0] += __shfl_xor_sync(0xffffffffu, w.l[0], m);
+        w.l[1] += __shfl_xor_sync(0xffffffffu, w.l[1], m);
+      }
+      float* part = reinterpret_cast<float*>(smem + SM_PART) + warp * kRepText * kPartRow;
+      const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          *reinterpret_cast<float4*>(part + (2 * t + h) * kPartRow + 32 * b + 4 * g) =
+              make_float4(w.o[2 * b][h], w.o[2 * b][2 + h], w.o[2 * b + 1][h], w.o[2 * b + 1][2 + h]);
+      if (g < 2) {
+        float2* ml = reinterpret_cast<float2*>(smem + SM_ML) + warp * kRepText;
+        ml[2 * t + g] = g ? make_float2(w.m[1], w.l[1]) : make_float2(w.m[0], w.l[0]);
+      }
+      if (lane == 0) reinterpret_cast<int*>(smem + SM_R)[warp] = w.ref;
+    }
+    __syncthreads();
+    if (warp < kWarps) {
+      // thread = head h, channels [4 c, 4 c + 4): the warps' partials in units of 2^(M + Rmax - 8)
+      const int h = tid >> 5, c = tid & 31;
+      const float2* ml = reinterpret_cast<const float2*>(smem + SM_ML);
+      const int* rf = reinterpret_cast<const int*>(smem + SM_R);
+      float M = -INFINITY, Lsum = 0.f;
+      int R = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        M = fmaxf(M, ml[w * kRepText + h].x);
+        R = max(R, rf[w]);
+      }
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 v = ml[w * kRepText + h];
+        const float a = ex2_approx(v.x - M);  // 0 for a warp without keys
+        Lsum = fmaf(v.y, a, Lsum);
+        const float s = ex2_approx(v.x - M + static_cast<float>(rf[w] - R));
+        const float4 o = *reinterpret_cast<const float4*>(smem + SM_PART + ((w * kRepText + h) * kPartRow + 4 * c) * 4);
+        acc.x = fmaf(s, o.x, acc.x);
+        acc.y = fmaf(s, o.y, acc.y);
+        acc.z = fmaf(s, o.z, acc.z);
+        acc.w = fmaf(s, o.w, acc.w);
+      }
+      // 2^(R - 127 - 8) / L, in two steps: the power alone may leave fp32's range
+      const float inv = 1.0f / Lsum, two_r = mx_scale(R), down = 0.00390625f;
+      acc.x = acc.x * inv * down * two_r;
+      acc.y = acc.y * inv * down * two_r;
+      acc.z = acc.z * inv * down * two_r;
+      acc.w = acc.w * inv * down * two_r;
+      const int l = u / kHkv, g = u % kHkv;
+      __nv_bfloat16* out = p.layer[l].out + (static_cast<size_t>(g) * kRepText + h) * kD + 4 * c;
+      if (f0 == u0 && last) {
+        *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+      } else {
+        // a part of the unit: slot 2 c + 1 if this CTA came to it from an earlier unit, else 2 c
+        const size_t ps = static_cast<size_t>(blockIdx.x) * 2 + (f0 == start ? 0 : 1);
+        *reinterpret_cast<float4*>(p.part_o + (ps * kRepText + h) * kD + 4 * c) = acc;
+        if (c == 0) p.part_lse[ps * kRepText + h] = M + log2f(Lsum);
+        const uint32_t c0 = cta_of(p, u0), c1 = p.T == 1 ? c0 : cta_of(p, u0 + p.T - 1);
+        uint32_t* flag = reinterpret_cast<uint32_t*>(smem + SM_FLAG);
+        bar_sync(1, kCompute);
+        if (tid == 0) {
+          uint32_t old;
+          asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(old) : "l"(p.unit_cnt + u) : "memory");
+          *flag = old == c1 - c0 ? 1u : 0u;
+        }
+        bar_sync(1, kCompute);
+        if (*flag != 0u) {  // the last part: merges them all, in their order
+          const uint32_t np = c1 - c0 + 1;
+          const size_t first = static_cast<size_t>(c0) * 2 + (cta_start(p, c0) >= u0 ? 0 : 1);
+          auto slot = [&](uint32_t k) -> size_t { return k == 0 ? first : static_cast<size_t>(c0 + k) * 2; };
+          float ML = -INFINITY;
+          for (uint32_t k = 0; k < np; ++k) ML = fmaxf(ML, __ldcg(p.part_lse + slot(k) * kRepText + h));
+          float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+          float ws = 0.f;
+#pragma unroll 4
+          for (uint32_t k = 0; k < np; ++k) {
+            const float wt = ex2_approx(__ldcg(p.part_lse + slot(k) * kRepText + h) - ML);
+            const float4 o = __ldcg(reinterpret_cast<const float4*>(p.part_o + (slot(k) * kRepText + h) * kD + 4 * c));
+            ws += wt;
+            s.x = fmaf(wt, o.x, s.x);
+            s.y = fmaf(wt, o.y, s.y);
+            s.z = fmaf(wt, o.z, s.z);
+            s.w = fmaf(wt, o.w, s.w);
+          }
+          const float iw = 1.0f / ws;
+          *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(s.x * iw, s.y * iw), pack_bf16x2(s.z * iw, s.w * iw));
+          if (tid == 0) p.unit_cnt[u] = 0u;  // every part has arrived: ready for the next call
+        }
+      }
+    }
+    f0 = f1;
+  }
+}
+
+cudaError_t mxfp4_decode_set_attributes() {
+  return cudaFuncSetAttribute(mxfp4_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(mxd::kSmemBytes));
+}
+
+cudaError_t launch_mxfp4_decode(const MxDecodeParams& p, cudaLaunchConfig_t cfg) {
+  cfg.blockDim = dim3(mxd::kThreads);
+  cfg.dynamicSmemBytes = mxd::kSmemBytes;
+  return cudaLaunchKernelEx(&cfg, mxfp4_decode_kernel, p);
+}
+
+}  // namespace ea
