@@ -34,26 +34,31 @@
 namespace ea {
 namespace mxd {
 
-constexpr int kWarps = 8;                    // compute warps
+constexpr int kWarps = 12;                   // compute warps (at least 8: a unit's merge takes one per head)
 constexpr int kCompute = 32 * kWarps;
 constexpr int kPrep = 96;                    // 12 octets: 8 q rows, the k row, the v row
 constexpr int kThreads = kCompute + kPrep;
 constexpr int kKeys = 32;                    // keys per chunk
-constexpr int kStages = 5;
+constexpr int kStages = 3;
 constexpr uint32_t kCodes = kKeys * kMxRowBytes, kScales = kKeys * kMxRowScales;
 constexpr uint32_t kStageBytes = 2 * kCodes + 2 * kScales;  // K codes, V codes, K scales, V scales
 constexpr uint32_t SM_RING = 0;
-constexpr uint32_t SM_PART = SM_RING + kWarps * kStages * kStageBytes;  // [warp][head][132] fp32
+constexpr uint32_t kFactorBytes = kKeys * 16 + kKeys * 8;  // a chunk's scales as factors: K's fp32, V's f16
+constexpr uint32_t SM_FACT = SM_RING + kWarps * kStages * kStageBytes;
+constexpr uint32_t SM_PART = SM_FACT + kWarps * kFactorBytes;  // [warp][head][132] fp32
 constexpr uint32_t kPartRow = 132;           // 128 channels + 4 words: heads 2 apart fall in other banks
 constexpr uint32_t SM_ML = SM_PART + kWarps * kRepText * kPartRow * 4;  // [warp][head] (m, l)
 constexpr uint32_t SM_R = SM_ML + kWarps * kRepText * 8;                // [warp] reference scale byte
-constexpr uint32_t SM_Q = SM_R + kWarps * 4;                            // 2 x [8 heads][128] f16
+constexpr uint32_t SM_Q = (SM_R + kWarps * 4 + 15) & ~15u;              // 2 x [8 heads][128] f16
 constexpr uint32_t SM_QF = SM_Q + 2 * kRepText * kD * 2;                // 2 x [8 heads] score factor
 constexpr uint32_t kNewBytes = 2 * kMxRowBytes + 8;
 constexpr uint32_t SM_NEW = SM_QF + 2 * kRepText * 4;                   // 2 x (K codes, V codes, scale words)
 constexpr uint32_t SM_FLAG = SM_NEW + 2 * 144;
 constexpr uint32_t kSmemBytes = SM_FLAG + 16;
 static_assert(kNewBytes <= 144 && kSmemBytes <= 232448, "shared memory budget of one sm_103 CTA");
+static_assert(kStageBytes % 128 == 0 && SM_FACT % 16 == 0 && SM_PART % 16 == 0 && SM_ML % 8 == 0 && SM_Q % 16 == 0 &&
+                  SM_QF % 8 == 0 && SM_NEW % 16 == 0,
+              "alignment of the vector accesses");
 
 // P 2^(ev - R): a block at the reference has factor 2^8 (f16 exponent field 23); fields above 26 only
 // occur for all-zero blocks and are cut there, so that P <= 2^4 times the factor stays finite.
@@ -92,6 +97,14 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// the same onto a zero accumulator
+__device__ __forceinline__ void mma16816_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -106,6 +119,12 @@ __device__ __forceinline__ uint2 ld_shared_v2(uint32_t a) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
   return v;
+}
+// x << 4 as a product: the multipliers are idle here, the logic pipe is what bounds the warps
+__device__ __forceinline__ uint32_t times16(uint32_t x) {
+  uint32_t r;
+  asm("mul.lo.u32 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(16u));
+  return r;
 }
 // (a & m) | (b & ~m)
 __device__ __forceinline__ uint32_t select_bits(uint32_t a, uint32_t b, uint32_t m) { return (a & m) | (b & ~m); }
@@ -125,28 +144,56 @@ __device__ __forceinline__ uint32_t cta_of(const MxDecodeParams& p, uint32_t x) 
 }
 
 // ------------------------------------------------------------------------------ chunk loads
-// Chunk f: rows [32 j, 32 j + 32) of unit u that lie before pos (the rest arrives as zeros; row pos is put
-// in by the warp itself). Block b of row r goes to 16-byte slot b ^ (r / 2 % 4) of its row, so that the
-// eight rows of an ldmatrix phase fall in different banks.
-__device__ __forceinline__ void load_chunk(const MxDecodeParams& p, uint32_t dst, uint32_t f, int lane) {
-  const uint32_t u = f / p.T, j = f - u * p.T;
-  const MxAttnLayer& L = p.layer[u / kHkv];
-  const int row0 = static_cast<int>(j) * kKeys, valid = min(kKeys, p.pos - row0);
-  const size_t base = static_cast<size_t>(u % kHkv) * p.Smax + row0;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int r = 8 * q + (lane >> 2), b = lane & 3;
-    const bool live = r < valid;
-    const size_t off = (base + (live ? r : 0)) * kMxRowBytes + 16 * b;
-    const uint32_t to = dst + r * kMxRowBytes + ((b ^ ((r >> 1) & 3)) << 4);
-    cp16(to, L.kc + off, live ? 16 : 0);
-    cp16(to + kCodes, L.vc + off, live ? 16 : 0);
+// A warp's next chunk to load: chunk j of unit u, and where this lane's pieces of it start.
+struct Cursor {
+  uint32_t u, j;
+  const uint8_t *k, *v;  // codes, at this lane's 16 bytes
+  const uint8_t* s;      // scales: K's (lanes 0-7) or V's (lanes 8-15), at this lane's 16 bytes
+};
+__device__ __forceinline__ void cursor_unit(const MxDecodeParams& p, Cursor& c, int lane) {
+  const MxAttnLayer& L = p.layer[c.u / kHkv];
+  const size_t row = static_cast<size_t>(c.u % kHkv) * p.Smax + static_cast<size_t>(c.j) * kKeys;
+  c.k = L.kc + row * kMxRowBytes + 16 * lane;
+  c.v = L.vc + row * kMxRowBytes + 16 * lane;
+  c.s = (lane < 8 ? L.ks : L.vs) + row * kMxRowScales + 16 * (lane & 7);
+}
+// The same warp's next chunk, kWarps further on.
+__device__ __forceinline__ void cursor_next(const MxDecodeParams& p, Cursor& c, int lane) {
+  c.j += kWarps;
+  c.k += kWarps * kCodes;
+  c.v += kWarps * kCodes;
+  c.s += kWarps * kScales;
+  if (c.j >= p.T) {
+    c.u += c.j / p.T;
+    c.j %= p.T;
+    cursor_unit(p, c, lane);
   }
-  if (lane < 16) {
-    const int q = lane & 7;
-    const int bytes = max(0, min(16, 4 * valid - 16 * q));
-    cp16(dst + 2 * kCodes + (lane >> 3) * kScales + 16 * q,
-         (lane < 8 ? L.ks : L.vs) + base * kMxRowScales + (bytes > 0 ? 16 * q : 0), bytes);
+}
+// Loads the rows of the cursor's chunk that lie before pos (the others arrive as zeros; row pos is put in
+// by the warp itself). A chunk's codes are contiguous: lane i takes 16-byte pieces i, i + 32, ..; block b
+// of row r goes to 16-byte slot b ^ (r / 2 % 4) of its row, so that the eight rows of an ldmatrix phase
+// fall in different banks. `loff` is the lane's first piece's place.
+__device__ __forceinline__ void load_chunk(const MxDecodeParams& p, const Cursor& c, uint32_t dst, uint32_t loff, int lane) {
+  const int valid = p.pos - static_cast<int>(c.j) * kKeys;
+  const uint32_t to = dst + loff;
+  if (valid >= kKeys) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      cp16(to + 512 * q, c.k + 512 * q, 16);
+      cp16(to + kCodes + 512 * q, c.v + 512 * q, 16);
+    }
+    if (lane < 16) cp16(dst + 2 * kCodes + 16 * lane, c.s, 16);
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const bool live = 8 * q + (lane >> 2) < valid;  // a row that is not read is named by the chunk's first
+      cp16(to + 512 * q, live ? c.k + 512 * q : c.k - 16 * lane, live ? 16 : 0);
+      cp16(to + kCodes + 512 * q, live ? c.v + 512 * q : c.v - 16 * lane, live ? 16 : 0);
+    }
+    if (lane < 16) {
+      const int bytes = max(0, min(16, 4 * valid - 16 * (lane & 7)));
+      cp16(dst + 2 * kCodes + 16 * lane, bytes > 0 ? c.s : c.s - 16 * (lane & 7), bytes);
+    }
   }
 }
 
@@ -285,9 +332,31 @@ __device__ __forceinline__ void raise_ref(Warp& w, uint32_t st, int lane) {
     for (int k = 0; k < 4; ++k) w.o[i][k] *= a;
 }
 
-__device__ __forceinline__ void chunk(Warp& w, const uint32_t (&q)[4][4], const float (&qf)[2], uint32_t st, int live,
-                                      int lane) {
+// `fact`: the warp's 768 bytes for the chunk's factors; `live`: the chunk's keys from here on are masked
+__device__ __forceinline__ void chunk(Warp& w, const uint32_t (&q)[4][4], const float (&qf)[2], uint32_t st, uint32_t fact,
+                                      int live, int lane) {
   const int g = lane >> 2, t = lane & 3;
+  // The scales become factors once per key (lane = key), not once per thread that needs them:
+  // K's four as fp32, at fact + 16 key; V's four as f16 2^(ev - R + 8), the pair of keys 2i and 2i + 1 of
+  // block b at fact + 512 + 16 i + 4 b.
+  {
+    const uint32_t ks = ld_shared_u32(st + 2 * kCodes + 4 * lane), vs = ld_shared_u32(st + 2 * kCodes + kScales + 4 * lane);
+    // (a K scale byte of 0, 2^-127, is taken as 0: such a block adds nothing to a score)
+    st_shared_v4(fact + 16 * lane, (ks << 23) & 0x7F800000u, (ks << 15) & 0x7F800000u, (ks << 7) & 0x7F800000u,
+                 (ks >> 1) & 0x7F800000u);
+    const uint32_t v02 = vs & 0x00FF00FFu, v13 = (vs >> 8) & 0x00FF00FFu, top = __vmaxu2(v02, v13);
+    if (__any_sync(0xffffffffu, static_cast<int>(max(top & 0xFFFFu, top >> 16)) > w.ref + (kMaxField - kRefField)))
+      raise_ref(w, st, lane);
+    const uint32_t add = static_cast<uint32_t>((kRefField - w.ref) & 0xFFFF) * 0x10001u;
+    const uint32_t f02 = __viaddmin_s16x2_relu(v02, add, kMaxField * 0x10001u) << 10;
+    const uint32_t f13 = __viaddmin_s16x2_relu(v13, add, kMaxField * 0x10001u) << 10;
+    const uint32_t a = fact + 512 + 16 * (lane >> 1) + 2 * (lane & 1);
+    st_shared_u16(a, static_cast<uint16_t>(f02));
+    st_shared_u16(a + 4, static_cast<uint16_t>(f13));
+    st_shared_u16(a + 8, static_cast<uint16_t>(f02 >> 16));
+    st_shared_u16(a + 12, static_cast<uint16_t>(f13 >> 16));
+    __syncwarp();
+  }
   // ldmatrix: lane i names row (i & 7) + 8 ((i >> 3) & 1) of block (i >> 4) + {0, 2}
   const int lr = lane & 15;
   const uint32_t lrow = st + lr * kMxRowBytes;
@@ -296,27 +365,24 @@ __device__ __forceinline__ void chunk(Warp& w, const uint32_t (&q)[4][4], const 
   float x[2][4];  // [16 keys][key g: heads 2t, 2t+1; key g + 8: the same]
 #pragma unroll
   for (int a = 0; a < 2; ++a) {
-    const uint32_t s0 = ld_shared_u32(st + 2 * kCodes + 4 * (16 * a + g)), s1 = ld_shared_u32(st + 2 * kCodes + 4 * (16 * a + g + 8));
     uint32_t r[8];
     ldm4(a0 + a * 16 * kMxRowBytes, *reinterpret_cast<uint32_t(*)[4]>(r));
     ldm4(a1 + a * 16 * kMxRowBytes, *reinterpret_cast<uint32_t(*)[4]>(r + 4));
-#pragma unroll
-    for (int k = 0; k < 4; ++k) x[a][k] = 0.f;
+    const uint4 u0 = ld_shared_v4(fact + 16 * (16 * a + g)), u1 = ld_shared_v4(fact + 16 * (16 * a + g + 8));
+    const uint32_t f0[4] = {u0.x, u0.y, u0.z, u0.w}, f1[4] = {u1.x, u1.y, u1.z, u1.w};
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
       uint32_t h0[4], h1[4];  // f16 pairs of the eight codes of keys g and g + 8
       mx_unpack8(r[2 * b], h0);
       mx_unpack8(r[2 * b + 1], h1);
-      float d[4] = {0.f, 0.f, 0.f, 0.f};
-      mma16816(d, {h0[0], h1[0], h0[1], h1[1]}, q[b][0], q[b][1]);
+      float d[4];
+      mma16816_first(d, {h0[0], h1[0], h0[1], h1[1]}, q[b][0], q[b][1]);
       mma16816(d, {h0[2], h1[2], h0[3], h1[3]}, q[b][2], q[b][3]);
-      // (a scale byte of 0, 2^-127, is taken as 0 here: such a block adds nothing to a score)
-      const float f0 = __uint_as_float(b == 3 ? (s0 >> 1) & 0x7F800000u : (s0 << (23 - 8 * b)) & 0x7F800000u);
-      const float f1 = __uint_as_float(b == 3 ? (s1 >> 1) & 0x7F800000u : (s1 << (23 - 8 * b)) & 0x7F800000u);
-      x[a][0] = fmaf(f0, d[0], x[a][0]);
-      x[a][1] = fmaf(f0, d[1], x[a][1]);
-      x[a][2] = fmaf(f1, d[2], x[a][2]);
-      x[a][3] = fmaf(f1, d[3], x[a][3]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float f = __uint_as_float(k < 2 ? f0[b] : f1[b]);
+        x[a][k] = b == 0 ? f * d[k] : fmaf(f, d[k], x[a][k]);
+      }
     }
   }
 #pragma unroll
@@ -330,16 +396,9 @@ __device__ __forceinline__ void chunk(Warp& w, const uint32_t (&q)[4][4], const 
       for (int k = 0; k < 4; ++k)
         if (16 * a + g + 4 * (k & 2) >= live) x[a][k] = -INFINITY;
   }
-  const float mx0 = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
-  const float mx1 = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
+  const float mx0 = fmax3(fmaxf(x[0][0], x[0][2]), x[1][0], x[1][2]);
+  const float mx1 = fmax3(fmaxf(x[0][1], x[0][3]), x[1][1], x[1][3]);
   if (__any_sync(0xffffffffu, mx0 > w.m[0] + kLazy || mx1 > w.m[1] + kLazy)) raise_max(w, mx0, mx1);
-  {
-    const uint32_t vs = ld_shared_u32(st + 2 * kCodes + kScales + 4 * lane);
-    const uint32_t mx2 = __vmaxu2(vs & 0x00FF00FFu, (vs >> 8) & 0x00FF00FFu);
-    const int top = static_cast<int>(max(mx2 & 0xFFFFu, mx2 >> 16));
-    if (__any_sync(0xffffffffu, top > w.ref + (kMaxField - kRefField))) raise_ref(w, st, lane);
-  }
-  const uint32_t add = static_cast<uint32_t>((kRefField - w.ref) & 0xFFFF) * 0x10001u;
 #pragma unroll
   for (int a = 0; a < 2; ++a) {
     uint32_t pb[2];
@@ -350,21 +409,17 @@ __device__ __forceinline__ void chunk(Warp& w, const uint32_t (&q)[4][4], const 
       w.l[1] += p1;
       pb[k] = transpose8x8(pack_f16x2(p0, p1));  // -> head lane / 4, keys 2t, 2t + 1
     }
-    // V's scale words of keys 2t, 2t + 1 and 2t + 8, 2t + 9 of this 16-key step
-    const uint2 va = ld_shared_v2(st + 2 * kCodes + kScales + 4 * (16 * a + 2 * t));
-    const uint2 vb = ld_shared_v2(st + 2 * kCodes + kScales + 4 * (16 * a + 2 * t + 8));
+    // V's factors of keys 2t, 2t + 1 and 2t + 8, 2t + 9 of this 16-key step
+    const uint4 ua = ld_shared_v4(fact + 512 + 16 * (8 * a + t)), ub = ld_shared_v4(fact + 512 + 16 * (8 * a + t + 4));
+    const uint32_t fa[4] = {ua.x, ua.y, ua.z, ua.w}, fb[4] = {ub.x, ub.y, ub.z, ub.w};
     uint32_t r[8];
     ldm4t(a0 + kCodes + a * 16 * kMxRowBytes, *reinterpret_cast<uint32_t(*)[4]>(r));
     ldm4t(a1 + kCodes + a * 16 * kMxRowBytes, *reinterpret_cast<uint32_t(*)[4]>(r + 4));
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
-      auto factor = [&](uint2 s) -> uint32_t {  // f16 pair 2^(ev - R + 8) of the two keys, block b
-        const uint32_t z = __byte_perm(s.x, s.y, b | (4 + b) << 8) & 0x00FF00FFu;
-        return __viaddmin_s16x2_relu(z, add, kMaxField * 0x10001u) << 10;
-      };
-      const uint32_t q0 = hmul2(pb[0], factor(va)), q1 = hmul2(pb[1], factor(vb));
+      const uint32_t q0 = hmul2(pb[0], fa[b]), q1 = hmul2(pb[1], fb[b]);
       const uint32_t lo = __byte_perm(r[2 * b], r[2 * b + 1], 0x5410), hi = __byte_perm(r[2 * b], r[2 * b + 1], 0x7632);
-      const uint32_t even = select_bits(lo, hi << 4, 0x0F0F0F0Fu), odd = select_bits(lo >> 4, hi, 0x0F0F0F0Fu);
+      const uint32_t even = select_bits(lo, times16(hi), 0x0F0F0F0Fu), odd = select_bits(lo >> 4, hi, 0x0F0F0F0Fu);
       uint32_t he[4], ho[4];  // channels 4g + {0, 2} and {1, 3}: keys (2t, 2t+1), then (2t+8, 2t+9)
       mx_unpack8(even, he);
       mx_unpack8(odd, ho);
@@ -383,15 +438,26 @@ __global__ void __launch_bounds__(mxd::kThreads, 1) mxfp4_decode_kernel(const __
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t start = cta_start(p, blockIdx.x), end = cta_start(p, blockIdx.x + 1);
   pdl_wait_primary();
-  const uint32_t ring = sbase + SM_RING + warp * kStages * kStageBytes;
-  uint32_t n = 0;  // chunks of this warp so far: chunk n is start + warp + 8 n, in slot n % kStages
-  if (warp < kWarps) {
-#pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) {
-      const uint32_t f = start + warp + kWarps * s;
-      if (f < end) load_chunk(p, ring + s * kStageBytes, f, lane);
-      cp_commit();
+  // a warp's chunks are start + warp + kWarps i; chunk i sits in slot i % kStages of its ring
+  const uint32_t ring = sbase + SM_RING + warp * kStages * kStageBytes, fact = sbase + SM_FACT + warp * kFactorBytes;
+  const uint32_t loff = 64 * (lane >> 2) + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
+  uint32_t f = start + warp, fl = f, slot = 0, lslot = 0;  // next chunk to use and to load, and their slots' offsets
+  Cursor cur;
+  auto load = [&] {
+    if (fl < end) {
+      load_chunk(p, cur, ring + lslot, loff, lane);
+      fl += kWarps;
+      if (fl < end) cursor_next(p, cur, lane);
     }
+    cp_commit();
+    lslot = lslot + kStageBytes == kStages * kStageBytes ? 0 : lslot + kStageBytes;
+  };
+  if (warp < kWarps) {
+    cur.u = f / p.T;
+    cur.j = f - cur.u * p.T;
+    if (f < end) cursor_unit(p, cur, lane);
+#pragma unroll 1
+    for (int s = 0; s < kStages - 1; ++s) load();
   }
   int seg = 0;
   for (uint32_t f0 = start; f0 < end; ++seg) {
@@ -422,15 +488,14 @@ __global__ void __launch_bounds__(mxd::kThreads, 1) mxfp4_decode_kernel(const __
       for (int i = 0; i < 8; ++i)
 #pragma unroll
         for (int k = 0; k < 4; ++k) w.o[i][k] = 0.f;
-      for (uint32_t f = start + warp + kWarps * n; f < f1; f += kWarps, ++n) {
-        const uint32_t st = ring + (n % kStages) * kStageBytes;
+#pragma unroll 1
+      for (; f < f1; f += kWarps) {
+        const uint32_t st = ring + slot;
+        slot = slot + kStageBytes == kStages * kStageBytes ? 0 : slot + kStageBytes;
         cp_wait<kStages - 2>();
         __syncwarp();  // the chunk has landed for every lane, and every lane has left the slot that is refilled
-        const uint32_t fn = f + kWarps * (kStages - 1);
-        if (fn < end) load_chunk(p, ring + ((n + kStages - 1) % kStages) * kStageBytes, fn, lane);
-        cp_commit();
-        const int row0 = static_cast<int>(f - u0) * kKeys;
-        const int rr = p.pos - row0;  // the new row's place in this chunk
+        load();
+        const int rr = p.pos - static_cast<int>(f - u0) * kKeys;  // the new row's place in this chunk
         if (rr < kKeys) {
           const uint8_t* nw = smem + SM_NEW + buf * 144;
           if (lane < 8) {
@@ -442,7 +507,7 @@ __global__ void __launch_bounds__(mxd::kThreads, 1) mxfp4_decode_kernel(const __
           }
           __syncwarp();
         }
-        chunk(w, q, qf, st, rr + 1, lane);
+        chunk(w, q, qf, st, fact, rr + 1, lane);
       }
       // this warp's partial: O in units of 2^(m + R - 8), m, l, R
 #pragma unroll
@@ -465,7 +530,7 @@ __global__ void __launch_bounds__(mxd::kThreads, 1) mxfp4_decode_kernel(const __
       if (lane == 0) reinterpret_cast<int*>(smem + SM_R)[warp] = w.ref;
     }
     __syncthreads();
-    if (warp < kWarps) {
+    if (warp < kRepText) {
       // thread = head h, channels [4 c, 4 c + 4): the warps' partials in units of 2^(M + Rmax - 8)
       const int h = tid >> 5, c = tid & 31;
       const float2* ml = reinterpret_cast<const float2*>(smem + SM_ML);
@@ -507,13 +572,13 @@ __global__ void __launch_bounds__(mxd::kThreads, 1) mxfp4_decode_kernel(const __
         if (c == 0) p.part_lse[ps * kRepText + h] = M + log2f(Lsum);
         const uint32_t c0 = cta_of(p, u0), c1 = p.T == 1 ? c0 : cta_of(p, u0 + p.T - 1);
         uint32_t* flag = reinterpret_cast<uint32_t*>(smem + SM_FLAG);
-        bar_sync(1, kCompute);
+        bar_sync(1, kRepText * 32);
         if (tid == 0) {
           uint32_t old;
           asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(old) : "l"(p.unit_cnt + u) : "memory");
           *flag = old == c1 - c0 ? 1u : 0u;
         }
-        bar_sync(1, kCompute);
+        bar_sync(1, kRepText * 32);
         if (*flag != 0u) {  // the last part: merges them all, in their order
           const uint32_t np = c1 - c0 + 1;
           const size_t first = static_cast<size_t>(c0) * 2 + (cta_start(p, c0) >= u0 ? 0 : 1);
