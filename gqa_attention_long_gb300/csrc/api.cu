@@ -1097,7 +1097,9 @@ int text_decode_attention(const ea_decode_args* layers, int n_layers, int pos, i
 // Host side of the 4-bit cache's writer, reader and attentions.
 namespace ea {
 cudaError_t launch_mxfp4_rows(const MxRowsParams& p, int n_layers, int dtype, bool write, cudaLaunchConfig_t cfg);
-cudaError_t launch_mxfp4_attention(const MxAttnParams& p, int n_layers, cudaLaunchConfig_t cfg);
+cudaError_t mxfp4_attention_set_attributes();
+cudaError_t launch_mxfp4_prologue(const MxPrologueParams& p, int n_layers, cudaLaunchConfig_t cfg);
+cudaError_t launch_mxfp4_attention(const MxExpertParams& p, cudaLaunchConfig_t cfg);
 cudaError_t mxfp4_decode_set_attributes();
 cudaError_t launch_mxfp4_decode(const MxDecodeParams& p, cudaLaunchConfig_t cfg);
 }  // namespace ea
@@ -1174,7 +1176,7 @@ int run_mx_rows(const ea_mxfp4_rows* a, int n_layers, int row0, int n_rows, int 
   return EA_OK;
 }
 
-// Rotations of positions p0 + t, t < 64 (see MxAttnParams): rot_a[i] at p0 + 8 i, rot_b[i] at i, in
+// Rotations of positions p0 + t, t < 64 (see MxPrologueParams): rot_a[i] at p0 + 8 i, rot_b[i] at i, in
 // 64 bits (a far position's angle needs them), split into fp32 pairs. The angles of i and 8 i are
 // formed once per process.
 float4 split_rotation(double c, double s) {
@@ -1202,7 +1204,7 @@ const MxSteps& mx_steps() {
   return st;
 }
 
-void mx_rotations(long long p0, MxAttnParams* p) {
+void mx_rotations(long long p0, MxPrologueParams* p) {
   const MxSteps& st = mx_steps();
   for (int j = 0; j < kD / 2; ++j) {
     const double a = static_cast<double>(p0) * st.f[j], c = std::cos(a), s = std::sin(a);
@@ -1231,11 +1233,6 @@ int validate_mx_attn(const A* a, int n_layers, long long p0, int tok, const void
   return mx_caches_distinct(a, n_layers) ? EA_OK : EA_ERR_INVALID_ARG;
 }
 
-size_t mx_ws_bytes(int n_layers, int rq) {
-  const int per = n_layers < kMaxLayersPerLaunch ? n_layers : kMaxLayersPerLaunch;
-  return 1024 + static_cast<size_t>(per) * kHkv * rq * kD * sizeof(float);
-}
-
 // layer l of a call as the kernels take it
 template <class A>
 MxAttnLayer mx_layer(const A& x) {
@@ -1246,11 +1243,11 @@ MxAttnLayer mx_layer(const A& x) {
           static_cast<__nv_bfloat16*>(x.k_new), static_cast<__nv_bfloat16*>(x.v_new)};
 }
 
-bool mx_decode_attrs_ready() {
+bool mx_attrs_ready() {
   static std::once_flag once;
   static bool ok = false;
   std::call_once(once, [] {
-    ok = mxfp4_decode_set_attributes() == cudaSuccess;
+    ok = mxfp4_decode_set_attributes() == cudaSuccess && mxfp4_attention_set_attributes() == cudaSuccess;
     cudaGetLastError();
   });
   return ok;
@@ -1260,7 +1257,7 @@ int run_mx_decode(const ea_decode_mxfp4_args* a, int n_layers, int pos, int Smax
                   size_t ws_bytes, ea_stream_t stream) {
   int dev;
   DeviceInfo di;
-  if (!device_info(&dev, &di) || !mx_decode_attrs_ready()) return EA_ERR_UNSUPPORTED;
+  if (!device_info(&dev, &di) || !mx_attrs_ready()) return EA_ERR_UNSUPPORTED;
   const int per = n_layers < kMaxLayersPerLaunch ? n_layers : kMaxLayersPerLaunch;
   const DecodeWs wl = decode_ws_layout(per, di.sm_count);
   if (ws_bytes < wl.total) return EA_ERR_WORKSPACE;
@@ -1304,31 +1301,62 @@ int run_mx_decode(const ea_decode_mxfp4_args* a, int n_layers, int pos, int Smax
   return EA_OK;
 }
 
-template <class A>
-int run_mx_attn(const A* a, int n_layers, int rep, int tok, int first, int new_row0, int Smax, long long p0,
-                void* workspace, size_t ws_bytes, ea_stream_t stream) {
+// The units that the partition of W tiles (T per unit) over n_ctas CTAs cuts, in order.
+int mx_split_units(long long W, int T, int n_ctas, SplitUnit* out) {
+  int n = 0;
+  for (int b = 1; b < n_ctas; ++b) {
+    const long long tb = cta_tile_start(b, W, n_ctas);
+    const int u = static_cast<int>(tb / T);
+    if (tb % T == 0 || (n > 0 && out[n - 1].u == u)) continue;
+    const long long first = static_cast<long long>(u) * T;
+    SplitUnit& su = out[n++];
+    su.u = u;
+    su.c0 = static_cast<short>(cta_of_tile(first, W, n_ctas));
+    su.nparts = static_cast<short>(cta_of_tile(first + T - 1, W, n_ctas) - su.c0 + 1);
+    su.slot0 = cta_tile_start(su.c0, W, n_ctas) >= first ? 0 : 1;
+  }
+  return n;
+}
+
+int run_mx_expert(const ea_layer_mxfp4_args* a, int n_layers, int S, int Smax, long long p0, void* workspace,
+                  size_t ws_bytes, ea_stream_t stream) {
   int dev;
   DeviceInfo di;
-  if (!device_info(&dev, &di)) return EA_ERR_UNSUPPORTED;
-  if (ws_bytes < mx_ws_bytes(n_layers, rep * tok)) return EA_ERR_WORKSPACE;
-  MxAttnParams p;
+  if (!device_info(&dev, &di) || !mx_attrs_ready()) return EA_ERR_UNSUPPORTED;
+  const int per = n_layers < kMaxLayersPerLaunch ? n_layers : kMaxLayersPerLaunch;
+  const MxExpertWs wl = mx_expert_ws(per, di.sm_count);
+  if (ws_bytes < wl.total) return EA_ERR_WORKSPACE;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  MxPrologueParams pp;
+  MxExpertParams p;
+  std::memset(&pp, 0, sizeof(pp));
   std::memset(&p, 0, sizeof(p));
-  mx_rotations(p0, &p);
-  p.status = static_cast<uint32_t*>(workspace);
-  p.q_ws = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 1024);
-  p.rep = rep;
-  p.tok = tok;
-  p.first = first;
-  p.new_row0 = new_row0;
+  mx_rotations(p0, &pp);
+  pp.q_ws = ws + wl.q_off;
+  pp.q_factor = reinterpret_cast<float*>(ws + wl.factor_off);
+  pp.Smax = Smax;
+  pp.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(kD)));
+  p.q_ws = pp.q_ws;
+  p.q_factor = pp.q_factor;
+  p.part_o = reinterpret_cast<uint4*>(ws + wl.part_o_off);
+  p.part_lse = reinterpret_cast<float*>(ws + wl.part_lse_off);
+  p.status = reinterpret_cast<uint32_t*>(ws);
+  p.n_main = (S + kKeyTile - 1) / kKeyTile;
+  p.T = p.n_main + 1;
+  p.S = S;
   p.Smax = Smax;
-  p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(kD)));
   cudaLaunchAttribute attr[1];
-  for (int l0 = 0; l0 < n_layers; l0 += kMaxLayersPerLaunch) {
-    const int n = n_layers - l0 < kMaxLayersPerLaunch ? n_layers - l0 : kMaxLayersPerLaunch;
-    for (int l = 0; l < n; ++l) {
-      p.layer[l] = mx_layer(a[l0 + l]);
-    }
-    if (launch_mxfp4_attention(p, n, launch_config(static_cast<cudaStream_t>(stream), attr, true)) != cudaSuccess) {
+  const cudaLaunchConfig_t cfg = launch_config(static_cast<cudaStream_t>(stream), attr, true);
+  for (int l0 = 0; l0 < n_layers; l0 += per) {
+    const int n = n_layers - l0 < per ? n_layers - l0 : per;
+    for (int l = 0; l < n; ++l) p.layer[l] = pp.layer[l] = mx_layer(a[l0 + l]);
+    p.W = static_cast<long long>(n) * kHkv * p.T;
+    int n_ctas = di.sm_count < kMaxGridCtas ? di.sm_count : kMaxGridCtas;
+    if (static_cast<long long>(n_ctas) > p.W) n_ctas = static_cast<int>(p.W);
+    p.n_split = mx_split_units(p.W, p.T, n_ctas, p.split);
+    cudaLaunchConfig_t c = cfg;
+    c.gridDim = dim3(n_ctas);
+    if (launch_mxfp4_prologue(pp, n, cfg) != cudaSuccess || launch_mxfp4_attention(p, c) != cudaSuccess) {
       cudaGetLastError();
       return EA_ERR_CUDA;
     }
@@ -1370,7 +1398,7 @@ size_t expert_attn_mxfp4_workspace_size(int n_layers) {
   int dev;
   DeviceInfo di;
   if (n_layers < 1 || !device_info(&dev, &di)) return 0;
-  return mx_ws_bytes(n_layers, kRows);
+  return mx_expert_ws(n_layers < kMaxLayersPerLaunch ? n_layers : kMaxLayersPerLaunch, di.sm_count).total;
 }
 
 int expert_attn_layers_mxfp4(const ea_layer_mxfp4_args* layers, int n_layers, int S, int Smax, int rope_delta,
@@ -1379,7 +1407,7 @@ int expert_attn_layers_mxfp4(const ea_layer_mxfp4_args* layers, int n_layers, in
   if (Smax < 2 * kTok || Smax % kTok != 0 || Smax > (1 << 22) || S < 0 || S > Smax - kTok) return EA_ERR_INVALID_ARG;
   const int rc = validate_mx_attn(layers, n_layers, p0, kTok, workspace);
   if (rc != EA_OK) return rc;
-  return run_mx_attn(layers, n_layers, kHq / kHkv, kTok, S, Smax - kTok, Smax, p0, workspace, ws_bytes, stream);
+  return run_mx_expert(layers, n_layers, S, Smax, p0, workspace, ws_bytes, stream);
 }
 
 }  // extern "C"

@@ -278,17 +278,49 @@ struct MxDecodeParams {
 };
 constexpr int kMxDecodeKeys = 32;
 
-struct MxAttnParams {
+// The expert's attention over 4-bit caches (mxfp4_attention.cu).
+struct MxPrologueParams {
   MxAttnLayer layer[kMaxLayersPerLaunch];
   // rotations by position: token t sits at angle(rot_a[t / 8]) + angle(rot_b[t % 8]); each entry is
   // the cosine (x + y) and the sine (z + w) as fp32 pairs, by frequency
   float4 rot_a[kTok / 8][kD / 2];
   float4 rot_b[8][kD / 2];
-  float* q_ws;  // [unit][rep * tok][128]
-  uint32_t* status;
-  int rep, tok, first, new_row0, Smax;
+  uint8_t* q_ws;     // [unit] f16 q tile, 128 rows, the swizzled K-major layout (kQTileBytes)
+  float* q_factor;   // [unit][128]: what a row's scores are multiplied by (log2 units)
+  int Smax;
   float scale_log2;  // log2(e) / sqrt(128)
 };
+struct MxExpertParams {
+  MxAttnLayer layer[kMaxLayersPerLaunch];
+  const uint8_t* q_ws;
+  const float* q_factor;
+  uint4* part_o;     // partials as in AttnParams
+  float* part_lse;
+  uint32_t* status;
+  long long W;       // tiles: n_layers * 8 * T
+  int T, n_main;     // tiles per unit: n_main = ceil(S / 128) and the own rows'
+  int S, Smax;
+  int n_split;
+  SplitUnit split[kMaxSplitUnits];
+};
+// Workspace: [0, 1024) status word; q_factor; q tiles; partials of at most max_ctas CTAs.
+struct MxExpertWs {
+  size_t factor_off, q_off, part_o_off, part_lse_off, total;
+};
+constexpr MxExpertWs mx_expert_ws(int n_layers, int max_ctas) {
+  MxExpertWs w{};
+  size_t off = 1024;
+  w.factor_off = off;
+  off += static_cast<size_t>(n_layers) * kHkv * kRows * sizeof(float);
+  w.q_off = off;
+  off += static_cast<size_t>(n_layers) * kHkv * kQTileBytes;
+  w.part_o_off = off;
+  off += static_cast<size_t>(max_ctas) * 2 * kRows * kD * 2;
+  w.part_lse_off = off;
+  off += static_cast<size_t>(max_ctas) * 2 * 3 * kRows * sizeof(float);
+  w.total = (off + 1023) & ~static_cast<size_t>(1023);
+  return w;
+}
 
 // ------------------------------------------------------------ decoder-layer projections
 constexpr int kMaxHidden = 8192;   // widest residual stream of the decoder layer

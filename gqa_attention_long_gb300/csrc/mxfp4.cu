@@ -1,4 +1,4 @@
-// mxfp4.cu — the 4-bit cache's writer and reader, and the attention over it.
+// mxfp4.cu — the 4-bit cache's writer and reader.
 //
 // Writer: rows [row0, row0 + n) of K and V, as they come (bf16, fp16 or fp32; any head and row
 // strides), become E2M1 codes and scale bytes in the same rows of the cache. Reader: the same rows as
@@ -106,128 +106,6 @@ cudaError_t launch_mxfp4_rows(const MxRowsParams& p, int n_layers, int dtype, bo
     return cudaLaunchKernelEx(&cfg, write ? mxfp4_write_kernel<__nv_bfloat16> : mxfp4_read_kernel<__nv_bfloat16>, p);
   if (dtype == 1) return cudaLaunchKernelEx(&cfg, write ? mxfp4_write_kernel<__half> : mxfp4_read_kernel<__half>, p);
   return cudaLaunchKernelEx(&cfg, write ? mxfp4_write_kernel<float> : mxfp4_read_kernel<float>, p);
-}
-
-// ------------------------------------------------------------------------------ attention
-// Prologue: q rows normed and roped into the workspace (fp32), the new k rows normed, roped and
-// encoded and the new v rows encoded into the cache. One octet of threads per row; grid
-// (row blocks of 32, kv heads, layers); rows [0, rq) of a unit are its q rows, then tok k rows, then
-// tok v rows.
-__global__ void __launch_bounds__(256) mxfp4_prologue_kernel(const __grid_constant__ MxAttnParams p) {
-  const int g = blockIdx.y, l = blockIdx.z, i = threadIdx.x & 7;
-  const int rq = p.rep * p.tok;
-  const int row0 = blockIdx.x * 32 + (threadIdx.x >> 3), rows = rq + 2 * p.tok;
-  const bool live = row0 < rows;  // octets past the end repeat the last row and store nothing
-  const int row = live ? row0 : rows - 1;
-  pdl_wait_primary();
-  const int kind = row < rq ? 0 : row < rq + p.tok ? 1 : 2;
-  const int rr = kind == 0 ? row : kind == 1 ? row - rq : row - rq - p.tok;
-  const int t = rr % p.tok;
-  const MxAttnLayer& L = p.layer[l];
-  const __nv_bfloat16* src = kind == 0 ? L.q_raw + (static_cast<size_t>(g) * rq + rr) * kD
-                                       : (kind == 1 ? L.k_raw : L.v_raw) + (static_cast<size_t>(g) * p.tok + rr) * kD;
-  const __nv_bfloat16* gam = kind == 0 ? L.q_gamma : L.k_gamma;
-  const int dl = 8 * i, dh = 64 + 8 * i;
-  float xl[8], xh[8], gl[8], gh[8], yl[8], yh[8];
-  unpack_bf16x8(*reinterpret_cast<const uint4*>(src + dl), xl);
-  unpack_bf16x8(*reinterpret_cast<const uint4*>(src + dh), xh);
-  unpack_bf16x8(*reinterpret_cast<const uint4*>(gam + dl), gl);
-  unpack_bf16x8(*reinterpret_cast<const uint4*>(gam + dh), gh);
-  Pair cs[8], sn[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float4 a = p.rot_a[t >> 3][dl + e], b = p.rot_b[t & 7][dl + e];
-    const Pair ca = {a.x, a.y}, sa = {a.z, a.w}, cb = {b.x, b.y}, sb = {b.z, b.w};
-    cs[e] = ca * cb + -(sa * sb);
-    sn[e] = sa * cb + ca * sb;
-  }
-  if (kind == 2) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      yl[e] = xl[e];
-      yh[e] = xh[e];
-    }
-  }
-  float zl[8], zh[8];
-  pair_norm_rope(xl, xh, gl, gh, cs, sn, zl, zh);
-  if (kind != 2) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      yl[e] = zl[e];
-      yh[e] = zh[e];
-    }
-  }
-  uint32_t cl, ch, sc;
-  int el, eh;
-  mx_encode_octet(yl, yh, cl, ch, sc, el, eh);
-  if (!live) return;
-  if (kind == 0) {
-    float* dst = p.q_ws + ((static_cast<size_t>(l) * kHkv + g) * rq + rr) * kD;
-    mx::store8(dst + dl, yl);
-    mx::store8(dst + dh, yh);
-  } else {
-    const size_t crow = static_cast<size_t>(g) * p.Smax + p.new_row0 + rr;
-    uint8_t* codes = (kind == 1 ? L.kc : L.vc) + crow * kMxRowBytes;
-    *reinterpret_cast<uint32_t*>(codes + 4 * i) = cl;
-    *reinterpret_cast<uint32_t*>(codes + 32 + 4 * i) = ch;
-    if (i == 0) *reinterpret_cast<uint32_t*>((kind == 1 ? L.ks : L.vs) + crow * kMxRowScales) = sc;
-    __nv_bfloat16* val = kind == 1 ? L.k_new : L.v_new;
-    if (val != nullptr) {
-      val += (static_cast<size_t>(g) * p.tok + rr) * kD;
-      mx_values8(cl, mx_pow2(el), xl);
-      mx_values8(ch, mx_pow2(eh), xh);
-      mx::store8(val + dl, xl);
-      mx::store8(val + dh, xh);
-    }
-  }
-}
-
-// One warp per query row: lane l holds channels [4l, 4l + 4); online softmax over the keys one by one.
-__global__ void __launch_bounds__(256) mxfp4_attention_kernel(const __grid_constant__ MxAttnParams p) {
-  const int g = blockIdx.y, l = blockIdx.z, lane = threadIdx.x & 31;
-  const int rq = p.rep * p.tok, row = blockIdx.x * 8 + (threadIdx.x >> 5);
-  pdl_wait_primary();
-  const MxAttnLayer& L = p.layer[l];
-  const size_t unit = static_cast<size_t>(l) * kHkv + g;
-  const float4 q = *reinterpret_cast<const float4*>(p.q_ws + (unit * rq + row) * kD + 4 * lane);
-  float m = -INFINITY, sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  const int n = p.first + p.tok;
-  for (int j = 0; j < n; ++j) {
-    const size_t r = static_cast<size_t>(g) * p.Smax + (j < p.first ? j : p.new_row0 + (j - p.first));
-    auto four = [&](const uint8_t* codes, const uint8_t* scales, float (&x)[4]) {
-      const uint32_t w = *reinterpret_cast<const uint16_t*>(codes + r * kMxRowBytes + 2 * lane);
-      const float s = mx_scale(scales[r * kMxRowScales + (lane >> 3)]);
-      float y[8];
-      mx_values8(w, s, y);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = y[e];
-    };
-    float k[4], v[4];
-    four(L.kc, L.ks, k);
-    four(L.vc, L.vs, v);
-    float s = q.x * k[0] + q.y * k[1] + q.z * k[2] + q.w * k[3];
-#pragma unroll
-    for (int x = 16; x >= 1; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    s *= p.scale_log2;
-    const float mn = fmaxf(m, s), a = exp2f(m - mn), w = exp2f(s - mn);
-    m = mn;
-    sum = sum * a + w;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] = o[e] * a + w * v[e];
-  }
-  const float inv = 1.0f / sum;
-  *reinterpret_cast<uint2*>(L.out + (static_cast<size_t>(g) * rq + row) * kD + 4 * lane) =
-      make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
-}
-
-cudaError_t launch_mxfp4_attention(const MxAttnParams& p, int n_layers, cudaLaunchConfig_t cfg) {
-  const int rq = p.rep * p.tok;
-  cfg.blockDim = dim3(256);
-  cfg.gridDim = dim3((rq + 2 * p.tok + 31) / 32, kHkv, n_layers);
-  cudaError_t e = cudaLaunchKernelEx(&cfg, mxfp4_prologue_kernel, p);
-  if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(rq / 8, kHkv, n_layers);
-  return cudaLaunchKernelEx(&cfg, mxfp4_attention_kernel, p);
 }
 
 }  // namespace ea

@@ -136,6 +136,24 @@ __device__ __forceinline__ void pair_norm_rope(const float (&xl)[8], const float
   }
 }
 
+// A q row held by an octet, times the power of two that puts its largest magnitude in [1, 2) (so that f16
+// holds any gain's rows); factor = scale over that power.
+__device__ __forceinline__ void f16_row(float (&yl)[8], float (&yh)[8], float scale, float& factor) {
+  float amax = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fmaxf(fabsf(yl[e]), fabsf(yh[e])));
+#pragma unroll
+  for (int m = 4; m >= 1; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
+  const int e = amax == 0.f ? 0 : min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -126), 126);
+  const float inv = mx_pow2(-e);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    yl[k] *= inv;
+    yh[k] *= inv;
+  }
+  factor = scale * mx_pow2(e);
+}
+
 // Encodes a row held by an octet (lane i: channels [8i, 8i+8) in xl and [64+8i, ..) in xh): each
 // lane's two words of codes, and the four scale bytes of the row (the same in every lane).
 __device__ __forceinline__ void mx_encode_octet(const float (&xl)[8], const float (&xh)[8], uint32_t& cl,

@@ -226,22 +226,12 @@ __device__ __forceinline__ void prepare(const MxDecodeParams& p, uint8_t* smem, 
       sn[e] = p.rot[dl + e].z;
     }
     norm_rope(xl, xh, gl, gh, cs, sn, yl, yh);
-    float amax = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fmaxf(fabsf(yl[e]), fabsf(yh[e])));
-#pragma unroll
-    for (int m = 4; m >= 1; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
-    const int e = amax == 0.f ? 0 : min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -126), 126);
-    const float inv = mx_pow2(-e);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      yl[k] *= inv;
-      yh[k] *= inv;
-    }
+    float factor;
+    f16_row(yl, yh, p.scale_log2, factor);
     uint8_t* q = smem + SM_Q + (buf * kRepText + oct) * kD * 2;
     *reinterpret_cast<uint4*>(q + 2 * dl) = pack8(yl, true);
     *reinterpret_cast<uint4*>(q + 2 * dh) = pack8(yh, true);
-    if (i == 0) reinterpret_cast<float*>(smem + SM_QF)[buf * kRepText + oct] = p.scale_log2 * mx_pow2(e);
+    if (i == 0) reinterpret_cast<float*>(smem + SM_QF)[buf * kRepText + oct] = factor;
     return;
   }
   Pair cs[8], sn[8];
