@@ -19,7 +19,7 @@
 //   warps 0-3, 4-7  softmax of the even / odd tiles of the CTA: thread = query row = TMEM lane
 //   warps 8-11, 12-15  converters of K and of V: thread = key row of the tile; into double-buffered f16 tiles
 //   warps 16, 17  loads of K's and of V's packed rows: one thread, bulk copies into a three-stage ring
-//   warp 18    MMA: one thread issues S = Q K^T, O += P V (P from TMEM) and the next segment's Q load
+//   warps 18, 19  issue S = Q K^T (and load each segment's Q) and O += P V (P from TMEM)
 // TMEM: three score buffers (P(n) goes over S(n)) and one accumulator. QK(n + 2) runs while the softmax
 // of tiles n and n + 1 does, so a softmax warpgroup finds its next scores ready; with two buffers and an
 // accumulator per warpgroup it waited for PV(n) and QK(n + 2) in turn, two thirds of the time. The
@@ -135,7 +135,7 @@ constexpr uint32_t SM_BAR = SM_MAX + 8 * 4;
 // by tile n % 3: FULL and EMPTY (K's ring, V's ring), SFULL, MDONE, PFULL, ODONE; by n % 2: RDY (K's f16 tiles,
 // V's); by n % 8: REF
 constexpr int B_FULL = 0, B_EMPTY = 6, B_SFULL = 12, B_MDONE = 15, B_PFULL = 18, B_ODONE = 21, B_RDY = 24, B_REF = 28,
-              B_QFULL = 36, B_OFREE = 37, B_DRAIN = 38, kNumBars = 39;
+              B_QFULL = 36, B_OFREE = 37, B_DRAIN = 38, kNumBars = 40;
 static_assert(kRing == 3, "barrier indices");
 __device__ __forceinline__ uint32_t bar_count(int b) {
   return b >= B_EMPTY && b < B_SFULL ? kConvert : b >= B_MDONE && b < B_ODONE ? 128 : b >= B_RDY && b < B_REF ? kConvert
@@ -158,18 +158,24 @@ __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// A CTA's tiles as segments: the part [j0, j1) of unit u's tiles that its range holds.
 struct Seg {
-  int u, j0, j1;
+  int u, j0, j1, left;  // left: tiles of the range after this segment
 };
-__device__ __forceinline__ bool next_seg(long long& t, long long end, int T, Seg& s) {
-  if (t >= end) return false;
-  const int ti = static_cast<int>(t);
-  s.u = ti / T;
-  s.j0 = ti - s.u * T;
-  const long long j1 = s.j0 + (end - t);
-  s.j1 = static_cast<int>(j1 < T ? j1 : T);
-  t += s.j1 - s.j0;
-  return true;
+__device__ __forceinline__ Seg first_seg(long long start, long long end, int T) {
+  const int t = static_cast<int>(start), n = static_cast<int>(end - start);
+  Seg s;
+  s.u = t / T;
+  s.j0 = t - s.u * T;
+  s.j1 = min(T, s.j0 + n);
+  s.left = n - (s.j1 - s.j0);
+  return s;
+}
+__device__ __forceinline__ void next_seg(Seg& s, int T) {  // the range's later segments start at their unit's first tile
+  ++s.u;
+  s.j0 = 0;
+  s.j1 = min(T, s.left);
+  s.left -= s.j1;
 }
 
 struct Ctx {
@@ -201,13 +207,13 @@ __device__ __forceinline__ void producer(const MxExpertParams& p, const Ctx cx, 
   const uint32_t ring = cx.sbase + SM_RING + kv * kRing * kStageBytes;
   uint32_t n = 0;
   bool ok = true;
-  long long t = cx.start;
-  Seg s;
-  while (ok && next_seg(t, cx.end, p.T, s)) {
+#pragma unroll 1
+  for (Seg s = first_seg(cx.start, cx.end, p.T); ok && s.j1 > s.j0; next_seg(s, p.T)) {
     const MxAttnLayer& L = p.layer[s.u / kHkv];
     const uint8_t* codes = kv ? L.vc : L.kc;
     const uint8_t* scales = kv ? L.vs : L.ks;
     const size_t head = static_cast<size_t>(s.u % kHkv) * p.Smax;
+#pragma unroll 1
     for (int j = s.j0; j < s.j1; ++j) {
       if (n >= kRing && !cx.wait3(empty, n - kRing, kErrProducerWait)) {
         ok = false;
@@ -282,9 +288,8 @@ __device__ __forceinline__ void converter(const MxExpertParams& p, const Ctx cx,
   volatile uint32_t* tops = reinterpret_cast<volatile uint32_t*>(cx.smem + SM_MAX) + 4 * kv;
   uint32_t n = 0;
   bool ok = true;  // on a wait that gave up: no more work, but every barrier of the warps is still passed
-  long long t = cx.start;
-  Seg s;
-  while (next_seg(t, cx.end, p.T, s)) {
+#pragma unroll 1
+  for (Seg s = first_seg(cx.start, cx.end, p.T); s.j1 > s.j0; next_seg(s, p.T)) {
     int ref = 0;  // as a scale byte
 #pragma unroll 1
     for (int j = s.j0; j < s.j1; ++j, ++n) {
@@ -322,9 +327,10 @@ __device__ __forceinline__ void converter(const MxExpertParams& p, const Ctx cx,
 }
 
 // ------------------------------------------------------------------------------------ MMA
-// QK(n) needs K(n)'s tile, its segment's Q, and score buffer n % 3, which held P(n-3) until PV(n-3) was done.
-// PV(n) needs P(n), V(n)'s tile and, for a segment's first, the accumulator read. Whichever is ready is
-// issued. After a segment's last QK the Q buffer is refilled for the next segment.
+// One warp issues S = Q K^T, another O += P V, each tile by tile as its inputs arrive: QK(n) needs K(n)'s tile, its
+// segment's Q, and score buffer n % 3, which held P(n-3) until PV(n-3) was done; PV(n) needs P(n), V(n)'s tile and,
+// for a segment's first, the accumulator read. (One warp that watched for both took 1,300 cycles a tile to look
+// at its barriers, beside 1,370 to issue.) After a segment's last QK the Q buffer is refilled for the next.
 //
 // The whole warp runs the loop and one elected lane issues: so every operand is uniform over the warp and sits in
 // the uniform registers that the instruction takes. From a lone lane's registers each of an MMA's operands
@@ -339,117 +345,89 @@ constexpr uint64_t kDescK = (1ull << 61 << 1) | (1ull << 46) | (static_cast<uint
 constexpr uint64_t kDescMN = (1ull << 61 << 1) | (1ull << 46) | (static_cast<uint64_t>(1024 >> 4) << 32) |
                              (static_cast<uint64_t>(kAtom >> 4) << 16);
 
-__device__ __forceinline__ void mma_issuer(const MxExpertParams& p, const Ctx cx) {
-  constexpr uint32_t kIdescQK = umma_idesc_f16(128, 128, false, false, false);
-  constexpr uint32_t kIdescPV = umma_idesc_f16(128, 128, false, false, true);
-  const uint32_t total = static_cast<uint32_t>(cx.end - cx.start);
-  const uint64_t qd = kDescK | ((cx.sbase + SM_Q) >> 4), kd = kDescK | ((cx.sbase + SM_K) >> 4),
-                 vd = kDescMN | ((cx.sbase + SM_V) >> 4);
-  auto load_q = [&](int u) {
+__device__ __forceinline__ void qk_issuer(const MxExpertParams& p, const Ctx cx) {
+  constexpr uint32_t kIdesc = umma_idesc_f16(128, 128, false, false, false);
+  const uint64_t qd = kDescK | ((cx.sbase + SM_Q) >> 4), kd = kDescK | ((cx.sbase + SM_K) >> 4);
+  auto wait = [&](int b, uint32_t parity) -> bool { return __all_sync(0xffffffffu, cx.wait(b, parity, kErrMmaWait)); };
+  uint32_t n = 0, b3 = 0, par = 0, loads = 0;  // b3 = n % 3, par = n / 3 & 1
+  bool ok = true;
+#pragma unroll 1
+  for (Seg s = first_seg(cx.start, cx.end, p.T); ok && s.j1 > s.j0; next_seg(s, p.T)) {
+    if (n > 0) ok = wait(B_SFULL + (b3 == 0 ? 2 : b3 - 1), b3 == 0 ? par ^ 1 : par);  // QK(n-1) has read the buffer
+    if (!ok) break;
     if (elect_one()) {
       mbar_expect_tx(cx.bar(B_QFULL), kTile);
-      bulk_load(cx.sbase + SM_Q, p.q_ws + static_cast<size_t>(u) * kQTileBytes, kTile, cx.bar(B_QFULL), l2_policy_evict_first());
+      bulk_load(cx.sbase + SM_Q, p.q_ws + static_cast<size_t>(s.u) * kQTileBytes, kTile, cx.bar(B_QFULL), l2_policy_evict_first());
     }
     __syncwarp();
-  };
-  auto done = [&](int b, uint32_t parity) -> bool { return __all_sync(0xffffffffu, mbar_test_wait(cx.bar(b), parity)); };
-  uint32_t nq = 0, np = 0;        // tiles whose QK, PV is issued
-  uint32_t q3 = 0, q3p = 0, p3 = 0, p3p = 0;  // nq % 3 and the parity of nq / 3; of np
-  uint32_t segq = 0, segp = 0;    // their next tiles' segments
-  long long tq = cx.start, tp = cx.start;
-  Seg sq{}, sp{};
-  int iq = 0, ip = 0;             // the next tiles' places in them
-  next_seg(tq, cx.end, p.T, sq);
-  next_seg(tp, cx.end, p.T, sp);
-  load_q(sq.u);
-  uint32_t q_loads = 1;
-  bool q_ready = false, q_due = false;  // Q of segment segq is there; its load waits for QK(nq - 1)
-  uint64_t t0 = 0;
+    ++loads;
+    ok = wait(B_QFULL, (loads - 1) & 1);
 #pragma unroll 1
-  for (uint32_t it = 0; np < total; ++it) {
-    bool moved = false;
-    if (nq < total) {
-      // (tile nq - 1's barriers: the one before q3; tile nq - 3's: q3, the phase before)
-      if (q_due && done(B_SFULL + (q3 == 0 ? 2 : q3 - 1), q3 == 0 ? q3p ^ 1 : q3p)) {
-        load_q(sq.u);
-        ++q_loads;
-        q_due = false;
-      }
-      if (!q_ready && !q_due) q_ready = done(B_QFULL, segq & 1);
-      if (q_ready && done(B_RDY + (nq & 1), (nq >> 1) & 1) && (nq < 3 || done(B_ODONE + q3, q3p ^ 1))) {
-        tc_fence_after();
-        const uint64_t k0 = kd + (nq & 1) * (kTile >> 4);
-        if (elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint32_t off = ((kk >> 2) * kAtom + (kk & 3) * 32) >> 4;
-            umma_f16_ss(TM_S + q3 * 128, qd + off, k0 + off, kIdescQK, kk > 0);
-          }
-          umma_commit(cx.bar(B_SFULL + q3));
-        }
-        __syncwarp();
-        ++nq;
-        if (++q3 == 3) {
-          q3 = 0;
-          q3p ^= 1;
-        }
-        if (++iq == sq.j1 - sq.j0 && nq < total) {
-          next_seg(tq, cx.end, p.T, sq);
-          iq = 0;
-          ++segq;
-          q_ready = false;
-          q_due = true;
-        }
-        moved = true;
-      }
-    }
-    if (np < nq && done(B_PFULL + p3, p3p) && done(B_RDY + 2 + (np & 1), (np >> 1) & 1) &&
-        (ip > 0 || segp == 0 || done(B_OFREE, (segp - 1) & 1))) {
+    for (int i = s.j1 - s.j0; ok && i > 0; --i) {
+      ok = wait(B_RDY + (n & 1), (n >> 1) & 1) && (n < 3 || wait(B_ODONE + b3, par ^ 1));
+      if (!ok) break;
       tc_fence_after();
-      const uint64_t v0 = vd + (np & 1) * (kTile >> 4);
-      const bool own = sp.j0 + ip >= p.n_main;  // the own tile has 64 keys
+      const uint64_t k0 = kd + (n & 1) * (kTile >> 4);
+      const uint32_t d = TM_S + b3 * 128;
       if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          if (kk < 4 || !own)
-            umma_f16_ts(TM_O, TM_S + p3 * 128 + kk * 8, v0 + kk * (16 * 128 >> 4), kIdescPV, kk > 0 || ip > 0);
-        umma_commit(cx.bar(B_ODONE + p3));
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t off = ((kk >> 2) * kAtom + (kk & 3) * 32) >> 4;
+          umma_f16_ss(d, qd + off, k0 + off, kIdesc, kk > 0);
+        }
+        umma_commit(cx.bar(B_SFULL + b3));
       }
       __syncwarp();
-      ++np;
-      if (++p3 == 3) {
-        p3 = 0;
-        p3p ^= 1;
-      }
-      if (++ip == sp.j1 - sp.j0 && np < total) {
-        next_seg(tp, cx.end, p.T, sp);
-        ip = 0;
-        ++segp;
-      }
-      moved = true;
-    }
-    if (moved) {
-      t0 = 0;
-      it = 0;
-    } else if ((it & 63u) == 63u) {  // bounded like every other wait
-      if (__any_sync(0xffffffffu, *cx.abort_flag != 0u)) break;
-      const uint64_t now = __shfl_sync(0xffffffffu, globaltimer_ns(), 0);
-      if (t0 == 0) t0 = now;
-      if (now - t0 > kWaitLimitNs || it >= 0x7fffffc0u) {
-        if (elect_one()) {
-          *cx.abort_flag = 1u;
-          atomicOr(cx.status, kErrMmaWait);
-        }
-        break;
+      ++n;
+      if (++b3 == 3) {
+        b3 = 0;
+        par ^= 1;
       }
     }
   }
-  __syncwarp();
   // every load and MMA issued is complete before shared memory and TMEM are given back
   if (elect_one()) {
-    if (!drain_wait(cx.bar(B_QFULL), (q_loads - 1) & 1)) atomicOr(cx.status, kErrDrain);
+    if (loads > 0 && !drain_wait(cx.bar(B_QFULL), (loads - 1) & 1)) atomicOr(cx.status, kErrDrain);
     umma_commit(cx.bar(B_DRAIN));
     if (!drain_wait(cx.bar(B_DRAIN), 0)) atomicOr(cx.status, kErrDrain);
+  }
+  __syncwarp();
+}
+
+__device__ __forceinline__ void pv_issuer(const MxExpertParams& p, const Ctx cx) {
+  constexpr uint32_t kIdesc = umma_idesc_f16(128, 128, false, false, true);
+  const uint64_t vd = kDescMN | ((cx.sbase + SM_V) >> 4);
+  auto wait = [&](int b, uint32_t parity) -> bool { return __all_sync(0xffffffffu, cx.wait(b, parity, kErrMmaWait)); };
+  uint32_t n = 0, b3 = 0, par = 0, seg = 0;
+  bool ok = true;
+#pragma unroll 1
+  for (Seg s = first_seg(cx.start, cx.end, p.T); ok && s.j1 > s.j0; next_seg(s, p.T), ++seg) {
+    if (seg > 0) ok = wait(B_OFREE, (seg - 1) & 1);
+#pragma unroll 1
+    for (int j = s.j0; ok && j < s.j1; ++j) {
+      ok = wait(B_RDY + 2 + (n & 1), (n >> 1) & 1) && wait(B_PFULL + b3, par);
+      if (!ok) break;
+      tc_fence_after();
+      const uint64_t v0 = vd + (n & 1) * (kTile >> 4);
+      const uint32_t a = TM_S + b3 * 128, more = j > s.j0;
+      const bool own = j >= p.n_main;  // the own tile has 64 keys
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          if (kk < 4 || !own) umma_f16_ts(TM_O, a + kk * 8, v0 + kk * (16 * 128 >> 4), kIdesc, kk > 0 ? 1u : more);
+        umma_commit(cx.bar(B_ODONE + b3));
+      }
+      __syncwarp();
+      ++n;
+      if (++b3 == 3) {
+        b3 = 0;
+        par ^= 1;
+      }
+    }
+  }
+  if (elect_one()) {
+    umma_commit(cx.bar(B_DRAIN + 1));
+    if (!drain_wait(cx.bar(B_DRAIN + 1), 0)) atomicOr(cx.status, kErrDrain);
   }
   __syncwarp();
 }
@@ -492,9 +470,8 @@ __device__ __forceinline__ void softmax_warps(const MxExpertParams& p, const Ctx
   uint32_t base = 0, seg = 0;
   bool ok = true;
   auto wait3 = [&](int b, uint32_t n) -> bool { return __all_sync(0xffffffffu, cx.wait3(b, n, kErrSoftmaxWait)); };
-  long long t = cx.start;
-  Seg s;
-  while (next_seg(t, cx.end, p.T, s)) {
+#pragma unroll 1
+  for (Seg s = first_seg(cx.start, cx.end, p.T); s.j1 > s.j0; next_seg(s, p.T)) {
     const int nt = s.j1 - s.j0;
     const float qf = p.q_factor[static_cast<size_t>(s.u) * kRows + r] * 0.00390625f;  // K's tiles carry 2^8
     float m = -INFINITY, lsum = 0.f;  // lsum: this warpgroup's keys, in units of 2^m
@@ -681,7 +658,8 @@ __global__ void __launch_bounds__(mxa::kThreads, 1) mxfp4_attention_kernel(const
   } else {
     regs_down<kRegIssue>();
     if (warp < 18 && (threadIdx.x & 31) == 0) producer(p, cx, warp & 1);
-    if (warp == 18) mma_issuer(p, cx);
+    if (warp == 18) qk_issuer(p, cx);
+    if (warp == 19) pv_issuer(p, cx);
   }
   tc_fence_before();
   __syncthreads();
