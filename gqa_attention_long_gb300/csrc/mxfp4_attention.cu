@@ -18,14 +18,18 @@
 // Warp roles (640 threads):
 //   warps 0-3, 4-7  softmax of the even / odd tiles of the CTA: thread = query row = TMEM lane
 //   warps 8-11, 12-15  converters of K and of V: thread = key row of the tile; into double-buffered f16 tiles
-//   warps 16, 17  loads of K's and of V's packed rows: one thread, bulk copies into a three-stage ring
+//   warps 16, 17  load K's and V's packed rows (bulk copies into three-stage rings) and set the tiles' references
 //   warps 18, 19  issue S = Q K^T (and load each segment's Q) and O += P V (P from TMEM)
 // TMEM: three score buffers (P(n) goes over S(n)) and one accumulator. QK(n + 2) runs while the softmax
 // of tiles n and n + 1 does, so a softmax warpgroup finds its next scores ready; with two buffers and an
 // accumulator per warpgroup it waited for PV(n) and QK(n + 2) in turn, two thirds of the time. The
-// price is a running maximum shared by both warpgroups: it is decided tile by tile, from a first pass
-// over the scores, and handed on through shared memory; it moves only when a tile's maximum passes it
-// by 2^8, and the warpgroup that moves it scales the accumulator once PV(n - 1) is done.
+// price is a running maximum shared by both warpgroups. A warpgroup works on tile n with the maximum that it
+// last knew (raised when a chunk passes it by 2^8) and compares notes with tile n - 1's warpgroup at the end,
+// through shared memory: only where the two differ is P(n), or the accumulator, scaled.
+//
+// The instruction cache held earlier forms back: with the roles' loops unrolled, 68 % of the peak of
+// instruction fetches went to the second level and every role crawled (3,600 cycles a tile). So the
+// loops are small, K and V share their code, and what is rare is out of line.
 #include "merge.cuh"
 #include "mxfp4.cuh"
 #include "rope.cuh"
@@ -130,16 +134,15 @@ constexpr uint32_t SM_Q = 0, SM_K = SM_Q + kTile, SM_V = SM_K + 2 * kTile, SM_RI
 constexpr uint32_t SM_X = SM_RING + 2 * kRing * kStageBytes;   // [segment parity][warpgroup][row] (m, l)
 constexpr uint32_t SM_M = SM_X + 4 * kRows * 8;             // [row] running maximum (log2 units)
 constexpr uint32_t SM_REF = SM_M + kRows * 4;               // [K, V][8]: R of tile n % 8
-constexpr uint32_t SM_MAX = SM_REF + 16 * 4;                // [K, V][4 warps]: a reference's raise
-constexpr uint32_t SM_BAR = SM_MAX + 8 * 4;
+constexpr uint32_t SM_BAR = SM_REF + 16 * 4;
 // by tile n % 3: FULL and EMPTY (K's ring, V's ring), SFULL, MDONE, PFULL, ODONE; by n % 2: RDY (K's f16 tiles,
-// V's); by n % 8: REF
+// V's); by n % 8: REF (K's, V's)
 constexpr int B_FULL = 0, B_EMPTY = 6, B_SFULL = 12, B_MDONE = 15, B_PFULL = 18, B_ODONE = 21, B_RDY = 24, B_REF = 28,
-              B_QFULL = 36, B_OFREE = 37, B_DRAIN = 38, kNumBars = 40;
+              B_QFULL = 44, B_OFREE = 45, B_DRAIN = 46, kNumBars = 48;
 static_assert(kRing == 3, "barrier indices");
 __device__ __forceinline__ uint32_t bar_count(int b) {
   return b >= B_EMPTY && b < B_SFULL ? kConvert : b >= B_MDONE && b < B_ODONE ? 128 : b >= B_RDY && b < B_REF ? kConvert
-         : b >= B_REF && b < B_QFULL ? 2 : b == B_OFREE ? kSoftmax : 1;
+         : b == B_OFREE ? kSoftmax : 1;
 }
 constexpr uint32_t SM_TMEM = SM_BAR + kNumBars * 8, SM_ABORT = SM_TMEM + 4;
 constexpr uint32_t kSmemBytes = SM_ABORT + 4 + 1024;  // + slack to align the base
@@ -147,7 +150,7 @@ static_assert(kSmemBytes <= 232448 && SM_RING % 128 == 0 && SM_X % 16 == 0 && SM
 constexpr uint32_t TM_S = 0, TM_O = 384, kTmemCols = 512;  // three score (then P) buffers, the accumulator
 constexpr int kRefField = 23, kMaxField = 26;  // f16 exponent field of 2^(e - R + 8), and its cut (all-zero blocks)
 constexpr float kLazy = 8.0f;
-constexpr uint32_t kBarSoftmax = 1, kBarConvert = 2;  // kBarConvert: K's converters, + 1: V's
+constexpr uint32_t kBarSoftmax = 1;
 
 template <int N>
 __device__ __forceinline__ void regs_up() {
@@ -185,8 +188,17 @@ struct Ctx {
   uint32_t* status;
   long long start, end;
   __device__ __forceinline__ uint32_t bar(int i) const { return sbase + SM_BAR + 8u * i; }
+  // As bounded_wait, in less code: limited by the number of looks (2^20 of them, each of which suspends the thread
+  // for a while, last longer than any wait of a call that works).
   __device__ __forceinline__ bool wait(int b, uint32_t parity, uint32_t err) const {
-    return bounded_wait(bar(b), parity, abort_flag, status, err);
+#pragma unroll 1
+    for (uint32_t it = 0; it < (1u << 20); ++it) {
+      if (mbar_try_wait(bar(b), parity)) return true;
+      if (*abort_flag) return false;
+    }
+    *abort_flag = 1u;
+    atomicOr(status, err);
+    return false;
   }
   // tile n's phase of a barrier of three
   __device__ __forceinline__ bool wait3(int b, uint32_t n, uint32_t err) const { return wait(b + n % 3, (n / 3) & 1, err); }
@@ -200,57 +212,102 @@ __device__ __forceinline__ int tile_live(const MxExpertParams& p, int j) {
 }
 
 // ---------------------------------------------------------------------------------- loads
-// One thread each for K (kv = 0) and V (kv = 1).
+// The largest scale of a block that holds a code other than zero, over the tile's live rows (the whole warp's result;
+// lane: rows lane, lane + 32, ..).
+__device__ __noinline__ int top_nonzero(uint32_t tile, int lane, int live) {
+  uint32_t top = 0;
+#pragma unroll 1
+  for (int i = 4 * lane; i < 4 * live; i += i % 4 == 3 ? 4 * 32 - 3 : 1) {
+    const uint4 c = ld_shared_v4(tile + 16 * i);
+    uint32_t sc;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(sc) : "r"(tile + kCodes + i) : "memory");
+    if (((c.x | c.y | c.z | c.w) & 0x77777777u) != 0u) top = max(top, sc);
+  }
+  return static_cast<int>(__reduce_max_sync(0xffffffffu, top));
+}
+
+// One warp each for K (kv = 0) and V (kv = 1): loads the tiles, and one tile ahead of the converters looks
+// at a tile's scales and publishes its reference.
 __device__ __forceinline__ void producer(const MxExpertParams& p, const Ctx cx, int kv) {
-  const uint64_t pol = l2_policy_evict_first();
+  const int lane = threadIdx.x & 31;
   const int full = B_FULL + kRing * kv, empty = B_EMPTY + kRing * kv;
   const uint32_t ring = cx.sbase + SM_RING + kv * kRing * kStageBytes;
-  uint32_t n = 0;
+  volatile int* refs = reinterpret_cast<volatile int*>(cx.smem + SM_REF) + 8 * kv;
+  const uint32_t total = static_cast<uint32_t>(cx.end - cx.start);
+  Seg l = first_seg(cx.start, cx.end, p.T), v = l;  // of the next tile to load, and of the next to look at
+  int lj = l.j0, vj = v.j0, ref = 0;
+  uint32_t ln = 0;
   bool ok = true;
 #pragma unroll 1
-  for (Seg s = first_seg(cx.start, cx.end, p.T); ok && s.j1 > s.j0; next_seg(s, p.T)) {
-    const MxAttnLayer& L = p.layer[s.u / kHkv];
-    const uint8_t* codes = kv ? L.vc : L.kc;
-    const uint8_t* scales = kv ? L.vs : L.ks;
-    const size_t head = static_cast<size_t>(s.u % kHkv) * p.Smax;
+  for (uint32_t vn = 0; vn < total; ++vn) {
+    // tile vn + 1 is loaded once tile vn - 2, whose slot it takes, is converted; then tile vn is looked at
 #pragma unroll 1
-    for (int j = s.j0; j < s.j1; ++j) {
-      if (n >= kRing && !cx.wait3(empty, n - kRing, kErrProducerWait)) {
-        ok = false;
-        break;
+    while (ok && ln < total && ln <= vn + 1) {
+      if (ln >= kRing) ok = __all_sync(0xffffffffu, cx.wait3(empty, ln - kRing, kErrProducerWait));
+      if (!ok) break;
+      if (lane == 0) {
+        const MxAttnLayer& L = p.layer[l.u / kHkv];
+        const size_t row = static_cast<size_t>(l.u % kHkv) * p.Smax + tile_row0(p, lj);
+        const int live = tile_live(p, lj);
+        // scale words come in fours: up to three rows past the last key (still in the cache) come along
+        const uint32_t cb = live * kMxRowBytes, sb = ((live + 3) & ~3) * kMxRowScales;
+        const uint32_t fb = cx.bar(full + ln % 3), dst = ring + ln % 3 * kStageBytes;
+        const uint64_t pol = l2_policy_evict_first();
+        mbar_expect_tx(fb, cb + sb);
+        bulk_load(dst, (kv ? L.vc : L.kc) + row * kMxRowBytes, cb, fb, pol);
+        bulk_load(dst + kCodes, (kv ? L.vs : L.ks) + row * kMxRowScales, sb, fb, pol);
       }
-      const size_t row = head + tile_row0(p, j);
-      const int live = tile_live(p, j);
-      // scale words come in fours: up to three rows past the last key (still in the cache) come along
-      const uint32_t cb = live * kMxRowBytes, sb = ((live + 3) & ~3) * kMxRowScales;
-      const uint32_t fb = cx.bar(full + n % 3), dst = ring + n % 3 * kStageBytes;
-      mbar_expect_tx(fb, cb + sb);
-      bulk_load(dst, codes + row * kMxRowBytes, cb, fb, pol);
-      bulk_load(dst + kCodes, scales + row * kMxRowScales, sb, fb, pol);
-      ++n;
+      ++ln;
+      if (++lj == l.j1) {
+        next_seg(l, p.T);
+        lj = 0;
+      }
+    }
+    ok = ok && __all_sync(0xffffffffu, cx.wait3(full, vn, kErrProducerWait));
+    if (!ok) break;
+    if (vj == v.j0) ref = 0;  // a segment starts: references of its own
+    const int live = tile_live(p, vj);
+    const uint32_t tile = ring + vn % 3 * kStageBytes;
+    const uint4 sc = ld_shared_v4(tile + kCodes + 16 * lane);  // of four rows
+    const uint32_t a = __vmaxu2(__vmaxu2(sc.x & 0x00FF00FFu, sc.y & 0x00FF00FFu), __vmaxu2(sc.z & 0x00FF00FFu, sc.w & 0x00FF00FFu));
+    const uint32_t b = __vmaxu2(__vmaxu2((sc.x >> 8) & 0x00FF00FFu, (sc.y >> 8) & 0x00FF00FFu),
+                                __vmaxu2((sc.z >> 8) & 0x00FF00FFu, (sc.w >> 8) & 0x00FF00FFu));
+    const uint32_t m = __vmaxu2(a, b);
+    const int high = 4 * lane >= live ? 0 : 4 * lane + 3 >= live ? 255 : static_cast<int>(max(m & 0xFFFFu, m >> 16));
+    if (__any_sync(0xffffffffu, high > ref + (kMaxField - kRefField))) {  // (a ragged end is always looked at closely)
+      const int top = top_nonzero(tile, lane, live);
+      if (top > ref + (kMaxField - kRefField)) ref = top;
+    }
+    if (lane == 0) {
+      refs[vn & 7] = ref;
+      mbar_arrive(cx.bar(B_REF + 8 * kv + (vn & 7)));
+    }
+    if (++vj == v.j1) {
+      next_seg(v, p.T);
+      vj = 0;
     }
   }
+  __syncwarp();
   if (kv) pdl_launch_dependents();
-  if (!ok)  // let every copy already issued land before the CTA gives its shared memory back
-    for (uint32_t k = 1; k <= kRing && k <= n; ++k)
-      if (!drain_wait(cx.bar(full + (n - k) % 3), ((n - k) / 3) & 1)) atomicOr(cx.status, kErrDrain);
+  if (!ok && lane == 0)  // let every copy already issued land before the CTA gives its shared memory back
+    for (uint32_t k = 1; k <= kRing && k <= ln; ++k)
+      if (!drain_wait(cx.bar(full + (ln - k) % 3), ((ln - k) / 3) & 1)) atomicOr(cx.status, kErrDrain);
+  __syncwarp();
 }
 
 // ----------------------------------------------------------------------------- converters
-// The instruction cache, not the issue slots, held an earlier form of this kernel back: with the roles'
-// loops unrolled, 68 % of the peak of instruction fetches went to the second level and every role crawled
-// (3,600 cycles a tile). The loops here are kept small, K and V share one converter.
-
 // Row `row` of a packed tile as f16 into a tile of the swizzled layout: block b's codes times
 // 2^(scale - ref + 8), 0 for a dead row. The lanes take their blocks in an order that spreads them over the banks.
 __device__ __forceinline__ void convert_row(uint32_t dst, uint32_t src, int row, uint32_t scales, int ref, bool live) {
   const uint32_t d = dst + row * 128, from = src + row * kMxRowBytes;
+  const uint32_t add = static_cast<uint32_t>((kRefField - ref) & 0xFFFF) * 0x10001u, cut = live ? kMaxField * 0x10001u : 0u;
+  const uint32_t f02 = __viaddmin_s16x2_relu(scales & 0x00FF00FFu, add, cut) << 10;         // blocks 0 and 2
+  const uint32_t f13 = __viaddmin_s16x2_relu((scales >> 8) & 0x00FF00FFu, add, cut) << 10;  // blocks 1 and 3
 #pragma unroll 1
   for (int i = 0; i < 4; ++i) {
     const int b = (i + (row >> 1)) & 3;
     const uint4 c = ld_shared_v4(from + (b << 4));
-    const int field = static_cast<int>((scales >> (8 * b)) & 255u) - ref + kRefField;
-    const uint32_t f = live ? static_cast<uint32_t>(max(min(field, kMaxField), 0)) * 0x04000400u : 0u;
+    const uint32_t f = __byte_perm(b & 1 ? f13 : f02, 0u, b & 2 ? 0x3232 : 0x1010);
     const uint32_t w[4] = {c.x, c.y, c.z, c.w};
     const uint32_t at = d + (b >> 1) * kAtom;
 #pragma unroll
@@ -263,65 +320,30 @@ __device__ __forceinline__ void convert_row(uint32_t dst, uint32_t src, int row,
     }
   }
 }
-__device__ __forceinline__ int top_byte(uint32_t w) {
-  const uint32_t m = __vmaxu2(w & 0x00FF00FFu, (w >> 8) & 0x00FF00FFu);
-  return static_cast<int>(max(m & 0xFFFFu, m >> 16));
-}
-// the largest scale of the row's blocks that hold a code other than zero
-__device__ __noinline__ uint32_t top_nonzero(uint32_t row_addr, uint32_t scales) {
-  uint32_t top = 0;
-#pragma unroll 1
-  for (int b = 0; b < 4; ++b) {
-    const uint4 c = ld_shared_v4(row_addr + 16 * b);
-    if (((c.x | c.y | c.z | c.w) & 0x77777777u) != 0u) top = max(top, (scales >> (8 * b)) & 255u);
-  }
-  return top;
-}
 
 // One warpgroup each for K (kv = 0) and V (kv = 1).
 __device__ __forceinline__ void converter(const MxExpertParams& p, const Ctx cx, int kv) {
-  const int row = threadIdx.x & 127, warp = row >> 5;
-  const uint32_t bar_id = kBarConvert + kv;
+  const int row = threadIdx.x & 127;
   const int full = B_FULL + kRing * kv, empty = B_EMPTY + kRing * kv, used = kv ? B_ODONE : B_SFULL, rdy = B_RDY + 2 * kv;
   const uint32_t ring = cx.sbase + SM_RING + kv * kRing * kStageBytes, tiles = cx.sbase + (kv ? SM_V : SM_K);
-  volatile int* refs = reinterpret_cast<volatile int*>(cx.smem + SM_REF) + 8 * kv;
-  volatile uint32_t* tops = reinterpret_cast<volatile uint32_t*>(cx.smem + SM_MAX) + 4 * kv;
+  const volatile int* refs = reinterpret_cast<const volatile int*>(cx.smem + SM_REF) + 8 * kv;
   uint32_t n = 0;
-  bool ok = true;  // on a wait that gave up: no more work, but every barrier of the warps is still passed
+  bool ok = true;
 #pragma unroll 1
-  for (Seg s = first_seg(cx.start, cx.end, p.T); s.j1 > s.j0; next_seg(s, p.T)) {
-    int ref = 0;  // as a scale byte
+  for (Seg s = first_seg(cx.start, cx.end, p.T); ok && s.j1 > s.j0; next_seg(s, p.T)) {
 #pragma unroll 1
     for (int j = s.j0; j < s.j1; ++j, ++n) {
       const uint32_t src = ring + n % 3 * kStageBytes;
-      const bool live = row < tile_live(p, j);
-      ok = ok && cx.wait3(full, n, kErrProducerWait);
-      uint32_t sc = 0;
-      if (ok) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(sc) : "r"(src + kCodes + 4 * row) : "memory");
-      if (!live) sc = 0;
-      if (!bar_sync_and(bar_id, kConvert, top_byte(sc) <= ref + (kMaxField - kRefField))) {
-        const uint32_t tp = __reduce_max_sync(0xffffffffu, ok && live ? top_nonzero(src + row * kMxRowBytes, sc) : 0u);
-        if ((row & 31) == 0) tops[warp] = tp;
-        bar_sync(bar_id, kConvert);
-        int mx = 0;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) mx = max(mx, static_cast<int>(tops[w]));
-        bar_sync(bar_id, kConvert);  // read before the next raise writes
-        if (mx > ref + (kMaxField - kRefField)) ref = mx;
-      }
-      // (the softmax has long passed tile n - 8's phase: this group is at most five tiles ahead of it)
-      if (ok && row == 0) {
-        refs[n & 7] = ref;
-        mbar_arrive(cx.bar(B_REF + (n & 7)));
-      }
       // the f16 buffer held tile n - 2: K's is free once QK(n-2) is done, V's once PV(n-2) is
-      if (n >= 2) ok = ok && cx.wait3(used, n - 2, kErrProducerWait);
-      if (ok) {
-        convert_row(tiles + (n & 1) * kTile, src, row, sc, ref, live);
-        fence_proxy_async_smem();
-        mbar_arrive(cx.bar(rdy + (n & 1)));
-        mbar_arrive(cx.bar(empty + n % 3));
-      }
+      ok = cx.wait(B_REF + 8 * kv + (n & 7), (n >> 3) & 1, kErrProducerWait) && cx.wait3(full, n, kErrProducerWait) &&
+           (n < 2 || cx.wait3(used, n - 2, kErrProducerWait));
+      if (!ok) break;
+      uint32_t sc;
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(sc) : "r"(src + kCodes + 4 * row) : "memory");
+      convert_row(tiles + (n & 1) * kTile, src, row, sc, refs[n & 7], row < tile_live(p, j));
+      fence_proxy_async_smem();
+      mbar_arrive(cx.bar(rdy + (n & 1)));
+      mbar_arrive(cx.bar(empty + n % 3));
     }
   }
 }
@@ -446,6 +468,24 @@ __device__ __noinline__ void scale_accumulator(uint32_t addr, float a) {
   tmem_wait_st();
 }
 
+// P of a tile's first `chunks` 64-key chunks: 32 columns of f16 pairs each.
+__device__ __noinline__ void scale_p(uint32_t addr, float a, int chunks) {
+  for (int c = 0; c < chunks; ++c) {
+    uint32_t q[32];
+    tmem_wait_st();
+    tmem_ld32(addr + 32 * c, q);
+    tmem_wait_ld();
+    reg_fence32(q);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+      const float2 f = unpack_f16x2(q[e]);
+      q[e] = pack_f16x2(f.x * a, f.y * a);
+    }
+    tmem_st32(addr + 32 * c, q);
+  }
+  tmem_wait_st();
+}
+
 // Scores of columns [live, cols) of a tile become -inf (a unit's last cache tile), before they are read.
 __device__ __noinline__ void mask_scores(uint32_t addr, int live, int cols) {
   for (int c = live & ~31; c < cols; c += 32) {
@@ -478,7 +518,8 @@ __device__ __forceinline__ void softmax_warps(const MxExpertParams& p, const Ctx
     for (int i = (k ^ static_cast<int>(base)) & 1; ok && i < nt; i += 2) {
       const uint32_t n = base + i;
       const int j = s.j0 + i;
-      ok = __all_sync(0xffffffffu, cx.wait(B_REF + (n & 7), (n >> 3) & 1, kErrSoftmaxWait)) && wait3(B_SFULL, n);
+      ok = __all_sync(0xffffffffu, cx.wait(B_REF + (n & 7), (n >> 3) & 1, kErrSoftmaxWait) &&
+                                       cx.wait(B_REF + 8 + (n & 7), (n >> 3) & 1, kErrSoftmaxWait)) && wait3(B_SFULL, n);
       if (!ok) break;
       tc_fence_after();
       const uint32_t sa = cx.tmem + lane + TM_S + (n % 3) * 128;
@@ -493,55 +534,38 @@ __device__ __forceinline__ void softmax_warps(const MxExpertParams& p, const Ctx
         reg_fence32(v[0]);
         reg_fence32(v[1]);
       };
-      // first pass: the tile's maximum, and the running maximum it leaves for tile n + 1
-      float mx[8];
+      const float2 ct2 = make_float2(ct, ct);
+      float2 ts[4];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) mx[q] = -INFINITY;
+      for (int q = 0; q < 4; ++q) ts[q] = make_float2(0.f, 0.f);
+      // P goes over the scores' first columns: chunk pr's 32 columns of pairs hold scores of chunks <= pr
 #pragma unroll 1
       for (int pr = 0; pr < npair; ++pr) {
         uint32_t v[2][32];
         load_pair(pr, v);
+        float mx[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) mx[q] = -INFINITY;
 #pragma unroll
         for (int ch = 0; ch < 2; ++ch)
 #pragma unroll
           for (int e = 0; e < 32; e += 2)
             mx[(e >> 1) & 7] = fmax3(mx[(e >> 1) & 7], __uint_as_float(v[ch][e]), __uint_as_float(v[ch][e + 1]));
-      }
-      const float mc = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * ct;
-      float before = -INFINITY, scale = 1.f;
-      if (i > 0) {
-        ok = wait3(B_MDONE, n - 1);
-        if (!ok) break;
-        before = *run;
-        const int from = refs[8 + ((n - 1) & 7)];  // V's reference of the tile before, in the same segment
-        if (from != ref) scale = from - ref < -126 ? 0.f : mx_pow2(from - ref);
-      }
-      // (every tile holds a key, so the maximum is finite from the segment's first tile on)
-      const float mn = mc > before + kLazy || before == -INFINITY ? fmaxf(before, mc) : before;
-      *run = mn;
-      mbar_arrive(cx.bar(B_MDONE + n % 3));
-      if (i > 0) {
-        scale *= ex2_approx(before - mn);
-        if (__any_sync(0xffffffffu, scale != 1.f)) {  // the accumulator moves: stable once PV(n-1) is done
-          ok = wait3(B_ODONE, n - 1);
-          if (!ok) break;
-          tc_fence_after();
-          scale_accumulator(oa, scale);
-        }
-      }
-      if (m != mn) {
-        lsum *= ex2_approx(m - mn);  // (0 for this warpgroup's first tile)
-        m = mn;
-      }
-      // second pass: P over the scores' first columns (chunk pr's 32 columns of pairs hold scores of chunks <= pr)
-      const float2 ct2 = make_float2(ct, ct), neg = make_float2(-m, -m);
-      float2 ts[4];
+        const float mc = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * ct;
+        // (chunk 0 always holds a key, so m is finite from there on)
+        const bool up = mc > m + kLazy || m == -INFINITY;
+        if (__any_sync(0xffffffffu, up)) {
+          const float mn = up ? fmaxf(m, mc) : m, a = ex2_approx(m - mn);
+          if (pr > 0) {  // the first chunk's P moves too
+            scale_p(sa, a, 1);
+            load_pair(pr, v);
+          }
 #pragma unroll
-      for (int q = 0; q < 4; ++q) ts[q] = make_float2(0.f, 0.f);
-#pragma unroll 1
-      for (int pr = 0; pr < npair; ++pr) {
-        uint32_t v[2][32];
-        load_pair(pr, v);
+          for (int q = 0; q < 4; ++q) ts[q] = make_float2(ts[q].x * a, ts[q].y * a);
+          lsum *= a;
+          m = mn;
+        }
+        const float2 neg = make_float2(-m, -m);
 #pragma unroll
         for (int ch = 0; ch < 2; ++ch) {
           uint32_t pk[16];
@@ -557,6 +581,27 @@ __device__ __forceinline__ void softmax_warps(const MxExpertParams& p, const Ctx
       }
       lsum += ((ts[0].x + ts[0].y) + (ts[1].x + ts[1].y)) + ((ts[2].x + ts[2].y) + (ts[3].x + ts[3].y));
       tmem_wait_st();
+      // the maximum that tile n - 1 left: the larger one holds from here on
+      float scale = 1.f;  // of the accumulator
+      if (i > 0) {
+        ok = wait3(B_MDONE, n - 1);
+        if (!ok) break;
+        const float before = *run, mn = fmaxf(m, before), a = ex2_approx(m - mn);
+        if (__any_sync(0xffffffffu, a != 1.f)) scale_p(sa, a, npair);
+        lsum *= a;
+        m = mn;
+        scale = ex2_approx(before - mn);
+        const int from = refs[8 + ((n - 1) & 7)];  // V's reference of the tile before, in the same segment
+        if (from != ref) scale = from - ref < -126 ? 0.f : scale * mx_pow2(from - ref);
+      }
+      *run = m;
+      mbar_arrive(cx.bar(B_MDONE + n % 3));
+      if (__any_sync(0xffffffffu, scale != 1.f)) {  // the accumulator moves: stable once PV(n-1) is done
+        ok = wait3(B_ODONE, n - 1);
+        if (!ok) break;
+        tc_fence_after();
+        scale_accumulator(oa, scale);
+      }
       tc_fence_before();
       mbar_arrive(cx.bar(B_PFULL + n % 3));
     }
@@ -573,48 +618,50 @@ __device__ __forceinline__ void softmax_warps(const MxExpertParams& p, const Ctx
       const float2 x0 = xch[r], x1 = xch[kRows + r];
       const float M = fmaxf(x0.x, x1.x);  // the maximum never falls, so the last tile's is the larger
       const float L = ex2_approx(x0.x - M) * x0.y + ex2_approx(x1.x - M) * x1.y;
-      const float inv = 1.0f / L;
       // O is in units of 2^(R - 127 - 8)
-      const float two_r = mx_scale(refs[8 + (last & 7)]);
+      const float inv = 1.0f / L * 0.00390625f, two_r = mx_scale(refs[8 + (last & 7)]);
       const int l = s.u / kHkv, g = s.u % kHkv;
       const bool full = s.j0 == 0 && s.j1 == p.T;
-      float o[64];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t v[32];
-        tmem_ld32(oa + 64 * k + 32 * h, v);
+      const uint32_t col = oa + 64 * k;
+      // columns [8 c, 8 c + 8) of the half row
+      auto load8 = [&](int c, float (&o)[8]) {
+        uint32_t v[8];
+        tmem_ld8(col + 8 * c, v);
         tmem_wait_ld();
-        reg_fence32(v);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[32 * h + e] = __uint_as_float(v[e]);
-      }
-      tc_fence_before();
-      mbar_arrive(cx.bar(B_OFREE));  // the accumulator is read
-#pragma unroll
-      for (int e = 0; e < 64; ++e) o[e] = o[e] * inv * 0.00390625f * two_r;
+        for (int e = 0; e < 8; ++e) o[e] = __uint_as_float(v[e]) * inv * two_r;
+      };
+      float o[8], up = 1.f;
+      uint4* dst;
+      size_t step = 1;
       if (full) {
-        __nv_bfloat16* dst = p.layer[l].out + (static_cast<size_t>(g) * kRows + r) * kD + 64 * k;
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          *reinterpret_cast<uint4*>(dst + 8 * c) =
-              make_uint4(pack_bf16x2(o[8 * c], o[8 * c + 1]), pack_bf16x2(o[8 * c + 2], o[8 * c + 3]),
-                         pack_bf16x2(o[8 * c + 4], o[8 * c + 5]), pack_bf16x2(o[8 * c + 6], o[8 * c + 7]));
+        dst = reinterpret_cast<uint4*>(p.layer[l].out + (static_cast<size_t>(g) * kRows + r) * kD + 64 * k);
       } else {
         // a part: f16, the half row times the power of two that puts its largest magnitude in [2^14, 2^15)
         const size_t sl = static_cast<size_t>(blockIdx.x) * 2 + (base == 0 ? 0 : 1);
         float amax = 0.f;
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+          load8(c, o);
 #pragma unroll
-        for (int e = 0; e < 64; ++e) amax = fmaxf(amax, fabsf(o[e]));
+          for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(o[e]));
+        }
         const int ex = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 14, -126), 112);
-        const float up = mx_pow2(-ex);
-        uint4* po = p.part_o + (sl * kPartChunks + 8 * k) * kRows + r;
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          po[c * kRows] = make_uint4(pack_f16x2(o[8 * c] * up, o[8 * c + 1] * up), pack_f16x2(o[8 * c + 2] * up, o[8 * c + 3] * up),
-                                     pack_f16x2(o[8 * c + 4] * up, o[8 * c + 5] * up), pack_f16x2(o[8 * c + 6] * up, o[8 * c + 7] * up));
+        up = mx_pow2(-ex);
+        dst = p.part_o + (sl * kPartChunks + 8 * k) * kRows + r;
+        step = kRows;
         p.part_lse[(sl * 3 + 1 + k) * kRows + r] = mx_pow2(ex);
         if (k == 0) p.part_lse[sl * 3 * kRows + r] = M + log2f(L);
       }
+#pragma unroll 1
+      for (int c = 0; c < 8; ++c) {
+        load8(c, o);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] *= up;
+        dst[c * step] = pack8(o, !full);
+      }
+      tc_fence_before();
+      mbar_arrive(cx.bar(B_OFREE));  // the accumulator is read
     }
     base += nt;
     ++seg;
@@ -657,7 +704,7 @@ __global__ void __launch_bounds__(mxa::kThreads, 1) mxfp4_attention_kernel(const
     converter(p, cx, warp >= 12);
   } else {
     regs_down<kRegIssue>();
-    if (warp < 18 && (threadIdx.x & 31) == 0) producer(p, cx, warp & 1);
+    if (warp < 18) producer(p, cx, warp & 1);
     if (warp == 18) qk_issuer(p, cx);
     if (warp == 19) pv_issuer(p, cx);
   }
