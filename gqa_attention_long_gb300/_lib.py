@@ -444,10 +444,11 @@ def alloc_mxfp4_cache(Smax: int, device="cuda") -> Mxfp4Cache:
 
 
 class _Arr:
-    """A marshalled argument array, the device its tensors are on, and (rows) their type and strides."""
+    """A marshalled argument array with the buffers that it points into, the device they are on, and (rows) their
+    type and strides."""
 
-    def __init__(self, arr, device, dtype=None, strides=(0, 0), n_rows=0, Smax=0):
-        self.arr, self.n, self.device, self.dtype, self.strides = arr, len(arr), device, dtype, strides
+    def __init__(self, arr, layers, device, dtype=None, strides=(0, 0), n_rows=0, Smax=0):
+        self.arr, self.layers, self.n, self.device, self.dtype, self.strides = arr, layers, len(arr), device, dtype, strides
         self.n_rows, self.Smax = n_rows, Smax
 
 
@@ -458,11 +459,21 @@ def _one_device(tensors, what: str) -> int:
     return devices.pop()
 
 
-def _current(a: _Arr, Smax: int, ws: torch.Tensor | None = None) -> None:
-    if a.device != torch.cuda.current_device() or (ws is not None and ws.device.index != a.device):
+# The calls below are launch-bound on small caches: what torch offers as plain numbers is taken as such (a Stream
+# object costs 3 us a call).
+_device_now = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_stream_now = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _current(a: _Arr, Smax: int, stream, ws: torch.Tensor | None = None) -> int | None:
+    """Checks a call's arguments against its marshalled ones; the stream's handle."""
+    if a.device != _device_now() or (ws is not None and ws.get_device() != a.device):
         raise ValueError(f"the tensors are on cuda:{a.device}, which must be the current device (and the workspace's)")
     if a.Smax != Smax:
         raise ValueError(f"the arguments were made for caches of {a.Smax} rows, not {Smax}")
+    if ws is not None and (ws.dtype is not torch.uint8 or not ws.is_contiguous()):
+        raise TypeError("workspace must be a contiguous uint8 tensor")
+    return _stream_now(a.device) if stream is None and _stream_now is not None else _stream(stream)
 
 
 def _mx_cache(a, c: Mxfp4Cache, Smax: int) -> None:
@@ -502,18 +513,19 @@ def make_rows_args(layers: list[Mxfp4Rows], Smax: int) -> _Arr:
         a.k, a.v = L.k.data_ptr(), L.v.data_ptr()
         _mx_cache(a, L.cache, Smax)
     dev = _one_device([t for L in layers for t in (L.k, L.v, *L.cache.__dict__.values())], "rows")
-    return _Arr(arr, dev, _ROWS_DTYPES[first.dtype], (first.stride(0), first.stride(1)), first.shape[1], Smax)
+    return _Arr(arr, list(layers), dev, _ROWS_DTYPES[first.dtype], (first.stride(0), first.stride(1)), first.shape[1], Smax)
 
 
 def _rows_call(fn: str, layers, row0: int, n_rows: int, Smax: int, stream, a: _Arr | None) -> None:
     a = a if a is not None else make_rows_args(layers, Smax)
-    _current(a, Smax)
+    st = _current(a, Smax, stream)
     if n_rows > a.n_rows:
         raise ValueError(f"k and v have {a.n_rows} rows, {n_rows} are asked for")
     if n_rows == 0:
         return
-    _check(fn, getattr(lib(), fn)(a.arr, a.n, int(row0), int(n_rows), int(Smax), a.dtype, a.strides[0], a.strides[1],
-                                  _stream(stream)))
+    rc = getattr(_lib_handle or lib(), fn)(a.arr, a.n, int(row0), int(n_rows), int(Smax), a.dtype, *a.strides, st)
+    if rc:
+        _check(fn, rc)
 
 
 def expert_attn_write_mxfp4(layers: list[Mxfp4Rows], row0: int, n_rows: int, Smax: int, stream=None, _arr=None) -> None:
@@ -565,7 +577,7 @@ def _mx_attn_args(layers, Smax: int, hq: int, tok: int) -> _Arr:
         _mx_cache(a, L.cache, Smax)
     dev = _one_device([t for L in layers for t in (L.q_raw, L.k_raw, L.v_raw, L.q_gamma, L.k_gamma, L.out, L.k_new, L.v_new,
                                                    *L.cache.__dict__.values())], "layers")
-    return _Arr(arr, dev, Smax=Smax)
+    return _Arr(arr, list(layers), dev, Smax=Smax)
 
 
 def make_decode_mxfp4_args(layers: list[DecodeMxfp4Buffers], Smax: int) -> _Arr:
@@ -610,10 +622,11 @@ def text_decode_attention_mxfp4(layers: list[DecodeMxfp4Buffers], pos: int, Smax
                                 stream=None, _arr=None) -> None:
     """One decode step over 4-bit caches: the new row quantised into row pos, then attention over rows [0, pos]."""
     a = _arr if _arr is not None else make_decode_mxfp4_args(layers, Smax)
-    _current(a, Smax, ws)
-    p, n = _ws(ws)
-    _check("text_decode_attention_mxfp4", lib().text_decode_attention_mxfp4(
-        a.arr, a.n, int(pos), int(Smax), int(rope_delta), p, n, _stream(stream)))
+    st = _current(a, Smax, stream, ws)
+    rc = (_lib_handle or lib()).text_decode_attention_mxfp4(a.arr, a.n, int(pos), int(Smax), int(rope_delta), ws.data_ptr(),
+                                                               ws.numel(), st)
+    if rc:
+        _check("text_decode_attention_mxfp4", rc)
 
 
 def expert_attn_layers_mxfp4(layers: list[LayerMxfp4Buffers], S: int, Smax: int, rope_delta: int, ws: torch.Tensor,
@@ -621,7 +634,8 @@ def expert_attn_layers_mxfp4(layers: list[LayerMxfp4Buffers], S: int, Smax: int,
     """The expert's attention over 4-bit caches: the own rows quantised into rows [Smax-64, Smax), then attention
     over rows [0, S) and the own rows."""
     a = _arr if _arr is not None else make_mxfp4_args(layers, Smax)
-    _current(a, Smax, ws)
-    p, n = _ws(ws)
-    _check("expert_attn_layers_mxfp4", lib().expert_attn_layers_mxfp4(
-        a.arr, a.n, int(S), int(Smax), int(rope_delta), p, n, _stream(stream)))
+    st = _current(a, Smax, stream, ws)
+    rc = (_lib_handle or lib()).expert_attn_layers_mxfp4(a.arr, a.n, int(S), int(Smax), int(rope_delta), ws.data_ptr(),
+                                                            ws.numel(), st)
+    if rc:
+        _check("expert_attn_layers_mxfp4", rc)

@@ -1176,42 +1176,55 @@ int run_mx_rows(const ea_mxfp4_rows* a, int n_layers, int row0, int n_rows, int 
   return EA_OK;
 }
 
-// Rotations of positions p0 + t, t < 64 (see MxPrologueParams): rot_a[i] at p0 + 8 i, rot_b[i] at i, in
-// 64 bits (a far position's angle needs them), split into fp32 pairs. The angles of i and 8 i are
-// formed once per process.
-float4 split_rotation(double c, double s) {
-  const float ch = static_cast<float>(c), sh = static_cast<float>(s);
-  return make_float4(ch, static_cast<float>(c - ch), sh, static_cast<float>(s - sh));
-}
-
-struct MxSteps {  // the frequencies 5e6^(-j/64), and the rotations by i and 8 i positions
-  double f[kD / 2], c8[kTok / 8][kD / 2], s8[kTok / 8][kD / 2];
-  float4 b[8][kD / 2];
-};
-const MxSteps& mx_steps() {
-  static MxSteps st;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    for (int j = 0; j < kD / 2; ++j) {
-      st.f[j] = std::pow(5.0e6, -static_cast<double>(j) / (kD / 2));
-      for (int i = 0; i < 8; ++i) {
-        st.c8[i][j] = std::cos(8 * i * st.f[j]);
-        st.s8[i][j] = std::sin(8 * i * st.f[j]);
-        st.b[i][j] = split_rotation(std::cos(i * st.f[j]), std::sin(i * st.f[j]));
-      }
-    }
-  });
-  return st;
-}
-
-void mx_rotations(long long p0, MxPrologueParams* p) {
-  const MxSteps& st = mx_steps();
-  for (int j = 0; j < kD / 2; ++j) {
-    const double a = static_cast<double>(p0) * st.f[j], c = std::cos(a), s = std::sin(a);
-    for (int i = 0; i < kTok / 8; ++i)
-      p->rot_a[i][j] = split_rotation(c * st.c8[i][j] - s * st.s8[i][j], s * st.c8[i][j] + c * st.s8[i][j]);
+// Cosines and sines of pos * 5e6^(-j/64), |pos| < 2^24, in 64 bits (a far position's angle needs them): the product of
+// four rotations, by the position's base-64 digits, from a table that is formed once per process (64 library
+// sines and cosines would be half of a small call's time on the host).
+class MxRotations {
+ public:
+  struct Cis {
+    double c, s;
+  };
+  static const MxRotations& get() {
+    static const MxRotations r;
+    return r;
   }
-  std::memcpy(p->rot_b, st.b, sizeof(st.b));
+  Cis at(long long pos, int j) const {
+    const uint32_t a = static_cast<uint32_t>(pos < 0 ? -pos : pos);
+    Cis r = t_[0][a & 63][j];
+    for (int d = 1; d < 4; ++d)
+      if (const uint32_t k = (a >> (6 * d)) & 63) r = mul(r, t_[d][k][j]);
+    if (pos < 0) r.s = -r.s;
+    return r;
+  }
+  static Cis mul(const Cis& a, const Cis& b) { return {a.c * b.c - a.s * b.s, a.s * b.c + a.c * b.s}; }
+  // as fp32 pairs: cosine x + y, sine z + w
+  static float4 split(const Cis& a) {
+    const float c = static_cast<float>(a.c), s = static_cast<float>(a.s);
+    return make_float4(c, static_cast<float>(a.c - c), s, static_cast<float>(a.s - s));
+  }
+
+ private:
+  MxRotations() {
+    for (int j = 0; j < kD / 2; ++j) {
+      const double f = std::pow(5.0e6, -static_cast<double>(j) / (kD / 2));
+      for (int d = 0; d < 4; ++d)
+        for (int k = 0; k < 64; ++k) {
+          const double x = std::ldexp(static_cast<double>(k), 6 * d) * f;
+          t_[d][k][j] = {std::cos(x), std::sin(x)};
+        }
+    }
+  }
+  Cis t_[4][64][kD / 2];
+};
+
+// Rotations of positions p0 + t, t < 64 (see MxPrologueParams): rot_a[i] at p0 + 8 i, rot_b[i] at i.
+void mx_rotations(long long p0, MxPrologueParams* p) {
+  const MxRotations& r = MxRotations::get();
+  for (int j = 0; j < kD / 2; ++j) {
+    const MxRotations::Cis base = r.at(p0, j);
+    for (int i = 0; i < kTok / 8; ++i) p->rot_a[i][j] = MxRotations::split(MxRotations::mul(base, r.at(8 * i, j)));
+    for (int i = 0; i < 8; ++i) p->rot_b[i][j] = MxRotations::split(r.at(i, j));
+  }
 }
 
 template <class A>
@@ -1264,10 +1277,7 @@ int run_mx_decode(const ea_decode_mxfp4_args* a, int n_layers, int pos, int Smax
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   MxDecodeParams p;
   std::memset(&p, 0, sizeof(p));
-  for (int j = 0; j < kD / 2; ++j) {
-    const double x = static_cast<double>(p0) * mx_steps().f[j];
-    p.rot[j] = split_rotation(std::cos(x), std::sin(x));
-  }
+  for (int j = 0; j < kD / 2; ++j) p.rot[j] = MxRotations::split(MxRotations::get().at(p0, j));
   p.part_o = reinterpret_cast<float*>(ws + wl.part_o_off);
   p.part_lse = reinterpret_cast<float*>(ws + wl.part_ml_off);
   p.unit_cnt = reinterpret_cast<uint32_t*>(ws + wl.cnt_off);
@@ -1280,7 +1290,8 @@ int run_mx_decode(const ea_decode_mxfp4_args* a, int n_layers, int pos, int Smax
     const int n = n_layers - l0 < per ? n_layers - l0 : per;
     for (int l = 0; l < n; ++l) p.layer[l] = mx_layer(a[l0 + l]);
     const uint32_t units = static_cast<uint32_t>(n) * kHkv, sms = static_cast<uint32_t>(di.sm_count);
-    const uint32_t W = units * p.T, full = (p.T + 7) / 8;  // parts of at most eight chunks: one per warp
+    const uint32_t W = units * p.T;
+    const uint32_t full = (p.T + kMxDecodeWarps - 1) / kMxDecodeWarps;  // parts of at most one chunk per warp
     uint32_t grid;
     if (units <= sms && (units * full <= sms || sms / units * units * 20 >= sms * 19)) {
       p.parts = full < sms / units ? full : sms / units;

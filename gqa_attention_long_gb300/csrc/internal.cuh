@@ -276,7 +276,8 @@ struct MxDecodeParams {
   int pos, Smax;
   float scale_log2;     // log2(e) / sqrt(128)
 };
-constexpr int kMxDecodeKeys = 32;
+constexpr int kMxDecodeKeys = 32, kMxDecodeWarps = 12;
+constexpr int kMxMaxParts = 32;  // parts of a unit that one warp can weigh
 
 // The expert's attention over 4-bit caches (mxfp4_attention.cu).
 struct MxPrologueParams {

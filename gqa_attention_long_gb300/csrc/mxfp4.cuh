@@ -100,8 +100,19 @@ __device__ __forceinline__ Pair operator*(Pair a, Pair b) {
   return pair_fast_sum(p, __fmaf_rn(a.h, b.l, __fmaf_rn(a.l, b.h, __fmaf_rn(a.h, b.h, -p))));
 }
 
-// 1 / sqrt(mean of the row's 128 squares + 1e-6), the row held by an octet as in norm_rope
-// (lane i: channels [8i, 8i+8) and [64+8i, 64+8i+8)). A square of a bf16 number is exact in fp32.
+// 1 / sqrt(ss / 128 + 1e-6)
+__device__ __forceinline__ Pair pair_rsqrt_mean(Pair ss) {
+  constexpr double kEps = 1e-6;
+  constexpr float kEpsHi = static_cast<float>(kEps), kEpsLo = static_cast<float>(kEps - kEpsHi);
+  const Pair m = Pair{ss.h * (1.0f / kD), ss.l * (1.0f / kD)} + Pair{kEpsHi, kEpsLo};
+  // one Newton step from the hardware estimate r: r (1 + e/2 + 3 e^2 / 8), e = 1 - m r^2
+  const float r = rsqrtf(m.h);
+  const Pair u = m * (Pair{r, 0.f} * r);
+  const float e = __fadd_rn(__fadd_rn(1.0f, -u.h), -u.l);
+  return pair_fast_sum(r, r * fmaf(0.375f * e, e, 0.5f * e));
+}
+// ... from the row's 128 squares, the row held by an octet as in norm_rope (lane i: channels [8i, 8i+8) and
+// [64+8i, 64+8i+8)). A square of a bf16 number is exact in fp32.
 __device__ __forceinline__ Pair pair_inv_rms(const float (&xl)[8], const float (&xh)[8]) {
   Pair ss = {0.f, 0.f};
 #pragma unroll
@@ -112,14 +123,7 @@ __device__ __forceinline__ Pair pair_inv_rms(const float (&xl)[8], const float (
 #pragma unroll
   for (int m = 4; m >= 1; m >>= 1)
     ss = ss + Pair{__shfl_xor_sync(0xffffffffu, ss.h, m), __shfl_xor_sync(0xffffffffu, ss.l, m)};
-  constexpr double kEps = 1e-6;
-  constexpr float kEpsHi = static_cast<float>(kEps), kEpsLo = static_cast<float>(kEps - kEpsHi);
-  const Pair m = Pair{ss.h * (1.0f / kD), ss.l * (1.0f / kD)} + Pair{kEpsHi, kEpsLo};
-  // one Newton step from the hardware estimate r: r (1 + e/2 + 3 e^2 / 8), e = 1 - m r^2
-  const float r = rsqrtf(m.h);
-  const Pair u = m * (Pair{r, 0.f} * r);
-  const float e = __fadd_rn(__fadd_rn(1.0f, -u.h), -u.l);
-  return pair_fast_sum(r, r * fmaf(0.375f * e, e, 0.5f * e));
+  return pair_rsqrt_mean(ss);
 }
 
 // The normed, rotated row rounded to fp32: channels as in norm_rope; cs and sn are the eight angles'
@@ -152,6 +156,40 @@ __device__ __forceinline__ void f16_row(float (&yl)[8], float (&yh)[8], float sc
     yh[k] *= inv;
   }
   factor = scale * mx_pow2(e);
+}
+
+// The same of one row held by a whole warp (lane i: channels 2i, 2i + 1 and 64 + 2i, 65 + 2i), for a row
+// that something waits for: a quarter of the octet's steps.
+__device__ __forceinline__ void pair_norm_rope_warp(const float (&x)[4], const float (&g)[4], const Pair (&cs)[2],
+                                                    const Pair (&sn)[2], float (&y)[4]) {
+  Pair ss = {__fmul_rn(x[0], x[0]), 0.f};
+#pragma unroll
+  for (int e = 1; e < 4; ++e) ss = ss + Pair{__fmul_rn(x[e], x[e]), 0.f};
+#pragma unroll
+  for (int m = 16; m >= 1; m >>= 1)
+    ss = ss + Pair{__shfl_xor_sync(0xffffffffu, ss.h, m), __shfl_xor_sync(0xffffffffu, ss.l, m)};
+  const Pair rs = pair_rsqrt_mean(ss);
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const float nl = __fmul_rn(x[e], g[e]), nh = __fmul_rn(x[2 + e], g[2 + e]);
+    y[e] = ((cs[e] * nl + -(sn[e] * nh)) * rs).h;
+    y[2 + e] = ((cs[e] * nh + sn[e] * nl) * rs).h;
+  }
+}
+// Encodes such a row: the lane's byte of codes (2i, 2i + 1) and of (64 + 2i, ..), its blocks' exponents (block i / 16 and
+// 2 + i / 16).
+__device__ __forceinline__ void mx_encode_warp(const float (&x)[4], uint32_t& cl, uint32_t& ch, int& el, int& eh) {
+  float al = fmaxf(fabsf(x[0]), fabsf(x[1])), ah = fmaxf(fabsf(x[2]), fabsf(x[3]));
+#pragma unroll
+  for (int m = 8; m >= 1; m >>= 1) {
+    al = fmaxf(al, __shfl_xor_sync(0xffffffffu, al, m));
+    ah = fmaxf(ah, __shfl_xor_sync(0xffffffffu, ah, m));
+  }
+  el = mx_exponent(al);
+  eh = mx_exponent(ah);
+  const float l[8] = {x[0], x[1]}, h[8] = {x[2], x[3]};
+  cl = mx_pack8(l, mx_pow2(-el)) & 0xFFu;
+  ch = mx_pack8(h, mx_pow2(-eh)) & 0xFFu;
 }
 
 // Encodes a row held by an octet (lane i: channels [8i, 8i+8) in xl and [64+8i, ..) in xh): each

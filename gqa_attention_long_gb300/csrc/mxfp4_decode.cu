@@ -26,7 +26,7 @@
 //
 // Work decomposition: the units' keys in chunks of 32, unit-major, one contiguous range per CTA; a CTA's
 // eight compute warps take its chunks in turn. At the end of a unit the warps' partials meet in
-// shared memory; a unit cut over several CTAs is merged by the part that finishes last. Three further
+// shared memory; a unit cut over several CTAs is merged by the part that finishes last. Four further
 // warps prepare the next unit's q rows and encode the new rows.
 #include "mxfp4.cuh"
 #include "rope.cuh"
@@ -34,9 +34,9 @@
 namespace ea {
 namespace mxd {
 
-constexpr int kWarps = 12;                   // compute warps (at least 8: a unit's merge takes one per head)
+constexpr int kWarps = kMxDecodeWarps;       // compute warps (at least 8: a unit's merge takes one per head)
 constexpr int kCompute = 32 * kWarps;
-constexpr int kPrep = 96;                    // 12 octets: 8 q rows, the k row, the v row
+constexpr int kPrep = 128;                   // two warps for the 8 q rows, one each for the k row and the v row
 constexpr int kThreads = kCompute + kPrep;
 constexpr int kKeys = 32;                    // keys per chunk
 constexpr int kStages = 3;
@@ -120,6 +120,11 @@ __device__ __forceinline__ uint2 ld_shared_v2(uint32_t a) {
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
   return v;
 }
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int m = 16; m >= 1; m >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, m));
+  return x;
+}
 // x << 4 as a product: the multipliers are idle here, the logic pipe is what bounds the warps
 __device__ __forceinline__ uint32_t times16(uint32_t x) {
   uint32_t r;
@@ -198,33 +203,27 @@ __device__ __forceinline__ void load_chunk(const MxDecodeParams& p, const Cursor
 }
 
 // ------------------------------------------------------------------------------ preparation
-// Unit u's q rows (octets 0-7: normed, roped, f16 times a power of two that puts the row's largest
-// magnitude in [1, 2)), and, when the segment holds the unit's last chunk, the new k row (octet 8) and v
-// row (octet 9): into shared memory for this CTA, into the cache, and their values to the caller.
+// Unit u's q rows (warps 0 and 1, an octet each: normed, roped, f16 times a power of two that puts the row's
+// largest magnitude in [1, 2)), and, when the segment holds the unit's last chunk, the new k row (warp 2) and v
+// row (warp 3): into shared memory for this CTA, into the cache, and their values to the caller.
 __device__ __forceinline__ void prepare(const MxDecodeParams& p, uint8_t* smem, uint32_t u, bool last, int buf, int tid) {
-  const int oct = tid >> 3, i = tid & 7;
   const int l = u / kHkv, g = u % kHkv;
-  if (tid >= 64 && !last) return;
   const MxAttnLayer& L = p.layer[l];
-  const int dl = 8 * i, dh = 64 + 8 * i;
-  const int kind = oct < 8 ? 0 : oct == 8 ? 1 : 2;  // the last two octets repeat octet 9 and store nothing
-  const __nv_bfloat16* src = kind == 0 ? L.q_raw + (static_cast<size_t>(g) * kRepText + oct) * kD
-                                       : (kind == 1 ? L.k_raw : L.v_raw) + static_cast<size_t>(g) * kD;
-  const __nv_bfloat16* gam = kind == 0 ? L.q_gamma : L.k_gamma;
-  float xl[8], xh[8], gl[8], gh[8], yl[8], yh[8];
-  const uint4 r0 = *reinterpret_cast<const uint4*>(src + dl), r1 = *reinterpret_cast<const uint4*>(src + dh);
-  const uint4 r2 = *reinterpret_cast<const uint4*>(gam + dl), r3 = *reinterpret_cast<const uint4*>(gam + dh);
-  unpack_bf16x8(r0, xl);
-  unpack_bf16x8(r1, xh);
-  unpack_bf16x8(r2, gl);
-  unpack_bf16x8(r3, gh);
   if (tid < 64) {
-    float cs[8], sn[8];
+    const int oct = tid >> 3, i = tid & 7, dl = 8 * i, dh = 64 + 8 * i;
+    const __nv_bfloat16* src = L.q_raw + (static_cast<size_t>(g) * kRepText + oct) * kD;
+    float xl[8], xh[8], gl[8], gh[8], yl[8], yh[8], cs[8], sn[8];
+    const uint4 r0 = *reinterpret_cast<const uint4*>(src + dl), r1 = *reinterpret_cast<const uint4*>(src + dh);
+    const uint4 r2 = *reinterpret_cast<const uint4*>(L.q_gamma + dl), r3 = *reinterpret_cast<const uint4*>(L.q_gamma + dh);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       cs[e] = p.rot[dl + e].x;
       sn[e] = p.rot[dl + e].z;
     }
+    unpack_bf16x8(r0, xl);
+    unpack_bf16x8(r1, xh);
+    unpack_bf16x8(r2, gl);
+    unpack_bf16x8(r3, gh);
     norm_rope(xl, xh, gl, gh, cs, sn, yl, yh);
     float factor;
     f16_row(yl, yh, p.scale_log2, factor);
@@ -234,42 +233,46 @@ __device__ __forceinline__ void prepare(const MxDecodeParams& p, uint8_t* smem, 
     if (i == 0) reinterpret_cast<float*>(smem + SM_QF)[buf * kRepText + oct] = factor;
     return;
   }
-  Pair cs[8], sn[8];
+  if (!last) return;
+  const int v = tid < 96 ? 0 : 1, i = tid & 31;
+  const __nv_bfloat16* src = (v ? L.v_raw : L.k_raw) + static_cast<size_t>(g) * kD;
+  auto two = [](const __nv_bfloat16* a) { return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(a)); };
+  const float2 a = two(src + 2 * i), b = two(src + 64 + 2 * i);
+  float x[4] = {a.x, a.y, b.x, b.y};
+  if (v == 0) {
+    const float2 ga = two(L.k_gamma + 2 * i), gb = two(L.k_gamma + 64 + 2 * i);
+    const float gm[4] = {ga.x, ga.y, gb.x, gb.y};
+    const float4 r0 = p.rot[2 * i], r1 = p.rot[2 * i + 1];
+    const Pair cs[2] = {{r0.x, r0.y}, {r1.x, r1.y}}, sn[2] = {{r0.z, r0.w}, {r1.z, r1.w}};
+    float y[4];
+    pair_norm_rope_warp(x, gm, cs, sn, y);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float4 a = p.rot[dl + e];
-    cs[e] = {a.x, a.y};
-    sn[e] = {a.z, a.w};
+    for (int e = 0; e < 4; ++e) x[e] = y[e];
   }
-  pair_norm_rope(xl, xh, gl, gh, cs, sn, yl, yh);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    yl[e] = kind == 1 ? yl[e] : xl[e];
-    yh[e] = kind == 1 ? yh[e] : xh[e];
-  }
-  uint32_t cl, ch, sc;
+  uint32_t cl, ch;
   int el, eh;
-  mx_encode_octet(yl, yh, cl, ch, sc, el, eh);
-  if (oct > 9) return;
-  uint32_t* nw = reinterpret_cast<uint32_t*>(smem + SM_NEW + buf * 144);
-  const int v = kind == 2 ? 1 : 0;
-  nw[16 * v + i] = cl;
-  nw[16 * v + 8 + i] = ch;
+  mx_encode_warp(x, cl, ch, el, eh);
+  uint8_t* nw = smem + SM_NEW + buf * 144;
+  nw[64 * v + i] = static_cast<uint8_t>(cl);
+  nw[64 * v + 32 + i] = static_cast<uint8_t>(ch);
   const size_t crow = static_cast<size_t>(g) * p.Smax + p.pos;
   uint8_t* codes = (v ? L.vc : L.kc) + crow * kMxRowBytes;
-  *reinterpret_cast<uint32_t*>(codes + 4 * i) = cl;
-  *reinterpret_cast<uint32_t*>(codes + 32 + 4 * i) = ch;
-  if (i == 0) {
-    nw[32 + v] = sc;
-    *reinterpret_cast<uint32_t*>((v ? L.vs : L.ks) + crow * kMxRowScales) = sc;
+  codes[i] = static_cast<uint8_t>(cl);
+  codes[32 + i] = static_cast<uint8_t>(ch);
+  if ((i & 15) == 0) {
+    uint8_t* scales = (v ? L.vs : L.ks) + crow * kMxRowScales;
+    const int b0 = i >> 4;
+    nw[128 + 4 * v + b0] = scales[b0] = static_cast<uint8_t>(el + 127);
+    nw[128 + 4 * v + 2 + b0] = scales[2 + b0] = static_cast<uint8_t>(eh + 127);
   }
   __nv_bfloat16* val = v ? L.v_new : L.k_new;
   if (val != nullptr) {
     val += static_cast<size_t>(g) * kD;
-    mx_values8(cl, mx_pow2(el), xl);
-    mx_values8(ch, mx_pow2(eh), xh);
-    *reinterpret_cast<uint4*>(val + dl) = pack8(xl, false);
-    *reinterpret_cast<uint4*>(val + dh) = pack8(xh, false);
+    float yl[8], yh[8];
+    mx_values8(cl, mx_pow2(el), yl);
+    mx_values8(ch, mx_pow2(eh), yh);
+    *reinterpret_cast<uint32_t*>(val + 2 * i) = pack_bf16x2(yl[0], yl[1]);
+    *reinterpret_cast<uint32_t*>(val + 64 + 2 * i) = pack_bf16x2(yh[0], yh[1]);
   }
 }
 
@@ -573,19 +576,20 @@ __global__ void __launch_bounds__(mxd::kThreads, 1) mxfp4_decode_kernel(const __
           const uint32_t np = c1 - c0 + 1;
           const size_t first = static_cast<size_t>(c0) * 2 + (cta_start(p, c0) >= u0 ? 0 : 1);
           auto slot = [&](uint32_t k) -> size_t { return k == 0 ? first : static_cast<size_t>(c0 + k) * 2; };
-          float ML = -INFINITY;
-          for (uint32_t k = 0; k < np; ++k) ML = fmaxf(ML, __ldcg(p.part_lse + slot(k) * kRepText + h));
+          // lane k of head h's warp: part k's weight (np <= 32: kMxMaxParts)
+          const float lse = c < np ? __ldcg(p.part_lse + slot(c) * kRepText + h) : -INFINITY;
+          const float wt = ex2_approx(lse - warp_max(lse));
           float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
           float ws = 0.f;
-#pragma unroll 4
+#pragma unroll 8
           for (uint32_t k = 0; k < np; ++k) {
-            const float wt = ex2_approx(__ldcg(p.part_lse + slot(k) * kRepText + h) - ML);
+            const float wk = __shfl_sync(0xffffffffu, wt, k);
             const float4 o = __ldcg(reinterpret_cast<const float4*>(p.part_o + (slot(k) * kRepText + h) * kD + 4 * c));
-            ws += wt;
-            s.x = fmaf(wt, o.x, s.x);
-            s.y = fmaf(wt, o.y, s.y);
-            s.z = fmaf(wt, o.z, s.z);
-            s.w = fmaf(wt, o.w, s.w);
+            ws += wk;
+            s.x = fmaf(wk, o.x, s.x);
+            s.y = fmaf(wk, o.y, s.y);
+            s.z = fmaf(wk, o.z, s.z);
+            s.w = fmaf(wk, o.w, s.w);
           }
           const float iw = 1.0f / ws;
           *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(s.x * iw, s.y * iw), pack_bf16x2(s.z * iw, s.w * iw));
