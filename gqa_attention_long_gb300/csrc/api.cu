@@ -1118,12 +1118,25 @@ int validate_mx_cache(const void* kc, const void* ks, const void* vc, const void
 // No two of the caches that one call writes may be the same: their rows would be written twice.
 template <class A>
 bool mx_caches_distinct(const A* a, int n) {
-  for (int i = 0; i < n; ++i) {
-    if (a[i].k_codes == a[i].v_codes) return false;
-    for (int j = 0; j < i; ++j)
-      if (a[i].k_codes == a[j].k_codes || a[i].v_codes == a[j].v_codes || a[i].k_codes == a[j].v_codes ||
-          a[i].v_codes == a[j].k_codes)
-        return false;
+  for (int l0 = 0; l0 < n; l0 += kMaxLayersPerLaunch) {
+    constexpr uint32_t kSlots = 512;
+    const void* seen[kSlots] = {};
+    auto add = [&](const void* p) {
+      uint32_t h = static_cast<uint32_t>((reinterpret_cast<uintptr_t>(p) >> 4) * 0x9E3779B97F4A7C15ull >> 55);
+      for (; seen[h] != nullptr; h = (h + 1) % kSlots)
+        if (seen[h] == p) return false;
+      seen[h] = p;
+      return true;
+    };
+    const int l1 = l0 + kMaxLayersPerLaunch < n ? l0 + kMaxLayersPerLaunch : n;
+    for (int l = l0; l < l1; ++l)
+      if (!add(a[l].k_codes) || !add(a[l].v_codes)) return false;
+    for (int l = l1; l < n; ++l)  // this table's caches against the later layers'
+      for (const void* p : {static_cast<const void*>(a[l].k_codes), static_cast<const void*>(a[l].v_codes)}) {
+        uint32_t h = static_cast<uint32_t>((reinterpret_cast<uintptr_t>(p) >> 4) * 0x9E3779B97F4A7C15ull >> 55);
+        for (; seen[h] != nullptr; h = (h + 1) % kSlots)
+          if (seen[h] == p) return false;
+      }
   }
   return true;
 }

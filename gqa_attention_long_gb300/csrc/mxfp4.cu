@@ -11,8 +11,10 @@
 namespace ea {
 namespace mx {
 
-constexpr int kThreads = 256;
-constexpr int kRowsPerCta = kThreads / 16;
+constexpr int kThreads = 128;
+constexpr int kUnroll = 2;  // (write, 16 layers x 4700 rows: 137 us with 1, 124 with 2, 131 with 4)
+constexpr int kRowStep = kThreads / 16;           // rows side by side in a CTA
+constexpr int kRowsPerCta = kUnroll * kRowStep;
 
 template <class T>
 __device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
@@ -47,55 +49,81 @@ __device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
 
 }  // namespace mx
 
-// grid (row blocks, kv heads, layers); thread = 8 channels of a K row and of a V row
+// grid (row blocks, kv heads, layers); thread = 8 channels of kUnroll rows of K, then of V: the rows' loads go out
+// together, so that a thread has kUnroll of them in flight.
 template <class T>
 __global__ void __launch_bounds__(mx::kThreads) mxfp4_write_kernel(const __grid_constant__ MxRowsParams p) {
+  using namespace mx;
   const int c = threadIdx.x & 15;
-  const int r = blockIdx.x * mx::kRowsPerCta + (threadIdx.x >> 4);
+  const int r0 = blockIdx.x * kRowsPerCta + (threadIdx.x >> 4);
   const int g = blockIdx.y;
   const MxRowsLayer& L = p.layer[blockIdx.z];
   pdl_wait_primary();
   pdl_launch_dependents();
-  // a row's 16 threads are half a warp: the shuffles below stay inside it
-  const bool live = r < p.n_rows;
-  const size_t row = static_cast<size_t>(g) * p.Smax + p.row0 + (live ? r : 0);
-  const long long src = g * p.head_stride + (live ? r : 0) * p.row_stride + 8 * c;
+  if ((r0 & ~1) >= p.n_rows) return;  // the warp's first row
 #pragma unroll
   for (int kv = 0; kv < 2; ++kv) {
-    float x[8];
-    mx::load8(static_cast<const T*>(kv ? L.v : L.k) + src, x);
-    float amax = 0.f;
+    const T* src = static_cast<const T*>(kv ? L.v : L.k) + g * p.head_stride + 8 * c;
+    uint8_t* codes = kv ? L.vc : L.kc;
+    uint8_t* scales = kv ? L.vs : L.ks;
+    float x[kUnroll][8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    const int e = mx_exponent(amax);
-    const uint32_t codes = mx_pack8(x, mx_pow2(-e));
-    if (live) {
-      *reinterpret_cast<uint32_t*>((kv ? L.vc : L.kc) + row * kMxRowBytes + 4 * c) = codes;
-      if ((c & 3) == 0) (kv ? L.vs : L.ks)[row * kMxRowScales + (c >> 2)] = static_cast<uint8_t>(e + 127);
+    for (int u = 0; u < kUnroll; ++u) {  // a row past the end repeats the last one: its threads shuffle along
+      const int r = min(r0 + u * kRowStep, p.n_rows - 1);
+      load8(src + r * p.row_stride, x[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      float amax = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[u][i]));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      const int e = mx_exponent(amax);
+      const uint32_t w = mx_pack8(x[u], mx_pow2(-e));
+      // the row's four scale bytes (lanes 0, 4, 8, 12 of its 16) in one word
+      uint32_t sc = static_cast<uint32_t>(e + 127) << (8 * (c >> 2));
+      sc |= __shfl_xor_sync(0xffffffffu, sc, 4);
+      sc |= __shfl_xor_sync(0xffffffffu, sc, 8);
+      const int r = r0 + u * kRowStep;
+      if (r < p.n_rows) {
+        const size_t row = static_cast<size_t>(g) * p.Smax + p.row0 + r;
+        *reinterpret_cast<uint32_t*>(codes + row * kMxRowBytes + 4 * c) = w;
+        if (c == 0) *reinterpret_cast<uint32_t*>(scales + row * kMxRowScales) = sc;
+      }
     }
   }
 }
 
 template <class T>
 __global__ void __launch_bounds__(mx::kThreads) mxfp4_read_kernel(const __grid_constant__ MxRowsParams p) {
+  using namespace mx;
   const int c = threadIdx.x & 15;
-  const int r = blockIdx.x * mx::kRowsPerCta + (threadIdx.x >> 4);
+  const int r0 = blockIdx.x * kRowsPerCta + (threadIdx.x >> 4);
   const int g = blockIdx.y;
   const MxRowsLayer& L = p.layer[blockIdx.z];
   pdl_wait_primary();
   pdl_launch_dependents();
-  if (r >= p.n_rows) return;
-  const size_t row = static_cast<size_t>(g) * p.Smax + p.row0 + r;
-  const long long dst = g * p.head_stride + r * p.row_stride + 8 * c;
+  if (r0 >= p.n_rows) return;
+  uint32_t w[2][kUnroll], b[2][kUnroll];
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const size_t row = static_cast<size_t>(g) * p.Smax + p.row0 + min(r0 + u * kRowStep, p.n_rows - 1);
+      w[kv][u] = *reinterpret_cast<const uint32_t*>((kv ? L.vc : L.kc) + row * kMxRowBytes + 4 * c);
+      b[kv][u] = (kv ? L.vs : L.ks)[row * kMxRowScales + (c >> 2)];
+    }
 #pragma unroll
   for (int kv = 0; kv < 2; ++kv) {
-    const uint32_t w = *reinterpret_cast<const uint32_t*>((kv ? L.vc : L.kc) + row * kMxRowBytes + 4 * c);
-    const uint32_t b = (kv ? L.vs : L.ks)[row * kMxRowScales + (c >> 2)];
-    float x[8];
-    mx_values8(w, mx_scale(b), x);
-    mx::store8(static_cast<T*>(kv ? L.v : L.k) + dst, x);
+    T* dst = static_cast<T*>(kv ? L.v : L.k) + g * p.head_stride + 8 * c;
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int r = r0 + u * kRowStep;
+      float x[8];
+      mx_values8(w[kv][u], mx_scale(b[kv][u]), x);
+      if (r < p.n_rows) store8(dst + r * p.row_stride, x);
+    }
   }
 }
 
