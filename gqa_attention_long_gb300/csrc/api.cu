@@ -1100,6 +1100,7 @@ cudaError_t launch_mxfp4_rows(const MxRowsParams& p, int n_layers, int dtype, bo
 cudaError_t mxfp4_attention_set_attributes();
 cudaError_t launch_mxfp4_prologue(const MxPrologueParams& p, int n_layers, cudaLaunchConfig_t cfg);
 cudaError_t launch_mxfp4_attention(const MxExpertParams& p, cudaLaunchConfig_t cfg);
+cudaError_t launch_mxfp4_merge(const MxMergeParams& p, int n_split, cudaLaunchConfig_t cfg);
 cudaError_t mxfp4_decode_set_attributes();
 cudaError_t launch_mxfp4_decode(const MxDecodeParams& p, cudaLaunchConfig_t cfg);
 }  // namespace ea
@@ -1342,6 +1343,8 @@ int mx_split_units(long long W, int T, int n_ctas, SplitUnit* out) {
   return n;
 }
 
+constexpr int kMxWholeUnitTiles = 4;
+
 int run_mx_expert(const ea_layer_mxfp4_args* a, int n_layers, int S, int Smax, long long p0, void* workspace,
                   size_t ws_bytes, ea_stream_t stream) {
   int dev;
@@ -1353,7 +1356,9 @@ int run_mx_expert(const ea_layer_mxfp4_args* a, int n_layers, int S, int Smax, l
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   MxPrologueParams pp;
   MxExpertParams p;
+  MxMergeParams mp;
   std::memset(&pp, 0, sizeof(pp));
+  std::memset(&mp, 0, sizeof(mp));
   std::memset(&p, 0, sizeof(p));
   mx_rotations(p0, &pp);
   pp.q_ws = ws + wl.q_off;
@@ -1364,6 +1369,8 @@ int run_mx_expert(const ea_layer_mxfp4_args* a, int n_layers, int S, int Smax, l
   p.q_factor = pp.q_factor;
   p.part_o = reinterpret_cast<uint4*>(ws + wl.part_o_off);
   p.part_lse = reinterpret_cast<float*>(ws + wl.part_lse_off);
+  mp.part_o = p.part_o;
+  mp.part_lse = p.part_lse;
   p.status = reinterpret_cast<uint32_t*>(ws);
   p.n_main = (S + kKeyTile - 1) / kKeyTile;
   p.T = p.n_main + 1;
@@ -1373,14 +1380,20 @@ int run_mx_expert(const ea_layer_mxfp4_args* a, int n_layers, int S, int Smax, l
   const cudaLaunchConfig_t cfg = launch_config(static_cast<cudaStream_t>(stream), attr, true);
   for (int l0 = 0; l0 < n_layers; l0 += per) {
     const int n = n_layers - l0 < per ? n_layers - l0 : per;
-    for (int l = 0; l < n; ++l) p.layer[l] = pp.layer[l] = mx_layer(a[l0 + l]);
+    for (int l = 0; l < n; ++l) {
+      p.layer[l] = pp.layer[l] = mx_layer(a[l0 + l]);
+      mp.out[l] = p.layer[l].out;
+    }
     p.W = static_cast<long long>(n) * kHkv * p.T;
     int n_ctas = di.sm_count < kMaxGridCtas ? di.sm_count : kMaxGridCtas;
     if (static_cast<long long>(n_ctas) > p.W) n_ctas = static_cast<int>(p.W);
-    p.n_split = mx_split_units(p.W, p.T, n_ctas, p.split);
+    // a CTA per unit, and so no merge, where splitting saves less than the merge costs
+    if (p.T <= kMxWholeUnitTiles && n * kHkv < n_ctas) n_ctas = n * kHkv;
+    const int n_split = mx_split_units(p.W, p.T, n_ctas, mp.split);
     cudaLaunchConfig_t c = cfg;
     c.gridDim = dim3(n_ctas);
-    if (launch_mxfp4_prologue(pp, n, cfg) != cudaSuccess || launch_mxfp4_attention(p, c) != cudaSuccess) {
+    if (launch_mxfp4_prologue(pp, n, cfg) != cudaSuccess || launch_mxfp4_attention(p, c) != cudaSuccess ||
+        (n_split > 0 && launch_mxfp4_merge(mp, n_split, cfg) != cudaSuccess)) {
       cudaGetLastError();
       return EA_ERR_CUDA;
     }

@@ -301,7 +301,11 @@ struct MxExpertParams {
   long long W;       // tiles: n_layers * 8 * T
   int T, n_main;     // tiles per unit: n_main = ceil(S / 128) and the own rows'
   int S, Smax;
-  int n_split;
+};
+struct MxMergeParams {
+  const uint4* part_o;
+  const float* part_lse;
+  __nv_bfloat16* out[kMaxLayersPerLaunch];
   SplitUnit split[kMaxSplitUnits];
 };
 // Workspace: [0, 1024) status word; q_factor; q tiles; partials of at most max_ctas CTAs.

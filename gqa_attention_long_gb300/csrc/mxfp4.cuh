@@ -111,35 +111,10 @@ __device__ __forceinline__ Pair pair_rsqrt_mean(Pair ss) {
   const float e = __fadd_rn(__fadd_rn(1.0f, -u.h), -u.l);
   return pair_fast_sum(r, r * fmaf(0.375f * e, e, 0.5f * e));
 }
-// ... from the row's 128 squares, the row held by an octet as in norm_rope (lane i: channels [8i, 8i+8) and
-// [64+8i, 64+8i+8)). A square of a bf16 number is exact in fp32.
-__device__ __forceinline__ Pair pair_inv_rms(const float (&xl)[8], const float (&xh)[8]) {
-  Pair ss = {0.f, 0.f};
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    ss = ss + Pair{__fmul_rn(xl[e], xl[e]), 0.f};
-    ss = ss + Pair{__fmul_rn(xh[e], xh[e]), 0.f};
-  }
-#pragma unroll
-  for (int m = 4; m >= 1; m >>= 1)
-    ss = ss + Pair{__shfl_xor_sync(0xffffffffu, ss.h, m), __shfl_xor_sync(0xffffffffu, ss.l, m)};
-  return pair_rsqrt_mean(ss);
+// The power of two below a row's largest magnitude.
+__device__ __forceinline__ int f16_exponent(float amax) {
+  return amax == 0.f ? 0 : min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -126), 126);
 }
-
-// The normed, rotated row rounded to fp32: channels as in norm_rope; cs and sn are the eight angles'
-// cosines and sines.
-__device__ __forceinline__ void pair_norm_rope(const float (&xl)[8], const float (&xh)[8], const float (&gl)[8],
-                                               const float (&gh)[8], const Pair (&cs)[8], const Pair (&sn)[8],
-                                               float (&yl)[8], float (&yh)[8]) {
-  const Pair rs = pair_inv_rms(xl, xh);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float nl = __fmul_rn(xl[e], gl[e]), nh = __fmul_rn(xh[e], gh[e]);  // exact: 8 + 8 bits
-    yl[e] = ((cs[e] * nl + -(sn[e] * nh)) * rs).h;
-    yh[e] = ((cs[e] * nh + sn[e] * nl) * rs).h;
-  }
-}
-
 // A q row held by an octet, times the power of two that puts its largest magnitude in [1, 2) (so that f16
 // holds any gain's rows); factor = scale over that power.
 __device__ __forceinline__ void f16_row(float (&yl)[8], float (&yh)[8], float scale, float& factor) {
@@ -148,7 +123,7 @@ __device__ __forceinline__ void f16_row(float (&yl)[8], float (&yh)[8], float sc
   for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fmaxf(fabsf(yl[e]), fabsf(yh[e])));
 #pragma unroll
   for (int m = 4; m >= 1; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
-  const int e = amax == 0.f ? 0 : min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -126), 126);
+  const int e = f16_exponent(amax);
   const float inv = mx_pow2(-e);
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
@@ -158,8 +133,9 @@ __device__ __forceinline__ void f16_row(float (&yl)[8], float (&yh)[8], float sc
   factor = scale * mx_pow2(e);
 }
 
-// The same of one row held by a whole warp (lane i: channels 2i, 2i + 1 and 64 + 2i, 65 + 2i), for a row
-// that something waits for: a quarter of the octet's steps.
+// The normed, rotated row rounded to fp32, the row held by a warp (lane i: channels 2i, 2i + 1 and their partners
+// 64 + 2i, 65 + 2i); cs and sn are the two angles' cosines and sines. A square of a bf16 number, and
+// the product of two, is exact in fp32.
 __device__ __forceinline__ void pair_norm_rope_warp(const float (&x)[4], const float (&g)[4], const Pair (&cs)[2],
                                                     const Pair (&sn)[2], float (&y)[4]) {
   Pair ss = {__fmul_rn(x[0], x[0]), 0.f};
@@ -192,29 +168,27 @@ __device__ __forceinline__ void mx_encode_warp(const float (&x)[4], uint32_t& cl
   ch = mx_pack8(h, mx_pow2(-eh)) & 0xFFu;
 }
 
-// Encodes a row held by an octet (lane i: channels [8i, 8i+8) in xl and [64+8i, ..) in xh): each
-// lane's two words of codes, and the four scale bytes of the row (the same in every lane).
-__device__ __forceinline__ void mx_encode_octet(const float (&xl)[8], const float (&xh)[8], uint32_t& cl,
-                                                uint32_t& ch, uint32_t& scales, int& el, int& eh) {
-  float al = 0.f, ah = 0.f;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    al = fmaxf(al, fabsf(xl[e]));
-    ah = fmaxf(ah, fabsf(xh[e]));
+// Encodes such a row into row `row` of a cache, and its stored values to val (if not null), lane i.
+__device__ __forceinline__ void mx_store_warp(const float (&x)[4], uint8_t* codes, uint8_t* scales, size_t row, int i,
+                                              __nv_bfloat16* val) {
+  uint32_t cl, ch;
+  int el, eh;
+  mx_encode_warp(x, cl, ch, el, eh);
+  codes += row * kMxRowBytes;
+  codes[i] = static_cast<uint8_t>(cl);
+  codes[32 + i] = static_cast<uint8_t>(ch);
+  if ((i & 15) == 0) {
+    scales += row * kMxRowScales + (i >> 4);
+    scales[0] = static_cast<uint8_t>(el + 127);
+    scales[2] = static_cast<uint8_t>(eh + 127);
   }
-#pragma unroll
-  for (int m = 2; m >= 1; m >>= 1) {  // lanes 4 j .. 4 j + 3 of an octet hold block j and block 2 + j
-    al = fmaxf(al, __shfl_xor_sync(0xffffffffu, al, m));
-    ah = fmaxf(ah, __shfl_xor_sync(0xffffffffu, ah, m));
+  if (val != nullptr) {
+    float yl[8], yh[8];
+    mx_values8(cl, mx_pow2(el), yl);
+    mx_values8(ch, mx_pow2(eh), yh);
+    *reinterpret_cast<uint32_t*>(val + 2 * i) = pack_bf16x2(yl[0], yl[1]);
+    *reinterpret_cast<uint32_t*>(val + 64 + 2 * i) = pack_bf16x2(yh[0], yh[1]);
   }
-  el = mx_exponent(al);
-  eh = mx_exponent(ah);
-  cl = mx_pack8(xl, mx_pow2(-el));
-  ch = mx_pack8(xh, mx_pow2(-eh));
-  const uint32_t mine = static_cast<uint32_t>(el + 127) | static_cast<uint32_t>(eh + 127) << 16;
-  const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 4);
-  const bool low = (threadIdx.x & 4) == 0;
-  scales = (low ? mine : other) | (low ? other : mine) << 8;
 }
 
 }  // namespace ea

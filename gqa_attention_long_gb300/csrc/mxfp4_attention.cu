@@ -37,85 +37,73 @@
 namespace ea {
 
 // ------------------------------------------------------------------------------- prologue
-// One octet of threads per token and kv head: the token's two q rows, its k row and its v row, whose angles
-// are formed once (from the tables of eight positions each, copied to shared memory while the preceding
-// kernel ends). grid (2, kv heads, layers), or (8, ..) with one of the four rows per octet, when there are
-// too few octets to fill the GPU.
+// One warp per token and kv head: the token's two q rows, its k row and its v row, whose angles are formed once; or,
+// when there are too few of them to fill the GPU (gridDim.x = 32), one of the four rows per warp. Lane i holds
+// channels 2i, 2i + 1 and their partners 64 + 2i, 65 + 2i. grid (8 or 32, kv heads, layers).
 __global__ void __launch_bounds__(256) mxfp4_prologue_kernel(const __grid_constant__ MxPrologueParams p) {
-  __shared__ float4 rot[4 + 8][kD / 2];
-  const int g = blockIdx.y, l = blockIdx.z, i = threadIdx.x & 7;
-  const int oct = threadIdx.x >> 3, t = 32 * (blockIdx.x & 1) + oct;
-  const int row0 = gridDim.x == 8 ? blockIdx.x >> 1 : 0, row1 = gridDim.x == 8 ? row0 + 1 : 4;
-  const int dl = 8 * i, dh = 64 + 8 * i;
+  const int g = blockIdx.y, l = blockIdx.z, i = threadIdx.x & 31;
+  const int t = 8 * (blockIdx.x & 7) + (threadIdx.x >> 5);
+  const int row0 = gridDim.x == 32 ? blockIdx.x >> 3 : 0, row1 = gridDim.x == 32 ? row0 + 1 : 4;
+  Pair cs[2], sn[2];
   {  // the tables are read by lane-dependent index: through a generic address, not the constant bank
-    const float4 *ra = &p.rot_a[4 * (blockIdx.x & 1)][0], *rb = &p.rot_b[0][0];
+    const float4 *ra = &p.rot_a[t >> 3][2 * i], *rb = &p.rot_b[t & 7][2 * i];
     asm volatile("" : "+l"(ra), "+l"(rb));
-    for (int k = threadIdx.x; k < 12 * (kD / 2); k += 256) rot[0][k] = k < 4 * (kD / 2) ? ra[k] : rb[k - 4 * (kD / 2)];
-  }
-  __syncthreads();
-  Pair cs[8], sn[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float4 a = rot[oct >> 3][dl + e], b = rot[4 + (oct & 7)][dl + e];
-    const Pair ca = {a.x, a.y}, sa = {a.z, a.w}, cb = {b.x, b.y}, sb = {b.z, b.w};
-    cs[e] = ca * cb + -(sa * sb);
-    sn[e] = sa * cb + ca * sb;
+    for (int e = 0; e < 2; ++e) {
+      const float4 a = ra[e], b = rb[e];
+      const Pair ca = {a.x, a.y}, sa = {a.z, a.w}, cb = {b.x, b.y}, sb = {b.z, b.w};
+      cs[e] = ca * cb + -(sa * sb);
+      sn[e] = sa * cb + ca * sb;
+    }
   }
   pdl_wait_primary();
   pdl_launch_dependents();
   const MxAttnLayer& L = p.layer[l];
   const size_t unit = static_cast<size_t>(l) * kHkv + g;
+  auto load4 = [&](const __nv_bfloat16* a, float (&x)[4]) {
+    const float2 lo = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(a + 2 * i));
+    const float2 hi = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(a + 64 + 2 * i));
+    x[0] = lo.x; x[1] = lo.y; x[2] = hi.x; x[3] = hi.y;
+  };
 #pragma unroll 1
   for (int kind = row0; kind < row1; ++kind) {  // q of the even head, q of the odd head, k, v
     const __nv_bfloat16* src = kind < 2 ? L.q_raw + ((static_cast<size_t>(g) * 2 + kind) * kTok + t) * kD
                                         : (kind == 2 ? L.k_raw : L.v_raw) + (static_cast<size_t>(g) * kTok + t) * kD;
-    const __nv_bfloat16* gam = kind < 2 ? L.q_gamma : L.k_gamma;
-    float xl[8], xh[8], gl[8], gh[8], yl[8], yh[8];
-    unpack_bf16x8(*reinterpret_cast<const uint4*>(src + dl), xl);
-    unpack_bf16x8(*reinterpret_cast<const uint4*>(src + dh), xh);
-    unpack_bf16x8(*reinterpret_cast<const uint4*>(gam + dl), gl);
-    unpack_bf16x8(*reinterpret_cast<const uint4*>(gam + dh), gh);
+    float x[4], gm[4], y[4];
+    load4(src, x);
+    load4(kind < 2 ? L.q_gamma : L.k_gamma, gm);
     if (kind < 2) {
-      float c[8], sv[8];
+      float ss = x[0] * x[0] + x[1] * x[1] + x[2] * x[2] + x[3] * x[3];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        c[e] = cs[e].h;
-        sv[e] = sn[e].h;
+      for (int m = 16; m >= 1; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+      const float rs = rsqrtf(ss * (1.0f / kD) + 1e-6f);
+      float amax = 0.f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float nl = x[e] * rs * gm[e], nh = x[2 + e] * rs * gm[2 + e];
+        y[e] = fmaf(nl, cs[e].h, -nh * sn[e].h);
+        y[2 + e] = fmaf(nh, cs[e].h, nl * sn[e].h);
+        amax = fmaxf(amax, fmaxf(fabsf(y[e]), fabsf(y[2 + e])));
       }
-      norm_rope(xl, xh, gl, gh, c, sv, yl, yh);
-      float factor;
-      f16_row(yl, yh, p.scale_log2, factor);
+#pragma unroll
+      for (int m = 16; m >= 1; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
+      const int ex = f16_exponent(amax);
+      const float inv = mx_pow2(-ex);
       const int r = kind * kTok + t;
-      uint8_t* q = p.q_ws + unit * kQTileBytes;
-      *reinterpret_cast<uint4*>(q + swz_off(r, i, kQTileBytes / 2)) = pack8(yl, true);
-      *reinterpret_cast<uint4*>(q + swz_off(r, i + 8, kQTileBytes / 2)) = pack8(yh, true);
-      if (i == 0) p.q_factor[unit * kRows + r] = factor;
+      uint8_t* q = p.q_ws + unit * kQTileBytes;  // channels 2i: chunk i / 4 of the first half, bytes 4 (i % 4)
+      *reinterpret_cast<uint32_t*>(q + swz_off(r, i >> 2, kQTileBytes / 2) + 4 * (i & 3)) = pack_f16x2(y[0] * inv, y[1] * inv);
+      *reinterpret_cast<uint32_t*>(q + swz_off(r, 8 + (i >> 2), kQTileBytes / 2) + 4 * (i & 3)) = pack_f16x2(y[2] * inv, y[3] * inv);
+      if (i == 0) p.q_factor[unit * kRows + r] = p.scale_log2 * mx_pow2(ex);
       continue;
     }
     if (kind == 2) {
-      pair_norm_rope(xl, xh, gl, gh, cs, sn, yl, yh);
+      pair_norm_rope_warp(x, gm, cs, sn, y);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        xl[e] = yl[e];
-        xh[e] = yh[e];
-      }
+      for (int e = 0; e < 4; ++e) x[e] = y[e];
     }
-    uint32_t cl, ch, sc;
-    int el, eh;
-    mx_encode_octet(xl, xh, cl, ch, sc, el, eh);
-    const size_t crow = static_cast<size_t>(g) * p.Smax + p.Smax - kTok + t;
-    uint8_t* codes = (kind == 2 ? L.kc : L.vc) + crow * kMxRowBytes;
-    *reinterpret_cast<uint32_t*>(codes + 4 * i) = cl;
-    *reinterpret_cast<uint32_t*>(codes + 32 + 4 * i) = ch;
-    if (i == 0) *reinterpret_cast<uint32_t*>((kind == 2 ? L.ks : L.vs) + crow * kMxRowScales) = sc;
     __nv_bfloat16* val = kind == 2 ? L.k_new : L.v_new;
-    if (val != nullptr) {
-      val += (static_cast<size_t>(g) * kTok + t) * kD;
-      mx_values8(cl, mx_pow2(el), xl);
-      mx_values8(ch, mx_pow2(eh), xh);
-      *reinterpret_cast<uint4*>(val + dl) = pack8(xl, false);
-      *reinterpret_cast<uint4*>(val + dh) = pack8(xh, false);
-    }
+    if (val != nullptr) val += (static_cast<size_t>(g) * kTok + t) * kD;
+    mx_store_warp(x, (kind == 2 ? L.kc : L.vc), (kind == 2 ? L.ks : L.vs), static_cast<size_t>(g) * p.Smax + p.Smax - kTok + t, i, val);
   }
 }
 
@@ -623,15 +611,16 @@ __device__ __forceinline__ void softmax_warps(const MxExpertParams& p, const Ctx
       const int l = s.u / kHkv, g = s.u % kHkv;
       const bool full = s.j0 == 0 && s.j1 == p.T;
       const uint32_t col = oa + 64 * k;
-      // columns [8 c, 8 c + 8) of the half row
-      auto load8 = [&](int c, float (&o)[8]) {
-        uint32_t v[8];
-        tmem_ld8(col + 8 * c, v);
+      // columns [32 h, 32 h + 32) of the half row
+      auto load32 = [&](int h, float (&o)[32]) {
+        uint32_t v[32];
+        tmem_ld32(col + 32 * h, v);
         tmem_wait_ld();
+        reg_fence32(v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = __uint_as_float(v[e]) * inv * two_r;
+        for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(v[e]) * inv * two_r;
       };
-      float o[8], up = 1.f;
+      float up = 1.f;
       uint4* dst;
       size_t step = 1;
       if (full) {
@@ -641,10 +630,11 @@ __device__ __forceinline__ void softmax_warps(const MxExpertParams& p, const Ctx
         const size_t sl = static_cast<size_t>(blockIdx.x) * 2 + (base == 0 ? 0 : 1);
         float amax = 0.f;
 #pragma unroll 1
-        for (int c = 0; c < 8; ++c) {
-          load8(c, o);
+        for (int h = 0; h < 2; ++h) {
+          float o[32];
+          load32(h, o);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(o[e]));
+          for (int e = 0; e < 32; ++e) amax = fmaxf(amax, fabsf(o[e]));
         }
         const int ex = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 14, -126), 112);
         up = mx_pow2(-ex);
@@ -654,11 +644,16 @@ __device__ __forceinline__ void softmax_warps(const MxExpertParams& p, const Ctx
         if (k == 0) p.part_lse[sl * 3 * kRows + r] = M + log2f(L);
       }
 #pragma unroll 1
-      for (int c = 0; c < 8; ++c) {
-        load8(c, o);
+      for (int h = 0; h < 2; ++h) {
+        float o[32];
+        load32(h, o);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] *= up;
-        dst[c * step] = pack8(o, !full);
+        for (int c = 0; c < 4; ++c) {
+          float x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = o[8 * c + e] * up;
+          dst[(4 * h + c) * step] = pack8(x, !full);
+        }
       }
       tc_fence_before();
       mbar_arrive(cx.bar(B_OFREE));  // the accumulator is read
@@ -714,14 +709,14 @@ __global__ void __launch_bounds__(mxa::kThreads, 1) mxfp4_attention_kernel(const
   if (warp == 0) tmem_dealloc(cx.tmem, kTmemCols);
 }
 
-// The units that the CTA ranges cut: grid (units, 8), thread = one row's 8 columns.
-__global__ void __launch_bounds__(256) mxfp4_merge_kernel(const __grid_constant__ MxExpertParams p) {
+// The units that the CTA ranges cut: grid (units, 16), thread = one row's 8 columns.
+__global__ void __launch_bounds__(kRows) mxfp4_merge_kernel(const __grid_constant__ MxMergeParams p) {
   pdl_wait_primary();
   pdl_launch_dependents();
   const SplitUnit su = p.split[blockIdx.x];
-  const int c = blockIdx.y * 2 + (threadIdx.x >> 7), r = threadIdx.x & 127;
-  if (su.nparts == 2) merge_row_chunk<2>(p.part_o, p.part_lse, su, c, r, p.layer[su.u / kHkv].out);
-  else merge_row_chunk<8>(p.part_o, p.part_lse, su, c, r, p.layer[su.u / kHkv].out);
+  __nv_bfloat16* out = p.out[su.u / kHkv];
+  if (su.nparts == 2) merge_row_chunk<2>(p.part_o, p.part_lse, su, blockIdx.y, threadIdx.x, out);
+  else merge_row_chunk<20>(p.part_o, p.part_lse, su, blockIdx.y, threadIdx.x, out);
 }
 
 cudaError_t mxfp4_attention_set_attributes() {
@@ -731,18 +726,19 @@ cudaError_t mxfp4_attention_set_attributes() {
 
 cudaError_t launch_mxfp4_prologue(const MxPrologueParams& p, int n_layers, cudaLaunchConfig_t cfg) {
   cfg.blockDim = dim3(256);
-  cfg.gridDim = dim3(n_layers <= 4 ? 8 : 2, kHkv, n_layers);
+  cfg.gridDim = dim3(n_layers <= 4 ? 32 : 8, kHkv, n_layers);
   return cudaLaunchKernelEx(&cfg, mxfp4_prologue_kernel, p);
 }
 
 cudaError_t launch_mxfp4_attention(const MxExpertParams& p, cudaLaunchConfig_t cfg) {
-  cudaLaunchConfig_t c = cfg;
-  c.blockDim = dim3(mxa::kThreads);
-  c.dynamicSmemBytes = mxa::kSmemBytes;
-  cudaError_t e = cudaLaunchKernelEx(&c, mxfp4_attention_kernel, p);
-  if (e != cudaSuccess || p.n_split == 0) return e;
-  cfg.gridDim = dim3(p.n_split, 8);
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(mxa::kThreads);
+  cfg.dynamicSmemBytes = mxa::kSmemBytes;
+  return cudaLaunchKernelEx(&cfg, mxfp4_attention_kernel, p);
+}
+
+cudaError_t launch_mxfp4_merge(const MxMergeParams& p, int n_split, cudaLaunchConfig_t cfg) {
+  cfg.gridDim = dim3(n_split, kPartChunks);
+  cfg.blockDim = dim3(kRows);
   return cudaLaunchKernelEx(&cfg, mxfp4_merge_kernel, p);
 }
 

@@ -249,31 +249,10 @@ __device__ __forceinline__ void prepare(const MxDecodeParams& p, uint8_t* smem, 
 #pragma unroll
     for (int e = 0; e < 4; ++e) x[e] = y[e];
   }
-  uint32_t cl, ch;
-  int el, eh;
-  mx_encode_warp(x, cl, ch, el, eh);
-  uint8_t* nw = smem + SM_NEW + buf * 144;
-  nw[64 * v + i] = static_cast<uint8_t>(cl);
-  nw[64 * v + 32 + i] = static_cast<uint8_t>(ch);
-  const size_t crow = static_cast<size_t>(g) * p.Smax + p.pos;
-  uint8_t* codes = (v ? L.vc : L.kc) + crow * kMxRowBytes;
-  codes[i] = static_cast<uint8_t>(cl);
-  codes[32 + i] = static_cast<uint8_t>(ch);
-  if ((i & 15) == 0) {
-    uint8_t* scales = (v ? L.vs : L.ks) + crow * kMxRowScales;
-    const int b0 = i >> 4;
-    nw[128 + 4 * v + b0] = scales[b0] = static_cast<uint8_t>(el + 127);
-    nw[128 + 4 * v + 2 + b0] = scales[2 + b0] = static_cast<uint8_t>(eh + 127);
-  }
   __nv_bfloat16* val = v ? L.v_new : L.k_new;
-  if (val != nullptr) {
-    val += static_cast<size_t>(g) * kD;
-    float yl[8], yh[8];
-    mx_values8(cl, mx_pow2(el), yl);
-    mx_values8(ch, mx_pow2(eh), yh);
-    *reinterpret_cast<uint32_t*>(val + 2 * i) = pack_bf16x2(yl[0], yl[1]);
-    *reinterpret_cast<uint32_t*>(val + 64 + 2 * i) = pack_bf16x2(yh[0], yh[1]);
-  }
+  mx_store_warp(x, smem + SM_NEW + buf * 144 + 64 * v, smem + SM_NEW + buf * 144 + 128 + 4 * v, 0, i, nullptr);
+  mx_store_warp(x, v ? L.vc : L.kc, v ? L.vs : L.ks, static_cast<size_t>(g) * p.Smax + p.pos, i,
+                val == nullptr ? nullptr : val + static_cast<size_t>(g) * kD);
 }
 
 // --------------------------------------------------------------------------------- one chunk
