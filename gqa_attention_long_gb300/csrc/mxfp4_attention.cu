@@ -201,15 +201,19 @@ __device__ __forceinline__ int tile_live(const MxExpertParams& p, int j) {
 
 // ---------------------------------------------------------------------------------- loads
 // The largest scale of a block that holds a code other than zero, over the tile's live rows (the whole warp's result;
-// lane: rows lane, lane + 32, ..).
+// lane: rows lane, lane + 32, .., each row's four blocks at once).
 __device__ __noinline__ int top_nonzero(uint32_t tile, int lane, int live) {
   uint32_t top = 0;
 #pragma unroll 1
-  for (int i = 4 * lane; i < 4 * live; i += i % 4 == 3 ? 4 * 32 - 3 : 1) {
-    const uint4 c = ld_shared_v4(tile + 16 * i);
+  for (int r = lane; r < live; r += 32) {
+    uint4 c[4];
     uint32_t sc;
-    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(sc) : "r"(tile + kCodes + i) : "memory");
-    if (((c.x | c.y | c.z | c.w) & 0x77777777u) != 0u) top = max(top, sc);
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(sc) : "r"(tile + kCodes + 4 * r) : "memory");
+#pragma unroll
+    for (int b = 0; b < 4; ++b) c[b] = ld_shared_v4(tile + r * kMxRowBytes + (((b + (r >> 1)) & 3) << 4));
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+      if (((c[b].x | c[b].y | c[b].z | c[b].w) & 0x77777777u) != 0u) top = max(top, (sc >> (8 * ((b + (r >> 1)) & 3))) & 255u);
   }
   return static_cast<int>(__reduce_max_sync(0xffffffffu, top));
 }
@@ -522,6 +526,12 @@ __device__ __forceinline__ void softmax_warps(const MxExpertParams& p, const Ctx
         reg_fence32(v[0]);
         reg_fence32(v[1]);
       };
+      // (a segment's second tile starts from the first one's maximum: its own would seldom do)
+      if (i == 1) {
+        ok = wait3(B_MDONE, n - 1);
+        if (!ok) break;
+        m = *run;
+      }
       const float2 ct2 = make_float2(ct, ct);
       float2 ts[4];
 #pragma unroll
@@ -677,9 +687,9 @@ __global__ void __launch_bounds__(mxa::kThreads, 1) mxfp4_attention_kernel(const
   cx.start = cta_tile_start(blockIdx.x, p.W, gridDim.x);
   cx.end = cta_tile_start(blockIdx.x + 1, p.W, gridDim.x);
   const int warp = threadIdx.x >> 5;
-  if (threadIdx.x == 0) {
-    for (int b = 0; b < kNumBars; ++b) mbar_init(cx.bar(b), bar_count(b));
-    *cx.abort_flag = 0u;
+  if (warp == 1) {
+    for (int b = threadIdx.x & 31; b < kNumBars; b += 32) mbar_init(cx.bar(b), bar_count(b));
+    if ((threadIdx.x & 31) == 0) *cx.abort_flag = 0u;
     fence_mbar_init();
   }
   if (warp == 0) {
