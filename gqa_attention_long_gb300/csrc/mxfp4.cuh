@@ -9,6 +9,7 @@
 
 #include "internal.cuh"
 #include "ptx.cuh"
+#include "rope.cuh"
 
 namespace ea {
 
@@ -70,11 +71,13 @@ __device__ __forceinline__ void mx_values8(uint32_t w, float scale, float (&x)[8
   }
 }
 
-// --------------------------------------------------- norm and rotation in pairs of fp32 numbers
+// ------------------------------------------------------------------- a k row's norm, rotation and codes
 // A k row is normed, rotated, rounded to fp32 and encoded. The encoder has borders (2.5 -> 2, just
-// above -> 3), so a row that is off in its last fp32 bits can land on another code than the
-// formula's. It is therefore formed as unevaluated sums h + l of two fp32 numbers (about 2^-45
-// relative), at fp32 rates; FP64 arithmetic, 1/60 of the fp32 rate here, would bound the kernel.
+// above -> 3), and a row that is off in its last fp32 bits can land on another code than the
+// formula's. So the row is formed in fp32 with a bound on its error, and where the bound leaves a code or an
+// exponent open (about one row in two hundred), once more as unevaluated sums h + l of two fp32 numbers
+// (about 2^-45 relative). FP64 arithmetic, 1/60 of the fp32 rate here, would bound the kernels; pairs
+// throughout took three times the instructions.
 struct Pair {
   float h, l;
 };
@@ -133,61 +136,122 @@ __device__ __forceinline__ void f16_row(float (&yl)[8], float (&yh)[8], float sc
   factor = scale * mx_pow2(e);
 }
 
-// The normed, rotated row rounded to fp32, the row held by a warp (lane i: channels 2i, 2i + 1 and their partners
-// 64 + 2i, 65 + 2i); cs and sn are the two angles' cosines and sines. A square of a bf16 number, and
-// the product of two, is exact in fp32.
-__device__ __forceinline__ void pair_norm_rope_warp(const float (&x)[4], const float (&g)[4], const Pair (&cs)[2],
-                                                    const Pair (&sn)[2], float (&y)[4]) {
-  Pair ss = {__fmul_rn(x[0], x[0]), 0.f};
+// The normed, rotated row rounded to fp32, held by an octet as in norm_rope (lane i: channels [8i, 8i+8) and their
+// partners [64+8i, 64+8i+8)); angle(e, cs, sn) gives frequency 8i + e's cosine and sine. A square of a bf16 number,
+// and the product of two, is exact in fp32.
+template <class Angle>
+__device__ __forceinline__ void pair_norm_rope(const float (&xl)[8], const float (&xh)[8], const float (&gl)[8],
+                                               const float (&gh)[8], Angle angle, float (&yl)[8], float (&yh)[8]) {
+  Pair ss = {0.f, 0.f};
 #pragma unroll
-  for (int e = 1; e < 4; ++e) ss = ss + Pair{__fmul_rn(x[e], x[e]), 0.f};
+  for (int e = 0; e < 8; ++e) {
+    ss = ss + Pair{__fmul_rn(xl[e], xl[e]), 0.f};
+    ss = ss + Pair{__fmul_rn(xh[e], xh[e]), 0.f};
+  }
 #pragma unroll
-  for (int m = 16; m >= 1; m >>= 1)
+  for (int m = 4; m >= 1; m >>= 1)
     ss = ss + Pair{__shfl_xor_sync(0xffffffffu, ss.h, m), __shfl_xor_sync(0xffffffffu, ss.l, m)};
   const Pair rs = pair_rsqrt_mean(ss);
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const float nl = __fmul_rn(x[e], g[e]), nh = __fmul_rn(x[2 + e], g[2 + e]);
-    y[e] = ((cs[e] * nl + -(sn[e] * nh)) * rs).h;
-    y[2 + e] = ((cs[e] * nh + sn[e] * nl) * rs).h;
+  for (int e = 0; e < 8; ++e) {
+    Pair cs, sn;
+    angle(e, cs, sn);
+    const float nl = __fmul_rn(xl[e], gl[e]), nh = __fmul_rn(xh[e], gh[e]);
+    yl[e] = ((cs * nl + -(sn * nh)) * rs).h;
+    yh[e] = ((cs * nh + sn * nl) * rs).h;
   }
 }
-// Encodes such a row: the lane's byte of codes (2i, 2i + 1) and of (64 + 2i, ..), its blocks' exponents (block i / 16 and
-// 2 + i / 16).
-__device__ __forceinline__ void mx_encode_warp(const float (&x)[4], uint32_t& cl, uint32_t& ch, int& el, int& eh) {
-  float al = fmaxf(fabsf(x[0]), fabsf(x[1])), ah = fmaxf(fabsf(x[2]), fabsf(x[3]));
+
+// Encodes a row held by an octet: each lane's two words of codes, its blocks' exponents (block i / 4 and 2 + i / 4).
+__device__ __forceinline__ void mx_encode_octet(const float (&xl)[8], const float (&xh)[8], uint32_t& cl, uint32_t& ch,
+                                                int& el, int& eh) {
+  float al = 0.f, ah = 0.f;
 #pragma unroll
-  for (int m = 8; m >= 1; m >>= 1) {
+  for (int e = 0; e < 8; ++e) {
+    al = fmaxf(al, fabsf(xl[e]));
+    ah = fmaxf(ah, fabsf(xh[e]));
+  }
+#pragma unroll
+  for (int m = 2; m >= 1; m >>= 1) {
     al = fmaxf(al, __shfl_xor_sync(0xffffffffu, al, m));
     ah = fmaxf(ah, __shfl_xor_sync(0xffffffffu, ah, m));
   }
   el = mx_exponent(al);
   eh = mx_exponent(ah);
-  const float l[8] = {x[0], x[1]}, h[8] = {x[2], x[3]};
-  cl = mx_pack8(l, mx_pow2(-el)) & 0xFFu;
-  ch = mx_pack8(h, mx_pow2(-eh)) & 0xFFu;
+  cl = mx_pack8(xl, mx_pow2(-el));
+  ch = mx_pack8(xh, mx_pow2(-eh));
 }
 
-// Encodes such a row into row `row` of a cache, and its stored values to val (if not null), lane i.
-__device__ __forceinline__ void mx_store_warp(const float (&x)[4], uint8_t* codes, uint8_t* scales, size_t row, int i,
-                                              __nv_bfloat16* val) {
-  uint32_t cl, ch;
-  int el, eh;
-  mx_encode_warp(x, cl, ch, el, eh);
+// Norms, rotates and encodes a k row held by an octet (all four octets of the warp do so together): cs, sn in fp32 as in
+// norm_rope, angle as in pair_norm_rope.
+template <class Angle>
+__device__ __forceinline__ void mx_encode_k_octet(const float (&xl)[8], const float (&xh)[8], const float (&gl)[8],
+                                                  const float (&gh)[8], const float (&cs)[8], const float (&sn)[8],
+                                                  Angle angle, uint32_t& cl, uint32_t& ch, int& el, int& eh) {
+  float yl[8], yh[8];
+  norm_rope(xl, xh, gl, gh, cs, sn, yl, yh);
+  // |n cos| + |n' sin| <= |n| + |n'| = sl: an output is off by less than 2^-18 of it. (The sum of squares: 19
+  // additions, 2^-19.7, half of which reaches the root; 2^-22 each for the root, the two products by it and the
+  // gain, and the angle's cosine and sine; the rotation's own 2^-24. Under 2^-19 together.) The norm of the
+  // rotated pair bounds both terms: |n| + |n'| <= sqrt(2) |(y, y')| <= 1.5 (|y| + |y'|).
+  float dl = 0.f, dh = 0.f, al = 0.f, ah = 0.f, d[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    d[e] = (fabsf(yl[e]) + fabsf(yh[e])) * (1.5f * 0x1p-18f);
+    al = fmaxf(al, fabsf(yl[e]));
+    ah = fmaxf(ah, fabsf(yh[e]));
+    dl = fmaxf(dl, d[e]);
+  }
+#pragma unroll
+  for (int m = 2; m >= 1; m >>= 1) {
+    al = fmaxf(al, __shfl_xor_sync(0xffffffffu, al, m));
+    ah = fmaxf(ah, __shfl_xor_sync(0xffffffffu, ah, m));
+    dl = fmaxf(dl, __shfl_xor_sync(0xffffffffu, dl, m));
+  }
+  dh = dl;
+  el = mx_exponent(al);
+  eh = mx_exponent(ah);
+  float a[8], b[8];
+  const float il = mx_pow2(-el), ih = mx_pow2(-eh);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    a[e] = yl[e] - d[e];
+    b[e] = yl[e] + d[e];
+  }
+  cl = mx_pack8(a, il);
+  bool open = mx_pack8(b, il) != cl;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    a[e] = yh[e] - d[e];
+    b[e] = yh[e] + d[e];
+  }
+  ch = mx_pack8(a, ih);
+  open |= mx_pack8(b, ih) != ch;
+  open |= mx_exponent(al - dl) != mx_exponent(al + dl) || mx_exponent(ah - dh) != mx_exponent(ah + dh);
+  open |= !(al + ah < 1e30f) || !(al > 1e-30f) || !(ah > 1e-30f);  // infinities, NaN and all but zero rows: the long way
+  if (__any_sync(0xffffffffu, open)) {
+    pair_norm_rope(xl, xh, gl, gh, angle, yl, yh);
+    mx_encode_octet(yl, yh, cl, ch, el, eh);
+  }
+}
+
+// Stores such a row as row `row` of a cache, and its values to val (if not null); i: the lane of the octet.
+__device__ __forceinline__ void mx_store_octet(uint32_t cl, uint32_t ch, int el, int eh, uint8_t* codes, uint8_t* scales,
+                                               size_t row, int i, __nv_bfloat16* val) {
   codes += row * kMxRowBytes;
-  codes[i] = static_cast<uint8_t>(cl);
-  codes[32 + i] = static_cast<uint8_t>(ch);
-  if ((i & 15) == 0) {
-    scales += row * kMxRowScales + (i >> 4);
+  *reinterpret_cast<uint32_t*>(codes + 4 * i) = cl;
+  *reinterpret_cast<uint32_t*>(codes + 32 + 4 * i) = ch;
+  if ((i & 3) == 0) {
+    scales += row * kMxRowScales + (i >> 2);
     scales[0] = static_cast<uint8_t>(el + 127);
     scales[2] = static_cast<uint8_t>(eh + 127);
   }
   if (val != nullptr) {
-    float yl[8], yh[8];
-    mx_values8(cl, mx_pow2(el), yl);
-    mx_values8(ch, mx_pow2(eh), yh);
-    *reinterpret_cast<uint32_t*>(val + 2 * i) = pack_bf16x2(yl[0], yl[1]);
-    *reinterpret_cast<uint32_t*>(val + 64 + 2 * i) = pack_bf16x2(yh[0], yh[1]);
+    float x[8];
+    mx_values8(cl, mx_pow2(el), x);
+    *reinterpret_cast<uint4*>(val + 8 * i) = pack8(x, false);
+    mx_values8(ch, mx_pow2(eh), x);
+    *reinterpret_cast<uint4*>(val + 64 + 8 * i) = pack8(x, false);
   }
 }
 

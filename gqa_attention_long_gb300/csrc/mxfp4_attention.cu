@@ -37,73 +37,84 @@
 namespace ea {
 
 // ------------------------------------------------------------------------------- prologue
-// One warp per token and kv head: the token's two q rows, its k row and its v row, whose angles are formed once; or,
-// when there are too few of them to fill the GPU (gridDim.x = 32), one of the four rows per warp. Lane i holds
-// channels 2i, 2i + 1 and their partners 64 + 2i, 65 + 2i. grid (8 or 32, kv heads, layers).
+// One octet of threads per token and kv head: the token's two q rows, its k row and its v row, whose angles are formed
+// once; or, when there are too few of them to fill the GPU (gridDim.x = 8), one of the four rows. grid (2 or 8, kv
+// heads, layers).
 __global__ void __launch_bounds__(256) mxfp4_prologue_kernel(const __grid_constant__ MxPrologueParams p) {
-  const int g = blockIdx.y, l = blockIdx.z, i = threadIdx.x & 31;
-  const int t = 8 * (blockIdx.x & 7) + (threadIdx.x >> 5);
-  const int row0 = gridDim.x == 32 ? blockIdx.x >> 3 : 0, row1 = gridDim.x == 32 ? row0 + 1 : 4;
-  Pair cs[2], sn[2];
-  {  // the tables are read by lane-dependent index: through a generic address, not the constant bank
-    const float4 *ra = &p.rot_a[t >> 3][2 * i], *rb = &p.rot_b[t & 7][2 * i];
-    asm volatile("" : "+l"(ra), "+l"(rb));
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float4 a = ra[e], b = rb[e];
-      const Pair ca = {a.x, a.y}, sa = {a.z, a.w}, cb = {b.x, b.y}, sb = {b.z, b.w};
-      cs[e] = ca * cb + -(sa * sb);
-      sn[e] = sa * cb + ca * sb;
+  const int g = blockIdx.y, l = blockIdx.z, i = threadIdx.x & 7;
+  const int t = 32 * (blockIdx.x & 1) + (threadIdx.x >> 3);
+  const int row0 = gridDim.x == 8 ? blockIdx.x >> 1 : 0, row1 = gridDim.x == 8 ? row0 + 1 : 4;
+  const int dl = 8 * i, dh = 64 + 8 * i;
+  // The tables' rows that this half of the tokens needs, copied to shared memory while the preceding kernel ends (they
+  // are read by lane-dependent index: through a generic address, not the constant bank). Frequency j at j + j / 8: an
+  // octet's lanes, eight frequencies apart, fall in different banks.
+  __shared__ float4 rot[4 + 8][kD / 2 + 8];
+  {
+    const float4 *pa = &p.rot_a[4 * (blockIdx.x & 1)][0], *pb = &p.rot_b[0][0];
+    asm volatile("" : "+l"(pa), "+l"(pb));
+    for (int k = threadIdx.x; k < 12 * (kD / 2); k += 256) {
+      const int j = k % (kD / 2);
+      rot[k / (kD / 2)][j + j / 8] = k < 4 * (kD / 2) ? pa[k] : pb[k - 4 * (kD / 2)];
     }
   }
+  __syncthreads();
+  const float4 *ra = &rot[(t >> 3) & 3][9 * i], *rb = &rot[4 + (t & 7)][9 * i];
+  float cs[8], sn[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float4 a = ra[e], b = rb[e];
+    cs[e] = fmaf(a.x, b.x, -a.z * b.z);
+    sn[e] = fmaf(a.z, b.x, a.x * b.z);
+  }
+  auto angle = [&](int e, Pair& c, Pair& s) {
+    const float4 a = ra[e], b = rb[e];
+    const Pair ca = {a.x, a.y}, sa = {a.z, a.w}, cb = {b.x, b.y}, sb = {b.z, b.w};
+    c = ca * cb + -(sa * sb);
+    s = sa * cb + ca * sb;
+  };
   pdl_wait_primary();
   pdl_launch_dependents();
   const MxAttnLayer& L = p.layer[l];
   const size_t unit = static_cast<size_t>(l) * kHkv + g;
-  auto load4 = [&](const __nv_bfloat16* a, float (&x)[4]) {
-    const float2 lo = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(a + 2 * i));
-    const float2 hi = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(a + 64 + 2 * i));
-    x[0] = lo.x; x[1] = lo.y; x[2] = hi.x; x[3] = hi.y;
-  };
-#pragma unroll 1
-  for (int kind = row0; kind < row1; ++kind) {  // q of the even head, q of the odd head, k, v
-    const __nv_bfloat16* src = kind < 2 ? L.q_raw + ((static_cast<size_t>(g) * 2 + kind) * kTok + t) * kD
-                                        : (kind == 2 ? L.k_raw : L.v_raw) + (static_cast<size_t>(g) * kTok + t) * kD;
-    float x[4], gm[4], y[4];
-    load4(src, x);
-    load4(kind < 2 ? L.q_gamma : L.k_gamma, gm);
+  const __nv_bfloat16* q0 = L.q_raw + (static_cast<size_t>(g) * 2 * kTok + t) * kD;
+  const size_t own = (static_cast<size_t>(g) * kTok + t) * kD;
+  const __nv_bfloat16* src[4] = {q0, q0 + kTok * kD, L.k_raw + own, L.v_raw + own};  // q of both heads, k, v
+  uint4 raw[4][2];  // (every row's loads go out before the first is used)
+#pragma unroll
+  for (int kind = 0; kind < 4; ++kind)
+    if (kind >= row0 && kind < row1) {
+      raw[kind][0] = *reinterpret_cast<const uint4*>(src[kind] + dl);
+      raw[kind][1] = *reinterpret_cast<const uint4*>(src[kind] + dh);
+    }
+  const uint4 gq[2] = {*reinterpret_cast<const uint4*>(L.q_gamma + dl), *reinterpret_cast<const uint4*>(L.q_gamma + dh)};
+  const uint4 gk[2] = {*reinterpret_cast<const uint4*>(L.k_gamma + dl), *reinterpret_cast<const uint4*>(L.k_gamma + dh)};
+#pragma unroll
+  for (int kind = 0; kind < 4; ++kind) {
+    if (kind < row0 || kind >= row1) continue;
+    float xl[8], xh[8], gl[8], gh[8];
+    unpack_bf16x8(raw[kind][0], xl);
+    unpack_bf16x8(raw[kind][1], xh);
+    unpack_bf16x8(kind < 2 ? gq[0] : gk[0], gl);
+    unpack_bf16x8(kind < 2 ? gq[1] : gk[1], gh);
     if (kind < 2) {
-      float ss = x[0] * x[0] + x[1] * x[1] + x[2] * x[2] + x[3] * x[3];
-#pragma unroll
-      for (int m = 16; m >= 1; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-      const float rs = rsqrtf(ss * (1.0f / kD) + 1e-6f);
-      float amax = 0.f;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float nl = x[e] * rs * gm[e], nh = x[2 + e] * rs * gm[2 + e];
-        y[e] = fmaf(nl, cs[e].h, -nh * sn[e].h);
-        y[2 + e] = fmaf(nh, cs[e].h, nl * sn[e].h);
-        amax = fmaxf(amax, fmaxf(fabsf(y[e]), fabsf(y[2 + e])));
-      }
-#pragma unroll
-      for (int m = 16; m >= 1; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
-      const int ex = f16_exponent(amax);
-      const float inv = mx_pow2(-ex);
+      float yl[8], yh[8], factor;
+      norm_rope(xl, xh, gl, gh, cs, sn, yl, yh);
+      f16_row(yl, yh, p.scale_log2, factor);
       const int r = kind * kTok + t;
-      uint8_t* q = p.q_ws + unit * kQTileBytes;  // channels 2i: chunk i / 4 of the first half, bytes 4 (i % 4)
-      *reinterpret_cast<uint32_t*>(q + swz_off(r, i >> 2, kQTileBytes / 2) + 4 * (i & 3)) = pack_f16x2(y[0] * inv, y[1] * inv);
-      *reinterpret_cast<uint32_t*>(q + swz_off(r, 8 + (i >> 2), kQTileBytes / 2) + 4 * (i & 3)) = pack_f16x2(y[2] * inv, y[3] * inv);
-      if (i == 0) p.q_factor[unit * kRows + r] = p.scale_log2 * mx_pow2(ex);
+      uint8_t* q = p.q_ws + unit * kQTileBytes;
+      *reinterpret_cast<uint4*>(q + swz_off(r, i, kQTileBytes / 2)) = pack8(yl, true);
+      *reinterpret_cast<uint4*>(q + swz_off(r, i + 8, kQTileBytes / 2)) = pack8(yh, true);
+      if (i == 0) p.q_factor[unit * kRows + r] = factor;
       continue;
     }
-    if (kind == 2) {
-      pair_norm_rope_warp(x, gm, cs, sn, y);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = y[e];
-    }
+    uint32_t cl, ch;
+    int el, eh;
+    if (kind == 2) mx_encode_k_octet(xl, xh, gl, gh, cs, sn, angle, cl, ch, el, eh);
+    else mx_encode_octet(xl, xh, cl, ch, el, eh);
     __nv_bfloat16* val = kind == 2 ? L.k_new : L.v_new;
     if (val != nullptr) val += (static_cast<size_t>(g) * kTok + t) * kD;
-    mx_store_warp(x, (kind == 2 ? L.kc : L.vc), (kind == 2 ? L.ks : L.vs), static_cast<size_t>(g) * p.Smax + p.Smax - kTok + t, i, val);
+    mx_store_octet(cl, ch, el, eh, kind == 2 ? L.kc : L.vc, kind == 2 ? L.ks : L.vs,
+                   static_cast<size_t>(g) * p.Smax + p.Smax - kTok + t, i, val);
   }
 }
 
@@ -736,7 +747,7 @@ cudaError_t mxfp4_attention_set_attributes() {
 
 cudaError_t launch_mxfp4_prologue(const MxPrologueParams& p, int n_layers, cudaLaunchConfig_t cfg) {
   cfg.blockDim = dim3(256);
-  cfg.gridDim = dim3(n_layers <= 4 ? 32 : 8, kHkv, n_layers);
+  cfg.gridDim = dim3(n_layers <= 4 ? 8 : 2, kHkv, n_layers);
   return cudaLaunchKernelEx(&cfg, mxfp4_prologue_kernel, p);
 }
 

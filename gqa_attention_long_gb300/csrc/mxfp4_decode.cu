@@ -203,29 +203,32 @@ __device__ __forceinline__ void load_chunk(const MxDecodeParams& p, const Cursor
 }
 
 // ------------------------------------------------------------------------------ preparation
-// Unit u's q rows (warps 0 and 1, an octet each: normed, roped, f16 times a power of two that puts the row's
-// largest magnitude in [1, 2)), and, when the segment holds the unit's last chunk, the new k row (warp 2) and v
-// row (warp 3): into shared memory for this CTA, into the cache, and their values to the caller.
+// Unit u's q rows (octets 0-7: normed, roped, f16 times a power of two that puts the row's largest magnitude in
+// [1, 2)), and, when the segment holds the unit's last chunk, the new k row (octet 8) and v row (octet 12): into
+// shared memory for this CTA, into the cache, and their values to the caller.
 __device__ __forceinline__ void prepare(const MxDecodeParams& p, uint8_t* smem, uint32_t u, bool last, int buf, int tid) {
-  const int l = u / kHkv, g = u % kHkv;
+  const int l = u / kHkv, g = u % kHkv, oct = tid >> 3, i = tid & 7, dl = 8 * i, dh = 64 + 8 * i;
+  const int kind = tid < 64 ? 0 : tid < 96 ? 1 : 2;  // (the same for a warp; octets 8-11 all hold the k row)
+  if (kind > 0 && !last) return;
   const MxAttnLayer& L = p.layer[l];
-  if (tid < 64) {
-    const int oct = tid >> 3, i = tid & 7, dl = 8 * i, dh = 64 + 8 * i;
-    const __nv_bfloat16* src = L.q_raw + (static_cast<size_t>(g) * kRepText + oct) * kD;
-    float xl[8], xh[8], gl[8], gh[8], yl[8], yh[8], cs[8], sn[8];
-    const uint4 r0 = *reinterpret_cast<const uint4*>(src + dl), r1 = *reinterpret_cast<const uint4*>(src + dh);
-    const uint4 r2 = *reinterpret_cast<const uint4*>(L.q_gamma + dl), r3 = *reinterpret_cast<const uint4*>(L.q_gamma + dh);
+  const __nv_bfloat16* src = kind == 0 ? L.q_raw + (static_cast<size_t>(g) * kRepText + oct) * kD
+                                       : (kind == 1 ? L.k_raw : L.v_raw) + static_cast<size_t>(g) * kD;
+  const __nv_bfloat16* gam = kind == 0 ? L.q_gamma : L.k_gamma;
+  const uint4 r0 = *reinterpret_cast<const uint4*>(src + dl), r1 = *reinterpret_cast<const uint4*>(src + dh);
+  const uint4 r2 = *reinterpret_cast<const uint4*>(gam + dl), r3 = *reinterpret_cast<const uint4*>(gam + dh);
+  float xl[8], xh[8], gl[8], gh[8], cs[8], sn[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      cs[e] = p.rot[dl + e].x;
-      sn[e] = p.rot[dl + e].z;
-    }
-    unpack_bf16x8(r0, xl);
-    unpack_bf16x8(r1, xh);
-    unpack_bf16x8(r2, gl);
-    unpack_bf16x8(r3, gh);
+  for (int e = 0; e < 8; ++e) {
+    cs[e] = p.rot[dl + e].x;
+    sn[e] = p.rot[dl + e].z;
+  }
+  unpack_bf16x8(r0, xl);
+  unpack_bf16x8(r1, xh);
+  unpack_bf16x8(r2, gl);
+  unpack_bf16x8(r3, gh);
+  if (kind == 0) {
+    float yl[8], yh[8], factor;
     norm_rope(xl, xh, gl, gh, cs, sn, yl, yh);
-    float factor;
     f16_row(yl, yh, p.scale_log2, factor);
     uint8_t* q = smem + SM_Q + (buf * kRepText + oct) * kD * 2;
     *reinterpret_cast<uint4*>(q + 2 * dl) = pack8(yl, true);
@@ -233,26 +236,22 @@ __device__ __forceinline__ void prepare(const MxDecodeParams& p, uint8_t* smem, 
     if (i == 0) reinterpret_cast<float*>(smem + SM_QF)[buf * kRepText + oct] = factor;
     return;
   }
-  if (!last) return;
-  const int v = tid < 96 ? 0 : 1, i = tid & 31;
-  const __nv_bfloat16* src = (v ? L.v_raw : L.k_raw) + static_cast<size_t>(g) * kD;
-  auto two = [](const __nv_bfloat16* a) { return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(a)); };
-  const float2 a = two(src + 2 * i), b = two(src + 64 + 2 * i);
-  float x[4] = {a.x, a.y, b.x, b.y};
-  if (v == 0) {
-    const float2 ga = two(L.k_gamma + 2 * i), gb = two(L.k_gamma + 64 + 2 * i);
-    const float gm[4] = {ga.x, ga.y, gb.x, gb.y};
-    const float4 r0 = p.rot[2 * i], r1 = p.rot[2 * i + 1];
-    const Pair cs[2] = {{r0.x, r0.y}, {r1.x, r1.y}}, sn[2] = {{r0.z, r0.w}, {r1.z, r1.w}};
-    float y[4];
-    pair_norm_rope_warp(x, gm, cs, sn, y);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = y[e];
-  }
+  auto angle = [&](int e, Pair& c, Pair& s) {
+    const float4 a = p.rot[dl + e];
+    c = {a.x, a.y};
+    s = {a.z, a.w};
+  };
+  uint32_t cl, ch;
+  int el, eh;
+  if (kind == 1) mx_encode_k_octet(xl, xh, gl, gh, cs, sn, angle, cl, ch, el, eh);
+  else mx_encode_octet(xl, xh, cl, ch, el, eh);
+  if ((oct & 3) != 0) return;
+  const int v = kind - 1;
+  uint8_t* nw = smem + SM_NEW + buf * 144;
+  mx_store_octet(cl, ch, el, eh, nw + 64 * v, nw + 128 + 4 * v, 0, i, nullptr);
   __nv_bfloat16* val = v ? L.v_new : L.k_new;
-  mx_store_warp(x, smem + SM_NEW + buf * 144 + 64 * v, smem + SM_NEW + buf * 144 + 128 + 4 * v, 0, i, nullptr);
-  mx_store_warp(x, v ? L.vc : L.kc, v ? L.vs : L.ks, static_cast<size_t>(g) * p.Smax + p.pos, i,
-                val == nullptr ? nullptr : val + static_cast<size_t>(g) * kD);
+  mx_store_octet(cl, ch, el, eh, v ? L.vc : L.kc, v ? L.vs : L.ks, static_cast<size_t>(g) * p.Smax + p.pos, i,
+                 val == nullptr ? nullptr : val + static_cast<size_t>(g) * kD);
 }
 
 // --------------------------------------------------------------------------------- one chunk
