@@ -24,7 +24,7 @@
 // of tiles n and n + 1 does, so a softmax warpgroup finds its next scores ready; with two buffers and an
 // accumulator per warpgroup it waited for PV(n) and QK(n + 2) in turn, two thirds of the time. The
 // price is a running maximum shared by both warpgroups. A warpgroup works on tile n with the maximum that it
-// last knew (raised when a chunk passes it by 2^8) and compares notes with tile n - 1's warpgroup at the end,
+// last knew (raised when a chunk's weights pass it by far) and compares notes with tile n - 1's warpgroup at the end,
 // through shared memory: only where the two differ is P(n), or the accumulator, scaled.
 //
 // The instruction cache held earlier forms back: with the roles' loops unrolled, 68 % of the peak of
@@ -148,7 +148,6 @@ constexpr uint32_t kSmemBytes = SM_ABORT + 4 + 1024;  // + slack to align the ba
 static_assert(kSmemBytes <= 232448 && SM_RING % 128 == 0 && SM_X % 16 == 0 && SM_BAR % 8 == 0, "shared memory of one sm_103 CTA");
 constexpr uint32_t TM_S = 0, TM_O = 384, kTmemCols = 512;  // three score (then P) buffers, the accumulator
 constexpr int kRefField = 23, kMaxField = 26;  // f16 exponent field of 2^(e - R + 8), and its cut (all-zero blocks)
-constexpr float kLazy = 8.0f;
 constexpr uint32_t kBarSoftmax = 1;
 
 template <int N>
@@ -180,6 +179,24 @@ __device__ __forceinline__ void next_seg(Seg& s, int T) {  // the range's later 
   s.left -= s.j1;
 }
 
+// Tile n's place in a ring of three: b = n % 3, par = n / 3 & 1 (the parity of its barriers' phase).
+struct Ring3 {
+  uint32_t b = 0, par = 0;
+  __device__ __forceinline__ void step(uint32_t by = 1) {  // by 1 or 2 tiles
+    b += by;
+    if (b >= 3) {
+      b -= 3;
+      par ^= 1;
+    }
+  }
+  __device__ __forceinline__ Ring3 back(uint32_t by) const {  // the place of tile n - by, by 1 or 2
+    Ring3 r;
+    r.b = b >= by ? b - by : b + 3 - by;
+    r.par = b >= by ? par : par ^ 1;
+    return r;
+  }
+};
+
 struct Ctx {
   uint8_t* smem;
   uint32_t sbase, tmem;
@@ -199,6 +216,7 @@ struct Ctx {
     atomicOr(status, err);
     return false;
   }
+  __device__ __forceinline__ bool wait3(int b, const Ring3& r, uint32_t err) const { return wait(b + r.b, r.par, err); }
   // tile n's phase of a barrier of three
   __device__ __forceinline__ bool wait3(int b, uint32_t n, uint32_t err) const { return wait(b + n % 3, (n / 3) & 1, err); }
   __device__ __forceinline__ bool done3(int b, uint32_t n) const { return mbar_test_wait(bar(b + n % 3), (n / 3) & 1); }
@@ -299,54 +317,62 @@ __device__ __forceinline__ void producer(const MxExpertParams& p, const Ctx cx, 
 }
 
 // ----------------------------------------------------------------------------- converters
-// Row `row` of a packed tile as f16 into a tile of the swizzled layout: block b's codes times
-// 2^(scale - ref + 8), 0 for a dead row. The lanes take their blocks in an order that spreads them over the banks.
-__device__ __forceinline__ void convert_row(uint32_t dst, uint32_t src, int row, uint32_t scales, int ref, bool live) {
-  const uint32_t d = dst + row * 128, from = src + row * kMxRowBytes;
-  const uint32_t add = static_cast<uint32_t>((kRefField - ref) & 0xFFFF) * 0x10001u, cut = live ? kMaxField * 0x10001u : 0u;
-  const uint32_t f02 = __viaddmin_s16x2_relu(scales & 0x00FF00FFu, add, cut) << 10;         // blocks 0 and 2
-  const uint32_t f13 = __viaddmin_s16x2_relu((scales >> 8) & 0x00FF00FFu, add, cut) << 10;  // blocks 1 and 3
-#pragma unroll 1
-  for (int i = 0; i < 4; ++i) {
-    const int b = (i + (row >> 1)) & 3;
-    const uint4 c = ld_shared_v4(from + (b << 4));
-    const uint32_t f = __byte_perm(b & 1 ? f13 : f02, 0u, b & 2 ? 0x3232 : 0x1010);
-    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-    const uint32_t at = d + (b >> 1) * kAtom;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      uint32_t h[4];
-      mx_unpack8(w[k], h);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h[e]) : "r"(f));
-      st_shared_v4(at + (((4 * (b & 1) + k) ^ (row & 7)) << 4), h[0], h[1], h[2], h[3]);
-    }
-  }
-}
-
-// One warpgroup each for K (kv = 0) and V (kv = 1).
+// One warpgroup each for K (kv = 0) and V (kv = 1): thread = row of a packed tile, whose codes it writes as f16 into a
+// tile of the swizzled layout: block b's codes times 2^(scale - ref + 8), 0 for a dead row. A lane takes its row's
+// blocks in an order that spreads the lanes over the banks; what follows from that order is formed once, so that a
+// block costs 36 instructions for its codes and 7 more.
 __device__ __forceinline__ void converter(const MxExpertParams& p, const Ctx cx, int kv) {
   const int row = threadIdx.x & 127;
   const int full = B_FULL + kRing * kv, empty = B_EMPTY + kRing * kv, used = kv ? B_ODONE : B_SFULL, rdy = B_RDY + 2 * kv;
-  const uint32_t ring = cx.sbase + SM_RING + kv * kRing * kStageBytes, tiles = cx.sbase + (kv ? SM_V : SM_K);
   const volatile int* refs = reinterpret_cast<const volatile int*>(cx.smem + SM_REF) + 8 * kv;
+  uint32_t from[4], to[4], sel[4];  // the i-th block's place in the ring's first slot, in the first tile; its factor's selector
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int b = (i + (row >> 1)) & 3;
+    from[i] = cx.sbase + SM_RING + kv * kRing * kStageBytes + row * kMxRowBytes + 16 * b;
+    // word k of the block is chunk 4 (b % 2) + k of half b / 2; chunk c of a row sits at c ^ (row % 8)
+    to[i] = cx.sbase + (kv ? SM_V : SM_K) + (b >> 1) * kAtom + row * 128 + (((4 * (b & 1)) ^ (row & 7)) << 4);
+    sel[i] = b == 0 ? 0x1010 : b == 1 ? 0x5454 : b == 2 ? 0x3232 : 0x7676;
+  }
+  const uint32_t scale_at = cx.sbase + SM_RING + kv * kRing * kStageBytes + kCodes + 4 * row;
   uint32_t n = 0;
+  Ring3 r;
   bool ok = true;
 #pragma unroll 1
   for (Seg s = first_seg(cx.start, cx.end, p.T); ok && s.j1 > s.j0; next_seg(s, p.T)) {
 #pragma unroll 1
-    for (int j = s.j0; j < s.j1; ++j, ++n) {
-      const uint32_t src = ring + n % 3 * kStageBytes;
+    for (int j = s.j0; j < s.j1; ++j) {
       // the f16 buffer held tile n - 2: K's is free once QK(n-2) is done, V's once PV(n-2) is
-      ok = cx.wait(B_REF + 8 * kv + (n & 7), (n >> 3) & 1, kErrProducerWait) && cx.wait3(full, n, kErrProducerWait) &&
-           (n < 2 || cx.wait3(used, n - 2, kErrProducerWait));
+      ok = cx.wait(B_REF + 8 * kv + (n & 7), (n >> 3) & 1, kErrProducerWait) && cx.wait3(full, r, kErrProducerWait) &&
+           (n < 2 || cx.wait3(used, r.back(2), kErrProducerWait));
       if (!ok) break;
+      const uint32_t slot = r.b * kStageBytes, tile = (n & 1) * kTile;
       uint32_t sc;
-      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(sc) : "r"(src + kCodes + 4 * row) : "memory");
-      convert_row(tiles + (n & 1) * kTile, src, row, sc, refs[n & 7], row < tile_live(p, j));
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(sc) : "r"(scale_at + slot) : "memory");
+      const uint32_t add = static_cast<uint32_t>((kRefField - refs[n & 7]) & 0xFFFF) * 0x10001u;
+      const uint32_t cut = row < tile_live(p, j) ? kMaxField * 0x10001u : 0u;
+      const uint32_t f02 = __viaddmin_s16x2_relu(sc & 0x00FF00FFu, add, cut) << 10;         // blocks 0 and 2
+      const uint32_t f13 = __viaddmin_s16x2_relu((sc >> 8) & 0x00FF00FFu, add, cut) << 10;  // blocks 1 and 3
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 c = ld_shared_v4(from[i] + slot);
+        const uint32_t f = __byte_perm(f02, f13, sel[i]);
+        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+        const uint32_t at = to[i] + tile;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t h[4];
+          mx_unpack8(w[k], h);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h[e]) : "r"(f));
+          st_shared_v4(at ^ (16u * k), h[0], h[1], h[2], h[3]);
+        }
+      }
       fence_proxy_async_smem();
       mbar_arrive(cx.bar(rdy + (n & 1)));
-      mbar_arrive(cx.bar(empty + n % 3));
+      mbar_arrive(cx.bar(empty + r.b));
+      ++n;
+      r.step();
     }
   }
 }
@@ -511,112 +537,117 @@ __device__ __forceinline__ void softmax_warps(const MxExpertParams& p, const Ctx
   const volatile int* refs = reinterpret_cast<const volatile int*>(cx.smem + SM_REF);
   volatile float* run = reinterpret_cast<volatile float*>(cx.smem + SM_M) + r;
   uint32_t base = 0, seg = 0;
+  Ring3 rn;  // of this warpgroup's next tile
+  rn.step(k);
   bool ok = true;
-  auto wait3 = [&](int b, uint32_t n) -> bool { return __all_sync(0xffffffffu, cx.wait3(b, n, kErrSoftmaxWait)); };
+  auto wait3 = [&](int b, const Ring3& at) -> bool { return __all_sync(0xffffffffu, cx.wait3(b, at, kErrSoftmaxWait)); };
 #pragma unroll 1
   for (Seg s = first_seg(cx.start, cx.end, p.T); s.j1 > s.j0; next_seg(s, p.T)) {
     const int nt = s.j1 - s.j0;
     const float qf = p.q_factor[static_cast<size_t>(s.u) * kRows + r] * 0.00390625f;  // K's tiles carry 2^8
     float m = -INFINITY, lsum = 0.f;  // lsum: this warpgroup's keys, in units of 2^m
-    for (int i = (k ^ static_cast<int>(base)) & 1; ok && i < nt; i += 2) {
+#pragma unroll 1
+    for (int i = (k ^ static_cast<int>(base)) & 1; ok && i < nt; i += 2, rn.step(2)) {
       const uint32_t n = base + i;
       const int j = s.j0 + i;
       ok = __all_sync(0xffffffffu, cx.wait(B_REF + (n & 7), (n >> 3) & 1, kErrSoftmaxWait) &&
-                                       cx.wait(B_REF + 8 + (n & 7), (n >> 3) & 1, kErrSoftmaxWait)) && wait3(B_SFULL, n);
+                                       cx.wait(B_REF + 8 + (n & 7), (n >> 3) & 1, kErrSoftmaxWait)) && wait3(B_SFULL, rn);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t sa = cx.tmem + lane + TM_S + (n % 3) * 128;
+      const uint32_t sa = cx.tmem + lane + TM_S + rn.b * 128;
       const int ref = refs[8 + (n & 7)];
       const float ct = qf * mx_scale(refs[n & 7]);
       const int live = tile_live(p, j), npair = j < p.n_main ? 2 : 1;
       if (live < 64 * npair) mask_scores(sa, live, 64 * npair);
-      auto load_pair = [&](int pr, uint32_t (&v)[2][32]) {
-        tmem_ld32(sa + 64 * pr, v[0]);
-        tmem_ld32(sa + 64 * pr + 32, v[1]);
-        tmem_wait_ld();
-        reg_fence32(v[0]);
-        reg_fence32(v[1]);
-      };
       // (a segment's second tile starts from the first one's maximum: its own would seldom do)
       if (i == 1) {
-        ok = wait3(B_MDONE, n - 1);
+        ok = wait3(B_MDONE, rn.back(1));
         if (!ok) break;
         m = *run;
       }
       const float2 ct2 = make_float2(ct, ct);
-      float2 ts[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) ts[q] = make_float2(0.f, 0.f);
-      // P goes over the scores' first columns: chunk pr's 32 columns of pairs hold scores of chunks <= pr
+      // P goes over the scores' first columns: chunk pr's 32 columns of pairs hold scores of chunks <= pr.
+      // The maximum is not looked for: a chunk's sum that passes 2^13 tells that it has to rise (f16 holds
+      // weights up to 2^16), and then, as in the segment's first chunk, the chunk is done once more.
+      float tsum = 0.f;
 #pragma unroll 1
       for (int pr = 0; pr < npair; ++pr) {
-        uint32_t v[2][32];
-        load_pair(pr, v);
-        float mx[8];
+        uint32_t pk[2][16];
+        float cs;
+        bool rise = __any_sync(0xffffffffu, m == -INFINITY), again = !rise;
+#pragma unroll 1
+        for (;;) {
+          uint32_t v[2][32];
+          tmem_ld32(sa + 64 * pr, v[0]);
+          tmem_ld32(sa + 64 * pr + 32, v[1]);
+          tmem_wait_ld();
+          reg_fence32(v[0]);
+          reg_fence32(v[1]);
+          if (rise) {
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int q = 0; q < 8; ++q) mx[q] = -INFINITY;
+            for (int ch = 0; ch < 2; ++ch)
 #pragma unroll
-        for (int ch = 0; ch < 2; ++ch)
-#pragma unroll
-          for (int e = 0; e < 32; e += 2)
-            mx[(e >> 1) & 7] = fmax3(mx[(e >> 1) & 7], __uint_as_float(v[ch][e]), __uint_as_float(v[ch][e + 1]));
-        const float mc = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * ct;
-        // (chunk 0 always holds a key, so m is finite from there on)
-        const bool up = mc > m + kLazy || m == -INFINITY;
-        if (__any_sync(0xffffffffu, up)) {
-          const float mn = up ? fmaxf(m, mc) : m, a = ex2_approx(m - mn);
-          if (pr > 0) {  // the first chunk's P moves too
-            scale_p(sa, a, 1);
-            load_pair(pr, v);
+              for (int e = 0; e < 32; e += 2)
+                mx[(e >> 1) & 3] = fmax3(mx[(e >> 1) & 3], __uint_as_float(v[ch][e]), __uint_as_float(v[ch][e + 1]));
+            const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * ct), a = ex2_approx(m - mn);
+            if (pr > 0) scale_p(sa, a, 1);  // the first chunk's P moves too
+            tsum *= a;
+            lsum *= a;
+            m = mn;
           }
+          const float2 neg = make_float2(-m, -m);
+          float2 ts[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) ts[q] = make_float2(ts[q].x * a, ts[q].y * a);
-          lsum *= a;
-          m = mn;
+          for (int q = 0; q < 4; ++q) ts[q] = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int ch = 0; ch < 2; ++ch)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[ch][2 * e]), __uint_as_float(v[ch][2 * e + 1])), ct2, neg);
+              const float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
+              ts[e & 3] = __fadd2_rn(ts[e & 3], make_float2(p0, p1));
+              pk[ch][e] = pack_f16x2(p0, p1);
+            }
+          const float2 t01 = __fadd2_rn(ts[0], ts[1]), t23 = __fadd2_rn(ts[2], ts[3]), tt = __fadd2_rn(t01, t23);
+          cs = tt.x + tt.y;
+          if (!again || !__any_sync(0xffffffffu, cs > 8192.f)) break;
+          rise = true;
+          again = false;
         }
-        const float2 neg = make_float2(-m, -m);
-#pragma unroll
-        for (int ch = 0; ch < 2; ++ch) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[ch][2 * e]), __uint_as_float(v[ch][2 * e + 1])), ct2, neg);
-            const float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
-            ts[e & 3] = __fadd2_rn(ts[e & 3], make_float2(p0, p1));
-            pk[e] = pack_f16x2(p0, p1);
-          }
-          tmem_st16(sa + 32 * pr + 16 * ch, pk);
-        }
+        tsum += cs;
+        tmem_st16(sa + 32 * pr, pk[0]);
+        tmem_st16(sa + 32 * pr + 16, pk[1]);
       }
-      lsum += ((ts[0].x + ts[0].y) + (ts[1].x + ts[1].y)) + ((ts[2].x + ts[2].y) + (ts[3].x + ts[3].y));
+      lsum += tsum;
       tmem_wait_st();
       // the maximum that tile n - 1 left: the larger one holds from here on
       float scale = 1.f;  // of the accumulator
       if (i > 0) {
-        ok = wait3(B_MDONE, n - 1);
+        ok = wait3(B_MDONE, rn.back(1));
         if (!ok) break;
         const float before = *run, mn = fmaxf(m, before), a = ex2_approx(m - mn);
         if (__any_sync(0xffffffffu, a != 1.f)) scale_p(sa, a, npair);
         lsum *= a;
         m = mn;
         scale = ex2_approx(before - mn);
-        const int from = refs[8 + ((n - 1) & 7)];  // V's reference of the tile before, in the same segment
-        if (from != ref) scale = from - ref < -126 ? 0.f : scale * mx_pow2(from - ref);
+        const int prev = refs[8 + ((n - 1) & 7)];  // V's reference of the tile before, in the same segment
+        if (prev != ref) scale = prev - ref < -126 ? 0.f : scale * mx_pow2(prev - ref);
       }
       *run = m;
-      mbar_arrive(cx.bar(B_MDONE + n % 3));
+      mbar_arrive(cx.bar(B_MDONE + rn.b));
       if (__any_sync(0xffffffffu, scale != 1.f)) {  // the accumulator moves: stable once PV(n-1) is done
-        ok = wait3(B_ODONE, n - 1);
+        ok = wait3(B_ODONE, rn.back(1));
         if (!ok) break;
         tc_fence_after();
         scale_accumulator(oa, scale);
       }
       tc_fence_before();
-      mbar_arrive(cx.bar(B_PFULL + n % 3));
+      mbar_arrive(cx.bar(B_PFULL + rn.b));
     }
     // ---- the segment's end: the last PV, both warpgroups' sums; thread (k, r) takes columns [64 k, 64 k + 64)
     const uint32_t last = base + nt - 1;
-    if (ok) ok = wait3(B_ODONE, last);
+    if (ok) ok = __all_sync(0xffffffffu, cx.wait3(B_ODONE, last, kErrSoftmaxWait));
     // (by segment parity: a warpgroup may be here while the other still reads the segment before; it cannot
     // pass this segment's barrier before that)
     float2* xch = reinterpret_cast<float2*>(cx.smem + SM_X) + (seg & 1) * 2 * kRows;
