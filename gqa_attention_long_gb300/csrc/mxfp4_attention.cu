@@ -15,17 +15,16 @@
 // (raised when a tile exceeds it by 2^3). K's reference goes back into the scores, V's into the
 // output, both in fp32.
 //
-// Warp roles (640 threads):
-//   warps 0-3, 4-7  softmax of the even / odd tiles of the CTA: thread = query row = TMEM lane
-//   warps 8-11, 12-15  converters of K and of V: thread = key row of the tile; into double-buffered f16 tiles
-//   warps 16, 17  load K's and V's packed rows (bulk copies into three-stage rings) and set the tiles' references
-//   warps 18, 19  issue S = Q K^T (and load each segment's Q) and O += P V (P from TMEM)
-// TMEM: three score buffers (P(n) goes over S(n)) and one accumulator. QK(n + 2) runs while the softmax
-// of tiles n and n + 1 does, so a softmax warpgroup finds its next scores ready; with two buffers and an
-// accumulator per warpgroup it waited for PV(n) and QK(n + 2) in turn, two thirds of the time. The
-// price is a running maximum shared by both warpgroups. A warpgroup works on tile n with the maximum that it
-// last knew (raised when a chunk's weights pass it by far) and compares notes with tile n - 1's warpgroup at the end,
-// through shared memory: only where the two differ is P(n), or the accumulator, scaled.
+// Warp roles (768 threads):
+//   warps 0-3, 4-7, 8-11  softmax of the CTA's tiles in turn: thread = query row = TMEM lane
+//   warps 12-15, 16-19  converters of K and of V: thread = key row of the tile; into double-buffered f16 tiles
+//   warps 20, 21  load K's and V's packed rows (bulk copies into three-stage rings) and set the tiles' references
+//   warps 22, 23  issue S = Q K^T (and load each segment's Q) and O += P V (P from TMEM)
+// TMEM: three score buffers (P(n) goes over S(n)), one per softmax warpgroup, and one accumulator. A softmax warpgroup
+// waits for PV(n) and QK(n + 3) while the other two work; with two warpgroups, each with an accumulator, they
+// waited two thirds of the time. The price is a running maximum shared by the warpgroups: one works on tile n
+// with the maximum that it last knew (raised when a chunk's weights pass it by far) and compares notes with
+// tile n - 1's at the end, through shared memory: only where the two differ is P(n), or the accumulator, scaled.
 //
 // The instruction cache held earlier forms back: with the roles' loops unrolled, 68 % of the peak of
 // instruction fetches went to the second level and every role crawled (3,600 cycles a tile). So the
@@ -120,18 +119,20 @@ __global__ void __launch_bounds__(256) mxfp4_prologue_kernel(const __grid_consta
 
 namespace mxa {
 
-constexpr int kThreads = 640;
-constexpr int kSoftmax = 256, kConvert = 128;
-// registers per thread after the roles part (launched with 96): the sum is the launch's at most
-constexpr int kRegSoftmax = 136, kRegConvert = 72, kRegIssue = 64;
-static_assert(256 * kRegSoftmax + 256 * kRegConvert + 128 * kRegIssue <= kThreads * 96, "register split");
+constexpr int kSoftWg = 2, kConvWg = 2;  // warpgroups: softmax; converters of K, and of V
+constexpr int kSoftmax = 128 * kSoftWg, kConvert = 128 * kConvWg;
+constexpr int kThreads = kSoftmax + 2 * kConvert + 128;
+// registers per thread after the roles part (launched with kRegLaunch): the sum is the launch's at most
+constexpr int kRegLaunch = 65536 / kThreads / 8 * 8;
+constexpr int kRegSoftmax = 96, kRegConvert = 56, kRegIssue = 64;
+static_assert(kSoftmax * kRegSoftmax + 2 * kConvert * kRegConvert + 128 * kRegIssue <= kThreads * kRegLaunch, "register split");
 constexpr int kRing = 3;
 constexpr uint32_t kCodes = kKeyTile * kMxRowBytes, kScales = kKeyTile * kMxRowScales;
 constexpr uint32_t kStageBytes = kCodes + kScales;          // a tile's codes and scales, of K or of V
 constexpr uint32_t kAtom = 16384, kTile = 2 * kAtom;        // an f16 tile: two 64-channel halves
 constexpr uint32_t SM_Q = 0, SM_K = SM_Q + kTile, SM_V = SM_K + 2 * kTile, SM_RING = SM_V + 2 * kTile;
 constexpr uint32_t SM_X = SM_RING + 2 * kRing * kStageBytes;   // [segment parity][warpgroup][row] (m, l)
-constexpr uint32_t SM_M = SM_X + 4 * kRows * 8;             // [row] running maximum (log2 units)
+constexpr uint32_t SM_M = SM_X + 2 * kSoftWg * kRows * 8;             // [row] running maximum (log2 units)
 constexpr uint32_t SM_REF = SM_M + kRows * 4;               // [K, V][8]: R of tile n % 8
 constexpr uint32_t SM_BAR = SM_REF + 16 * 4;
 // by tile n % 3: FULL and EMPTY (K's ring, V's ring), SFULL, MDONE, PFULL, ODONE; by n % 2: RDY (K's f16 tiles,
@@ -141,7 +142,7 @@ constexpr int B_FULL = 0, B_EMPTY = 6, B_SFULL = 12, B_MDONE = 15, B_PFULL = 18,
 static_assert(kRing == 3, "barrier indices");
 __device__ __forceinline__ uint32_t bar_count(int b) {
   return b >= B_EMPTY && b < B_SFULL ? kConvert : b >= B_MDONE && b < B_ODONE ? 128 : b >= B_RDY && b < B_REF ? kConvert
-         : b == B_OFREE ? kSoftmax : 1;
+         : b == B_OFREE ? 256 : 1;
 }
 constexpr uint32_t SM_TMEM = SM_BAR + kNumBars * 8, SM_ABORT = SM_TMEM + 4;
 constexpr uint32_t kSmemBytes = SM_ABORT + 4 + 1024;  // + slack to align the base
@@ -182,7 +183,7 @@ __device__ __forceinline__ void next_seg(Seg& s, int T) {  // the range's later 
 // Tile n's place in a ring of three: b = n % 3, par = n / 3 & 1 (the parity of its barriers' phase).
 struct Ring3 {
   uint32_t b = 0, par = 0;
-  __device__ __forceinline__ void step(uint32_t by = 1) {  // by 1 or 2 tiles
+  __device__ __forceinline__ void step(uint32_t by = 1) {  // by 1 to 3 tiles
     b += by;
     if (b >= 3) {
       b -= 3;
@@ -317,18 +318,20 @@ __device__ __forceinline__ void producer(const MxExpertParams& p, const Ctx cx, 
 }
 
 // ----------------------------------------------------------------------------- converters
-// One warpgroup each for K (kv = 0) and V (kv = 1): thread = row of a packed tile, whose codes it writes as f16 into a
-// tile of the swizzled layout: block b's codes times 2^(scale - ref + 8), 0 for a dead row. A lane takes its row's
+// kConvWg warpgroups each for K (kv = 0) and V (kv = 1): thread = row of a packed tile (half of it, with two
+// warpgroups), whose codes it writes as f16 into a tile of the swizzled layout: block b's codes times 2^(scale - ref + 8), 0 for a dead row. A lane takes its row's
 // blocks in an order that spreads the lanes over the banks; what follows from that order is formed once, so that a
 // block costs 36 instructions for its codes and 7 more.
 __device__ __forceinline__ void converter(const MxExpertParams& p, const Ctx cx, int kv) {
   const int row = threadIdx.x & 127;
   const int full = B_FULL + kRing * kv, empty = B_EMPTY + kRing * kv, used = kv ? B_ODONE : B_SFULL, rdy = B_RDY + 2 * kv;
   const volatile int* refs = reinterpret_cast<const volatile int*>(cx.smem + SM_REF) + 8 * kv;
-  uint32_t from[4], to[4], sel[4];  // the i-th block's place in the ring's first slot, in the first tile; its factor's selector
+  constexpr int kBlocks = 4 / kConvWg;  // of a row's four, for this thread
+  const int first = (threadIdx.x - kSoftmax - kv * kConvert) / 128 * kBlocks;
+  uint32_t from[kBlocks], to[kBlocks], sel[kBlocks];  // the i-th block's place in the ring's first slot, in the first tile; its factor's selector
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int b = (i + (row >> 1)) & 3;
+  for (int i = 0; i < kBlocks; ++i) {
+    const int b = (first + i + (row >> 1)) & 3;
     from[i] = cx.sbase + SM_RING + kv * kRing * kStageBytes + row * kMxRowBytes + 16 * b;
     // word k of the block is chunk 4 (b % 2) + k of half b / 2; chunk c of a row sits at c ^ (row % 8)
     to[i] = cx.sbase + (kv ? SM_V : SM_K) + (b >> 1) * kAtom + row * 128 + (((4 * (b & 1)) ^ (row & 7)) << 4);
@@ -353,9 +356,12 @@ __device__ __forceinline__ void converter(const MxExpertParams& p, const Ctx cx,
       const uint32_t cut = row < tile_live(p, j) ? kMaxField * 0x10001u : 0u;
       const uint32_t f02 = __viaddmin_s16x2_relu(sc & 0x00FF00FFu, add, cut) << 10;         // blocks 0 and 2
       const uint32_t f13 = __viaddmin_s16x2_relu((sc >> 8) & 0x00FF00FFu, add, cut) << 10;  // blocks 1 and 3
+      uint4 blk[kBlocks];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint4 c = ld_shared_v4(from[i] + slot);
+      for (int i = 0; i < kBlocks; ++i) blk[i] = ld_shared_v4(from[i] + slot);
+#pragma unroll
+      for (int i = 0; i < kBlocks; ++i) {
+        const uint4 c = blk[i];
         const uint32_t f = __byte_perm(f02, f13, sel[i]);
         const uint32_t w[4] = {c.x, c.y, c.z, c.w};
         const uint32_t at = to[i] + tile;
@@ -497,20 +503,19 @@ __device__ __noinline__ void scale_accumulator(uint32_t addr, float a) {
   tmem_wait_st();
 }
 
-// P of a tile's first `chunks` 64-key chunks: 32 columns of f16 pairs each.
+// P of a tile's first `chunks` 32-key chunks: 16 columns of f16 pairs each.
 __device__ __noinline__ void scale_p(uint32_t addr, float a, int chunks) {
-  for (int c = 0; c < chunks; ++c) {
-    uint32_t q[32];
+  for (int c = 0; c < 2 * chunks; ++c) {
+    uint32_t q[8];
     tmem_wait_st();
-    tmem_ld32(addr + 32 * c, q);
+    tmem_ld8(addr + 8 * c, q);
     tmem_wait_ld();
-    reg_fence32(q);
 #pragma unroll
-    for (int e = 0; e < 32; ++e) {
+    for (int e = 0; e < 8; ++e) {
       const float2 f = unpack_f16x2(q[e]);
       q[e] = pack_f16x2(f.x * a, f.y * a);
     }
-    tmem_st32(addr + 32 * c, q);
+    tmem_st8(addr + 8 * c, q);
   }
   tmem_wait_st();
 }
@@ -538,7 +543,7 @@ __device__ __forceinline__ void softmax_warps(const MxExpertParams& p, const Ctx
   volatile float* run = reinterpret_cast<volatile float*>(cx.smem + SM_M) + r;
   uint32_t base = 0, seg = 0;
   Ring3 rn;  // of this warpgroup's next tile
-  rn.step(k);
+  rn.b = k;
   bool ok = true;
   auto wait3 = [&](int b, const Ring3& at) -> bool { return __all_sync(0xffffffffu, cx.wait3(b, at, kErrSoftmaxWait)); };
 #pragma unroll 1
@@ -547,7 +552,7 @@ __device__ __forceinline__ void softmax_warps(const MxExpertParams& p, const Ctx
     const float qf = p.q_factor[static_cast<size_t>(s.u) * kRows + r] * 0.00390625f;  // K's tiles carry 2^8
     float m = -INFINITY, lsum = 0.f;  // lsum: this warpgroup's keys, in units of 2^m
 #pragma unroll 1
-    for (int i = (k ^ static_cast<int>(base)) & 1; ok && i < nt; i += 2, rn.step(2)) {
+    for (int i = static_cast<int>((k + kSoftWg - base % kSoftWg) % kSoftWg); ok && i < nt; i += kSoftWg, rn.step(kSoftWg)) {
       const uint32_t n = base + i;
       const int j = s.j0 + i;
       ok = __all_sync(0xffffffffu, cx.wait(B_REF + (n & 7), (n >> 3) & 1, kErrSoftmaxWait) &&
@@ -557,67 +562,58 @@ __device__ __forceinline__ void softmax_warps(const MxExpertParams& p, const Ctx
       const uint32_t sa = cx.tmem + lane + TM_S + rn.b * 128;
       const int ref = refs[8 + (n & 7)];
       const float ct = qf * mx_scale(refs[n & 7]);
-      const int live = tile_live(p, j), npair = j < p.n_main ? 2 : 1;
-      if (live < 64 * npair) mask_scores(sa, live, 64 * npair);
-      // (a segment's second tile starts from the first one's maximum: its own would seldom do)
-      if (i == 1) {
-        ok = wait3(B_MDONE, rn.back(1));
+      const int live = tile_live(p, j), chunks = j < p.n_main ? 4 : 2;
+      if (live < 32 * chunks) mask_scores(sa, live, 32 * chunks);
+      // (the other warpgroups' first tiles of a segment start from its first tile's maximum: their own would seldom do)
+      if (i > 0 && i < kSoftWg) {
+        ok = wait3(B_MDONE, rn.back(i));
         if (!ok) break;
         m = *run;
       }
       const float2 ct2 = make_float2(ct, ct);
-      // P goes over the scores' first columns: chunk pr's 32 columns of pairs hold scores of chunks <= pr.
+      // P goes over the scores' first columns: chunk c's 16 columns of pairs hold scores of chunks <= c.
       // The maximum is not looked for: a chunk's sum that passes 2^13 tells that it has to rise (f16 holds
       // weights up to 2^16), and then, as in the segment's first chunk, the chunk is done once more.
       float tsum = 0.f;
 #pragma unroll 1
-      for (int pr = 0; pr < npair; ++pr) {
-        uint32_t pk[2][16];
+      for (int c = 0; c < chunks; ++c) {
+        uint32_t pk[16];
         float cs;
         bool rise = __any_sync(0xffffffffu, m == -INFINITY), again = !rise;
 #pragma unroll 1
         for (;;) {
-          uint32_t v[2][32];
-          tmem_ld32(sa + 64 * pr, v[0]);
-          tmem_ld32(sa + 64 * pr + 32, v[1]);
+          uint32_t v[32];
+          tmem_ld32(sa + 32 * c, v);
           tmem_wait_ld();
-          reg_fence32(v[0]);
-          reg_fence32(v[1]);
+          reg_fence32(v);
           if (rise) {
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int ch = 0; ch < 2; ++ch)
-#pragma unroll
-              for (int e = 0; e < 32; e += 2)
-                mx[(e >> 1) & 3] = fmax3(mx[(e >> 1) & 3], __uint_as_float(v[ch][e]), __uint_as_float(v[ch][e + 1]));
+            for (int e = 0; e < 32; e += 2)
+              mx[(e >> 1) & 3] = fmax3(mx[(e >> 1) & 3], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
             const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * ct), a = ex2_approx(m - mn);
-            if (pr > 0) scale_p(sa, a, 1);  // the first chunk's P moves too
+            if (c > 0) scale_p(sa, a, c);  // the earlier chunks' P moves too
             tsum *= a;
             lsum *= a;
             m = mn;
           }
           const float2 neg = make_float2(-m, -m);
-          float2 ts[4];
+          float2 ts[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-          for (int q = 0; q < 4; ++q) ts[q] = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int ch = 0; ch < 2; ++ch)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[ch][2 * e]), __uint_as_float(v[ch][2 * e + 1])), ct2, neg);
-              const float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
-              ts[e & 3] = __fadd2_rn(ts[e & 3], make_float2(p0, p1));
-              pk[ch][e] = pack_f16x2(p0, p1);
-            }
-          const float2 t01 = __fadd2_rn(ts[0], ts[1]), t23 = __fadd2_rn(ts[2], ts[3]), tt = __fadd2_rn(t01, t23);
+          for (int e = 0; e < 16; ++e) {
+            const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), ct2, neg);
+            const float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
+            ts[e & 1] = __fadd2_rn(ts[e & 1], make_float2(p0, p1));
+            pk[e] = pack_f16x2(p0, p1);
+          }
+          const float2 tt = __fadd2_rn(ts[0], ts[1]);
           cs = tt.x + tt.y;
           if (!again || !__any_sync(0xffffffffu, cs > 8192.f)) break;
           rise = true;
           again = false;
         }
         tsum += cs;
-        tmem_st16(sa + 32 * pr, pk[0]);
-        tmem_st16(sa + 32 * pr + 16, pk[1]);
+        tmem_st16(sa + 16 * c, pk);
       }
       lsum += tsum;
       tmem_wait_st();
@@ -627,7 +623,7 @@ __device__ __forceinline__ void softmax_warps(const MxExpertParams& p, const Ctx
         ok = wait3(B_MDONE, rn.back(1));
         if (!ok) break;
         const float before = *run, mn = fmaxf(m, before), a = ex2_approx(m - mn);
-        if (__any_sync(0xffffffffu, a != 1.f)) scale_p(sa, a, npair);
+        if (__any_sync(0xffffffffu, a != 1.f)) scale_p(sa, a, chunks);
         lsum *= a;
         m = mn;
         scale = ex2_approx(before - mn);
@@ -645,19 +641,21 @@ __device__ __forceinline__ void softmax_warps(const MxExpertParams& p, const Ctx
       tc_fence_before();
       mbar_arrive(cx.bar(B_PFULL + rn.b));
     }
-    // ---- the segment's end: the last PV, both warpgroups' sums; thread (k, r) takes columns [64 k, 64 k + 64)
+    // ---- the segment's end: the last PV, the warpgroups' sums; thread (k, r), k < 2, takes columns [64 k, 64 k + 64)
     const uint32_t last = base + nt - 1;
     if (ok) ok = __all_sync(0xffffffffu, cx.wait3(B_ODONE, last, kErrSoftmaxWait));
     // (by segment parity: a warpgroup may be here while the other still reads the segment before; it cannot
     // pass this segment's barrier before that)
-    float2* xch = reinterpret_cast<float2*>(cx.smem + SM_X) + (seg & 1) * 2 * kRows;
+    float2* xch = reinterpret_cast<float2*>(cx.smem + SM_X) + (seg & 1) * kSoftWg * kRows;
     xch[k * kRows + r] = make_float2(m, lsum);
     ok = bar_sync_and(kBarSoftmax, kSoftmax, ok);
-    if (ok) {
+    if (ok && k < 2) {
       tc_fence_after();
-      const float2 x0 = xch[r], x1 = xch[kRows + r];
-      const float M = fmaxf(x0.x, x1.x);  // the maximum never falls, so the last tile's is the larger
-      const float L = ex2_approx(x0.x - M) * x0.y + ex2_approx(x1.x - M) * x1.y;
+      float M = -INFINITY, L = 0.f;  // (the maximum never falls: the last tile's is the largest)
+#pragma unroll
+      for (int w = 0; w < kSoftWg; ++w) M = fmaxf(M, xch[w * kRows + r].x);
+#pragma unroll
+      for (int w = 0; w < kSoftWg; ++w) L += ex2_approx(xch[w * kRows + r].x - M) * xch[w * kRows + r].y;
       // O is in units of 2^(R - 127 - 8)
       const float inv = 1.0f / L * 0.00390625f, two_r = mx_scale(refs[8 + (last & 7)]);
       const int l = s.u / kHkv, g = s.u % kHkv;
@@ -743,17 +741,18 @@ __global__ void __launch_bounds__(mxa::kThreads, 1) mxfp4_attention_kernel(const
   tc_fence_after();
   cx.tmem = *reinterpret_cast<volatile uint32_t*>(smem + SM_TMEM);
   pdl_wait_primary();
-  if (warp < 8) {
-    regs_up<kRegSoftmax>();
+  constexpr int kConv0 = kSoftmax / 32, kIssue0 = kConv0 + 2 * kConvert / 32;  // the roles' first warps
+  if (warp < kConv0) {
+    if constexpr (kRegSoftmax > kRegLaunch) regs_up<kRegSoftmax>();
     softmax_warps(p, cx);
-  } else if (warp < 16) {
+  } else if (warp < kIssue0) {
     regs_down<kRegConvert>();
-    converter(p, cx, warp >= 12);
+    converter(p, cx, warp >= kConv0 + kConvert / 32);
   } else {
     regs_down<kRegIssue>();
-    if (warp < 18) producer(p, cx, warp & 1);
-    if (warp == 18) qk_issuer(p, cx);
-    if (warp == 19) pv_issuer(p, cx);
+    if (warp < kIssue0 + 2) producer(p, cx, warp - kIssue0);
+    if (warp == kIssue0 + 2) qk_issuer(p, cx);
+    if (warp == kIssue0 + 3) pv_issuer(p, cx);
   }
   tc_fence_before();
   __syncthreads();
