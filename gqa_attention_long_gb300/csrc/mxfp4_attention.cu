@@ -119,12 +119,12 @@ __global__ void __launch_bounds__(256) mxfp4_prologue_kernel(const __grid_consta
 
 namespace mxa {
 
-constexpr int kSoftWg = 2, kConvWg = 2;  // warpgroups: softmax; converters of K, and of V
+constexpr int kSoftWg = 3, kConvWg = 1;  // warpgroups: softmax; converters of K, and of V
 constexpr int kSoftmax = 128 * kSoftWg, kConvert = 128 * kConvWg;
 constexpr int kThreads = kSoftmax + 2 * kConvert + 128;
 // registers per thread after the roles part (launched with kRegLaunch): the sum is the launch's at most
 constexpr int kRegLaunch = 65536 / kThreads / 8 * 8;
-constexpr int kRegSoftmax = 96, kRegConvert = 56, kRegIssue = 64;
+constexpr int kRegSoftmax = 88, kRegConvert = 72, kRegIssue = 64;
 static_assert(kSoftmax * kRegSoftmax + 2 * kConvert * kRegConvert + 128 * kRegIssue <= kThreads * kRegLaunch, "register split");
 constexpr int kRing = 3;
 constexpr uint32_t kCodes = kKeyTile * kMxRowBytes, kScales = kKeyTile * kMxRowScales;
