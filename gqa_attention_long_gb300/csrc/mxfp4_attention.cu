@@ -223,6 +223,13 @@ struct Ctx {
   __device__ __forceinline__ bool done3(int b, uint32_t n) const { return mbar_test_wait(bar(b + n % 3), (n / 3) & 1); }
 };
 
+// One lane of a warp that has converged, so that what it issues may take operands from the warp's uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // Tile j of a unit: its first cache row and how many of its 128 rows are keys.
 __device__ __forceinline__ int tile_row0(const MxExpertParams& p, int j) { return j < p.n_main ? j * kKeyTile : p.Smax - kTok; }
 __device__ __forceinline__ int tile_live(const MxExpertParams& p, int j) {
@@ -249,47 +256,61 @@ __device__ __noinline__ int top_nonzero(uint32_t tile, int lane, int live) {
 }
 
 // One warp each for K (kv = 0) and V (kv = 1): loads the tiles, and one tile ahead of the converters looks
-// at a tile's scales and publishes its reference.
-__device__ __forceinline__ void producer(const MxExpertParams& p, const Ctx cx, int kv) {
+// at a tile's scales and publishes its reference. (Its own time a tile is what the rest waits for when it is long:
+// the copies' operands are uniform over the warp, as the MMAs' are, and their sources step from tile to tile.)
+template <int kv>
+__device__ __forceinline__ void producer(const MxExpertParams& p, const Ctx cx) {
   const int lane = threadIdx.x & 31;
-  const int full = B_FULL + kRing * kv, empty = B_EMPTY + kRing * kv;
+  constexpr int kFull = B_FULL + kRing * kv, kEmpty = B_EMPTY + kRing * kv;
   const uint32_t ring = cx.sbase + SM_RING + kv * kRing * kStageBytes;
   volatile int* refs = reinterpret_cast<volatile int*>(cx.smem + SM_REF) + 8 * kv;
-  const uint32_t total = static_cast<uint32_t>(cx.end - cx.start);
+  const int total = static_cast<int>(cx.end - cx.start);
+  const uint64_t pol = l2_policy_evict_first();
   Seg l = first_seg(cx.start, cx.end, p.T), v = l;  // of the next tile to load, and of the next to look at
-  int lj = l.j0, vj = v.j0, ref = 0;
-  uint32_t ln = 0;
+  int lj = l.j0, vj = v.j0, ref = 0, ln = 0;
+  const uint8_t *codes = nullptr, *scales = nullptr;  // of the next tile to load
+  bool jump = true;                                   // they are to be formed anew
+  Ring3 at, look;                                     // the places of the two tiles
   bool ok = true;
 #pragma unroll 1
-  for (uint32_t vn = 0; vn < total; ++vn) {
+  for (int vn = -1; vn < total; ++vn) {
     // tile vn + 1 is loaded once tile vn - 2, whose slot it takes, is converted; then tile vn is looked at
-#pragma unroll 1
-    while (ok && ln < total && ln <= vn + 1) {
-      if (ln >= kRing) ok = __all_sync(0xffffffffu, cx.wait3(empty, ln - kRing, kErrProducerWait));
-      if (!ok) break;
-      if (lane == 0) {
+    if (vn + 1 < total) {
+      if (jump) {
         const MxAttnLayer& L = p.layer[l.u / kHkv];
         const size_t row = static_cast<size_t>(l.u % kHkv) * p.Smax + tile_row0(p, lj);
-        const int live = tile_live(p, lj);
-        // scale words come in fours: up to three rows past the last key (still in the cache) come along
-        const uint32_t cb = live * kMxRowBytes, sb = ((live + 3) & ~3) * kMxRowScales;
-        const uint32_t fb = cx.bar(full + ln % 3), dst = ring + ln % 3 * kStageBytes;
-        const uint64_t pol = l2_policy_evict_first();
-        mbar_expect_tx(fb, cb + sb);
-        bulk_load(dst, (kv ? L.vc : L.kc) + row * kMxRowBytes, cb, fb, pol);
-        bulk_load(dst + kCodes, (kv ? L.vs : L.ks) + row * kMxRowScales, sb, fb, pol);
+        codes = (kv ? L.vc : L.kc) + row * kMxRowBytes;
+        scales = (kv ? L.vs : L.ks) + row * kMxRowScales;
       }
+      if (vn >= kRing - 1) ok = __all_sync(0xffffffffu, cx.wait(kEmpty + at.b, at.par ^ 1, kErrProducerWait));
+      if (!ok) break;
+      const int live = tile_live(p, lj);
+      // scale words come in fours: up to three rows past the last key (still in the cache) come along
+      const uint32_t cb = live * kMxRowBytes, sb = ((live + 3) & ~3) * kMxRowScales;
+      const uint32_t fb = cx.bar(kFull + at.b), dst = ring + at.b * kStageBytes;
+      if (elect_one()) {
+        mbar_expect_tx(fb, cb + sb);
+        bulk_load(dst, codes, cb, fb, pol);
+        bulk_load(dst + kCodes, scales, sb, fb, pol);
+      }
+      __syncwarp();
       ++ln;
-      if (++lj == l.j1) {
+      at.step();
+      codes += kCodes;
+      scales += kScales;
+      ++lj;
+      jump = lj == l.j1 || lj == p.n_main;
+      if (lj == l.j1) {
         next_seg(l, p.T);
         lj = 0;
       }
     }
-    ok = ok && __all_sync(0xffffffffu, cx.wait3(full, vn, kErrProducerWait));
+    if (vn < 0) continue;
+    ok = __all_sync(0xffffffffu, cx.wait(kFull + look.b, look.par, kErrProducerWait));
     if (!ok) break;
     if (vj == v.j0) ref = 0;  // a segment starts: references of its own
     const int live = tile_live(p, vj);
-    const uint32_t tile = ring + vn % 3 * kStageBytes;
+    const uint32_t tile = ring + look.b * kStageBytes;
     const uint4 sc = ld_shared_v4(tile + kCodes + 16 * lane);  // of four rows
     const uint32_t a = __vmaxu2(__vmaxu2(sc.x & 0x00FF00FFu, sc.y & 0x00FF00FFu), __vmaxu2(sc.z & 0x00FF00FFu, sc.w & 0x00FF00FFu));
     const uint32_t b = __vmaxu2(__vmaxu2((sc.x >> 8) & 0x00FF00FFu, (sc.y >> 8) & 0x00FF00FFu),
@@ -304,6 +325,7 @@ __device__ __forceinline__ void producer(const MxExpertParams& p, const Ctx cx, 
       refs[vn & 7] = ref;
       mbar_arrive(cx.bar(B_REF + 8 * kv + (vn & 7)));
     }
+    look.step();
     if (++vj == v.j1) {
       next_seg(v, p.T);
       vj = 0;
@@ -312,8 +334,8 @@ __device__ __forceinline__ void producer(const MxExpertParams& p, const Ctx cx, 
   __syncwarp();
   if (kv) pdl_launch_dependents();
   if (!ok && lane == 0)  // let every copy already issued land before the CTA gives its shared memory back
-    for (uint32_t k = 1; k <= kRing && k <= ln; ++k)
-      if (!drain_wait(cx.bar(full + (ln - k) % 3), ((ln - k) / 3) & 1)) atomicOr(cx.status, kErrDrain);
+    for (int k = 1; k <= kRing && k <= ln; ++k)
+      if (!drain_wait(cx.bar(kFull + (ln - k) % 3), ((ln - k) / 3) & 1)) atomicOr(cx.status, kErrDrain);
   __syncwarp();
 }
 
@@ -324,7 +346,7 @@ __device__ __forceinline__ void producer(const MxExpertParams& p, const Ctx cx, 
 // block costs 36 instructions for its codes and 7 more.
 __device__ __forceinline__ void converter(const MxExpertParams& p, const Ctx cx, int kv) {
   const int row = threadIdx.x & 127;
-  const int full = B_FULL + kRing * kv, empty = B_EMPTY + kRing * kv, used = kv ? B_ODONE : B_SFULL, rdy = B_RDY + 2 * kv;
+  const int empty = B_EMPTY + kRing * kv, used = kv ? B_ODONE : B_SFULL, rdy = B_RDY + 2 * kv;
   const volatile int* refs = reinterpret_cast<const volatile int*>(cx.smem + SM_REF) + 8 * kv;
   constexpr int kBlocks = 4 / kConvWg;  // of a row's four, for this thread
   const int first = (threadIdx.x - kSoftmax - kv * kConvert) / 128 * kBlocks;
@@ -345,9 +367,8 @@ __device__ __forceinline__ void converter(const MxExpertParams& p, const Ctx cx,
   for (Seg s = first_seg(cx.start, cx.end, p.T); ok && s.j1 > s.j0; next_seg(s, p.T)) {
 #pragma unroll 1
     for (int j = s.j0; j < s.j1; ++j) {
-      // the f16 buffer held tile n - 2: K's is free once QK(n-2) is done, V's once PV(n-2) is
-      ok = cx.wait(B_REF + 8 * kv + (n & 7), (n >> 3) & 1, kErrProducerWait) && cx.wait3(full, r, kErrProducerWait) &&
-           (n < 2 || cx.wait3(used, r.back(2), kErrProducerWait));
+      // (whoever published the reference had seen the tile arrive)
+      ok = cx.wait(B_REF + 8 * kv + (n & 7), (n >> 3) & 1, kErrProducerWait);
       if (!ok) break;
       const uint32_t slot = r.b * kStageBytes, tile = (n & 1) * kTile;
       uint32_t sc;
@@ -359,6 +380,9 @@ __device__ __forceinline__ void converter(const MxExpertParams& p, const Ctx cx,
       uint4 blk[kBlocks];
 #pragma unroll
       for (int i = 0; i < kBlocks; ++i) blk[i] = ld_shared_v4(from[i] + slot);
+      // the f16 buffer held tile n - 2: K's is free once QK(n-2) is done, V's once PV(n-2) is
+      ok = n < 2 || cx.wait3(used, r.back(2), kErrProducerWait);
+      if (!ok) break;
 #pragma unroll
       for (int i = 0; i < kBlocks; ++i) {
         const uint4 c = blk[i];
@@ -392,11 +416,6 @@ __device__ __forceinline__ void converter(const MxExpertParams& p, const Ctx cx,
 // The whole warp runs the loop and one elected lane issues: so every operand is uniform over the warp and sits in
 // the uniform registers that the instruction takes. From a lone lane's registers each of an MMA's operands
 // was moved over first, about 130 cycles an MMA where the tensor core takes 64.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-  return p != 0;
-}
 // Both operands' descriptors differ from tile to tile and step to step in their address field alone.
 constexpr uint64_t kDescK = (1ull << 61 << 1) | (1ull << 46) | (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 16);
 constexpr uint64_t kDescMN = (1ull << 61 << 1) | (1ull << 46) | (static_cast<uint64_t>(1024 >> 4) << 32) |
@@ -560,8 +579,13 @@ __device__ __forceinline__ void softmax_warps(const MxExpertParams& p, const Ctx
       if (!ok) break;
       tc_fence_after();
       const uint32_t sa = cx.tmem + lane + TM_S + rn.b * 128;
-      const int ref = refs[8 + (n & 7)];
       const float ct = qf * mx_scale(refs[n & 7]);
+      // what V's reference, if it rose from the tile before (in the same segment) to this one, makes of the accumulator
+      float scale = 1.f;
+      if (i > 0) {
+        const int d = refs[8 + ((n - 1) & 7)] - refs[8 + (n & 7)];
+        if (d != 0) scale = d < -126 ? 0.f : mx_pow2(d);
+      }
       const int live = tile_live(p, j), chunks = j < p.n_main ? 4 : 2;
       if (live < 32 * chunks) mask_scores(sa, live, 32 * chunks);
       // (the other warpgroups' first tiles of a segment start from its first tile's maximum: their own would seldom do)
@@ -617,20 +641,22 @@ __device__ __forceinline__ void softmax_warps(const MxExpertParams& p, const Ctx
       }
       lsum += tsum;
       tmem_wait_st();
-      // the maximum that tile n - 1 left: the larger one holds from here on
-      float scale = 1.f;  // of the accumulator
+      // the maximum that tile n - 1 left, nearly always this tile's too: else the larger one holds from here on
       if (i > 0) {
         ok = wait3(B_MDONE, rn.back(1));
         if (!ok) break;
-        const float before = *run, mn = fmaxf(m, before), a = ex2_approx(m - mn);
-        if (__any_sync(0xffffffffu, a != 1.f)) scale_p(sa, a, chunks);
-        lsum *= a;
-        m = mn;
-        scale = ex2_approx(before - mn);
-        const int prev = refs[8 + ((n - 1) & 7)];  // V's reference of the tile before, in the same segment
-        if (prev != ref) scale = prev - ref < -126 ? 0.f : scale * mx_pow2(prev - ref);
+        const float before = *run;
+        if (__any_sync(0xffffffffu, before != m)) {
+          const float mn = fmaxf(m, before), a = ex2_approx(m - mn);
+          if (__any_sync(0xffffffffu, a != 1.f)) scale_p(sa, a, chunks);
+          lsum *= a;
+          m = mn;
+          scale *= ex2_approx(before - mn);
+          *run = m;
+        }
+      } else {
+        *run = m;
       }
-      *run = m;
       mbar_arrive(cx.bar(B_MDONE + rn.b));
       if (__any_sync(0xffffffffu, scale != 1.f)) {  // the accumulator moves: stable once PV(n-1) is done
         ok = wait3(B_ODONE, rn.back(1));
@@ -750,7 +776,8 @@ __global__ void __launch_bounds__(mxa::kThreads, 1) mxfp4_attention_kernel(const
     converter(p, cx, warp >= kConv0 + kConvert / 32);
   } else {
     regs_down<kRegIssue>();
-    if (warp < kIssue0 + 2) producer(p, cx, warp - kIssue0);
+    if (warp == kIssue0) producer<0>(p, cx);
+    if (warp == kIssue0 + 1) producer<1>(p, cx);
     if (warp == kIssue0 + 2) qk_issuer(p, cx);
     if (warp == kIssue0 + 3) pv_issuer(p, cx);
   }
