@@ -37,12 +37,13 @@ namespace ea {
 
 // ------------------------------------------------------------------------------- prologue
 // One octet of threads per token and kv head: the token's two q rows, its k row and its v row, whose angles are formed
-// once; or, when there are too few of them to fill the GPU (gridDim.x = 8), one of the four rows. grid (2 or 8, kv
-// heads, layers).
-__global__ void __launch_bounds__(256) mxfp4_prologue_kernel(const __grid_constant__ MxPrologueParams p) {
+// once (three CTAs to an SM); or, when there are too few of them to fill the GPU (kSplit), one of the four
+// rows. grid (2 or 8, kv heads, layers).
+template <bool kSplit>
+__global__ void __launch_bounds__(256, kSplit ? 1 : 3) mxfp4_prologue_kernel(const __grid_constant__ MxPrologueParams p) {
   const int g = blockIdx.y, l = blockIdx.z, i = threadIdx.x & 7;
   const int t = 32 * (blockIdx.x & 1) + (threadIdx.x >> 3);
-  const int row0 = gridDim.x == 8 ? blockIdx.x >> 1 : 0, row1 = gridDim.x == 8 ? row0 + 1 : 4;
+  const int row0 = kSplit ? blockIdx.x >> 1 : 0, row1 = kSplit ? row0 + 1 : 4;
   const int dl = 8 * i, dh = 64 + 8 * i;
   // The tables' rows that this half of the tokens needs, copied to shared memory while the preceding kernel ends (they
   // are read by lane-dependent index: through a generic address, not the constant bank). Frequency j at j + j / 8: an
@@ -804,8 +805,9 @@ cudaError_t mxfp4_attention_set_attributes() {
 
 cudaError_t launch_mxfp4_prologue(const MxPrologueParams& p, int n_layers, cudaLaunchConfig_t cfg) {
   cfg.blockDim = dim3(256);
-  cfg.gridDim = dim3(n_layers <= 4 ? 8 : 2, kHkv, n_layers);
-  return cudaLaunchKernelEx(&cfg, mxfp4_prologue_kernel, p);
+  const bool split = n_layers <= 4;
+  cfg.gridDim = dim3(split ? 8 : 2, kHkv, n_layers);
+  return cudaLaunchKernelEx(&cfg, split ? mxfp4_prologue_kernel<true> : mxfp4_prologue_kernel<false>, p);
 }
 
 cudaError_t launch_mxfp4_attention(const MxExpertParams& p, cudaLaunchConfig_t cfg) {
