@@ -575,8 +575,8 @@ __device__ __forceinline__ void softmax_warps(const MxExpertParams& p, const Ctx
     for (int i = static_cast<int>((k + kSoftWg - base % kSoftWg) % kSoftWg); ok && i < nt; i += kSoftWg, rn.step(kSoftWg)) {
       const uint32_t n = base + i;
       const int j = s.j0 + i;
-      ok = __all_sync(0xffffffffu, cx.wait(B_REF + (n & 7), (n >> 3) & 1, kErrSoftmaxWait) &&
-                                       cx.wait(B_REF + 8 + (n & 7), (n >> 3) & 1, kErrSoftmaxWait)) && wait3(B_SFULL, rn);
+      // (K's reference was there before its tile was converted)
+      ok = __all_sync(0xffffffffu, cx.wait(B_REF + 8 + (n & 7), (n >> 3) & 1, kErrSoftmaxWait)) && wait3(B_SFULL, rn);
       if (!ok) break;
       tc_fence_after();
       const uint32_t sa = cx.tmem + lane + TM_S + rn.b * 128;
@@ -600,11 +600,13 @@ __device__ __forceinline__ void softmax_warps(const MxExpertParams& p, const Ctx
       // The maximum is not looked for: a chunk's sum that passes 2^13 tells that it has to rise (f16 holds
       // weights up to 2^16), and then, as in the segment's first chunk, the chunk is done once more.
       float tsum = 0.f;
+      bool first = __any_sync(0xffffffffu, m == -INFINITY);
 #pragma unroll 1
       for (int c = 0; c < chunks; ++c) {
         uint32_t pk[16];
         float cs;
-        bool rise = __any_sync(0xffffffffu, m == -INFINITY), again = !rise;
+        bool rise = first, again = !first;
+        first = false;
 #pragma unroll 1
         for (;;) {
           uint32_t v[32];
