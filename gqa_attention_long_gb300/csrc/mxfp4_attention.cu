@@ -685,21 +685,12 @@ __device__ __forceinline__ void softmax_warps(const MxExpertParams& p, const Ctx
       for (int w = 0; w < kSoftWg; ++w) M = fmaxf(M, xch[w * kRows + r].x);
 #pragma unroll
       for (int w = 0; w < kSoftWg; ++w) L += ex2_approx(xch[w * kRows + r].x - M) * xch[w * kRows + r].y;
-      // O is in units of 2^(R - 127 - 8)
-      const float inv = 1.0f / L * 0.00390625f, two_r = mx_scale(refs[8 + (last & 7)]);
-      const int l = s.u / kHkv, g = s.u % kHkv;
+      // O is in units of 2^(R - 127 - 8): a value is o * inv * f
+      const float inv = 1.0f / L * 0.00390625f;
+      const int rv = refs[8 + (last & 7)], l = s.u / kHkv, g = s.u % kHkv;
       const bool full = s.j0 == 0 && s.j1 == p.T;
       const uint32_t col = oa + 64 * k;
-      // columns [32 h, 32 h + 32) of the half row
-      auto load32 = [&](int h, float (&o)[32]) {
-        uint32_t v[32];
-        tmem_ld32(col + 32 * h, v);
-        tmem_wait_ld();
-        reg_fence32(v);
-#pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(v[e]) * inv * two_r;
-      };
-      float up = 1.f;
+      float f = mx_scale(rv);
       uint4* dst;
       size_t step = 1;
       if (full) {
@@ -710,13 +701,16 @@ __device__ __forceinline__ void softmax_warps(const MxExpertParams& p, const Ctx
         float amax = 0.f;
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
-          float o[32];
-          load32(h, o);
+          uint32_t v[32];
+          tmem_ld32(col + 32 * h, v);
+          tmem_wait_ld();
+          reg_fence32(v);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) amax = fmaxf(amax, fabsf(o[e]));
+          for (int e = 0; e < 32; e += 2) amax = fmax3(amax, fabsf(__uint_as_float(v[e])), fabsf(__uint_as_float(v[e + 1])));
         }
+        amax = amax * inv * f;
         const int ex = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 14, -126), 112);
-        up = mx_pow2(-ex);
+        if (rv != 255) f = mx_pow2(min(max(rv - 127 - ex, -126), 127));
         dst = p.part_o + (sl * kPartChunks + 8 * k) * kRows + r;
         step = kRows;
         p.part_lse[(sl * 3 + 1 + k) * kRows + r] = mx_pow2(ex);
@@ -724,18 +718,22 @@ __device__ __forceinline__ void softmax_warps(const MxExpertParams& p, const Ctx
       }
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
-        float o[32];
-        load32(h, o);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float x[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = o[8 * c + e] * up;
-          dst[(4 * h + c) * step] = pack8(x, !full);
+        uint32_t v[32], pk[16];
+        tmem_ld32(col + 32 * h, v);
+        tmem_wait_ld();
+        reg_fence32(v);
+        if (h == 1) {
+          tc_fence_before();
+          mbar_arrive(cx.bar(B_OFREE));  // the accumulator is read
         }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float x = __uint_as_float(v[2 * e]) * inv * f, y = __uint_as_float(v[2 * e + 1]) * inv * f;
+          pk[e] = full ? pack_bf16x2(x, y) : pack_f16x2(x, y);
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) dst[(4 * h + c) * step] = make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
       }
-      tc_fence_before();
-      mbar_arrive(cx.bar(B_OFREE));  // the accumulator is read
     }
     base += nt;
     ++seg;
