@@ -74,13 +74,17 @@ __global__ void __launch_bounds__(mx::kThreads) mxfp4_write_kernel(const __grid_
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      float amax = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[u][i]));
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      auto block_max = [&] {
+        const float a = mx_amax8<true>(x[u]), b = mx_max<true>(a, __shfl_xor_sync(0xffffffffu, a, 1));
+        return mx_max<true>(b, __shfl_xor_sync(0xffffffffu, b, 2));
+      };
+      float amax = block_max();
+      if (__any_sync(0xffffffffu, amax != amax)) {
+        mx_clean8(x[u]);
+        amax = block_max();
+      }
       const int e = mx_exponent(amax);
-      const uint32_t w = mx_pack8(x[u], mx_pow2(-e));
+      const uint32_t w = mx_pack8<true>(x[u], mx_pow2(-e));
       // the row's four scale bytes (lanes 0, 4, 8, 12 of its 16) in one word
       uint32_t sc = static_cast<uint32_t>(e + 127) << (8 * (c >> 2));
       sc |= __shfl_xor_sync(0xffffffffu, sc, 4);

@@ -109,8 +109,8 @@ __global__ void __launch_bounds__(256, kSplit ? 1 : 3) mxfp4_prologue_kernel(con
     }
     uint32_t cl, ch;
     int el, eh;
-    if (kind == 2) mx_encode_k_octet(xl, xh, gl, gh, cs, sn, angle, cl, ch, el, eh);
-    else mx_encode_octet(xl, xh, cl, ch, el, eh);
+    if (kind == 2) mx_encode_k_octet<true>(xl, xh, gl, gh, cs, sn, angle, cl, ch, el, eh);
+    else mx_encode_octet<true>(xl, xh, cl, ch, el, eh);
     __nv_bfloat16* val = kind == 2 ? L.k_new : L.v_new;
     if (val != nullptr) val += (static_cast<size_t>(g) * kTok + t) * kD;
     mx_store_octet(cl, ch, el, eh, kind == 2 ? L.kc : L.vc, kind == 2 ? L.ks : L.vs,

@@ -243,8 +243,8 @@ __device__ __forceinline__ void prepare(const MxDecodeParams& p, uint8_t* smem, 
   };
   uint32_t cl, ch;
   int el, eh;
-  if (kind == 1) mx_encode_k_octet(xl, xh, gl, gh, cs, sn, angle, cl, ch, el, eh);
-  else mx_encode_octet(xl, xh, cl, ch, el, eh);
+  if (kind == 1) mx_encode_k_octet<false>(xl, xh, gl, gh, cs, sn, angle, cl, ch, el, eh);
+  else mx_encode_octet<false>(xl, xh, cl, ch, el, eh);
   if ((oct & 3) != 0) return;
   const int v = kind - 1;
   uint8_t* nw = smem + SM_NEW + buf * 144;
