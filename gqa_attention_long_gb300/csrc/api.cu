@@ -3,6 +3,7 @@
 // prologue kernel; the attention kernel, which does the bf16 prologue itself and merges the split
 // units), chained with programmatic dependent launch.
 // See include/expert_attn.h for the contract.
+#include <array>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
@@ -1116,30 +1117,32 @@ int validate_mx_cache(const void* kc, const void* ks, const void* vc, const void
   return EA_OK;
 }
 
-// No two of the caches that one call writes may be the same: their rows would be written twice.
-template <class A>
-bool mx_caches_distinct(const A* a, int n) {
+// Whether the arrays that one call writes, get(a[l])[0 .. N) of every layer, are all different: what stands twice
+// would be written twice, in any order.
+template <int N, class A, class Get>
+bool mx_distinct(const A* a, int n, Get get) {
+  constexpr uint32_t kSlots = 512;
+  static_assert(N * kMaxLayersPerLaunch <= kSlots / 2, "table");
   for (int l0 = 0; l0 < n; l0 += kMaxLayersPerLaunch) {
-    constexpr uint32_t kSlots = 512;
     const void* seen[kSlots] = {};
-    auto add = [&](const void* p) {
+    auto find = [&](const void* p) {  // p's place, or the free one where it belongs
       uint32_t h = static_cast<uint32_t>((reinterpret_cast<uintptr_t>(p) >> 4) * 0x9E3779B97F4A7C15ull >> 55);
-      for (; seen[h] != nullptr; h = (h + 1) % kSlots)
-        if (seen[h] == p) return false;
-      seen[h] = p;
-      return true;
+      while (seen[h] != nullptr && seen[h] != p) h = (h + 1) % kSlots;
+      return h;
     };
     const int l1 = l0 + kMaxLayersPerLaunch < n ? l0 + kMaxLayersPerLaunch : n;
-    for (int l = l0; l < l1; ++l)
-      if (!add(a[l].k_codes) || !add(a[l].v_codes)) return false;
-    for (int l = l1; l < n; ++l)  // this table's caches against the later layers'
-      for (const void* p : {static_cast<const void*>(a[l].k_codes), static_cast<const void*>(a[l].v_codes)}) {
-        uint32_t h = static_cast<uint32_t>((reinterpret_cast<uintptr_t>(p) >> 4) * 0x9E3779B97F4A7C15ull >> 55);
-        for (; seen[h] != nullptr; h = (h + 1) % kSlots)
-          if (seen[h] == p) return false;
+    for (int l = l0; l < n; ++l)  // 64 layers into the table, the later ones against it
+      for (const void* p : get(a[l])) {
+        const uint32_t h = find(p);
+        if (seen[h] != nullptr) return false;
+        if (l < l1) seen[h] = p;
       }
   }
   return true;
+}
+template <class A>
+bool mx_caches_distinct(const A* a, int n) {
+  return mx_distinct<4>(a, n, [](const A& x) { return std::array<const void*, 4>{x.k_codes, x.v_codes, x.k_scales, x.v_scales}; });
 }
 
 int run_mx_rows(const ea_mxfp4_rows* a, int n_layers, int row0, int n_rows, int Smax, int dtype,
@@ -1161,7 +1164,9 @@ int run_mx_rows(const ea_mxfp4_rows* a, int n_layers, int row0, int n_rows, int 
     const int rc = validate_mx_cache(a[l].k_codes, a[l].k_scales, a[l].v_codes, a[l].v_scales);
     if (rc != EA_OK) return rc;
   }
-  if (write && !mx_caches_distinct(a, n_layers)) return EA_ERR_INVALID_ARG;
+  if (!(write ? mx_caches_distinct(a, n_layers)
+              : mx_distinct<2>(a, n_layers, [](const ea_mxfp4_rows& x) { return std::array<const void*, 2>{x.k, x.v}; })))
+    return EA_ERR_INVALID_ARG;
   int dev;
   DeviceInfo di;
   if (!device_info(&dev, &di)) return EA_ERR_UNSUPPORTED;
@@ -1244,7 +1249,7 @@ void mx_rotations(long long p0, MxPrologueParams* p) {
 template <class A>
 int validate_mx_attn(const A* a, int n_layers, long long p0, int tok, const void* ws) {
   if (a == nullptr || n_layers < 1 || ws == nullptr) return EA_ERR_INVALID_ARG;
-  if (p0 <= -(1LL << 24) || p0 + tok >= (1LL << 24)) return EA_ERR_INVALID_ARG;
+  if (p0 <= -(1LL << 24) || p0 + tok > (1LL << 24)) return EA_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return EA_ERR_MISALIGNED;
   for (int l = 0; l < n_layers; ++l) {
     const A& x = a[l];

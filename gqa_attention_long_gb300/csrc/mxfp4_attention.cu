@@ -221,7 +221,6 @@ struct Ctx {
   __device__ __forceinline__ bool wait3(int b, const Ring3& r, uint32_t err) const { return wait(b + r.b, r.par, err); }
   // tile n's phase of a barrier of three
   __device__ __forceinline__ bool wait3(int b, uint32_t n, uint32_t err) const { return wait(b + n % 3, (n / 3) & 1, err); }
-  __device__ __forceinline__ bool done3(int b, uint32_t n) const { return mbar_test_wait(bar(b + n % 3), (n / 3) & 1); }
 };
 
 // One lane of a warp that has converged, so that what it issues may take operands from the warp's uniform registers.

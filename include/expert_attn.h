@@ -308,8 +308,8 @@ int text_decode_attention(const ea_decode_args* layers, int n_layers, int pos, i
  * code * 2^(scale - 127). The functions below write rows into such caches, read them back and
  * attend over them. A scale byte of 255 stands for NaN: none of the library's writers stores one,
  * and an attention that meets one in a row it reads gives undefined output.
- * Asynchrony, ownership and errors are those of the functions above. The caches that one call
- * writes must be distinct (else EA_ERR_INVALID_ARG). */
+ * Asynchrony, ownership and errors are those of the functions above. What one call writes must not
+ * overlap: a cache's codes or scales (or, of the reader, rows) that stand twice are EA_ERR_INVALID_ARG. */
 
 /* The type of rows outside the cache. */
 typedef enum { EA_ROWS_BF16 = 0, EA_ROWS_FP16 = 1, EA_ROWS_FP32 = 2 } ea_rows_dtype;
@@ -336,7 +336,8 @@ int expert_attn_write_mxfp4(const ea_mxfp4_rows* layers, int n_layers, int row0,
 
 /* The reverse: k and v receive the values of cache rows [row0, row0 + n_rows), exactly in bf16 and fp32
  * (up to overflow to infinity above the type's range), rounded to nearest in fp16. The caches are not
- * written. The rows of k and v must not overlap (else EA_ERR_INVALID_ARG); the rest as above. */
+ * written. The rows of k, and of v, must not overlap: either head_stride >= (n_rows - 1) row_stride + 128 or
+ * row_stride >= 7 head_stride + 128, and both at least 128 (else EA_ERR_INVALID_ARG); the rest as above. */
 int expert_attn_read_mxfp4(const ea_mxfp4_rows* layers, int n_layers, int row0, int n_rows, int Smax, int dtype,
                            int64_t head_stride, int64_t row_stride, ea_stream_t stream);
 
@@ -362,8 +363,8 @@ typedef struct {
 } ea_decode_mxfp4_args;
 
 /* Bytes of workspace for a call over n_layers layers on the current device (0 without a suitable one):
- * 256-byte aligned, cleared once with text_decode_workspace_init, not shared by calls that overlap;
- * expert_attn_read_status reads its status word. */
+ * 256-byte aligned, cleared once with text_decode_workspace_init, used by this function alone and not
+ * by calls that overlap; expert_attn_read_status reads its status word. */
 size_t text_decode_mxfp4_workspace_size(int n_layers);
 int text_decode_attention_mxfp4(const ea_decode_mxfp4_args* layers, int n_layers, int pos, int Smax, int rope_delta,
                                 void* workspace, size_t ws_bytes, ea_stream_t stream);
@@ -373,7 +374,7 @@ int text_decode_attention_mxfp4(const ea_decode_mxfp4_args* layers, int n_layers
  * [0, S) and of the own rows. Rows [S, Smax-64) are never used and stay as they are. q_raw bf16
  * [16][64][128], k_raw and v_raw bf16 [8][64][128], out bf16 [16][64][128]; k_new and v_new, if not NULL,
  * bf16 [8][64][128], receive the own rows' stored values. 0 <= S <= Smax-64, Smax a multiple of 64,
- * 128 <= Smax <= 2^22; |S + rope_delta| + 64 < 2^24. */
+ * 128 <= Smax <= 2^22; -2^24 < S + rope_delta <= 2^24 - 64. */
 typedef struct {
   const void* q_raw;
   const void* k_raw;
