@@ -150,6 +150,9 @@ constexpr uint32_t kSmemBytes = SM_ABORT + 4 + 1024;  // + slack to align the ba
 static_assert(kSmemBytes <= 232448 && SM_RING % 128 == 0 && SM_X % 16 == 0 && SM_BAR % 8 == 0, "shared memory of one sm_103 CTA");
 constexpr uint32_t TM_S = 0, TM_O = 384, kTmemCols = 512;  // three score (then P) buffers, the accumulator
 constexpr int kRefField = 23, kMaxField = 26;  // f16 exponent field of 2^(e - R + 8), and its cut (all-zero blocks)
+// A row's weights are 2^(s - m) with m set kLift below a maximum, so that f16 holds those down to 2^-32 of the largest
+// (2^-24 of it would lose a key's weight where half a million of them still count).
+constexpr float kLift = 8.f;
 constexpr uint32_t kBarSoftmax = 1;
 
 template <int N>
@@ -596,7 +599,7 @@ __device__ __forceinline__ void softmax_warps(const MxExpertParams& p, const Ctx
       }
       const float2 ct2 = make_float2(ct, ct);
       // P goes over the scores' first columns: chunk c's 16 columns of pairs hold scores of chunks <= c.
-      // The maximum is not looked for: a chunk's sum that passes 2^13 tells that it has to rise (f16 holds
+      // The maximum is not looked for: a chunk's sum that passes 2^15 tells that it has to rise (f16 holds
       // weights up to 2^16), and then, as in the segment's first chunk, the chunk is done once more.
       float tsum = 0.f;
       bool first = __any_sync(0xffffffffu, m == -INFINITY);
@@ -617,7 +620,7 @@ __device__ __forceinline__ void softmax_warps(const MxExpertParams& p, const Ctx
 #pragma unroll
             for (int e = 0; e < 32; e += 2)
               mx[(e >> 1) & 3] = fmax3(mx[(e >> 1) & 3], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-            const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * ct), a = ex2_approx(m - mn);
+            const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * ct - kLift), a = ex2_approx(m - mn);
             if (c > 0) scale_p(sa, a, c);  // the earlier chunks' P moves too
             tsum *= a;
             lsum *= a;
@@ -634,7 +637,7 @@ __device__ __forceinline__ void softmax_warps(const MxExpertParams& p, const Ctx
           }
           const float2 tt = __fadd2_rn(ts[0], ts[1]);
           cs = tt.x + tt.y;
-          if (!again || !__any_sync(0xffffffffu, cs > 8192.f)) break;
+          if (!again || !__any_sync(0xffffffffu, cs > 32768.f)) break;
           rise = true;
           again = false;
         }

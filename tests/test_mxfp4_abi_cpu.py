@@ -101,3 +101,30 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
     for f in (ea.make_rows_args, ea.make_decode_mxfp4_args, ea.make_mxfp4_args):
         with pytest.raises(ValueError):
             f([], 64)
+
+
+def test_scales_twice_are_refused(h):
+    ws = ctypes.c_void_p(0x100000)
+    for n, over in ((1, dict(k_scales=0x900000, v_scales=0x900000)), (2, dict(k_scales=0x900000)), (70, dict(v_scales=0x90000000))):
+        assert rows(h, fake(_lib.EaMxfp4Rows, n, **over), n=n) == INV
+        a = fake(_lib.EaAttnMxfp4Args, n, **over)
+        assert h.text_decode_attention_mxfp4(a, n, 10, 128, 0, ws, 1 << 40, None) == INV
+        assert h.expert_attn_layers_mxfp4(a, n, 10, 128, 0, ws, 1 << 40, None) == INV
+    a = fake(_lib.EaAttnMxfp4Args, 70)
+    assert h.text_decode_attention_mxfp4(a, 70, 10, 128, 0, ws, 1 << 40, None) not in (INV, MIS)
+
+
+def test_rows_read_into_one_place_twice_are_refused(h):
+    for n, over in ((1, dict(k=0x900000, v=0x900000)), (2, dict(k=0x900000)), (66, dict(v=0x90000000))):
+        assert rows(h, fake(_lib.EaMxfp4Rows, n, **over), n=n, read=True) == INV
+        assert rows(h, fake(_lib.EaMxfp4Rows, n, **over), n=n) not in (INV, MIS)  # a source may
+    one = fake(_lib.EaMxfp4Rows, 2, k_codes=0x900000, k_scales=0xA00000)
+    assert rows(h, one, n=2, read=True) not in (INV, MIS)  # as may a cache that is read
+
+
+@pytest.mark.parametrize("fn,tok", [("text_decode_attention_mxfp4", 1), ("expert_attn_layers_mxfp4", 64)])
+def test_positions_up_to_the_documented_ends(h, fn, tok):
+    call = lambda p0: getattr(h, fn)(fake(_lib.EaAttnMxfp4Args), 1, 10, 128, p0 - 10, ctypes.c_void_p(0x100000), 1 << 40, None)  # noqa: E731
+    last, first = (1 << 24) - tok, 1 - (1 << 24)
+    assert call(last) not in (INV, MIS) and call(first) not in (INV, MIS)
+    assert call(last + 1) == INV and call(first - 1) == INV
