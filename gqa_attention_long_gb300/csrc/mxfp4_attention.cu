@@ -26,6 +26,14 @@
 // with the maximum that it last knew (raised when a chunk's weights pass it by far) and compares notes with
 // tile n - 1's at the end, through shared memory: only where the two differ is P(n), or the accumulator, scaled.
 //
+// Measured: 64 layers at S = 4700 163 us (of these the prologue 15, the merge 2), 2 layers at S = 65537 68 us,
+// 1 layer at S = 4700 17.4 us, at S = 256 12.3 us. A tile takes about 1,900 cycles, of which its MMAs are 1,025 (tensor pipe
+// 48 % busy). No unit is full: a converter spends 1,100 cycles on a row and as many on its waits and hand-overs, a
+// softmax warpgroup 2,700 on a tile, of which three are in flight, and together they take 61 % of the issue slots.
+// Tried and slower: tiles of 96 keys with four score buffers (183 us: a tile's fixed costs), two warpgroups to a
+// converter (183), two for the softmax (175), waits that spin (174), scores fetched a chunk ahead (181). One
+// layer is a chain: prologue 3.8 us, load and reference 2.3, two tiles 3.4, epilogue 1.5, merge 3.3.
+//
 // The instruction cache held earlier forms back: with the roles' loops unrolled, 68 % of the peak of
 // instruction fetches went to the second level and every role crawled (3,600 cycles a tile). So the
 // loops are small, K and V share their code, and what is rare is out of line.
@@ -38,7 +46,8 @@ namespace ea {
 // ------------------------------------------------------------------------------- prologue
 // One octet of threads per token and kv head: the token's two q rows, its k row and its v row, whose angles are formed
 // once (three CTAs to an SM); or, when there are too few of them to fill the GPU (kSplit), one of the four
-// rows. grid (2 or 8, kv heads, layers).
+// rows (at S = 300, four rows and one: 1 layer 14.9 and 13.4 us, 4 layers 14.8 and 14.7, 8 layers 16.4 and 17.5). grid (2
+// or 8, kv heads, layers).
 template <bool kSplit>
 __global__ void __launch_bounds__(256, kSplit ? 1 : 3) mxfp4_prologue_kernel(const __grid_constant__ MxPrologueParams p) {
   const int g = blockIdx.y, l = blockIdx.z, i = threadIdx.x & 7;
@@ -120,8 +129,8 @@ __global__ void __launch_bounds__(256, kSplit ? 1 : 3) mxfp4_prologue_kernel(con
 
 namespace mxa {
 
-constexpr int kSoftWg = 3, kConvWg = 1;  // warpgroups: softmax; converters of K, and of V
-constexpr int kSoftmax = 128 * kSoftWg, kConvert = 128 * kConvWg;
+constexpr int kSoftWg = 3, kSoftmax = 128 * kSoftWg;  // softmax warpgroups, and their threads
+constexpr int kConvert = 128;                         // threads of K's converters, and of V's
 constexpr int kThreads = kSoftmax + 2 * kConvert + 128;
 // registers per thread after the roles part (launched with kRegLaunch): the sum is the launch's at most
 constexpr int kRegLaunch = 65536 / kThreads / 8 * 8;
@@ -133,7 +142,7 @@ constexpr uint32_t kStageBytes = kCodes + kScales;          // a tile's codes an
 constexpr uint32_t kAtom = 16384, kTile = 2 * kAtom;        // an f16 tile: two 64-channel halves
 constexpr uint32_t SM_Q = 0, SM_K = SM_Q + kTile, SM_V = SM_K + 2 * kTile, SM_RING = SM_V + 2 * kTile;
 constexpr uint32_t SM_X = SM_RING + 2 * kRing * kStageBytes;   // [segment parity][warpgroup][row] (m, l)
-constexpr uint32_t SM_M = SM_X + 2 * kSoftWg * kRows * 8;             // [row] running maximum (log2 units)
+constexpr uint32_t SM_M = SM_X + 2 * kSoftWg * kRows * 8;      // [row] running maximum (log2 units)
 constexpr uint32_t SM_REF = SM_M + kRows * 4;               // [K, V][8]: R of tile n % 8
 constexpr uint32_t SM_BAR = SM_REF + 16 * 4;
 // by tile n % 3: FULL and EMPTY (K's ring, V's ring), SFULL, MDONE, PFULL, ODONE; by n % 2: RDY (K's f16 tiles,
@@ -343,20 +352,18 @@ __device__ __forceinline__ void producer(const MxExpertParams& p, const Ctx cx) 
 }
 
 // ----------------------------------------------------------------------------- converters
-// kConvWg warpgroups each for K (kv = 0) and V (kv = 1): thread = row of a packed tile (half of it, with two
-// warpgroups), whose codes it writes as f16 into a tile of the swizzled layout: block b's codes times 2^(scale - ref + 8), 0 for a dead row. A lane takes its row's
+// One warpgroup each for K (kv = 0) and V (kv = 1): thread = row of a packed tile, whose codes it writes as f16 into a
+// tile of the swizzled layout: block b's codes times 2^(scale - ref + 8), 0 for a dead row. A lane takes its row's
 // blocks in an order that spreads the lanes over the banks; what follows from that order is formed once, so that a
 // block costs 36 instructions for its codes and 7 more.
 __device__ __forceinline__ void converter(const MxExpertParams& p, const Ctx cx, int kv) {
   const int row = threadIdx.x & 127;
   const int empty = B_EMPTY + kRing * kv, used = kv ? B_ODONE : B_SFULL, rdy = B_RDY + 2 * kv;
   const volatile int* refs = reinterpret_cast<const volatile int*>(cx.smem + SM_REF) + 8 * kv;
-  constexpr int kBlocks = 4 / kConvWg;  // of a row's four, for this thread
-  const int first = (threadIdx.x - kSoftmax - kv * kConvert) / 128 * kBlocks;
-  uint32_t from[kBlocks], to[kBlocks], sel[kBlocks];  // the i-th block's place in the ring's first slot, in the first tile; its factor's selector
+  uint32_t from[4], to[4], sel[4];  // the i-th block's place in the ring's first slot, in the first tile; its factor's selector
 #pragma unroll
-  for (int i = 0; i < kBlocks; ++i) {
-    const int b = (first + i + (row >> 1)) & 3;
+  for (int i = 0; i < 4; ++i) {
+    const int b = (i + (row >> 1)) & 3;
     from[i] = cx.sbase + SM_RING + kv * kRing * kStageBytes + row * kMxRowBytes + 16 * b;
     // word k of the block is chunk 4 (b % 2) + k of half b / 2; chunk c of a row sits at c ^ (row % 8)
     to[i] = cx.sbase + (kv ? SM_V : SM_K) + (b >> 1) * kAtom + row * 128 + (((4 * (b & 1)) ^ (row & 7)) << 4);
@@ -380,14 +387,14 @@ __device__ __forceinline__ void converter(const MxExpertParams& p, const Ctx cx,
       const uint32_t cut = row < tile_live(p, j) ? kMaxField * 0x10001u : 0u;
       const uint32_t f02 = __viaddmin_s16x2_relu(sc & 0x00FF00FFu, add, cut) << 10;         // blocks 0 and 2
       const uint32_t f13 = __viaddmin_s16x2_relu((sc >> 8) & 0x00FF00FFu, add, cut) << 10;  // blocks 1 and 3
-      uint4 blk[kBlocks];
+      uint4 blk[4];
 #pragma unroll
-      for (int i = 0; i < kBlocks; ++i) blk[i] = ld_shared_v4(from[i] + slot);
+      for (int i = 0; i < 4; ++i) blk[i] = ld_shared_v4(from[i] + slot);
       // the f16 buffer held tile n - 2: K's is free once QK(n-2) is done, V's once PV(n-2) is
       ok = n < 2 || cx.wait3(used, r.back(2), kErrProducerWait);
       if (!ok) break;
 #pragma unroll
-      for (int i = 0; i < kBlocks; ++i) {
+      for (int i = 0; i < 4; ++i) {
         const uint4 c = blk[i];
         const uint32_t f = __byte_perm(f02, f13, sel[i]);
         const uint32_t w[4] = {c.x, c.y, c.z, c.w};
