@@ -1300,6 +1300,7 @@ int run_mx_decode(const ea_decode_mxfp4_args* a, int n_layers, int pos, int Smax
   p.part_o = reinterpret_cast<float*>(ws + wl.part_o_off);
   p.part_lse = reinterpret_cast<float*>(ws + wl.part_ml_off);
   p.unit_cnt = reinterpret_cast<uint32_t*>(ws + wl.cnt_off);
+  p.status = reinterpret_cast<uint32_t*>(ws);
   p.T = static_cast<uint32_t>(pos / kMxDecodeKeys + 1);
   p.pos = pos;
   p.Smax = Smax;

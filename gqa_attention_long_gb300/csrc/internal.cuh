@@ -270,6 +270,7 @@ struct MxDecodeParams {
   float* part_o;        // [n_ctas][2 slots][8 heads][128]: a part's normalised output
   float* part_lse;      // [n_ctas][2 slots][8 heads]: its log2-sum-exp
   uint32_t* unit_cnt;   // [unit]: parts that have written their partial (zero between calls)
+  uint32_t* status;
   uint32_t T;           // chunks of 32 keys per unit: pos / 32 + 1
   uint32_t parts;       // > 0: CTAs per unit, each with its share of the unit's chunks
   uint32_t per_cta, extra;  // else: CTA c owns per_cta chunks, one more for c < extra

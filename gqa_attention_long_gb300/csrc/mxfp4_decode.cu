@@ -25,15 +25,16 @@
 // 4 (P <= 2^4), so that both rescalings are rare.
 //
 // Work decomposition: the units' keys in chunks of 32, unit-major, one contiguous range per CTA; a CTA's
-// twelve compute warps take its chunks in turn (64 layers at pos 4700: 79 us with eight). At the end of a
-// unit the warps' partials meet in shared memory; a unit cut over several CTAs is merged by the part that
-// finishes last. Four further warps prepare the next unit's q rows and encode the new rows.
+// twelve compute warps take its chunks in turn (64 layers at pos 4700: 79 us with eight). Where a unit ends a
+// warp leaves its partial in shared memory and goes on with the next: four further warps join the
+// partials, after they have prepared the next units' q rows and encoded the new rows. (When all warps met at a
+// unit's end, each lost up to a chunk's time there: 64 layers 72.7 us, now 65.7.) A unit cut over several CTAs
+// is merged by the part that finishes last.
 //
-// Measured: 64 layers at pos 4700 72.7 us (4.5 TB/s, 67 % of a plain copy), 4 layers at pos 131070 103 us (5.5 TB/s,
-// 82 %); 1 layer at pos 4700 8.9 us, at pos 300 5.3 us. What holds it below the copy: the conversions share the ALU
-// pipe (57 % busy) and the issue slots (50 %) with the softmax, and a unit's end (12 partials met behind two
-// barriers) stops the loads' consumers about every 12 chunks of a warp; at one layer the latencies of the launch,
-// one chunk's load, the parts' arrival and the merge.
+// Measured: 64 layers at pos 4700 65.7 us (5.0 TB/s, 74 % of a plain copy), 4 layers at pos 131070 104.5 us (5.5 TB/s,
+// 81 %); 1 layer at pos 4700 9.1 us, at pos 300 5.3 us. What holds it below the copy: the conversions share the ALU
+// pipe (57 % busy) and the issue slots (50 %) with the softmax; at one layer the latencies of the launch, one
+// chunk's load, the parts' arrival and the merge.
 #include "mxfp4.cuh"
 #include "rope.cuh"
 
@@ -59,11 +60,15 @@ constexpr uint32_t SM_Q = (SM_R + kWarps * 4 + 15) & ~15u;              // 2 x [
 constexpr uint32_t SM_QF = SM_Q + 2 * kRepText * kD * 2;                // 2 x [8 heads] score factor
 constexpr uint32_t kNewBytes = 2 * kMxRowBytes + 8;
 constexpr uint32_t SM_NEW = SM_QF + 2 * kRepText * 4;                   // 2 x (K codes, V codes, scale words)
-constexpr uint32_t SM_FLAG = SM_NEW + 2 * 144;
-constexpr uint32_t kSmemBytes = SM_FLAG + 16;
+constexpr uint32_t SM_FLAG = SM_NEW + 2 * 144, SM_ABORT = SM_FLAG + 4;
+constexpr uint32_t SM_BAR = SM_FLAG + 16;
+// by segment: a unit's q (and new rows) are there (in the buffer of its parity); its partials are; they are read
+constexpr uint32_t B_QRDY = 0, B_PART = 2, B_READ = 3, kNumBars = 4;
+constexpr uint32_t kSmemBytes = SM_BAR + 8 * kNumBars;
+constexpr uint32_t kBarPrep = 1, kBarLast = 2, kBarEnd = 3;  // named barriers: the preparing warps; with four compute warps, at the end
 static_assert(kNewBytes <= 144 && kSmemBytes <= 232448, "shared memory budget of one sm_103 CTA");
 static_assert(kStageBytes % 128 == 0 && SM_FACT % 16 == 0 && SM_PART % 16 == 0 && SM_ML % 8 == 0 && SM_Q % 16 == 0 &&
-                  SM_QF % 8 == 0 && SM_NEW % 16 == 0,
+                  SM_QF % 8 == 0 && SM_NEW % 16 == 0 && SM_BAR % 8 == 0,
               "alignment of the vector accesses");
 
 // P 2^(ev - R): a block at the reference has factor 2^8 (f16 exponent field 23); fields above 26 only
@@ -406,6 +411,94 @@ __device__ __forceinline__ void chunk(Warp& w, const uint32_t (&q)[4][4], const 
   }
 }
 
+// ------------------------------------------------------------------------------- a unit's end
+// The warps' partials of unit u (in units of 2^(M + Rmax - 8)) joined by nw warps, this one the w-th: a warp per head,
+// lane = channels [4 c, 4 c + 4). whole: the unit is this CTA's alone; else it is a part, and the part that comes last
+// merges them all. The nw warps come here together.
+__device__ __forceinline__ void join(const MxDecodeParams& p, uint8_t* smem, uint32_t u, uint32_t seg, bool whole, int w, int nw) {
+  const int c = threadIdx.x & 31, l = u / kHkv, g = u % kHkv;
+  const float2* ml = reinterpret_cast<const float2*>(smem + SM_ML);
+  const int* rf = reinterpret_cast<const int*>(smem + SM_R);
+  __nv_bfloat16* out = p.layer[l].out + static_cast<size_t>(g) * kRepText * kD + 4 * c;
+  // slot 2 c + 1 if this CTA came to the unit from an earlier one, else 2 c
+  const size_t ps = static_cast<size_t>(blockIdx.x) * 2 + (seg == 0 ? 0 : 1);
+#pragma unroll 1
+  for (int h = w; h < kRepText; h += nw) {
+    float M = -INFINITY, Lsum = 0.f;
+    int R = 0;
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) {
+      M = fmaxf(M, ml[k * kRepText + h].x);
+      R = max(R, rf[k]);
+    }
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) {
+      const float2 v = ml[k * kRepText + h];
+      const float a = ex2_approx(v.x - M);  // 0 for a warp without keys
+      Lsum = fmaf(v.y, a, Lsum);
+      const float s = ex2_approx(v.x - M + static_cast<float>(rf[k] - R));
+      const float4 o = *reinterpret_cast<const float4*>(smem + SM_PART + ((k * kRepText + h) * kPartRow + 4 * c) * 4);
+      acc.x = fmaf(s, o.x, acc.x);
+      acc.y = fmaf(s, o.y, acc.y);
+      acc.z = fmaf(s, o.z, acc.z);
+      acc.w = fmaf(s, o.w, acc.w);
+    }
+    // 2^(R - 127 - 8) / L, in two steps: the power alone may leave fp32's range
+    const float inv = 1.0f / Lsum, two_r = mx_scale(R), down = 0.00390625f;
+    acc.x = acc.x * inv * down * two_r;
+    acc.y = acc.y * inv * down * two_r;
+    acc.z = acc.z * inv * down * two_r;
+    acc.w = acc.w * inv * down * two_r;
+    if (whole) {
+      *reinterpret_cast<uint2*>(out + h * kD) = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+    } else {
+      *reinterpret_cast<float4*>(p.part_o + (ps * kRepText + h) * kD + 4 * c) = acc;
+      if (c == 0) p.part_lse[ps * kRepText + h] = M + log2f(Lsum);
+    }
+  }
+  if (whole) return;
+  auto together = [&] {
+    if (nw == kPrep / 32) bar_sync(kBarPrep, kPrep);
+    else bar_sync(kBarLast, 2 * kPrep);
+  };
+  const uint32_t u0 = u * p.T, c0 = cta_of(p, u0), c1 = p.T == 1 ? c0 : cta_of(p, u0 + p.T - 1);
+  volatile uint32_t* flag = reinterpret_cast<volatile uint32_t*>(smem + SM_FLAG);
+  together();
+  if (w == 0 && c == 0) {
+    uint32_t old;
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(old) : "l"(p.unit_cnt + u) : "memory");
+    *flag = old == c1 - c0 ? 1u : 0u;
+  }
+  together();
+  if (*flag == 0u) return;
+  // the last part: merges them all, in their order
+  const uint32_t np = c1 - c0 + 1;
+  const size_t first = static_cast<size_t>(c0) * 2 + (cta_start(p, c0) >= u0 ? 0 : 1);
+  auto slot = [&](uint32_t k) -> size_t { return k == 0 ? first : static_cast<size_t>(c0 + k) * 2; };
+#pragma unroll 1
+  for (int h = w; h < kRepText; h += nw) {
+    // lane k: part k's weight (np <= 32: kMxMaxParts)
+    const float lse = c < np ? __ldcg(p.part_lse + slot(c) * kRepText + h) : -INFINITY;
+    const float wt = ex2_approx(lse - warp_max(lse));
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    float ws = 0.f;
+#pragma unroll 8
+    for (uint32_t k = 0; k < np; ++k) {
+      const float wk = __shfl_sync(0xffffffffu, wt, k);
+      const float4 o = __ldcg(reinterpret_cast<const float4*>(p.part_o + (slot(k) * kRepText + h) * kD + 4 * c));
+      ws += wk;
+      s.x = fmaf(wk, o.x, s.x);
+      s.y = fmaf(wk, o.y, s.y);
+      s.z = fmaf(wk, o.z, s.z);
+      s.w = fmaf(wk, o.w, s.w);
+    }
+    const float iw = 1.0f / ws;
+    *reinterpret_cast<uint2*>(out + h * kD) = make_uint2(pack_bf16x2(s.x * iw, s.y * iw), pack_bf16x2(s.z * iw, s.w * iw));
+  }
+  if (w == 0 && c == 0) p.unit_cnt[u] = 0u;  // every part has arrived: ready for the next call
+}
+
 }  // namespace mxd
 
 __global__ void __launch_bounds__(mxd::kThreads, 1) mxfp4_decode_kernel(const __grid_constant__ MxDecodeParams p) {
@@ -414,39 +507,55 @@ __global__ void __launch_bounds__(mxd::kThreads, 1) mxfp4_decode_kernel(const __
   const uint32_t sbase = smem_u32(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t start = cta_start(p, blockIdx.x), end = cta_start(p, blockIdx.x + 1);
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + SM_ABORT);
+  auto bar = [&](uint32_t b) { return sbase + SM_BAR + 8 * b; };
+  if (tid == 0) {
+    mbar_init(bar(B_QRDY), kPrep / 32);
+    mbar_init(bar(B_QRDY + 1), kPrep / 32);
+    mbar_init(bar(B_PART), kWarps);
+    mbar_init(bar(B_READ), kPrep / 32);
+    *abort_flag = 0u;
+    fence_mbar_init();
+  }
   pdl_wait_primary();
-  // a warp's chunks are start + warp + kWarps i; chunk i sits in slot i % kStages of its ring
-  const uint32_t ring = sbase + SM_RING + warp * kStages * kStageBytes, fact = sbase + SM_FACT + warp * kFactorBytes;
-  const uint32_t loff = 64 * (lane >> 2) + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
-  uint32_t f = start + warp, fl = f, slot = 0, lslot = 0;  // next chunk to use and to load, and their slots' offsets
-  Cursor cur;
-  auto load = [&] {
-    if (fl < end) {
-      load_chunk(p, cur, ring + lslot, loff, lane);
-      fl += kWarps;
-      if (fl < end) cursor_next(p, cur, lane);
-    }
-    cp_commit();
-    lslot = lslot + kStageBytes == kStages * kStageBytes ? 0 : lslot + kStageBytes;
+  auto wait = [&](uint32_t b, uint32_t parity) -> bool {
+    return __all_sync(0xffffffffu, bounded_wait(bar(b), parity, abort_flag, p.status, kErrDecodeWait));
   };
+  auto arrive = [&](uint32_t b) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(b));
+  };
+  // The CTA's segments: what its range holds of unit u1 + seg's chunks [u0, u0 + T).
+  const uint32_t u1 = start / p.T;
+  int seg = 0;
+  bool ok = true;
   if (warp < kWarps) {
+    // a warp's chunks are start + warp + kWarps i; chunk i sits in slot i % kStages of its ring
+    const uint32_t ring = sbase + SM_RING + warp * kStages * kStageBytes, fact = sbase + SM_FACT + warp * kFactorBytes;
+    const uint32_t loff = 64 * (lane >> 2) + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
+    uint32_t f = start + warp, fl = f, slot = 0, lslot = 0;  // next chunk to use and to load, and their slots' offsets
+    Cursor cur;
+    auto load = [&] {
+      if (fl < end) {
+        load_chunk(p, cur, ring + lslot, loff, lane);
+        fl += kWarps;
+        if (fl < end) cursor_next(p, cur, lane);
+      }
+      cp_commit();
+      lslot = lslot + kStageBytes == kStages * kStageBytes ? 0 : lslot + kStageBytes;
+    };
     cur.u = f / p.T;
     cur.j = f - cur.u * p.T;
     if (f < end) cursor_unit(p, cur, lane);
 #pragma unroll 1
     for (int s = 0; s < kStages - 1; ++s) load();
-  }
-  int seg = 0;
-  for (uint32_t f0 = start; f0 < end; ++seg) {
-    const uint32_t u = f0 / p.T, u0 = u * p.T, f1 = min(end, u0 + p.T);
-    const int buf = seg & 1;
-    const bool last = f1 == u0 + p.T;
-    if (warp >= kWarps && seg == 0) prepare(p, smem, u, last, 0, tid - kCompute);
-    __syncthreads();  // this unit's q (and new row) are ready, the last unit's partials are read
-    if (warp >= kWarps) {
-      if (f1 < end) prepare(p, smem, u + 1, end >= f1 + p.T, buf ^ 1, tid - kCompute);
-      else pdl_launch_dependents();
-    } else {
+    __syncthreads();  // the first unit's q is ready, and the barriers are
+#pragma unroll 1
+    for (;; ++seg) {
+      const uint32_t u0 = (u1 + seg) * p.T, f1 = min(end, u0 + p.T);
+      const int buf = seg & 1;
+      if (seg > 0) ok = wait(B_QRDY + buf, ((seg - 1) >> 1) & 1);
+      if (!ok) break;
       uint32_t q[4][4];
       float qf[2];
 #pragma unroll
@@ -492,6 +601,8 @@ __global__ void __launch_bounds__(mxd::kThreads, 1) mxfp4_decode_kernel(const __
         w.l[0] += __shfl_xor_sync(0xffffffffu, w.l[0], m);
         w.l[1] += __shfl_xor_sync(0xffffffffu, w.l[1], m);
       }
+      if (seg > 0) ok = wait(B_READ, (seg - 1) & 1);  // the segment before's partials are read
+      if (!ok) break;
       float* part = reinterpret_cast<float*>(smem + SM_PART) + warp * kRepText * kPartRow;
       const int g = lane >> 2, t = lane & 3;
 #pragma unroll
@@ -505,83 +616,37 @@ __global__ void __launch_bounds__(mxd::kThreads, 1) mxfp4_decode_kernel(const __
         ml[2 * t + g] = g ? make_float2(w.m[1], w.l[1]) : make_float2(w.m[0], w.l[0]);
       }
       if (lane == 0) reinterpret_cast<int*>(smem + SM_R)[warp] = w.ref;
+      if (f1 == end) break;
+      arrive(B_PART);
     }
-    __syncthreads();
-    if (warp < kRepText) {
-      // thread = head h, channels [4 c, 4 c + 4): the warps' partials in units of 2^(M + Rmax - 8)
-      const int h = tid >> 5, c = tid & 31;
-      const float2* ml = reinterpret_cast<const float2*>(smem + SM_ML);
-      const int* rf = reinterpret_cast<const int*>(smem + SM_R);
-      float M = -INFINITY, Lsum = 0.f;
-      int R = 0;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        M = fmaxf(M, ml[w * kRepText + h].x);
-        R = max(R, rf[w]);
+    cp_wait<0>();
+    ok = bar_sync_and(kBarEnd, kThreads, ok);
+    if (!ok || warp >= kPrep / 32) return;
+  }
+  // The preparing warps: unit 0, unit 1, then, segment by segment, the end of its unit and the unit after the next. At
+  // the last segment four compute warps join half of the heads (from here on, too: one copy of the code).
+  const bool prep = warp >= kWarps;
+#pragma unroll 1
+  for (int s = prep ? -2 : seg;; ++s) {
+    const uint32_t us = u1 + s, un = us + 2;
+    if (s >= 0) {
+      const uint32_t u0 = us * p.T, f1 = min(end, u0 + p.T);
+      const bool fin = f1 == end;
+      if (prep) {
+        if (fin) pdl_launch_dependents();
+        else ok = bar_sync_and(kBarPrep, kPrep, wait(B_PART, s & 1));
+        if (fin || !ok) ok = bar_sync_and(kBarEnd, kThreads, ok);  // (the compute warps come there in any case)
+        if (!ok) break;
       }
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float2 v = ml[w * kRepText + h];
-        const float a = ex2_approx(v.x - M);  // 0 for a warp without keys
-        Lsum = fmaf(v.y, a, Lsum);
-        const float s = ex2_approx(v.x - M + static_cast<float>(rf[w] - R));
-        const float4 o = *reinterpret_cast<const float4*>(smem + SM_PART + ((w * kRepText + h) * kPartRow + 4 * c) * 4);
-        acc.x = fmaf(s, o.x, acc.x);
-        acc.y = fmaf(s, o.y, acc.y);
-        acc.z = fmaf(s, o.z, acc.z);
-        acc.w = fmaf(s, o.w, acc.w);
-      }
-      // 2^(R - 127 - 8) / L, in two steps: the power alone may leave fp32's range
-      const float inv = 1.0f / Lsum, two_r = mx_scale(R), down = 0.00390625f;
-      acc.x = acc.x * inv * down * two_r;
-      acc.y = acc.y * inv * down * two_r;
-      acc.z = acc.z * inv * down * two_r;
-      acc.w = acc.w * inv * down * two_r;
-      const int l = u / kHkv, g = u % kHkv;
-      __nv_bfloat16* out = p.layer[l].out + (static_cast<size_t>(g) * kRepText + h) * kD + 4 * c;
-      if (f0 == u0 && last) {
-        *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
-      } else {
-        // a part of the unit: slot 2 c + 1 if this CTA came to it from an earlier unit, else 2 c
-        const size_t ps = static_cast<size_t>(blockIdx.x) * 2 + (f0 == start ? 0 : 1);
-        *reinterpret_cast<float4*>(p.part_o + (ps * kRepText + h) * kD + 4 * c) = acc;
-        if (c == 0) p.part_lse[ps * kRepText + h] = M + log2f(Lsum);
-        const uint32_t c0 = cta_of(p, u0), c1 = p.T == 1 ? c0 : cta_of(p, u0 + p.T - 1);
-        uint32_t* flag = reinterpret_cast<uint32_t*>(smem + SM_FLAG);
-        bar_sync(1, kRepText * 32);
-        if (tid == 0) {
-          uint32_t old;
-          asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(old) : "l"(p.unit_cnt + u) : "memory");
-          *flag = old == c1 - c0 ? 1u : 0u;
-        }
-        bar_sync(1, kRepText * 32);
-        if (*flag != 0u) {  // the last part: merges them all, in their order
-          const uint32_t np = c1 - c0 + 1;
-          const size_t first = static_cast<size_t>(c0) * 2 + (cta_start(p, c0) >= u0 ? 0 : 1);
-          auto slot = [&](uint32_t k) -> size_t { return k == 0 ? first : static_cast<size_t>(c0 + k) * 2; };
-          // lane k of head h's warp: part k's weight (np <= 32: kMxMaxParts)
-          const float lse = c < np ? __ldcg(p.part_lse + slot(c) * kRepText + h) : -INFINITY;
-          const float wt = ex2_approx(lse - warp_max(lse));
-          float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-          float ws = 0.f;
-#pragma unroll 8
-          for (uint32_t k = 0; k < np; ++k) {
-            const float wk = __shfl_sync(0xffffffffu, wt, k);
-            const float4 o = __ldcg(reinterpret_cast<const float4*>(p.part_o + (slot(k) * kRepText + h) * kD + 4 * c));
-            ws += wk;
-            s.x = fmaf(wk, o.x, s.x);
-            s.y = fmaf(wk, o.y, s.y);
-            s.z = fmaf(wk, o.z, s.z);
-            s.w = fmaf(wk, o.w, s.w);
-          }
-          const float iw = 1.0f / ws;
-          *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(s.x * iw, s.y * iw), pack_bf16x2(s.z * iw, s.w * iw));
-          if (tid == 0) p.unit_cnt[u] = 0u;  // every part has arrived: ready for the next call
-        }
-      }
+      join(p, smem, us, s, start <= u0 && f1 == u0 + p.T, prep ? warp - kWarps : kPrep / 32 + warp, fin ? kPrep / 16 : kPrep / 32);
+      if (fin) break;
+      arrive(B_READ);
     }
-    f0 = f1;
+    if (un * p.T < end) {
+      prepare(p, smem, un, end >= (un + 1) * p.T, s & 1, tid - kCompute);
+      if (s > -2) arrive(B_QRDY + (s & 1));
+    }
+    if (s == -2) __syncthreads();
   }
 }
 
