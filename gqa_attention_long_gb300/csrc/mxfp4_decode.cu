@@ -31,8 +31,8 @@
 // unit's end, each lost up to a chunk's time there: 64 layers 72.7 us, now 65.7.) A unit cut over several CTAs
 // is merged by the part that finishes last.
 //
-// Measured: 64 layers at pos 4700 65.7 us (5.0 TB/s, 74 % of a plain copy), 4 layers at pos 131070 104.5 us (5.5 TB/s,
-// 81 %); 1 layer at pos 4700 9.1 us, at pos 300 5.3 us. What holds it below the copy: the conversions share the ALU
+// Measured: 64 layers at pos 4700 63.7 us (5.2 TB/s, 76 % of a plain copy), 4 layers at pos 131070 98.3 us (5.8 TB/s,
+// 86 %); 1 layer at pos 4700 9.2 us, at pos 300 5.4 us. What holds it below the copy: the conversions share the ALU
 // pipe (57 % busy) and the issue slots (50 %) with the softmax; at one layer the latencies of the launch, one
 // chunk's load, the parts' arrival and the merge.
 #include "mxfp4.cuh"
@@ -318,38 +318,32 @@ __device__ __forceinline__ void raise_ref(Warp& w, uint32_t st, int lane) {
 __device__ __forceinline__ void chunk(Warp& w, const uint32_t (&q)[4][4], const float (&qf)[2], uint32_t st, uint32_t fact,
                                       int live, int lane) {
   const int g = lane >> 2, t = lane & 3;
-  // The scales become factors once per key (lane = key), not once per thread that needs them:
-  // K's four as fp32, at fact + 16 key; V's four as f16 2^(ev - R + 8), the pair of keys 2i and 2i + 1 of
-  // block b at fact + 512 + 16 i + 4 b.
-  {
-    const uint32_t ks = ld_shared_u32(st + 2 * kCodes + 4 * lane), vs = ld_shared_u32(st + 2 * kCodes + kScales + 4 * lane);
-    // (a K scale byte of 0, 2^-127, is taken as 0: such a block adds nothing to a score)
-    st_shared_v4(fact + 16 * lane, (ks << 23) & 0x7F800000u, (ks << 15) & 0x7F800000u, (ks << 7) & 0x7F800000u,
-                 (ks >> 1) & 0x7F800000u);
-    const uint32_t v02 = vs & 0x00FF00FFu, v13 = (vs >> 8) & 0x00FF00FFu, top = __vmaxu2(v02, v13);
-    if (__any_sync(0xffffffffu, static_cast<int>(max(top & 0xFFFFu, top >> 16)) > w.ref + (kMaxField - kRefField)))
-      raise_ref(w, st, lane);
-    const uint32_t add = static_cast<uint32_t>((kRefField - w.ref) & 0xFFFF) * 0x10001u;
-    const uint32_t f02 = __viaddmin_s16x2_relu(v02, add, kMaxField * 0x10001u) << 10;
-    const uint32_t f13 = __viaddmin_s16x2_relu(v13, add, kMaxField * 0x10001u) << 10;
-    const uint32_t a = fact + 512 + 16 * (lane >> 1) + 2 * (lane & 1);
-    st_shared_u16(a, static_cast<uint16_t>(f02));
-    st_shared_u16(a + 4, static_cast<uint16_t>(f13));
-    st_shared_u16(a + 8, static_cast<uint16_t>(f02 >> 16));
-    st_shared_u16(a + 12, static_cast<uint16_t>(f13 >> 16));
-    __syncwarp();
-  }
   // ldmatrix: lane i names row (i & 7) + 8 ((i >> 3) & 1) of block (i >> 4) + {0, 2}
   const int lr = lane & 15;
   const uint32_t lrow = st + lr * kMxRowBytes;
   const uint32_t sw = (lr >> 1) & 3, b0 = lane >> 4;
   const uint32_t a0 = lrow + ((b0 ^ sw) << 4), a1 = lrow + (((b0 + 2) ^ sw) << 4);
+  uint32_t rk[2][8];
+#pragma unroll
+  for (int a = 0; a < 2; ++a) {
+    ldm4(a0 + a * 16 * kMxRowBytes, *reinterpret_cast<uint32_t(*)[4]>(rk[a]));
+    ldm4(a1 + a * 16 * kMxRowBytes, *reinterpret_cast<uint32_t(*)[4]>(rk[a] + 4));
+  }
+  // The scales become factors once per key (lane = key), not once per thread that needs them:
+  // K's four as fp32, at fact + 16 key; V's four as f16 2^(ev - R + 8), the pair of keys 2i and 2i + 1 of
+  // block b at fact + 512 + 16 i + 4 b. (With K's codes read before, and V's factors formed between the products: 64
+  // layers at pos 4700 65.8 -> 63.7 us, 4 layers at pos 131070 104 -> 98.)
+  {
+    const uint32_t ks = ld_shared_u32(st + 2 * kCodes + 4 * lane);
+    // (a K scale byte of 0, 2^-127, is taken as 0: such a block adds nothing to a score)
+    st_shared_v4(fact + 16 * lane, (ks << 23) & 0x7F800000u, (ks << 15) & 0x7F800000u, (ks << 7) & 0x7F800000u,
+                 (ks >> 1) & 0x7F800000u);
+    __syncwarp();
+  }
   float x[2][4];  // [16 keys][key g: heads 2t, 2t+1; key g + 8: the same]
 #pragma unroll
   for (int a = 0; a < 2; ++a) {
-    uint32_t r[8];
-    ldm4(a0 + a * 16 * kMxRowBytes, *reinterpret_cast<uint32_t(*)[4]>(r));
-    ldm4(a1 + a * 16 * kMxRowBytes, *reinterpret_cast<uint32_t(*)[4]>(r + 4));
+    const uint32_t(&r)[8] = rk[a];
     const uint4 u0 = ld_shared_v4(fact + 16 * (16 * a + g)), u1 = ld_shared_v4(fact + 16 * (16 * a + g + 8));
     const uint32_t f0[4] = {u0.x, u0.y, u0.z, u0.w}, f1[4] = {u1.x, u1.y, u1.z, u1.w};
 #pragma unroll
@@ -365,6 +359,21 @@ __device__ __forceinline__ void chunk(Warp& w, const uint32_t (&q)[4][4], const 
         const float f = __uint_as_float(k < 2 ? f0[b] : f1[b]);
         x[a][k] = b == 0 ? f * d[k] : fmaf(f, d[k], x[a][k]);
       }
+    }
+    if (a == 0) {  // (here, while the products run)
+      const uint32_t vs = ld_shared_u32(st + 2 * kCodes + kScales + 4 * lane);
+      const uint32_t v02 = vs & 0x00FF00FFu, v13 = (vs >> 8) & 0x00FF00FFu, top = __vmaxu2(v02, v13);
+      if (__any_sync(0xffffffffu, static_cast<int>(max(top & 0xFFFFu, top >> 16)) > w.ref + (kMaxField - kRefField)))
+        raise_ref(w, st, lane);
+      const uint32_t add = static_cast<uint32_t>((kRefField - w.ref) & 0xFFFF) * 0x10001u;
+      const uint32_t f02 = __viaddmin_s16x2_relu(v02, add, kMaxField * 0x10001u) << 10;
+      const uint32_t f13 = __viaddmin_s16x2_relu(v13, add, kMaxField * 0x10001u) << 10;
+      const uint32_t at = fact + 512 + 16 * (lane >> 1) + 2 * (lane & 1);
+      st_shared_u16(at, static_cast<uint16_t>(f02));
+      st_shared_u16(at + 4, static_cast<uint16_t>(f13));
+      st_shared_u16(at + 8, static_cast<uint16_t>(f02 >> 16));
+      st_shared_u16(at + 12, static_cast<uint16_t>(f13 >> 16));
+      __syncwarp();
     }
   }
 #pragma unroll
