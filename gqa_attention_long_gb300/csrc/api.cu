@@ -1311,17 +1311,17 @@ int run_mx_decode(const ea_decode_mxfp4_args* a, int n_layers, int pos, int Smax
     for (int l = 0; l < n; ++l) p.layer[l] = mx_layer(a[l0 + l]);
     const uint32_t units = static_cast<uint32_t>(n) * kHkv, sms = static_cast<uint32_t>(di.sm_count);
     const uint32_t W = units * p.T;
-    const uint32_t full = (p.T + kMxDecodeWarps - 1) / kMxDecodeWarps;  // parts of at most one chunk per warp
-    // Ranges that follow the units' ends, where they take as few CTAs as give every warp one chunk, or 95 % of the
-    // SMs: no CTA then works on two units. Else equal ranges over all of them. (With and without this rule: 1 layer at
-    // pos 300 5.3 and 7.5 us, at pos 4700 8.9 and 13.9; 3 layers at pos 1000 8.0 and 13.2.)
-    uint32_t grid;
-    if (units <= sms && (units * full <= sms || sms / units * units * 20 >= sms * 19)) {
-      p.parts = full < sms / units ? full : sms / units;
-      grid = units * p.parts;
-    } else {
+    // Parts that end with their unit (each of at least one chunk per warp), unless equal ranges over all SMs, which cut
+    // units anywhere, save a warp more than four chunks: a CTA that works on two units, and a unit of three parts, cost that
+    // much. Parts and ranges: 1 layer at pos 4700 9.2 and 14.6 us, 2 layers 9.3 and 13.8, 9 layers 16.0 and 18.0, 18 layers
+    // at pos 20000 (3.6 chunks more) 68.2 and 70.3, 5 layers there (4.3) 28.7 and 27.3, 4 layers at pos 131000 109 and 99.
+    auto ceil_div = [](uint32_t x, uint32_t y) { return (x + y - 1) / y; };
+    const uint32_t full = ceil_div(p.T, kMxDecodeWarps), fit = sms / units;
+    p.parts = full < fit ? full : fit;
+    if (p.parts > 0 && ceil_div(ceil_div(p.T, p.parts), kMxDecodeWarps) * sms * kMxDecodeWarps > W + 4 * sms * kMxDecodeWarps) p.parts = 0;
+    uint32_t grid = units * p.parts;
+    if (p.parts == 0) {
       grid = sms < W ? sms : W;
-      p.parts = 0;
       p.per_cta = W / grid;
       p.extra = W % grid;
     }

@@ -103,6 +103,26 @@ def test_half_a_million_keys_far_below_one(form, first):
         assert off <= bar
 
 
+@pytest.mark.parametrize("layers,pos,Smax", [(10, 8191, 8192), (5, 20000, 20032), (40, 1500, 1536)])
+def test_decode_units_cut_anywhere(layers, pos, Smax):
+    """Shapes whose units are cut over several CTAs at any chunk, a CTA working on more than one unit; two calls, so that the
+    second meets the counters that the first left."""
+    call, alloc, ref, hq, tok = FORMS["decode"]
+    picks = sorted({0, layers // 2, layers - 1})
+    xs = [step_inputs(50 + l, hq, tok) for l in range(layers)]
+    hs = [random_cache(60 + l % 3, Smax, pos) for l in range(3)]
+    bufs = [device_buffers(x, hs[l % 3].device()) for l, x in enumerate(xs)]
+    ws = alloc(layers)
+    for _ in range(2):
+        for b in bufs:
+            b.out.fill_(float("nan"))
+        call(bufs, pos, Smax, 0, ws)
+        check_status(ws)
+        for l in picks:
+            close(bufs[l].out, ref(xs[l], hs[l % 3], pos, 0)["out"], f"layer {l}")
+        assert all(torch.isfinite(b.out).all() for b in bufs)
+
+
 @pytest.mark.parametrize("form", FORMS)
 def test_a_query_that_is_not_a_number_stays_alone(form):
     call, alloc, ref, hq, tok = FORMS[form]
