@@ -134,7 +134,7 @@ constexpr int kConvert = 128;                         // threads of K's converte
 constexpr int kThreads = kSoftmax + 2 * kConvert + 128;
 // registers per thread after the roles part (launched with kRegLaunch): the sum is the launch's at most
 constexpr int kRegLaunch = 65536 / kThreads / 8 * 8;
-constexpr int kRegSoftmax = 88, kRegConvert = 72, kRegIssue = 64;
+constexpr int kRegSoftmax = 96, kRegConvert = 64, kRegIssue = 64;
 static_assert(kSoftmax * kRegSoftmax + 2 * kConvert * kRegConvert + 128 * kRegIssue <= kThreads * kRegLaunch, "register split");
 constexpr int kRing = 3;
 constexpr uint32_t kCodes = kKeyTile * kMxRowBytes, kScales = kKeyTile * kMxRowScales;
