@@ -226,8 +226,7 @@ struct Ctx {
       if (mbar_try_wait(bar(b), parity)) return true;
       if (*abort_flag) return false;
     }
-    *abort_flag = 1u;
-    atomicOr(status, err);
+    *abort_flag = err;  // (goes to the status word at the kernel's end)
     return false;
   }
   __device__ __forceinline__ bool wait3(int b, const Ring3& r, uint32_t err) const { return wait(b + r.b, r.par, err); }
@@ -795,6 +794,7 @@ __global__ void __launch_bounds__(mxa::kThreads, 1) mxfp4_attention_kernel(const
   __syncthreads();
   tc_fence_after();
   if (warp == 0) tmem_dealloc(cx.tmem, kTmemCols);
+  if (threadIdx.x == 0 && *cx.abort_flag != 0u) atomicOr(p.status, *cx.abort_flag);
 }
 
 // The units that the CTA ranges cut: grid (units, 16), thread = one row's 8 columns.
