@@ -52,7 +52,6 @@ template <bool kSplit>
 __global__ void __launch_bounds__(256, kSplit ? 1 : 3) mxfp4_prologue_kernel(const __grid_constant__ MxPrologueParams p) {
   const int g = blockIdx.y, l = blockIdx.z, i = threadIdx.x & 7;
   const int t = 32 * (blockIdx.x & 1) + (threadIdx.x >> 3);
-  const int row0 = kSplit ? blockIdx.x >> 1 : 0, row1 = kSplit ? row0 + 1 : 4;
   const int dl = 8 * i, dh = 64 + 8 * i;
   // The tables' rows that this half of the tokens needs, copied to shared memory while the preceding kernel ends (they
   // are read by lane-dependent index: through a generic address, not the constant bank). Frequency j at j + j / 8: an
@@ -85,45 +84,62 @@ __global__ void __launch_bounds__(256, kSplit ? 1 : 3) mxfp4_prologue_kernel(con
   pdl_launch_dependents();
   const MxAttnLayer& L = p.layer[l];
   const size_t unit = static_cast<size_t>(l) * kHkv + g;
-  const __nv_bfloat16* q0 = L.q_raw + (static_cast<size_t>(g) * 2 * kTok + t) * kD;
-  const size_t own = (static_cast<size_t>(g) * kTok + t) * kD;
-  const __nv_bfloat16* src[4] = {q0, q0 + kTok * kD, L.k_raw + own, L.v_raw + own};  // q of both heads, k, v
-  uint4 raw[4][2];  // (every row's loads go out before the first is used)
-#pragma unroll
-  for (int kind = 0; kind < 4; ++kind)
-    if (kind >= row0 && kind < row1) {
-      raw[kind][0] = *reinterpret_cast<const uint4*>(src[kind] + dl);
-      raw[kind][1] = *reinterpret_cast<const uint4*>(src[kind] + dh);
-    }
-  const uint4 gq[2] = {*reinterpret_cast<const uint4*>(L.q_gamma + dl), *reinterpret_cast<const uint4*>(L.q_gamma + dh)};
-  const uint4 gk[2] = {*reinterpret_cast<const uint4*>(L.k_gamma + dl), *reinterpret_cast<const uint4*>(L.k_gamma + dh)};
-#pragma unroll
-  for (int kind = 0; kind < 4; ++kind) {
-    if (kind < row0 || kind >= row1) continue;
+  auto load = [&](const __nv_bfloat16* src, uint4 (&to)[2]) {
+    to[0] = *reinterpret_cast<const uint4*>(src + dl);
+    to[1] = *reinterpret_cast<const uint4*>(src + dh);
+  };
+  auto load_row = [&](int kind, uint4 (&to)[2]) {  // kind: q of the unit's two heads, k, v
+    load(kind < 2 ? L.q_raw + (static_cast<size_t>(2 * g + kind) * kTok + t) * kD
+                  : (kind == 2 ? L.k_raw : L.v_raw) + (static_cast<size_t>(g) * kTok + t) * kD, to);
+  };
+  auto q_row = [&](int kind, const uint4 (&raw)[2], const uint4 (&gain)[2]) {
+    float xl[8], xh[8], gl[8], gh[8], yl[8], yh[8], factor;
+    unpack_bf16x8(raw[0], xl);
+    unpack_bf16x8(raw[1], xh);
+    unpack_bf16x8(gain[0], gl);
+    unpack_bf16x8(gain[1], gh);
+    norm_rope(xl, xh, gl, gh, cs, sn, yl, yh);
+    f16_row(yl, yh, p.scale_log2, factor);
+    const int r = kind * kTok + t;
+    uint8_t* q = p.q_ws + unit * kQTileBytes;
+    *reinterpret_cast<uint4*>(q + swz_off(r, i, kQTileBytes / 2)) = pack8(yl, true);
+    *reinterpret_cast<uint4*>(q + swz_off(r, i + 8, kQTileBytes / 2)) = pack8(yh, true);
+    if (i == 0) p.q_factor[unit * kRows + r] = factor;
+  };
+  auto new_row = [&](bool v, const uint4 (&raw)[2], const uint4 (&gain)[2]) {
     float xl[8], xh[8], gl[8], gh[8];
-    unpack_bf16x8(raw[kind][0], xl);
-    unpack_bf16x8(raw[kind][1], xh);
-    unpack_bf16x8(kind < 2 ? gq[0] : gk[0], gl);
-    unpack_bf16x8(kind < 2 ? gq[1] : gk[1], gh);
-    if (kind < 2) {
-      float yl[8], yh[8], factor;
-      norm_rope(xl, xh, gl, gh, cs, sn, yl, yh);
-      f16_row(yl, yh, p.scale_log2, factor);
-      const int r = kind * kTok + t;
-      uint8_t* q = p.q_ws + unit * kQTileBytes;
-      *reinterpret_cast<uint4*>(q + swz_off(r, i, kQTileBytes / 2)) = pack8(yl, true);
-      *reinterpret_cast<uint4*>(q + swz_off(r, i + 8, kQTileBytes / 2)) = pack8(yh, true);
-      if (i == 0) p.q_factor[unit * kRows + r] = factor;
-      continue;
-    }
+    unpack_bf16x8(raw[0], xl);
+    unpack_bf16x8(raw[1], xh);
     uint32_t cl, ch;
     int el, eh;
-    if (kind == 2) mx_encode_k_octet<true>(xl, xh, gl, gh, cs, sn, angle, cl, ch, el, eh);
-    else mx_encode_octet<true>(xl, xh, cl, ch, el, eh);
-    __nv_bfloat16* val = kind == 2 ? L.k_new : L.v_new;
+    if (v) {
+      mx_encode_octet<true>(xl, xh, cl, ch, el, eh);
+    } else {
+      unpack_bf16x8(gain[0], gl);
+      unpack_bf16x8(gain[1], gh);
+      mx_encode_k_octet<true>(xl, xh, gl, gh, cs, sn, angle, cl, ch, el, eh);
+    }
+    __nv_bfloat16* val = v ? L.v_new : L.k_new;
     if (val != nullptr) val += (static_cast<size_t>(g) * kTok + t) * kD;
-    mx_store_octet(cl, ch, el, eh, kind == 2 ? L.kc : L.vc, kind == 2 ? L.ks : L.vs,
-                   static_cast<size_t>(g) * p.Smax + p.Smax - kTok + t, i, val);
+    mx_store_octet(cl, ch, el, eh, v ? L.vc : L.kc, v ? L.vs : L.ks, static_cast<size_t>(g) * p.Smax + p.Smax - kTok + t, i, val);
+  };
+  if constexpr (kSplit) {
+    const int kind = blockIdx.x >> 1;
+    uint4 raw[2], gain[2];
+    load_row(kind, raw);
+    load(kind < 2 ? L.q_gamma : L.k_gamma, gain);
+    if (kind < 2) q_row(kind, raw, gain);
+    else new_row(kind == 3, raw, gain);
+  } else {
+    uint4 raw[4][2], gq[2], gk[2];  // (every row's loads go out before the first is used)
+#pragma unroll
+    for (int kind = 0; kind < 4; ++kind) load_row(kind, raw[kind]);
+    load(L.q_gamma, gq);
+    load(L.k_gamma, gk);
+    q_row(0, raw[0], gq);
+    q_row(1, raw[1], gq);
+    new_row(false, raw[2], gk);
+    new_row(true, raw[3], gk);
   }
 }
 
@@ -154,8 +170,8 @@ __device__ __forceinline__ uint32_t bar_count(int b) {
   return b >= B_EMPTY && b < B_SFULL ? kConvert : b >= B_MDONE && b < B_ODONE ? 128 : b >= B_RDY && b < B_REF ? kConvert
          : b == B_OFREE ? 256 : 1;
 }
-constexpr uint32_t SM_TMEM = SM_BAR + kNumBars * 8, SM_ABORT = SM_TMEM + 4;
-constexpr uint32_t kSmemBytes = SM_ABORT + 4 + 1024;  // + slack to align the base
+constexpr uint32_t SM_TMEM = SM_BAR + kNumBars * 8, SM_FAILED = SM_TMEM + 4;
+constexpr uint32_t kSmemBytes = SM_FAILED + 4 + 1024;  // + slack to align the base
 static_assert(kSmemBytes <= 232448 && SM_RING % 128 == 0 && SM_X % 16 == 0 && SM_BAR % 8 == 0, "shared memory of one sm_103 CTA");
 constexpr uint32_t TM_S = 0, TM_O = 384, kTmemCols = 512;  // three score (then P) buffers, the accumulator
 constexpr int kRefField = 23, kMaxField = 26;  // f16 exponent field of 2^(e - R + 8), and its cut (all-zero blocks)
@@ -214,19 +230,19 @@ struct Ring3 {
 struct Ctx {
   uint8_t* smem;
   uint32_t sbase, tmem;
-  volatile uint32_t* abort_flag;
+  volatile uint32_t* failed;
   uint32_t* status;
   long long start, end;
   __device__ __forceinline__ uint32_t bar(int i) const { return sbase + SM_BAR + 8u * i; }
-  // As bounded_wait, in less code: limited by the number of looks (2^20 of them, each of which suspends the thread
-  // for a while, last longer than any wait of a call that works).
+  // As bounded_wait, in less code (with its code in every role the 64 layers took 5 us more), by a whole warp: limited by
+  // the number of looks (2^20 of them, each of which suspends the warp for a while, last longer than any wait of a
+  // call that works). Whoever has to give up notes why; the other roles then run out of looks themselves.
   __device__ __forceinline__ bool wait(int b, uint32_t parity, uint32_t err) const {
 #pragma unroll 1
     for (uint32_t it = 0; it < (1u << 20); ++it) {
-      if (mbar_try_wait(bar(b), parity)) return true;
-      if (*abort_flag) return false;
+      if (__all_sync(0xffffffffu, mbar_try_wait(bar(b), parity))) return true;
     }
-    *abort_flag = err;  // (goes to the status word at the kernel's end)
+    *failed = err;  // (goes to the status word at the kernel's end)
     return false;
   }
   __device__ __forceinline__ bool wait3(int b, const Ring3& r, uint32_t err) const { return wait(b + r.b, r.par, err); }
@@ -293,7 +309,7 @@ __device__ __forceinline__ void producer(const MxExpertParams& p, const Ctx cx) 
         codes = (kv ? L.vc : L.kc) + row * kMxRowBytes;
         scales = (kv ? L.vs : L.ks) + row * kMxRowScales;
       }
-      if (vn >= kRing - 1) ok = __all_sync(0xffffffffu, cx.wait(kEmpty + at.b, at.par ^ 1, kErrProducerWait));
+      if (vn >= kRing - 1) ok = cx.wait(kEmpty + at.b, at.par ^ 1, kErrProducerWait);
       if (!ok) break;
       const int live = tile_live(p, lj);
       // scale words come in fours: up to three rows past the last key (still in the cache) come along
@@ -317,7 +333,7 @@ __device__ __forceinline__ void producer(const MxExpertParams& p, const Ctx cx) 
       }
     }
     if (vn < 0) continue;
-    ok = __all_sync(0xffffffffu, cx.wait(kFull + look.b, look.par, kErrProducerWait));
+    ok = cx.wait(kFull + look.b, look.par, kErrProducerWait);
     if (!ok) break;
     if (vj == v.j0) ref = 0;  // a segment starts: references of its own
     const int live = tile_live(p, vj);
@@ -433,7 +449,7 @@ constexpr uint64_t kDescMN = (1ull << 61 << 1) | (1ull << 46) | (static_cast<uin
 __device__ __forceinline__ void qk_issuer(const MxExpertParams& p, const Ctx cx) {
   constexpr uint32_t kIdesc = umma_idesc_f16(128, 128, false, false, false);
   const uint64_t qd = kDescK | ((cx.sbase + SM_Q) >> 4), kd = kDescK | ((cx.sbase + SM_K) >> 4);
-  auto wait = [&](int b, uint32_t parity) -> bool { return __all_sync(0xffffffffu, cx.wait(b, parity, kErrMmaWait)); };
+  auto wait = [&](int b, uint32_t parity) -> bool { return cx.wait(b, parity, kErrMmaWait); };
   uint32_t n = 0, b3 = 0, par = 0, loads = 0;  // b3 = n % 3, par = n / 3 & 1
   bool ok = true;
 #pragma unroll 1
@@ -482,7 +498,7 @@ __device__ __forceinline__ void qk_issuer(const MxExpertParams& p, const Ctx cx)
 __device__ __forceinline__ void pv_issuer(const MxExpertParams& p, const Ctx cx) {
   constexpr uint32_t kIdesc = umma_idesc_f16(128, 128, false, false, true);
   const uint64_t vd = kDescMN | ((cx.sbase + SM_V) >> 4);
-  auto wait = [&](int b, uint32_t parity) -> bool { return __all_sync(0xffffffffu, cx.wait(b, parity, kErrMmaWait)); };
+  auto wait = [&](int b, uint32_t parity) -> bool { return cx.wait(b, parity, kErrMmaWait); };
   uint32_t n = 0, b3 = 0, par = 0, seg = 0;
   bool ok = true;
 #pragma unroll 1
@@ -573,7 +589,7 @@ __device__ __forceinline__ void softmax_warps(const MxExpertParams& p, const Ctx
   Ring3 rn;  // of this warpgroup's next tile
   rn.b = k;
   bool ok = true;
-  auto wait3 = [&](int b, const Ring3& at) -> bool { return __all_sync(0xffffffffu, cx.wait3(b, at, kErrSoftmaxWait)); };
+  auto wait3 = [&](int b, const Ring3& at) -> bool { return cx.wait3(b, at, kErrSoftmaxWait); };
 #pragma unroll 1
   for (Seg s = first_seg(cx.start, cx.end, p.T); s.j1 > s.j0; next_seg(s, p.T)) {
     const int nt = s.j1 - s.j0;
@@ -584,7 +600,7 @@ __device__ __forceinline__ void softmax_warps(const MxExpertParams& p, const Ctx
       const uint32_t n = base + i;
       const int j = s.j0 + i;
       // (K's reference was there before its tile was converted)
-      ok = __all_sync(0xffffffffu, cx.wait(B_REF + 8 + (n & 7), (n >> 3) & 1, kErrSoftmaxWait)) && wait3(B_SFULL, rn);
+      ok = cx.wait(B_REF + 8 + (n & 7), (n >> 3) & 1, kErrSoftmaxWait) && wait3(B_SFULL, rn);
       if (!ok) break;
       tc_fence_after();
       const uint32_t sa = cx.tmem + lane + TM_S + rn.b * 128;
@@ -680,7 +696,7 @@ __device__ __forceinline__ void softmax_warps(const MxExpertParams& p, const Ctx
     }
     // ---- the segment's end: the last PV, the warpgroups' sums; thread (k, r), k < 2, takes columns [64 k, 64 k + 64)
     const uint32_t last = base + nt - 1;
-    if (ok) ok = __all_sync(0xffffffffu, cx.wait3(B_ODONE, last, kErrSoftmaxWait));
+    if (ok) ok = cx.wait3(B_ODONE, last, kErrSoftmaxWait);
     // (by segment parity: a warpgroup may be here while the other still reads the segment before; it cannot
     // pass this segment's barrier before that)
     float2* xch = reinterpret_cast<float2*>(cx.smem + SM_X) + (seg & 1) * kSoftWg * kRows;
@@ -757,14 +773,14 @@ __global__ void __launch_bounds__(mxa::kThreads, 1) mxfp4_attention_kernel(const
   Ctx cx;
   cx.smem = smem;
   cx.sbase = smem_u32(smem);
-  cx.abort_flag = reinterpret_cast<volatile uint32_t*>(smem + SM_ABORT);
+  cx.failed = reinterpret_cast<volatile uint32_t*>(smem + SM_FAILED);
   cx.status = p.status;
   cx.start = cta_tile_start(blockIdx.x, p.W, gridDim.x);
   cx.end = cta_tile_start(blockIdx.x + 1, p.W, gridDim.x);
   const int warp = threadIdx.x >> 5;
   if (warp == 1) {
     for (int b = threadIdx.x & 31; b < kNumBars; b += 32) mbar_init(cx.bar(b), bar_count(b));
-    if ((threadIdx.x & 31) == 0) *cx.abort_flag = 0u;
+    if ((threadIdx.x & 31) == 0) *cx.failed = 0u;
     fence_mbar_init();
   }
   if (warp == 0) {
@@ -794,7 +810,7 @@ __global__ void __launch_bounds__(mxa::kThreads, 1) mxfp4_attention_kernel(const
   __syncthreads();
   tc_fence_after();
   if (warp == 0) tmem_dealloc(cx.tmem, kTmemCols);
-  if (threadIdx.x == 0 && *cx.abort_flag != 0u) atomicOr(p.status, *cx.abort_flag);
+  if (threadIdx.x == 0 && *cx.failed != 0u) atomicOr(p.status, *cx.failed);
 }
 
 // The units that the CTA ranges cut: grid (units, 16), thread = one row's 8 columns.

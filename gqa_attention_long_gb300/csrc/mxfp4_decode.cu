@@ -60,7 +60,7 @@ constexpr uint32_t SM_Q = (SM_R + kWarps * 4 + 15) & ~15u;              // 2 x [
 constexpr uint32_t SM_QF = SM_Q + 2 * kRepText * kD * 2;                // 2 x [8 heads] score factor
 constexpr uint32_t kNewBytes = 2 * kMxRowBytes + 8;
 constexpr uint32_t SM_NEW = SM_QF + 2 * kRepText * 4;                   // 2 x (K codes, V codes, scale words)
-constexpr uint32_t SM_FLAG = SM_NEW + 2 * 144, SM_ABORT = SM_FLAG + 4;
+constexpr uint32_t SM_FLAG = SM_NEW + 2 * 144;
 constexpr uint32_t SM_BAR = SM_FLAG + 16;
 // by segment: a unit's q (and new rows) are there (in the buffer of its parity); its partials are; they are read
 constexpr uint32_t B_QRDY = 0, B_PART = 2, B_READ = 3, kNumBars = 4;
@@ -516,19 +516,20 @@ __global__ void __launch_bounds__(mxd::kThreads, 1) mxfp4_decode_kernel(const __
   const uint32_t sbase = smem_u32(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t start = cta_start(p, blockIdx.x), end = cta_start(p, blockIdx.x + 1);
-  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + SM_ABORT);
   auto bar = [&](uint32_t b) { return sbase + SM_BAR + 8 * b; };
   if (tid == 0) {
     mbar_init(bar(B_QRDY), kPrep / 32);
     mbar_init(bar(B_QRDY + 1), kPrep / 32);
     mbar_init(bar(B_PART), kWarps);
     mbar_init(bar(B_READ), kPrep / 32);
-    *abort_flag = 0u;
     fence_mbar_init();
   }
   pdl_wait_primary();
-  auto wait = [&](uint32_t b, uint32_t parity) -> bool {
-    return __all_sync(0xffffffffu, bounded_wait(bar(b), parity, abort_flag, p.status, kErrDecodeWait));
+  auto wait = [&](uint32_t b, uint32_t parity) -> bool {  // gives up after 2^20 looks, each of which takes a while
+    bool done = false;
+#pragma unroll 1
+    for (uint32_t it = 0; !done && it < (1u << 20); ++it) done = mbar_try_wait(bar(b), parity);
+    return __all_sync(0xffffffffu, done);
   };
   auto arrive = [&](uint32_t b) {
     __syncwarp();
@@ -630,6 +631,7 @@ __global__ void __launch_bounds__(mxd::kThreads, 1) mxfp4_decode_kernel(const __
     }
     cp_wait<0>();
     ok = bar_sync_and(kBarEnd, kThreads, ok);
+    if (!ok && tid == 0) atomicOr(p.status, kErrDecodeWait);
     if (!ok || warp >= kPrep / 32) return;
   }
   // The preparing warps: unit 0, unit 1, then, segment by segment, the end of its unit and the unit after the next. At
