@@ -1353,7 +1353,8 @@ int mx_split_units(long long W, int T, int n_ctas, SplitUnit* out) {
 }
 
 // Up to so many tiles a unit is one CTA's, if the units do not fill the GPU: that saves the parts' merge. One layer, cut and
-// whole: S = 256 (3 tiles) 13.5 and 12.1 us, S = 384 (4) 13.6 and 12.7, S = 512 (5) 13.7 and 14.1.
+// whole: S = 256 (3 tiles) 13.5 and 12.1 us, S = 384 (4) 13.6 and 12.7,
+// S = 512 (5) 13.7 and 14.1.
 constexpr int kMxWholeUnitTiles = 4;
 
 int run_mx_expert(const ea_layer_mxfp4_args* a, int n_layers, int S, int Smax, long long p0, void* workspace,

@@ -26,13 +26,13 @@
 // with the maximum that it last knew (raised when a chunk's weights pass it by far) and compares notes with
 // tile n - 1's at the end, through shared memory: only where the two differ is P(n), or the accumulator, scaled.
 //
-// Measured: 64 layers at S = 4700 163 us (of these the prologue 15, the merge 2), 2 layers at S = 65537 68 us,
-// 1 layer at S = 4700 17.4 us, at S = 256 12.3 us. A tile takes about 1,900 cycles, of which its MMAs are 1,025 (tensor pipe
-// 48 % busy). No unit is full: a converter spends 1,100 cycles on a row and as many on its waits and hand-overs, a
-// softmax warpgroup 2,700 on a tile, of which three are in flight, and together they take 61 % of the issue slots.
-// Tried and slower: tiles of 96 keys with four score buffers (183 us: a tile's fixed costs), two warpgroups to a
-// converter (183), two for the softmax (175), waits that spin (174), scores fetched a chunk ahead (181). One
-// layer is a chain: prologue 3.8 us, load and reference 2.3, two tiles 3.4, epilogue 1.5, merge 3.3.
+// Measured: 64 layers at S = 4700 156 us (of these the prologue 15, the merge 2), 2 layers at S = 65537 65 us,
+// 1 layer at S = 4700 16.6 us, at S = 256 11.4 us. A tile takes about 1,800 cycles, of which its MMAs are 1,025 (tensor pipe
+// 50 % busy). No unit is full: a converter spends 1,100 cycles on a row and 700 on its waits and hand-overs, a
+// softmax warpgroup 2,700 on a tile, of which three are in flight, and together they take 60 % of the issue slots.
+// Tried and slower, at 64 layers: tiles of 96 keys with four score buffers (+13 %: a tile's fixed costs), two
+// warpgroups to a converter (+9 %), two for the softmax (+2 %), waits that spin (+5 %), scores fetched a chunk ahead
+// (+6 %). One layer is a chain: prologue 3.5 us, load and reference 2.3, two tiles 3.2, epilogue 1.5, merge 3.3.
 //
 // The instruction cache held earlier forms back: with the roles' loops unrolled, 68 % of the peak of
 // instruction fetches went to the second level and every role crawled (3,600 cycles a tile). So the
@@ -46,8 +46,8 @@ namespace ea {
 // ------------------------------------------------------------------------------- prologue
 // One octet of threads per token and kv head: the token's two q rows, its k row and its v row, whose angles are formed
 // once (three CTAs to an SM); or, when there are too few of them to fill the GPU (kSplit), one of the four
-// rows (at S = 300, four rows and one: 1 layer 14.9 and 13.4 us, 4 layers 14.8 and 14.7, 8 layers 16.4 and 17.5). grid (2
-// or 8, kv heads, layers).
+// rows (with four rows or one, at S = 300: 1 layer 14.9 or 13.4 us, 4 layers 14.8 or 14.7, 8 layers 16.4 or 17.5). grid
+// (2 or 8, kv heads, layers).
 template <bool kSplit>
 __global__ void __launch_bounds__(256, kSplit ? 1 : 3) mxfp4_prologue_kernel(const __grid_constant__ MxPrologueParams p) {
   const int g = blockIdx.y, l = blockIdx.z, i = threadIdx.x & 7;

@@ -31,8 +31,8 @@
 // unit's end, each lost up to a chunk's time there: 64 layers 72.7 us, now 65.7.) A unit cut over several CTAs
 // is merged by the part that finishes last.
 //
-// Measured: 64 layers at pos 4700 63.7 us (5.2 TB/s, 76 % of a plain copy), 4 layers at pos 131070 98.3 us (5.8 TB/s,
-// 86 %); 1 layer at pos 4700 9.2 us, at pos 300 5.4 us. What holds it below the copy: the conversions share the ALU
+// Measured: 64 layers at pos 4700 63.7 us (5.2 TB/s, 76 % of a plain copy), 4 layers at pos 131070 99 us (5.8 TB/s,
+// 85 %); 1 layer at pos 4700 9.2 us, at pos 300 5.4 us. What holds it below the copy: the conversions share the ALU
 // pipe (57 % busy) and the issue slots (50 %) with the softmax; at one layer the latencies of the launch, one
 // chunk's load, the parts' arrival and the merge.
 #include "mxfp4.cuh"
