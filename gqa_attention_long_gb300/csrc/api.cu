@@ -1291,7 +1291,9 @@ int run_mx_decode(const ea_decode_mxfp4_args* a, int n_layers, int pos, int Smax
   DeviceInfo di;
   if (!device_info(&dev, &di) || !mx_attrs_ready()) return EA_ERR_UNSUPPORTED;
   const int per = n_layers < kMaxLayersPerLaunch ? n_layers : kMaxLayersPerLaunch;
-  const DecodeWs wl = decode_ws_layout(per, di.sm_count);
+  // (the layout of 64 layers whatever their number: the counters that a larger call needs at zero stay out of a smaller
+  // call's partials)
+  const DecodeWs wl = decode_ws_layout(kMaxLayersPerLaunch, di.sm_count);
   if (ws_bytes < wl.total) return EA_ERR_WORKSPACE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   MxDecodeParams p;
@@ -1430,7 +1432,7 @@ size_t text_decode_mxfp4_workspace_size(int n_layers) {
   int dev;
   DeviceInfo di;
   if (n_layers < 1 || !device_info(&dev, &di)) return 0;
-  return decode_ws_layout(n_layers < kMaxLayersPerLaunch ? n_layers : kMaxLayersPerLaunch, di.sm_count).total;
+  return decode_ws_layout(kMaxLayersPerLaunch, di.sm_count).total;
 }
 
 int text_decode_attention_mxfp4(const ea_decode_mxfp4_args* layers, int n_layers, int pos, int Smax, int rope_delta,

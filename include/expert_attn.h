@@ -362,7 +362,7 @@ typedef struct {
   void* v_new; /* optional */
 } ea_decode_mxfp4_args;
 
-/* Bytes of workspace for a call over n_layers layers on the current device (0 without a suitable one):
+/* Bytes of workspace for calls over up to n_layers layers on the current device (0 without a suitable one):
  * 256-byte aligned, cleared once with text_decode_workspace_init, used by this function alone and not
  * by calls that overlap; expert_attn_read_status reads its status word. */
 size_t text_decode_mxfp4_workspace_size(int n_layers);

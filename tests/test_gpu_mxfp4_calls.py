@@ -202,3 +202,25 @@ def test_two_streams_at_once():
         check_status(ws)
         for b, o in zip(bufs, alone):
             assert torch.equal(b.out, o)
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_one_workspace_for_calls_of_different_layer_counts(form):
+    """A workspace made for 64 layers serves smaller calls in between: whatever they keep there stays out of the way."""
+    call, alloc, ref, hq, tok = FORMS[form]
+    ws = alloc(64)
+    h = [random_cache(3 + l, 512, 400) for l in range(3)]
+    many = [device_buffers(step_inputs(l, hq, tok), h[l % 3].device()) for l in range(64)]
+    few = [device_buffers(step_inputs(100 + l, hq, tok), random_cache(8 + l, 1088, 1000).device()) for l in range(3)]
+    outs = []
+    for _ in range(2):
+        for b in many:
+            b.out.fill_(float("nan"))
+        call(many, 400, 512, 0, ws)
+        outs.append([b.out.clone() for b in many])
+        call(few, 1000, 1088, 0, ws)
+    check_status(ws)
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+    for l in (0, 40, 63):
+        close(outs[1][l], ref(step_inputs(l, hq, tok), h[l % 3], 400, 0)["out"], f"layer {l}")
