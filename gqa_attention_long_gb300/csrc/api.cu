@@ -1315,7 +1315,7 @@ int run_mx_decode(const ea_decode_mxfp4_args* a, int n_layers, int pos, int Smax
     const uint32_t W = units * p.T;
     // Parts that end with their unit (each of at least one chunk per warp), unless equal ranges over all SMs, which cut
     // units anywhere, save a warp more than four chunks: a CTA that works on two units, and a unit of three parts, cost that
-    // much. Parts and ranges: 1 layer at pos 4700 9.2 and 14.6 us, 2 layers 9.3 and 13.8, 9 layers 16.0 and 18.0, 18 layers
+    // much. Parts and ranges: 1 layer at pos 4700 8.2 and 14.6 us, 2 layers 8.9 and 13.8, 9 layers 16.0 and 18.0, 18 layers
     // at pos 20000 (3.6 chunks more) 68.2 and 70.3, 5 layers there (4.3) 28.7 and 27.3, 4 layers at pos 131000 109 and 99.
     auto ceil_div = [](uint32_t x, uint32_t y) { return (x + y - 1) / y; };
     const uint32_t full = ceil_div(p.T, kMxDecodeWarps), fit = sms / units;

@@ -31,8 +31,8 @@
 // unit's end, each lost up to a chunk's time there: 64 layers 72.7 us, now 65.7.) A unit cut over several CTAs
 // is merged by the part that finishes last.
 //
-// Measured: 64 layers at pos 4700 63.7 us (5.2 TB/s, 76 % of a plain copy), 4 layers at pos 131070 99 us (5.8 TB/s,
-// 85 %); 1 layer at pos 4700 9.2 us, at pos 300 5.4 us. What holds it below the copy: the conversions share the ALU
+// Measured: 64 layers at pos 4700 63.7 us (5.2 TB/s, 76 % of a plain copy), 4 layers at pos 131070 98 us (5.8 TB/s,
+// 86 %); 1 layer at pos 4700 8.2 us, at pos 300 5.2 us. What holds it below the copy: the conversions share the ALU
 // pipe (57 % busy) and the issue slots (50 %) with the softmax; at one layer the latencies of the launch, one
 // chunk's load, the parts' arrival and the merge.
 #include "mxfp4.cuh"
@@ -487,21 +487,30 @@ __device__ __forceinline__ void join(const MxDecodeParams& p, uint8_t* smem, uin
   auto slot = [&](uint32_t k) -> size_t { return k == 0 ? first : static_cast<size_t>(c0 + k) * 2; };
 #pragma unroll 1
   for (int h = w; h < kRepText; h += nw) {
-    // lane k: part k's weight (np <= 32: kMxMaxParts)
+    // lane k: part k's weight (np <= 32: kMxMaxParts); the first parts' loads go out together with the weights' (1
+    // layer at pos 4700, 13 parts: 9.2 -> 8.2 us)
+    constexpr uint32_t kAhead = 16;
     const float lse = c < np ? __ldcg(p.part_lse + slot(c) * kRepText + h) : -INFINITY;
+    const float4* src = reinterpret_cast<const float4*>(p.part_o + h * kD + 4 * c);
+    float4 ahead[kAhead];
+#pragma unroll
+    for (uint32_t k = 0; k < kAhead; ++k) ahead[k] = k < np ? __ldcg(src + slot(k) * (kRepText * kD / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
     const float wt = ex2_approx(lse - warp_max(lse));
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     float ws = 0.f;
-#pragma unroll 8
-    for (uint32_t k = 0; k < np; ++k) {
+    auto add = [&](uint32_t k, const float4& o) {
       const float wk = __shfl_sync(0xffffffffu, wt, k);
-      const float4 o = __ldcg(reinterpret_cast<const float4*>(p.part_o + (slot(k) * kRepText + h) * kD + 4 * c));
       ws += wk;
       s.x = fmaf(wk, o.x, s.x);
       s.y = fmaf(wk, o.y, s.y);
       s.z = fmaf(wk, o.z, s.z);
       s.w = fmaf(wk, o.w, s.w);
-    }
+    };
+#pragma unroll
+    for (uint32_t k = 0; k < kAhead; ++k)
+      if (k < np) add(k, ahead[k]);
+#pragma unroll 4
+    for (uint32_t k = kAhead; k < np; ++k) add(k, __ldcg(src + slot(k) * (kRepText * kD / 4)));
     const float iw = 1.0f / ws;
     *reinterpret_cast<uint2*>(out + h * kD) = make_uint2(pack_bf16x2(s.x * iw, s.y * iw), pack_bf16x2(s.z * iw, s.w * iw));
   }
