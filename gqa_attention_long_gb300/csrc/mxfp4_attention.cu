@@ -604,7 +604,8 @@ __device__ __forceinline__ void softmax_warps(const MxExpertParams& p, const Ctx
       if (!ok) break;
       tc_fence_after();
       const uint32_t sa = cx.tmem + lane + TM_S + rn.b * 128;
-      const float ct = qf * mx_scale(refs[n & 7]);
+      // (never 0, as the product of a small query's factor and a small reference can be: a masked score is -inf)
+      const float ct = fmaxf(qf * mx_scale(refs[n & 7]), 0x1p-126f);
       // what V's reference, if it rose from the tile before (in the same segment) to this one, makes of the accumulator
       float scale = 1.f;
       if (i > 0) {

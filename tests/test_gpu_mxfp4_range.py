@@ -1,0 +1,50 @@
+"""The attentions over a 4-bit cache where scales differ by far more than 16-bit numbers hold: between the channel blocks
+of the values or the keys, between rows, and between queries and keys. Outputs are compared 32 channels at a time, so that
+small channels count beside large ones. The bar is that of the attentions' other tests, relative L2 <= 5e-3 (its terms are
+added up there); the references are fp64."""
+import numpy as np
+import pytest
+import torch
+
+import gqa_attention_long_gb300 as ea
+from tests._gpu_util import check_status
+from tests._mxfp4_util import HostCache, decode_oracle, device_buffers, expert_oracle, f64, step_inputs
+from tests.test_gpu_mxfp4_attention import REL
+
+pytestmark = pytest.mark.gpu
+FORMS = {"decode": (ea.text_decode_attention_mxfp4, ea.alloc_decode_mxfp4_workspace, decode_oracle, 64, 1),
+         "expert": (ea.expert_attn_layers_mxfp4, ea.alloc_mxfp4_workspace, expert_oracle, 16, 64)}
+
+
+def close_by_block(got: torch.Tensor, want: np.ndarray, what: str):
+    g = f64(got)
+    assert np.isfinite(g).all(), what
+    for b in range(4):
+        c = slice(32 * b, 32 * b + 32)
+        rel = np.linalg.norm(g[..., c] - want[..., c]) / np.linalg.norm(want[..., c])
+        assert rel <= REL, f"{what}: channels {32 * b} to {32 * b + 31}: rel-L2 {rel:.2e}"
+
+
+def run(form, x, h, n, delta, layers):
+    """The same layer `layers` times in one call: with 20 of them a CTA's keys are many tiles of a unit, with one layer a
+    unit is cut over all of them."""
+    call, alloc, ref, _, _ = FORMS[form]
+    bufs = [device_buffers(x, h.device()) for _ in range(layers)]
+    ws = alloc(layers)
+    call(bufs, n, h.Smax, delta, ws)
+    check_status(ws)
+    want = ref(x, h, n, delta)["out"]
+    for l in {0, layers // 2, layers - 1}:
+        close_by_block(bufs[l].out, want, f"layer {l}")
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("n", [1, 72, 200, 127, 300])
+@pytest.mark.parametrize("size", [1e-6, 1e-8, 1e-12])
+def test_small_queries_over_zero_keys(form, n, size):
+    """Rows that were never written before the last key, and a query of next to nothing: every key counts the same."""
+    _, _, _, hq, tok = FORMS[form]
+    x = step_inputs(n, hq, tok)
+    x["q_raw"] = (x["q_raw"].float() * size).to(torch.bfloat16)
+    v = np.random.default_rng(n).standard_normal((8, 512, 128))
+    run(form, x, HostCache(np.zeros_like(v), v, n), n, 0, 1)
