@@ -296,7 +296,7 @@ struct MxExpertParams {
   MxAttnLayer layer[kMaxLayersPerLaunch];
   const uint8_t* q_ws;
   const float* q_factor;
-  uint4* part_o;     // partials as in AttnParams
+  uint4* part_o;     // partials as in AttnParams, but a power of two for every 32 columns of a row
   float* part_lse;
   uint32_t* status;
   long long W;       // tiles: n_layers * 8 * T
@@ -309,6 +309,7 @@ struct MxMergeParams {
   __nv_bfloat16* out[kMaxLayersPerLaunch];
   SplitUnit split[kMaxSplitUnits];
 };
+constexpr int kMxPartRows = 1 + kD / 32;  // fp32 rows of a partial: log2-sum-exp, and the four inverse powers
 // Workspace: [0, 1024) status word; q_factor; q tiles; partials of at most max_ctas CTAs.
 struct MxExpertWs {
   size_t factor_off, q_off, part_o_off, part_lse_off, total;
@@ -323,7 +324,7 @@ constexpr MxExpertWs mx_expert_ws(int n_layers, int max_ctas) {
   w.part_o_off = off;
   off += static_cast<size_t>(max_ctas) * 2 * kRows * kD * 2;
   w.part_lse_off = off;
-  off += static_cast<size_t>(max_ctas) * 2 * 3 * kRows * sizeof(float);
+  off += static_cast<size_t>(max_ctas) * 2 * kMxPartRows * kRows * sizeof(float);
   w.total = (off + 1023) & ~static_cast<size_t>(1023);
   return w;
 }

@@ -8,8 +8,8 @@
 //   M = max_s lse_s,   w_s = 2^(lse_s - M) / sum_t 2^(lse_t - M),   out = sum_s w_s O_s,
 // written as bf16 to out[layer][2g + r/64][r%64][:] (folded row r of kv head g).
 //
-// Partials are f16, each half row (64 columns) stored times a power of two whose inverse sits
-// beside the lse, and chunk-major (16-byte chunk c, columns 8c .. 8c+7, of row r at c * 128 + r).
+// Partials are f16, each half row (kScales = 2) or 32 columns (4) stored times a power of two whose
+// inverse sits beside the lse, and chunk-major (16-byte chunk c, columns 8c .. 8c+7, of row r at c * 128 + r).
 // One thread merges one row's chunk c (8 output columns); the 128 threads of a group take the
 // 128 rows of one chunk, so that every load instruction of a warp reads 512 contiguous bytes.
 // Parts are taken kBatch at a time, each thread requesting a batch's lse values, scales and
@@ -23,7 +23,7 @@
 
 namespace ea {
 
-template <int kBatch>
+template <int kBatch, int kScales = 2>
 __device__ __forceinline__ void merge_row_chunk(const uint4* part_o, const float* part_lse,
                                                 const SplitUnit& su, int c, int r,
                                                 __nv_bfloat16* out_layer) {
@@ -40,8 +40,8 @@ __device__ __forceinline__ void merge_row_chunk(const uint4* part_o, const float
       const int q = min(q0 + e, nparts - 1);
       // part q's slot: 2 (c0 + q), except the first part's, which is 2 c0 + slot0
       const size_t sl = static_cast<size_t>(su.c0 + q) * 2 + (q == 0 ? su.slot0 : 0);
-      lse[e] = __ldcg(part_lse + sl * 3 * kRows + r);
-      isc[e] = __ldcg(part_lse + (sl * 3 + 1 + (c >> 3)) * kRows + r);
+      lse[e] = __ldcg(part_lse + sl * (1 + kScales) * kRows + r);
+      isc[e] = __ldcg(part_lse + (sl * (1 + kScales) + 1 + c * kScales / kPartChunks) * kRows + r);
       o[e] = __ldcg(part_o + (sl * kPartChunks + c) * kRows + r);
     }
 #pragma unroll

@@ -10,10 +10,12 @@
 //
 // The codes are widened to f16 tiles in shared memory, where tcgen05.mma takes them (a fragment in
 // registers, as the decode step has it, would have to be formed again for each of the 128 query rows'
-// warps). A code times 2^(e - R + 8) is exact in f16 as long as its block's scale e is within 2^22 below R;
-// R is a running reference per segment and tensor, the largest scale of a block that is not all zeros
-// (raised when a tile exceeds it by 2^3). K's reference goes back into the scores, V's into the
-// output, both in fp32.
+// warps). A code times 2^(e - R + 8) is exact in f16 as long as its block's scale e is within 2^22 below R, a
+// reference per segment and tensor: the largest scale of a block that is not all zeros, as of the last tile that had one
+// 2^3 above it or 2^22 below. K's reference goes back into the scores, V's into the output, both in fp32. A tile whose own
+// blocks lie more than 2^22 apart goes through the tensor cores without the blocks below, and the softmax adds what
+// those give in fp32 (to the scores before they are used, to the accumulator before the tile's P V): a tile of 128 keys
+// then takes tens of microseconds, but no block counts as zero down to 2^100 below the segment's largest.
 //
 // Warp roles (768 threads):
 //   warps 0-3, 4-7, 8-11  softmax of the CTA's tiles in turn: thread = query row = TMEM lane
@@ -159,7 +161,7 @@ constexpr uint32_t kAtom = 16384, kTile = 2 * kAtom;        // an f16 tile: two 
 constexpr uint32_t SM_Q = 0, SM_K = SM_Q + kTile, SM_V = SM_K + 2 * kTile, SM_RING = SM_V + 2 * kTile;
 constexpr uint32_t SM_X = SM_RING + 2 * kRing * kStageBytes;   // [segment parity][warpgroup][row] (m, l)
 constexpr uint32_t SM_M = SM_X + 2 * kSoftWg * kRows * 8;      // [row] running maximum (log2 units)
-constexpr uint32_t SM_REF = SM_M + kRows * 4;               // [K, V][8]: R of tile n % 8
+constexpr uint32_t SM_REF = SM_M + kRows * 4;               // [K, V][8]: R of tile n % 8, and kLow
 constexpr uint32_t SM_BAR = SM_REF + 16 * 4;
 // by tile n % 3: FULL and EMPTY (K's ring, V's ring), SFULL, MDONE, PFULL, ODONE; by n % 2: RDY (K's f16 tiles,
 // V's); by n % 8: REF (K's, V's)
@@ -175,6 +177,11 @@ constexpr uint32_t kSmemBytes = SM_FAILED + 4 + 1024;  // + slack to align the b
 static_assert(kSmemBytes <= 232448 && SM_RING % 128 == 0 && SM_X % 16 == 0 && SM_BAR % 8 == 0, "shared memory of one sm_103 CTA");
 constexpr uint32_t TM_S = 0, TM_O = 384, kTmemCols = 512;  // three score (then P) buffers, the accumulator
 constexpr int kRefField = 23, kMaxField = 26;  // f16 exponent field of 2^(e - R + 8), and its cut (all-zero blocks)
+constexpr int kWindow = kRefField - 1;         // blocks from R - kWindow on are held
+// V's reference follows a tile down to 2^-40 of the segment's highest: the accumulator, at most 2^52 (weights of 2^16, values
+// of 2^14, 2^22 keys) in the highest one's units, stays within fp32.
+constexpr int kFollow = 40;
+constexpr int kLow = 256;                      // beside a tile's reference: the tile has blocks below the window
 // A row's weights are 2^(s - m) with m set kLift below a maximum, so that f16 holds those down to 2^-32 of the largest
 // (2^-24 of it would lose a key's weight where half a million of them still count).
 constexpr float kLift = 8.f;
@@ -264,10 +271,10 @@ __device__ __forceinline__ int tile_live(const MxExpertParams& p, int j) {
 }
 
 // ---------------------------------------------------------------------------------- loads
-// The largest scale of a block that holds a code other than zero, over the tile's live rows (the whole warp's result;
-// lane: rows lane, lane + 32, .., each row's four blocks at once).
-__device__ __noinline__ int top_nonzero(uint32_t tile, int lane, int live) {
-  uint32_t top = 0;
+// The largest and the smallest scale of the blocks that hold a code other than zero, over the tile's live rows: 0 and 255 if
+// there are none (the whole warp's result; lane: rows lane, lane + 32, .., each row's four blocks at once).
+__device__ __noinline__ int2 nonzero_scales(uint32_t tile, int lane, int live) {
+  uint32_t top = 0, low = 255;
 #pragma unroll 1
   for (int r = lane; r < live; r += 32) {
     uint4 c[4];
@@ -276,10 +283,14 @@ __device__ __noinline__ int top_nonzero(uint32_t tile, int lane, int live) {
 #pragma unroll
     for (int b = 0; b < 4; ++b) c[b] = ld_shared_v4(tile + r * kMxRowBytes + (((b + (r >> 1)) & 3) << 4));
 #pragma unroll
-    for (int b = 0; b < 4; ++b)
-      if (((c[b].x | c[b].y | c[b].z | c[b].w) & 0x77777777u) != 0u) top = max(top, (sc >> (8 * ((b + (r >> 1)) & 3))) & 255u);
+    for (int b = 0; b < 4; ++b) {
+      const bool some = ((c[b].x | c[b].y | c[b].z | c[b].w) & 0x77777777u) != 0u;
+      const uint32_t e = (sc >> (8 * ((b + (r >> 1)) & 3))) & 255u;
+      top = max(top, some ? e : 0u);
+      low = min(low, some ? e : 255u);
+    }
   }
-  return static_cast<int>(__reduce_max_sync(0xffffffffu, top));
+  return make_int2(static_cast<int>(__reduce_max_sync(0xffffffffu, top)), static_cast<int>(__reduce_min_sync(0xffffffffu, low)));
 }
 
 // One warp each for K (kv = 0) and V (kv = 1): loads the tiles, and one tile ahead of the converters looks
@@ -294,7 +305,7 @@ __device__ __forceinline__ void producer(const MxExpertParams& p, const Ctx cx) 
   const int total = static_cast<int>(cx.end - cx.start);
   const uint64_t pol = l2_policy_evict_first();
   Seg l = first_seg(cx.start, cx.end, p.T), v = l;  // of the next tile to load, and of the next to look at
-  int lj = l.j0, vj = v.j0, ref = 0, ln = 0;
+  int lj = l.j0, vj = v.j0, ref = 0, peak = 0, ln = 0;
   const uint8_t *codes = nullptr, *scales = nullptr;  // of the next tile to load
   bool jump = true;                                   // they are to be formed anew
   Ring3 at, look;                                     // the places of the two tiles
@@ -335,21 +346,28 @@ __device__ __forceinline__ void producer(const MxExpertParams& p, const Ctx cx) 
     if (vn < 0) continue;
     ok = cx.wait(kFull + look.b, look.par, kErrProducerWait);
     if (!ok) break;
-    if (vj == v.j0) ref = 0;  // a segment starts: references of its own
+    if (vj == v.j0) ref = peak = 0;  // a segment starts: references of its own
     const int live = tile_live(p, vj);
     const uint32_t tile = ring + look.b * kStageBytes;
     const uint4 sc = ld_shared_v4(tile + kCodes + 16 * lane);  // of four rows
-    const uint32_t a = __vmaxu2(__vmaxu2(sc.x & 0x00FF00FFu, sc.y & 0x00FF00FFu), __vmaxu2(sc.z & 0x00FF00FFu, sc.w & 0x00FF00FFu));
-    const uint32_t b = __vmaxu2(__vmaxu2((sc.x >> 8) & 0x00FF00FFu, (sc.y >> 8) & 0x00FF00FFu),
-                                __vmaxu2((sc.z >> 8) & 0x00FF00FFu, (sc.w >> 8) & 0x00FF00FFu));
-    const uint32_t m = __vmaxu2(a, b);
-    const int high = 4 * lane >= live ? 0 : 4 * lane + 3 >= live ? 255 : static_cast<int>(max(m & 0xFFFFu, m >> 16));
-    if (__any_sync(0xffffffffu, high > ref + (kMaxField - kRefField))) {  // (a ragged end is always looked at closely)
-      const int top = top_nonzero(tile, lane, live);
-      if (top > ref + (kMaxField - kRefField)) ref = top;
+    const uint32_t e0 = sc.x & 0x00FF00FFu, e1 = sc.y & 0x00FF00FFu, e2 = sc.z & 0x00FF00FFu, e3 = sc.w & 0x00FF00FFu;
+    const uint32_t f0 = (sc.x >> 8) & 0x00FF00FFu, f1 = (sc.y >> 8) & 0x00FF00FFu, f2 = (sc.z >> 8) & 0x00FF00FFu,
+                   f3 = (sc.w >> 8) & 0x00FF00FFu;
+    const uint32_t m = __vimax3_u16x2(__vimax3_u16x2(e0, e1, e2), __vimax3_u16x2(e3, f0, f1), __vmaxu2(f2, f3));
+    const uint32_t w = __vimin3_u16x2(__vimin3_u16x2(e0, e1, e2), __vimin3_u16x2(e3, f0, f1), __vminu2(f2, f3));
+    const bool dead = 4 * lane >= live, ragged = 4 * lane + 3 >= live;  // (a ragged end is always looked at closely)
+    const int high = dead ? 0 : ragged ? 255 : static_cast<int>(max(m & 0xFFFFu, m >> 16));
+    const int deep = ragged ? 255 : static_cast<int>(min(w & 0xFFFFu, w >> 16));
+    int low = 0;
+    if (__any_sync(0xffffffffu, high > ref + (kMaxField - kRefField) || deep < ref - kWindow)) {
+      const int2 t = nonzero_scales(tile, lane, live);
+      if (t.x > ref + (kMaxField - kRefField)) ref = t.x;
+      else if (t.y < ref - kWindow) ref = kv ? max(t.x, peak - kFollow) : t.x;
+      peak = max(peak, ref);
+      if (t.y < ref - kWindow) low = kLow;
     }
     if (lane == 0) {
-      refs[vn & 7] = ref;
+      refs[vn & 7] = ref | low;
       mbar_arrive(cx.bar(B_REF + 8 * kv + (vn & 7)));
     }
     look.step();
@@ -398,7 +416,7 @@ __device__ __forceinline__ void converter(const MxExpertParams& p, const Ctx cx,
       const uint32_t slot = r.b * kStageBytes, tile = (n & 1) * kTile;
       uint32_t sc;
       asm volatile("ld.shared.u32 %0, [%1];" : "=r"(sc) : "r"(scale_at + slot) : "memory");
-      const uint32_t add = static_cast<uint32_t>((kRefField - refs[n & 7]) & 0xFFFF) * 0x10001u;
+      const uint32_t add = static_cast<uint32_t>((kRefField - (refs[n & 7] & 255)) & 0xFFFF) * 0x10001u;
       const uint32_t cut = row < tile_live(p, j) ? kMaxField * 0x10001u : 0u;
       const uint32_t f02 = __viaddmin_s16x2_relu(sc & 0x00FF00FFu, add, cut) << 10;         // blocks 0 and 2
       const uint32_t f13 = __viaddmin_s16x2_relu((sc >> 8) & 0x00FF00FFu, add, cut) << 10;  // blocks 1 and 3
@@ -499,6 +517,7 @@ __device__ __forceinline__ void pv_issuer(const MxExpertParams& p, const Ctx cx)
   constexpr uint32_t kIdesc = umma_idesc_f16(128, 128, false, false, true);
   const uint64_t vd = kDescMN | ((cx.sbase + SM_V) >> 4);
   auto wait = [&](int b, uint32_t parity) -> bool { return cx.wait(b, parity, kErrMmaWait); };
+  const volatile int* refs = reinterpret_cast<const volatile int*>(cx.smem + SM_REF) + 8;
   uint32_t n = 0, b3 = 0, par = 0, seg = 0;
   bool ok = true;
 #pragma unroll 1
@@ -510,7 +529,8 @@ __device__ __forceinline__ void pv_issuer(const MxExpertParams& p, const Ctx cx)
       if (!ok) break;
       tc_fence_after();
       const uint64_t v0 = vd + (n & 1) * (kTile >> 4);
-      const uint32_t a = TM_S + b3 * 128, more = j > s.j0;
+      // (the accumulator of a segment's first tile may hold what its low blocks give)
+      const uint32_t a = TM_S + b3 * 128, more = j > s.j0 || refs[n & 7] >= kLow;
       const bool own = j >= p.n_main;  // the own tile has 64 keys
       if (elect_one()) {
 #pragma unroll
@@ -579,6 +599,123 @@ __device__ __noinline__ void mask_scores(uint32_t addr, int live, int cols) {
   tmem_wait_st();
 }
 
+// One column, of this warp's 32 lanes.
+__device__ __forceinline__ uint32_t tmem_ld1(uint32_t addr) {
+  uint32_t v;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  tmem_wait_ld();
+  asm volatile("" : "+r"(v) : : "memory");
+  return v;
+}
+__device__ __forceinline__ void tmem_st1(uint32_t addr, uint32_t v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(addr), "r"(v) : "memory");
+}
+// x 2^d for d <= 127, in two steps: the power alone may leave fp32's range
+__device__ __forceinline__ float times_pow2(float x, int d) {
+  return x * mx_pow2(max(d, -126)) * mx_pow2(max(min(d + 126, 0), -126));
+}
+// The rows of K (kv = 0) or V of a tile in the cache.
+struct TileRows {
+  const uint8_t *codes, *scales;
+};
+__device__ __forceinline__ TileRows tile_rows(const MxExpertParams& p, int kv, int u, int j) {
+  const MxAttnLayer& L = p.layer[u / kHkv];
+  const size_t row = static_cast<size_t>(u % kHkv) * p.Smax + tile_row0(p, j);
+  return {(kv ? L.vc : L.kc) + row * kMxRowBytes, (kv ? L.vs : L.ks) + row * kMxRowScales};
+}
+// Block b of a tile's row, if it is below the window of reference ref and not all zeros: its scale, else -1 (the same for
+// a whole warp).
+__device__ __forceinline__ int low_block(const TileRows& t, int row, int b, int ref, uint4& c) {
+  const int e = t.scales[row * kMxRowScales + b];
+  if (e >= ref - kWindow) return -1;
+  c = *reinterpret_cast<const uint4*>(t.codes + row * kMxRowBytes + 16 * b);
+  return ((c.x | c.y | c.z | c.w) & 0x77777777u) != 0u ? e : -1;
+}
+
+// Adds to a tile's scores what its blocks of K below the window give, in the scores' unit 2^(ref - 8); r: this thread's row
+// of the unit's q tile.
+__device__ __noinline__ void low_scores(const MxExpertParams& p, uint32_t addr, int u, int j, int ref, int r) {
+  const TileRows t = tile_rows(p, 0, u, j);
+  const uint8_t* q = p.q_ws + static_cast<size_t>(u) * kQTileBytes;
+  const int live = tile_live(p, j);
+#pragma unroll 1
+  for (int key = 0; key < live; ++key) {
+    float add = 0.f;
+    bool any = false;
+#pragma unroll 1
+    for (int b = 0; b < 4; ++b) {
+      uint4 c;
+      const int e = low_block(t, key, b, ref, c);
+      if (e < 0) continue;
+      any = true;
+      const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+      float dot = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float x[8];
+        mx_values8(w[k], 1.f, x);
+        const uint4 v = *reinterpret_cast<const uint4*>(q + swz_off(r, 4 * b + k, kQTileBytes / 2));
+        const uint32_t h[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = unpack_f16x2(h[i]);
+          dot = fmaf(f.x, x[2 * i], fmaf(f.y, x[2 * i + 1], dot));
+        }
+      }
+      add += times_pow2(dot, e - ref + kRefField - 15);
+    }
+    if (any) tmem_st1(addr + key, __float_as_uint(__uint_as_float(tmem_ld1(addr + key)) + add));
+  }
+  tmem_wait_st();
+}
+
+// Adds to the accumulator what a tile's blocks of V below the window give with its weights P, in the accumulator's unit
+// 2^(ref - 8); fresh: to zero.
+__device__ __noinline__ void low_values(const MxExpertParams& p, uint32_t oa, uint32_t pa, int u, int j, int ref, bool fresh) {
+  const TileRows t = tile_rows(p, 1, u, j);
+  const int live = tile_live(p, j);
+#pragma unroll 1
+  for (int b = 0; b < 4; ++b) {
+    float acc[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) acc[i] = 0.f;
+    bool any = fresh;
+#pragma unroll 1
+    for (int key = 0; key < live; ++key) {
+      uint4 c;
+      const int e = low_block(t, key, b, ref, c);
+      if (e < 0) continue;
+      any = true;
+      const float2 pp = unpack_f16x2(tmem_ld1(pa + (key >> 1)));
+      const float f = times_pow2(key & 1 ? pp.y : pp.x, e - ref + kRefField - 15);
+      const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float x[8];
+        mx_values8(w[k], 1.f, x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[8 * k + i] = fmaf(f, x[i], acc[8 * k + i]);
+      }
+    }
+    if (!any) continue;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint32_t o[8];
+      if (!fresh) {
+        tmem_ld8(oa + 32 * b + 8 * k, o);
+        tmem_wait_ld();
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        asm volatile("" : "+r"(o[i]) : : "memory");
+        o[i] = __float_as_uint((fresh ? 0.f : __uint_as_float(o[i])) + acc[8 * k + i]);
+      }
+      tmem_st8(oa + 32 * b + 8 * k, o);
+    }
+  }
+  tmem_wait_st();
+}
+
 __device__ __forceinline__ void softmax_warps(const MxExpertParams& p, const Ctx cx) {
   const int k = threadIdx.x >> 7, r = threadIdx.x & 127;
   const uint32_t lane = static_cast<uint32_t>(r & ~31) << 16;
@@ -605,14 +742,17 @@ __device__ __forceinline__ void softmax_warps(const MxExpertParams& p, const Ctx
       tc_fence_after();
       const uint32_t sa = cx.tmem + lane + TM_S + rn.b * 128;
       // (never 0, as the product of a small query's factor and a small reference can be: a masked score is -inf)
-      const float ct = fmaxf(qf * mx_scale(refs[n & 7]), 0x1p-126f);
-      // what V's reference, if it rose from the tile before (in the same segment) to this one, makes of the accumulator
+      const int kr = refs[n & 7];
+      const float ct = fmaxf(qf * mx_scale(kr & 255), 0x1p-126f);
+      // what V's reference, if it moved from the tile before (in the same segment) to this one, makes of the accumulator
+      const int vr = refs[8 + (n & 7)];
       float scale = 1.f;
       if (i > 0) {
-        const int d = refs[8 + ((n - 1) & 7)] - refs[8 + (n & 7)];
+        const int d = (refs[8 + ((n - 1) & 7)] & 255) - (vr & 255);
         if (d != 0) scale = d < -126 ? 0.f : mx_pow2(d);
       }
       const int live = tile_live(p, j), chunks = j < p.n_main ? 4 : 2;
+      if (kr >= kLow) low_scores(p, sa, s.u, j, kr & 255, r);
       if (live < 32 * chunks) mask_scores(sa, live, 32 * chunks);
       // (the other warpgroups' first tiles of a segment start from its first tile's maximum: their own would seldom do)
       if (i > 0 && i < kSoftWg) {
@@ -686,11 +826,14 @@ __device__ __forceinline__ void softmax_warps(const MxExpertParams& p, const Ctx
         *run = m;
       }
       mbar_arrive(cx.bar(B_MDONE + rn.b));
-      if (__any_sync(0xffffffffu, scale != 1.f)) {  // the accumulator moves: stable once PV(n-1) is done
-        ok = wait3(B_ODONE, rn.back(1));
+      const bool moves = __any_sync(0xffffffffu, scale != 1.f);
+      if (moves || vr >= kLow) {  // the accumulator changes: stable once PV(n-1) is done, or the segment before is read
+        if (i > 0) ok = wait3(B_ODONE, rn.back(1));
+        else if (seg > 0) ok = cx.wait(B_OFREE, (seg - 1) & 1, kErrSoftmaxWait);
         if (!ok) break;
         tc_fence_after();
-        scale_accumulator(oa, scale);
+        if (moves) scale_accumulator(oa, scale);
+        if (vr >= kLow) low_values(p, oa, sa, s.u, j, vr & 255, i == 0);
       }
       tc_fence_before();
       mbar_arrive(cx.bar(B_PFULL + rn.b));
@@ -712,35 +855,15 @@ __device__ __forceinline__ void softmax_warps(const MxExpertParams& p, const Ctx
       for (int w = 0; w < kSoftWg; ++w) L += ex2_approx(xch[w * kRows + r].x - M) * xch[w * kRows + r].y;
       // O is in units of 2^(R - 127 - 8): a value is o * inv * f
       const float inv = 1.0f / L * 0.00390625f;
-      const int rv = refs[8 + (last & 7)], l = s.u / kHkv, g = s.u % kHkv;
+      const int rv = refs[8 + (last & 7)] & 255, l = s.u / kHkv, g = s.u % kHkv;
       const bool full = s.j0 == 0 && s.j1 == p.T;
       const uint32_t col = oa + 64 * k;
-      float f = mx_scale(rv);
-      uint4* dst;
-      size_t step = 1;
-      if (full) {
-        dst = reinterpret_cast<uint4*>(p.layer[l].out + (static_cast<size_t>(g) * kRows + r) * kD + 64 * k);
-      } else {
-        // a part: f16, the half row times the power of two that puts its largest magnitude in [2^14, 2^15)
-        const size_t sl = static_cast<size_t>(blockIdx.x) * 2 + (base == 0 ? 0 : 1);
-        float amax = 0.f;
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          uint32_t v[32];
-          tmem_ld32(col + 32 * h, v);
-          tmem_wait_ld();
-          reg_fence32(v);
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) amax = fmax3(amax, fabsf(__uint_as_float(v[e])), fabsf(__uint_as_float(v[e + 1])));
-        }
-        amax = amax * inv * f;
-        const int ex = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 14, -126), 112);
-        if (rv != 255) f = mx_pow2(min(max(rv - 127 - ex, -126), 127));
-        dst = p.part_o + (sl * kPartChunks + 8 * k) * kRows + r;
-        step = kRows;
-        p.part_lse[(sl * 3 + 1 + k) * kRows + r] = mx_pow2(ex);
-        if (k == 0) p.part_lse[sl * 3 * kRows + r] = M + log2f(L);
-      }
+      const float f = mx_scale(rv);
+      const size_t sl = static_cast<size_t>(blockIdx.x) * 2 + (base == 0 ? 0 : 1);
+      uint4* dst = full ? reinterpret_cast<uint4*>(p.layer[l].out + (static_cast<size_t>(g) * kRows + r) * kD + 64 * k)
+                        : p.part_o + (sl * kPartChunks + 8 * k) * kRows + r;
+      const size_t step = full ? 1 : kRows;
+      if (!full && k == 0) p.part_lse[sl * kMxPartRows * kRows + r] = M + log2f(L);
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
         uint32_t v[32], pk[16];
@@ -751,9 +874,22 @@ __device__ __forceinline__ void softmax_warps(const MxExpertParams& p, const Ctx
           tc_fence_before();
           mbar_arrive(cx.bar(B_OFREE));  // the accumulator is read
         }
+        float up = 1.f;
+        if (!full) {
+          // a part: f16 (11 bits: the bf16 output has 8), the 32 channels times the power of two that puts their largest
+          // magnitude in [2^14, 2^15)
+          float mx[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int e = 0; e < 32; e += 2)
+            mx[(e >> 1) & 3] = fmax3(mx[(e >> 1) & 3], fabsf(__uint_as_float(v[e])), fabsf(__uint_as_float(v[e + 1])));
+          const float amax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * inv * f;
+          const int ex = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 14, -126), 112);
+          up = mx_pow2(-ex);
+          p.part_lse[(sl * kMxPartRows + 1 + 2 * k + h) * kRows + r] = mx_pow2(ex);
+        }
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const float x = __uint_as_float(v[2 * e]) * inv * f, y = __uint_as_float(v[2 * e + 1]) * inv * f;
+          const float x = __uint_as_float(v[2 * e]) * inv * f * up, y = __uint_as_float(v[2 * e + 1]) * inv * f * up;
           pk[e] = full ? pack_bf16x2(x, y) : pack_f16x2(x, y);
         }
 #pragma unroll
@@ -820,8 +956,8 @@ __global__ void __launch_bounds__(kRows) mxfp4_merge_kernel(const __grid_constan
   pdl_launch_dependents();
   const SplitUnit su = p.split[blockIdx.x];
   __nv_bfloat16* out = p.out[su.u / kHkv];
-  if (su.nparts == 2) merge_row_chunk<2>(p.part_o, p.part_lse, su, blockIdx.y, threadIdx.x, out);
-  else merge_row_chunk<20>(p.part_o, p.part_lse, su, blockIdx.y, threadIdx.x, out);
+  if (su.nparts == 2) merge_row_chunk<2, kD / 32>(p.part_o, p.part_lse, su, blockIdx.y, threadIdx.x, out);
+  else merge_row_chunk<20, kD / 32>(p.part_o, p.part_lse, su, blockIdx.y, threadIdx.x, out);
 }
 
 cudaError_t mxfp4_attention_set_attributes() {

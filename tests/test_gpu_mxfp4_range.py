@@ -48,3 +48,80 @@ def test_small_queries_over_zero_keys(form, n, size):
     x["q_raw"] = (x["q_raw"].float() * size).to(torch.bfloat16)
     v = np.random.default_rng(n).standard_normal((8, 512, 128))
     run(form, x, HostCache(np.zeros_like(v), v, n), n, 0, 1)
+
+
+WIDE = ["expert"]
+
+
+def one_sided(seed, hq, tok):
+    """Queries that all point the same way in channels 63 and 127 (which hardly rotate at positions 0 to 63)."""
+    x = step_inputs(seed, hq, tok)
+    q = 0.25 * x["q_raw"].float()
+    q[..., 63] = q[..., 127] = 1.0
+    x["q_raw"] = q.to(torch.bfloat16)
+    return x
+
+
+@pytest.mark.parametrize("form", WIDE)
+@pytest.mark.parametrize("layers", [1, 20])
+@pytest.mark.parametrize("steps", [(0, -8, -16, -24), (45, 15, -15, -45), (-30, 0, -2, -32), (60, -60, 0, 0)])
+def test_values_of_blocks_far_apart(form, layers, steps):
+    _, _, _, hq, tok = FORMS[form]
+    x = step_inputs(17, hq, tok)
+    k, v = np.random.default_rng(17).standard_normal((2, 8, 896, 128))
+    by = np.exp2(steps).repeat(32)
+    v *= by
+    x["v_raw"] = (x["v_raw"].float() * torch.from_numpy(by)).to(torch.bfloat16)
+    run(form, x, HostCache(k, v, 700), 700, 0, layers)
+
+
+@pytest.mark.parametrize("form", WIDE)
+@pytest.mark.parametrize("layers", [1, 20])
+@pytest.mark.parametrize("at", [0, 333, 699])
+@pytest.mark.parametrize("by", [30, 60, 100])
+def test_large_value_without_weight(form, layers, at, by):
+    """A row whose values are 2^by above the others', at a key that no query looks at."""
+    _, _, _, hq, tok = FORMS[form]
+    x = one_sided(at, hq, tok)
+    k, v = np.random.default_rng(at + by).standard_normal((2, 8, 896, 128))
+    k[:, at, [63, 127]] = -512.0
+    v[:, at] *= 2.0 ** by
+    run(form, x, HostCache(k, v, 700), 700, -700, layers)
+
+
+@pytest.mark.parametrize("form", WIDE)
+@pytest.mark.parametrize("layers", [1, 20])
+def test_values_spread_at_random(form, layers):
+    _, _, _, hq, tok = FORMS[form]
+    x = step_inputs(23, hq, tok)
+    rng = np.random.default_rng(23)
+    k, v = rng.standard_normal((2, 8, 896, 128))
+    v *= np.exp2(rng.integers(-60, 1, (8, 896, 4)) + np.array([0, -20, 30, 7])).repeat(32, -1)
+    run(form, x, HostCache(k, v, 700), 700, 0, layers)
+
+
+@pytest.mark.parametrize("form", WIDE)
+@pytest.mark.parametrize("layers", [1, 20])
+@pytest.mark.parametrize("by", [26, 50, 90])
+def test_keys_of_blocks_far_apart(form, layers, by):
+    """Blocks 0 and 2 of the keys 2^by above blocks 1 and 3, in channels where the queries are zero."""
+    _, _, _, hq, tok = FORMS[form]
+    x = step_inputs(29, hq, tok)
+    x["q_gamma"][0:32] = x["q_gamma"][64:96] = 0.0
+    k, v = np.random.default_rng(29).standard_normal((2, 8, 896, 128))
+    k[..., 0:32] *= 2.0 ** by
+    k[..., 64:96] *= 2.0 ** by
+    x["k_gamma"][0:32] = x["k_gamma"][64:96] = 2.0 ** by
+    run(form, x, HostCache(k, v, 700), 700, 0, layers)
+
+
+@pytest.mark.parametrize("form", WIDE)
+@pytest.mark.parametrize("layers", [1, 20])
+@pytest.mark.parametrize("at", [0, 333, 699])
+@pytest.mark.parametrize("by", [26, 60])
+def test_large_key_against_every_query(form, layers, at, by):
+    _, _, _, hq, tok = FORMS[form]
+    x = one_sided(at, hq, tok)
+    k, v = np.random.default_rng(at).standard_normal((2, 8, 896, 128))
+    k[:, at, [63, 127]] = -2.0 ** by
+    run(form, x, HostCache(k, v, 700), 700, -700, layers)
