@@ -20,9 +20,10 @@
 //      that V^T (A = 16 channels, K = 16 keys) needs. V's scales go into P instead, once per block of
 //      channels: 8 products of f16 pairs a step in place of 32.
 // P 2^(ev - R) is held in f16: R is a running reference of the warp, the largest scale of a block that
-// is not all zeros (as of the last time it was exceeded by 2^3), put at 2^8, so that weights times
-// scales keep 11 bits down to 2^-22 of the largest. m is raised only when a score passes it by
-// 4 (P <= 2^4), so that both rescalings are rare.
+// is not all zeros (as of the last time it was exceeded by 2^3), put at 2^8. A block 2^23 or more below R
+// has no f16 factor: a chunk that holds such blocks goes over them again, at a reference of their own, and adds
+// what they give in fp32 (such a chunk takes about three times as long). m is raised only when a score passes
+// it by 4 (P <= 2^4), so that both rescalings are rare.
 //
 // Work decomposition: the units' keys in chunks of 32, unit-major, one contiguous range per CTA; a CTA's
 // twelve compute warps take its chunks in turn (64 layers at pos 4700: 79 us with eight). Where a unit ends a
@@ -74,6 +75,7 @@ static_assert(kStageBytes % 128 == 0 && SM_FACT % 16 == 0 && SM_PART % 16 == 0 &
 // P 2^(ev - R): a block at the reference has factor 2^8 (f16 exponent field 23); fields above 26 only
 // occur for all-zero blocks and are cut there, so that P <= 2^4 times the factor stays finite.
 constexpr int kRefField = 23, kMaxField = 26;
+constexpr int kWindow = kRefField - 1;  // blocks from R - kWindow on have a factor
 constexpr float kLazy = 4.0f;
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, int bytes) {
@@ -294,24 +296,93 @@ __device__ __forceinline__ void raise_max(Warp& w, float x0, float x1) {
   }
 }
 
-// Some scale of the chunk is far above the reference: raises the reference to the largest scale of a
-// block that has a code other than zero (lane = key), if that is the case for such a block.
-__device__ __forceinline__ void raise_ref(Warp& w, uint32_t st, int lane) {
+// Words of ldmatrix.trans of V's codes: f16 pairs of channels 4g + {0, 2} (he) and {1, 3} (ho), keys (2t, 2t + 1), then
+// (2t + 8, 2t + 9).
+__device__ __forceinline__ void value_pairs(uint32_t r0, uint32_t r1, uint32_t (&he)[4], uint32_t (&ho)[4]) {
+  const uint32_t lo = __byte_perm(r0, r1, 0x5410), hi = __byte_perm(r0, r1, 0x7632);
+  mx_unpack8(select_bits(lo, times16(hi), 0x0F0F0F0Fu), he);
+  mx_unpack8(select_bits(lo >> 4, hi, 0x0F0F0F0Fu), ho);
+}
+
+// The largest (kTop) or smallest scale of the chunk's V blocks that have a code other than zero, of those below `below`;
+// -1, or 255, if there is none (lane = key; the whole warp's result).
+template <bool kTop>
+__device__ __forceinline__ int nonzero_scale(uint32_t st, int lane, int below) {
   const uint32_t sc = ld_shared_u32(st + 2 * kCodes + kScales + 4 * lane);
-  uint32_t top = 0;
+  int r = kTop ? -1 : 255;
 #pragma unroll
   for (int b = 0; b < 4; ++b) {
     const uint4 c = ld_shared_v4(st + kCodes + lane * kMxRowBytes + ((b ^ ((lane >> 1) & 3)) << 4));
-    if (((c.x | c.y | c.z | c.w) & 0x77777777u) != 0u) top = max(top, (sc >> (8 * b)) & 255u);
+    const int e = (sc >> (8 * b)) & 255;
+    if (((c.x | c.y | c.z | c.w) & 0x77777777u) != 0u && e < below) r = kTop ? max(r, e) : min(r, e);
   }
-  const int t = static_cast<int>(__reduce_max_sync(0xffffffffu, top));
-  if (t <= w.ref + (kMaxField - kRefField)) return;
-  const float a = w.ref - t < -126 ? 0.f : mx_pow2(w.ref - t);
-  w.ref = t;
+  return kTop ? __reduce_max_sync(0xffffffffu, r) : __reduce_min_sync(0xffffffffu, r);
+}
+
+// Some scale of the chunk is far from the reference: raises the reference to the largest scale of a block that has a code
+// other than zero, if that is far above it; whether such a block lies below the reference's window.
+__device__ __forceinline__ bool look_at_scales(Warp& w, uint32_t st, int lane) {
+  const int t = nonzero_scale<true>(st, lane, 256);
+  if (t > w.ref + (kMaxField - kRefField)) {
+    const float a = w.ref - t < -126 ? 0.f : mx_pow2(w.ref - t);
+    w.ref = t;
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 8; ++i)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) w.o[i][k] *= a;
+      for (int k = 0; k < 4; ++k) w.o[i][k] *= a;
+  }
+  return nonzero_scale<false>(st, lane, 256) < w.ref - kWindow;
+}
+
+// Writes the factors of the chunk's V blocks whose scale is below `below`, at a reference of their own: the largest such
+// scale, which it returns (-1: there is none).
+__device__ __forceinline__ int low_factors(uint32_t st, uint32_t fact, int lane, int below) {
+  const int top = nonzero_scale<true>(st, lane, below);
+  const uint32_t vs = ld_shared_u32(st + 2 * kCodes + kScales + 4 * lane);
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const int e = (vs >> (8 * b)) & 255, field = e < below ? min(max(e - top + kRefField, 0), kMaxField) : 0;
+    st_shared_u16(fact + 512 + 16 * (lane >> 1) + 4 * b + 2 * (lane & 1), static_cast<uint16_t>(field << 10));
+  }
+  __syncwarp();
+  return top;
+}
+
+// The V blocks below the reference's window (their factors were 0), window by window, each from zero and added in fp32.
+// pb: the weights of both 16-key steps; a0, a1: as in chunk(). (A function of its own, on a copy of the accumulators: in
+// line it costs the chunks that do not need it 5 %.)
+__device__ __noinline__ void low_values(float* o, int ref, uint4 pb, uint32_t st, uint32_t fact, uint32_t a0, uint32_t a1) {
+  const int lane = threadIdx.x & 31, t = lane & 3;
+  int below = ref - kWindow;
+#pragma unroll 1
+  for (;;) {
+    __syncwarp();
+    const int top = low_factors(st, fact, lane, below);
+    if (top < 0) return;
+    const float down = top - ref < -126 ? 0.f : mx_pow2(top - ref);
+#pragma unroll 1
+    for (int a = 0; a < 2; ++a) {
+      const uint4 ua = ld_shared_v4(fact + 512 + 16 * (8 * a + t)), ub = ld_shared_v4(fact + 512 + 16 * (8 * a + t + 4));
+      const uint32_t fa[4] = {ua.x, ua.y, ua.z, ua.w}, fb[4] = {ub.x, ub.y, ub.z, ub.w};
+      uint32_t r[8];
+      ldm4t(a0 + kCodes + a * 16 * kMxRowBytes, *reinterpret_cast<uint32_t(*)[4]>(r));
+      ldm4t(a1 + kCodes + a * 16 * kMxRowBytes, *reinterpret_cast<uint32_t(*)[4]>(r + 4));
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const uint32_t q0 = hmul2(a ? pb.z : pb.x, fa[b]), q1 = hmul2(a ? pb.w : pb.y, fb[b]);
+        uint32_t he[4], ho[4];
+        value_pairs(r[2 * b], r[2 * b + 1], he, ho);
+        float d[2][4];
+        mma16816_first(d[0], {he[0], ho[0], he[2], ho[2]}, q0, q1);
+        mma16816_first(d[1], {he[1], ho[1], he[3], ho[3]}, q0, q1);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[8 * b + 4 * h + k] = fmaf(down, d[h][k], o[8 * b + 4 * h + k]);
+      }
+    }
+    below = top - kWindow;
+  }
 }
 
 // `fact`: the warp's 768 bytes for the chunk's factors; `live`: the chunk's keys from here on are masked
@@ -340,6 +411,7 @@ __device__ __forceinline__ void chunk(Warp& w, const uint32_t (&q)[4][4], const 
                  (ks >> 1) & 0x7F800000u);
     __syncwarp();
   }
+  bool low = false;
   float x[2][4];  // [16 keys][key g: heads 2t, 2t+1; key g + 8: the same]
 #pragma unroll
   for (int a = 0; a < 2; ++a) {
@@ -362,9 +434,10 @@ __device__ __forceinline__ void chunk(Warp& w, const uint32_t (&q)[4][4], const 
     }
     if (a == 0) {  // (here, while the products run)
       const uint32_t vs = ld_shared_u32(st + 2 * kCodes + kScales + 4 * lane);
-      const uint32_t v02 = vs & 0x00FF00FFu, v13 = (vs >> 8) & 0x00FF00FFu, top = __vmaxu2(v02, v13);
-      if (__any_sync(0xffffffffu, static_cast<int>(max(top & 0xFFFFu, top >> 16)) > w.ref + (kMaxField - kRefField)))
-        raise_ref(w, st, lane);
+      const uint32_t v02 = vs & 0x00FF00FFu, v13 = (vs >> 8) & 0x00FF00FFu, top = __vmaxu2(v02, v13), end = __vminu2(v02, v13);
+      if (__any_sync(0xffffffffu, static_cast<int>(max(top & 0xFFFFu, top >> 16)) > w.ref + (kMaxField - kRefField) ||
+                                      static_cast<int>(min(end & 0xFFFFu, end >> 16)) < w.ref - kWindow))
+        low = look_at_scales(w, st, lane);
       const uint32_t add = static_cast<uint32_t>((kRefField - w.ref) & 0xFFFF) * 0x10001u;
       const uint32_t f02 = __viaddmin_s16x2_relu(v02, add, kMaxField * 0x10001u) << 10;
       const uint32_t f13 = __viaddmin_s16x2_relu(v13, add, kMaxField * 0x10001u) << 10;
@@ -390,16 +463,18 @@ __device__ __forceinline__ void chunk(Warp& w, const uint32_t (&q)[4][4], const 
   const float mx0 = fmax3(fmaxf(x[0][0], x[0][2]), x[1][0], x[1][2]);
   const float mx1 = fmax3(fmaxf(x[0][1], x[0][3]), x[1][1], x[1][3]);
   if (__any_sync(0xffffffffu, mx0 > w.m[0] + kLazy || mx1 > w.m[1] + kLazy)) raise_max(w, mx0, mx1);
+  uint32_t pb[2][2];
 #pragma unroll
-  for (int a = 0; a < 2; ++a) {
-    uint32_t pb[2];
+  for (int a = 0; a < 2; ++a)
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const float p0 = ex2_approx(x[a][2 * k] - w.m[0]), p1 = ex2_approx(x[a][2 * k + 1] - w.m[1]);
       w.l[0] += p0;
       w.l[1] += p1;
-      pb[k] = transpose8x8(pack_f16x2(p0, p1));  // -> head lane / 4, keys 2t, 2t + 1
+      pb[a][k] = transpose8x8(pack_f16x2(p0, p1));  // -> head lane / 4, keys 2t, 2t + 1
     }
+#pragma unroll
+  for (int a = 0; a < 2; ++a) {
     // V's factors of keys 2t, 2t + 1 and 2t + 8, 2t + 9 of this 16-key step
     const uint4 ua = ld_shared_v4(fact + 512 + 16 * (8 * a + t)), ub = ld_shared_v4(fact + 512 + 16 * (8 * a + t + 4));
     const uint32_t fa[4] = {ua.x, ua.y, ua.z, ua.w}, fb[4] = {ub.x, ub.y, ub.z, ub.w};
@@ -408,15 +483,20 @@ __device__ __forceinline__ void chunk(Warp& w, const uint32_t (&q)[4][4], const 
     ldm4t(a1 + kCodes + a * 16 * kMxRowBytes, *reinterpret_cast<uint32_t(*)[4]>(r + 4));
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
-      const uint32_t q0 = hmul2(pb[0], fa[b]), q1 = hmul2(pb[1], fb[b]);
-      const uint32_t lo = __byte_perm(r[2 * b], r[2 * b + 1], 0x5410), hi = __byte_perm(r[2 * b], r[2 * b + 1], 0x7632);
-      const uint32_t even = select_bits(lo, times16(hi), 0x0F0F0F0Fu), odd = select_bits(lo >> 4, hi, 0x0F0F0F0Fu);
-      uint32_t he[4], ho[4];  // channels 4g + {0, 2} and {1, 3}: keys (2t, 2t+1), then (2t+8, 2t+9)
-      mx_unpack8(even, he);
-      mx_unpack8(odd, ho);
+      const uint32_t q0 = hmul2(pb[a][0], fa[b]), q1 = hmul2(pb[a][1], fb[b]);
+      uint32_t he[4], ho[4];
+      value_pairs(r[2 * b], r[2 * b + 1], he, ho);
       mma16816(w.o[2 * b], {he[0], ho[0], he[2], ho[2]}, q0, q1);
       mma16816(w.o[2 * b + 1], {he[1], ho[1], he[3], ho[3]}, q0, q1);
     }
+  }
+  if (low) {
+    float o[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) o[i] = w.o[i >> 2][i & 3];
+    low_values(o, w.ref, make_uint4(pb[0][0], pb[0][1], pb[1][0], pb[1][1]), st, fact, a0, a1);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) w.o[i >> 2][i & 3] = o[i];
   }
 }
 

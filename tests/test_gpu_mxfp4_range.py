@@ -50,7 +50,7 @@ def test_small_queries_over_zero_keys(form, n, size):
     run(form, x, HostCache(np.zeros_like(v), v, n), n, 0, 1)
 
 
-WIDE = ["expert"]
+WIDE = list(FORMS)
 
 
 def one_sided(seed, hq, tok):
