@@ -19,11 +19,14 @@
 //      exchanging nibbles pairs the two keys in a byte, and cvt gives the f16 pair along the keys
 //      that V^T (A = 16 channels, K = 16 keys) needs. V's scales go into P instead, once per block of
 //      channels: 8 products of f16 pairs a step in place of 32.
-// P 2^(ev - R) is held in f16: R is a running reference of the warp, the largest scale of a block that
-// is not all zeros (as of the last time it was exceeded by 2^3), put at 2^8. A block 2^23 or more below R
-// has no f16 factor: a chunk that holds such blocks goes over them again, at a reference of their own, and adds
-// what they give in fp32 (such a chunk takes about three times as long). m is raised only when a score passes
-// it by 4 (P <= 2^4), so that both rescalings are rare.
+// P 2^(ev - R) is held in f16, as the product of two f16 numbers. m stands 2^8 below a warp's maximum and is raised when a
+// score passes that by 2^4 (so the largest P is 2^8 to 2^12); R is a running reference of the warp, the largest scale of a
+// block that is not all zeros, as of the last time it was exceeded by 2^1, put at 2^2. So a weight keeps 11 bits down to
+// 2^-22 of the largest, its product with a scale down to 2^-24, and a weight that is lost below is at most 2^-33 of the
+// largest (with m at the maximum itself weights below 2^-25 counted as zero: of 350,000 keys, a warp's share of the
+// longest cache, 1 % of the largest). A block more than 2^10 below R is not multiplied so: a chunk that holds such
+// blocks goes over them again, at a reference of their own, and adds what they give in fp32 (it takes about three times
+// as long).
 //
 // Work decomposition: the units' keys in chunks of 32, unit-major, one contiguous range per CTA; a CTA's
 // twelve compute warps take its chunks in turn (64 layers at pos 4700: 79 us with eight). Where a unit ends a
@@ -72,11 +75,12 @@ static_assert(kStageBytes % 128 == 0 && SM_FACT % 16 == 0 && SM_PART % 16 == 0 &
                   SM_QF % 8 == 0 && SM_NEW % 16 == 0 && SM_BAR % 8 == 0,
               "alignment of the vector accesses");
 
-// P 2^(ev - R): a block at the reference has factor 2^8 (f16 exponent field 23); fields above 26 only
-// occur for all-zero blocks and are cut there, so that P <= 2^4 times the factor stays finite.
-constexpr int kRefField = 23, kMaxField = 26;
-constexpr int kWindow = kRefField - 1;  // blocks from R - kWindow on have a factor
-constexpr float kLazy = 4.0f;
+// P 2^(ev - R): P <= 2^(kLift + kLazy); a block at the reference has the factor 2^(kRefField - 15) (f16 exponent fields);
+// fields above kMaxField only occur for all-zero blocks and are cut there.
+constexpr float kLift = 8.0f, kLazy = 4.0f;
+constexpr int kRefField = 17, kMaxField = 18;
+constexpr int kWindow = 10;  // blocks from R - kWindow on are multiplied in f16
+static_assert(kLift + kLazy + kMaxField - 15 <= 15 && kRefField - kWindow >= 1, "products within f16");
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -274,14 +278,14 @@ struct Warp {
   int ref;           // R as a scale byte
 };
 
-// Raises the reference maximum of both heads to the chunk's (x: scores in log2 units).
+// Raises the reference maximum of both heads to 2^kLift below the chunk's (x: scores in log2 units).
 __device__ __forceinline__ void raise_max(Warp& w, float x0, float x1) {
 #pragma unroll
   for (int m = 4; m <= 16; m <<= 1) {
     x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, m));
     x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, m));
   }
-  const float n0 = fmaxf(w.m[0], x0), n1 = fmaxf(w.m[1], x1);
+  const float n0 = fmaxf(w.m[0], x0 - kLift), n1 = fmaxf(w.m[1], x1 - kLift);
   const float a0 = ex2_approx(w.m[0] - n0), a1 = ex2_approx(w.m[1] - n1);
   w.m[0] = n0;
   w.m[1] = n1;
@@ -341,7 +345,7 @@ __device__ __forceinline__ int low_factors(uint32_t st, uint32_t fact, int lane,
   const uint32_t vs = ld_shared_u32(st + 2 * kCodes + kScales + 4 * lane);
 #pragma unroll
   for (int b = 0; b < 4; ++b) {
-    const int e = (vs >> (8 * b)) & 255, field = e < below ? min(max(e - top + kRefField, 0), kMaxField) : 0;
+    const int e = (vs >> (8 * b)) & 255, field = e < below && e >= top - kWindow ? min(e - top + kRefField, kMaxField) : 0;
     st_shared_u16(fact + 512 + 16 * (lane >> 1) + 4 * b + 2 * (lane & 1), static_cast<uint16_t>(field << 10));
   }
   __syncwarp();
@@ -401,7 +405,7 @@ __device__ __forceinline__ void chunk(Warp& w, const uint32_t (&q)[4][4], const 
     ldm4(a1 + a * 16 * kMxRowBytes, *reinterpret_cast<uint32_t(*)[4]>(rk[a] + 4));
   }
   // The scales become factors once per key (lane = key), not once per thread that needs them:
-  // K's four as fp32, at fact + 16 key; V's four as f16 2^(ev - R + 8), the pair of keys 2i and 2i + 1 of
+  // K's four as fp32, at fact + 16 key; V's four as f16 2^(ev - R + 2), the pair of keys 2i and 2i + 1 of
   // block b at fact + 512 + 16 i + 4 b. (With K's codes read before, and V's factors formed between the products: 64
   // layers at pos 4700 65.8 -> 63.7 us, 4 layers at pos 131070 104 -> 98.)
   {
@@ -434,10 +438,17 @@ __device__ __forceinline__ void chunk(Warp& w, const uint32_t (&q)[4][4], const 
     }
     if (a == 0) {  // (here, while the products run)
       const uint32_t vs = ld_shared_u32(st + 2 * kCodes + kScales + 4 * lane);
-      const uint32_t v02 = vs & 0x00FF00FFu, v13 = (vs >> 8) & 0x00FF00FFu, top = __vmaxu2(v02, v13), end = __vminu2(v02, v13);
+      uint32_t v02 = vs & 0x00FF00FFu, v13 = (vs >> 8) & 0x00FF00FFu;
+      const uint32_t top = __vmaxu2(v02, v13), end = __vminu2(v02, v13);
       if (__any_sync(0xffffffffu, static_cast<int>(max(top & 0xFFFFu, top >> 16)) > w.ref + (kMaxField - kRefField) ||
-                                      static_cast<int>(min(end & 0xFFFFu, end >> 16)) < w.ref - kWindow))
+                                      static_cast<int>(min(end & 0xFFFFu, end >> 16)) < w.ref - kWindow)) {
         low = look_at_scales(w, st, lane);
+        if (low) {  // the blocks below the window have their turn later: no factor here
+          const uint32_t from = static_cast<uint32_t>((w.ref - kWindow) & 0xFFFF) * 0x10001u;
+          v02 = select_bits(v02, 0xC000C000u, __vcmpges2(v02, from));
+          v13 = select_bits(v13, 0xC000C000u, __vcmpges2(v13, from));
+        }
+      }
       const uint32_t add = static_cast<uint32_t>((kRefField - w.ref) & 0xFFFF) * 0x10001u;
       const uint32_t f02 = __viaddmin_s16x2_relu(v02, add, kMaxField * 0x10001u) << 10;
       const uint32_t f13 = __viaddmin_s16x2_relu(v13, add, kMaxField * 0x10001u) << 10;
@@ -462,7 +473,7 @@ __device__ __forceinline__ void chunk(Warp& w, const uint32_t (&q)[4][4], const 
   }
   const float mx0 = fmax3(fmaxf(x[0][0], x[0][2]), x[1][0], x[1][2]);
   const float mx1 = fmax3(fmaxf(x[0][1], x[0][3]), x[1][1], x[1][3]);
-  if (__any_sync(0xffffffffu, mx0 > w.m[0] + kLazy || mx1 > w.m[1] + kLazy)) raise_max(w, mx0, mx1);
+  if (__any_sync(0xffffffffu, mx0 > w.m[0] + (kLift + kLazy) || mx1 > w.m[1] + (kLift + kLazy))) raise_max(w, mx0, mx1);
   uint32_t pb[2][2];
 #pragma unroll
   for (int a = 0; a < 2; ++a)
@@ -501,7 +512,7 @@ __device__ __forceinline__ void chunk(Warp& w, const uint32_t (&q)[4][4], const 
 }
 
 // ------------------------------------------------------------------------------- a unit's end
-// The warps' partials of unit u (in units of 2^(M + Rmax - 8)) joined by nw warps, this one the w-th: a warp per head,
+// The warps' partials of unit u (in units of 2^(M + Rmax - 2)) joined by nw warps, this one the w-th: a warp per head,
 // lane = channels [4 c, 4 c + 4). whole: the unit is this CTA's alone; else it is a part, and the part that comes last
 // merges them all. The nw warps come here together.
 __device__ __forceinline__ void join(const MxDecodeParams& p, uint8_t* smem, uint32_t u, uint32_t seg, bool whole, int w, int nw) {
@@ -533,8 +544,8 @@ __device__ __forceinline__ void join(const MxDecodeParams& p, uint8_t* smem, uin
       acc.z = fmaf(s, o.z, acc.z);
       acc.w = fmaf(s, o.w, acc.w);
     }
-    // 2^(R - 127 - 8) / L, in two steps: the power alone may leave fp32's range
-    const float inv = 1.0f / Lsum, two_r = mx_scale(R), down = 0.00390625f;
+    // 2^(R - 127 - 2) / L, in two steps: the power alone may leave fp32's range
+    const float inv = 1.0f / Lsum, two_r = mx_scale(R), down = 1.0f / (1 << (kRefField - 15));
     acc.x = acc.x * inv * down * two_r;
     acc.y = acc.y * inv * down * two_r;
     acc.z = acc.z * inv * down * two_r;
@@ -694,7 +705,7 @@ __global__ void __launch_bounds__(mxd::kThreads, 1) mxfp4_decode_kernel(const __
         }
         chunk(w, q, qf, st, fact, rr + 1, lane);
       }
-      // this warp's partial: O in units of 2^(m + R - 8), m, l, R
+      // this warp's partial: O in units of 2^(m + R - 2), m, l, R
 #pragma unroll
       for (int m = 4; m <= 16; m <<= 1) {
         w.l[0] += __shfl_xor_sync(0xffffffffu, w.l[0], m);

@@ -125,3 +125,35 @@ def test_large_key_against_every_query(form, layers, at, by):
     k, v = np.random.default_rng(at).standard_normal((2, 8, 896, 128))
     k[:, at, [63, 127]] = -2.0 ** by
     run(form, x, HostCache(k, v, 700), 700, -700, layers)
+
+
+@pytest.mark.parametrize("layers,n", [(1, 700), (20, 700), (3, 1500)])
+@pytest.mark.parametrize("high", [16, 12])
+def test_weights_far_below_the_largest(layers, n, high):
+    """One key in every 32 is a sink, 8 (high + 8 - 2) / sqrt(128) nats above the rest, with values of zero: the output is what
+    the rest add. Decode holds weights in f16 with a warp's largest at 2^8 at least, to 2^-25 of absolute error."""
+    x = step_inputs(1, 64, 1)
+    for name in ("q_gamma", "k_gamma"):
+        x[name].fill_(1.0)
+    x["q_raw"].zero_()
+    x["q_raw"][..., 63] = x["q_raw"][..., 127] = 1.0  # normed: 8 in both
+    x["k_raw"].zero_()
+    x["v_raw"].fill_(1.0)
+    Smax = -(-(n + 1) // 64) * 64
+    k, v = np.zeros((8, Smax, 128)), np.ones((8, Smax, 128))
+    k[:, ::32, 63], k[:, ::32, 127] = high, 8.0
+    v[:, ::32] = 0.0
+    h = HostCache(k, v, n)
+    bufs = [device_buffers(x, h.device()) for _ in range(layers)]
+    ws = ea.alloc_decode_mxfp4_workspace(layers)
+    ea.text_decode_attention_mxfp4(bufs, n, Smax, -n, ws)
+    check_status(ws)
+    small = np.exp2(-8 * (high + 8) / 128 ** 0.5 / np.log(2))  # a rest key's weight, the sink's being 1
+    sinks = -(-n // 32)
+    rest = n + 1 - sinks
+    want = rest * small / (sinks + rest * small)
+    # bf16's half step, the weight's (2^-25 at 2^8), and 1e-4 for fp32 sums and exponentials
+    bar = 2.0 ** -9 + 2.0 ** -33 / small + 1e-4
+    for b in bufs:
+        off = float((b.out.double() / want - 1).abs().max())
+        assert off <= bar, f"off by {off:.2e}, bar {bar:.2e}"
