@@ -69,6 +69,22 @@ DeviceInfo g_dev[kMaxDevices];
 std::mutex g_mu;
 int g_splits = 0;
 
+// What a kernel's attributes need: done once for each device (they hold for the current device alone), and again where it
+// failed.
+class OncePerDevice {
+ public:
+  template <class Set>
+  bool operator()(int dev, Set set) {
+    std::lock_guard<std::mutex> lk(mu_);
+    if (!done_[dev]) done_[dev] = set();
+    return done_[dev];
+  }
+
+ private:
+  std::mutex mu_;
+  bool done_[kMaxDevices] = {};
+};
+
 // Queries (once per device) the SM count and that the device is an sm_103 part, and raises
 // the attention kernel's dynamic shared-memory limit.
 bool device_info(int* dev_out, DeviceInfo* info) {
@@ -817,14 +833,13 @@ int run_linear(const CUtensorMap& xmap, int c1, const void* w0, const void* w1, 
   return EA_OK;
 }
 
-bool linear_attrs_ready() {
-  static std::once_flag once;
-  static bool ok = false;
-  std::call_once(once, [] {
-    ok = linear_set_attributes() == cudaSuccess;
+bool linear_attrs_ready(int dev) {
+  static OncePerDevice once;
+  return once(dev, [] {
+    const bool ok = linear_set_attributes() == cudaSuccess;
     cudaGetLastError();
+    return ok;
   });
-  return ok;
 }
 
 }  // namespace
@@ -853,7 +868,7 @@ int expert_decoder_layer(const ea_decoder_layer_args* a, int S, int Smax, int ro
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return EA_ERR_MISALIGNED;
   int dev;
   DeviceInfo di;
-  if (!device_info(&dev, &di) || !linear_attrs_ready()) return EA_ERR_UNSUPPORTED;
+  if (!device_info(&dev, &di) || !linear_attrs_ready(dev)) return EA_ERR_UNSUPPORTED;
   const int H = a->hidden, I = a->inter;
   const LayerWs wl = layer_ws_layout(H, I, di.sm_count);
   if (ws_bytes < wl.total) return EA_ERR_WORKSPACE;
@@ -918,7 +933,7 @@ int expert_linear64(const void* x, const void* w, void* y, int K, int N, void* w
   if (ws_bytes < 1024) return EA_ERR_WORKSPACE;
   int dev;
   DeviceInfo di;
-  if (!device_info(&dev, &di) || !linear_attrs_ready()) return EA_ERR_UNSUPPORTED;
+  if (!device_info(&dev, &di) || !linear_attrs_ready(dev)) return EA_ERR_UNSUPPORTED;
   CUtensorMap xm;
   if (!rows_map(x, K, &xm)) return EA_ERR_CUDA;
   return run_linear(xm, K / 64, w, nullptr, N, K, kLinPlain, nullptr, static_cast<__nv_bfloat16*>(y),
@@ -940,14 +955,13 @@ cudaError_t launch_decode_kernel(const DecodeParams<CAP>& dp, cudaLaunchConfig_t
 
 namespace {
 
-bool decode_attrs_ready() {
-  static std::once_flag once;
-  static bool ok = false;
-  std::call_once(once, [] {
-    ok = decode_set_attributes() == cudaSuccess;
+bool decode_attrs_ready(int dev) {
+  static OncePerDevice once;
+  return once(dev, [] {
+    const bool ok = decode_set_attributes() == cudaSuccess;
     cudaGetLastError();
+    return ok;
   });
-  return ok;
 }
 
 int validate_decode(const ea_decode_args* a, int n_layers, int pos, int Smax, int rope_delta,
@@ -1076,7 +1090,7 @@ int text_decode_attention(const ea_decode_args* layers, int n_layers, int pos, i
   if (rc != EA_OK) return rc;
   int dev;
   DeviceInfo di;
-  if (!device_info(&dev, &di) || !decode_attrs_ready()) return EA_ERR_UNSUPPORTED;
+  if (!device_info(&dev, &di) || !decode_attrs_ready(dev)) return EA_ERR_UNSUPPORTED;
   const int per = n_layers < kDecodeMaxLayers ? n_layers : kDecodeMaxLayers;
   const DecodeWs wl = decode_ws_layout(per, di.sm_count);
   if (ws_bytes < wl.total) return EA_ERR_WORKSPACE;
@@ -1275,21 +1289,20 @@ MxAttnLayer mx_layer(const A& x) {
           static_cast<__nv_bfloat16*>(x.k_new), static_cast<__nv_bfloat16*>(x.v_new)};
 }
 
-bool mx_attrs_ready() {
-  static std::once_flag once;
-  static bool ok = false;
-  std::call_once(once, [] {
-    ok = mxfp4_decode_set_attributes() == cudaSuccess && mxfp4_attention_set_attributes() == cudaSuccess;
+bool mx_attrs_ready(int dev) {
+  static OncePerDevice once;
+  return once(dev, [] {
+    const bool ok = mxfp4_decode_set_attributes() == cudaSuccess && mxfp4_attention_set_attributes() == cudaSuccess;
     cudaGetLastError();
+    return ok;
   });
-  return ok;
 }
 
 int run_mx_decode(const ea_decode_mxfp4_args* a, int n_layers, int pos, int Smax, long long p0, void* workspace,
                   size_t ws_bytes, ea_stream_t stream) {
   int dev;
   DeviceInfo di;
-  if (!device_info(&dev, &di) || !mx_attrs_ready()) return EA_ERR_UNSUPPORTED;
+  if (!device_info(&dev, &di) || !mx_attrs_ready(dev)) return EA_ERR_UNSUPPORTED;
   const int per = n_layers < kMaxLayersPerLaunch ? n_layers : kMaxLayersPerLaunch;
   // (the layout of 64 layers whatever their number: the counters that a larger call needs at zero stay out of a smaller
   // call's partials)
@@ -1363,7 +1376,7 @@ int run_mx_expert(const ea_layer_mxfp4_args* a, int n_layers, int S, int Smax, l
                   size_t ws_bytes, ea_stream_t stream) {
   int dev;
   DeviceInfo di;
-  if (!device_info(&dev, &di) || !mx_attrs_ready()) return EA_ERR_UNSUPPORTED;
+  if (!device_info(&dev, &di) || !mx_attrs_ready(dev)) return EA_ERR_UNSUPPORTED;
   const int per = n_layers < kMaxLayersPerLaunch ? n_layers : kMaxLayersPerLaunch;
   const MxExpertWs wl = mx_expert_ws(per, di.sm_count);
   if (ws_bytes < wl.total) return EA_ERR_WORKSPACE;

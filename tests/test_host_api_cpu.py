@@ -1,0 +1,41 @@
+"""The library's host side with fake devices (runs without a GPU): what it does once for a device, and where it lays things in
+a workspace that calls of different sizes share."""
+import pytest
+
+from tests import _host_api as host
+
+OK, UNSUPPORTED = host._lib.EA_OK, host._lib.EA_ERR_UNSUPPORTED
+
+
+@pytest.fixture(scope="module")
+def h(tmp_path_factory):
+    return host.load(str(tmp_path_factory.mktemp("host")))
+
+
+# a call of one layer, and which of the fake's counts of attributes is its own
+CALLS = {"expert": (lambda h: host.expert(h, 1), 0), "decode": (lambda h: host.decode(h, 1), 3), "linear": (host.linear, 2),
+         "decode mxfp4": (lambda h: host.decode_mxfp4(h, 1), 4), "expert mxfp4": (lambda h: host.expert_mxfp4(h, 1), 4)}
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_every_device_gets_its_attributes(h, name):
+    """Shared memory beyond 48 KB is granted device by device: the first call on each has to ask for it."""
+    call, what = CALLS[name]
+    for d in (0, 5, 2):
+        h.fake_device(d, -1)
+        assert call(h) == OK
+        n = h.fake_set(d, what)
+        assert n >= 1
+        assert call(h) == OK and h.fake_set(d, what) == n  # and only the first
+
+
+@pytest.mark.parametrize("name", ["decode", "linear", "decode mxfp4", "expert mxfp4"])
+def test_a_device_that_refuses_is_asked_again(h, name):
+    call, _ = CALLS[name]
+    d = 10 + list(CALLS).index(name)
+    h.fake_device(d, -1)
+    assert h.expert_attn_workspace_size(1, 512, 0) > 0  # (the device's own set-up)
+    h.fake_device(d, d)
+    assert call(h) == UNSUPPORTED
+    h.fake_device(d, -1)
+    assert call(h) == OK
