@@ -1068,14 +1068,13 @@ size_t text_decode_workspace_size(int n_layers) {
   int dev;
   DeviceInfo di;
   if (!device_info(&dev, &di)) return 0;
-  const int per = n_layers < kDecodeMaxLayers ? n_layers : kDecodeMaxLayers;
-  return decode_ws_layout(per, di.sm_count).total;
+  return decode_ws_layout(di.sm_count).total;
 }
 
 int text_decode_workspace_init(void* workspace, size_t ws_bytes, ea_stream_t stream) {
   if (workspace == nullptr || ws_bytes < 1024) return EA_ERR_INVALID_ARG;
   // the status word and the per-unit arrival counts of up to 64 layers per launch
-  const size_t init = decode_ws_layout(kDecodeMaxLayers, 1).part_o_off;
+  const size_t init = decode_ws_layout(1).part_o_off;
   const size_t n = ws_bytes < init ? ws_bytes : init;
   if (cudaMemsetAsync(workspace, 0, n, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
     cudaGetLastError();
@@ -1092,7 +1091,7 @@ int text_decode_attention(const ea_decode_args* layers, int n_layers, int pos, i
   DeviceInfo di;
   if (!device_info(&dev, &di) || !decode_attrs_ready(dev)) return EA_ERR_UNSUPPORTED;
   const int per = n_layers < kDecodeMaxLayers ? n_layers : kDecodeMaxLayers;
-  const DecodeWs wl = decode_ws_layout(per, di.sm_count);
+  const DecodeWs wl = decode_ws_layout(di.sm_count);
   if (ws_bytes < wl.total) return EA_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -1304,9 +1303,7 @@ int run_mx_decode(const ea_decode_mxfp4_args* a, int n_layers, int pos, int Smax
   DeviceInfo di;
   if (!device_info(&dev, &di) || !mx_attrs_ready(dev)) return EA_ERR_UNSUPPORTED;
   const int per = n_layers < kMaxLayersPerLaunch ? n_layers : kMaxLayersPerLaunch;
-  // (the layout of 64 layers whatever their number: the counters that a larger call needs at zero stay out of a smaller
-  // call's partials)
-  const DecodeWs wl = decode_ws_layout(kMaxLayersPerLaunch, di.sm_count);
+  const DecodeWs wl = decode_ws_layout(di.sm_count);
   if (ws_bytes < wl.total) return EA_ERR_WORKSPACE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   MxDecodeParams p;
@@ -1445,7 +1442,7 @@ size_t text_decode_mxfp4_workspace_size(int n_layers) {
   int dev;
   DeviceInfo di;
   if (n_layers < 1 || !device_info(&dev, &di)) return 0;
-  return decode_ws_layout(kMaxLayersPerLaunch, di.sm_count).total;
+  return decode_ws_layout(di.sm_count).total;
 }
 
 int text_decode_attention_mxfp4(const ea_decode_mxfp4_args* layers, int n_layers, int pos, int Smax, int rope_delta,

@@ -213,16 +213,18 @@ struct DecodeParams {
   float scale_log2;      // log2(e) / sqrt(128)
 };
 
-// Decode workspace: [0, 1024) status word; unit counters n_layers * 8 uint32 (1 KB aligned);
+// Decode workspace: [0, 1024) status word; unit counters of 64 layers * 8 uint32, whatever the call's
+// number of layers (those that a larger call needs at zero stay out of a smaller call's partials);
 // partial outputs and statistics for at most max_ctas CTAs.
 struct DecodeWs {
   size_t cnt_off, part_o_off, part_ml_off, total;
 };
-constexpr DecodeWs decode_ws_layout(int n_layers, int max_ctas) {
+constexpr DecodeWs decode_ws_layout(int max_ctas) {
   DecodeWs w{};
   size_t off = 1024;
   w.cnt_off = off;
-  off += ((static_cast<size_t>(n_layers) * kHkv * sizeof(uint32_t)) + 1023) & ~static_cast<size_t>(1023);
+  off += static_cast<size_t>(kDecodeMaxLayers) * kHkv * sizeof(uint32_t);
+  static_assert(kDecodeMaxLayers * kHkv * sizeof(uint32_t) % 1024 == 0, "alignment of the partials");
   w.part_o_off = off;
   off += static_cast<size_t>(max_ctas) * 2 * kRepText * kD * sizeof(float);
   w.part_ml_off = off;

@@ -39,3 +39,23 @@ def test_a_device_that_refuses_is_asked_again(h, name):
     assert call(h) == UNSUPPORTED
     h.fake_device(d, -1)
     assert call(h) == OK
+
+
+def check_one_workspace(spans):
+    """spans: by call, the words that it needs at zero (and leaves so) and the scratch that it writes, in one workspace: no
+    call's scratch may lie over another's words."""
+    for a, (_, (lo, hi)) in spans.items():
+        for b, ((z0, z1), _) in spans.items():
+            assert hi <= z0 or lo >= z1, f"{a}'s scratch [{lo - host.WS}, {hi - host.WS}) over {b}'s words [{z0 - host.WS}, {z1 - host.WS})"
+
+
+@pytest.mark.parametrize("call", [host.decode, host.decode_mxfp4])
+def test_decode_calls_of_any_layer_count_share_a_workspace(h, call):
+    h.fake_device(0, -1)
+    spans = {}
+    for n in range(1, 65):
+        for pos in (0, 300, 511):
+            assert call(h, n, pos) == OK
+            spans[n, pos] = host.last(h)
+    check_one_workspace(spans)
+    assert max(s[1][1] for s in spans.values()) - host.WS <= h.text_decode_workspace_size(1)
