@@ -583,7 +583,7 @@ const char* expert_attn_status_string(int status) {
 namespace {
 
 constexpr size_t noalloc_bytes() {
-  return ws_layout(EA_NOALLOC_MAX_LAYERS, EA_NOALLOC_MAX_CTAS, true).total;
+  return ws_layout(EA_NOALLOC_MAX_LAYERS, EA_NOALLOC_MAX_CTAS, true, EA_NOALLOC_MAX_LAYERS).total;
 }
 static_assert(noalloc_bytes() == EA_NOALLOC_SCRATCH_BYTES, "scratch size in the header is stale");
 
@@ -618,7 +618,7 @@ extern "C" int expert_attn_layers_noalloc(const ea_layer_args* layers, int n_lay
   if (!device_info(&dev, &di)) return EA_ERR_UNSUPPORTED;
   DeviceInfo capped = di;
   if (capped.sm_count > EA_NOALLOC_MAX_CTAS) capped.sm_count = EA_NOALLOC_MAX_CTAS;
-  const WsLayout wl = ws_layout(n_layers, capped.sm_count, kv_dtype == EA_KV_FP8_E4M3);
+  const WsLayout wl = ws_layout(n_layers, capped.sm_count, kv_dtype == EA_KV_FP8_E4M3, EA_NOALLOC_MAX_LAYERS);
   if (wl.total > EA_NOALLOC_SCRATCH_BYTES) return EA_ERR_WORKSPACE;
   uint8_t* ws = static_cast<uint8_t*>(noalloc_scratch(dev));
   if (ws == nullptr) return EA_ERR_CUDA;

@@ -49,8 +49,10 @@ enum : uint32_t {
 // ------------------------------------------------------------------------- workspace layout
 //   [0, 1024)                    status word (bytes 0-3); grid-merge arrival and departure
 //                                 counts (bytes 4-11, zero between calls); rest reserved
-//   sync    n_layers * 8 * 2 uint32  per unit: arrival count and partial-ready flag of the
-//                                   in-kernel merge of two-part units (zero between calls)
+//   sync    64 layers * 8 * 2 uint32  per unit: arrival count and partial-ready flag of the
+//                                   in-kernel merge of two-part units (zero between calls); for 64
+//                                   layers whatever the call's number (or sync_layers), so that
+//                                   no call's scratch lies over a larger one's words
 //   qscale  n_layers * 8 * 128 fp32    FP8 only: per-row scale of the e4m3 roped Q
 //   svref   n_layers * 8 fp32          FP8 only: per-unit reference V scale (max over its tiles)
 //   q       n_layers * 8 * 32 KB  e4m3 only: roped Q per (layer, kv head) as high and low e4m3
@@ -66,11 +68,12 @@ struct WsLayout {
   size_t sync_off, qscale_off, svref_off, q_off, part_o_off, part_lse_off, total;
 };
 
-constexpr WsLayout ws_layout(int n_layers_per_launch, int max_ctas, bool fp8) {
+constexpr WsLayout ws_layout(int n_layers_per_launch, int max_ctas, bool fp8,
+                             int sync_layers = kMaxLayersPerLaunch) {
   WsLayout w{};
   size_t off = 1024;
   w.sync_off = off;
-  off += ((static_cast<size_t>(n_layers_per_launch) * kHkv * 2 * sizeof(uint32_t)) + 1023) &
+  off += ((static_cast<size_t>(sync_layers) * kHkv * 2 * sizeof(uint32_t)) + 1023) &
          ~static_cast<size_t>(1023);
   w.qscale_off = off;
   off += static_cast<size_t>(n_layers_per_launch) * kHkv * kRows * sizeof(float);

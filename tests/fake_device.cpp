@@ -81,8 +81,8 @@ cudaError_t launch_prologue_kernel(const PrologueParams<CAP>&, bool, int, cudaLa
 template cudaError_t launch_prologue_kernel(const PrologueParams<kSmallCap>&, bool, int, cudaLaunchConfig_t);
 template cudaError_t launch_prologue_kernel(const PrologueParams<kMaxLayersPerLaunch>&, bool, int, cudaLaunchConfig_t);
 template <int CAP>
-cudaError_t launch_attention_kernel(const AttnParams<CAP>& p, bool, cudaLaunchConfig_t cfg) {
-  g_last = {at(p.unit_sync), at(p.unit_sync + 2 * (p.W / p.T)), at(p.q_scale != nullptr ? static_cast<const void*>(p.q_scale) : p.part_o),
+cudaError_t launch_attention_kernel(const AttnParams<CAP>& p, bool f8, cudaLaunchConfig_t cfg) {
+  g_last = {at(p.unit_sync), at(p.unit_sync + 2 * (p.W / p.T)), f8 ? at(p.q_scale) : at(p.part_o),
             at(p.part_lse + static_cast<size_t>(cfg.gridDim.x) * 6 * kRows)};
   return cudaSuccess;
 }

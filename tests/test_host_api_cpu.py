@@ -59,3 +59,15 @@ def test_decode_calls_of_any_layer_count_share_a_workspace(h, call):
             spans[n, pos] = host.last(h)
     check_one_workspace(spans)
     assert max(s[1][1] for s in spans.values()) - host.WS <= h.text_decode_workspace_size(1)
+
+
+def test_expert_calls_of_any_layer_count_and_cache_share_a_workspace(h):
+    """An e4m3 workspace also serves bf16 calls, which count on words that every call leaves at zero."""
+    h.fake_device(0, -1)
+    spans = {}
+    for n in range(1, 65):
+        for dtype in (host._lib.EA_KV_BF16, host._lib.EA_KV_FP8_E4M3):
+            assert host.expert(h, n, dtype=dtype) == OK
+            spans[n, dtype] = host.last(h)
+    check_one_workspace(spans)
+    assert max(s[1][1] for s in spans.values()) - host.WS <= h.expert_attn_workspace_size(64, 512, host._lib.EA_KV_FP8_E4M3)
