@@ -444,12 +444,12 @@ def alloc_mxfp4_cache(Smax: int, device="cuda") -> Mxfp4Cache:
 
 
 class _Arr:
-    """A marshalled argument array with the buffers that it points into, the device they are on, and (rows) their
-    type and strides."""
+    """A marshalled argument array with the function that made it, the buffers that it points into, the device they are on,
+    and (rows) their type and strides."""
 
-    def __init__(self, arr, layers, device, dtype=None, strides=(0, 0), n_rows=0, Smax=0):
-        self.arr, self.layers, self.n, self.device, self.dtype, self.strides = arr, layers, len(arr), device, dtype, strides
-        self.n_rows, self.Smax = n_rows, Smax
+    def __init__(self, maker, arr, layers, device, dtype=None, strides=(0, 0), n_rows=0, Smax=0):
+        self.maker, self.arr, self.layers, self.n, self.device = maker, arr, layers, len(arr), device
+        self.dtype, self.strides, self.n_rows, self.Smax = dtype, strides, n_rows, Smax
 
 
 def _one_device(tensors, what: str) -> int:
@@ -465,8 +465,10 @@ _device_now = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _stream_now = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _current(a: _Arr, Smax: int, stream, ws: torch.Tensor | None = None) -> int | None:
+def _current(a: _Arr, maker: str, Smax: int, stream, ws: torch.Tensor | None = None) -> int | None:
     """Checks a call's arguments against its marshalled ones; the stream's handle."""
+    if not isinstance(a, _Arr) or a.maker != maker:  # (the decode step's and the expert's are of one struct)
+        raise TypeError(f"marshalled arguments of {maker} are expected")
     if a.device != _device_now() or (ws is not None and ws.get_device() != a.device):
         raise ValueError(f"the tensors are on cuda:{a.device}, which must be the current device (and the workspace's)")
     if a.Smax != Smax:
@@ -513,12 +515,12 @@ def make_rows_args(layers: list[Mxfp4Rows], Smax: int) -> _Arr:
         a.k, a.v = L.k.data_ptr(), L.v.data_ptr()
         _mx_cache(a, L.cache, Smax)
     dev = _one_device([t for L in layers for t in (L.k, L.v, *L.cache.__dict__.values())], "rows")
-    return _Arr(arr, list(layers), dev, _ROWS_DTYPES[first.dtype], (first.stride(0), first.stride(1)), first.shape[1], Smax)
+    return _Arr("make_rows_args", arr, list(layers), dev, _ROWS_DTYPES[first.dtype], (first.stride(0), first.stride(1)), first.shape[1], Smax)
 
 
 def _rows_call(fn: str, layers, row0: int, n_rows: int, Smax: int, stream, a: _Arr | None) -> None:
     a = a if a is not None else make_rows_args(layers, Smax)
-    st = _current(a, Smax, stream)
+    st = _current(a, "make_rows_args", Smax, stream)
     if n_rows > a.n_rows:
         raise ValueError(f"k and v have {a.n_rows} rows, {n_rows} are asked for")
     if n_rows == 0:
@@ -566,7 +568,7 @@ class LayerMxfp4Buffers:
     v_new: torch.Tensor | None = None
 
 
-def _mx_attn_args(layers, Smax: int, hq: int, tok: int) -> _Arr:
+def _mx_attn_args(maker: str, layers, Smax: int, hq: int, tok: int) -> _Arr:
     if not layers:
         raise ValueError("no layers")
     arr, bf = (EaAttnMxfp4Args * len(layers))(), torch.bfloat16
@@ -577,17 +579,17 @@ def _mx_attn_args(layers, Smax: int, hq: int, tok: int) -> _Arr:
         _mx_cache(a, L.cache, Smax)
     dev = _one_device([t for L in layers for t in (L.q_raw, L.k_raw, L.v_raw, L.q_gamma, L.k_gamma, L.out, L.k_new, L.v_new,
                                                    *L.cache.__dict__.values())], "layers")
-    return _Arr(arr, list(layers), dev, Smax=Smax)
+    return _Arr(maker, arr, list(layers), dev, Smax=Smax)
 
 
 def make_decode_mxfp4_args(layers: list[DecodeMxfp4Buffers], Smax: int) -> _Arr:
     """Marshalled arguments of text_decode_attention_mxfp4, for loops that call it often."""
-    return _mx_attn_args(layers, Smax, 64, 1)
+    return _mx_attn_args("make_decode_mxfp4_args", layers, Smax, 64, 1)
 
 
 def make_mxfp4_args(layers: list[LayerMxfp4Buffers], Smax: int) -> _Arr:
     """Marshalled arguments of expert_attn_layers_mxfp4, for loops that call it often."""
-    return _mx_attn_args(layers, Smax, 16, 64)
+    return _mx_attn_args("make_mxfp4_args", layers, Smax, 16, 64)
 
 
 def text_decode_mxfp4_workspace_size(n_layers: int) -> int:
@@ -622,7 +624,7 @@ def text_decode_attention_mxfp4(layers: list[DecodeMxfp4Buffers], pos: int, Smax
                                 stream=None, _arr=None) -> None:
     """One decode step over 4-bit caches: the new row quantised into row pos, then attention over rows [0, pos]."""
     a = _arr if _arr is not None else make_decode_mxfp4_args(layers, Smax)
-    st = _current(a, Smax, stream, ws)
+    st = _current(a, "make_decode_mxfp4_args", Smax, stream, ws)
     rc = (_lib_handle or lib()).text_decode_attention_mxfp4(a.arr, a.n, int(pos), int(Smax), int(rope_delta), ws.data_ptr(),
                                                                ws.numel(), st)
     if rc:
@@ -634,7 +636,7 @@ def expert_attn_layers_mxfp4(layers: list[LayerMxfp4Buffers], S: int, Smax: int,
     """The expert's attention over 4-bit caches: the own rows quantised into rows [Smax-64, Smax), then attention
     over rows [0, S) and the own rows."""
     a = _arr if _arr is not None else make_mxfp4_args(layers, Smax)
-    st = _current(a, Smax, stream, ws)
+    st = _current(a, "make_mxfp4_args", Smax, stream, ws)
     rc = (_lib_handle or lib()).expert_attn_layers_mxfp4(a.arr, a.n, int(S), int(Smax), int(rope_delta), ws.data_ptr(),
                                                             ws.numel(), st)
     if rc:
