@@ -1325,18 +1325,21 @@ int run_mx_decode(const ea_decode_mxfp4_args* a, int n_layers, int pos, int Smax
     const uint32_t W = units * p.T;
     // Parts that end with their unit (each of at least one chunk per warp), unless equal ranges over all SMs, which cut
     // units anywhere, save a warp more than four chunks: a CTA that works on two units, and a unit of three parts, cost that
-    // much. Parts and ranges: 1 layer at pos 4700 8.2 and 14.6 us, 2 layers 8.9 and 13.8, 9 layers 16.0 and 18.0, 18 layers
-    // at pos 20000 (3.6 chunks more) 68.2 and 70.3, 5 layers there (4.3) 28.7 and 27.3, 4 layers at pos 131000 109 and 99.
+    // much. Parts and ranges (calls four in a row, caches out of L2): 1 layer at pos 4700 9.9 and 16.6 us, 2 layers 10.9 and
+    // 14.5, 9 layers 17.6 and 18.6, 18 layers at pos 20000 (3.6 chunks more) 72.9 and 75.0, 5 layers there (4.3) 30.9 and
+    // 30.4, 4 layers at pos 131000 114 and 103. Either way a unit has few enough parts for one warp to weigh, a lane each.
     auto ceil_div = [](uint32_t x, uint32_t y) { return (x + y - 1) / y; };
     const uint32_t full = ceil_div(p.T, kMxDecodeWarps), fit = sms / units;
     p.parts = full < fit ? full : fit;
     if (p.parts > 0 && ceil_div(ceil_div(p.T, p.parts), kMxDecodeWarps) * sms * kMxDecodeWarps > W + 4 * sms * kMxDecodeWarps) p.parts = 0;
-    uint32_t grid = units * p.parts;
+    uint32_t grid = units * p.parts, most = p.parts;  // most: the parts of a unit, at most
     if (p.parts == 0) {
       grid = sms < W ? sms : W;
       p.per_cta = W / grid;
       p.extra = W % grid;
+      most = ceil_div(p.T, p.per_cta) + 1;
     }
+    if (most > kMxMaxParts) return EA_ERR_UNSUPPORTED;  // (a GPU of 250 SMs and more)
     cudaLaunchConfig_t cfg = launch_config(static_cast<cudaStream_t>(stream), attr, true);
     cfg.gridDim = dim3(grid);
     if (launch_mxfp4_decode(p, cfg) != cudaSuccess) {

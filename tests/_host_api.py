@@ -29,7 +29,7 @@ def load(folder) -> ctypes.CDLL:
                             ("expert_attn_layers_mxfp4", I, [V, I, I, I, I, V, S, V]),
                             ("expert_linear64_workspace_size", S, [I, I]),
                             ("expert_linear64", I, [V, V, V, I, I, V, S, V]),
-                            ("fake_device", None, [I, I]), ("fake_set", I, [I, I]), ("fake_last", None, [V])):
+                            ("fake_device", None, [I, I]), ("fake_set", I, [I, I]), ("fake_sms", None, [I]), ("fake_parts", I, []), ("fake_last", None, [V])):
         f = getattr(h, name)
         f.restype, f.argtypes = res, args
     return h

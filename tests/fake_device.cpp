@@ -8,6 +8,8 @@
 
 namespace {
 int g_device = 0, g_failing = -1;
+unsigned g_parts;  // of a unit, at most, in the last decode step over a 4-bit cache
+int g_sms = 152;
 int g_set[64][5];  // attributes set, by device: attention, prologue, linear, decode, 4-bit (its decode step and attention)
 struct Launch {
   uint64_t counters, counters_end, scratch, scratch_end;  // words that a call needs at zero; what it writes besides
@@ -30,6 +32,8 @@ void fake_device(int d, int failing) {
   g_failing = failing;
 }
 int fake_set(int d, int what) { return g_set[d][what]; }
+void fake_sms(int n) { g_sms = n; }
+int fake_parts() { return static_cast<int>(g_parts); }
 void fake_last(uint64_t* out) { std::memcpy(out, &g_last, sizeof(g_last)); }
 
 cudaError_t cudaGetDevice(int* d) {
@@ -37,7 +41,7 @@ cudaError_t cudaGetDevice(int* d) {
   return cudaSuccess;
 }
 cudaError_t cudaDeviceGetAttribute(int* v, cudaDeviceAttr a, int) {
-  *v = a == cudaDevAttrComputeCapabilityMajor ? 10 : a == cudaDevAttrComputeCapabilityMinor ? 3 : 152;
+  *v = a == cudaDevAttrComputeCapabilityMajor ? 10 : a == cudaDevAttrComputeCapabilityMinor ? 3 : g_sms;
   return cudaSuccess;
 }
 cudaError_t cudaGetLastError() { return cudaSuccess; }
@@ -100,6 +104,19 @@ cudaError_t launch_mxfp4_prologue(const MxPrologueParams&, int, cudaLaunchConfig
 cudaError_t launch_mxfp4_attention(const MxExpertParams&, cudaLaunchConfig_t) { return cudaSuccess; }
 cudaError_t launch_mxfp4_merge(const MxMergeParams&, int, cudaLaunchConfig_t) { return cudaSuccess; }
 cudaError_t launch_mxfp4_decode(const MxDecodeParams& p, cudaLaunchConfig_t cfg) {
+  // the parts that the kernel will count, from the ranges' starts
+  auto start = [&](uint32_t c) {
+    return p.parts > 0 ? c / p.parts * p.T + c % p.parts * p.T / p.parts : c * p.per_cta + (c < p.extra ? c : p.extra);
+  };
+  g_parts = 0;
+  uint32_t unit = 0, n = 0;
+  for (uint32_t c = 0; c < cfg.gridDim.x; ++c) {
+    for (uint32_t u = start(c) / p.T; u <= (start(c + 1) - 1) / p.T; ++u, ++n) {
+      if (u != unit) n = 0;
+      unit = u;
+      g_parts = n + 1 > g_parts ? n + 1 : g_parts;
+    }
+  }
   g_last = {at(p.unit_cnt), at(p.unit_cnt + kMaxLayersPerLaunch * kHkv), at(p.part_o),
             at(p.part_lse + static_cast<size_t>(cfg.gridDim.x) * 2 * kRepText)};
   return cudaSuccess;

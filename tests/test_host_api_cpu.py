@@ -71,3 +71,26 @@ def test_expert_calls_of_any_layer_count_and_cache_share_a_workspace(h):
             spans[n, dtype] = host.last(h)
     check_one_workspace(spans)
     assert max(s[1][1] for s in spans.values()) - host.WS <= h.expert_attn_workspace_size(64, 512, host._lib.EA_KV_FP8_E4M3)
+
+
+@pytest.mark.parametrize("device,sms", [(30, 152), (31, 148), (32, 132), (33, 77), (34, 8)])
+def test_units_of_a_decode_step_have_at_most_32_parts(h, device, sms):
+    """A lane of one warp weighs a part, of any number of layers at any length, on GPUs of any size up to this one's."""
+    h.fake_device(device, -1)
+    h.fake_sms(sms)
+    try:
+        for n in (1, 2, 3, 4, 5, 6, 9, 18, 19, 20, 33, 64):
+            for pos in (0, 31, 400, 1000, 1087, 1100, 2000, 4700, 9999, 20000, 70001, 131071, (1 << 22) - 1):
+                assert host.decode_mxfp4(h, n, pos, max(128, -(-(pos + 1) // 64) * 64)) == OK, (n, pos)
+                assert 1 <= h.fake_parts() <= 32, (n, pos)
+    finally:
+        h.fake_sms(152)
+
+
+def test_a_gpu_with_more_parts_than_that_is_refused(h):
+    h.fake_device(40, -1)
+    h.fake_sms(400)
+    try:
+        assert host.decode_mxfp4(h, 1, 131071, 131072) == UNSUPPORTED
+    finally:
+        h.fake_sms(152)
