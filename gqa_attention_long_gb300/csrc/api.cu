@@ -36,14 +36,17 @@ using namespace ea;
 
 constexpr int kMaxDevices = 64;
 
-// One thread waits, with a time limit, on an mbarrier that nothing arrives on: the bounded-wait
-// failure path of the library's kernels, made to run out on purpose (see the header).
+// One thread waits, with a time limit, on an mbarrier that nothing arrives on, then the warp, with a limit of looks, on that
+// one and on one that is arrived on: the failure paths of the library's waits, made to run out on purpose (see the
+// header).
 __global__ void selftest_wait_kernel(uint32_t* status, uint64_t limit_ns) {
-  __shared__ uint64_t bar;
-  const uint32_t b = smem_u32(&bar);
+  __shared__ uint64_t bar[2];
+  const uint32_t b = smem_u32(bar);
   if (threadIdx.x == 0) {
     mbar_init(b, 1);
+    mbar_init(b + 8, 1);
     fence_mbar_init();
+    mbar_arrive(b + 8);
   }
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -58,6 +61,9 @@ __global__ void selftest_wait_kernel(uint32_t* status, uint64_t limit_ns) {
     }
     if (!done) atomicOr(status, kErrSelftestWait);
   }
+  __syncwarp();
+  const bool gave_up = !counted_wait(b, 0, 100), there = counted_wait(b + 8, 0, 100);
+  if (threadIdx.x == 0 && gave_up && there) atomicOr(status, kErrSelftestLooks);
 }
 
 struct DeviceInfo {

@@ -44,6 +44,7 @@ enum : uint32_t {
   kErrSelftestWait = 1u << 6,
   kErrLinearWait = 1u << 7,
   kErrDecodeWait = 1u << 8,
+  kErrSelftestLooks = 1u << 9,
 };
 
 // ------------------------------------------------------------------------- workspace layout

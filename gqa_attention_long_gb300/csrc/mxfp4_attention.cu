@@ -241,14 +241,10 @@ struct Ctx {
   uint32_t* status;
   long long start, end;
   __device__ __forceinline__ uint32_t bar(int i) const { return sbase + SM_BAR + 8u * i; }
-  // As bounded_wait, in less code (with its code in every role the 64 layers took 5 us more), by a whole warp: limited by
-  // the number of looks (2^20 of them, each of which suspends the warp for a while, last longer than any wait of a
-  // call that works). Whoever has to give up notes why; the other roles then run out of looks themselves.
+  // (With bounded_wait's code in every role the 64 layers took 5 us more.) Whoever has to give up notes why; the other roles
+  // then run out of looks themselves.
   __device__ __forceinline__ bool wait(int b, uint32_t parity, uint32_t err) const {
-#pragma unroll 1
-    for (uint32_t it = 0; it < (1u << 20); ++it) {
-      if (__all_sync(0xffffffffu, mbar_try_wait(bar(b), parity))) return true;
-    }
+    if (counted_wait(bar(b), parity)) return true;
     *failed = err;  // (goes to the status word at the kernel's end)
     return false;
   }

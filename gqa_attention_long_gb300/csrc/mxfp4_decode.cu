@@ -625,12 +625,7 @@ __global__ void __launch_bounds__(mxd::kThreads, 1) mxfp4_decode_kernel(const __
     fence_mbar_init();
   }
   pdl_wait_primary();
-  auto wait = [&](uint32_t b, uint32_t parity) -> bool {  // gives up after 2^20 looks, each of which takes a while
-    bool done = false;
-#pragma unroll 1
-    for (uint32_t it = 0; !done && it < (1u << 20); ++it) done = mbar_try_wait(bar(b), parity);
-    return __all_sync(0xffffffffu, done);
-  };
+  auto wait = [&](uint32_t b, uint32_t parity) -> bool { return counted_wait(bar(b), parity); };
   auto arrive = [&](uint32_t b) {
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(b));

@@ -1,7 +1,7 @@
 // ptx.cuh — inline-PTX building blocks for sm_103a: mbarriers, TMA / bulk copies, tcgen05
 // (TMEM allocation, UMMA issue and commit, TMEM loads / stores), programmatic dependent
-// launch, and bounded waits. Every wait in the library goes through bounded_wait(), which gives
-// up after a time limit, records the failure and lets the kernel tear down cleanly.
+// launch, and bounded waits. Every wait in the library gives up in the end, so that the kernel records the
+// failure and tears down cleanly: bounded_wait() and its like after a time limit, counted_wait() after a number of looks.
 #pragma once
 
 #include <cuda.h>
@@ -98,6 +98,17 @@ __device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity,
   }
   *abort_flag = 1u;
   atomicOr(status, err_bit);
+  return false;
+}
+
+// The same by a whole warp, in less code, without a clock or a flag: gives up after so many looks, each of which suspends
+// the warp for up to 4 us (measured; kLooks of them 4 s). What failed is the caller's to note.
+constexpr uint32_t kLooks = 1u << 20;
+__device__ __forceinline__ bool counted_wait(uint32_t bar, uint32_t parity, uint32_t looks = kLooks) {
+#pragma unroll 1
+  for (uint32_t it = 0; it < looks; ++it) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  }
   return false;
 }
 

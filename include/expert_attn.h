@@ -157,8 +157,9 @@ const char* expert_attn_status_string(int status);
 /* Failure-detection self-test (the pages have no counterpart): launches one CTA on the stream
  * whose thread waits on a shared-memory barrier that nothing ever arrives on, giving up after
  * limit_us microseconds (1 .. 2000000) exactly as the library's kernels give up a bounded wait:
- * it records a timeout bit in the workspace's status word and returns (no trap, no hang), so
- * that expert_attn_read_status then reports EA_ERR_TIMEOUT and the context stays usable.
+ * it records a timeout bit (1 << 6) in the workspace's status word and returns (no trap, no hang), so
+ * that expert_attn_read_status then reports EA_ERR_TIMEOUT and the context stays usable. Then the same
+ * for the wait of the kernels over 4-bit caches, which counts looks in place of time (bit 1 << 9).
  * Returns EA_ERR_INVALID_ARG for a null workspace or an out-of-range limit. */
 int expert_attn_selftest_wait_timeout(int limit_us, void* workspace, size_t ws_bytes,
                                       ea_stream_t stream);
