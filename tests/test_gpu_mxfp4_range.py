@@ -50,9 +50,6 @@ def test_small_queries_over_zero_keys(form, n, size):
     run(form, x, HostCache(np.zeros_like(v), v, n), n, 0, 1)
 
 
-WIDE = list(FORMS)
-
-
 def one_sided(seed, hq, tok):
     """Queries that all point the same way in channels 63 and 127 (which hardly rotate at positions 0 to 63)."""
     x = step_inputs(seed, hq, tok)
@@ -62,7 +59,7 @@ def one_sided(seed, hq, tok):
     return x
 
 
-@pytest.mark.parametrize("form", WIDE)
+@pytest.mark.parametrize("form", FORMS)
 @pytest.mark.parametrize("layers", [1, 20])
 @pytest.mark.parametrize("steps", [(0, -8, -16, -24), (45, 15, -15, -45), (-30, 0, -2, -32), (60, -60, 0, 0)])
 def test_values_of_blocks_far_apart(form, layers, steps):
@@ -75,7 +72,7 @@ def test_values_of_blocks_far_apart(form, layers, steps):
     run(form, x, HostCache(k, v, 700), 700, 0, layers)
 
 
-@pytest.mark.parametrize("form", WIDE)
+@pytest.mark.parametrize("form", FORMS)
 @pytest.mark.parametrize("layers", [1, 20])
 @pytest.mark.parametrize("at", [0, 333, 699])
 @pytest.mark.parametrize("by", [30, 60, 100])
@@ -89,7 +86,7 @@ def test_large_value_without_weight(form, layers, at, by):
     run(form, x, HostCache(k, v, 700), 700, -700, layers)
 
 
-@pytest.mark.parametrize("form", WIDE)
+@pytest.mark.parametrize("form", FORMS)
 @pytest.mark.parametrize("layers", [1, 20])
 def test_values_spread_at_random(form, layers):
     _, _, _, hq, tok = FORMS[form]
@@ -100,7 +97,7 @@ def test_values_spread_at_random(form, layers):
     run(form, x, HostCache(k, v, 700), 700, 0, layers)
 
 
-@pytest.mark.parametrize("form", WIDE)
+@pytest.mark.parametrize("form", FORMS)
 @pytest.mark.parametrize("layers", [1, 20])
 @pytest.mark.parametrize("by", [26, 50, 90])
 def test_keys_of_blocks_far_apart(form, layers, by):
@@ -115,7 +112,7 @@ def test_keys_of_blocks_far_apart(form, layers, by):
     run(form, x, HostCache(k, v, 700), 700, 0, layers)
 
 
-@pytest.mark.parametrize("form", WIDE)
+@pytest.mark.parametrize("form", FORMS)
 @pytest.mark.parametrize("layers", [1, 20])
 @pytest.mark.parametrize("at", [0, 333, 699])
 @pytest.mark.parametrize("by", [26, 60])
@@ -157,3 +154,42 @@ def test_weights_far_below_the_largest(layers, n, high):
     for b in bufs:
         off = float((b.out.double() / want - 1).abs().max())
         assert off <= bar, f"off by {off:.2e}, bar {bar:.2e}"
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("n", [0, 1, 130, 384])
+def test_few_rows_far_apart(form, n):
+    """Blocks of keys and values far apart where the own rows are all there is, or a whole unit is one CTA's."""
+    _, _, _, hq, tok = FORMS[form]
+    x = step_inputs(n + 3, hq, tok)
+    x["q_gamma"][0:32] = x["q_gamma"][64:96] = 0.0
+    x["k_gamma"][0:32] = x["k_gamma"][64:96] = 2.0 ** 40
+    by = np.exp2([0, -12, 25, -40]).repeat(32)
+    x["v_raw"] = (x["v_raw"].float() * torch.from_numpy(by)).to(torch.bfloat16)
+    k, v = np.random.default_rng(n).standard_normal((2, 8, 512, 128))
+    k[..., 0:32] *= 2.0 ** 40
+    k[..., 64:96] *= 2.0 ** 40
+    run(form, x, HostCache(k, v * by, n), n, 0, 3)
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_far_apart_again_and_captured(form):
+    """The same bits from every call, and from a graph's replay."""
+    call, alloc, _, hq, tok = FORMS[form]
+    x = step_inputs(5, hq, tok)
+    k, v = np.random.default_rng(5).standard_normal((2, 8, 1088, 128))
+    by = np.exp2([0, -30, -15, 5]).repeat(32)
+    h = HostCache(k * by[::-1], v * by, 1000)
+    bufs, ws = [device_buffers(x, h.device()) for _ in range(9)], alloc(9)
+    call(bufs, 1000, 1088, 0, ws)
+    outs = [b.out.clone() for b in bufs]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(bufs, 1000, 1088, 0, ws)
+    for _ in range(3):
+        for b in bufs:
+            b.out.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        check_status(ws)
+        assert all(torch.equal(b.out, o) for b, o in zip(bufs, outs))

@@ -6,6 +6,8 @@ import torch
 import gqa_attention_long_gb300 as ea
 from gqa_attention_long_gb300.inputs import decode_inputs_on_device
 from tests._gpu_util import check_status
+from tests._mxfp4_util import decode_oracle, device_buffers, expert_oracle, random_cache, step_inputs
+from tests.test_gpu_mxfp4_attention import close
 
 pytestmark = pytest.mark.gpu
 
@@ -65,3 +67,25 @@ def test_expert_over_both_cache_types():
         runs.append((lambda ws, Ls=Ls, S=S, Smax=Smax, d=dtype: ea.expert_attn_layers(Ls, S, Smax, 0, d, ws), [L.out for L in Ls], n))
     alloc = lambda n: ea.alloc_workspace(n, 1152, ea.EA_KV_FP8_E4M3)  # noqa: E731
     in_turn(runs, alloc(64), alloc, one_rounding)
+
+
+@pytest.mark.parametrize("form", ["decode", "expert"])
+def test_small_calls_between_large_ones_over_a_4_bit_cache(form):
+    """What a large call leaves in a workspace does not reach the small one's outputs."""
+    call, alloc, ref, hq, tok = {
+        "decode": (ea.text_decode_attention_mxfp4, ea.alloc_decode_mxfp4_workspace, decode_oracle, 64, 1),
+        "expert": (ea.expert_attn_layers_mxfp4, ea.alloc_mxfp4_workspace, expert_oracle, 16, 64)}[form]
+    ws = alloc(64)
+    h = random_cache(3, 512, 400)
+    many = [device_buffers(step_inputs(l, hq, tok), h.device()) for l in range(64)]
+    xs, hs = [step_inputs(100 + l, hq, tok) for l in range(3)], [random_cache(8 + l, 1088, 1000) for l in range(3)]
+    few = [device_buffers(a, b.device()) for a, b in zip(xs, hs)]
+    want = [ref(a, b, 1000, 0)["out"] for a, b in zip(xs, hs)]
+    for turn in range(3):
+        call(many, 400, 512, 0, ws)
+        for b in few:
+            b.out.fill_(float("nan"))
+        call(few, 1000, 1088, 0, ws)
+        for l in range(3):
+            close(few[l].out, want[l], f"turn {turn}, layer {l}")
+    check_status(ws)
