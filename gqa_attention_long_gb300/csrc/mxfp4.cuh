@@ -104,7 +104,7 @@ __device__ __forceinline__ void mx_values8(uint32_t w, float scale, float (&x)[8
 // above -> 3), and a row that is off in its last fp32 bits can land on another code than the
 // formula's. So the row is formed in fp32 with a bound on its error, and where the bound leaves a code or an
 // exponent open (about one row in two hundred), once more as unevaluated sums h + l of two fp32 numbers
-// (about 2^-45 relative). FP64 arithmetic, 1/60 of the fp32 rate here, would bound the kernels; pairs
+// (about 2^-45 relative; Dekker's and Knuth's error-free sums). FP64 arithmetic, 1/60 of the fp32 rate here, would bound the kernels; pairs
 // throughout took three times the instructions.
 struct Pair {
   float h, l;
@@ -146,8 +146,9 @@ __device__ __forceinline__ Pair pair_rsqrt_mean(Pair ss) {
 __device__ __forceinline__ int f16_exponent(float amax) {
   return amax == 0.f ? 0 : min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -126), 126);
 }
-// A q row held by an octet, times the power of two that puts its largest magnitude in [1, 2) (so that f16
-// holds any gain's rows); factor = scale over that power.
+// A q row held by an octet, times the power of two that puts its largest magnitude in [1, 2), so that f16 holds any gain's
+// rows, to 11 bits down to 2^-14 of their largest channel (tensor cores take 16-bit operands beside codes, and a
+// rounding of 2^-12 in a score's terms stays under the bf16 output's); factor = scale over that power.
 __device__ __forceinline__ void f16_row(float (&yl)[8], float (&yh)[8], float scale, float& factor) {
   float amax = 0.f;
 #pragma unroll

@@ -3,7 +3,8 @@
 // Per (layer, kv head) unit: 128 folded query rows (2 heads x 64 tokens) against cache rows [0, S) and
 // the 64 own rows, softmax(Q K^T / sqrt(128)) V over the stored values.
 //
-// A prologue kernel norms and ropes q and k, stages q as f16 tiles (times a power of two per row) and
+// A prologue kernel norms and ropes q and k, stages q as f16 tiles (times a power of two per row; 11 bits, of which a
+// score of unit variance feels 2^-12, against 2^-9 of the bf16 output; the weights P are f16 for the same reason) and
 // encodes the own rows into the cache; the attention kernel follows; units cut over several CTAs
 // are joined by a merge kernel. The units' tiles of 128 keys (ceil(S / 128), then the own rows) are cut into
 // one contiguous range per CTA, one CTA per SM.
@@ -28,8 +29,8 @@
 // with the maximum that it last knew (raised when a chunk's weights pass it by far) and compares notes with
 // tile n - 1's at the end, through shared memory: only where the two differ is P(n), or the accumulator, scaled.
 //
-// Measured: 64 layers at S = 4700 156 us (of these the prologue 15, the merge 2), 2 layers at S = 65537 65 us,
-// 1 layer at S = 4700 16.6 us, at S = 256 11.4 us. A tile takes about 1,800 cycles, of which its MMAs are 1,025 (tensor pipe
+// Measured: 64 layers at S = 4700 158 us (of these the prologue 15, the merge 2), 2 layers at S = 65537 66 us,
+// 1 layer at S = 4700 16.8 us, at S = 256 11.8 us. A tile takes about 1,800 cycles, of which its MMAs are 1,025 (tensor pipe
 // 50 % busy). No unit is full: a converter spends 1,100 cycles on a row and 700 on its waits and hand-overs, a
 // softmax warpgroup 2,700 on a tile, of which three are in flight, and together they take 60 % of the issue slots.
 // Tried and slower, at 64 layers: tiles of 96 keys with four score buffers (+13 %: a tile's fixed costs), two

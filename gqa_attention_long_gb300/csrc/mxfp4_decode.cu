@@ -32,12 +32,12 @@
 // twelve compute warps take its chunks in turn (64 layers at pos 4700: 79 us with eight). Where a unit ends a
 // warp leaves its partial in shared memory and goes on with the next: four further warps join the
 // partials, after they have prepared the next units' q rows and encoded the new rows. (When all warps met at a
-// unit's end, each lost up to a chunk's time there: 64 layers 72.7 us, now 65.7.) A unit cut over several CTAs
+// unit's end, each lost up to a chunk's time there: 64 layers 72.7 us, 65.7 without.) A unit cut over several CTAs
 // is merged by the part that finishes last.
 //
-// Measured: 64 layers at pos 4700 63.7 us (5.2 TB/s, 76 % of a plain copy), 4 layers at pos 131070 98 us (5.8 TB/s,
-// 86 %); 1 layer at pos 4700 8.2 us, at pos 300 5.2 us. What holds it below the copy: the conversions share the ALU
-// pipe (57 % busy) and the issue slots (50 %) with the softmax; at one layer the latencies of the launch, one
+// Measured: 64 layers at pos 4700 65.3 us (5.1 TB/s, 74 % of a plain copy), 4 layers at pos 131070 100 us (5.7 TB/s,
+// 84 %); 1 layer at pos 4700 8.3 us, at pos 300 5.0 us. What holds it below the copy: the conversions share the ALU
+// pipe (60 % busy) and the issue slots (55 %) with the softmax; at one layer the latencies of the launch, one
 // chunk's load, the parts' arrival and the merge.
 #include "mxfp4.cuh"
 #include "rope.cuh"

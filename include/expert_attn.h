@@ -309,7 +309,8 @@ int text_decode_attention(const ea_decode_args* layers, int n_layers, int pos, i
  * code * 2^(scale - 127). The functions below write rows into such caches, read them back and
  * attend over them. The attentions take K and V as stored, without rounding: scales may differ within a call by up to
  * 2^100 (what lies further below the largest may count as zero). They run at full speed while V's (the expert's: K's and V's)
- * stay within 2^10 (2^20) of one another. A scale byte of 255 stands for NaN: none of the library's writers stores one,
+ * stay within 2^10 (2^20) of one another; the decode step takes K's scales up to 2^117. q rows and softmax weights are held
+ * with 11 bits. A scale byte of 255 stands for NaN: none of the library's writers stores one,
  * and an attention that meets one in a row it reads gives undefined output.
  * Asynchrony, ownership and errors are those of the functions above. What one call writes must not
  * overlap: a cache's codes or scales (or, of the reader, rows) that stand twice are EA_ERR_INVALID_ARG. */
