@@ -465,12 +465,14 @@ _device_now = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _stream_now = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _current(a: _Arr, maker: str, Smax: int, stream, ws: torch.Tensor | None = None) -> int | None:
-    """Checks a call's arguments against its marshalled ones; the stream's handle."""
+def _current(a: _Arr, maker: str, Smax: int, at: int, n: int, stream, ws: torch.Tensor | None = None) -> int | None:
+    """Checks a call's arguments (at, n: its other numbers) against its marshalled ones; the stream's handle."""
     if not isinstance(a, _Arr) or a.maker != maker:  # (the decode step's and the expert's are of one struct)
         raise TypeError(f"marshalled arguments of {maker} are expected")
     if a.device != _device_now() or (ws is not None and ws.get_device() != a.device):
         raise ValueError(f"the tensors are on cuda:{a.device}, which must be the current device (and the workspace's)")
+    if not (-0x80000000 <= at <= 0x7FFFFFFF and -0x80000000 <= n <= 0x7FFFFFFF):  # (ctypes would cut them)
+        raise ValueError(f"{at} or {n} does not fit 32 bits")
     if a.Smax != Smax:
         raise ValueError(f"the arguments were made for caches of {a.Smax} rows, not {Smax}")
     if ws is not None and (ws.dtype is not torch.uint8 or not ws.is_contiguous()):
@@ -520,7 +522,7 @@ def make_rows_args(layers: list[Mxfp4Rows], Smax: int) -> _Arr:
 
 def _rows_call(fn: str, layers, row0: int, n_rows: int, Smax: int, stream, a: _Arr | None) -> None:
     a = a if a is not None else make_rows_args(layers, Smax)
-    st = _current(a, "make_rows_args", Smax, stream)
+    st = _current(a, "make_rows_args", Smax, row0, n_rows, stream)
     if n_rows > a.n_rows:
         raise ValueError(f"k and v have {a.n_rows} rows, {n_rows} are asked for")
     if n_rows == 0:
@@ -624,7 +626,7 @@ def text_decode_attention_mxfp4(layers: list[DecodeMxfp4Buffers], pos: int, Smax
                                 stream=None, _arr=None) -> None:
     """One decode step over 4-bit caches: the new row quantised into row pos, then attention over rows [0, pos]."""
     a = _arr if _arr is not None else make_decode_mxfp4_args(layers, Smax)
-    st = _current(a, "make_decode_mxfp4_args", Smax, stream, ws)
+    st = _current(a, "make_decode_mxfp4_args", Smax, pos, rope_delta, stream, ws)
     rc = (_lib_handle or lib()).text_decode_attention_mxfp4(a.arr, a.n, int(pos), int(Smax), int(rope_delta), ws.data_ptr(),
                                                                ws.numel(), st)
     if rc:
@@ -636,7 +638,7 @@ def expert_attn_layers_mxfp4(layers: list[LayerMxfp4Buffers], S: int, Smax: int,
     """The expert's attention over 4-bit caches: the own rows quantised into rows [Smax-64, Smax), then attention
     over rows [0, S) and the own rows."""
     a = _arr if _arr is not None else make_mxfp4_args(layers, Smax)
-    st = _current(a, "make_mxfp4_args", Smax, stream, ws)
+    st = _current(a, "make_mxfp4_args", Smax, S, rope_delta, stream, ws)
     rc = (_lib_handle or lib()).expert_attn_layers_mxfp4(a.arr, a.n, int(S), int(Smax), int(rope_delta), ws.data_ptr(),
                                                             ws.numel(), st)
     if rc:

@@ -56,3 +56,23 @@ def test_arguments_for_another_cache_length_are_refused(calls):
     with pytest.raises(ValueError, match="128 rows"):
         ea.text_decode_attention_mxfp4(None, 10, 192, 0, Ws, _arr=dec)
     assert calls == []
+
+
+@pytest.mark.parametrize("far", [1 << 31, (1 << 32) + 3, -(1 << 32) + 3])
+def test_numbers_past_32_bits_are_refused(calls, far):
+    """ctypes would cut them: row 2^32 + 3 is not row 3."""
+    dec = ea.make_decode_mxfp4_args([bufs(ea.DecodeMxfp4Buffers, 64, 1)], 128)
+    exp = ea.make_mxfp4_args([bufs(ea.LayerMxfp4Buffers, 16, 64)], 128)
+    z = torch.zeros(8, 4, 128)
+    c = ea.alloc_mxfp4_cache(128, "cpu")
+    a = _lib._Arr("make_rows_args", (_lib.EaMxfp4Rows * 1)(), [z, c], None, 2, (512, 128), 4, 128)
+    for f in (lambda: ea.text_decode_attention_mxfp4(None, far, 128, 0, Ws, _arr=dec),
+              lambda: ea.text_decode_attention_mxfp4(None, 10, 128, far, Ws, _arr=dec),
+              lambda: ea.expert_attn_layers_mxfp4(None, far, 128, 0, Ws, _arr=exp),
+              lambda: ea.expert_attn_layers_mxfp4(None, 10, 128, far, Ws, _arr=exp),
+              lambda: ea.expert_attn_write_mxfp4(None, far, 1, 128, _arr=a),
+              lambda: ea.expert_attn_read_mxfp4(None, far, 1, 128, _arr=a),
+              lambda: ea.expert_attn_write_mxfp4(None, 0, -abs(far) - 1, 128, _arr=a)):
+        with pytest.raises(ValueError, match="32 bits"):
+            f()
+    assert calls == []
