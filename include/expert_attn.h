@@ -79,7 +79,7 @@ typedef struct {
 /* Utility (no counterpart on the pages). Bytes of device workspace needed by a call over
  * n_layers layers of the given cache dtype on
  * the current device (0 if no suitable device is present; an e4m3 workspace also serves bf16
- * calls). The workspace must be 256-byte aligned and, before
+ * calls, and one for more layers serves calls over fewer, in any order). The workspace must be 256-byte aligned and, before
  * its first use, cleared with expert_attn_workspace_init. */
 size_t expert_attn_workspace_size(int n_layers, int Smax, int kv_dtype);
 
@@ -286,7 +286,7 @@ typedef struct {
 } ea_decode_args;
 
 /* Bytes of workspace for text_decode_attention over n_layers layers per call on the current
- * device (0 if no suitable device is present). */
+ * device (0 if no suitable device is present). It serves calls over any number of layers, in any order. */
 size_t text_decode_workspace_size(int n_layers);
 
 /* Zeroes the status word and the per-unit arrival counts (cudaMemsetAsync on `stream`). Call
@@ -310,7 +310,7 @@ int text_decode_attention(const ea_decode_args* layers, int n_layers, int pos, i
  * attend over them. The attentions take K and V as stored, without rounding: scales may differ within a call by up to
  * 2^100 (what lies further below the largest may count as zero). They run at full speed while V's (the expert's: K's and V's)
  * stay within 2^10 (2^20) of one another; the decode step takes K's scales up to 2^117. q rows and softmax weights are held
- * with 11 bits. A scale byte of 255 stands for NaN: none of the library's writers stores one,
+ * with 11 bits; q_raw's and k_raw's squares are summed in fp32 (values below 2^60). A scale byte of 255 stands for NaN: none of the library's writers stores one,
  * and an attention that meets one in a row it reads gives undefined output.
  * Asynchrony, ownership and errors are those of the functions above. What one call writes must not
  * overlap: a cache's codes or scales (or, of the reader, rows) that stand twice are EA_ERR_INVALID_ARG. */
