@@ -138,6 +138,8 @@ def prepare(case, seed):
                 st["q"][i], st["k"][i], st["v"][i], st["q_gamma"][i], st["k_gamma"][i], caches[i], st["out"][i], st["k_new"][i],
                 st["v_new"][i], st["weight"][i] if w else None, st["weight_out"][i] if w else None) for i in range(n)], Smax)
             st["ws"] = ea.alloc_decode_fp8_workspace(n, Smax, weights=w)
+            st["got"] = (st["out"], st["k_new"], st["v_new"], *_tail(st))
+            st["got"] += (st["weight_out"][..., :case["pos"] + 1],) if w else ()
         elif case["op"] == "write":
             st["args"] = ea.make_fp8_rows_args([ea.Fp8Rows(st["k"][i], st["v"][i], caches[i]) for i in range(n)], Smax)
             st["back"] = ea.make_fp8_rows_args([ea.Fp8Rows(st["k_back"][i], st["v_back"][i], caches[i]) for i in range(n)], Smax)
@@ -146,6 +148,10 @@ def prepare(case, seed):
             st["args"] = ea.make_evict_fp8_args([ea.EvictFp8Buffers(caches[i], st["weight"][i], st["kept"][i], to[i],
                                                                   st["weight_out"][i]) for i in range(n)], Smax)
             st["ws"] = ea.alloc_evict_fp8_workspace(n, Smax)
+            keep = case["keep"]
+            k, v = (c[:, :, :keep].view(E4M3) for c in st["to"])
+            ks, vs = (s[..., :(keep - 1) // BLOCK + 1] for s in st["to_scale"])
+            st["got"] = (st["kept"], st["weight_out"][..., :keep], k, v, ks, vs)
     return st
 
 
@@ -257,14 +263,10 @@ def run(st):
         ea.expert_attn_read_fp8(None, a, b - a, Smax, _arr=st["back"])
         return st["k_back"], st["v_back"]
     if case["op"] == "evict":
-        rows, keep = case["rows"], case["keep"]
-        ea.expert_attn_evict_fp8(None, rows, keep, case["first"], case["recent"], Smax, st["ws"], _arr=st["args"])
-        k, v = (c[:, :, :keep].view(E4M3) for c in st["to"])
-        ks, vs = (s[..., :(keep - 1) // BLOCK + 1] for s in st["to_scale"])
-        return st["kept"], st["weight_out"][..., :keep], k, v, ks, vs
+        ea.expert_attn_evict_fp8(None, case["rows"], case["keep"], case["first"], case["recent"], Smax, st["ws"], _arr=st["args"])
+        return st["got"]
     ea.text_decode_attention_fp8(None, case["pos"], Smax, case["delta"], st["ws"], _arr=st["args"])
-    got = (st["out"], st["k_new"], st["v_new"], *_tail(st))
-    return got if case["op"] == "decode" else (*got, st["weight_out"][..., :case["pos"] + 1])
+    return st["got"]
 
 
 def work(case):
