@@ -20,4 +20,9 @@ from ._lib import (  # noqa: F401
     text_decode_mxfp4_workspace_size,
     LayerMxfp4Buffers, alloc_mxfp4_workspace, make_mxfp4_args, expert_attn_layers_mxfp4,
     expert_attn_mxfp4_workspace_size,
+    Fp8Cache, alloc_fp8_cache, Fp8Rows, make_fp8_rows_args, expert_attn_write_fp8, expert_attn_read_fp8,
+    DecodeFp8Buffers, alloc_decode_fp8_workspace, make_decode_fp8_args, text_decode_attention_fp8,
+    text_decode_fp8_workspace_size,
+    EvictFp8Buffers, alloc_evict_fp8_workspace, make_evict_fp8_args, expert_attn_evict_fp8,
+    expert_attn_evict_fp8_workspace_size,
 )

@@ -49,6 +49,22 @@ class EaAttnMxfp4Args(ctypes.Structure):  # ea_decode_mxfp4_args and ea_layer_mx
         "out", "k_new", "v_new")]
 
 
+class EaFp8Rows(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_cache", "v_cache", "k_scale", "v_scale")]
+
+
+class EaDecodeFp8Args(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "q_raw", "k_raw", "v_raw", "q_gamma", "k_gamma", "k_cache", "v_cache", "k_scale", "v_scale", "out", "k_new",
+        "v_new", "weight_in", "weight_out")]
+
+
+class EaEvictFp8Args(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "k_cache", "v_cache", "k_scale", "v_scale", "weight", "k_dst", "v_dst", "k_scale_dst", "v_scale_dst", "weight_dst",
+        "kept")]
+
+
 _lib_handle = None
 
 
@@ -62,6 +78,7 @@ def lib() -> ctypes.CDLL:
         h = ctypes.CDLL(LIB_PATH)
         P, I, S, V = ctypes.POINTER(EaLayerArgs), ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p
         R, M, L = ctypes.POINTER(EaMxfp4Rows), ctypes.POINTER(EaAttnMxfp4Args), ctypes.c_int64
+        F = ctypes.POINTER(EaFp8Rows)
         sig = {
             "expert_attn_workspace_size": (S, [I, I, I]),
             "expert_attn_workspace_init": (I, [V, S, V]),
@@ -88,6 +105,12 @@ def lib() -> ctypes.CDLL:
             "text_decode_attention_mxfp4": (I, [M, I, I, I, I, V, S, V]),
             "expert_attn_mxfp4_workspace_size": (S, [I]),
             "expert_attn_layers_mxfp4": (I, [M, I, I, I, I, V, S, V]),
+            "expert_attn_write_fp8": (I, [F, I, I, I, I, I, L, L, V]),
+            "expert_attn_read_fp8": (I, [F, I, I, I, I, I, L, L, V]),
+            "text_decode_fp8_workspace_size": (S, [I, I, I]),
+            "text_decode_attention_fp8": (I, [ctypes.POINTER(EaDecodeFp8Args), I, I, I, I, V, S, V]),
+            "expert_attn_evict_fp8_workspace_size": (S, [I, I]),
+            "expert_attn_evict_fp8": (I, [ctypes.POINTER(EaEvictFp8Args), I, I, I, I, I, I, V, S, V]),
         }
         for name, (res, args) in sig.items():
             f = getattr(h, name)
@@ -497,11 +520,11 @@ class Mxfp4Rows:
 _ROWS_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
-def make_rows_args(layers: list[Mxfp4Rows], Smax: int) -> _Arr:
-    """Marshalled arguments of expert_attn_write_mxfp4 and expert_attn_read_mxfp4."""
+def _rows_arr(struct, layers):
+    """An array of `struct` with the layers' k and v, after the checks that all row calls share; the first layer's k."""
     if not layers:
         raise ValueError("no layers")
-    arr, first = (EaMxfp4Rows * len(layers))(), layers[0].k
+    arr, first = (struct * len(layers))(), layers[0].k
     for a, L in zip(arr, layers):
         for name, t in (("k", L.k), ("v", L.v)):
             if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -515,14 +538,21 @@ def make_rows_args(layers: list[Mxfp4Rows], Smax: int) -> _Arr:
                 raise ValueError(f"{name} has strides {t.stride()}: contiguous channels and the same strides in every "
                                  "layer are expected")
         a.k, a.v = L.k.data_ptr(), L.v.data_ptr()
+    return arr, first
+
+
+def make_rows_args(layers: list[Mxfp4Rows], Smax: int) -> _Arr:
+    """Marshalled arguments of expert_attn_write_mxfp4 and expert_attn_read_mxfp4."""
+    arr, first = _rows_arr(EaMxfp4Rows, layers)
+    for a, L in zip(arr, layers):
         _mx_cache(a, L.cache, Smax)
     dev = _one_device([t for L in layers for t in (L.k, L.v, *L.cache.__dict__.values())], "rows")
     return _Arr("make_rows_args", arr, list(layers), dev, _ROWS_DTYPES[first.dtype], (first.stride(0), first.stride(1)), first.shape[1], Smax)
 
 
-def _rows_call(fn: str, layers, row0: int, n_rows: int, Smax: int, stream, a: _Arr | None) -> None:
-    a = a if a is not None else make_rows_args(layers, Smax)
-    st = _current(a, "make_rows_args", Smax, row0, n_rows, stream)
+def _rows_call(fn: str, layers, row0: int, n_rows: int, Smax: int, stream, a: _Arr | None, make=make_rows_args) -> None:
+    a = a if a is not None else make(layers, Smax)
+    st = _current(a, make.__name__, Smax, row0, n_rows, stream)
     if n_rows > a.n_rows:
         raise ValueError(f"k and v have {a.n_rows} rows, {n_rows} are asked for")
     if n_rows == 0:
@@ -643,3 +673,161 @@ def expert_attn_layers_mxfp4(layers: list[LayerMxfp4Buffers], S: int, Smax: int,
                                                             ws.numel(), st)
     if rc:
         _check("expert_attn_layers_mxfp4", rc)
+
+
+# ------------------------------------------------------------------------------- 8-bit cache (e4m3)
+@dataclass
+class Fp8Cache:
+    """One layer's e4m3 K and V caches (include/expert_attn.h): codes, and a scale for each head and block of 128 rows."""
+    k_cache: torch.Tensor  # uint8 or float8_e4m3fn [8, Smax, 128]
+    v_cache: torch.Tensor
+    k_scale: torch.Tensor  # fp32 [8, Smax // 128 + 1]
+    v_scale: torch.Tensor
+
+
+def alloc_fp8_cache(Smax: int, device="cuda") -> Fp8Cache:
+    """An 8-bit cache of Smax rows that holds none yet: codes of zero, scales of one."""
+    codes = lambda: torch.zeros(8, Smax, 128, dtype=torch.uint8, device=device)  # noqa: E731
+    return Fp8Cache(codes(), codes(), *(torch.ones(8, Smax // 128 + 1, device=device) for _ in range(2)))
+
+
+def _f8_cache(c: Fp8Cache, Smax: int, what: str = "") -> tuple:
+    u8 = (torch.uint8, torch.float8_e4m3fn)
+    return (_ptr(c.k_cache, what + "k_cache", u8, 8 * Smax * 128), _ptr(c.v_cache, what + "v_cache", u8, 8 * Smax * 128),
+            _ptr(c.k_scale, what + "k_scale", torch.float32, 8 * (Smax // 128 + 1)),
+            _ptr(c.v_scale, what + "v_scale", torch.float32, 8 * (Smax // 128 + 1)))
+
+
+@dataclass
+class Fp8Rows:
+    """Rows of one layer's K and V beside the 8-bit cache they go to or come from."""
+    k: torch.Tensor  # [8, n, 128] bf16, fp16 or fp32; any head and row strides, channels contiguous
+    v: torch.Tensor  # the same shape, type and strides
+    cache: Fp8Cache
+
+
+def make_fp8_rows_args(layers: list[Fp8Rows], Smax: int) -> _Arr:
+    """Marshalled arguments of expert_attn_write_fp8 and expert_attn_read_fp8."""
+    arr, first = _rows_arr(EaFp8Rows, layers)
+    for a, L in zip(arr, layers):
+        a.k_cache, a.v_cache, a.k_scale, a.v_scale = _f8_cache(L.cache, Smax)
+    dev = _one_device([t for L in layers for t in (L.k, L.v, *L.cache.__dict__.values())], "rows")
+    return _Arr("make_fp8_rows_args", arr, list(layers), dev, _ROWS_DTYPES[first.dtype], (first.stride(0), first.stride(1)), first.shape[1], Smax)
+
+
+def expert_attn_write_fp8(layers: list[Fp8Rows], row0: int, n_rows: int, Smax: int, stream=None, _arr=None) -> None:
+    """Appends the first n_rows rows of every layer's k and v to its cache, which holds rows [0, row0)."""
+    _rows_call("expert_attn_write_fp8", layers, row0, n_rows, Smax, stream, _arr, make_fp8_rows_args)
+
+
+def expert_attn_read_fp8(layers: list[Fp8Rows], row0: int, n_rows: int, Smax: int, stream=None, _arr=None) -> None:
+    """Fills the first n_rows rows of every layer's k and v with the values of its cache's rows [row0, row0 + n_rows)."""
+    _rows_call("expert_attn_read_fp8", layers, row0, n_rows, Smax, stream, _arr, make_fp8_rows_args)
+
+
+@dataclass
+class DecodeFp8Buffers:
+    """One layer's device tensors for text_decode_attention_fp8 (include/expert_attn.h)."""
+    q_raw: torch.Tensor    # bf16 [64, 128]
+    k_raw: torch.Tensor    # bf16 [8, 128]
+    v_raw: torch.Tensor    # bf16 [8, 128]
+    q_gamma: torch.Tensor  # bf16 [128]
+    k_gamma: torch.Tensor  # bf16 [128]
+    cache: Fp8Cache
+    out: torch.Tensor      # bf16 [64, 128]
+    k_new: torch.Tensor | None = None  # optional bf16 [8, 128]: the new row's stored values
+    v_new: torch.Tensor | None = None
+    weight_in: torch.Tensor | None = None   # optional fp32 [8, Smax]: the rows' weight sums before this step
+    weight_out: torch.Tensor | None = None  # optional fp32 [8, Smax]: and after it (may be the same tensor)
+
+
+def make_decode_fp8_args(layers: list[DecodeFp8Buffers], Smax: int) -> _Arr:
+    """Marshalled arguments of text_decode_attention_fp8, for loops that call it often."""
+    if not layers:
+        raise ValueError("no layers")
+    arr, bf, f32 = (EaDecodeFp8Args * len(layers))(), torch.bfloat16, torch.float32
+    for a, L in zip(arr, layers):
+        for name, n in (("q_raw", 64), ("k_raw", 8), ("v_raw", 8), ("q_gamma", 1), ("k_gamma", 1), ("out", 64), ("k_new", 8), ("v_new", 8)):
+            setattr(a, name, _ptr(getattr(L, name), name, bf, n * 128))
+        a.weight_in, a.weight_out = _ptr(L.weight_in, "weight_in", f32, 8 * Smax), _ptr(L.weight_out, "weight_out", f32, 8 * Smax)
+        a.k_cache, a.v_cache, a.k_scale, a.v_scale = _f8_cache(L.cache, Smax)
+    dev = _one_device([t for L in layers for t in (*(v for k, v in L.__dict__.items() if k != "cache"), *L.cache.__dict__.values())], "layers")
+    return _Arr("make_decode_fp8_args", arr, list(layers), dev, Smax=Smax)
+
+
+def text_decode_fp8_workspace_size(n_layers: int, Smax: int, weights: bool = False) -> int:
+    return int(lib().text_decode_fp8_workspace_size(int(n_layers), int(Smax), int(weights)))
+
+
+def alloc_decode_fp8_workspace(n_layers: int, Smax: int, weights: bool = False, device="cuda") -> torch.Tensor:
+    """A cleared workspace for text_decode_attention_fp8 (torch-allocated); weights: whether calls ask for weight_out."""
+    return _mx_workspace(text_decode_fp8_workspace_size(n_layers, Smax, weights), "text_decode_fp8_workspace_size",
+                         text_decode_workspace_init, device)
+
+
+def text_decode_attention_fp8(layers: list[DecodeFp8Buffers], pos: int, Smax: int, rope_delta: int, ws: torch.Tensor,
+                              stream=None, _arr=None) -> None:
+    """One decode step over 8-bit caches: the new row appended as row pos, then attention over rows [0, pos]."""
+    a = _arr if _arr is not None else make_decode_fp8_args(layers, Smax)
+    st = _current(a, "make_decode_fp8_args", Smax, pos, rope_delta, stream, ws)
+    rc = (_lib_handle or lib()).text_decode_attention_fp8(a.arr, a.n, int(pos), int(Smax), int(rope_delta), ws.data_ptr(),
+                                                          ws.numel(), st)
+    if rc:
+        _check("text_decode_attention_fp8", rc)
+
+
+@dataclass
+class EvictFp8Buffers:
+    """One layer's device tensors for expert_attn_evict_fp8 (include/expert_attn.h). Without `to` and `weight_to`
+    the kept rows move up within the cache."""
+    cache: Fp8Cache
+    weight: torch.Tensor  # fp32 [8, Smax]
+    kept: torch.Tensor    # int32 [8, n_keep]: receives the rows that were kept
+    to: Fp8Cache | None = None
+    weight_to: torch.Tensor | None = None
+
+
+def make_evict_fp8_args(layers: list[EvictFp8Buffers], Smax: int) -> _Arr:
+    """Marshalled arguments of expert_attn_evict_fp8."""
+    if not layers:
+        raise ValueError("no layers")
+    arr, f32, n = (EaEvictFp8Args * len(layers))(), torch.float32, layers[0].kept.numel() // 8
+    for a, L in zip(arr, layers):
+        to, weight_to = L.to if L.to is not None else L.cache, L.weight_to if L.weight_to is not None else L.weight
+        a.k_cache, a.v_cache, a.k_scale, a.v_scale = _f8_cache(L.cache, Smax)
+        a.k_dst, a.v_dst, a.k_scale_dst, a.v_scale_dst = _f8_cache(to, Smax, "to.")
+        a.weight, a.weight_dst = _ptr(L.weight, "weight", f32, 8 * Smax), _ptr(weight_to, "weight_to", f32, 8 * Smax)
+        if L.kept.dim() != 2 or L.kept.shape[0] != 8:
+            raise ValueError(f"kept has shape {tuple(L.kept.shape)}: [8, n_keep] is expected")
+        a.kept = _ptr(L.kept, "kept", torch.int32, 8 * n)
+    dev = _one_device([t for L in layers for c in (L.cache, L.to) if c is not None for t in c.__dict__.values()] +
+                      [t for L in layers for t in (L.weight, L.kept, L.weight_to)], "layers")
+    return _Arr("make_evict_fp8_args", arr, list(layers), dev, n_rows=n, Smax=Smax)
+
+
+def expert_attn_evict_fp8_workspace_size(n_layers: int, Smax: int) -> int:
+    return int(lib().expert_attn_evict_fp8_workspace_size(int(n_layers), int(Smax)))
+
+
+def alloc_evict_fp8_workspace(n_layers: int, Smax: int, device="cuda") -> torch.Tensor:
+    """A cleared workspace for expert_attn_evict_fp8 (torch-allocated)."""
+    return _mx_workspace(expert_attn_evict_fp8_workspace_size(n_layers, Smax), "expert_attn_evict_fp8_workspace_size",
+                         expert_attn_workspace_init, device)
+
+
+def expert_attn_evict_fp8(layers: list[EvictFp8Buffers], n_rows: int, n_keep: int, n_first: int, n_recent: int, Smax: int,
+                          ws: torch.Tensor, stream=None, _arr=None) -> None:
+    """Of every head's n_rows rows the first n_first, the last n_recent and those of the largest weight stay, n_keep in all,
+    in their order, as rows [0, n_keep)."""
+    a = _arr if _arr is not None else make_evict_fp8_args(layers, Smax)
+    st = _current(a, "make_evict_fp8_args", Smax, n_rows, n_keep, stream, ws)
+    if not (0 <= n_first <= 0x7FFFFFFF and 0 <= n_recent <= 0x7FFFFFFF):  # (ctypes would cut them)
+        raise ValueError(f"n_first {n_first} and n_recent {n_recent} must not be negative, nor pass 32 bits")
+    if n_keep != a.n_rows:
+        raise ValueError(f"kept has room for {a.n_rows} rows a head, not {n_keep}")
+    if n_keep == 0:
+        return
+    rc = (_lib_handle or lib()).expert_attn_evict_fp8(a.arr, a.n, int(n_rows), int(n_keep), int(n_first), int(n_recent), int(Smax),
+                                                      ws.data_ptr(), ws.numel(), st)
+    if rc:
+        _check("expert_attn_evict_fp8", rc)

@@ -13,6 +13,7 @@
 #include <unordered_map>
 
 #include "expert_attn.h"
+#include "host.cuh"
 #include "internal.cuh"
 #include "ptx.cuh"
 
@@ -33,8 +34,6 @@ __global__ void quantize_cache_kernel(const __nv_bfloat16* src, uint8_t* dst, fl
 namespace {
 
 using namespace ea;
-
-constexpr int kMaxDevices = 64;
 
 // One thread waits, with a time limit, on an mbarrier that nothing arrives on, then the warp, with a limit of looks, on that
 // one and on one that is arrived on: the failure paths of the library's waits, made to run out on purpose (see the
@@ -66,31 +65,13 @@ __global__ void selftest_wait_kernel(uint32_t* status, uint64_t limit_ns) {
   if (threadIdx.x == 0 && gave_up && there) atomicOr(status, kErrSelftestLooks);
 }
 
-struct DeviceInfo {
-  bool init = false;
-  bool ok = false;
-  int sm_count = 0;
-};
 DeviceInfo g_dev[kMaxDevices];
 std::mutex g_mu;
 int g_splits = 0;
 
-// What a kernel's attributes need: done once for each device (they hold for the current device alone), and again where it
-// failed.
-class OncePerDevice {
- public:
-  template <class Set>
-  bool operator()(int dev, Set set) {
-    std::lock_guard<std::mutex> lk(mu_);
-    if (!done_[dev]) done_[dev] = set();
-    return done_[dev];
-  }
+}  // namespace
 
- private:
-  std::mutex mu_;
-  bool done_[kMaxDevices] = {};
-};
-
+namespace ea {
 // Queries (once per device) the SM count and that the device is an sm_103 part, and raises
 // the attention kernel's dynamic shared-memory limit.
 bool device_info(int* dev_out, DeviceInfo* info) {
@@ -117,6 +98,9 @@ bool device_info(int* dev_out, DeviceInfo* info) {
   *info = d;
   return d.ok;
 }
+}  // namespace ea
+
+namespace {
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                    const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
@@ -158,6 +142,9 @@ struct MapKeyHash {
 };
 std::unordered_map<MapKey, CUtensorMap, MapKeyHash> g_maps;
 
+}  // namespace
+
+namespace ea {
 // bf16 cache: box {64 channels, 128 rows, 1}; e4m3 cache: box {128 channels (bytes), 128, 1}.
 bool cache_map(const void* base, int S, int Smax, bool f8, CUtensorMap* out) {
   const MapKey key{base, S, Smax, f8};
@@ -192,7 +179,9 @@ bool cache_map(const void* base, int S, int Smax, bool f8, CUtensorMap* out) {
   return true;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+}  // namespace ea
+
+namespace {
 
 // Pure argument checks (no CUDA call), so that they also run on machines without a GPU.
 int validate(const ea_layer_args* a, int n_layers, int S, int Smax, int rope_delta, int kv_dtype,
@@ -255,6 +244,9 @@ int n_ctas_for(long long W, int sm_count) {
   return n < 1 ? 1 : n;
 }
 
+}  // namespace
+
+namespace ea {
 cudaLaunchConfig_t launch_config(cudaStream_t st, cudaLaunchAttribute* attr, bool pdl) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -265,6 +257,9 @@ cudaLaunchConfig_t launch_config(cudaStream_t st, cudaLaunchAttribute* attr, boo
   cfg.numAttrs = pdl ? 1 : 0;
   return cfg;
 }
+}  // namespace ea
+
+namespace {
 
 // The prologue is launched with programmatic stream serialization: its CTAs may become resident
 // while the preceding kernel drains, and wait (griddepcontrol.wait) for it before touching memory.
@@ -1136,29 +1131,6 @@ int validate_mx_cache(const void* kc, const void* ks, const void* vc, const void
   return EA_OK;
 }
 
-// Whether the arrays that one call writes, get(a[l])[0 .. N) of every layer, are all different: what stands twice
-// would be written twice, in any order.
-template <int N, class A, class Get>
-bool mx_distinct(const A* a, int n, Get get) {
-  constexpr uint32_t kSlots = 512;
-  static_assert(N * kMaxLayersPerLaunch <= kSlots / 2, "table");
-  for (int l0 = 0; l0 < n; l0 += kMaxLayersPerLaunch) {
-    const void* seen[kSlots] = {};
-    auto find = [&](const void* p) {  // p's place, or the free one where it belongs
-      uint32_t h = static_cast<uint32_t>((reinterpret_cast<uintptr_t>(p) >> 4) * 0x9E3779B97F4A7C15ull >> 55);
-      while (seen[h] != nullptr && seen[h] != p) h = (h + 1) % kSlots;
-      return h;
-    };
-    const int l1 = l0 + kMaxLayersPerLaunch < n ? l0 + kMaxLayersPerLaunch : n;
-    for (int l = l0; l < n; ++l)  // 64 layers into the table, the later ones against it
-      for (const void* p : get(a[l])) {
-        const uint32_t h = find(p);
-        if (seen[h] != nullptr) return false;
-        if (l < l1) seen[h] = p;
-      }
-  }
-  return true;
-}
 template <class A>
 bool mx_caches_distinct(const A* a, int n) {
   return mx_distinct<4>(a, n, [](const A& x) { return std::array<const void*, 4>{x.k_codes, x.v_codes, x.k_scales, x.v_scales}; });
@@ -1213,47 +1185,6 @@ int run_mx_rows(const ea_mxfp4_rows* a, int n_layers, int row0, int n_rows, int 
   }
   return EA_OK;
 }
-
-// Cosines and sines of pos * 5e6^(-j/64), |pos| < 2^24, in 64 bits (a far position's angle needs them): the product of
-// four rotations, by the position's base-64 digits, from a table that is formed once per process (64 library
-// sines and cosines would be half of a small call's time on the host).
-class MxRotations {
- public:
-  struct Cis {
-    double c, s;
-  };
-  static const MxRotations& get() {
-    static const MxRotations r;
-    return r;
-  }
-  Cis at(long long pos, int j) const {
-    const uint32_t a = static_cast<uint32_t>(pos < 0 ? -pos : pos);
-    Cis r = t_[0][a & 63][j];
-    for (int d = 1; d < 4; ++d)
-      if (const uint32_t k = (a >> (6 * d)) & 63) r = mul(r, t_[d][k][j]);
-    if (pos < 0) r.s = -r.s;
-    return r;
-  }
-  static Cis mul(const Cis& a, const Cis& b) { return {a.c * b.c - a.s * b.s, a.s * b.c + a.c * b.s}; }
-  // as fp32 pairs: cosine x + y, sine z + w
-  static float4 split(const Cis& a) {
-    const float c = static_cast<float>(a.c), s = static_cast<float>(a.s);
-    return make_float4(c, static_cast<float>(a.c - c), s, static_cast<float>(a.s - s));
-  }
-
- private:
-  MxRotations() {
-    for (int j = 0; j < kD / 2; ++j) {
-      const double f = std::pow(5.0e6, -static_cast<double>(j) / (kD / 2));
-      for (int d = 0; d < 4; ++d)
-        for (int k = 0; k < 64; ++k) {
-          const double x = std::ldexp(static_cast<double>(k), 6 * d) * f;
-          t_[d][k][j] = {std::cos(x), std::sin(x)};
-        }
-    }
-  }
-  Cis t_[4][64][kD / 2];
-};
 
 // Rotations of positions p0 + t, t < 64 (see MxPrologueParams): rot_a[i] at p0 + 8 i, rot_b[i] at i.
 void mx_rotations(long long p0, MxPrologueParams* p) {

@@ -1,0 +1,300 @@
+// api_fp8.cu — host side of the 8-bit cache's writer, reader, decode step and eviction: argument checks, launch planning and
+// the launches per chunk of 64 layers. See include/expert_attn.h for the contract.
+#include <array>
+#include <cstring>
+#include <mutex>
+
+#include "expert_attn.h"
+#include "host.cuh"
+#include "internal.cuh"
+
+namespace ea {
+cudaError_t launch_fp8_rows(const F8RowsParams& p, int n_layers, int dtype, bool write, cudaLaunchConfig_t cfg);
+cudaError_t fp8_decode_set_attributes();
+template <int CAP>
+cudaError_t launch_fp8_decode(const F8DecodeParams<CAP>& p, cudaLaunchConfig_t cfg);
+cudaError_t launch_fp8_evict(const F8EvictParams& p, int sm_count, cudaLaunchConfig_t cfg);
+}  // namespace ea
+
+namespace {
+
+using namespace ea;
+
+bool smax_ok(int Smax) { return Smax >= kScaleBlock && Smax % kScaleBlock == 0 && Smax <= (1 << 22); }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Pointers that have to be there, 16-byte aligned codes and rows and 4-byte aligned numbers.
+template <int N, int M>
+int check_pointers(const void* const (&wide)[N], const void* const (&narrow)[M]) {
+  for (const void* p : wide)
+    if (p == nullptr) return EA_ERR_INVALID_ARG;
+  for (const void* p : narrow)
+    if (p == nullptr) return EA_ERR_INVALID_ARG;
+  for (const void* p : wide)
+    if (!aligned16(p)) return EA_ERR_MISALIGNED;
+  for (const void* p : narrow)
+    if (!aligned4(p)) return EA_ERR_MISALIGNED;
+  return EA_OK;
+}
+
+int run_rows(const ea_fp8_rows* a, int n_layers, int row0, int n_rows, int Smax, int dtype, int64_t head_stride,
+             int64_t row_stride, bool write, ea_stream_t stream) {
+  if (a == nullptr || n_layers < 1) return EA_ERR_INVALID_ARG;
+  if (!smax_ok(Smax) || row0 < 0 || n_rows < 0 || n_rows > Smax - row0) return EA_ERR_INVALID_ARG;
+  if (dtype != EA_ROWS_BF16 && dtype != EA_ROWS_FP16 && dtype != EA_ROWS_FP32) return EA_ERR_INVALID_ARG;
+  constexpr int64_t kMaxStride = 1LL << 40;
+  if (head_stride < 0 || row_stride < 0 || head_stride > kMaxStride || row_stride > kMaxStride) return EA_ERR_INVALID_ARG;
+  const int64_t esz = dtype == EA_ROWS_FP32 ? 4 : 2;
+  if (head_stride * esz % 16 != 0 || (n_rows > 1 && row_stride * esz % 16 != 0)) return EA_ERR_MISALIGNED;
+  // rows that are written must not overlap
+  if (!write && (head_stride < kD || (n_rows > 1 && (row_stride < kD || (head_stride < (n_rows - 1) * row_stride + kD &&
+                                                                        row_stride < (kHkv - 1) * head_stride + kD)))))
+    return EA_ERR_INVALID_ARG;
+  for (int l = 0; l < n_layers; ++l) {
+    const ea_fp8_rows& x = a[l];
+    const int rc = check_pointers<4, 2>({x.k, x.v, x.k_cache, x.v_cache}, {x.k_scale, x.v_scale});
+    if (rc != EA_OK) return rc;
+  }
+  if (!(write ? mx_distinct<4>(a, n_layers, [](const ea_fp8_rows& x) {
+          return std::array<const void*, 4>{x.k_cache, x.v_cache, x.k_scale, x.v_scale};
+        })
+              : mx_distinct<2>(a, n_layers, [](const ea_fp8_rows& x) { return std::array<const void*, 2>{x.k, x.v}; })))
+    return EA_ERR_INVALID_ARG;
+  int dev;
+  DeviceInfo di;
+  if (!device_info(&dev, &di)) return EA_ERR_UNSUPPORTED;
+  if (n_rows == 0) return EA_OK;
+  F8RowsParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.head_stride = head_stride;
+  p.row_stride = n_rows > 1 ? row_stride : 0;
+  p.row0 = row0;
+  p.n_rows = n_rows;
+  p.Smax = Smax;
+  cudaLaunchAttribute attr[1];
+  for (int l0 = 0; l0 < n_layers; l0 += kMaxLayersPerLaunch) {
+    const int n = n_layers - l0 < kMaxLayersPerLaunch ? n_layers - l0 : kMaxLayersPerLaunch;
+    for (int l = 0; l < n; ++l) {
+      const ea_fp8_rows& x = a[l0 + l];
+      p.layer[l] = {x.k, x.v, static_cast<uint8_t*>(x.k_cache), static_cast<uint8_t*>(x.v_cache), x.k_scale, x.v_scale};
+    }
+    if (launch_fp8_rows(p, n, dtype, write, launch_config(static_cast<cudaStream_t>(stream), attr, true)) != cudaSuccess) {
+      cudaGetLastError();
+      return EA_ERR_CUDA;
+    }
+  }
+  return EA_OK;
+}
+
+bool decode_attrs_ready(int dev) {
+  static OncePerDevice once;
+  return once(dev, [] {
+    const bool ok = fp8_decode_set_attributes() == cudaSuccess;
+    cudaGetLastError();
+    return ok;
+  });
+}
+
+int validate_decode(const ea_decode_fp8_args* a, int n_layers, int pos, int Smax, long long p0, const void* ws) {
+  if (a == nullptr || n_layers < 1 || ws == nullptr) return EA_ERR_INVALID_ARG;
+  if (!smax_ok(Smax) || pos < 0 || pos >= Smax) return EA_ERR_INVALID_ARG;
+  if (p0 <= -(1LL << 24) || p0 >= (1LL << 24)) return EA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return EA_ERR_MISALIGNED;
+  for (int l = 0; l < n_layers; ++l) {
+    const ea_decode_fp8_args& x = a[l];
+    const int rc = check_pointers<8, 2>({x.q_raw, x.k_raw, x.v_raw, x.q_gamma, x.k_gamma, x.k_cache, x.v_cache, x.out},
+                                        {x.k_scale, x.v_scale});
+    if (rc != EA_OK) return rc;
+    if (x.weight_out == nullptr && x.weight_in != nullptr) return EA_ERR_INVALID_ARG;
+    if (!aligned16(x.k_new) || !aligned16(x.v_new) || !aligned16(x.weight_in) || !aligned16(x.weight_out))  // (null is aligned)
+      return EA_ERR_MISALIGNED;
+  }
+  // what is written stands once; sums that are read from elsewhere are not written
+  return mx_distinct<9>(a, n_layers, [](const ea_decode_fp8_args& x) {
+           return std::array<const void*, 9>{x.k_cache, x.v_cache, x.k_scale, x.v_scale, x.out, x.k_new, x.v_new, x.weight_out,
+                                             x.weight_in == x.weight_out ? nullptr : x.weight_in};
+         })
+             ? EA_OK
+             : EA_ERR_INVALID_ARG;
+}
+
+bool any_weights(const ea_decode_fp8_args* a, int n) {
+  for (int l = 0; l < n; ++l)
+    if (a[l].weight_out != nullptr) return true;
+  return false;
+}
+
+// Parameter blocks are large (24 KB at full capacity): kept off the stack, one per capacity, with a mutex of its own.
+template <int CAP>
+struct DecodeBlock {
+  F8DecodeParams<CAP> p;
+  std::mutex mu;
+};
+
+template <int CAP>
+int launch_decode_t(const ea_decode_fp8_args* a, int n, int pos, int Smax, long long p0, bool weights, uint8_t* ws,
+                    const F8DecodeWs& wl, int sm_count, cudaStream_t st) {
+  static DecodeBlock<CAP> block;
+  std::lock_guard<std::mutex> lk(block.mu);
+  F8DecodeParams<CAP>& p = block.p;
+  for (int l = 0; l < n; ++l) {
+    const ea_decode_fp8_args& x = a[l];
+    if (!cache_map(x.k_cache, 0, Smax, true, &p.kmap[l]) || !cache_map(x.v_cache, 0, Smax, true, &p.vmap[l])) return EA_ERR_CUDA;
+    auto bf = [](const void* q) { return static_cast<const __nv_bfloat16*>(q); };
+    p.layer[l] = {bf(x.q_raw), bf(x.k_raw), bf(x.v_raw), bf(x.q_gamma), bf(x.k_gamma), static_cast<uint8_t*>(x.k_cache),
+                  static_cast<uint8_t*>(x.v_cache), x.k_scale, x.v_scale, static_cast<__nv_bfloat16*>(x.out),
+                  static_cast<__nv_bfloat16*>(x.k_new), static_cast<__nv_bfloat16*>(x.v_new), x.weight_in, x.weight_out};
+  }
+  for (int j = 0; j < kD / 2; ++j) p.rot[j] = MxRotations::split(MxRotations::get().at(p0, j));
+  p.part_o = reinterpret_cast<float*>(ws + wl.part_o_off);
+  p.part_ml = reinterpret_cast<float*>(ws + wl.part_ml_off);
+  p.unit_cnt = reinterpret_cast<uint32_t*>(ws + wl.cnt_off);
+  p.status = reinterpret_cast<uint32_t*>(ws);
+  p.scores = weights ? reinterpret_cast<float*>(ws + wl.scores_off) : nullptr;
+  p.lse = reinterpret_cast<float*>(ws + wl.lse_off);
+  p.T = pos / kKeyTile + 1;
+  p.W = static_cast<long long>(n) * kHkv * p.T;
+  p.pos = pos;
+  p.Smax = Smax;
+  p.n_layers = n;
+  p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(kD)));
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = launch_config(st, attr, true);
+  int n_ctas = sm_count < kMaxGridCtas ? sm_count : kMaxGridCtas;
+  if (static_cast<long long>(n_ctas) > p.W) n_ctas = static_cast<int>(p.W);
+  cfg.gridDim = dim3(n_ctas);
+  if (launch_fp8_decode<CAP>(p, cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return EA_ERR_CUDA;
+  }
+  return EA_OK;
+}
+
+// Whether [a, a + n) and [b, b + n) share bytes without being the same.
+bool partly(const void* a, const void* b, size_t n) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x != y && (x > y ? x - y : y - x) < n;
+}
+
+int validate_evict(const ea_evict_fp8_args* a, int n_layers, int n_rows, int n_keep, int n_first, int n_recent, int Smax,
+                   const void* ws) {
+  if (a == nullptr || n_layers < 1 || ws == nullptr || !smax_ok(Smax)) return EA_ERR_INVALID_ARG;
+  if (n_rows < 0 || n_rows > Smax || n_keep < 0 || n_keep > n_rows || n_first < 0 || n_recent < 0 || n_first > n_keep ||
+      n_recent > n_keep - n_first)
+    return EA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return EA_ERR_MISALIGNED;
+  const size_t codes = static_cast<size_t>(kHkv) * Smax * kD, sums = static_cast<size_t>(kHkv) * Smax * sizeof(float),
+               scales = static_cast<size_t>(kHkv) * (Smax / kScaleBlock + 1) * sizeof(float);
+  for (int l = 0; l < n_layers; ++l) {
+    const ea_evict_fp8_args& x = a[l];
+    const int rc = check_pointers<4, 7>({x.k_cache, x.v_cache, x.k_dst, x.v_dst},
+                                        {x.k_scale, x.v_scale, x.k_scale_dst, x.v_scale_dst, x.weight, x.weight_dst, x.kept});
+    if (rc != EA_OK) return rc;
+    const int same = (x.k_cache == x.k_dst) + (x.v_cache == x.v_dst) + (x.k_scale == x.k_scale_dst) + (x.v_scale == x.v_scale_dst) +
+                     (x.weight == x.weight_dst);
+    if (same != 0 && same != 5) return EA_ERR_INVALID_ARG;  // in place, or into other arrays
+    if (partly(x.k_cache, x.k_dst, codes) || partly(x.v_cache, x.v_dst, codes) || partly(x.k_scale, x.k_scale_dst, scales) ||
+        partly(x.v_scale, x.v_scale_dst, scales) || partly(x.weight, x.weight_dst, sums))
+      return EA_ERR_INVALID_ARG;
+  }
+  return mx_distinct<11>(a, n_layers, [](const ea_evict_fp8_args& x) {
+           const bool other = x.k_cache != x.k_dst;
+           auto src = [&](const void* q) { return other ? q : nullptr; };
+           return std::array<const void*, 11>{x.k_dst, x.v_dst, x.k_scale_dst, x.v_scale_dst, x.weight_dst, x.kept, src(x.k_cache),
+                                              src(x.v_cache), src(x.k_scale), src(x.v_scale), src(x.weight)};
+         })
+             ? EA_OK
+             : EA_ERR_INVALID_ARG;
+}
+
+}  // namespace
+
+extern "C" {
+
+int expert_attn_write_fp8(const ea_fp8_rows* layers, int n_layers, int row0, int n_rows, int Smax, int dtype,
+                          int64_t head_stride, int64_t row_stride, ea_stream_t stream) {
+  return run_rows(layers, n_layers, row0, n_rows, Smax, dtype, head_stride, row_stride, true, stream);
+}
+
+int expert_attn_read_fp8(const ea_fp8_rows* layers, int n_layers, int row0, int n_rows, int Smax, int dtype,
+                         int64_t head_stride, int64_t row_stride, ea_stream_t stream) {
+  return run_rows(layers, n_layers, row0, n_rows, Smax, dtype, head_stride, row_stride, false, stream);
+}
+
+size_t text_decode_fp8_workspace_size(int n_layers, int Smax, int weights) {
+  int dev;
+  DeviceInfo di;
+  if (n_layers < 1 || !smax_ok(Smax) || !device_info(&dev, &di)) return 0;
+  return f8_decode_ws(di.sm_count, n_layers, Smax, weights != 0).total;
+}
+
+int text_decode_attention_fp8(const ea_decode_fp8_args* layers, int n_layers, int pos, int Smax, int rope_delta,
+                              void* workspace, size_t ws_bytes, ea_stream_t stream) {
+  const long long p0 = static_cast<long long>(pos) + rope_delta;
+  int rc = validate_decode(layers, n_layers, pos, Smax, p0, workspace);
+  if (rc != EA_OK) return rc;
+  int dev;
+  DeviceInfo di;
+  if (!device_info(&dev, &di) || !decode_attrs_ready(dev)) return EA_ERR_UNSUPPORTED;
+  const int per = n_layers < kDecodeMaxLayers ? n_layers : kDecodeMaxLayers;
+  const F8DecodeWs wl = f8_decode_ws(di.sm_count, n_layers, Smax, any_weights(layers, n_layers));
+  if (ws_bytes < wl.total) return EA_ERR_WORKSPACE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  for (int l0 = 0; l0 < n_layers; l0 += per) {
+    const int n = n_layers - l0 < per ? n_layers - l0 : per;
+    const bool weights = any_weights(layers + l0, n);
+    rc = n <= kSmallCap ? launch_decode_t<kSmallCap>(layers + l0, n, pos, Smax, p0, weights, ws, wl, di.sm_count, st)
+                        : launch_decode_t<kDecodeMaxLayers>(layers + l0, n, pos, Smax, p0, weights, ws, wl, di.sm_count, st);
+    if (rc != EA_OK) return rc;
+  }
+  return EA_OK;
+}
+
+size_t expert_attn_evict_fp8_workspace_size(int n_layers, int Smax) {
+  int dev;
+  DeviceInfo di;
+  if (n_layers < 1 || !smax_ok(Smax) || !device_info(&dev, &di)) return 0;
+  return f8_evict_ws(n_layers, Smax).total;
+}
+
+int expert_attn_evict_fp8(const ea_evict_fp8_args* layers, int n_layers, int n_rows, int n_keep, int n_first, int n_recent,
+                          int Smax, void* workspace, size_t ws_bytes, ea_stream_t stream) {
+  const int rc = validate_evict(layers, n_layers, n_rows, n_keep, n_first, n_recent, Smax, workspace);
+  if (rc != EA_OK) return rc;
+  int dev;
+  DeviceInfo di;
+  if (!device_info(&dev, &di)) return EA_ERR_UNSUPPORTED;
+  const F8EvictWs wl = f8_evict_ws(n_layers, Smax);
+  if (ws_bytes < wl.total) return EA_ERR_WORKSPACE;
+  if (n_keep == 0) return EA_OK;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  F8EvictParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.status = reinterpret_cast<uint32_t*>(ws);
+  p.ticket = reinterpret_cast<uint32_t*>(ws + wl.ticket_off);
+  p.before = reinterpret_cast<uint32_t*>(ws + wl.before_off);
+  p.loaded = reinterpret_cast<uint32_t*>(ws + wl.loaded_off);
+  p.n_rows = n_rows;
+  p.n_keep = n_keep;
+  p.n_first = n_first;
+  p.n_recent = n_recent;
+  p.Smax = Smax;
+  p.blocks = Smax / kScaleBlock;
+  cudaLaunchAttribute attr[1];
+  for (int l0 = 0; l0 < n_layers; l0 += kMaxLayersPerLaunch) {
+    p.n_layers = n_layers - l0 < kMaxLayersPerLaunch ? n_layers - l0 : kMaxLayersPerLaunch;
+    for (int l = 0; l < p.n_layers; ++l) {
+      const ea_evict_fp8_args& x = layers[l0 + l];
+      p.layer[l] = {static_cast<const uint8_t*>(x.k_cache), static_cast<const uint8_t*>(x.v_cache), x.k_scale, x.v_scale, x.weight,
+                    static_cast<uint8_t*>(x.k_dst), static_cast<uint8_t*>(x.v_dst), x.k_scale_dst, x.v_scale_dst, x.weight_dst, x.kept};
+    }
+    if (launch_fp8_evict(p, di.sm_count, launch_config(static_cast<cudaStream_t>(stream), attr, true)) != cudaSuccess) {
+      cudaGetLastError();
+      return EA_ERR_CUDA;
+    }
+  }
+  return EA_OK;
+}
+
+}  // extern "C"

@@ -45,6 +45,8 @@ enum : uint32_t {
   kErrLinearWait = 1u << 7,
   kErrDecodeWait = 1u << 8,
   kErrSelftestLooks = 1u << 9,
+  kErrF8DecodeWait = 1u << 10,
+  kErrEvictWait = 1u << 11,
 };
 
 // ------------------------------------------------------------------------- workspace layout
@@ -332,6 +334,118 @@ constexpr MxExpertWs mx_expert_ws(int n_layers, int max_ctas) {
   w.part_lse_off = off;
   off += static_cast<size_t>(max_ctas) * 2 * kMxPartRows * kRows * sizeof(float);
   w.total = (off + 1023) & ~static_cast<size_t>(1023);
+  return w;
+}
+
+// ------------------------------------------------------------------------------ 8-bit cache
+// Rows of K and V moved into or out of an 8-bit cache (one launch: <= 64 layers).
+struct F8RowsLayer {
+  void* k;      // rows [8][n_rows][128] with the launch's strides
+  void* v;
+  uint8_t* kc;  // codes [8][Smax][128]
+  uint8_t* vc;
+  float* ks;    // scales [8][Smax/128 + 1]
+  float* vs;
+};
+struct F8RowsParams {
+  F8RowsLayer layer[kMaxLayersPerLaunch];
+  long long head_stride, row_stride;  // of k and v, in elements
+  int row0, n_rows, Smax;
+};
+
+// One decode step over 8-bit caches (fp8_decode.cu).
+struct F8AttnLayer {
+  const __nv_bfloat16* q_raw;  // [64][128]
+  const __nv_bfloat16* k_raw;  // [8][128]
+  const __nv_bfloat16* v_raw;
+  const __nv_bfloat16* q_gamma;
+  const __nv_bfloat16* k_gamma;
+  uint8_t* kc;
+  uint8_t* vc;
+  float* ks;
+  float* vs;
+  __nv_bfloat16* out;    // [64][128]
+  __nv_bfloat16* k_new;  // optional: the new rows' values as stored, [8][128]
+  __nv_bfloat16* v_new;
+  const float* w_in;     // optional: weight sums before this step, [8][Smax]
+  float* w_out;          // optional: after it
+};
+
+template <int CAP>
+struct F8DecodeParams {
+  CUtensorMap kmap[CAP];  // all Smax rows of K: dims {128, Smax, 8}, box {128, 128, 1}, 128B swizzle
+  CUtensorMap vmap[CAP];
+  F8AttnLayer layer[CAP];
+  float4 rot[kD / 2];  // the token's rotation by frequency: cosine x + y, sine z + w
+  float* part_o;       // [n_ctas][2 slots][8 heads][128] unnormalised partial outputs
+  float* part_ml;      // [n_ctas][2 slots][8 heads][2]: reference (log2 units) and sum
+  uint32_t* unit_cnt;  // [unit]: parts that have written their partial (zero between calls)
+  uint32_t* status;
+  float* scores;       // [unit][Smax][8]: every key's scores in log2 units, if a layer's weights are asked for (else null)
+  float* lse;          // [unit][8]: the heads' log2-sum-exp
+  long long W;         // key tiles: n_layers * 8 * T
+  int T;               // key tiles per unit: pos / 128 + 1
+  int pos, Smax, n_layers;
+  float scale_log2;    // log2(e) / sqrt(128)
+};
+// Workspace: [0, 1024) status word; unit counters and log2-sum-exps of 64 layers, whatever the call's number; partials of at
+// most max_ctas CTAs; scores, for a call that asks for weights.
+struct F8DecodeWs {
+  size_t cnt_off, lse_off, part_o_off, part_ml_off, scores_off, total;
+};
+constexpr F8DecodeWs f8_decode_ws(int max_ctas, int n_layers, int Smax, bool weights) {
+  F8DecodeWs w{};
+  size_t off = 1024;
+  w.cnt_off = off;
+  off += static_cast<size_t>(kDecodeMaxLayers) * kHkv * sizeof(uint32_t);
+  w.lse_off = off;
+  off += static_cast<size_t>(kDecodeMaxLayers) * kHkv * kRepText * sizeof(float);
+  w.part_o_off = off;
+  off += static_cast<size_t>(max_ctas) * 2 * kRepText * kD * sizeof(float);
+  w.part_ml_off = off;
+  off += static_cast<size_t>(max_ctas) * 2 * kRepText * 2 * sizeof(float);
+  off = (off + 1023) & ~static_cast<size_t>(1023);
+  w.scores_off = off;
+  if (weights)
+    off += static_cast<size_t>(n_layers < kDecodeMaxLayers ? n_layers : kDecodeMaxLayers) * kHkv * Smax * kRepText * sizeof(float);
+  w.total = (off + 1023) & ~static_cast<size_t>(1023);
+  return w;
+}
+
+// Eviction (fp8_evict.cu).
+struct F8EvictLayer {
+  const uint8_t* kc;
+  const uint8_t* vc;
+  const float* ks;
+  const float* vs;
+  const float* w;   // [8][Smax]
+  uint8_t* kd;      // where the kept rows go: the same arrays, or others
+  uint8_t* vd;
+  float* ksd;
+  float* vsd;
+  float* wd;
+  int* kept;        // [8][n_keep]
+};
+struct F8EvictParams {
+  F8EvictLayer layer[kMaxLayersPerLaunch];
+  uint32_t* status;
+  uint32_t* ticket;  // the mover's next piece of work
+  uint32_t* before;  // [unit][blocks + 1]: kept rows before each source block
+  uint32_t* loaded;  // [unit][K, V][blocks]: whether a destination block's rows have been read
+  int n_rows, n_keep, n_first, n_recent, Smax, n_layers;
+  int blocks;        // Smax / 128
+};
+struct F8EvictWs {
+  size_t ticket_off, before_off, loaded_off, total;
+};
+constexpr F8EvictWs f8_evict_ws(int n_layers, int Smax) {
+  F8EvictWs w{};
+  const size_t units = static_cast<size_t>(n_layers < kMaxLayersPerLaunch ? n_layers : kMaxLayersPerLaunch) * kHkv;
+  const size_t blocks = Smax / kScaleBlock;
+  w.ticket_off = 512;
+  w.before_off = 1024;
+  w.loaded_off = w.before_off + units * (blocks + 1) * sizeof(uint32_t);
+  w.total = (w.loaded_off + units * 2 * blocks * sizeof(uint32_t) + 1023) & ~static_cast<size_t>(1023);
   return w;
 }
 

@@ -399,6 +399,102 @@ size_t expert_attn_mxfp4_workspace_size(int n_layers);
 int expert_attn_layers_mxfp4(const ea_layer_mxfp4_args* layers, int n_layers, int S, int Smax, int rope_delta,
                              void* workspace, size_t ws_bytes, ea_stream_t stream);
 
+/* ------------------------------------------------------------------------------- 8-bit cache
+ * The e4m3 cache of ea_layer_args (codes [8][Smax][128], scales fp32 [8][Smax/128 + 1]), filled and read row by row, with
+ * the text model's decode step over it and the eviction of rows that earned little attention. A value is code * scale. Column b of
+ * the scales belongs to rows [128 b, 128 b + 128); the last column (the expert's own rows) is neither read nor written here.
+ * expert_attn_layers and expert_attn_quantize_cache work on the same caches. Asynchrony, ownership and errors are those of the functions
+ * above. Smax is a multiple of 128, 128 <= Smax <= 2^22. Codes and rows are 16-byte, scales 4-byte aligned. Scales
+ * that are read must be positive normal numbers (anything else gives undefined values, no fault). What one call writes
+ * must not overlap: an array that stands twice among its outputs is EA_ERR_INVALID_ARG. */
+
+typedef struct {
+  void* k;        /* rows of K: element (head g, row r, channel d) at g head_stride + r row_stride + d */
+  void* v;        /* rows of V, the same strides */
+  void* k_cache;
+  void* v_cache;
+  float* k_scale;
+  float* v_scale;
+} ea_fp8_rows;
+
+/* Appends n_rows rows to the caches of n_layers layers (layers: a HOST array), which hold rows [0, row0), and hold
+ * [0, row0 + n_rows) afterwards; rows from there on keep their codes, and stand for nothing. A block that begins with these
+ * rows gets the scale 2^e, the least with amax <= 448 * 2^e (e >= -100). A block that holds earlier rows keeps its scale s if
+ * amax <= 448 s; else the scale becomes s 2^k for the least k that holds amax, and the earlier rows' codes are rounded again, times 2^-k
+ * (exact but for e4m3's subnormals). Codes round x / scale to nearest (even on ties), saturating at 448. No scale grows past
+ * 2^118 (values from 1.5e38 on and infinities saturate there); a NaN is stored as NaN and does not count for amax.
+ * dtype (ea_rows_dtype), head_stride, row_stride and the limits on them as for expert_attn_write_mxfp4;
+ * 0 <= row0, 0 <= n_rows <= Smax - row0. One launch per 64 layers. */
+int expert_attn_write_fp8(const ea_fp8_rows* layers, int n_layers, int row0, int n_rows, int Smax, int dtype,
+                          int64_t head_stride, int64_t row_stride, ea_stream_t stream);
+
+/* The reverse: k and v receive the values of cache rows [row0, row0 + n_rows), rounded to nearest from the fp32 product code *
+ * scale. The caches are not written; rows must not overlap (as for expert_attn_read_mxfp4). */
+int expert_attn_read_fp8(const ea_fp8_rows* layers, int n_layers, int row0, int n_rows, int Smax, int dtype,
+                         int64_t head_stride, int64_t row_stride, ea_stream_t stream);
+
+/* text_decode_attention over 8-bit caches: the roped k, rounded to fp32, and the raw v are appended as row pos by the rule of
+ * expert_attn_write_fp8 (so earlier rows of its block can be rounded again), and every query head attends to the values
+ * that rows [0, pos] then have. Rows after pos are never used and stay as they are. q_raw bf16 [64][128], k_raw and v_raw
+ * bf16 [8][128], gains bf16 [128], out bf16 [64][128]; k_new and v_new, if not NULL, bf16 [8][128], receive the new row's
+ * values. q rows are held to 2^-19 of their largest channel, softmax weights to 2^-14, K and V as stored; q_raw's and k_raw's
+ * squares are summed in fp32 (values below 2^60).
+ * weight_out, if not NULL (layer by layer): fp32 [8][Smax]; element (g, r), r < pos, becomes weight_in's (0 if weight_in is NULL) plus the
+ * softmax weights of row r summed over the 8 query heads of KV head g, and element (g, pos) those of row pos alone; later
+ * elements stay as they are. weight_in may be weight_out; otherwise it must not stand twice in a call either. Both
+ * 16-byte aligned. 0 <= pos < Smax; |pos + rope_delta| < 2^24. */
+typedef struct {
+  const void* q_raw;
+  const void* k_raw;
+  const void* v_raw;
+  const void* q_gamma;
+  const void* k_gamma;
+  void* k_cache;
+  void* v_cache;
+  float* k_scale;
+  float* v_scale;
+  void* out;
+  void* k_new;            /* optional */
+  void* v_new;            /* optional */
+  const float* weight_in; /* optional */
+  float* weight_out;      /* optional */
+} ea_decode_fp8_args;
+
+/* Bytes of workspace for calls over up to n_layers layers of up to Smax rows on the current device (0 without a suitable
+ * one): 256-byte aligned, cleared once with text_decode_workspace_init, used by this function alone and not by calls that
+ * overlap; expert_attn_read_status reads its status word. weights: whether calls ask for weight_out (32 bytes a row and head more). */
+size_t text_decode_fp8_workspace_size(int n_layers, int Smax, int weights);
+int text_decode_attention_fp8(const ea_decode_fp8_args* layers, int n_layers, int pos, int Smax, int rope_delta,
+                              void* workspace, size_t ws_bytes, ea_stream_t stream);
+
+/* Eviction by accumulated attention weight. Of the n_rows rows of each KV head the first n_first and the last n_recent stay,
+ * and of the others those of the largest weight, n_keep rows in all (equal weights: the lowest row first; the zeros are
+ * equal, NaN is above all). They become rows [0, n_keep) of the destination, in their order, with their weights, and kept [8][n_keep] names the rows
+ * that they were. A destination block's scale is the largest scale s of its rows' blocks; a code whose row had another
+ * scale s' is rounded again: the fp32 product code * (s' / s) to nearest. What lies behind row n_keep in the destination, its scales
+ * and weights among it, stays as it was. Heads choose for themselves, so that after a call row r of two heads can be different
+ * tokens: keys keep the rotation of their own position, and later calls give the next token's position as pos + rope_delta.
+ * In place (every destination is its source), or into other arrays (none is, nor overlaps one).
+ * 0 <= n_first, 0 <= n_recent, n_first + n_recent <= n_keep <= n_rows <= Smax. Two launches per 64 layers. */
+typedef struct {
+  const void* k_cache;
+  const void* v_cache;
+  const float* k_scale;
+  const float* v_scale;
+  const float* weight;    /* fp32 [8][Smax] */
+  void* k_dst;
+  void* v_dst;
+  float* k_scale_dst;
+  float* v_scale_dst;
+  float* weight_dst;
+  int32_t* kept;          /* [8][n_keep] */
+} ea_evict_fp8_args;
+
+/* Workspace as for the decode step above, cleared once with expert_attn_workspace_init. */
+size_t expert_attn_evict_fp8_workspace_size(int n_layers, int Smax);
+int expert_attn_evict_fp8(const ea_evict_fp8_args* layers, int n_layers, int n_rows, int n_keep, int n_first, int n_recent,
+                          int Smax, void* workspace, size_t ws_bytes, ea_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
