@@ -16,9 +16,10 @@
 // Each tile's weights are taken relative to its own largest score, and its O^T is read out and added, times its share and V's scale, in
 // fp32: whatever scales and maxima the other tiles have, none of it is rounded away.
 //
-// Warp roles (384 threads): warps 0-3 softmax (thread = key = TMEM lane); warps 4-7 output (thread = channel = TMEM lane): sums of O^T,
-// a segment's end, the merge; warp 8 loads tiles by TMA into a ring; warp 9 issues the MMAs; warps 10 and 11 append the new K and V
-// row. S, P and O are double-buffered. A unit cut over several CTAs is merged by the part that finishes last.
+// Warp roles (512 threads): warps 0-3 and 4-7 softmax, of even and of odd tiles (thread = key = TMEM lane); warps 8-11 output
+// (thread = channel = TMEM lane): sums of O^T, a segment's end, the merge; warp 12 loads tiles by TMA into a ring; warp 13 issues the MMAs;
+// warps 14 and 15 prepare: the next segment's Q, and the new K and V row, which they append. S has four buffers, Q, P and O have two. A unit cut
+// over several CTAs is merged by the part that finishes last.
 // For layers whose weights are asked for, the scores go to the workspace (32 bytes a key) and a second kernel forms the weights
 // from them and the units' log2-sum-exps.
 #include "fp8.cuh"
@@ -26,43 +27,42 @@
 namespace ea {
 namespace f8d {
 
-constexpr int kThreads = 384;
-constexpr int kGroup = 128;  // threads of the softmax warps, and of the output warps
+constexpr int kThreads = 512;
+constexpr int kGroup = 128;  // threads of either set of softmax warps, and of the output warps
 constexpr int kStages = 6;
 constexpr uint32_t kTileBytes = kKeyTile * kD;      // a K or a V tile: 128 rows of 128 bytes, 128-byte swizzle
 constexpr uint32_t kStageBytes = 2 * kTileBytes;
 constexpr int kCols = 32;                           // N of both products
 constexpr uint32_t kOpBytes = kCols * 128;          // Q or P: 32 rows of 128 bytes
 constexpr int kMaxParts = 160;                      // parts of one unit (at most one per CTA)
-constexpr int kMergeBatch = 10;
+constexpr int kMergeBatch = 6;
 constexpr int kTails = 72;                          // units of one CTA, at most
 // Shared memory (offsets from the 1024-byte-aligned base)
 constexpr uint32_t SM_RING = 0;
-constexpr uint32_t SM_QT = SM_RING + kStages * kStageBytes;
-constexpr uint32_t SM_PT = SM_QT + kOpBytes;                     // 2 buffers
+constexpr uint32_t SM_QT = SM_RING + kStages * kStageBytes;      // 2 buffers
+constexpr uint32_t SM_PT = SM_QT + 2 * kOpBytes;                 // 2 buffers
 constexpr uint32_t SM_ROT = SM_PT + 2 * kOpBytes;                // float4 [64]
-constexpr uint32_t SM_KS = SM_ROT + (kD / 2) * 16;               // 128 tiles' K scales
-constexpr uint32_t SM_VS = SM_KS + 128 * 4;
-constexpr uint32_t SM_RED = SM_VS + 128 * 4;                     // [2][4 warps][8 heads]
-constexpr uint32_t SM_FAC = SM_RED + 2 * 4 * kRepText * 4;       // [4][8 heads]: (what the sums before are multiplied by, the tile's share)
-constexpr uint32_t SM_FIN = SM_FAC + 4 * kRepText * 8;           // [8 segments][8 heads]: (reference, sum)
-constexpr uint32_t SM_QF = SM_FIN + 8 * kRepText * 8;            // [8]: what a head's S columns are multiplied by
-constexpr uint32_t SM_LRED = SM_QF + kRepText * 4;               // [4 warps][8 heads]
-constexpr uint32_t SM_TAILS = SM_LRED + 4 * kRepText * 4;        // [K, V][kTails]: the appended block's scale
+constexpr uint32_t SM_RED = SM_ROT + (kD / 2) * 16;              // [2 sets][2][4 warps][8 heads]
+constexpr uint32_t SM_FAC = SM_RED + 2 * 2 * 4 * kRepText * 4;   // [4][8 heads]: (what the set's sums before are multiplied by, the tile's share)
+constexpr uint32_t SM_FIN = SM_FAC + 4 * kRepText * 8;           // [8 segments][2 sets][8 heads]: (reference, sum)
+constexpr uint32_t SM_QF = SM_FIN + 8 * 2 * kRepText * 8;        // [8 segments][8]: what a head's S columns are multiplied by (read up to four tiles after the last QK)
+constexpr uint32_t SM_LRED = SM_QF + 8 * kRepText * 4;           // [2 sets][4 warps][8 heads]
+constexpr uint32_t SM_TAILS = SM_LRED + 2 * 4 * kRepText * 4;    // [K, V][kTails]: the appended block's scale
 constexpr uint32_t SM_SW = SM_TAILS + 2 * kTails * 4;            // merge weights [part][head]
 constexpr uint32_t SM_BAR = (SM_SW + kMaxParts * kRepText * 4 + 7) & ~7u;
-// SDONE, PFULL, ODONE, OFREE: one barrier per parity of the tile count. The softmax warps can be two tiles, and so three segments, ahead
-// of the output warps: what those wait for from them has as many barriers (FAC by tile, FIN by segment) as it takes for none to
-// complete twice unseen.
-constexpr int B_FULL = 0, B_EMPTY = kStages, B_SDONE = 2 * kStages, B_PFULL = B_SDONE + 2, B_ODONE = B_PFULL + 2,
-              B_OFREE = B_ODONE + 2, B_QFULL = B_OFREE + 2, B_FAC = B_QFULL + 1, B_FIN = B_FAC + 4, B_DRAIN = B_FIN + 8, kNumBars = B_DRAIN + 1;
+// PFULL, ODONE, OFREE: one barrier per parity of the tile count; SDONE: per S buffer; QFULL, QFREE: per Q buffer. The softmax warps
+// can be two tiles, and so three segments, ahead of the output warps: what those wait for from them has as many barriers (FAC by
+// tile, FIN by segment) as it takes for none to complete twice unseen.
+constexpr int B_FULL = 0, B_EMPTY = kStages, B_SDONE = 2 * kStages, B_PFULL = B_SDONE + 4, B_ODONE = B_PFULL + 2,
+              B_OFREE = B_ODONE + 2, B_QFULL = B_OFREE + 2, B_QFREE = B_QFULL + 2, B_FAC = B_QFREE + 2, B_FIN = B_FAC + 4,
+              B_DRAIN = B_FIN + 8, kNumBars = B_DRAIN + 1;
 constexpr uint32_t SM_TMEM = SM_BAR + kNumBars * 8;
 constexpr uint32_t SM_ABORT = SM_TMEM + 4;
 constexpr uint32_t SM_MERGE = SM_ABORT + 4;
 constexpr uint32_t SM_TAILN = SM_MERGE + 4;  // [K, V]: units whose new row is in place
 constexpr uint32_t kSmemBytes = SM_TAILN + 8 + 1024;  // + base alignment
 static_assert(kSmemBytes <= 232448, "shared memory budget of one sm_103 CTA");
-constexpr uint32_t kTmemCols = 128, TM_S = 0, TM_O = 64;  // 2 x 32 columns each
+constexpr uint32_t kTmemCols = 256, TM_S = 0, TM_O = 128;  // 4 and 2 buffers of 32 columns
 
 struct Seg {
   int u, j0, j1;  // unit and its key-tile range [j0, j1)
@@ -134,15 +134,56 @@ __device__ __forceinline__ bool wait_tail(const P& p, uint32_t sbase, int kv, ui
   return false;
 }
 
-// One warp appends the new K (kv = 0) or V row of every unit whose last tile this CTA has.
+// q rows h0 .. h0 + N - 1 of segment seg's unit, as pieces, into its Q buffer: one warp.
+template <int N, int CAP>
+__device__ __forceinline__ void prepare_q(const F8DecodeParams<CAP>& p, uint32_t sbase, uint8_t* smem, int u, int h0, uint32_t seg, int lane) {
+  const F8AttnLayer& L = p.layer[u / kHkv];
+  const float4* rot = reinterpret_cast<const float4*>(smem + SM_ROT);
+  float x[N][4], gm[4];
+  f8_load_row(L.q_gamma, lane, gm);
+#pragma unroll
+  for (int k = 0; k < N; ++k) f8_load_row(L.q_raw + (kRepText * (u % kHkv) + h0 + k) * kD, lane, x[k]);
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const int h = h0 + k;
+    float y[4];
+    f8_norm_rope(x[k], gm, rot, lane, y);
+    const int e = f16_exponent(f8_row_max(y));  // the row's largest magnitude is in [2^e, 2^(e + 1)): put it in [128, 256)
+    const float up = f8_pow2(min(7 - e, 126));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] *= up;
+    if (lane == 0) reinterpret_cast<float*>(smem + SM_QF)[(seg & 7) * kRepText + h] = __fdiv_rn(p.scale_log2, up);
+#pragma unroll
+    for (int piece = 0; piece < 4; ++piece) {
+      const uint32_t lo = take_piece(y[0], y[1]), hi = take_piece(y[2], y[3]);
+      const uint32_t row = sbase + SM_QT + (seg & 1) * kOpBytes + (piece * kRepText + h) * 128;  // 16-byte chunk c of row r at chunk c ^ (r % 8)
+      st_shared_u16(row + (((lane >> 3) ^ h) << 4) + ((2 * lane) & 15), static_cast<uint16_t>(lo));
+      st_shared_u16(row + ((((lane >> 3) + 4) ^ h) << 4) + ((2 * lane) & 15), static_cast<uint16_t>(hi));
+    }
+  }
+  fence_proxy_async_smem();  // read by the tensor core
+}
+
+// One warp for K (kv = 0), one for V: half of every later segment's Q (the softmax warps prepare the first one), and the new row of every unit
+// whose last tile this CTA has.
 template <int CAP>
-__device__ __noinline__ void append_rows(const F8DecodeParams<CAP>& p, uint32_t sbase, uint8_t* smem, int kv, long long start, long long end) {
+__device__ __noinline__ void prepare(const F8DecodeParams<CAP>& p, uint32_t sbase, uint8_t* smem, int kv, long long start, long long end,
+                                     volatile uint32_t* abort_flag) {
   const int lane = threadIdx.x & 31;
   const float4* rot = reinterpret_cast<const float4*>(smem + SM_ROT);
   const int blk = p.pos / kScaleBlock, before = p.pos % kScaleBlock;
-  uint32_t n = 0;
+  uint32_t n = 0, seg = 0;
   Seg s;
-  for (long long t = start; next_seg(t, end, p.T, s);) {
+  for (long long t = start; next_seg(t, end, p.T, s); ++seg) {
+    if (seg > 0) {
+      const uint32_t bar0 = sbase + SM_BAR, buf = seg & 1;
+      bool ok = true;
+      if (seg > 1) ok = bounded_wait(bar0 + 8 * (B_QFREE + buf), ((seg - 2) >> 1) & 1, abort_flag, p.status, kErrF8DecodeWait);
+      if (!__all_sync(0xffffffffu, ok)) return;
+      prepare_q<4>(p, sbase, smem, s.u, 4 * kv, seg, lane);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar0 + 8 * (B_QFULL + buf));
+    }
     if (s.j1 != p.T) continue;
     const int g = s.u % kHkv;
     const F8AttnLayer& L = p.layer[s.u / kHkv];
@@ -236,9 +277,8 @@ __device__ __noinline__ void producer(const F8DecodeParams<CAP>& p, uint32_t sba
 }
 
 // ------------------------------------------------------------------------------- MMA issuer
-// Step i issues QK(i) and PV(i - 1), in whichever order their inputs arrive (i: over all of the CTA's tiles). QK(i) needs its tile, its
-// segment's Q, and score buffer i % 2 released by the softmax of tile i - 2 (its PFULL); PV(i) needs P(i) and O buffer i % 2 read
-// out by the output warps (OFREE of tile i - 2).
+// QK(i) needs its tile, its segment's Q, and score buffer i % 4 read by the softmax of tile i - 4 (whose P, and so PV(i - 4), comes
+// after that); PV(i) needs P(i) and O buffer i % 2 read out by the output warps (OFREE of tile i - 2).
 template <int CAP>
 __device__ __noinline__ void mma_issuer(const F8DecodeParams<CAP>& p, uint32_t sbase, uint32_t tmem, long long start, long long end,
                                         volatile uint32_t* abort_flag) {
@@ -248,61 +288,57 @@ __device__ __noinline__ void mma_issuer(const F8DecodeParams<CAP>& p, uint32_t s
   constexpr uint32_t kIdescO = umma_idesc_f16(128, kCols, false, true, false);
   auto bar = [&](int b) { return bar0 + 8 * b; };
   const int total = static_cast<int>(end - start);
-  int left = 0, segs = 0;  // QKs of the current segment to come; segments begun
+  int qk = 0, pv = 0, left = 0, seg = -1;  // tiles issued; QKs of the current segment to come; its number
   long long t = start;
   Seg s;
-  bool ok = true;
-  for (int i = 0; i <= total && ok; ++i) {
-    bool qk_todo = i < total, pv_todo = i > 0;
-    if (qk_todo && left == 0) {
-      next_seg(t, end, p.T, s);
-      left = s.j1 - s.j0;
-      ++segs;
-    }
-    uint64_t t0 = 0;
-    for (uint32_t it = 0; qk_todo || pv_todo; ++it) {
-      bool moved = false;
-      if (qk_todo && mbar_test_wait(bar(B_QFULL), (segs - 1) & 1) && mbar_test_wait(bar(B_FULL + i % kStages), (i / kStages) & 1) &&
-          (i < 2 || mbar_test_wait(bar(B_PFULL + (i & 1)), ((i - 2) >> 1) & 1))) {
-        const uint32_t ka = sbase + SM_RING + (i % kStages) * kStageBytes, qt = sbase + SM_QT;
+  uint64_t t0 = 0;
+  for (uint32_t it = 0; pv < total;) {
+    bool moved = false;
+    if (qk < total && qk < pv + 4) {
+      if (left == 0) {
+        next_seg(t, end, p.T, s);
+        left = s.j1 - s.j0;
+        ++seg;
+      }
+      if (mbar_test_wait(bar(B_FULL + qk % kStages), (qk / kStages) & 1) && mbar_test_wait(bar(B_QFULL + (seg & 1)), (seg >> 1) & 1)) {
+        const uint32_t ka = sbase + SM_RING + (qk % kStages) * kStageBytes, qt = sbase + SM_QT + (seg & 1) * kOpBytes;
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)  // 32 channels per step
-          umma_f8_ss(tmem + TM_S + (i & 1) * kCols, sw128_desc(ka + kk * 32, 16, 1024), sw128_desc(qt + kk * 32, 16, 1024), kIdescS, kk > 0);
-        umma_commit(bar(B_SDONE + (i & 1)));
-        --left;
-        qk_todo = false;
+          umma_f8_ss(tmem + TM_S + (qk & 3) * kCols, sw128_desc(ka + kk * 32, 16, 1024), sw128_desc(qt + kk * 32, 16, 1024), kIdescS, kk > 0);
+        umma_commit(bar(B_SDONE + (qk & 3)));
+        ++qk;
+        if (--left == 0) umma_commit(bar(B_QFREE + (seg & 1)));
         moved = true;
       }
-      const int n = i - 1;
-      if (pv_todo && mbar_test_wait(bar(B_PFULL + (n & 1)), (n >> 1) & 1) &&
-          (n < 2 || mbar_test_wait(bar(B_OFREE + (n & 1)), ((n - 2) >> 1) & 1))) {
-        const uint32_t va = sbase + SM_RING + (n % kStages) * kStageBytes + kTileBytes, pt = sbase + SM_PT + (n & 1) * kOpBytes;
-        tc_fence_after();
+    }
+    if (pv < qk && mbar_test_wait(bar(B_PFULL + (pv & 1)), (pv >> 1) & 1) &&
+        (pv < 2 || mbar_test_wait(bar(B_OFREE + (pv & 1)), ((pv - 2) >> 1) & 1))) {
+      const uint32_t va = sbase + SM_RING + (pv % kStages) * kStageBytes + kTileBytes, pt = sbase + SM_PT + (pv & 1) * kOpBytes;
+      tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)  // 32 keys per step
-          umma_f8_ss(tmem + TM_O + (n & 1) * kCols, sw128_desc(va + kk * 32 * 128, kTileBytes, 1024), sw128_desc(pt + kk * 32, 16, 1024), kIdescO,
-                     kk > 0);
-        umma_commit(bar(B_EMPTY + n % kStages));  // K and V of this stage are consumed
-        umma_commit(bar(B_ODONE + (n & 1)));
-        pv_todo = false;
-        moved = true;
-      }
-      if (moved) continue;
-      // bounded like every other wait: the CTA's abort flag, a time limit and a poll limit
-      if ((it & 63u) == 0) {
-        if (*abort_flag) {
-          ok = false;
-          break;
-        }
-        const uint64_t now = globaltimer_ns();
-        if (t0 == 0) t0 = now;
-        if (now - t0 > kWaitLimitNs || it >= 0x7fffffc0u) {
-          *abort_flag = 1u;
-          atomicOr(p.status, kErrF8DecodeWait);
-          ok = false;
-          break;
-        }
+      for (int kk = 0; kk < 4; ++kk)  // 32 keys per step
+        umma_f8_ss(tmem + TM_O + (pv & 1) * kCols, sw128_desc(va + kk * 32 * 128, kTileBytes, 1024), sw128_desc(pt + kk * 32, 16, 1024), kIdescO,
+                   kk > 0);
+      umma_commit(bar(B_ODONE + (pv & 1)));
+      umma_commit(bar(B_EMPTY + pv % kStages));  // K and V of this stage are consumed
+      ++pv;
+      moved = true;
+    }
+    if (moved) {
+      it = 0;
+      t0 = 0;
+      continue;
+    }
+    // bounded like every other wait: the CTA's abort flag, a time limit and a poll limit
+    if ((it++ & 63u) == 0) {
+      if (*abort_flag) break;
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > kWaitLimitNs || it >= 0x7fffffc0u) {
+        *abort_flag = 1u;
+        atomicOr(p.status, kErrF8DecodeWait);
+        break;
       }
     }
   }
@@ -312,88 +348,57 @@ __device__ __noinline__ void mma_issuer(const F8DecodeParams<CAP>& p, uint32_t s
 }
 
 // ---------------------------------------------------------------------------- softmax warps
-// q rows of a unit, as pieces: warp w takes heads 2w and 2w + 1.
+// One set of warps: tiles of this CTA whose number has parity `set`.
 template <int CAP>
-__device__ __forceinline__ void prepare_q(const F8DecodeParams<CAP>& p, uint32_t sbase, uint8_t* smem, int u, int warp, int lane) {
-  const F8AttnLayer& L = p.layer[u / kHkv];
-  const float4* rot = reinterpret_cast<const float4*>(smem + SM_ROT);
-  float x[2][4], gm[4];
-  f8_load_row(L.q_gamma, lane, gm);
-#pragma unroll
-  for (int k = 0; k < 2; ++k) f8_load_row(L.q_raw + (kRepText * (u % kHkv) + 2 * warp + k) * kD, lane, x[k]);
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int h = 2 * warp + k;
-    float y[4];
-    f8_norm_rope(x[k], gm, rot, lane, y);
-    const int e = f16_exponent(f8_row_max(y));  // the row's largest magnitude is in [2^e, 2^(e + 1)): put it in [128, 256)
-    const float up = f8_pow2(min(7 - e, 126));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] *= up;
-    if (lane == 0) reinterpret_cast<float*>(smem + SM_QF)[h] = __fdiv_rn(p.scale_log2, up);
-#pragma unroll
-    for (int piece = 0; piece < 4; ++piece) {
-      const uint32_t lo = take_piece(y[0], y[1]), hi = take_piece(y[2], y[3]);
-      const uint32_t row = sbase + SM_QT + (piece * kRepText + h) * 128;  // 16-byte chunk c of row r at chunk c ^ (r % 8)
-      st_shared_u16(row + (((lane >> 3) ^ h) << 4) + ((2 * lane) & 15), static_cast<uint16_t>(lo));
-      st_shared_u16(row + ((((lane >> 3) + 4) ^ h) << 4) + ((2 * lane) & 15), static_cast<uint16_t>(hi));
-    }
-  }
-}
-
-template <int CAP>
-__device__ __noinline__ void softmax(const F8DecodeParams<CAP>& p, uint32_t sbase, uint8_t* smem, uint32_t tmem, long long start,
+__device__ __noinline__ void softmax(const F8DecodeParams<CAP>& p, uint32_t sbase, uint8_t* smem, uint32_t tmem, int set, long long start,
                                      long long end, volatile uint32_t* abort_flag) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;  // key of a tile = TMEM lane
-  const uint32_t lane_addr = static_cast<uint32_t>(warp * 32) << 16, bar0 = sbase + SM_BAR;
-  float* red = reinterpret_cast<float*>(smem + SM_RED);
-  float* ksm = reinterpret_cast<float*>(smem + SM_KS);
+  const int tid = threadIdx.x & (kGroup - 1), warp = tid >> 5, lane = tid & 31;  // key of a tile = TMEM lane
+  const uint32_t lane_addr = static_cast<uint32_t>(warp * 32) << 16, bar0 = sbase + SM_BAR, id = 1 + set;
+  float* red = reinterpret_cast<float*>(smem + SM_RED) + set * 64;
   auto wait = [&](int b, uint32_t parity) { return bounded_wait(bar0 + 8 * b, parity, abort_flag, p.status, kErrF8DecodeWait); };
-  uint32_t n = 0, seg = 0, tails = 0;
-  bool ok = true;
+  uint32_t base = 0, seg = 0, tails = 0;  // this CTA's tiles before the segment, its segments, and appended rows
   Seg s;
-  for (long long t = start; ok && next_seg(t, end, p.T, s); ++seg) {
-    const int l = s.u / kHkv, g = s.u % kHkv;
+  for (long long t = start; next_seg(t, end, p.T, s); ++seg) {
+    const int l = s.u / kHkv, g = s.u % kHkv, nt = s.j1 - s.j0;
     const F8AttnLayer& L = p.layer[l];
-    const float* ks = L.ks + g * (p.Smax / kScaleBlock + 1);
+    const float* ks = L.ks + g * (p.Smax / kScaleBlock + 1) + s.j0;
     float4* scores = p.scores != nullptr && L.w_out != nullptr
-                         ? reinterpret_cast<float4*>(p.scores) + (static_cast<size_t>(s.u) * p.T * kKeyTile + tid) * 2
+                         ? reinterpret_cast<float4*>(p.scores) + (static_cast<size_t>(s.u) * p.T * kKeyTile + static_cast<size_t>(s.j0) * kKeyTile + tid) * 2
                          : nullptr;
-    // (every QK of the segment before has been seen complete: QT is free)
-    prepare_q(p, sbase, smem, s.u, warp, lane);
-    fence_proxy_async_smem();
-    bar_sync(1, kGroup);
-    if (tid == 0) mbar_arrive(bar0 + 8 * B_QFULL);
-    float qf[kRepText], lsum[kRepText];
-#pragma unroll
-    for (int h = 0; h < kRepText; ++h) {
-      qf[h] = reinterpret_cast<const float*>(smem + SM_QF)[h];
-      lsum[h] = 0.f;
+    const int last = s.j1 == p.T ? nt - 1 : nt;  // the tile whose scale the appending warp hands over
+    tails += s.j1 == p.T ? 1 : 0;
+    int i = static_cast<int>((base + set) & 1u);  // (the set's first tile of this segment)
+    float k_next = i < last ? ks[i] : 0.f;
+    if (seg == 0) {
+      prepare_q<1>(p, sbase, smem, s.u, 4 * set + warp, seg, lane);
+      bar_sync(id, kGroup);
+      if (tid == 0) mbar_arrive(bar0 + 8 * B_QFULL);
     }
+    float lsum[kRepText];
+#pragma unroll
+    for (int h = 0; h < kRepText; ++h) lsum[h] = 0.f;
     float m_run = -INFINITY;  // thread h < 8: head h's reference
-    for (int j = s.j0; j < s.j1; ++j, ++n) {
-      if (((j - s.j0) & 127) == 0) {  // the next 128 tiles' scales (the last read of the ones before lies before a barrier)
-        if (j + tid < s.j1 && j + tid != p.T - 1) ksm[tid] = ks[j + tid];
-        bar_sync(1, kGroup);
-      }
-      // S(n) is there; P buffer n % 2 is free, PV(n - 2) being complete
-      bool okt = wait(B_SDONE + (n & 1), (n >> 1) & 1);
-      if (n >= 2) okt = okt && wait(B_ODONE + (n & 1), ((n - 2) >> 1) & 1);
-      float k_scale;
-      if (j == p.T - 1) {
-        ++tails;
+    for (; i < nt; i += 2) {
+      const uint32_t n = base + i;
+      // S(n) is there; the set's P buffer is free, PV(n - 2) being complete
+      bool okt = wait(B_SDONE + (n & 3), (n >> 2) & 1);
+      if (n >= 2) okt = okt && wait(B_ODONE + set, ((n - 2) >> 1) & 1);
+      float k_scale = k_next;
+      if (i + 2 < last) k_next = ks[i + 2];
+      if (i == last) {
         okt = okt && wait_tail(p, sbase, 0, tails, abort_flag);
         k_scale = reinterpret_cast<const float*>(smem + SM_TAILS)[tails - 1];
-      } else {
-        k_scale = ksm[(j - s.j0) & 127];
       }
       okt = __all_sync(0xffffffffu, okt);
-      const bool live = j * kKeyTile + tid <= p.pos;
+      const bool live = (s.j0 + i) * kKeyTile + tid <= p.pos;
       float x[kRepText];
       if (okt) {
         tc_fence_after();
         uint32_t d[32];
-        tmem_ld32(tmem + lane_addr + TM_S + (n & 1) * kCols, d);
+        tmem_ld32(tmem + lane_addr + TM_S + (n & 3) * kCols, d);
+        const float4* q4 = reinterpret_cast<const float4*>(smem + SM_QF) + (seg & 7) * 2;
+        const float4 qa = q4[0], qb = q4[1];
+        const float qf[kRepText] = {qa.x, qa.y, qa.z, qa.w, qb.x, qb.y, qb.z, qb.w};
         tmem_wait_ld();
         reg_fence32(d);
 #pragma unroll
@@ -403,7 +408,7 @@ __device__ __noinline__ void softmax(const F8DecodeParams<CAP>& p, uint32_t sbas
           x[h] = live ? b * (qf[h] * k_scale) : -INFINITY;
         }
         if (scores != nullptr && live) {
-          float4* to = scores + static_cast<size_t>(j) * kKeyTile * 2;
+          float4* to = scores + static_cast<size_t>(i) * kKeyTile * 2;
           to[0] = make_float4(x[0], x[1], x[2], x[3]);
           to[1] = make_float4(x[4], x[5], x[6], x[7]);
         }
@@ -413,19 +418,16 @@ __device__ __noinline__ void softmax(const F8DecodeParams<CAP>& p, uint32_t sbas
           const float mx = warp_max(x[h]);
           mine = lane == h ? mx : mine;
         }
-        if (lane < kRepText) red[(n & 1) * 32 + warp * kRepText + lane] = mine;
+        if (lane < kRepText) red[(n & 2) * 16 + warp * kRepText + lane] = mine;
         if (!live) {  // a row behind the last one (or past Smax): its V row counts as zero
           const uint32_t v = sbase + SM_RING + (n % kStages) * kStageBytes + kTileBytes + tid * 128;
 #pragma unroll
           for (int c = 0; c < 8; ++c) st_shared_v4(v + 16 * c, 0u, 0u, 0u, 0u);
         }
       }
-      if (!bar_sync_and(1, kGroup, okt)) {
-        ok = false;
-        break;
-      }
+      if (!bar_sync_and(id, kGroup, okt)) return;
       float m[kRepText], y[kRepText];
-      const float4* r4 = reinterpret_cast<const float4*>(red + (n & 1) * 32);
+      const float4* r4 = reinterpret_cast<const float4*>(red + (n & 2) * 16);
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         const float4 a = r4[q], b = r4[2 + q], c = r4[4 + q], d = r4[6 + q];
@@ -440,7 +442,7 @@ __device__ __noinline__ void softmax(const F8DecodeParams<CAP>& p, uint32_t sbas
         x[h] = live ? ex2_approx(x[h] - m[h]) : 0.f;
         y[h] = x[h] * 256.0f;
       }
-      const uint32_t at = sbase + SM_PT + (n & 1) * kOpBytes + (tid & 15);
+      const uint32_t at = sbase + SM_PT + set * kOpBytes + (tid & 15);
 #pragma unroll
       for (int piece = 0; piece < 3; ++piece)
 #pragma unroll
@@ -460,9 +462,9 @@ __device__ __noinline__ void softmax(const F8DecodeParams<CAP>& p, uint32_t sbas
       }
       fence_proxy_async_smem();  // P, and zeroed V rows, are read by the tensor core
       tc_fence_before();
-      bar_sync(1, kGroup);
+      bar_sync(id, kGroup);
       if (tid == 0) {
-        mbar_arrive(bar0 + 8 * (B_PFULL + (n & 1)));  // P(n) is out, S(n) read
+        mbar_arrive(bar0 + 8 * (B_PFULL + set));  // P(n) is out, S(n) read
         mbar_arrive(bar0 + 8 * (B_FAC + (n & 3)));
       }
 #pragma unroll
@@ -471,22 +473,23 @@ __device__ __noinline__ void softmax(const F8DecodeParams<CAP>& p, uint32_t sbas
         lsum[h] = fmaf(lsum[h], f.x, x[h] * f.y);
       }
     }
-    if (!ok) break;
-    float* lred = reinterpret_cast<float*>(smem + SM_LRED);
+    base += nt;
+    float* lred = reinterpret_cast<float*>(smem + SM_LRED) + set * 32;
 #pragma unroll
     for (int h = 0; h < kRepText; ++h) {
       const float v = warp_sum(lsum[h]);
       if (lane == 0) lred[warp * kRepText + h] = v;
     }
-    bar_sync(1, kGroup);
-    if (tid < kRepText) {
-      reinterpret_cast<float2*>(smem + SM_FIN)[(seg & 7) * kRepText + tid] =
-          make_float2(m_run, (lred[tid] + lred[kRepText + tid]) + (lred[2 * kRepText + tid] + lred[3 * kRepText + tid]));
-    }
-    if (tid < 32) {
+    bar_sync(id, kGroup);
+    if (warp == 0) {
+      if (lane < kRepText)
+        reinterpret_cast<float2*>(smem + SM_FIN)[((seg & 7) * 2 + set) * kRepText + lane] =
+            make_float2(m_run, (lred[lane] + lred[kRepText + lane]) + (lred[2 * kRepText + lane] + lred[3 * kRepText + lane]));
       __syncwarp();
-      if (tid == 0) mbar_arrive(bar0 + 8 * (B_FIN + (seg & 7)));
+      if (lane == 0) mbar_arrive(bar0 + 8 * (B_FIN + (seg & 7)));
     }
+    // (lred is written again after a barrier that warp 0 reaches after this read: the next segment's, or that segment's end's)
+    bar_sync(id, kGroup);
   }
 }
 
@@ -494,9 +497,8 @@ __device__ __noinline__ void softmax(const F8DecodeParams<CAP>& p, uint32_t sbas
 template <int CAP>
 __device__ __noinline__ void output(const F8DecodeParams<CAP>& p, uint32_t sbase, uint8_t* smem, uint32_t tmem, long long start,
                                     long long end, volatile uint32_t* abort_flag) {
-  const int tid = threadIdx.x - kGroup, warp = tid >> 5;  // channel = TMEM lane
+  const int tid = threadIdx.x - 2 * kGroup, warp = tid >> 5;  // channel = TMEM lane
   const uint32_t lane_addr = static_cast<uint32_t>(warp * 32) << 16, bar0 = sbase + SM_BAR;
-  float* vsm = reinterpret_cast<float*>(smem + SM_VS);
   volatile uint32_t* merge_flag = reinterpret_cast<volatile uint32_t*>(smem + SM_MERGE);
   auto wait = [&](int b, uint32_t parity) { return bounded_wait(bar0 + 8 * b, parity, abort_flag, p.status, kErrF8DecodeWait); };
   uint32_t n = 0, seg = 0, tails = 0;
@@ -505,24 +507,20 @@ __device__ __noinline__ void output(const F8DecodeParams<CAP>& p, uint32_t sbase
     const int l = s.u / kHkv, g = s.u % kHkv;
     const F8AttnLayer& L = p.layer[l];
     const float* vs = L.vs + g * (p.Smax / kScaleBlock + 1);
-    float acc[kRepText];
+    const int last = s.j1 == p.T ? p.T - 1 : s.j1;  // the tile whose scale the appending warp hands over
+    tails += s.j1 == p.T ? 1 : 0;
+    float v_next = s.j0 < last ? vs[s.j0] : 0.f;
+    float sums[2][kRepText];  // each softmax set's tiles, relative to its own reference
 #pragma unroll
-    for (int h = 0; h < kRepText; ++h) acc[h] = 0.f;
+    for (int h = 0; h < kRepText; ++h) sums[0][h] = sums[1][h] = 0.f;
     for (int j = s.j0; j < s.j1; ++j, ++n) {
-      if (((j - s.j0) & 127) == 0) {
-        bar_sync(2, kGroup);  // the scales before have been read
-        if (j + tid < s.j1 && j + tid != p.T - 1) vsm[tid] = vs[j + tid];
-        bar_sync(2, kGroup);
-      }
       bool okt = wait(B_FAC + (n & 3), (n >> 2) & 1);  // the tile's factors are there,
       okt = okt && wait(B_ODONE + (n & 1), (n >> 1) & 1);  // and its O
-      float v_scale;
-      if (j == p.T - 1) {
-        ++tails;
+      float v_scale = v_next;
+      if (j + 1 < last) v_next = vs[j + 1];
+      if (j == last) {
         okt = okt && wait_tail(p, sbase, 1, tails, abort_flag);
         v_scale = reinterpret_cast<const float*>(smem + SM_TAILS)[kTails + tails - 1];
-      } else {
-        v_scale = vsm[(j - s.j0) & 127];
       }
       okt = __all_sync(0xffffffffu, okt);
       if (okt) {
@@ -531,27 +529,48 @@ __device__ __noinline__ void output(const F8DecodeParams<CAP>& p, uint32_t sbase
         tmem_ld32(tmem + lane_addr + TM_O + (n & 1) * kCols, d);
         tmem_wait_ld();
         reg_fence32(d);
-        const float2* fac = reinterpret_cast<const float2*>(smem + SM_FAC) + (n & 3) * kRepText;
+        const float4* fac = reinterpret_cast<const float4*>(smem + SM_FAC) + (n & 3) * (kRepText / 2);
         const float vf = v_scale * 0x1p-8f;
+        auto add = [&](float (&a)[kRepText]) {
 #pragma unroll
-        for (int h = 0; h < kRepText; ++h) {
-          const float2 f = fac[h];
-          const float o = fmaf(__uint_as_float(d[16 + h]), 0x1p-10f, __uint_as_float(d[8 + h]) * 0x1p-5f) + __uint_as_float(d[h]);
-          acc[h] = fmaf(acc[h], f.x, o * (f.y * vf));
-        }
+          for (int h = 0; h < kRepText; h += 2) {
+            const float4 f = fac[h / 2];
+            const float o0 = fmaf(__uint_as_float(d[16 + h]), 0x1p-10f, __uint_as_float(d[8 + h]) * 0x1p-5f) + __uint_as_float(d[h]);
+            const float o1 = fmaf(__uint_as_float(d[17 + h]), 0x1p-10f, __uint_as_float(d[9 + h]) * 0x1p-5f) + __uint_as_float(d[h + 1]);
+            a[h] = fmaf(a[h], f.x, o0 * (f.y * vf));
+            a[h + 1] = fmaf(a[h + 1], f.z, o1 * (f.w * vf));
+          }
+        };
+        if (n & 1) add(sums[1]);
+        else add(sums[0]);
         tc_fence_before();
       }
-      if (!bar_sync_and(2, kGroup, okt)) return;
+      if (!bar_sync_and(3, kGroup, okt)) return;
       if (tid == 0) mbar_arrive(bar0 + 8 * (B_OFREE + (n & 1)));
     }
     // ---- the segment's end: its sums, then its output or its part of one
-    if (!bar_sync_and(2, kGroup, wait(B_FIN + (seg & 7), (seg >> 3) & 1))) return;
-    const float2* fin = reinterpret_cast<const float2*>(smem + SM_FIN) + (seg & 7) * kRepText;
+    if (!bar_sync_and(3, kGroup, wait(B_FIN + (seg & 7), (seg >> 3) & 1))) return;
+    const float2* fin = reinterpret_cast<const float2*>(smem + SM_FIN) + (seg & 7) * 2 * kRepText;
+    float acc[kRepText];
+    float2 mine = make_float2(0.f, 1.f);  // thread h < 8: head h's reference and sum
+#pragma unroll
+    for (int h = 0; h < kRepText; ++h) {
+      const float2 a = fin[h], b = fin[kRepText + h];
+      const float top = fmaxf(a.x, b.x), fa = ex2_approx(a.x - top), fb = ex2_approx(b.x - top);
+      acc[h] = fmaf(sums[0][h], fa, sums[1][h] * fb);
+      if (tid == h) mine = make_float2(top, fmaf(a.y, fa, b.y * fb));
+    }
     if (s.j0 == 0 && s.j1 == p.T) {
+      float* inv = reinterpret_cast<float*>(smem + SM_SW);
+      if (tid < kRepText) {
+        inv[tid] = 1.0f / mine.y;
+        if (p.scores != nullptr) p.lse[s.u * kRepText + tid] = mine.x + log2f(mine.y);
+      }
+      bar_sync(3, kGroup);
       __nv_bfloat16* o = L.out + static_cast<size_t>(kRepText * g) * kD + tid;
 #pragma unroll
-      for (int h = 0; h < kRepText; ++h) o[h * kD] = __float2bfloat16_rn(acc[h] / fin[h].y);
-      if (p.scores != nullptr && tid < kRepText) p.lse[s.u * kRepText + tid] = fin[tid].x + log2f(fin[tid].y);
+      for (int h = 0; h < kRepText; ++h) o[h * kD] = __float2bfloat16_rn(acc[h] * inv[h]);
+      bar_sync(3, kGroup);  // read before they are written again
       continue;
     }
     // Part index: 2 c + slot (a part is its CTA's first segment or its last). Layout [part][channel][8 heads].
@@ -560,13 +579,13 @@ __device__ __noinline__ void output(const F8DecodeParams<CAP>& p, uint32_t sbase
     float4* po = reinterpret_cast<float4*>(p.part_o + ps * kRepText * kD) + 2 * tid;
     po[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
     po[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-    if (tid < kRepText) *reinterpret_cast<float2*>(p.part_ml + (ps * kRepText + tid) * 2) = fin[tid];
-    bar_sync(2, kGroup);
+    if (tid < kRepText) *reinterpret_cast<float2*>(p.part_ml + (ps * kRepText + tid) * 2) = mine;
+    bar_sync(3, kGroup);
     const long long u0 = static_cast<long long>(s.u) * p.T;
     const int c0 = cta_of_tile(u0, p.W, gridDim.x), c1 = cta_of_tile(u0 + p.T - 1, p.W, gridDim.x);
     // the count's release publishes this part, and the last part's acquire orders the others' before its reads
     if (tid == 0) *merge_flag = atom_add_acq_rel_gpu(p.unit_cnt + s.u, 1u) == static_cast<uint32_t>(c1 - c0) ? 1u : 0u;
-    bar_sync(2, kGroup);
+    bar_sync(3, kGroup);
     if (*merge_flag) {
       const int np = c1 - c0 + 1;
       const int slot0 = cta_tile_start(c0, p.W, gridDim.x) >= u0 ? 0 : 1;  // the first part may be its CTA's last segment
@@ -601,7 +620,7 @@ __device__ __noinline__ void output(const F8DecodeParams<CAP>& p, uint32_t sbase
           if (i + 16 * e < np) sw[(i + 16 * e) * kRepText + h] = ml[e].x * inv;
         if (p.scores != nullptr && i == 0) p.lse[s.u * kRepText + h] = M + log2f(sum);
       }
-      bar_sync(2, kGroup);
+      bar_sync(3, kGroup);
 #pragma unroll
       for (int h = 0; h < kRepText; ++h) acc[h] = 0.f;
       const float4* sw4 = reinterpret_cast<const float4*>(sw);
@@ -633,7 +652,7 @@ __device__ __noinline__ void output(const F8DecodeParams<CAP>& p, uint32_t sbase
       for (int h = 0; h < kRepText; ++h) L.out[static_cast<size_t>(kRepText * g + h) * kD + tid] = __float2bfloat16_rn(acc[h]);
       if (tid == 0) p.unit_cnt[s.u] = 0u;  // every part has arrived: ready for the next call
     }
-    bar_sync(2, kGroup);  // the flag is read before the next segment overwrites it
+    bar_sync(3, kGroup);  // the flag is read before the next segment overwrites it
   }
 }
 
@@ -649,7 +668,9 @@ __global__ void __launch_bounds__(f8d::kThreads, 1) fp8_decode_kernel(const __gr
   const long long start = cta_tile_start(blockIdx.x, p.W, gridDim.x), end = cta_tile_start(blockIdx.x + 1, p.W, gridDim.x);
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
-    for (int b = 0; b < kNumBars; ++b) mbar_init(bar0 + 8 * b, 1);
+    // (Q comes from two warps, or two sets; a segment's end from both sets)
+    for (int b = 0; b < kNumBars; ++b)
+      mbar_init(bar0 + 8 * b, (b >= B_QFULL && b < B_QFULL + 2) || (b >= B_FIN && b < B_FIN + 8) ? 2 : 1);
     *abort_flag = 0u;
     reinterpret_cast<uint32_t*>(smem + SM_TAILN)[0] = 0u;
     reinterpret_cast<uint32_t*>(smem + SM_TAILN)[1] = 0u;
@@ -670,7 +691,7 @@ __global__ void __launch_bounds__(f8d::kThreads, 1) fp8_decode_kernel(const __gr
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + SM_TMEM);
-  if (warp == 9 && (threadIdx.x & 31) == 0) {
+  if (warp == 13 && (threadIdx.x & 31) == 0) {
     // hints, while the kernel before finishes (what it still writes wins): the maps, and the first tiles into L2
     if (start < end) {
       const int l = static_cast<int>(start / p.T) / kHkv;
@@ -686,16 +707,16 @@ __global__ void __launch_bounds__(f8d::kThreads, 1) fp8_decode_kernel(const __gr
   }
   // everything below reads what earlier kernels in the stream wrote
   pdl_wait_primary();
-  if (warp < 4) {
-    softmax(p, sbase, smem, tmem, start, end, abort_flag);
-  } else if (warp < 8) {
+  if (warp < 8) {
+    softmax(p, sbase, smem, tmem, warp >> 2, start, end, abort_flag);
+  } else if (warp < 12) {
     output(p, sbase, smem, tmem, start, end, abort_flag);
-  } else if (warp == 8) {
+  } else if (warp == 12) {
     if ((threadIdx.x & 31) == 0) producer(p, sbase, start, end, abort_flag);
-  } else if (warp == 9) {
+  } else if (warp == 13) {
     if ((threadIdx.x & 31) == 0) mma_issuer(p, sbase, tmem, start, end, abort_flag);
   } else {
-    append_rows(p, sbase, smem, warp - 10, start, end);
+    prepare(p, sbase, smem, warp - 14, start, end, abort_flag);
   }
   pdl_launch_dependents();
   tc_fence_before();
