@@ -9,10 +9,11 @@
 // ever widened. What they meet has more bits than a code: it comes in pieces. A number y, |y| <= 256, is c0 + c1 / 32 + c2 / 1024 + ..,
 // each c the e4m3 number next to 32 times what the pieces before left: a code is off by at most half of its last place,
 // 2^-5 of a number's power of two, so that four pieces hold a q row to 2^-20 of its largest channel (scores that weights come from:
-// fp32 would be 2^-24), three hold a softmax weight to 2^-15 of itself down to 2^-13 of the tile's largest, and to 2^-28 of that below. Products of codes are exact, sums are in fp32, and
-// pieces are columns that the MMA has to spare: 8 heads in 4 pieces are N = 32.
+// fp32 would be 2^-24), two hold a softmax weight to 2^-10 of itself down to 2^-13 of the tile's largest, and to 2^-23 of that below (the output
+// is bf16, 2^-8). Products of codes are exact, sums are in fp32, and
+// pieces are columns that the MMA has to spare: 8 heads in 4 pieces are N = 32 (up to 64 columns an MMA takes the same 46 cycles).
 //   S^T  = K Q^T    M = 128 keys, N = 32 (half of the heads, piece, head), K = 128 channels; A = the K tile (K-major)
-//   O^T  = V^T P^T  M = 128 channels, N = 32 (3 pieces and zeros), K = 128 keys; A = the V tile (MN-major)
+//   O^T  = V^T P^T  M = 128 channels, N = 16 (piece, head), K = 128 keys; A = the V tile (MN-major)
 // Each tile's weights are taken relative to its own largest score, and its O^T is read out and added, times its share and V's scale, in
 // fp32: whatever scales and maxima the other tiles have, none of it is rounded away.
 //
@@ -20,8 +21,10 @@
 // (thread = channel = TMEM lane): sums of O^T, a segment's end, the merge; warp 12 loads tiles by TMA, K's into a ring of 4, V's, which
 // are held longer, into one of 8; warps 13 and 14 issue the MMAs, one product each; warp 15 prepares what later segments need: their Q, and
 // the new K and V rows, which it appends (the first segment's Q comes from the softmax warps, its new rows from two output warps, which
-// have nothing else to do yet). S has four buffers, Q, P and O have two. A unit cut over several CTAs is merged by the part that
-// finishes last.
+// have nothing else to do yet). S has four buffers, Q, P and O have two. Five loops run side by side on one scheduler's instruction cache, and fetching
+// was what they waited for most (2.8 of 10 warp cycles an instruction): they are short, and what is rare is out of their way.
+// A unit cut over several CTAs is merged by the part that finishes last; a part that is not its CTA's last segment is counted by warp
+// 15, and merged at the CTA's end should it be the last after all, so that the output warps need not wait.
 // For layers whose weights are asked for, the scores go to the workspace (32 bytes a key) and a second kernel forms the weights
 // from them and the units' log2-sum-exps.
 #include "fp8.cuh"
@@ -31,19 +34,21 @@ namespace f8d {
 
 constexpr int kThreads = 512;
 constexpr int kGroup = 128;  // threads of either set of softmax warps, and of the output warps
+constexpr int kOutWarp = 8;  // the first of the output warps
 constexpr int kKRing = 4, kVRing = 8;
 constexpr uint32_t kTileBytes = kKeyTile * kD;      // a K or a V tile: 128 rows of 128 bytes, 128-byte swizzle
-constexpr int kCols = 32;                           // N of both products
-constexpr uint32_t kOpBytes = kCols * 128;          // Q or P: 32 rows of 128 bytes
+constexpr int kCols = 32, kOutCols = 16;            // N of the two products
+constexpr uint32_t kOpBytes = kCols * 128;          // Q: 32 rows of 128 bytes
+constexpr uint32_t kPBytes = kOutCols * 128;        // P: 16
 constexpr int kMaxParts = 160;                      // parts of one unit (at most one per CTA)
-constexpr int kMergeBatch = 6;
+constexpr int kMergeBatch = 4;
 constexpr int kTails = 72;                          // units of one CTA, at most
 // Shared memory (offsets from the 1024-byte-aligned base)
 constexpr uint32_t SM_K = 0;
 constexpr uint32_t SM_V = SM_K + kKRing * kTileBytes;
 constexpr uint32_t SM_QT = SM_V + kVRing * kTileBytes;           // 2 buffers
 constexpr uint32_t SM_PT = SM_QT + 2 * kOpBytes;                 // 2 buffers
-constexpr uint32_t SM_ROT = SM_PT + 2 * kOpBytes;                // float4 [64]
+constexpr uint32_t SM_ROT = SM_PT + 2 * kPBytes;                // float4 [64]
 constexpr uint32_t SM_RED = SM_ROT + (kD / 2) * 16;              // [2][8 warps][4 heads]
 constexpr uint32_t SM_FAC = SM_RED + 2 * 8 * 4 * 4;              // [4][8 heads]: (what the sums before are multiplied by, the tile's share)
 constexpr uint32_t SM_FIN = SM_FAC + 4 * kRepText * 8;           // [8 segments][8 heads]: (reference, sum)
@@ -57,12 +62,10 @@ constexpr uint32_t SM_BAR = (SM_SW + kMaxParts * kRepText * 4 + 7) & ~7u;
 // tile, FIN by segment) as it takes for none to complete twice unseen. FAC also tells that a tile's S buffer has been read.
 constexpr int B_KFULL = 0, B_KEMPTY = B_KFULL + kKRing, B_VFULL = B_KEMPTY + kKRing, B_VEMPTY = B_VFULL + kVRing, B_SDONE = B_VEMPTY + kVRing, B_PFULL = B_SDONE + 4, B_ODONE = B_PFULL + 2,
               B_OFREE = B_ODONE + 2, B_QFULL = B_OFREE + 2, B_QFREE = B_QFULL + 2, B_FAC = B_QFREE + 2, B_FIN = B_FAC + 4,
-              B_DRAIN = B_FIN + 8, kNumBars = B_DRAIN + 2;
+              B_DRAIN = B_FIN + 8, B_PART = B_DRAIN + 2, B_LATE = B_PART + 1, B_TAIL = B_LATE + 1, kNumBars = B_TAIL + 2 * kTails;  // TAIL: [K, V][unit], whose new row is in place
 constexpr uint32_t SM_TMEM = SM_BAR + kNumBars * 8;
-constexpr uint32_t SM_ABORT = SM_TMEM + 4;
-constexpr uint32_t SM_MERGE = SM_ABORT + 4;
-constexpr uint32_t SM_TAILF = SM_MERGE + 4;  // [K, V][kTails]: whether the new row is in place
-constexpr uint32_t kSmemBytes = SM_TAILF + 2 * kTails * 4 + 1024;  // + base alignment
+constexpr uint32_t SM_MERGE = SM_TMEM + 4;
+constexpr uint32_t kSmemBytes = SM_MERGE + 4 + 1024;  // + base alignment
 static_assert(kSmemBytes <= 232448, "shared memory budget of one sm_103 CTA");
 constexpr uint32_t kTmemCols = 256, TM_S = 0, TM_O = 128;  // 4 and 2 buffers of 32 columns
 
@@ -100,33 +103,8 @@ __device__ __forceinline__ uint32_t atom_add_acq_rel_gpu(uint32_t* a, uint32_t v
 __device__ __forceinline__ void st_shared_u8(uint32_t a, uint32_t v) {
   asm volatile("st.shared.u8 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
-__device__ __forceinline__ uint32_t ld_acquire_shared(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ void st_release_shared(uint32_t a, uint32_t v) {
-  asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
-}
-
-// bounded_wait, whose clock is first read after 32 looks: a tile's waits are short, and the global timer takes as long as they do.
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, uint32_t* status) {
-  if (mbar_try_wait(bar, parity)) return true;
-  uint64_t t0 = 0;
-  for (uint32_t it = 1; it < 0x80000000u; ++it) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((it & 31u) == 0) {
-      if (*abort_flag) return false;
-      const uint64_t now = globaltimer_ns();
-      if (t0 == 0) t0 = now;
-      if (now - t0 > kWaitLimitNs) break;
-    }
-  }
-  *abort_flag = 1u;
-  atomicOr(status, kErrF8DecodeWait);
-  return false;
-}
-
+// The waits of this file are a whole warp's and take little code: counted_wait, which gives up after a number of looks. Who gives up notes
+// it and leaves, and then so does, the same number of looks later, who waits for it.
 // 16 consecutive TMEM columns of this warp's 32 lanes -> 16 registers per thread.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
@@ -156,24 +134,6 @@ __device__ __forceinline__ uint32_t take_piece(float& a, float& b) {
 }
 
 // ------------------------------------------------------------------------ preparing segments
-// Waits until the new row of the CTA's idx-th unit with a last tile (of K: kv = 0; of V: 1) is in place.
-template <class P>
-__device__ __forceinline__ bool wait_tail(const P& p, uint32_t sbase, int kv, uint32_t idx, volatile uint32_t* abort_flag) {
-  uint64_t t0 = 0;
-  for (uint32_t it = 0; it < 0x80000000u; ++it) {
-    if (ld_acquire_shared(sbase + SM_TAILF + 4 * (kv * kTails + idx)) != 0u) return true;
-    if ((it & 63u) == 63u) {
-      if (*abort_flag) return false;
-      const uint64_t now = globaltimer_ns();
-      if (t0 == 0) t0 = now;
-      if (now - t0 > kWaitLimitNs) break;
-    }
-  }
-  *abort_flag = 1u;
-  atomicOr(p.status, kErrF8DecodeWait);
-  return false;
-}
-
 // One warp appends unit u's new K (kv = 0) or V row: the CTA's idx-th.
 template <int CAP>
 __device__ __noinline__ void append_row(const F8DecodeParams<CAP>& p, uint32_t sbase, uint8_t* smem, int kv, int u, uint32_t idx) {
@@ -217,7 +177,7 @@ __device__ __noinline__ void append_row(const F8DecodeParams<CAP>& p, uint32_t s
   if (lane == 0) reinterpret_cast<float*>(smem + SM_TAILS)[kv * kTails + idx] = now;
   __syncwarp();
   if (lane == 0) {
-    st_release_shared(sbase + SM_TAILF + 4 * (kv * kTails + idx), 1u);
+    mbar_arrive(sbase + SM_BAR + 8 * (B_TAIL + kv * kTails + idx));
     *scale = now;
   }
   __nv_bfloat16* val = kv ? L.v_new : L.k_new;
@@ -259,10 +219,18 @@ __device__ __forceinline__ void prepare_q(const F8DecodeParams<CAP>& p, uint32_t
   fence_proxy_async_smem();  // read by the tensor core
 }
 
+// Counts a part of unit u whose partial the calling thread has seen written; whether it was the last one. (The count's release
+// publishes the partial, its acquire orders the others' before what follows.)
+template <class P>
+__device__ __forceinline__ bool count_part(const P& p, int u) {
+  const long long u0 = static_cast<long long>(u) * p.T;
+  const int parts = cta_of_tile(u0 + p.T - 1, p.W, gridDim.x) - cta_of_tile(u0, p.W, gridDim.x) + 1;
+  return atom_add_acq_rel_gpu(p.unit_cnt + u, 1u) == static_cast<uint32_t>(parts - 1);
+}
+
 // One warp: the Q and the new rows of every segment but the first.
 template <int CAP>
-__device__ __noinline__ void prepare(const F8DecodeParams<CAP>& p, uint32_t sbase, uint8_t* smem, long long start, long long end,
-                                     volatile uint32_t* abort_flag) {
+__device__ __noinline__ bool prepare(const F8DecodeParams<CAP>& p, uint32_t sbase, uint8_t* smem, long long start, long long end) {
   const int lane = threadIdx.x & 31;
   const uint32_t bar0 = sbase + SM_BAR;
   uint32_t idx = 0, seg = 0;
@@ -270,7 +238,7 @@ __device__ __noinline__ void prepare(const F8DecodeParams<CAP>& p, uint32_t sbas
   for (long long t = start; next_seg(t, end, p.T, s); ++seg) {
     if (seg > 0) {
       const uint32_t buf = seg & 1;
-      if (seg > 1 && !__all_sync(0xffffffffu, wait_bar(bar0 + 8 * (B_QFREE + buf), ((seg - 2) >> 1) & 1, abort_flag, p.status))) return;
+      if (seg > 1 && !counted_wait(bar0 + 8 * (B_QFREE + buf), ((seg - 2) >> 1) & 1)) return false;
       prepare_q<4>(p, sbase, smem, s.u, 0, seg, lane);
       prepare_q<4>(p, sbase, smem, s.u, 4, seg, lane);
       __syncwarp();
@@ -282,6 +250,15 @@ __device__ __noinline__ void prepare(const F8DecodeParams<CAP>& p, uint32_t sbas
     }
     idx += s.j1 == p.T ? 1 : 0;
   }
+  long long t = start;
+  if (!next_seg(t, end, p.T, s) || t >= end || (s.j0 == 0 && s.j1 == p.T)) return true;
+  // the first segment is a part, and not the last segment: its partial is counted here
+  const bool ok = counted_wait(bar0 + 8 * B_PART, 0);
+  if (lane == 0) {
+    *reinterpret_cast<volatile uint32_t*>(smem + SM_MERGE) = ok && count_part(p, s.u) ? 1u : 0u;
+    mbar_arrive(bar0 + 8 * B_LATE);
+  }
+  return ok;
 }
 
 // ---------------------------------------------------------------- producer and MMA issuers
@@ -295,11 +272,10 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 template <int CAP>
-__device__ __noinline__ void producer(const F8DecodeParams<CAP>& p, uint32_t sbase, long long start, long long end,
-                                      volatile uint32_t* abort_flag) {
+__device__ __noinline__ bool producer(const F8DecodeParams<CAP>& p, uint32_t sbase, long long start, long long end) {
   const uint64_t pol = l2_policy_evict_first();  // every cache tile is read once
   const uint32_t bar0 = sbase + SM_BAR;
-  auto wait = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, wait_bar(bar0 + 8 * b, parity, abort_flag, p.status)); };
+  auto wait = [&](int b, uint32_t parity) { return counted_wait(bar0 + 8 * b, parity); };
   uint32_t nk = 0, nv = 0, tails = 0;  // tiles of K and of V on their way
   bool ok = true;
   Seg s;
@@ -307,7 +283,7 @@ __device__ __noinline__ void producer(const F8DecodeParams<CAP>& p, uint32_t sba
     const int l = s.u / kHkv, g = s.u % kHkv;
     for (int j = s.j0; j < s.j1; ++j) {
       const bool tail = j == p.T - 1;  // the block of the new row
-      if (tail) ok = __all_sync(0xffffffffu, wait_tail(p, sbase, 0, tails, abort_flag));
+      if (tail) ok = wait(B_TAIL + tails, 0);
       if (nk >= kKRing) ok = ok && wait(B_KEMPTY + nk % kKRing, (nk / kKRing - 1) & 1);
       if (!ok) break;
       if (tail) fence_proxy_async_global();
@@ -318,7 +294,7 @@ __device__ __noinline__ void producer(const F8DecodeParams<CAP>& p, uint32_t sba
       }
       __syncwarp();
       ++nk;
-      if (tail) ok = __all_sync(0xffffffffu, wait_tail(p, sbase, 1, tails, abort_flag));
+      if (tail) ok = wait(B_TAIL + kTails + tails, 0);
       if (nv >= kVRing) ok = ok && wait(B_VEMPTY + nv % kVRing, (nv / kVRing - 1) & 1);
       if (!ok) break;
       if (tail) fence_proxy_async_global();
@@ -340,16 +316,16 @@ __device__ __noinline__ void producer(const F8DecodeParams<CAP>& p, uint32_t sba
       if (!drain_wait(bar0 + 8 * (B_VFULL + (nv - k) % kVRing), ((nv - k) / kVRing) & 1)) atomicOr(p.status, kErrDrain);
   }
   __syncwarp();
+  return ok;
 }
 
 // QK(n) needs its tile, its segment's Q, and score buffer n % 4 read by the softmax of tile n - 4.
 template <int CAP>
-__device__ __noinline__ void qk_issuer(const F8DecodeParams<CAP>& p, uint32_t sbase, uint32_t tmem, long long start, long long end,
-                                       volatile uint32_t* abort_flag) {
+__device__ __noinline__ bool qk_issuer(const F8DecodeParams<CAP>& p, uint32_t sbase, uint32_t tmem, long long start, long long end) {
   constexpr uint32_t kIdesc = umma_idesc_f16(128, kCols, false, false, false);  // (e4m3 is format code 0); A and B K-major
   const uint32_t bar0 = sbase + SM_BAR;
   const uint64_t kd = sw128_desc(sbase + SM_K, 16, 1024), qd = sw128_desc(sbase + SM_QT, 16, 1024);
-  auto wait = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, wait_bar(bar0 + 8 * b, parity, abort_flag, p.status)); };
+  auto wait = [&](int b, uint32_t parity) { return counted_wait(bar0 + 8 * b, parity); };
   uint32_t n = 0, seg = 0;
   bool ok = true;
   Seg s;
@@ -377,23 +353,25 @@ __device__ __noinline__ void qk_issuer(const F8DecodeParams<CAP>& p, uint32_t sb
     if (!drain_wait(bar0 + 8 * B_DRAIN, 0)) atomicOr(p.status, kErrDrain);
   }
   __syncwarp();
+  return ok;
 }
 
 // PV(n) needs its tile, P(n), and O buffer n % 2 read out by the output warps.
 template <int CAP>
-__device__ __noinline__ void pv_issuer(const F8DecodeParams<CAP>& p, uint32_t sbase, uint32_t tmem, uint32_t total, volatile uint32_t* abort_flag) {
-  constexpr uint32_t kIdesc = umma_idesc_f16(128, kCols, false, true, false);  // A = V MN-major, B = P K-major
+__device__ __noinline__ bool pv_issuer(const F8DecodeParams<CAP>& p, uint32_t sbase, uint32_t tmem, uint32_t total) {
+  constexpr uint32_t kIdesc = umma_idesc_f16(128, kOutCols, false, true, false);  // A = V MN-major, B = P K-major
   const uint32_t bar0 = sbase + SM_BAR;
   const uint64_t vd = sw128_desc(sbase + SM_V, kTileBytes, 1024), pd = sw128_desc(sbase + SM_PT, 16, 1024);
-  auto wait = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, wait_bar(bar0 + 8 * b, parity, abort_flag, p.status)); };
+  auto wait = [&](int b, uint32_t parity) { return counted_wait(bar0 + 8 * b, parity); };
+  uint32_t n = 0;
 #pragma unroll 1
-  for (uint32_t n = 0; n < total; ++n) {
+  for (; n < total; ++n) {
     if (!(wait(B_VFULL + n % kVRing, (n / kVRing) & 1) && wait(B_PFULL + (n & 1), (n >> 1) & 1) &&
           (n < 2 || wait(B_OFREE + (n & 1), ((n - 2) >> 1) & 1))))
       break;
     tc_fence_after();
-    const uint64_t v0 = vd + n % kVRing * (kTileBytes >> 4), p0 = pd + (n & 1) * (kOpBytes >> 4);
-    const uint32_t d = tmem + TM_O + (n & 1) * kCols;
+    const uint64_t v0 = vd + n % kVRing * (kTileBytes >> 4), p0 = pd + (n & 1) * (kPBytes >> 4);
+    const uint32_t d = tmem + TM_O + (n & 1) * kOutCols;
     if (elect_one()) {
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) umma_f8_ss(d, v0 + kk * (32 * 128 >> 4), p0 + 2 * kk, kIdesc, kk > 0);  // 32 keys per step
@@ -407,13 +385,31 @@ __device__ __noinline__ void pv_issuer(const F8DecodeParams<CAP>& p, uint32_t sb
     if (!drain_wait(bar0 + 8 * (B_DRAIN + 1), 0)) atomicOr(p.status, kErrDrain);
   }
   __syncwarp();
+  return n == total;
 }
 
 // ---------------------------------------------------------------------------- softmax warps
+// A unit's last tile: once its new K row is in place, the tile's scale; and its V rows behind the last key (which stand for nothing and
+// may hold anything) become zeros, once the tile is there.
+template <int CAP>
+__device__ __noinline__ float last_tile(const F8DecodeParams<CAP>& p, uint32_t sbase, const uint8_t* smem, uint32_t n, uint32_t tail, bool live, bool& ok) {
+  const uint32_t bar0 = sbase + SM_BAR;
+  ok = ok && counted_wait(bar0 + 8 * (B_TAIL + tail), 0);
+  if (threadIdx.x < kGroup && p.pos % kKeyTile != kKeyTile - 1) {
+    ok = ok && counted_wait(bar0 + 8 * (B_VFULL + n % kVRing), (n / kVRing) & 1);
+    if (ok && !live) {
+      const uint32_t v = sbase + SM_V + n % kVRing * kTileBytes + (threadIdx.x & (kGroup - 1)) * 128;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) st_shared_v4(v + 16 * c, 0u, 0u, 0u, 0u);
+    }
+  }
+  return reinterpret_cast<const float*>(smem + SM_TAILS)[tail];
+}
+
 // One set of warps: heads 4 set .. 4 set + 3 of every tile.
 template <int CAP>
-__device__ __noinline__ void softmax(const F8DecodeParams<CAP>& p, uint32_t sbase, uint8_t* smem, uint32_t tmem, int set, long long start,
-                                     long long end, volatile uint32_t* abort_flag) {
+__device__ __noinline__ bool softmax(const F8DecodeParams<CAP>& p, uint32_t sbase, uint8_t* smem, uint32_t tmem, int set, long long start,
+                                     long long end) {
   constexpr int H = kRepText / 2;
   const int tid = threadIdx.x & (kGroup - 1), warp = tid >> 5, lane = tid & 31;  // key of a tile = TMEM lane
   const uint32_t bar0 = sbase + SM_BAR, id = 1 + set;
@@ -423,7 +419,7 @@ __device__ __noinline__ void softmax(const F8DecodeParams<CAP>& p, uint32_t sbas
   uint32_t at[H];
 #pragma unroll
   for (int h = 0; h < H; ++h) at[h] = sbase + SM_PT + (4 * set + h) * 128 + (((tid >> 4) ^ (4 * set + h)) << 4) + (tid & 15);
-  auto wait = [&](int b, uint32_t parity) { return wait_bar(bar0 + 8 * b, parity, abort_flag, p.status); };
+  auto wait = [&](int b, uint32_t parity) { return counted_wait(bar0 + 8 * b, parity); };
   uint32_t n = 0, seg = 0, tails = 0;  // this CTA's tiles, its segments, and appended rows
   Seg s;
   for (long long t = start; next_seg(t, end, p.T, s); ++seg) {
@@ -434,7 +430,6 @@ __device__ __noinline__ void softmax(const F8DecodeParams<CAP>& p, uint32_t sbas
                          ? reinterpret_cast<float4*>(p.scores) + (static_cast<size_t>(s.u) * p.T * kKeyTile + tid) * 2 + set
                          : nullptr;
     const int last = s.j1 == p.T ? p.T - 1 : s.j1;  // the tile whose scale the appending warp hands over
-    tails += s.j1 == p.T ? 1 : 0;
     float k_next = s.j0 < last ? ks[s.j0] : 0.f;
     if (seg == 0) {
       prepare_q<1>(p, sbase, smem, s.u, 4 * set + warp, seg, lane);
@@ -449,62 +444,45 @@ __device__ __noinline__ void softmax(const F8DecodeParams<CAP>& p, uint32_t sbas
     }
 #pragma unroll 1
     for (int j = s.j0; j < s.j1; ++j, ++n) {
-      bool okt = wait(B_SDONE + (n & 3), (n >> 2) & 1);
+      bool ok = wait(B_SDONE + (n & 3), (n >> 2) & 1);
+      const bool live = j * kKeyTile + tid <= p.pos;
       float k_scale = k_next;
       if (j + 1 < last) k_next = ks[j + 1];
-      const bool live = j * kKeyTile + tid <= p.pos;
-      if (j == last) {
-        okt = okt && wait_tail(p, sbase, 0, tails - 1, abort_flag);
-        k_scale = reinterpret_cast<const float*>(smem + SM_TAILS)[tails - 1];
-        // a row behind the last one (or past Smax): its V row counts as zero, once the tile is there
-        if (set == 0 && p.pos % kKeyTile != kKeyTile - 1) okt = okt && wait(B_VFULL + n % kVRing, (n / kVRing) & 1);
+      if (j == last) k_scale = last_tile(p, sbase, smem, n, tails, live, ok);
+      tc_fence_after();
+      uint32_t d[16];
+      tmem_ld16(s_cols + (n & 3) * kCols, d);
+      const float4 qf = reinterpret_cast<const float4*>(smem + SM_QF)[(seg & 7) * 2 + set];
+      const float f[H] = {qf.x * k_scale, qf.y * k_scale, qf.z * k_scale, qf.w * k_scale};
+      tmem_landed16(d);
+      float x[H], mine = 0.f;
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        const float a = fmaf(__uint_as_float(d[12 + h]), 0x1p-15f, __uint_as_float(d[8 + h]) * 0x1p-10f);
+        const float b = fmaf(__uint_as_float(d[4 + h]), 0x1p-5f, a) + __uint_as_float(d[h]);
+        x[h] = live ? b * f[h] : -INFINITY;
+        const float mx = warp_max(x[h]);
+        mine = lane == h ? mx : mine;
       }
-      okt = __all_sync(0xffffffffu, okt);
-      float x[H];
-      if (okt) {
-        tc_fence_after();
-        uint32_t d[16];
-        tmem_ld16(s_cols + (n & 3) * kCols, d);
-        const float4 qf = reinterpret_cast<const float4*>(smem + SM_QF)[(seg & 7) * 2 + set];
-        const float f[H] = {qf.x * k_scale, qf.y * k_scale, qf.z * k_scale, qf.w * k_scale};
-        tmem_landed16(d);
-#pragma unroll
-        for (int h = 0; h < H; ++h) {
-          const float a = fmaf(__uint_as_float(d[12 + h]), 0x1p-15f, __uint_as_float(d[8 + h]) * 0x1p-10f);
-          const float b = fmaf(__uint_as_float(d[4 + h]), 0x1p-5f, a) + __uint_as_float(d[h]);
-          x[h] = live ? b * f[h] : -INFINITY;
-        }
-        float mine = 0.f;
-#pragma unroll
-        for (int h = 0; h < H; ++h) {
-          const float mx = warp_max(x[h]);
-          mine = lane == h ? mx : mine;
-        }
-        if (lane < H) red[(n & 1) * 32 + warp * H + lane] = mine;
-        if (scores != nullptr && live) scores[static_cast<size_t>(j) * kKeyTile * 2] = make_float4(x[0], x[1], x[2], x[3]);
-        if (!live && set == 0) {
-          const uint32_t v = sbase + SM_V + n % kVRing * kTileBytes + tid * 128;
-#pragma unroll
-          for (int c = 0; c < 8; ++c) st_shared_v4(v + 16 * c, 0u, 0u, 0u, 0u);
-        }
-      }
+      if (lane < H) red[(n & 1) * 32 + warp * H + lane] = mine;
+      if (scores != nullptr && live) scores[static_cast<size_t>(j) * kKeyTile * 2] = make_float4(x[0], x[1], x[2], x[3]);
       // P buffer n % 2 is free, PV(n - 2) being complete
-      if (n >= 2) okt = okt && wait(B_ODONE + (n & 1), ((n - 2) >> 1) & 1);
-      if (!bar_sync_and(id, kGroup, okt)) return;
+      if (n >= 2) ok = ok && wait(B_ODONE + (n & 1), ((n - 2) >> 1) & 1);
+      if (!bar_sync_and(id, kGroup, ok)) return false;
       const float4* r4 = reinterpret_cast<const float4*>(red + (n & 1) * 32);
       const float4 ra = r4[0], rb = r4[1], rc = r4[2], rd = r4[3];
       const float m[H] = {fmaxf(fmaxf(ra.x, rb.x), fmaxf(rc.x, rd.x)), fmaxf(fmaxf(ra.y, rb.y), fmaxf(rc.y, rd.y)),
                           fmaxf(fmaxf(ra.z, rb.z), fmaxf(rc.z, rd.z)), fmaxf(fmaxf(ra.w, rb.w), fmaxf(rc.w, rd.w))};
-      // weights relative to the tile's largest, times 256, in three pieces
+      // weights relative to the tile's largest, times 256, in two pieces
+      const uint32_t buf = (n & 1) * kPBytes;
       float y[H];
 #pragma unroll
       for (int h = 0; h < H; ++h) {
         x[h] = live ? ex2_approx(x[h] - m[h]) : 0.f;
         y[h] = x[h] * 256.0f;
       }
-      const uint32_t buf = (n & 1) * kOpBytes;
 #pragma unroll
-      for (int piece = 0; piece < 3; ++piece)
+      for (int piece = 0; piece < 2; ++piece)
 #pragma unroll
         for (int h = 0; h < H; h += 2) {
           const uint32_t c = take_piece(y[h], y[h + 1]);
@@ -530,6 +508,7 @@ __device__ __noinline__ void softmax(const F8DecodeParams<CAP>& p, uint32_t sbas
         mbar_arrive(bar0 + 8 * (B_FAC + (n & 3)));
       }
     }
+    tails += s.j1 == p.T ? 1 : 0;
     float* lred = reinterpret_cast<float*>(smem + SM_LRED) + set * 4 * H;
 #pragma unroll
     for (int h = 0; h < H; ++h) {
@@ -545,17 +524,91 @@ __device__ __noinline__ void softmax(const F8DecodeParams<CAP>& p, uint32_t sbas
     }
     // (lred is written again after the next segment's barriers, which thread 0 reaches after this read)
   }
+  return true;
 }
 
 // ----------------------------------------------------------------------------- output warps
+// Merges unit u from its parts' partials: output thread = channel.
 template <int CAP>
-__device__ __noinline__ void output(const F8DecodeParams<CAP>& p, uint32_t sbase, uint8_t* smem, uint32_t tmem, long long start,
-                                    long long end, volatile uint32_t* abort_flag) {
-  const int tid = threadIdx.x - 2 * kGroup, warp = tid >> 5;  // channel = TMEM lane
-  const uint32_t lane_addr = static_cast<uint32_t>(warp * 32) << 16, bar0 = sbase + SM_BAR;
+__device__ __noinline__ void merge(const F8DecodeParams<CAP>& p, uint8_t* smem, int u) {
+  const int tid = threadIdx.x - kOutWarp * 32, g = u % kHkv;
+  const long long u0 = static_cast<long long>(u) * p.T;
+  const int c0 = cta_of_tile(u0, p.W, gridDim.x), np = cta_of_tile(u0 + p.T - 1, p.W, gridDim.x) - c0 + 1;
+  const int slot0 = cta_tile_start(c0, p.W, gridDim.x) >= u0 ? 0 : 1;  // the first part may be its CTA's last segment
+  auto part_index = [&](int k) -> size_t { return static_cast<size_t>(c0 + k) * 2 + (k == 0 ? slot0 : 0); };
+  // weights 2^(m_k - M) / L of the parts, 16 threads a head
+  float* sw = reinterpret_cast<float*>(smem + SM_SW);  // [part][head]
+  {
+    constexpr int kPer = kMaxParts / 16;
+    const int h = tid >> 4, i = tid & 15;
+    float2 ml[kPer];
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      const int k = i + 16 * e;
+      ml[e] = k < np ? __ldcg(reinterpret_cast<const float2*>(p.part_ml + (part_index(k) * kRepText + h) * 2)) : make_float2(-INFINITY, 0.f);
+    }
+    float M = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) M = fmaxf(M, ml[e].x);
+#pragma unroll
+    for (int m = 8; m >= 1; m >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
+    float sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      ml[e].x = i + 16 * e < np ? ex2_approx(ml[e].x - M) : 0.f;
+      sum = fmaf(ml[e].y, ml[e].x, sum);
+    }
+#pragma unroll
+    for (int m = 8; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+    const float inv = 1.0f / sum;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e)
+      if (i + 16 * e < np) sw[(i + 16 * e) * kRepText + h] = ml[e].x * inv;
+    if (p.scores != nullptr && i == 0) p.lse[u * kRepText + h] = M + log2f(sum);
+  }
+  bar_sync(3, kGroup);
+  float acc[kRepText];
+#pragma unroll
+  for (int h = 0; h < kRepText; ++h) acc[h] = 0.f;
+  const float4* sw4 = reinterpret_cast<const float4*>(sw);
+  // from L2, kMergeBatch parts per round of independent 16-byte loads
+  for (int cb = 0; cb < np; cb += kMergeBatch) {
+    float4 v[kMergeBatch][2];
+#pragma unroll
+    for (int b = 0; b < kMergeBatch; ++b) {
+      const int k = min(cb + b, np - 1);  // past the last part: a repeat, unused
+      const float4* src = reinterpret_cast<const float4*>(p.part_o + part_index(k) * kRepText * kD) + 2 * tid;
+      v[b][0] = __ldcg(src);
+      v[b][1] = __ldcg(src + 1);
+    }
+#pragma unroll
+    for (int b = 0; b < kMergeBatch; ++b)
+      if (cb + b < np) {
+        const float4 w0 = sw4[2 * (cb + b)], w1 = sw4[2 * (cb + b) + 1];
+        acc[0] = fmaf(w0.x, v[b][0].x, acc[0]);
+        acc[1] = fmaf(w0.y, v[b][0].y, acc[1]);
+        acc[2] = fmaf(w0.z, v[b][0].z, acc[2]);
+        acc[3] = fmaf(w0.w, v[b][0].w, acc[3]);
+        acc[4] = fmaf(w1.x, v[b][1].x, acc[4]);
+        acc[5] = fmaf(w1.y, v[b][1].y, acc[5]);
+        acc[6] = fmaf(w1.z, v[b][1].z, acc[6]);
+        acc[7] = fmaf(w1.w, v[b][1].w, acc[7]);
+      }
+  }
+  __nv_bfloat16* o = p.layer[u / kHkv].out + static_cast<size_t>(kRepText * g) * kD + tid;
+#pragma unroll
+  for (int h = 0; h < kRepText; ++h) o[h * kD] = __float2bfloat16_rn(acc[h]);
+  if (tid == 0) p.unit_cnt[u] = 0u;  // every part has arrived: ready for the next call
+}
+
+template <int CAP>
+__device__ __noinline__ bool output(const F8DecodeParams<CAP>& p, uint32_t sbase, uint8_t* smem, uint32_t tmem, long long start, long long end) {
+  const int tid = threadIdx.x - kOutWarp * 32, warp = tid >> 5;  // channel = TMEM lane
+  const uint32_t o_cols = tmem + (static_cast<uint32_t>(warp * 32) << 16) + TM_O, bar0 = sbase + SM_BAR;
   volatile uint32_t* merge_flag = reinterpret_cast<volatile uint32_t*>(smem + SM_MERGE);
-  auto wait = [&](int b, uint32_t parity) { return wait_bar(bar0 + 8 * b, parity, abort_flag, p.status); };
+  auto wait = [&](int b, uint32_t parity) { return counted_wait(bar0 + 8 * b, parity); };
   uint32_t n = 0, seg = 0, tails = 0;
+  int late = -1;  // a unit whose part warp 15 counts
   Seg s;
   for (long long t = start; next_seg(t, end, p.T, s); ++seg) {
     const int l = s.u / kHkv, g = s.u % kHkv;
@@ -563,44 +616,38 @@ __device__ __noinline__ void output(const F8DecodeParams<CAP>& p, uint32_t sbase
     const float* vs = L.vs + g * (p.Smax / kScaleBlock + 1);
     if (seg == 0 && s.j1 == p.T && warp < 2) append_row(p, sbase, smem, warp, s.u, 0);
     const int last = s.j1 == p.T ? p.T - 1 : s.j1;  // the tile whose scale the appending warp hands over
-    tails += s.j1 == p.T ? 1 : 0;
     float v_next = s.j0 < last ? vs[s.j0] : 0.f;
     float acc[kRepText];
 #pragma unroll
     for (int h = 0; h < kRepText; ++h) acc[h] = 0.f;
+#pragma unroll 1
     for (int j = s.j0; j < s.j1; ++j, ++n) {
-      bool okt = wait(B_FAC + (n & 3), (n >> 2) & 1);  // the tile's factors are there,
-      okt = okt && wait(B_ODONE + (n & 1), (n >> 1) & 1);  // and its O
+      bool ok = wait(B_FAC + (n & 3), (n >> 2) & 1) && wait(B_ODONE + (n & 1), (n >> 1) & 1);  // the tile's factors, and its O
       float v_scale = v_next;
       if (j + 1 < last) v_next = vs[j + 1];
       if (j == last) {
-        okt = okt && wait_tail(p, sbase, 1, tails - 1, abort_flag);
-        v_scale = reinterpret_cast<const float*>(smem + SM_TAILS)[kTails + tails - 1];
+        ok = ok && wait(B_TAIL + kTails + tails, 0);
+        v_scale = reinterpret_cast<const float*>(smem + SM_TAILS)[kTails + tails];
       }
-      okt = __all_sync(0xffffffffu, okt);
-      if (okt) {
-        tc_fence_after();
-        uint32_t d[32];
-        tmem_ld32(tmem + lane_addr + TM_O + (n & 1) * kCols, d);
-        tmem_wait_ld();
-        reg_fence32(d);
-        const float4* fac = reinterpret_cast<const float4*>(smem + SM_FAC) + (n & 3) * (kRepText / 2);
-        const float vf = v_scale * 0x1p-8f;
-#pragma unroll
-        for (int h = 0; h < kRepText; h += 2) {
-          const float4 f = fac[h / 2];
-          const float o0 = fmaf(__uint_as_float(d[16 + h]), 0x1p-10f, __uint_as_float(d[8 + h]) * 0x1p-5f) + __uint_as_float(d[h]);
-          const float o1 = fmaf(__uint_as_float(d[17 + h]), 0x1p-10f, __uint_as_float(d[9 + h]) * 0x1p-5f) + __uint_as_float(d[h + 1]);
-          acc[h] = fmaf(acc[h], f.x, o0 * (f.y * vf));
-          acc[h + 1] = fmaf(acc[h + 1], f.z, o1 * (f.w * vf));
-        }
-        tc_fence_before();
-      }
-      if (!bar_sync_and(3, kGroup, okt)) return;
+      tc_fence_after();
+      uint32_t d[16];  // O^T row = channel tid, columns (piece, head)
+      tmem_ld16(o_cols + (n & 1) * kOutCols, d);
+      const float4* fac = reinterpret_cast<const float4*>(smem + SM_FAC) + (n & 3) * (kRepText / 2);
+      const float4 f[4] = {fac[0], fac[1], fac[2], fac[3]};
+      const float vf = v_scale * 0x1p-8f;
+      tmem_landed16(d);
+      tc_fence_before();
+      if (!bar_sync_and(3, kGroup, ok)) return false;
       if (tid == 0) mbar_arrive(bar0 + 8 * (B_OFREE + (n & 1)));
+#pragma unroll
+      for (int h = 0; h < kRepText; h += 2) {
+        acc[h] = fmaf(acc[h], f[h / 2].x, fmaf(__uint_as_float(d[8 + h]), 0x1p-5f, __uint_as_float(d[h])) * (f[h / 2].y * vf));
+        acc[h + 1] = fmaf(acc[h + 1], f[h / 2].z, fmaf(__uint_as_float(d[9 + h]), 0x1p-5f, __uint_as_float(d[h + 1])) * (f[h / 2].w * vf));
+      }
     }
+    tails += s.j1 == p.T ? 1 : 0;
     // ---- the segment's end: its sums, then its output or its part of one
-    if (!bar_sync_and(3, kGroup, wait(B_FIN + (seg & 7), (seg >> 3) & 1))) return;
+    if (!bar_sync_and(3, kGroup, wait(B_FIN + (seg & 7), (seg >> 3) & 1))) return false;
     const float2* fin = reinterpret_cast<const float2*>(smem + SM_FIN) + (seg & 7) * kRepText;
     if (s.j0 == 0 && s.j1 == p.T) {
       __nv_bfloat16* o = L.out + static_cast<size_t>(kRepText * g) * kD + tid;
@@ -610,86 +657,32 @@ __device__ __noinline__ void output(const F8DecodeParams<CAP>& p, uint32_t sbase
       continue;
     }
     // Part index: 2 c + slot (a part is its CTA's first segment or its last). Layout [part][channel][8 heads].
-    const int slot = seg == 0 ? 0 : 1;
-    const size_t ps = static_cast<size_t>(blockIdx.x) * 2 + slot;
+    const size_t ps = static_cast<size_t>(blockIdx.x) * 2 + (seg == 0 ? 0 : 1);
     float4* po = reinterpret_cast<float4*>(p.part_o + ps * kRepText * kD) + 2 * tid;
     po[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
     po[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
     if (tid < kRepText) *reinterpret_cast<float2*>(p.part_ml + (ps * kRepText + tid) * 2) = fin[tid];
     bar_sync(3, kGroup);
-    const long long u0 = static_cast<long long>(s.u) * p.T;
-    const int c0 = cta_of_tile(u0, p.W, gridDim.x), c1 = cta_of_tile(u0 + p.T - 1, p.W, gridDim.x);
-    // the count's release publishes this part, and the last part's acquire orders the others' before its reads
-    if (tid == 0) *merge_flag = atom_add_acq_rel_gpu(p.unit_cnt + s.u, 1u) == static_cast<uint32_t>(c1 - c0) ? 1u : 0u;
-    bar_sync(3, kGroup);
-    if (*merge_flag) {
-      const int np = c1 - c0 + 1;
-      const int slot0 = cta_tile_start(c0, p.W, gridDim.x) >= u0 ? 0 : 1;  // the first part may be its CTA's last segment
-      auto part_index = [&](int k) -> size_t { return static_cast<size_t>(c0 + k) * 2 + (k == 0 ? slot0 : 0); };
-      // weights 2^(m_k - M) / L of the parts, 16 threads a head
-      float* sw = reinterpret_cast<float*>(smem + SM_SW);  // [part][head]
-      {
-        constexpr int kPer = kMaxParts / 16;
-        const int h = tid >> 4, i = tid & 15;
-        float2 ml[kPer];
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-          const int k = i + 16 * e;
-          ml[e] = k < np ? __ldcg(reinterpret_cast<const float2*>(p.part_ml + (part_index(k) * kRepText + h) * 2)) : make_float2(-INFINITY, 0.f);
-        }
-        float M = -INFINITY;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) M = fmaxf(M, ml[e].x);
-#pragma unroll
-        for (int m = 8; m >= 1; m >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
-        float sum = 0.f;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-          ml[e].x = i + 16 * e < np ? ex2_approx(ml[e].x - M) : 0.f;
-          sum = fmaf(ml[e].y, ml[e].x, sum);
-        }
-#pragma unroll
-        for (int m = 8; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-        const float inv = 1.0f / sum;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e)
-          if (i + 16 * e < np) sw[(i + 16 * e) * kRepText + h] = ml[e].x * inv;
-        if (p.scores != nullptr && i == 0) p.lse[s.u * kRepText + h] = M + log2f(sum);
-      }
-      bar_sync(3, kGroup);
-#pragma unroll
-      for (int h = 0; h < kRepText; ++h) acc[h] = 0.f;
-      const float4* sw4 = reinterpret_cast<const float4*>(sw);
-      // from L2, kMergeBatch parts per round of independent 16-byte loads
-      for (int cb = 0; cb < np; cb += kMergeBatch) {
-        float4 v[kMergeBatch][2];
-#pragma unroll
-        for (int b = 0; b < kMergeBatch; ++b) {
-          const int k = min(cb + b, np - 1);  // past the last part: a repeat, unused
-          const float4* src = reinterpret_cast<const float4*>(p.part_o + part_index(k) * kRepText * kD) + 2 * tid;
-          v[b][0] = __ldcg(src);
-          v[b][1] = __ldcg(src + 1);
-        }
-#pragma unroll
-        for (int b = 0; b < kMergeBatch; ++b)
-          if (cb + b < np) {
-            const float4 w0 = sw4[2 * (cb + b)], w1 = sw4[2 * (cb + b) + 1];
-            acc[0] = fmaf(w0.x, v[b][0].x, acc[0]);
-            acc[1] = fmaf(w0.y, v[b][0].y, acc[1]);
-            acc[2] = fmaf(w0.z, v[b][0].z, acc[2]);
-            acc[3] = fmaf(w0.w, v[b][0].w, acc[3]);
-            acc[4] = fmaf(w1.x, v[b][1].x, acc[4]);
-            acc[5] = fmaf(w1.y, v[b][1].y, acc[5]);
-            acc[6] = fmaf(w1.z, v[b][1].z, acc[6]);
-            acc[7] = fmaf(w1.w, v[b][1].w, acc[7]);
-          }
-      }
-#pragma unroll
-      for (int h = 0; h < kRepText; ++h) L.out[static_cast<size_t>(kRepText * g + h) * kD + tid] = __float2bfloat16_rn(acc[h]);
-      if (tid == 0) p.unit_cnt[s.u] = 0u;  // every part has arrived: ready for the next call
+    if (t < end) {  // (the first segment)
+      late = s.u;
+      if (tid == 0) mbar_arrive(bar0 + 8 * B_PART);
+      continue;
     }
-    bar_sync(3, kGroup);  // the flag is read before the next segment overwrites it
+    if (late >= 0) break;  // (SM_MERGE is the other part's until it has been read)
+    if (tid == 0) *merge_flag = count_part(p, s.u) ? 1u : 0u;
+    bar_sync(3, kGroup);
+    if (*merge_flag) merge(p, smem, s.u);
+    return true;
   }
+  if (late < 0) return true;
+  if (!bar_sync_and(3, kGroup, wait(B_LATE, 0))) return false;
+  if (*merge_flag) merge(p, smem, late);
+  if (s.j1 == p.T || s.u == late) return true;  // (a CTA's last segment is a part unless it ends its unit)
+  bar_sync(3, kGroup);
+  if (tid == 0) *merge_flag = count_part(p, s.u) ? 1u : 0u;
+  bar_sync(3, kGroup);
+  if (*merge_flag) merge(p, smem, s.u);
+  return true;
 }
 
 }  // namespace f8d
@@ -700,22 +693,14 @@ __global__ void __launch_bounds__(f8d::kThreads, 1) fp8_decode_kernel(const __gr
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = smem_u32(smem), bar0 = sbase + SM_BAR;
-  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + SM_ABORT);
   const long long start = cta_tile_start(blockIdx.x, p.W, gridDim.x), end = cta_tile_start(blockIdx.x + 1, p.W, gridDim.x);
   const int warp = threadIdx.x >> 5;
-  if (threadIdx.x == 0) {
-    for (int b = 0; b < kNumBars; ++b)  // (what the softmax warps tell comes from both sets)
-      mbar_init(bar0 + 8 * b, (b >= B_PFULL && b < B_PFULL + 2) || (b >= B_FAC && b < B_FIN + 8) ? 2 : 1);
-    *abort_flag = 0u;
+  if (threadIdx.x >= 256 && threadIdx.x < 256 + kNumBars) {
+    const int b = threadIdx.x - 256;  // (what softmax warps tell comes from two sets)
+    mbar_init(bar0 + 8 * b, (b >= B_PFULL && b < B_PFULL + 2) || (b >= B_FAC && b < B_FIN + 8) ? 2 : 1);
     fence_mbar_init();
   }
   if (threadIdx.x < kD / 2) reinterpret_cast<float4*>(smem + SM_ROT)[threadIdx.x] = p.rot[threadIdx.x];
-  if (threadIdx.x >= 256 && threadIdx.x < 256 + 2 * kTails) reinterpret_cast<uint32_t*>(smem + SM_TAILF)[threadIdx.x - 256] = 0u;
-  // rows 24-31 of both P operands are the padding of N = 32
-  if (threadIdx.x >= 128 && threadIdx.x < 256) {
-    const uint32_t i = threadIdx.x - 128;
-    st_shared_v4(sbase + SM_PT + (i >> 6) * kOpBytes + 24 * 128 + (i & 63) * 16, 0u, 0u, 0u, 0u);
-  }
   if (warp == 0) {
     tmem_alloc(sbase + SM_TMEM, kTmemCols);
     tmem_relinquish();
@@ -741,19 +726,21 @@ __global__ void __launch_bounds__(f8d::kThreads, 1) fp8_decode_kernel(const __gr
   }
   // everything below reads what earlier kernels in the stream wrote
   pdl_wait_primary();
-  if (warp < 8) {
-    softmax(p, sbase, smem, tmem, warp >> 2, start, end, abort_flag);
-  } else if (warp < 12) {
-    output(p, sbase, smem, tmem, start, end, abort_flag);
+  bool ok = true;
+  if (warp < kOutWarp) {
+    ok = softmax(p, sbase, smem, tmem, warp >> 2, start, end);
+  } else if (warp < kOutWarp + 4) {
+    ok = output(p, sbase, smem, tmem, start, end);
   } else if (warp == 12) {
-    producer(p, sbase, start, end, abort_flag);
+    ok = producer(p, sbase, start, end);
   } else if (warp == 13) {
-    qk_issuer(p, sbase, tmem, start, end, abort_flag);
+    ok = qk_issuer(p, sbase, tmem, start, end);
   } else if (warp == 14) {
-    pv_issuer(p, sbase, tmem, static_cast<uint32_t>(end - start), abort_flag);
+    ok = pv_issuer(p, sbase, tmem, static_cast<uint32_t>(end - start));
   } else {
-    prepare(p, sbase, smem, start, end, abort_flag);
+    ok = prepare(p, sbase, smem, start, end);
   }
+  if (!ok && (threadIdx.x & 31) == 0) atomicOr(p.status, kErrF8DecodeWait);
   pdl_launch_dependents();
   tc_fence_before();
   __syncthreads();
