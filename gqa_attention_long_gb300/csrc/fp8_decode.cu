@@ -189,32 +189,28 @@ __device__ __noinline__ void append_row(const F8DecodeParams<CAP>& p, uint32_t s
   }
 }
 
-// q rows h0 .. h0 + N - 1 of segment seg's unit, as pieces, into its Q buffer: one warp.
-template <int N, int CAP>
-__device__ __forceinline__ void prepare_q(const F8DecodeParams<CAP>& p, uint32_t sbase, uint8_t* smem, int u, int h0, uint32_t seg, int lane) {
+// q row h of segment seg's unit, as pieces, into its Q buffer: one warp.
+template <int CAP>
+__device__ __noinline__ void prepare_q(const F8DecodeParams<CAP>& p, uint32_t sbase, uint8_t* smem, int u, int h, uint32_t seg) {
+  const int lane = threadIdx.x & 31;
   const F8AttnLayer& L = p.layer[u / kHkv];
-  const float4* rot = reinterpret_cast<const float4*>(smem + SM_ROT);
-  float x[N][4], gm[4];
+  float x[4], gm[4], y[4];
   f8_load_row(L.q_gamma, lane, gm);
+  f8_load_row(L.q_raw + (kRepText * (u % kHkv) + h) * kD, lane, x);
+  f8_norm_rope(x, gm, reinterpret_cast<const float4*>(smem + SM_ROT), lane, y);
+  const int e = f16_exponent(f8_row_max(y));  // the row's largest magnitude is in [2^e, 2^(e + 1)): put it in [128, 256)
+  const float up = f8_pow2(min(7 - e, 126));
 #pragma unroll
-  for (int k = 0; k < N; ++k) f8_load_row(L.q_raw + (kRepText * (u % kHkv) + h0 + k) * kD, lane, x[k]);
+  for (int i = 0; i < 4; ++i) y[i] *= up;
+  if (lane == 0) reinterpret_cast<float*>(smem + SM_QF)[(seg & 7) * kRepText + h] = p.scale_log2 * f8_pow2(max(e - 7, -126));  // over up
+  // 16-byte chunk c of row r at chunk c ^ (r % 8)
+  const uint32_t r0 = (h >> 2) * 16 + (h & 3), c = lane >> 3;
+  uint32_t row = sbase + SM_QT + (seg & 1) * kOpBytes + r0 * 128 + ((2 * lane) & 15);
 #pragma unroll
-  for (int k = 0; k < N; ++k) {
-    const int h = h0 + k;
-    float y[4];
-    f8_norm_rope(x[k], gm, rot, lane, y);
-    const int e = f16_exponent(f8_row_max(y));  // the row's largest magnitude is in [2^e, 2^(e + 1)): put it in [128, 256)
-    const float up = f8_pow2(min(7 - e, 126));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] *= up;
-    if (lane == 0) reinterpret_cast<float*>(smem + SM_QF)[(seg & 7) * kRepText + h] = __fdiv_rn(p.scale_log2, up);
-#pragma unroll
-    for (int piece = 0; piece < 4; ++piece) {
-      const uint32_t lo = take_piece(y[0], y[1]), hi = take_piece(y[2], y[3]);
-      const uint32_t r = (h >> 2) * 16 + piece * 4 + (h & 3), row = sbase + SM_QT + (seg & 1) * kOpBytes + r * 128;
-      st_shared_u16(row + (((lane >> 3) ^ (r & 7)) << 4) + ((2 * lane) & 15), static_cast<uint16_t>(lo));  // 16-byte chunk c of row r at chunk c ^ (r % 8)
-      st_shared_u16(row + ((((lane >> 3) + 4) ^ (r & 7)) << 4) + ((2 * lane) & 15), static_cast<uint16_t>(hi));
-    }
+  for (int piece = 0; piece < 4; ++piece, row += 4 * 128) {
+    const uint32_t r = (r0 + 4 * piece) & 7, lo = take_piece(y[0], y[1]), hi = take_piece(y[2], y[3]);
+    st_shared_u16(row + ((c ^ r) << 4), static_cast<uint16_t>(lo));
+    st_shared_u16(row + (((c + 4) ^ r) << 4), static_cast<uint16_t>(hi));
   }
   fence_proxy_async_smem();  // read by the tensor core
 }
@@ -230,7 +226,7 @@ __device__ __forceinline__ bool count_part(const P& p, int u) {
 
 // One warp: the Q and the new rows of every segment but the first.
 template <int CAP>
-__device__ __noinline__ bool prepare(const F8DecodeParams<CAP>& p, uint32_t sbase, uint8_t* smem, long long start, long long end) {
+__device__ __forceinline__ bool prepare(const F8DecodeParams<CAP>& p, uint32_t sbase, uint8_t* smem, long long start, long long end) {
   const int lane = threadIdx.x & 31;
   const uint32_t bar0 = sbase + SM_BAR;
   uint32_t idx = 0, seg = 0;
@@ -239,8 +235,8 @@ __device__ __noinline__ bool prepare(const F8DecodeParams<CAP>& p, uint32_t sbas
     if (seg > 0) {
       const uint32_t buf = seg & 1;
       if (seg > 1 && !counted_wait(bar0 + 8 * (B_QFREE + buf), ((seg - 2) >> 1) & 1)) return false;
-      prepare_q<4>(p, sbase, smem, s.u, 0, seg, lane);
-      prepare_q<4>(p, sbase, smem, s.u, 4, seg, lane);
+#pragma unroll 1
+      for (int h = 0; h < kRepText; ++h) prepare_q(p, sbase, smem, s.u, h, seg);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar0 + 8 * (B_QFULL + buf));
       if (s.j1 == p.T) {
@@ -272,7 +268,7 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 template <int CAP>
-__device__ __noinline__ bool producer(const F8DecodeParams<CAP>& p, uint32_t sbase, long long start, long long end) {
+__device__ __forceinline__ bool producer(const F8DecodeParams<CAP>& p, uint32_t sbase, long long start, long long end) {
   const uint64_t pol = l2_policy_evict_first();  // every cache tile is read once
   const uint32_t bar0 = sbase + SM_BAR;
   auto wait = [&](int b, uint32_t parity) { return counted_wait(bar0 + 8 * b, parity); };
@@ -321,7 +317,7 @@ __device__ __noinline__ bool producer(const F8DecodeParams<CAP>& p, uint32_t sba
 
 // QK(n) needs its tile, its segment's Q, and score buffer n % 4 read by the softmax of tile n - 4.
 template <int CAP>
-__device__ __noinline__ bool qk_issuer(const F8DecodeParams<CAP>& p, uint32_t sbase, uint32_t tmem, long long start, long long end) {
+__device__ __forceinline__ bool qk_issuer(const F8DecodeParams<CAP>& p, uint32_t sbase, uint32_t tmem, long long start, long long end) {
   constexpr uint32_t kIdesc = umma_idesc_f16(128, kCols, false, false, false);  // (e4m3 is format code 0); A and B K-major
   const uint32_t bar0 = sbase + SM_BAR;
   const uint64_t kd = sw128_desc(sbase + SM_K, 16, 1024), qd = sw128_desc(sbase + SM_QT, 16, 1024);
@@ -358,7 +354,7 @@ __device__ __noinline__ bool qk_issuer(const F8DecodeParams<CAP>& p, uint32_t sb
 
 // PV(n) needs its tile, P(n), and O buffer n % 2 read out by the output warps.
 template <int CAP>
-__device__ __noinline__ bool pv_issuer(const F8DecodeParams<CAP>& p, uint32_t sbase, uint32_t tmem, uint32_t total) {
+__device__ __forceinline__ bool pv_issuer(const F8DecodeParams<CAP>& p, uint32_t sbase, uint32_t tmem, uint32_t total) {
   constexpr uint32_t kIdesc = umma_idesc_f16(128, kOutCols, false, true, false);  // A = V MN-major, B = P K-major
   const uint32_t bar0 = sbase + SM_BAR;
   const uint64_t vd = sw128_desc(sbase + SM_V, kTileBytes, 1024), pd = sw128_desc(sbase + SM_PT, 16, 1024);
@@ -408,7 +404,7 @@ __device__ __noinline__ float last_tile(const F8DecodeParams<CAP>& p, uint32_t s
 
 // One set of warps: heads 4 set .. 4 set + 3 of every tile.
 template <int CAP>
-__device__ __noinline__ bool softmax(const F8DecodeParams<CAP>& p, uint32_t sbase, uint8_t* smem, uint32_t tmem, int set, long long start,
+__device__ __forceinline__ bool softmax(const F8DecodeParams<CAP>& p, uint32_t sbase, uint8_t* smem, uint32_t tmem, int set, long long start,
                                      long long end) {
   constexpr int H = kRepText / 2;
   const int tid = threadIdx.x & (kGroup - 1), warp = tid >> 5, lane = tid & 31;  // key of a tile = TMEM lane
@@ -432,7 +428,7 @@ __device__ __noinline__ bool softmax(const F8DecodeParams<CAP>& p, uint32_t sbas
     const int last = s.j1 == p.T ? p.T - 1 : s.j1;  // the tile whose scale the appending warp hands over
     float k_next = s.j0 < last ? ks[s.j0] : 0.f;
     if (seg == 0) {
-      prepare_q<1>(p, sbase, smem, s.u, 4 * set + warp, seg, lane);
+      prepare_q(p, sbase, smem, s.u, 4 * set + warp, seg);
       bar_sync(4, 2 * kGroup);
       if (threadIdx.x == 0) mbar_arrive(bar0 + 8 * B_QFULL);
     }
@@ -454,6 +450,8 @@ __device__ __noinline__ bool softmax(const F8DecodeParams<CAP>& p, uint32_t sbas
       tmem_ld16(s_cols + (n & 3) * kCols, d);
       const float4 qf = reinterpret_cast<const float4*>(smem + SM_QF)[(seg & 7) * 2 + set];
       const float f[H] = {qf.x * k_scale, qf.y * k_scale, qf.z * k_scale, qf.w * k_scale};
+      // P buffer n % 2 is free, PV(n - 2) being complete
+      if (n >= 2) ok = ok && wait(B_ODONE + (n & 1), ((n - 2) >> 1) & 1);
       tmem_landed16(d);
       float x[H], mine = 0.f;
 #pragma unroll
@@ -466,8 +464,6 @@ __device__ __noinline__ bool softmax(const F8DecodeParams<CAP>& p, uint32_t sbas
       }
       if (lane < H) red[(n & 1) * 32 + warp * H + lane] = mine;
       if (scores != nullptr && live) scores[static_cast<size_t>(j) * kKeyTile * 2] = make_float4(x[0], x[1], x[2], x[3]);
-      // P buffer n % 2 is free, PV(n - 2) being complete
-      if (n >= 2) ok = ok && wait(B_ODONE + (n & 1), ((n - 2) >> 1) & 1);
       if (!bar_sync_and(id, kGroup, ok)) return false;
       const float4* r4 = reinterpret_cast<const float4*>(red + (n & 1) * 32);
       const float4 ra = r4[0], rb = r4[1], rc = r4[2], rd = r4[3];
@@ -476,10 +472,15 @@ __device__ __noinline__ bool softmax(const F8DecodeParams<CAP>& p, uint32_t sbas
       // weights relative to the tile's largest, times 256, in two pieces
       const uint32_t buf = (n & 1) * kPBytes;
       float y[H];
+      float2 fac[H];  // (what the sums before are multiplied by, the tile's share)
 #pragma unroll
       for (int h = 0; h < H; ++h) {
         x[h] = live ? ex2_approx(x[h] - m[h]) : 0.f;
         y[h] = x[h] * 256.0f;
+        const float top = fmaxf(m_run[h], m[h]);
+        fac[h] = make_float2(ex2_approx(m_run[h] - top), ex2_approx(m[h] - top));
+        m_run[h] = top;
+        lsum[h] = fmaf(lsum[h], fac[h].x, x[h] * fac[h].y);
       }
 #pragma unroll
       for (int piece = 0; piece < 2; ++piece)
@@ -489,22 +490,16 @@ __device__ __noinline__ bool softmax(const F8DecodeParams<CAP>& p, uint32_t sbas
           st_shared_u8(at[h] + buf + piece * kRepText * 128, c);
           st_shared_u8(at[h + 1] + buf + piece * kRepText * 128, c >> 8);
         }
-      fence_proxy_async_smem();  // P, and zeroed V rows, are read by the tensor core
-      tc_fence_before();
-      bar_sync(id, kGroup);
-      if (tid == 0) mbar_arrive(bar0 + 8 * (B_PFULL + (n & 1)));  // P(n) is out
-      float2 fac[H];
-#pragma unroll
-      for (int h = 0; h < H; ++h) {
-        const float top = fmaxf(m_run[h], m[h]);
-        fac[h] = make_float2(ex2_approx(m_run[h] - top), ex2_approx(m[h] - top));
-        m_run[h] = top;
-        lsum[h] = fmaf(lsum[h], fac[h].x, x[h] * fac[h].y);
-      }
       if (tid == 0) {
         float4* to = reinterpret_cast<float4*>(smem + SM_FAC) + ((n & 3) * kRepText + set * H) / 2;
         to[0] = make_float4(fac[0].x, fac[0].y, fac[1].x, fac[1].y);
         to[1] = make_float4(fac[2].x, fac[2].y, fac[3].x, fac[3].y);
+      }
+      fence_proxy_async_smem();  // P, and zeroed V rows, are read by the tensor core
+      tc_fence_before();
+      bar_sync(id, kGroup);
+      if (tid == 0) {
+        mbar_arrive(bar0 + 8 * (B_PFULL + (n & 1)));  // P(n) is out
         mbar_arrive(bar0 + 8 * (B_FAC + (n & 3)));
       }
     }
@@ -602,7 +597,7 @@ __device__ __noinline__ void merge(const F8DecodeParams<CAP>& p, uint8_t* smem, 
 }
 
 template <int CAP>
-__device__ __noinline__ bool output(const F8DecodeParams<CAP>& p, uint32_t sbase, uint8_t* smem, uint32_t tmem, long long start, long long end) {
+__device__ __forceinline__ bool output(const F8DecodeParams<CAP>& p, uint32_t sbase, uint8_t* smem, uint32_t tmem, long long start, long long end) {
   const int tid = threadIdx.x - kOutWarp * 32, warp = tid >> 5;  // channel = TMEM lane
   const uint32_t o_cols = tmem + (static_cast<uint32_t>(warp * 32) << 16) + TM_O, bar0 = sbase + SM_BAR;
   volatile uint32_t* merge_flag = reinterpret_cast<volatile uint32_t*>(smem + SM_MERGE);
