@@ -13,7 +13,8 @@ cudaError_t launch_fp8_rows(const F8RowsParams& p, int n_layers, int dtype, bool
 cudaError_t fp8_decode_set_attributes();
 template <int CAP>
 cudaError_t launch_fp8_decode(const F8DecodeParams<CAP>& p, cudaLaunchConfig_t cfg);
-cudaError_t launch_fp8_evict(const F8EvictParams& p, int sm_count, cudaLaunchConfig_t cfg);
+cudaError_t fp8_evict_set_attributes();
+cudaError_t launch_fp8_evict(F8EvictParams& p, int sm_count, cudaLaunchConfig_t cfg);
 }  // namespace ea
 
 namespace {
@@ -90,6 +91,15 @@ bool decode_attrs_ready(int dev) {
   static OncePerDevice once;
   return once(dev, [] {
     const bool ok = fp8_decode_set_attributes() == cudaSuccess;
+    cudaGetLastError();
+    return ok;
+  });
+}
+
+bool evict_attrs_ready(int dev) {
+  static OncePerDevice once;
+  return once(dev, [] {
+    const bool ok = fp8_evict_set_attributes() == cudaSuccess;
     cudaGetLastError();
     return ok;
   });
@@ -264,7 +274,7 @@ int expert_attn_evict_fp8(const ea_evict_fp8_args* layers, int n_layers, int n_r
   if (rc != EA_OK) return rc;
   int dev;
   DeviceInfo di;
-  if (!device_info(&dev, &di)) return EA_ERR_UNSUPPORTED;
+  if (!device_info(&dev, &di) || !evict_attrs_ready(dev)) return EA_ERR_UNSUPPORTED;
   const F8EvictWs wl = f8_evict_ws(n_layers, Smax);
   if (ws_bytes < wl.total) return EA_ERR_WORKSPACE;
   if (n_keep == 0) return EA_OK;

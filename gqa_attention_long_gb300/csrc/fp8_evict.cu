@@ -5,17 +5,23 @@
 // [0, n_keep) in their order, in place or into another cache. Rows of several blocks meet in one: its scale becomes the
 // largest of theirs, and a code of a row with a smaller one, s', is rounded again, code (s' / s).
 //
-// Two kernels. The selector (one CTA per (layer, kv head)) finds the weight of the last row that stays by its bits, from
-// the top ones down, and writes the kept rows' numbers. The mover takes one destination block of K or of V of one head at a time:
+// Two kernels. The selector takes a head's weights with one CTA, or, from kSlice rows on, a cluster of up to eight that share them: it
+// finds the bits of the last weight that stays, eleven at a time from the top (a histogram of what shares the bits found so far, summed over the
+// cluster's shared memory), then numbers the rows that stay. The mover takes one destination block of K or of V of one head at a time:
 // 128 rows are read, all of them, before one is written. In place, a block may be written once the rows that were in it have been read: those
 // that stay go to at most two destination blocks, which the selector's counts name, with lower numbers or the same; work is
 // handed out in order, so whoever waits waits for work that is already under way. (Bytes: the weights, and a kept row's 256 twice.)
+#include "cluster_exit.cuh"
 #include "fp8.cuh"
 
 namespace ea {
 namespace ev {
 
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kSlice = 8192;        // rows of one CTA of a cluster, while eight suffice
+constexpr int kCached = 32768;      // rows of a slice whose bits are kept in shared memory (else they are read again)
+constexpr int kMaxCluster = 8;
 constexpr int kMoveThreads = 256;
 constexpr int kPieces = kScaleBlock * kD / 16 / kMoveThreads;  // 16-byte pieces of a block that a thread moves
 
@@ -24,86 +30,157 @@ __device__ __forceinline__ uint32_t key_of(float w) {
   const uint32_t u = __float_as_uint(w + 0.0f);
   return w != w ? 0xFFFFFFFFu : (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
+__device__ __forceinline__ uint4 ld_cluster_v4(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+
+struct Sel {  // a CTA's shared memory; the slice's bits follow
+  alignas(16) uint32_t hist[3][kBins];
+  uint32_t warp[kSelWarps][2];  // rows above the threshold and at it, by warp
+  uint32_t total[2];            // and of the slice
+  uint32_t scan[kSelWarps];
+  uint32_t found[2];
+};
 
 }  // namespace ev
 
 __global__ void __launch_bounds__(ev::kSelThreads) fp8_evict_select_kernel(const __grid_constant__ F8EvictParams p) {
   using namespace ev;
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t sums[2][32];
-  __shared__ uint32_t found[2];
-  const int u = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  extern __shared__ uint8_t ev_smem[];
+  Sel& sm = *reinterpret_cast<Sel*>(ev_smem);
+  uint32_t* keys = reinterpret_cast<uint32_t*>(ev_smem + sizeof(Sel));
+  const int cs = p.cluster, u = blockIdx.x / cs, rank = blockIdx.x % cs, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const F8EvictLayer& L = p.layer[u / kHkv];
   const float* w = L.w + static_cast<size_t>(u % kHkv) * p.Smax;
   int* kept = L.kept + static_cast<size_t>(u % kHkv) * p.n_keep;
   uint32_t* before = p.before + static_cast<size_t>(u) * (p.blocks + 1);
   const int lo = p.n_first, hi = p.n_rows - p.n_recent;  // rows that are chosen among
-  pdl_wait_primary();
-  for (int i = tid; i < 2 * p.blocks; i += kSelThreads) p.loaded[static_cast<size_t>(u) * 2 * p.blocks + i] = 0u;
-  if (u == 0 && tid == 0) *p.ticket = 0u;
-  // the bits of the least weight that stays: `top` of them are known, `need` rows stay among those that share them
+  const int s0 = min(rank * p.slice, p.n_rows), s1 = min(s0 + p.slice, p.n_rows);  // this CTA's rows
+  const bool cached = p.slice <= kCached;
   uint32_t need = p.n_keep - p.n_first - p.n_recent, bits = 0u;
-  for (int top = 0; top < 32; top += 8) {
-    const int shift = 24 - top;
-    if (tid < 256) hist[tid] = 0u;
-    __syncthreads();
-    for (int i = lo + tid; i < hi; i += kSelThreads) {
-      const uint32_t k = key_of(w[i]);
-      if (top == 0 || (k >> (shift + 8)) == (bits >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255u], 1u);
-    }
-    __syncthreads();
-    if (tid == 0) {
-      uint32_t n = 0, d = 255;
-      for (;; --d) {
-        if (n + hist[d] >= need || d == 0) break;
-        n += hist[d];
-      }
-      found[0] = d;
-      found[1] = n;
-    }
-    __syncthreads();
-    bits |= found[0] << shift;
-    need -= found[1];
-    __syncthreads();
+  for (int i = tid; i < 3 * kBins / 4; i += kSelThreads) reinterpret_cast<uint4*>(sm.hist)[i] = make_uint4(0u, 0u, 0u, 0u);
+  __syncthreads();
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  if (rank == 0) {
+    for (int i = tid; i < 2 * p.blocks; i += kSelThreads) p.loaded[static_cast<size_t>(u) * 2 * p.blocks + i] = 0u;
+    if (u == 0 && tid == 0) *p.ticket = 0u;
   }
-  // need > 0 rows of weight `bits` stay, the lowest ones (0 if no row is chosen at all)
-  uint32_t above = 0, equal = 0;  // among the rows before
-  for (int base = 0; base < p.n_rows; base += kSelThreads) {
-    const int i = base + tid;
-    bool gt = false, eq = false;
-    if (i < p.n_rows) {
+  // Of the least weight that stays: 11, then 11, then 10 bits. `need` rows stay among those that share the bits known so far.
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, width = pass == 2 ? 10 : 11;
+    uint32_t* hist = sm.hist[pass];
+    for (int i = s0 + tid; i < s1; i += kSelThreads) {
+      uint32_t k;
+      if (pass == 0 || !cached) {
+        k = i < lo || i >= hi ? 0u : key_of(w[i]);
+        if (cached) keys[i - s0] = k;
+      } else {
+        k = keys[i - s0];
+      }
+      if (i >= lo && i < hi && (pass == 0 || (k >> (shift + width)) == (bits >> (shift + width))))
+        atomicAdd(&hist[(k >> shift) & ((1u << width) - 1u)], 1u);
+    }
+    if (cs > 1) cluster_sync();
+    else __syncthreads();
+    // thread t: bins kBins - 4 - 4 t .. + 3, the cluster's; then how many rows lie above them
+    const int b0 = kBins - 4 - 4 * tid;
+    uint4 c = make_uint4(0u, 0u, 0u, 0u);
+    const uint32_t at = smem_u32(hist + b0);
+    for (int r = 0; r < cs; ++r) {
+      const uint4 v = cs > 1 ? ld_cluster_v4(mapa_shared(at, r)) : *reinterpret_cast<const uint4*>(hist + b0);
+      c.x += v.x; c.y += v.y; c.z += v.z; c.w += v.w;
+    }
+    const uint32_t mine = (c.x + c.y) + (c.z + c.w);
+    uint32_t sum = mine;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const uint32_t v = __shfl_up_sync(0xffffffffu, sum, m);
+      if (lane >= m) sum += v;
+    }
+    if (lane == 31) sm.scan[warp] = sum;
+    __syncthreads();
+    uint32_t above = sum - mine;
+#pragma unroll
+    for (int k = 0; k < kSelWarps; ++k) above += k < warp ? sm.scan[k] : 0u;
+    if (above < need && need <= above + mine) {  // (one thread, unless nothing is needed)
+      uint32_t d = b0 + 3;
+      if (above + c.w < need) { above += c.w; --d;
+        if (above + c.z < need) { above += c.z; --d;
+          if (above + c.y < need) { above += c.y; --d; } } }
+      sm.found[0] = d;
+      sm.found[1] = above;
+    }
+    __syncthreads();
+    if (need > 0) {
+      bits |= sm.found[0] << shift;
+      need -= sm.found[1];
+    }
+  }
+  if (p.n_keep == p.n_first + p.n_recent) bits = 0xFFFFFFFFu;  // none is chosen: nothing lies above, and need is 0
+  // Rows above the threshold (or kept anyway) and at it, by warp: a warp has 32-row groups in a row
+  const int groups = (s1 - s0 + 31) / 32, per = (groups + kSelWarps - 1) / kSelWarps;
+  const int g0 = min(warp * per, groups), g1 = min(g0 + per, groups);
+  auto look = [&](int grp, bool& gt, bool& eq) {
+    const int i = s0 + 32 * grp + lane;
+    gt = eq = false;
+    if (i < s1) {
       if (i < lo || i >= hi) {
         gt = true;
       } else {
-        const uint32_t k = key_of(w[i]);
+        const uint32_t k = cached ? keys[i - s0] : key_of(w[i]);
         gt = k > bits;
         eq = k == bits;
       }
     }
-    const uint32_t mg = __ballot_sync(0xffffffffu, gt), me = __ballot_sync(0xffffffffu, eq), below = (1u << lane) - 1u;
-    if (lane == 0) {
-      sums[0][warp] = __popc(mg);
-      sums[1][warp] = __popc(me);
-    }
-    __syncthreads();
-    uint32_t a = above + __popc(mg & below), e = equal + __popc(me & below);
-    for (int k = 0; k < kSelThreads / 32; ++k) {
-      if (k < warp) {
-        a += sums[0][k];
-        e += sums[1][k];
-      }
-      above += sums[0][k];
-      equal += sums[1][k];
-    }
-    const uint32_t at = a + min(e, need);
-    if (i < p.n_rows) {
-      if (gt || (eq && e < need)) kept[at] = i;
-      if (i % kScaleBlock == 0) before[i / kScaleBlock] = at;
-    }
-    __syncthreads();
+  };
+  uint32_t a = 0, e = 0;
+  for (int grp = g0; grp < g1; ++grp) {
+    bool gt, eq;
+    look(grp, gt, eq);
+    a += __popc(__ballot_sync(0xffffffffu, gt));
+    e += __popc(__ballot_sync(0xffffffffu, eq));
   }
-  for (int b = (p.n_rows - 1) / kScaleBlock + 1 + tid; b <= p.blocks; b += kSelThreads) before[b] = p.n_keep;
-  pdl_launch_dependents();
+  if (lane == 0) {
+    sm.warp[warp][0] = a;
+    sm.warp[warp][1] = e;
+  }
+  __syncthreads();
+  uint32_t above = 0, equal = 0;  // among the rows before the warp's
+  for (int k = 0; k < kSelWarps; ++k) {
+    above += k < warp ? sm.warp[k][0] : 0u;
+    equal += k < warp ? sm.warp[k][1] : 0u;
+  }
+  if (cs > 1) {
+    if (warp == kSelWarps - 1 && lane == 0) {
+      sm.total[0] = above + a;
+      sm.total[1] = equal + e;
+    }
+    cluster_sync();
+    for (int r = 0; r < rank; ++r) {
+      const float2 t = ld_shared_cluster_v2(mapa_shared(smem_u32(sm.total), r));
+      above += __float_as_uint(t.x);
+      equal += __float_as_uint(t.y);
+    }
+    cluster_sync_exit();  // no CTA leaves while another reads its shared memory
+  }
+  const uint32_t below = (1u << lane) - 1u;
+  for (int grp = g0; grp < g1; ++grp) {
+    bool gt, eq;
+    look(grp, gt, eq);
+    const uint32_t mg = __ballot_sync(0xffffffffu, gt), me = __ballot_sync(0xffffffffu, eq);
+    const uint32_t e1 = equal + __popc(me & below), at = above + __popc(mg & below) + min(e1, need);
+    const int i = s0 + 32 * grp + lane;
+    if (gt || (eq && e1 < need)) kept[at] = i;
+    if (i < s1 && i % kScaleBlock == 0) before[i / kScaleBlock] = at;
+    above += __popc(mg);
+    equal += __popc(me);
+  }
+  if (rank == cs - 1)
+    for (int b = (p.n_rows - 1) / kScaleBlock + 1 + tid; b <= p.blocks; b += kSelThreads) before[b] = p.n_keep;
 }
 
 __global__ void __launch_bounds__(ev::kMoveThreads) fp8_evict_move_kernel(const __grid_constant__ F8EvictParams p) {
@@ -183,10 +260,27 @@ __global__ void __launch_bounds__(ev::kMoveThreads) fp8_evict_move_kernel(const 
   }
 }
 
-cudaError_t launch_fp8_evict(const F8EvictParams& p, int sm_count, cudaLaunchConfig_t cfg) {
-  cfg.gridDim = dim3(p.n_layers * kHkv);
-  cfg.blockDim = dim3(ev::kSelThreads);
-  cudaError_t e = cudaLaunchKernelEx(&cfg, fp8_evict_select_kernel, p);
+cudaError_t fp8_evict_set_attributes() {
+  return cudaFuncSetAttribute(fp8_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(sizeof(ev::Sel) + ev::kCached * sizeof(uint32_t)));
+}
+
+cudaError_t launch_fp8_evict(F8EvictParams& p, int sm_count, cudaLaunchConfig_t cfg) {
+  // slices of whole 128-row blocks
+  p.cluster = (p.n_rows + ev::kSlice - 1) / ev::kSlice;
+  if (p.cluster > ev::kMaxCluster) p.cluster = ev::kMaxCluster;
+  p.slice = ((p.n_rows + p.cluster - 1) / p.cluster + kScaleBlock - 1) / kScaleBlock * kScaleBlock;
+  cudaLaunchConfig_t sel = cfg;
+  cudaLaunchAttribute attr[2];
+  attr[0] = cfg.attrs[0];
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {static_cast<unsigned>(p.cluster), 1, 1};
+  sel.attrs = attr;
+  sel.numAttrs = p.cluster > 1 ? 2 : 1;
+  sel.gridDim = dim3(p.n_layers * kHkv * p.cluster);
+  sel.blockDim = dim3(ev::kSelThreads);
+  sel.dynamicSmemBytes = sizeof(ev::Sel) + (p.slice <= ev::kCached ? p.slice * sizeof(uint32_t) : 0);
+  cudaError_t e = cudaLaunchKernelEx(&sel, fp8_evict_select_kernel, p);
   if (e != cudaSuccess) return e;
   const int work = ((p.n_keep - 1) / kScaleBlock + 1) * 2 * kHkv * p.n_layers, most = 6 * sm_count;
   cfg.gridDim = dim3(work < most ? work : most);

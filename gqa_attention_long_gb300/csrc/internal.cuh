@@ -434,6 +434,7 @@ struct F8EvictParams {
   uint32_t* loaded;  // [unit][K, V][blocks]: whether a destination block's rows have been read
   int n_rows, n_keep, n_first, n_recent, Smax, n_layers;
   int blocks;        // Smax / 128
+  int cluster, slice;  // the selector's CTAs to a head, and their rows
 };
 struct F8EvictWs {
   size_t ticket_off, before_off, loaded_off, total;
