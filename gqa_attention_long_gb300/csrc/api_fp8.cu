@@ -197,8 +197,8 @@ int validate_evict(const ea_evict_fp8_args* a, int n_layers, int n_rows, int n_k
                scales = static_cast<size_t>(kHkv) * (Smax / kScaleBlock + 1) * sizeof(float);
   for (int l = 0; l < n_layers; ++l) {
     const ea_evict_fp8_args& x = a[l];
-    const int rc = check_pointers<4, 7>({x.k_cache, x.v_cache, x.k_dst, x.v_dst},
-                                        {x.k_scale, x.v_scale, x.k_scale_dst, x.v_scale_dst, x.weight, x.weight_dst, x.kept});
+    const int rc = check_pointers<6, 5>({x.k_cache, x.v_cache, x.k_dst, x.v_dst, x.weight, x.weight_dst},
+                                        {x.k_scale, x.v_scale, x.k_scale_dst, x.v_scale_dst, x.kept});
     if (rc != EA_OK) return rc;
     const int same = (x.k_cache == x.k_dst) + (x.v_cache == x.v_dst) + (x.k_scale == x.k_scale_dst) + (x.v_scale == x.v_scale_dst) +
                      (x.weight == x.weight_dst);
@@ -294,8 +294,10 @@ int expert_attn_evict_fp8(const ea_evict_fp8_args* layers, int n_layers, int n_r
   cudaLaunchAttribute attr[1];
   for (int l0 = 0; l0 < n_layers; l0 += kMaxLayersPerLaunch) {
     p.n_layers = n_layers - l0 < kMaxLayersPerLaunch ? n_layers - l0 : kMaxLayersPerLaunch;
+    p.ordered = 0;
     for (int l = 0; l < p.n_layers; ++l) {
       const ea_evict_fp8_args& x = layers[l0 + l];
+      p.ordered |= x.k_cache == x.k_dst;
       p.layer[l] = {static_cast<const uint8_t*>(x.k_cache), static_cast<const uint8_t*>(x.v_cache), x.k_scale, x.v_scale, x.weight,
                     static_cast<uint8_t*>(x.k_dst), static_cast<uint8_t*>(x.v_dst), x.k_scale_dst, x.v_scale_dst, x.weight_dst, x.kept};
     }

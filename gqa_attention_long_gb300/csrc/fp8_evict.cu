@@ -7,7 +7,7 @@
 //
 // Two kernels. The selector takes a head's weights with one CTA, or, from kSlice rows on, a cluster of up to eight that share them: it
 // finds the bits of the last weight that stays, eleven at a time from the top (a histogram of what shares the bits found so far, summed over the
-// cluster's shared memory), then numbers the rows that stay. The mover takes one destination block of K or of V of one head at a time:
+// cluster's shared memory), then numbers the rows that stay. The mover takes one destination block of a head at a time, of K and V:
 // 128 rows are read, all of them, before one is written. In place, a block may be written once the rows that were in it have been read: those
 // that stay go to at most two destination blocks, which the selector's counts name, with lower numbers or the same; work is
 // handed out in order, so whoever waits waits for work that is already under way. (Bytes: the weights, and a kept row's 256 twice.)
@@ -22,6 +22,7 @@ constexpr int kBins = 2048;
 constexpr int kSlice = 8192;        // rows of one CTA of a cluster, while eight suffice
 constexpr int kCached = 32768;      // rows of a slice whose bits are kept in shared memory (else they are read again)
 constexpr int kMaxCluster = 8;
+constexpr int kLoads = 2;           // loads of four weights that a thread has in flight
 constexpr int kMoveThreads = 256;
 constexpr int kPieces = kScaleBlock * kD / 16 / kMoveThreads;  // 16-byte pieces of a block that a thread moves
 
@@ -46,7 +47,7 @@ struct Sel {  // a CTA's shared memory; the slice's bits follow
 
 }  // namespace ev
 
-__global__ void __launch_bounds__(ev::kSelThreads) fp8_evict_select_kernel(const __grid_constant__ F8EvictParams p) {
+__global__ void __launch_bounds__(ev::kSelThreads, 4) fp8_evict_select_kernel(const __grid_constant__ F8EvictParams p) {
   using namespace ev;
   extern __shared__ uint8_t ev_smem[];
   Sel& sm = *reinterpret_cast<Sel*>(ev_smem);
@@ -65,7 +66,7 @@ __global__ void __launch_bounds__(ev::kSelThreads) fp8_evict_select_kernel(const
   pdl_wait_primary();
   pdl_launch_dependents();
   if (rank == 0) {
-    for (int i = tid; i < 2 * p.blocks; i += kSelThreads) p.loaded[static_cast<size_t>(u) * 2 * p.blocks + i] = 0u;
+    for (int i = tid; i < p.blocks; i += kSelThreads) p.loaded[static_cast<size_t>(u) * p.blocks + i] = 0u;
     if (u == 0 && tid == 0) *p.ticket = 0u;
   }
   // Of the least weight that stays: 11, then 11, then 10 bits. `need` rows stay among those that share the bits known so far.
@@ -73,16 +74,31 @@ __global__ void __launch_bounds__(ev::kSelThreads) fp8_evict_select_kernel(const
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, width = pass == 2 ? 10 : 11;
     uint32_t* hist = sm.hist[pass];
-    for (int i = s0 + tid; i < s1; i += kSelThreads) {
-      uint32_t k;
-      if (pass == 0 || !cached) {
-        k = i < lo || i >= hi ? 0u : key_of(w[i]);
-        if (cached) keys[i - s0] = k;
-      } else {
-        k = keys[i - s0];
+    // (a load of four weights may end behind the last row, but not behind its block of the array)
+    const bool load = pass == 0 || !cached;
+#pragma unroll 1
+    for (int i0 = s0 + 4 * tid; i0 < s1; i0 += 4 * kLoads * kSelThreads) {
+      uint4 k[kLoads];
+#pragma unroll
+      for (int q = 0; q < kLoads; ++q) {
+        const int i = i0 + 4 * kSelThreads * q;
+        if (i < s1) k[q] = load ? *reinterpret_cast<const uint4*>(w + i) : *reinterpret_cast<const uint4*>(keys + (i - s0));
       }
-      if (i >= lo && i < hi && (pass == 0 || (k >> (shift + width)) == (bits >> (shift + width))))
-        atomicAdd(&hist[(k >> shift) & ((1u << width) - 1u)], 1u);
+#pragma unroll
+      for (int q = 0; q < kLoads; ++q) {
+        const int i = i0 + 4 * kSelThreads * q;
+        if (i >= s1) break;
+        uint32_t v[4] = {k[q].x, k[q].y, k[q].z, k[q].w};
+        if (load) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = key_of(__uint_as_float(v[e]));
+          if (cached) *reinterpret_cast<uint4*>(keys + (i - s0)) = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (i + e >= lo && i + e < hi && (pass == 0 || (v[e] >> (shift + width)) == (bits >> (shift + width))))
+            atomicAdd(&hist[(v[e] >> shift) & ((1u << width) - 1u)], 1u);
+      }
     }
     if (cs > 1) cluster_sync();
     else __syncthreads();
@@ -90,9 +106,22 @@ __global__ void __launch_bounds__(ev::kSelThreads) fp8_evict_select_kernel(const
     const int b0 = kBins - 4 - 4 * tid;
     uint4 c = make_uint4(0u, 0u, 0u, 0u);
     const uint32_t at = smem_u32(hist + b0);
-    for (int r = 0; r < cs; ++r) {
-      const uint4 v = cs > 1 ? ld_cluster_v4(mapa_shared(at, r)) : *reinterpret_cast<const uint4*>(hist + b0);
-      c.x += v.x; c.y += v.y; c.z += v.z; c.w += v.w;
+    if (cs == 1) {
+      c = *reinterpret_cast<const uint4*>(hist + b0);
+    } else {
+#pragma unroll 1
+      for (int r = 0; r < cs; r += 4) {  // four CTAs' loads in flight
+        uint4 v[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = r + q < cs ? ld_cluster_v4(mapa_shared(at, r + q)) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          c.x += v[q].x;
+          c.y += v[q].y;
+          c.z += v[q].z;
+          c.w += v[q].w;
+        }
+      }
     }
     const uint32_t mine = (c.x + c.y) + (c.z + c.w);
     uint32_t sum = mine;
@@ -121,38 +150,40 @@ __global__ void __launch_bounds__(ev::kSelThreads) fp8_evict_select_kernel(const
     }
   }
   if (p.n_keep == p.n_first + p.n_recent) bits = 0xFFFFFFFFu;  // none is chosen: nothing lies above, and need is 0
-  // Rows above the threshold (or kept anyway) and at it, by warp: a warp has 32-row groups in a row
-  const int groups = (s1 - s0 + 31) / 32, per = (groups + kSelWarps - 1) / kSelWarps;
+  // Rows above the threshold (or kept anyway) and at it, by warp: a warp has 128-row blocks in a row, a lane four rows of each
+  const int groups = (s1 - s0 + kScaleBlock - 1) / kScaleBlock, per = (groups + kSelWarps - 1) / kSelWarps;
   const int g0 = min(warp * per, groups), g1 = min(g0 + per, groups);
-  auto look = [&](int grp, bool& gt, bool& eq) {
-    const int i = s0 + 32 * grp + lane;
-    gt = eq = false;
-    if (i < s1) {
-      if (i < lo || i >= hi) {
-        gt = true;
-      } else {
-        const uint32_t k = cached ? keys[i - s0] : key_of(w[i]);
-        gt = k > bits;
-        eq = k == bits;
-      }
+  // bit e: whether row s0 + 128 grp + 4 lane + e is above; bit 16 + e: at
+  auto look = [&](int grp) {
+    const int j = kScaleBlock * grp + 4 * lane, i = s0 + j;
+    uint4 k = *reinterpret_cast<const uint4*>(cached ? keys + j : reinterpret_cast<const uint32_t*>(w) + i);
+    uint32_t v[4] = {k.x, k.y, k.z, k.w}, m = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (!cached) v[e] = key_of(__uint_as_float(v[e]));
+      const bool chosen = i + e >= lo && i + e < hi;
+      if (i + e < s1) m |= (!chosen || v[e] > bits ? 1u : v[e] == bits ? 0x10000u : 0u) << e;
     }
+    return m;
   };
   uint32_t a = 0, e = 0;
   for (int grp = g0; grp < g1; ++grp) {
-    bool gt, eq;
-    look(grp, gt, eq);
-    a += __popc(__ballot_sync(0xffffffffu, gt));
-    e += __popc(__ballot_sync(0xffffffffu, eq));
+    const uint32_t m = look(grp);
+    a += __popc(m & 0xFFFFu);
+    e += __popc(m >> 16);
   }
+  a = __reduce_add_sync(0xffffffffu, a);
+  e = __reduce_add_sync(0xffffffffu, e);
   if (lane == 0) {
     sm.warp[warp][0] = a;
     sm.warp[warp][1] = e;
   }
   __syncthreads();
   uint32_t above = 0, equal = 0;  // among the rows before the warp's
-  for (int k = 0; k < kSelWarps; ++k) {
-    above += k < warp ? sm.warp[k][0] : 0u;
-    equal += k < warp ? sm.warp[k][1] : 0u;
+#pragma unroll 1
+  for (int k = 0; k < warp; ++k) {
+    above += sm.warp[k][0];
+    equal += sm.warp[k][1];
   }
   if (cs > 1) {
     if (warp == kSelWarps - 1 && lane == 0) {
@@ -167,75 +198,94 @@ __global__ void __launch_bounds__(ev::kSelThreads) fp8_evict_select_kernel(const
     }
     cluster_sync_exit();  // no CTA leaves while another reads its shared memory
   }
-  const uint32_t below = (1u << lane) - 1u;
   for (int grp = g0; grp < g1; ++grp) {
-    bool gt, eq;
-    look(grp, gt, eq);
-    const uint32_t mg = __ballot_sync(0xffffffffu, gt), me = __ballot_sync(0xffffffffu, eq);
-    const uint32_t e1 = equal + __popc(me & below), at = above + __popc(mg & below) + min(e1, need);
-    const int i = s0 + 32 * grp + lane;
-    if (gt || (eq && e1 < need)) kept[at] = i;
-    if (i < s1 && i % kScaleBlock == 0) before[i / kScaleBlock] = at;
-    above += __popc(mg);
-    equal += __popc(me);
+    const uint32_t m = look(grp), c = __popc(m & 0xFFFFu) | __popc(m >> 16) << 16;
+    uint32_t sum = c;  // of the lanes up to this one: rows above, and (from bit 16) at the threshold
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t v = __shfl_up_sync(0xffffffffu, sum, d);
+      if (lane >= d) sum += v;
+    }
+    uint32_t a1 = above + ((sum - c) & 0xFFFFu), e1 = equal + ((sum - c) >> 16);
+    const int i = s0 + kScaleBlock * grp + 4 * lane;
+    if (lane == 0) before[i / kScaleBlock] = a1 + min(e1, need);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const bool gt = (m >> e) & 1u, eq = (m >> (16 + e)) & 1u;
+      if (gt || (eq && e1 < need)) kept[a1 + min(e1, need)] = i + e;
+      a1 += gt;
+      e1 += eq;
+    }
+    sum = __shfl_sync(0xffffffffu, sum, 31);
+    above += sum & 0xFFFFu;
+    equal += sum >> 16;
   }
   if (rank == cs - 1)
     for (int b = (p.n_rows - 1) / kScaleBlock + 1 + tid; b <= p.blocks; b += kSelThreads) before[b] = p.n_keep;
 }
 
-__global__ void __launch_bounds__(ev::kMoveThreads) fp8_evict_move_kernel(const __grid_constant__ F8EvictParams p) {
+__global__ void __launch_bounds__(ev::kMoveThreads, 4) fp8_evict_move_kernel(const __grid_constant__ F8EvictParams p) {
   using namespace ev;
-  __shared__ float red[kMoveThreads / 32];
-  __shared__ float factor[kScaleBlock];
-  __shared__ int rows[kScaleBlock];
+  __shared__ float red[2][kMoveThreads / 32];
+  __shared__ float factor[2][kScaleBlock];
   __shared__ uint32_t next;
   __shared__ volatile uint32_t abort_flag;
   const int tid = threadIdx.x;
-  const uint32_t chunks = (p.n_keep - 1) / kScaleBlock + 1, items = 2 * kHkv * p.n_layers;
+  const uint32_t chunks = (p.n_keep - 1) / kScaleBlock + 1, units = kHkv * p.n_layers;
   if (tid == 0) abort_flag = 0u;
   pdl_wait_primary();
   pdl_launch_dependents();
-  for (;;) {
-    __syncthreads();
-    if (tid == 0) next = atomicAdd(p.ticket, 1u);
-    __syncthreads();
-    const uint32_t t = next;
-    if (t >= chunks * items) return;
-    const int c = t / items, item = t % items, kv = item & 1, u = item >> 1, g = u % kHkv;
+  for (uint32_t t = blockIdx.x;; t += gridDim.x) {
+    if (p.ordered) {  // some layer's rows move within its cache
+      __syncthreads();
+      if (tid == 0) next = atomicAdd(p.ticket, 1u);
+      __syncthreads();
+      t = next;
+    }
+    if (t >= chunks * units) return;
+    const int c = t / units, u = t % units, g = u % kHkv;
     const F8EvictLayer& L = p.layer[u / kHkv];
-    const uint8_t* src = (kv ? L.vc : L.kc) + static_cast<size_t>(g) * p.Smax * kD;
-    uint8_t* dst = (kv ? L.vd : L.kd) + static_cast<size_t>(g) * p.Smax * kD;
-    const float* ss = (kv ? L.vs : L.ks) + g * (p.blocks + 1);
-    float* sd = (kv ? L.vsd : L.ksd) + g * (p.blocks + 1);
-    uint32_t* loaded = p.loaded + static_cast<size_t>(item) * p.blocks;
-    const bool in_place = src == dst;
+    const size_t head = static_cast<size_t>(g) * p.Smax * kD;
+    const int* kept = L.kept + static_cast<size_t>(g) * p.n_keep + c * kScaleBlock;
     const int n = min(kScaleBlock, p.n_keep - c * kScaleBlock);
-    // the rows and their scales
-    float s = 0.f, wgt = 0.f;
-    if (tid < n) {
-      const int r = L.kept[static_cast<size_t>(g) * p.n_keep + c * kScaleBlock + tid];
-      rows[tid] = r;
-      s = ss[r / kScaleBlock];
-      if (kv == 0) wgt = L.w[static_cast<size_t>(g) * p.Smax + r];
-    }
-    float top = s;
+    // a thread's pieces of rows tid / 8 + 32 i, of K and of V, and one row's scales and weight
+    int r[kPieces], mine = 0;
 #pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-    if ((tid & 31) == 0) red[tid >> 5] = top;
+    for (int i = 0; i < kPieces; ++i)
+      if (tid / 8 + 32 * i < n) r[i] = kept[tid / 8 + 32 * i];
+    if (tid < n) mine = kept[tid];
+    uint4 x[2][kPieces];
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i)
+        if (tid / 8 + 32 * i < n)
+          x[kv][i] = *reinterpret_cast<const uint4*>((kv ? L.vc : L.kc) + head + static_cast<size_t>(r[i]) * kD + 16 * (tid & 7));
+    float s[2] = {0.f, 0.f}, top[2], wgt = 0.f;
+    if (tid < n) {
+      const int b = g * (p.blocks + 1) + mine / kScaleBlock;
+      s[0] = L.ks[b];
+      s[1] = L.vs[b];
+      wgt = L.w[static_cast<size_t>(g) * p.Smax + mine];
+    }
+    __syncthreads();  // (the block before is done with red and factor)
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      top[kv] = s[kv];
+#pragma unroll
+      for (int m = 16; m >= 1; m >>= 1) top[kv] = fmaxf(top[kv], __shfl_xor_sync(0xffffffffu, top[kv], m));
+      if ((tid & 31) == 0) red[kv][tid >> 5] = top[kv];
+    }
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < kScaleBlock / 32; ++k) top = fmaxf(top, red[k]);
-    if (tid < n) factor[tid] = s == top ? 1.0f : __fdiv_rn(s, top);
-    uint4 x[kPieces];
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int q = tid + kMoveThreads * i;
-      if ((q >> 3) < n) x[i] = *reinterpret_cast<const uint4*>(src + static_cast<size_t>(rows[q >> 3]) * kD + 16 * (q & 7));
+    for (int kv = 0; kv < 2; ++kv) {
+      top[kv] = fmaxf(fmaxf(red[kv][0], red[kv][1]), fmaxf(red[kv][2], red[kv][3]));  // (n <= 128: four warps have rows)
+      if (tid < n) factor[kv][tid] = s[kv] == top[kv] ? 1.0f : __fdiv_rn(s[kv], top[kv]);
     }
-    if (in_place) {
-      asm volatile("" ::: "memory");
+    if (L.kc == L.kd) {
       __syncthreads();  // every thread's loads have returned what they read before any of the block's rows is written
       if (tid == 0) {
+        uint32_t* loaded = p.loaded + static_cast<size_t>(u) * p.blocks;
         st_release_gpu(loaded + c, 1u);
         // the destination blocks that read this block's rows
         const uint32_t* before = p.before + static_cast<size_t>(u) * (p.blocks + 1);
@@ -248,15 +298,21 @@ __global__ void __launch_bounds__(ev::kMoveThreads) fp8_evict_move_kernel(const 
     __syncthreads();
     if (abort_flag) return;
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int q = tid + kMoveThreads * i;
-      if ((q >> 3) < n) {
-        const float f = factor[q >> 3];
-        *reinterpret_cast<uint4*>(dst + (static_cast<size_t>(c) * kScaleBlock + (q >> 3)) * kD + 16 * (q & 7)) = f == 1.0f ? x[i] : f8_rescale16(x[i], f);
+    for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        const int row = tid / 8 + 32 * i;
+        if (row < n) {
+          const float f = factor[kv][row];
+          *reinterpret_cast<uint4*>((kv ? L.vd : L.kd) + head + (static_cast<size_t>(c) * kScaleBlock + row) * kD + 16 * (tid & 7)) =
+              f == 1.0f ? x[kv][i] : f8_rescale16(x[kv][i], f);
+        }
       }
+    if (tid < n) L.wd[static_cast<size_t>(g) * p.Smax + c * kScaleBlock + tid] = wgt;
+    if (tid == 0) {
+      L.ksd[g * (p.blocks + 1) + c] = top[0];
+      L.vsd[g * (p.blocks + 1) + c] = top[1];
     }
-    if (tid < n && kv == 0) L.wd[static_cast<size_t>(g) * p.Smax + c * kScaleBlock + tid] = wgt;
-    if (tid == 0) sd[c] = top;
   }
 }
 
@@ -282,7 +338,7 @@ cudaError_t launch_fp8_evict(F8EvictParams& p, int sm_count, cudaLaunchConfig_t 
   sel.dynamicSmemBytes = sizeof(ev::Sel) + (p.slice <= ev::kCached ? p.slice * sizeof(uint32_t) : 0);
   cudaError_t e = cudaLaunchKernelEx(&sel, fp8_evict_select_kernel, p);
   if (e != cudaSuccess) return e;
-  const int work = ((p.n_keep - 1) / kScaleBlock + 1) * 2 * kHkv * p.n_layers, most = 6 * sm_count;
+  const int work = ((p.n_keep - 1) / kScaleBlock + 1) * kHkv * p.n_layers, most = 4 * sm_count;
   cfg.gridDim = dim3(work < most ? work : most);
   cfg.blockDim = dim3(ev::kMoveThreads);
   return cudaLaunchKernelEx(&cfg, fp8_evict_move_kernel, p);

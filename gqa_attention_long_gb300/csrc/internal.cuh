@@ -431,10 +431,11 @@ struct F8EvictParams {
   uint32_t* status;
   uint32_t* ticket;  // the mover's next piece of work
   uint32_t* before;  // [unit][blocks + 1]: kept rows before each source block
-  uint32_t* loaded;  // [unit][K, V][blocks]: whether a destination block's rows have been read
+  uint32_t* loaded;  // [unit][blocks]: whether a destination block's rows have been read
   int n_rows, n_keep, n_first, n_recent, Smax, n_layers;
   int blocks;        // Smax / 128
   int cluster, slice;  // the selector's CTAs to a head, and their rows
+  int ordered;       // rows move within their cache: the mover takes its work in order
 };
 struct F8EvictWs {
   size_t ticket_off, before_off, loaded_off, total;
@@ -446,7 +447,7 @@ constexpr F8EvictWs f8_evict_ws(int n_layers, int Smax) {
   w.ticket_off = 512;
   w.before_off = 1024;
   w.loaded_off = w.before_off + units * (blocks + 1) * sizeof(uint32_t);
-  w.total = (w.loaded_off + units * 2 * blocks * sizeof(uint32_t) + 1023) & ~static_cast<size_t>(1023);
+  w.total = (w.loaded_off + units * blocks * sizeof(uint32_t) + 1023) & ~static_cast<size_t>(1023);
   return w;
 }
 

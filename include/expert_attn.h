@@ -481,7 +481,7 @@ typedef struct {
   const void* v_cache;
   const float* k_scale;
   const float* v_scale;
-  const float* weight;    /* fp32 [8][Smax] */
+  const float* weight;    /* fp32 [8][Smax], 16-byte aligned, as weight_dst */
   void* k_dst;
   void* v_dst;
   float* k_scale_dst;
