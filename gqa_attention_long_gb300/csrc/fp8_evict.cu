@@ -17,11 +17,13 @@
 namespace ea {
 namespace ev {
 
-constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
+constexpr int kSelWarps = 32;       // at most
 constexpr int kBins = 2048;
-constexpr int kSlice = 8192;        // rows of one CTA of a cluster, while eight suffice
+constexpr int kSlice = 8192;        // rows of one CTA of a cluster, while so many suffice
 constexpr int kCached = 32768;      // rows of a slice whose bits are kept in shared memory (else they are read again)
-constexpr int kMaxCluster = 8;
+// A cluster's CTAs, at most, while their slices stay in shared memory: twice as many read as much of one another's histograms, and wait
+// longer for as many free SMs beside one another (2 layers of 131001 rows: 75 us in fours, 91 in eights).
+constexpr int kCluster = 4;
 constexpr int kLoads = 2;           // loads of four weights that a thread has in flight
 constexpr int kMoveThreads = 256;
 constexpr int kPieces = kScaleBlock * kD / 16 / kMoveThreads;  // 16-byte pieces of a block that a thread moves
@@ -47,9 +49,13 @@ struct Sel {  // a CTA's shared memory; the slice's bits follow
 
 }  // namespace ev
 
-__global__ void __launch_bounds__(ev::kSelThreads, 4) fp8_evict_select_kernel(const __grid_constant__ F8EvictParams p) {
+// 512 threads, or 1024 for the slices of a cluster, which are longer (2 layers of 131001 rows: 77 and 75 us; one CTA's heads want more
+// CTAs to an SM).
+template <int kSelThreads>
+__global__ void __launch_bounds__(kSelThreads, 2048 / kSelThreads) fp8_evict_select_kernel(const __grid_constant__ F8EvictParams p) {
   using namespace ev;
-  extern __shared__ uint8_t ev_smem[];
+  constexpr int kSelWarps = kSelThreads / 32;
+  extern __shared__ __align__(16) uint8_t ev_smem[];
   Sel& sm = *reinterpret_cast<Sel*>(ev_smem);
   uint32_t* keys = reinterpret_cast<uint32_t*>(ev_smem + sizeof(Sel));
   const int cs = p.cluster, u = blockIdx.x / cs, rank = blockIdx.x % cs, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -106,14 +112,18 @@ __global__ void __launch_bounds__(ev::kSelThreads, 4) fp8_evict_select_kernel(co
     const int b0 = kBins - 4 - 4 * tid;
     uint4 c = make_uint4(0u, 0u, 0u, 0u);
     const uint32_t at = smem_u32(hist + b0);
-    if (cs == 1) {
+    if (tid >= kBins / 4) {
+    } else if (cs == 1) {
       c = *reinterpret_cast<const uint4*>(hist + b0);
     } else {
 #pragma unroll 1
-      for (int r = 0; r < cs; r += 4) {  // four CTAs' loads in flight
+      for (int r = 0; r < cs; r += 4) {  // four CTAs' loads in flight, the next CTA's first: not all of one CTA at a time
         uint4 v[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = r + q < cs ? ld_cluster_v4(mapa_shared(at, r + q)) : make_uint4(0u, 0u, 0u, 0u);
+        for (int q = 0; q < 4; ++q) {
+          const int from = rank + r + q;
+          v[q] = r + q < cs ? ld_cluster_v4(mapa_shared(at, from < cs ? from : from - cs)) : make_uint4(0u, 0u, 0u, 0u);
+        }
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           c.x += v[q].x;
@@ -317,14 +327,15 @@ __global__ void __launch_bounds__(ev::kMoveThreads, 4) fp8_evict_move_kernel(con
 }
 
 cudaError_t fp8_evict_set_attributes() {
-  return cudaFuncSetAttribute(fp8_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>(sizeof(ev::Sel) + ev::kCached * sizeof(uint32_t)));
+  const int most = static_cast<int>(sizeof(ev::Sel) + ev::kCached * sizeof(uint32_t));
+  const cudaError_t e = cudaFuncSetAttribute(fp8_evict_select_kernel<512>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  return e != cudaSuccess ? e : cudaFuncSetAttribute(fp8_evict_select_kernel<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
 }
 
 cudaError_t launch_fp8_evict(F8EvictParams& p, int sm_count, cudaLaunchConfig_t cfg) {
   // slices of whole 128-row blocks
   p.cluster = (p.n_rows + ev::kSlice - 1) / ev::kSlice;
-  if (p.cluster > ev::kMaxCluster) p.cluster = ev::kMaxCluster;
+  if (p.cluster > ev::kCluster) p.cluster = p.n_rows <= ev::kCluster * ev::kCached ? ev::kCluster : 2 * ev::kCluster;
   p.slice = ((p.n_rows + p.cluster - 1) / p.cluster + kScaleBlock - 1) / kScaleBlock * kScaleBlock;
   cudaLaunchConfig_t sel = cfg;
   cudaLaunchAttribute attr[2];
@@ -334,9 +345,9 @@ cudaError_t launch_fp8_evict(F8EvictParams& p, int sm_count, cudaLaunchConfig_t 
   sel.attrs = attr;
   sel.numAttrs = p.cluster > 1 ? 2 : 1;
   sel.gridDim = dim3(p.n_layers * kHkv * p.cluster);
-  sel.blockDim = dim3(ev::kSelThreads);
+  sel.blockDim = dim3(p.cluster > 1 ? 1024 : 512);
   sel.dynamicSmemBytes = sizeof(ev::Sel) + (p.slice <= ev::kCached ? p.slice * sizeof(uint32_t) : 0);
-  cudaError_t e = cudaLaunchKernelEx(&sel, fp8_evict_select_kernel, p);
+  const cudaError_t e = cudaLaunchKernelEx(&sel, p.cluster > 1 ? fp8_evict_select_kernel<1024> : fp8_evict_select_kernel<512>, p);
   if (e != cudaSuccess) return e;
   const int work = ((p.n_keep - 1) / kScaleBlock + 1) * kHkv * p.n_layers, most = 4 * sm_count;
   cfg.gridDim = dim3(work < most ? work : most);
