@@ -743,22 +743,36 @@ __global__ void __launch_bounds__(f8d::kThreads, 1) fp8_decode_kernel(const __gr
   if (warp == 0) tmem_dealloc(tmem, kTmemCols);
 }
 
-// Weights from the scores: thread = key of one unit. grid (key blocks, units)
+// Weights from the scores: a thread has kWKeys keys of one unit under way. grid (key blocks, units)
+constexpr int kWThreads = 128, kWKeys = 4;
 template <int CAP>
-__global__ void __launch_bounds__(256) fp8_weights_kernel(const __grid_constant__ F8DecodeParams<CAP> p) {
-  const int u = blockIdx.y, key = blockIdx.x * 256 + threadIdx.x;
+__global__ void __launch_bounds__(kWThreads) fp8_weights_kernel(const __grid_constant__ F8DecodeParams<CAP> p) {
+  const int u = blockIdx.y, key0 = blockIdx.x * (kWThreads * kWKeys) + threadIdx.x;
   const F8AttnLayer& L = p.layer[u / kHkv];
+  const size_t at = static_cast<size_t>(u % kHkv) * p.Smax + key0;
+  const float4* x = reinterpret_cast<const float4*>(p.scores) + (static_cast<size_t>(u) * p.T * kKeyTile + key0) * 2;
   pdl_wait_primary();
   pdl_launch_dependents();
-  if (L.w_out == nullptr || key > p.pos) return;
-  const float4* x = reinterpret_cast<const float4*>(p.scores) + (static_cast<size_t>(u) * p.T * kKeyTile + key) * 2;
+  if (L.w_out == nullptr) return;
+  float4 a[kWKeys], b[kWKeys];
+  float w[kWKeys];
+#pragma unroll
+  for (int i = 0; i < kWKeys; ++i) {
+    const int key = key0 + i * kWThreads;
+    if (key <= p.pos) {
+      a[i] = __ldcs(x + 2 * i * kWThreads);
+      b[i] = __ldcs(x + 2 * i * kWThreads + 1);
+    }
+    w[i] = key < p.pos && L.w_in != nullptr ? L.w_in[at + i * kWThreads] : 0.f;
+  }
   const float4* lse = reinterpret_cast<const float4*>(p.lse + u * kRepText);
-  const float4 a = __ldcs(x), b = __ldcs(x + 1), c = lse[0], d = lse[1];
-  const size_t at = static_cast<size_t>(u % kHkv) * p.Smax + key;
-  const float w = key < p.pos && L.w_in != nullptr ? L.w_in[at] : 0.f;
-  const float sum = ((ex2_approx(a.x - c.x) + ex2_approx(a.y - c.y)) + (ex2_approx(a.z - c.z) + ex2_approx(a.w - c.w))) +
-                    ((ex2_approx(b.x - d.x) + ex2_approx(b.y - d.y)) + (ex2_approx(b.z - d.z) + ex2_approx(b.w - d.w)));
-  L.w_out[at] = w + sum;
+  const float4 c = lse[0], d = lse[1];
+#pragma unroll
+  for (int i = 0; i < kWKeys; ++i)
+    if (key0 + i * kWThreads <= p.pos)
+      L.w_out[at + i * kWThreads] =
+          w[i] + (((ex2_approx(a[i].x - c.x) + ex2_approx(a[i].y - c.y)) + (ex2_approx(a[i].z - c.z) + ex2_approx(a[i].w - c.w))) +
+                  ((ex2_approx(b[i].x - d.x) + ex2_approx(b[i].y - d.y)) + (ex2_approx(b[i].z - d.z) + ex2_approx(b[i].w - d.w))));
 }
 
 cudaError_t fp8_decode_set_attributes() {
@@ -777,8 +791,8 @@ cudaError_t launch_fp8_decode(const F8DecodeParams<CAP>& p, cudaLaunchConfig_t c
   cfg.dynamicSmemBytes = f8d::kSmemBytes;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, fp8_decode_kernel<CAP>, p);
   if (e != cudaSuccess || p.scores == nullptr) return e;
-  cfg.gridDim = dim3(p.pos / 256 + 1, p.n_layers * kHkv);
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3(p.pos / (kWThreads * kWKeys) + 1, p.n_layers * kHkv);
+  cfg.blockDim = dim3(kWThreads);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, fp8_weights_kernel<CAP>, p);
 }
