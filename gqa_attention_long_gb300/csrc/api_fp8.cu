@@ -13,6 +13,9 @@ cudaError_t launch_fp8_rows(const F8RowsParams& p, int n_layers, int dtype, bool
 cudaError_t fp8_decode_set_attributes();
 template <int CAP>
 cudaError_t launch_fp8_decode(const F8DecodeParams<CAP>& p, cudaLaunchConfig_t cfg);
+cudaError_t fp8_decode_small_set_attributes();
+cudaError_t launch_fp8_decode_small(const F8SmallParams& p, cudaLaunchConfig_t cfg);
+cudaError_t launch_fp8_weights(const F8WeightsParams& p, cudaLaunchConfig_t cfg);
 cudaError_t fp8_evict_set_attributes();
 cudaError_t launch_fp8_evict(F8EvictParams& p, int sm_count, cudaLaunchConfig_t cfg);
 }  // namespace ea
@@ -90,7 +93,7 @@ int run_rows(const ea_fp8_rows* a, int n_layers, int row0, int n_rows, int Smax,
 bool decode_attrs_ready(int dev) {
   static OncePerDevice once;
   return once(dev, [] {
-    const bool ok = fp8_decode_set_attributes() == cudaSuccess;
+    const bool ok = fp8_decode_set_attributes() == cudaSuccess && fp8_decode_small_set_attributes() == cudaSuccess;
     cudaGetLastError();
     return ok;
   });
@@ -134,6 +137,13 @@ bool any_weights(const ea_decode_fp8_args* a, int n) {
   return false;
 }
 
+F8AttnLayer attn_layer(const ea_decode_fp8_args& x) {
+  auto bf = [](const void* q) { return static_cast<const __nv_bfloat16*>(q); };
+  return {bf(x.q_raw), bf(x.k_raw), bf(x.v_raw), bf(x.q_gamma), bf(x.k_gamma), static_cast<uint8_t*>(x.k_cache),
+          static_cast<uint8_t*>(x.v_cache), x.k_scale, x.v_scale, static_cast<__nv_bfloat16*>(x.out),
+          static_cast<__nv_bfloat16*>(x.k_new), static_cast<__nv_bfloat16*>(x.v_new), x.weight_in, x.weight_out};
+}
+
 // Parameter blocks are large (24 KB at full capacity): kept off the stack, one per capacity, with a mutex of its own.
 template <int CAP>
 struct DecodeBlock {
@@ -150,10 +160,7 @@ int launch_decode_t(const ea_decode_fp8_args* a, int n, int pos, int Smax, long 
   for (int l = 0; l < n; ++l) {
     const ea_decode_fp8_args& x = a[l];
     if (!cache_map(x.k_cache, 0, Smax, true, &p.kmap[l]) || !cache_map(x.v_cache, 0, Smax, true, &p.vmap[l])) return EA_ERR_CUDA;
-    auto bf = [](const void* q) { return static_cast<const __nv_bfloat16*>(q); };
-    p.layer[l] = {bf(x.q_raw), bf(x.k_raw), bf(x.v_raw), bf(x.q_gamma), bf(x.k_gamma), static_cast<uint8_t*>(x.k_cache),
-                  static_cast<uint8_t*>(x.v_cache), x.k_scale, x.v_scale, static_cast<__nv_bfloat16*>(x.out),
-                  static_cast<__nv_bfloat16*>(x.k_new), static_cast<__nv_bfloat16*>(x.v_new), x.weight_in, x.weight_out};
+    p.layer[l] = attn_layer(x);
   }
   for (int j = 0; j < kD / 2; ++j) p.rot[j] = MxRotations::split(MxRotations::get().at(p0, j));
   p.part_o = reinterpret_cast<float*>(ws + wl.part_o_off);
@@ -178,6 +185,61 @@ int launch_decode_t(const ea_decode_fp8_args* a, int n, int pos, int Smax, long 
     return EA_ERR_CUDA;
   }
   return EA_OK;
+}
+
+// Little work: see fp8_decode_small.cu.
+constexpr int kSmallTiles = 8, kOnePart = 4, kSmallParts = 32;
+
+int launch_small(const ea_decode_fp8_args* a, int n, int pos, int Smax, long long p0, bool weights, uint8_t* ws, const F8DecodeWs& wl,
+                 int parts, cudaStream_t st) {
+  F8SmallParams p;
+  for (int l = 0; l < n; ++l) p.layer[l] = attn_layer(a[l]);
+  for (int j = 0; j < kD / 2; ++j) p.rot[j] = MxRotations::split(MxRotations::get().at(p0, j));
+  p.part_o = reinterpret_cast<float*>(ws + wl.part_o_off);
+  p.part_ml = reinterpret_cast<float*>(ws + wl.part_ml_off);
+  p.unit_cnt = reinterpret_cast<uint32_t*>(ws + wl.cnt_off);
+  p.scores = weights ? reinterpret_cast<float*>(ws + wl.scores_off) : nullptr;
+  p.lse = reinterpret_cast<float*>(ws + wl.lse_off);
+  p.T = pos / kKeyTile + 1;
+  p.parts = parts;
+  p.pos = pos;
+  p.Smax = Smax;
+  p.n_layers = n;
+  p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(kD)));
+  cudaLaunchAttribute attr[1];
+  if (launch_fp8_decode_small(p, launch_config(st, attr, true)) != cudaSuccess) {
+    cudaGetLastError();
+    return EA_ERR_CUDA;
+  }
+  return EA_OK;
+}
+
+int launch_weights(const ea_decode_fp8_args* a, int n, int pos, int Smax, uint8_t* ws, const F8DecodeWs& wl, cudaStream_t st) {
+  F8WeightsParams p;
+  for (int l = 0; l < n; ++l) p.layer[l] = attn_layer(a[l]);
+  p.scores = reinterpret_cast<float*>(ws + wl.scores_off);
+  p.lse = reinterpret_cast<float*>(ws + wl.lse_off);
+  p.T = pos / kKeyTile + 1;
+  p.pos = pos;
+  p.Smax = Smax;
+  p.n_layers = n;
+  cudaLaunchAttribute attr[1];
+  if (launch_fp8_weights(p, launch_config(st, attr, true)) != cudaSuccess) {
+    cudaGetLastError();
+    return EA_ERR_CUDA;
+  }
+  return EA_OK;
+}
+
+// The CTAs to a unit for a call of little work, 0 for another's: at most kSmallTiles key tiles to an SM. A unit of up to kOnePart tiles is one
+// CTA's.
+int small_parts(int n, int pos, int sm_count) {
+  const int T = pos / kKeyTile + 1, units = n * kHkv;
+  if (n > kSmallCap || static_cast<long long>(units) * T > static_cast<long long>(kSmallTiles) * sm_count) return 0;
+  int parts = sm_count / units;
+  if (parts > (T + 1) / 2) parts = (T + 1) / 2;  // (two tiles keep a CTA's eight warps busy)
+  if (parts > kSmallParts) parts = kSmallParts;
+  return parts < 1 || T <= kOnePart ? 1 : parts;
 }
 
 // Whether [a, a + n) and [b, b + n) share bytes without being the same.
@@ -254,8 +316,11 @@ int text_decode_attention_fp8(const ea_decode_fp8_args* layers, int n_layers, in
   for (int l0 = 0; l0 < n_layers; l0 += per) {
     const int n = n_layers - l0 < per ? n_layers - l0 : per;
     const bool weights = any_weights(layers + l0, n);
-    rc = n <= kSmallCap ? launch_decode_t<kSmallCap>(layers + l0, n, pos, Smax, p0, weights, ws, wl, di.sm_count, st)
-                        : launch_decode_t<kDecodeMaxLayers>(layers + l0, n, pos, Smax, p0, weights, ws, wl, di.sm_count, st);
+    const int parts = small_parts(n, pos, di.sm_count);
+    rc = parts > 0      ? launch_small(layers + l0, n, pos, Smax, p0, weights, ws, wl, parts, st)
+         : n <= kSmallCap ? launch_decode_t<kSmallCap>(layers + l0, n, pos, Smax, p0, weights, ws, wl, di.sm_count, st)
+                          : launch_decode_t<kDecodeMaxLayers>(layers + l0, n, pos, Smax, p0, weights, ws, wl, di.sm_count, st);
+    if (rc == EA_OK && weights) rc = launch_weights(layers + l0, n, pos, Smax, ws, wl, st);
     if (rc != EA_OK) return rc;
   }
   return EA_OK;

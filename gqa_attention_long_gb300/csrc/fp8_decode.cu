@@ -745,8 +745,7 @@ __global__ void __launch_bounds__(f8d::kThreads, 1) fp8_decode_kernel(const __gr
 
 // Weights from the scores: a thread has kWKeys keys of one unit under way. grid (key blocks, units)
 constexpr int kWThreads = 128, kWKeys = 4;
-template <int CAP>
-__global__ void __launch_bounds__(kWThreads) fp8_weights_kernel(const __grid_constant__ F8DecodeParams<CAP> p) {
+__global__ void __launch_bounds__(kWThreads) fp8_weights_kernel(const __grid_constant__ F8WeightsParams p) {
   const int u = blockIdx.y, key0 = blockIdx.x * (kWThreads * kWKeys) + threadIdx.x;
   const F8AttnLayer& L = p.layer[u / kHkv];
   const size_t at = static_cast<size_t>(u % kHkv) * p.Smax + key0;
@@ -789,14 +788,15 @@ cudaError_t launch_fp8_decode(const F8DecodeParams<CAP>& p, cudaLaunchConfig_t c
   if (p.n_layers * kHkv / static_cast<int>(cfg.gridDim.x) + 2 > f8d::kTails) return cudaErrorInvalidConfiguration;  // (a GPU of 7 SMs)
   cfg.blockDim = dim3(f8d::kThreads);
   cfg.dynamicSmemBytes = f8d::kSmemBytes;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, fp8_decode_kernel<CAP>, p);
-  if (e != cudaSuccess || p.scores == nullptr) return e;
-  cfg.gridDim = dim3(p.pos / (kWThreads * kWKeys) + 1, p.n_layers * kHkv);
-  cfg.blockDim = dim3(kWThreads);
-  cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, fp8_weights_kernel<CAP>, p);
+  return cudaLaunchKernelEx(&cfg, fp8_decode_kernel<CAP>, p);
 }
 template cudaError_t launch_fp8_decode<kSmallCap>(const F8DecodeParams<kSmallCap>&, cudaLaunchConfig_t);
 template cudaError_t launch_fp8_decode<kDecodeMaxLayers>(const F8DecodeParams<kDecodeMaxLayers>&, cudaLaunchConfig_t);
+
+cudaError_t launch_fp8_weights(const F8WeightsParams& p, cudaLaunchConfig_t cfg) {
+  cfg.gridDim = dim3(p.pos / (kWThreads * kWKeys) + 1, p.n_layers * kHkv);
+  cfg.blockDim = dim3(kWThreads);
+  return cudaLaunchKernelEx(&cfg, fp8_weights_kernel, p);
+}
 
 }  // namespace ea

@@ -388,6 +388,25 @@ struct F8DecodeParams {
   int pos, Smax, n_layers;
   float scale_log2;    // log2(e) / sqrt(128)
 };
+// The same step for little work (fp8_decode_small.cu), and the weights from either's scores (fp8_decode.cu).
+struct F8SmallParams {
+  F8AttnLayer layer[kSmallCap];
+  float4 rot[kD / 2];
+  float* part_o;       // [unit][part][8 heads][128]
+  float* part_ml;      // [unit][part][8 heads][2]
+  uint32_t* unit_cnt;
+  float* scores;
+  float* lse;
+  int T, parts;        // CTAs to a unit, each with its share of the unit's tiles
+  int pos, Smax, n_layers;
+  float scale_log2;
+};
+struct F8WeightsParams {
+  F8AttnLayer layer[kMaxLayersPerLaunch];
+  const float* scores;
+  const float* lse;
+  int T, pos, Smax, n_layers;
+};
 // Workspace: [0, 1024) status word; unit counters and log2-sum-exps of 64 layers, whatever the call's number; partials of at
 // most max_ctas CTAs; scores, for a call that asks for weights.
 struct F8DecodeWs {
