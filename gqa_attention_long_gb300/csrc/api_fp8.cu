@@ -14,7 +14,8 @@ cudaError_t fp8_decode_set_attributes();
 template <int CAP>
 cudaError_t launch_fp8_decode(const F8DecodeParams<CAP>& p, cudaLaunchConfig_t cfg);
 cudaError_t fp8_decode_small_set_attributes();
-cudaError_t launch_fp8_decode_small(const F8SmallParams& p, cudaLaunchConfig_t cfg);
+template <int CAP>
+cudaError_t launch_fp8_decode_small(const F8SmallParams<CAP>& p, cudaLaunchConfig_t cfg);
 cudaError_t launch_fp8_weights(const F8WeightsParams& p, cudaLaunchConfig_t cfg);
 cudaError_t fp8_evict_set_attributes();
 cudaError_t launch_fp8_evict(F8EvictParams& p, int sm_count, cudaLaunchConfig_t cfg);
@@ -187,12 +188,16 @@ int launch_decode_t(const ea_decode_fp8_args* a, int n, int pos, int Smax, long 
   return EA_OK;
 }
 
-// Little work: see fp8_decode_small.cu.
-constexpr int kSmallTiles = 8, kOnePart = 4, kSmallParts = 32;
+// Little work (see fp8_decode_small.cu): at most kSmallTiles key tiles to an SM. Its kernel and the other one: 1 layer at pos 300 7.0 and 10.2 us, at
+// pos 4700 9.1 and 13.4, 4 layers 17.5 and 18.8, 8 layers (15.6 tiles) 26.8 and 24.7; 32 layers at pos 1000 (13.5) 26.6 and 29.4, 64 layers at
+// pos 500 (13.5) 35.9 and 44.3. Up to kOnePart tiles a unit is one CTA's: 1 layer at pos 500 7.6 us whole and 8.0 in two parts, at pos 700 9.2 and
+// 7.2.
+constexpr int kSmallTiles = 14, kOnePart = 4, kSmallParts = 32;
 
+template <int CAP>
 int launch_small(const ea_decode_fp8_args* a, int n, int pos, int Smax, long long p0, bool weights, uint8_t* ws, const F8DecodeWs& wl,
                  int parts, cudaStream_t st) {
-  F8SmallParams p;
+  F8SmallParams<CAP> p;
   for (int l = 0; l < n; ++l) p.layer[l] = attn_layer(a[l]);
   for (int j = 0; j < kD / 2; ++j) p.rot[j] = MxRotations::split(MxRotations::get().at(p0, j));
   p.part_o = reinterpret_cast<float*>(ws + wl.part_o_off);
@@ -231,11 +236,11 @@ int launch_weights(const ea_decode_fp8_args* a, int n, int pos, int Smax, uint8_
   return EA_OK;
 }
 
-// The CTAs to a unit for a call of little work, 0 for another's: at most kSmallTiles key tiles to an SM. A unit of up to kOnePart tiles is one
+// The CTAs to a unit for a call of little work, 0 for another. A unit of up to kOnePart tiles is one
 // CTA's.
 int small_parts(int n, int pos, int sm_count) {
   const int T = pos / kKeyTile + 1, units = n * kHkv;
-  if (n > kSmallCap || static_cast<long long>(units) * T > static_cast<long long>(kSmallTiles) * sm_count) return 0;
+  if (static_cast<long long>(units) * T > static_cast<long long>(kSmallTiles) * sm_count) return 0;
   int parts = sm_count / units;
   if (parts > (T + 1) / 2) parts = (T + 1) / 2;  // (two tiles keep a CTA's eight warps busy)
   if (parts > kSmallParts) parts = kSmallParts;
@@ -317,7 +322,8 @@ int text_decode_attention_fp8(const ea_decode_fp8_args* layers, int n_layers, in
     const int n = n_layers - l0 < per ? n_layers - l0 : per;
     const bool weights = any_weights(layers + l0, n);
     const int parts = small_parts(n, pos, di.sm_count);
-    rc = parts > 0      ? launch_small(layers + l0, n, pos, Smax, p0, weights, ws, wl, parts, st)
+    rc = parts > 0 && n <= kSmallCap ? launch_small<kSmallCap>(layers + l0, n, pos, Smax, p0, weights, ws, wl, parts, st)
+         : parts > 0 ? launch_small<kDecodeMaxLayers>(layers + l0, n, pos, Smax, p0, weights, ws, wl, parts, st)
          : n <= kSmallCap ? launch_decode_t<kSmallCap>(layers + l0, n, pos, Smax, p0, weights, ws, wl, di.sm_count, st)
                           : launch_decode_t<kDecodeMaxLayers>(layers + l0, n, pos, Smax, p0, weights, ws, wl, di.sm_count, st);
     if (rc == EA_OK && weights) rc = launch_weights(layers + l0, n, pos, Smax, ws, wl, st);

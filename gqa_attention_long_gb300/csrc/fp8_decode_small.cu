@@ -54,7 +54,8 @@ __device__ __forceinline__ void split_f16(float a, float b, uint32_t& hi, uint32
 }
 
 // The new K (kv = 0) or V row: its codes, its block's scale, and how the block's earlier rows move; one warp.
-__device__ __forceinline__ void new_row(const F8SmallParams& p, Smem& sm, const F8AttnLayer& L, int g, int kv, int lane) {
+template <class P>
+__device__ __forceinline__ void new_row(const P& p, Smem& sm, const F8AttnLayer& L, int g, int kv, int lane) {
   const int blk = p.pos / kScaleBlock, before = p.pos % kScaleBlock;
   float* scale = (kv ? L.vs : L.ks) + g * (p.Smax / kScaleBlock + 1) + blk;
   const float old = before > 0 ? *scale : f8_pow2(kF8FirstExp);
@@ -91,7 +92,8 @@ __device__ __forceinline__ void new_row(const F8SmallParams& p, Smem& sm, const 
 }
 
 // q row h as f16 halves, times the power of two that puts its largest magnitude in [1, 2).
-__device__ __forceinline__ void query_row(const F8SmallParams& p, Smem& sm, const F8AttnLayer& L, int g, int h, int lane) {
+template <class P>
+__device__ __forceinline__ void query_row(const P& p, Smem& sm, const F8AttnLayer& L, int g, int h, int lane) {
   float x[4], gm[4], y[4];
   f8_load_row(L.q_gamma, lane, gm);
   f8_load_row(L.q_raw + (kRepText * g + h) * kD, lane, x);
@@ -148,7 +150,8 @@ __device__ __forceinline__ void last_codes(Codes& c, Smem& sm, uint8_t* kc, uint
 
 }  // namespace f8s
 
-__global__ void __launch_bounds__(f8s::kThreads, 1) fp8_decode_small_kernel(const __grid_constant__ F8SmallParams p) {
+template <int CAP>
+__global__ void __launch_bounds__(f8s::kThreads, 1) fp8_decode_small_kernel(const __grid_constant__ F8SmallParams<CAP> p) {
   using namespace f8s;
   extern __shared__ __align__(16) uint8_t f8s_smem[];
   Smem& sm = *reinterpret_cast<Smem*>(f8s_smem);
@@ -346,14 +349,19 @@ __global__ void __launch_bounds__(f8s::kThreads, 1) fp8_decode_small_kernel(cons
 }
 
 cudaError_t fp8_decode_small_set_attributes() {
-  return cudaFuncSetAttribute(fp8_decode_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(sizeof(f8s::Smem)));
+  const int bytes = static_cast<int>(sizeof(f8s::Smem));
+  const cudaError_t e = cudaFuncSetAttribute(fp8_decode_small_kernel<kSmallCap>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  return e != cudaSuccess ? e : cudaFuncSetAttribute(fp8_decode_small_kernel<kDecodeMaxLayers>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
-cudaError_t launch_fp8_decode_small(const F8SmallParams& p, cudaLaunchConfig_t cfg) {
+template <int CAP>
+cudaError_t launch_fp8_decode_small(const F8SmallParams<CAP>& p, cudaLaunchConfig_t cfg) {
   cfg.gridDim = dim3(p.n_layers * kHkv * p.parts);
   cfg.blockDim = dim3(f8s::kThreads);
   cfg.dynamicSmemBytes = sizeof(f8s::Smem);
-  return cudaLaunchKernelEx(&cfg, fp8_decode_small_kernel, p);
+  return cudaLaunchKernelEx(&cfg, fp8_decode_small_kernel<CAP>, p);
 }
+template cudaError_t launch_fp8_decode_small<kSmallCap>(const F8SmallParams<kSmallCap>&, cudaLaunchConfig_t);
+template cudaError_t launch_fp8_decode_small<kDecodeMaxLayers>(const F8SmallParams<kDecodeMaxLayers>&, cudaLaunchConfig_t);
 
 }  // namespace ea

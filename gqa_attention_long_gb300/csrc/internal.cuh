@@ -389,8 +389,9 @@ struct F8DecodeParams {
   float scale_log2;    // log2(e) / sqrt(128)
 };
 // The same step for little work (fp8_decode_small.cu), and the weights from either's scores (fp8_decode.cu).
+template <int CAP>
 struct F8SmallParams {
-  F8AttnLayer layer[kSmallCap];
+  F8AttnLayer layer[CAP];
   float4 rot[kD / 2];
   float* part_o;       // [unit][part][8 heads][128]
   float* part_ml;      // [unit][part][8 heads][2]

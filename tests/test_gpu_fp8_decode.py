@@ -77,11 +77,37 @@ def test_layers(layers, pos, Smax):
     step(decode_inputs(layers), random_cache(layers, Smax, pos), pos, 0, layers, sums(1, Smax), in_place=layers % 2 == 0)
 
 
-def test_weights_of_some_layers_only():
-    pos, Smax = 900, 1024
+@pytest.mark.parametrize("layers,pos,Smax", [(20, 4000, 4096), (40, 2303, 2304), (64, 1200, 1280), (33, 1024, 1152), (5, 20000, 20096)])
+def test_units_cut_anywhere(layers, pos, Smax):
+    """More than 14 key tiles to an SM: CTAs that work on several units, whole and in parts; layers that differ, new rows that need
+    larger scales; a second call meets the counters that the first left."""
+    hs = [random_cache(60 + l, Smax, pos, v_gain=4.0 ** -l) for l in range(3)]
+    xs = [decode_inputs(50 + l) for l in range(3)]
+    for l, x in enumerate(xs):
+        x["k_gamma"] = x["k_gamma"] * (1 + 2 * l)
+    base = [sums(l, Smax) for l in range(3)]
+    bufs = [decode_buffers(xs[l % 3], hs[l % 3].device(), base[l % 3].clone(), torch.full((8, Smax), -7.0, device=DEV)) for l in range(layers)]
+    ws = ea.alloc_decode_fp8_workspace(layers, Smax, weights=True)
+    want = [decode_oracle(xs[l], hs[l], pos, 0) for l in range(3)]
+    for _ in range(2):  # (the second call's rows are there already, and fit)
+        for b in bufs:
+            b.out.fill_(float("nan"))
+            b.weight_out.fill_(-7.0)
+        ea.text_decode_attention_fp8(bufs, pos, Smax, 0, ws)
+        check_status(ws)
+        for l, b in enumerate(bufs):
+            if l < 3 or l % 7 == 0 or l == layers - 1:
+                same_cache(b.cache, hs[l % 3], f"layer {l}")
+            close(b.out, want[l % 3]["out"], f"layer {l}")
+            weights_close(b.weight_out, base[l % 3], want[l % 3]["weight"], pos)
+            assert (b.weight_out[:, pos + 1:] == -7.0).all()
+
+
+@pytest.mark.parametrize("pos,Smax,layers", [(900, 1024, 5), (4000, 4096, 14)])
+def test_weights_of_some_layers_only(pos, Smax, layers):
     h, base = random_cache(3, Smax, pos), sums(2, Smax)
-    bufs = [decode_buffers(decode_inputs(4), h.device(), None, torch.full_like(base, -7.0) if l % 3 == 1 else None) for l in range(5)]
-    ws = ea.alloc_decode_fp8_workspace(5, Smax, weights=True)
+    bufs = [decode_buffers(decode_inputs(4), h.device(), None, torch.full_like(base, -7.0) if l % 3 == 1 else None) for l in range(layers)]
+    ws = ea.alloc_decode_fp8_workspace(layers, Smax, weights=True)
     ea.text_decode_attention_fp8(bufs, pos, Smax, 0, ws)
     check_status(ws)
     r = decode_oracle(decode_inputs(4), h, pos, 0)
@@ -276,7 +302,7 @@ def test_two_graphs_share_a_workspace():
 def test_two_streams_at_once():
     """Calls with a workspace and caches of their own, on streams of their own: what they give alone, to the bit."""
     runs = []
-    for n, pos, Smax in ((2, 3000, 3200), (9, 300, 384), (1, 4000, 4096)):
+    for n, pos, Smax in ((2, 3000, 3200), (20, 2000, 2048), (1, 4000, 4096)):
         bufs = [decode_buffers(decode_inputs(7 * l + n), random_cache(9 * l % 4 + n, Smax, pos).device(), None, torch.zeros(8, Smax, device=DEV)) for l in range(n)]
         ws = ea.alloc_decode_fp8_workspace(n, Smax, weights=True)
         for _ in range(2):
@@ -296,22 +322,22 @@ def test_two_streams_at_once():
 
 def test_one_workspace_for_calls_of_different_layer_counts():
     ws = ea.alloc_decode_fp8_workspace(64, 1152, weights=True)
-    hs = [random_cache(3 + l, 512, 400) for l in range(3)]
-    many = [decode_buffers(decode_inputs(l), hs[l % 3].device(), None, torch.zeros(8, 512, device=DEV)) for l in range(64)]
+    hs = [random_cache(3 + l, 1024, 900) for l in range(3)]
+    many = [decode_buffers(decode_inputs(l), hs[l % 3].device(), None, torch.zeros(8, 1024, device=DEV)) for l in range(64)]
     few = [decode_buffers(decode_inputs(100 + l), random_cache(8 + l, 1152, 1000).device()) for l in range(3)]
-    ea.text_decode_attention_fp8(many, 400, 512, 0, ws)  # (a first one: what a second appends is there already)
+    ea.text_decode_attention_fp8(many, 900, 1024, 0, ws)  # (a first one: what a second appends is there already)
     outs = []
     for _ in range(2):
         for b in many:
             b.out.fill_(float("nan"))
-        ea.text_decode_attention_fp8(many, 400, 512, 0, ws)
+        ea.text_decode_attention_fp8(many, 900, 1024, 0, ws)
         outs.append([(b.out.clone(), b.weight_out.clone()) for b in many])
         ea.text_decode_attention_fp8(few, 1000, 1152, 0, ws)
     check_status(ws)
     for (a, v), (b, w) in zip(*outs):
         assert torch.equal(a, b) and torch.equal(v, w)
     for l in (0, 40, 63):
-        close(outs[1][l][0], decode_oracle(decode_inputs(l), hs[l % 3].copy(), 400, 0)["out"], f"layer {l}")
+        close(outs[1][l][0], decode_oracle(decode_inputs(l), hs[l % 3].copy(), 900, 0)["out"], f"layer {l}")
 
 
 def test_workspace_too_small_is_refused():
