@@ -20,8 +20,8 @@
 // Warp roles (512 threads): warps 0-3 and 4-7 softmax, of heads 0-3 and 4-7 (thread = key = TMEM lane); warps 8-11 output
 // (thread = channel = TMEM lane): sums of O^T, a segment's end, the merge; warp 12 loads tiles by TMA, K's into a ring of 4, V's, which
 // are held longer, into one of 8; warps 13 and 14 issue the MMAs, one product each; warp 15 prepares what later segments need: their Q, and
-// the new K and V rows, which it appends (the first segment's Q comes from the softmax warps, its new rows from two output warps, which
-// have nothing else to do yet). S has four buffers, Q, P and O have two. Five loops run side by side on one scheduler's instruction cache, and fetching
+// the new K and V rows, which it appends (the first segment's Q comes from the softmax warps, its new rows and the second segment's Q from
+// output warps, which have nothing else to do yet). S has four buffers, Q, P and O have two. Five loops run side by side on one scheduler's instruction cache, and fetching
 // was what they waited for most (2.8 of 10 warp cycles an instruction): they are short, and what is rare is out of their way.
 // A unit cut over several CTAs is merged by the part that finishes last; a part that is not its CTA's last segment is counted by warp
 // 15, and merged at the CTA's end should it be the last after all, so that the output warps need not wait.
@@ -103,8 +103,15 @@ __device__ __forceinline__ uint32_t atom_add_acq_rel_gpu(uint32_t* a, uint32_t v
 __device__ __forceinline__ void st_shared_u8(uint32_t a, uint32_t v) {
   asm volatile("st.shared.u8 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
-// The waits of this file are a whole warp's and take little code: counted_wait, which gives up after a number of looks. Who gives up notes
-// it and leaves, and then so does, the same number of looks later, who waits for it.
+// The waits of this file are a whole warp's and take little code: one look here, and the further ones (counted_wait, which gives up after a
+// number of them) out of the loops' way: 64 layers at pos 4700 107 -> 100 us. Who gives up notes it and leaves, and then so does, the
+// same number of looks later, who waits for it.
+__device__ __noinline__ bool long_wait(uint32_t bar, uint32_t parity) { return counted_wait(bar, parity); }
+__device__ __forceinline__ bool short_wait(uint32_t bar, uint32_t parity) {
+  if (__builtin_expect(__all_sync(0xffffffffu, mbar_try_wait(bar, parity)), 1)) return true;
+  return long_wait(bar, parity);
+}
+
 // 16 consecutive TMEM columns of this warp's 32 lanes -> 16 registers per thread.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
@@ -233,12 +240,14 @@ __device__ __forceinline__ bool prepare(const F8DecodeParams<CAP>& p, uint32_t s
   Seg s;
   for (long long t = start; next_seg(t, end, p.T, s); ++seg) {
     if (seg > 0) {
-      const uint32_t buf = seg & 1;
-      if (seg > 1 && !counted_wait(bar0 + 8 * (B_QFREE + buf), ((seg - 2) >> 1) & 1)) return false;
+      if (seg > 1) {  // (output warps have the second one's Q)
+        const uint32_t buf = seg & 1;
+        if (!counted_wait(bar0 + 8 * (B_QFREE + buf), ((seg - 2) >> 1) & 1)) return false;
 #pragma unroll 1
-      for (int h = 0; h < kRepText; ++h) prepare_q(p, sbase, smem, s.u, h, seg);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar0 + 8 * (B_QFULL + buf));
+        for (int h = 0; h < kRepText; ++h) prepare_q(p, sbase, smem, s.u, h, seg);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar0 + 8 * (B_QFULL + buf));
+      }
       if (s.j1 == p.T) {
         append_row(p, sbase, smem, 0, s.u, idx);
         append_row(p, sbase, smem, 1, s.u, idx);
@@ -271,7 +280,7 @@ template <int CAP>
 __device__ __forceinline__ bool producer(const F8DecodeParams<CAP>& p, uint32_t sbase, long long start, long long end) {
   const uint64_t pol = l2_policy_evict_first();  // every cache tile is read once
   const uint32_t bar0 = sbase + SM_BAR;
-  auto wait = [&](int b, uint32_t parity) { return counted_wait(bar0 + 8 * b, parity); };
+  auto wait = [&](int b, uint32_t parity) { return short_wait(bar0 + 8 * b, parity); };
   uint32_t nk = 0, nv = 0, tails = 0;  // tiles of K and of V on their way
   bool ok = true;
   Seg s;
@@ -321,7 +330,7 @@ __device__ __forceinline__ bool qk_issuer(const F8DecodeParams<CAP>& p, uint32_t
   constexpr uint32_t kIdesc = umma_idesc_f16(128, kCols, false, false, false);  // (e4m3 is format code 0); A and B K-major
   const uint32_t bar0 = sbase + SM_BAR;
   const uint64_t kd = sw128_desc(sbase + SM_K, 16, 1024), qd = sw128_desc(sbase + SM_QT, 16, 1024);
-  auto wait = [&](int b, uint32_t parity) { return counted_wait(bar0 + 8 * b, parity); };
+  auto wait = [&](int b, uint32_t parity) { return short_wait(bar0 + 8 * b, parity); };
   uint32_t n = 0, seg = 0;
   bool ok = true;
   Seg s;
@@ -358,7 +367,7 @@ __device__ __forceinline__ bool pv_issuer(const F8DecodeParams<CAP>& p, uint32_t
   constexpr uint32_t kIdesc = umma_idesc_f16(128, kOutCols, false, true, false);  // A = V MN-major, B = P K-major
   const uint32_t bar0 = sbase + SM_BAR;
   const uint64_t vd = sw128_desc(sbase + SM_V, kTileBytes, 1024), pd = sw128_desc(sbase + SM_PT, 16, 1024);
-  auto wait = [&](int b, uint32_t parity) { return counted_wait(bar0 + 8 * b, parity); };
+  auto wait = [&](int b, uint32_t parity) { return short_wait(bar0 + 8 * b, parity); };
   uint32_t n = 0;
 #pragma unroll 1
   for (; n < total; ++n) {
@@ -415,7 +424,7 @@ __device__ __forceinline__ bool softmax(const F8DecodeParams<CAP>& p, uint32_t s
   uint32_t at[H];
 #pragma unroll
   for (int h = 0; h < H; ++h) at[h] = sbase + SM_PT + (4 * set + h) * 128 + (((tid >> 4) ^ (4 * set + h)) << 4) + (tid & 15);
-  auto wait = [&](int b, uint32_t parity) { return counted_wait(bar0 + 8 * b, parity); };
+  auto wait = [&](int b, uint32_t parity) { return short_wait(bar0 + 8 * b, parity); };
   uint32_t n = 0, seg = 0, tails = 0;  // this CTA's tiles, its segments, and appended rows
   Seg s;
   for (long long t = start; next_seg(t, end, p.T, s); ++seg) {
@@ -444,7 +453,7 @@ __device__ __forceinline__ bool softmax(const F8DecodeParams<CAP>& p, uint32_t s
       const bool live = j * kKeyTile + tid <= p.pos;
       float k_scale = k_next;
       if (j + 1 < last) k_next = ks[j + 1];
-      if (j == last) k_scale = last_tile(p, sbase, smem, n, tails, live, ok);
+      if (__builtin_expect(j == last, 0)) k_scale = last_tile(p, sbase, smem, n, tails, live, ok);
       tc_fence_after();
       uint32_t d[16];
       tmem_ld16(s_cols + (n & 3) * kCols, d);
@@ -463,8 +472,8 @@ __device__ __forceinline__ bool softmax(const F8DecodeParams<CAP>& p, uint32_t s
         mine = lane == h ? mx : mine;
       }
       if (lane < H) red[(n & 1) * 32 + warp * H + lane] = mine;
-      if (scores != nullptr && live) scores[static_cast<size_t>(j) * kKeyTile * 2] = make_float4(x[0], x[1], x[2], x[3]);
-      if (!bar_sync_and(id, kGroup, ok)) return false;
+      if (__builtin_expect(scores != nullptr, 0) && live) scores[static_cast<size_t>(j) * kKeyTile * 2] = make_float4(x[0], x[1], x[2], x[3]);
+      if (__builtin_expect(!bar_sync_and(id, kGroup, ok), 0)) return false;
       const float4* r4 = reinterpret_cast<const float4*>(red + (n & 1) * 32);
       const float4 ra = r4[0], rb = r4[1], rc = r4[2], rd = r4[3];
       const float m[H] = {fmaxf(fmaxf(ra.x, rb.x), fmaxf(rc.x, rd.x)), fmaxf(fmaxf(ra.y, rb.y), fmaxf(rc.y, rd.y)),
@@ -596,12 +605,23 @@ __device__ __noinline__ void merge(const F8DecodeParams<CAP>& p, uint8_t* smem, 
   if (tid == 0) p.unit_cnt[u] = 0u;  // every part has arrived: ready for the next call
 }
 
+// What the output warps do before there is any output: the first segment's new rows, and the second segment's Q (its unit is the next one).
+template <int CAP>
+__device__ __noinline__ void early(const F8DecodeParams<CAP>& p, uint32_t sbase, uint8_t* smem, int u, bool tail, bool more, int warp) {
+  if (tail && warp < 2) append_row(p, sbase, smem, warp, u, 0);
+  if (!more) return;
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) prepare_q(p, sbase, smem, u + 1, 2 * warp + h, 1);
+  bar_sync(3, kGroup);
+  if (threadIdx.x == kOutWarp * 32) mbar_arrive(sbase + SM_BAR + 8 * (B_QFULL + 1));
+}
+
 template <int CAP>
 __device__ __forceinline__ bool output(const F8DecodeParams<CAP>& p, uint32_t sbase, uint8_t* smem, uint32_t tmem, long long start, long long end) {
   const int tid = threadIdx.x - kOutWarp * 32, warp = tid >> 5;  // channel = TMEM lane
   const uint32_t o_cols = tmem + (static_cast<uint32_t>(warp * 32) << 16) + TM_O, bar0 = sbase + SM_BAR;
   volatile uint32_t* merge_flag = reinterpret_cast<volatile uint32_t*>(smem + SM_MERGE);
-  auto wait = [&](int b, uint32_t parity) { return counted_wait(bar0 + 8 * b, parity); };
+  auto wait = [&](int b, uint32_t parity) { return short_wait(bar0 + 8 * b, parity); };
   uint32_t n = 0, seg = 0, tails = 0;
   int late = -1;  // a unit whose part warp 15 counts
   Seg s;
@@ -609,7 +629,7 @@ __device__ __forceinline__ bool output(const F8DecodeParams<CAP>& p, uint32_t sb
     const int l = s.u / kHkv, g = s.u % kHkv;
     const F8AttnLayer& L = p.layer[l];
     const float* vs = L.vs + g * (p.Smax / kScaleBlock + 1);
-    if (seg == 0 && s.j1 == p.T && warp < 2) append_row(p, sbase, smem, warp, s.u, 0);
+    if (seg == 0) early(p, sbase, smem, s.u, s.j1 == p.T, t < end, warp);
     const int last = s.j1 == p.T ? p.T - 1 : s.j1;  // the tile whose scale the appending warp hands over
     float v_next = s.j0 < last ? vs[s.j0] : 0.f;
     float acc[kRepText];
@@ -620,7 +640,7 @@ __device__ __forceinline__ bool output(const F8DecodeParams<CAP>& p, uint32_t sb
       bool ok = wait(B_FAC + (n & 3), (n >> 2) & 1) && wait(B_ODONE + (n & 1), (n >> 1) & 1);  // the tile's factors, and its O
       float v_scale = v_next;
       if (j + 1 < last) v_next = vs[j + 1];
-      if (j == last) {
+      if (__builtin_expect(j == last, 0)) {
         ok = ok && wait(B_TAIL + kTails + tails, 0);
         v_scale = reinterpret_cast<const float*>(smem + SM_TAILS)[kTails + tails];
       }
@@ -632,7 +652,7 @@ __device__ __forceinline__ bool output(const F8DecodeParams<CAP>& p, uint32_t sb
       const float vf = v_scale * 0x1p-8f;
       tmem_landed16(d);
       tc_fence_before();
-      if (!bar_sync_and(3, kGroup, ok)) return false;
+      if (__builtin_expect(!bar_sync_and(3, kGroup, ok), 0)) return false;
       if (tid == 0) mbar_arrive(bar0 + 8 * (B_OFREE + (n & 1)));
 #pragma unroll
       for (int h = 0; h < kRepText; h += 2) {
