@@ -432,7 +432,7 @@ __device__ __forceinline__ bool softmax(const F8DecodeParams<CAP>& p, uint32_t s
     const F8AttnLayer& L = p.layer[l];
     const float* ks = L.ks + g * (p.Smax / kScaleBlock + 1);
     float4* scores = p.scores != nullptr && L.w_out != nullptr
-                         ? reinterpret_cast<float4*>(p.scores) + (static_cast<size_t>(s.u) * p.T * kKeyTile + tid) * 2 + set
+                         ? reinterpret_cast<float4*>(p.scores) + static_cast<size_t>(2 * s.u + set) * p.T * kKeyTile + tid
                          : nullptr;
     const int last = s.j1 == p.T ? p.T - 1 : s.j1;  // the tile whose scale the appending warp hands over
     float k_next = s.j0 < last ? ks[s.j0] : 0.f;
@@ -472,7 +472,7 @@ __device__ __forceinline__ bool softmax(const F8DecodeParams<CAP>& p, uint32_t s
         mine = lane == h ? mx : mine;
       }
       if (lane < H) red[(n & 1) * 32 + warp * H + lane] = mine;
-      if (__builtin_expect(scores != nullptr, 0) && live) scores[static_cast<size_t>(j) * kKeyTile * 2] = make_float4(x[0], x[1], x[2], x[3]);
+      if (__builtin_expect(scores != nullptr, 0) && live) scores[static_cast<size_t>(j) * kKeyTile] = make_float4(x[0], x[1], x[2], x[3]);
       if (__builtin_expect(!bar_sync_and(id, kGroup, ok), 0)) return false;
       const float4* r4 = reinterpret_cast<const float4*>(red + (n & 1) * 32);
       const float4 ra = r4[0], rb = r4[1], rc = r4[2], rd = r4[3];
@@ -764,12 +764,13 @@ __global__ void __launch_bounds__(f8d::kThreads, 1) fp8_decode_kernel(const __gr
 }
 
 // Weights from the scores: a thread has kWKeys keys of one unit under way. grid (key blocks, units)
-constexpr int kWThreads = 128, kWKeys = 4;
+constexpr int kWThreads = 256, kWKeys = 2;
 __global__ void __launch_bounds__(kWThreads) fp8_weights_kernel(const __grid_constant__ F8WeightsParams p) {
   const int u = blockIdx.y, key0 = blockIdx.x * (kWThreads * kWKeys) + threadIdx.x;
   const F8AttnLayer& L = p.layer[u / kHkv];
   const size_t at = static_cast<size_t>(u % kHkv) * p.Smax + key0;
-  const float4* x = reinterpret_cast<const float4*>(p.scores) + (static_cast<size_t>(u) * p.T * kKeyTile + key0) * 2;
+  const size_t half = static_cast<size_t>(p.T) * kKeyTile;
+  const float4* x = reinterpret_cast<const float4*>(p.scores) + 2 * u * half + key0;
   pdl_wait_primary();
   pdl_launch_dependents();
   if (L.w_out == nullptr) return;
@@ -779,8 +780,8 @@ __global__ void __launch_bounds__(kWThreads) fp8_weights_kernel(const __grid_con
   for (int i = 0; i < kWKeys; ++i) {
     const int key = key0 + i * kWThreads;
     if (key <= p.pos) {
-      a[i] = __ldcs(x + 2 * i * kWThreads);
-      b[i] = __ldcs(x + 2 * i * kWThreads + 1);
+      a[i] = __ldcs(x + i * kWThreads);
+      b[i] = __ldcs(x + half + i * kWThreads);
     }
     w[i] = key < p.pos && L.w_in != nullptr ? L.w_in[at + i * kWThreads] : 0.f;
   }

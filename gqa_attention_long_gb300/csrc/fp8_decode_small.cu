@@ -224,11 +224,11 @@ __global__ void __launch_bounds__(f8s::kThreads, 1) fp8_decode_small_kernel(cons
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
     if (p.scores != nullptr && L.w_out != nullptr) {
-      float* to = p.scores + (static_cast<size_t>(u) * p.T * kKeyTile + key0 + 2 * t) * kRepText + gk;
+      float* to = p.scores + (static_cast<size_t>(2 * u + (gk >> 2)) * p.T * kKeyTile + key0 + 2 * t) * 4 + (gk & 3);
 #pragma unroll
       for (int n = 0; n < 4; ++n)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) to[(8 * n + e) * kRepText] = x[n][e];
+        for (int e = 0; e < 2; ++e) to[(8 * n + e) * 4] = x[n][e];
     }
     const float top = fmaxf(m_run, m), fa = ex2_approx(m_run - top), fb = ex2_approx(m - top);
     m_run = top;

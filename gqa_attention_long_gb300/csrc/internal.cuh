@@ -381,7 +381,7 @@ struct F8DecodeParams {
   float* part_ml;      // [n_ctas][2 slots][8 heads][2]: reference (log2 units) and sum
   uint32_t* unit_cnt;  // [unit]: parts that have written their partial (zero between calls)
   uint32_t* status;
-  float* scores;       // [unit][Smax][8]: every key's scores in log2 units, if a layer's weights are asked for (else null)
+  float* scores;       // [unit][heads 0-3, 4-7][128 T][4]: every key's scores in log2 units, if a layer's weights are asked for (else null)
   float* lse;          // [unit][8]: the heads' log2-sum-exp
   long long W;         // key tiles: n_layers * 8 * T
   int T;               // key tiles per unit: pos / 128 + 1
