@@ -189,10 +189,11 @@ int launch_decode_t(const ea_decode_fp8_args* a, int n, int pos, int Smax, long 
 }
 
 // Little work (see fp8_decode_small.cu): at most kSmallTiles key tiles to an SM. Its kernel and the other one: 1 layer at pos 300 7.0 and 10.2 us, at
-// pos 4700 9.1 and 13.4, 4 layers 17.5 and 18.8, 8 layers (15.6 tiles) 26.8 and 24.7; 32 layers at pos 1000 (13.5) 26.6 and 29.4, 64 layers at
-// pos 500 (13.5) 35.9 and 44.3. Up to kOnePart tiles a unit is one CTA's: 1 layer at pos 500 7.6 us whole and 8.0 in two parts, at pos 700 9.2 and
-// 7.2.
-constexpr int kSmallTiles = 14, kOnePart = 4, kSmallParts = 32;
+// pos 4700 9.1 and 13.4, 4 layers 16.6 and 18.8, 8 layers (15.6 tiles) 26.8 and 24.7; 32 layers at pos 1000 (13.5) 26.6 and 29.4, 64 layers at
+// pos 500 (13.5) 35.9 and 44.3. Up to kOnePart tiles a unit is one CTA's (4 layers at pos 300, three tiles: 7.6 us whole, 7.0 in two parts). Up
+// to kSmallCluster parts are a cluster (1 layer at pos 1000: 7.6 us, 7.9 through global memory; in clusters of eight 2 layers at pos 2000 wait for
+// as many free SMs beside one another: 14.9 us, and 8.1).
+constexpr int kSmallTiles = 14, kOnePart = 2, kSmallParts = 32, kSmallCluster = 4;
 
 template <int CAP>
 int launch_small(const ea_decode_fp8_args* a, int n, int pos, int Smax, long long p0, bool weights, uint8_t* ws, const F8DecodeWs& wl,
@@ -207,6 +208,7 @@ int launch_small(const ea_decode_fp8_args* a, int n, int pos, int Smax, long lon
   p.lse = reinterpret_cast<float*>(ws + wl.lse_off);
   p.T = pos / kKeyTile + 1;
   p.parts = parts;
+  p.cluster = parts > 1 && parts <= kSmallCluster;
   p.pos = pos;
   p.Smax = Smax;
   p.n_layers = n;

@@ -8,8 +8,12 @@
 //   K: lane 4 g + t holds bytes [16 t, 16 t + 16) and [64 + 16 t, 80 + 16 t) of key g of each eight: word s of them is its part of step s.
 //   V: it holds bytes [16 g, 16 g + 16) of keys 2t, 2t + 1, 2t + 8, 2t + 9 of each sixteen: byte i of two keys is a pair for columns of channel 16 g + i.
 // Scores come out in P's own fragment layout. A CTA has eight warps and whole 128-row blocks of one unit; the block of the new row is moved to a
-// larger scale in the registers of the four warps that hold it. Up to kOnePart tiles a unit is one CTA's; a unit of more parts is merged by
-// the last one to finish.
+// larger scale in the registers of the four warps that hold it. Two to four parts of a unit are a cluster and meet in shared memory; more of
+// them are merged by the last one to finish.
+//
+// What bounds it: latencies one after the other (launch, the rows' and the codes' loads, the norm and rotation, the merge); 1 layer at pos 300
+// 7.0 us, at pos 4700 (9.6 MB of cache) 9.0 us, 8 layers at pos 1000 9.8 us.
+#include "cluster_exit.cuh"
 #include "fp8.cuh"
 
 namespace ea {
@@ -17,7 +21,7 @@ namespace f8s {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kKeys = 32;  // of a warp's chunk
-constexpr int kMaxParts = 32;
+constexpr int kMaxParts = 32, kMaxCluster = 4;
 
 struct Smem {
   float4 rot[kD / 2];
@@ -27,8 +31,9 @@ struct Smem {
   float scale[2];                         // its block's scale
   float shrink[2];                        // what the block's earlier codes are multiplied by (1: nothing)
   float2 ml[kWarps][kRepText];            // (reference, sum)
-  float w[kMaxParts][kRepText];
   uint32_t last;
+  float2 part_ml[kRepText];               // this CTA's, read by its cluster
+  alignas(16) float part_o[kRepText][kD];
   alignas(16) float o[kWarps][kRepText][kD];
 };
 
@@ -53,18 +58,26 @@ __device__ __forceinline__ void split_f16(float a, float b, uint32_t& hi, uint32
   lo = pack_f16x2((a - f.x) * 2048.0f, (b - f.y) * 2048.0f);
 }
 
-// The new K (kv = 0) or V row: its codes, its block's scale, and how the block's earlier rows move; one warp.
+// The new K (kv = 0) or V row, one warp: what it is made from, and then its codes, its block's scale, and how the block's earlier rows
+// move.
+struct NewRow {
+  float x[4], gm[4], old;
+};
 template <class P>
-__device__ __forceinline__ void new_row(const P& p, Smem& sm, const F8AttnLayer& L, int g, int kv, int lane) {
+__device__ __forceinline__ void load_new_row(const P& p, const F8AttnLayer& L, int g, int kv, int lane, NewRow& r) {
+  f8_load_row((kv ? L.v_raw : L.k_raw) + g * kD, lane, r.x);
+  f8_load_row(L.k_gamma, lane, r.gm);
+  r.old = p.pos % kScaleBlock > 0 ? (kv ? L.vs : L.ks)[g * (p.Smax / kScaleBlock + 1) + p.pos / kScaleBlock] : f8_pow2(kF8FirstExp);
+}
+template <class P>
+__device__ __forceinline__ void new_row(const P& p, Smem& sm, const F8AttnLayer& L, int g, int kv, int lane, const NewRow& r) {
   const int blk = p.pos / kScaleBlock, before = p.pos % kScaleBlock;
   float* scale = (kv ? L.vs : L.ks) + g * (p.Smax / kScaleBlock + 1) + blk;
-  const float old = before > 0 ? *scale : f8_pow2(kF8FirstExp);
-  float x[4];
-  f8_load_row((kv ? L.v_raw : L.k_raw) + g * kD, lane, x);
+  const float old = r.old;
+  float x[4] = {r.x[0], r.x[1], r.x[2], r.x[3]};
   if (kv == 0) {
-    float gm[4], y[4];
-    f8_load_row(L.k_gamma, lane, gm);
-    f8_norm_rope_pair(x, gm, sm.rot, lane, y);
+    float y[4];
+    f8_norm_rope_pair(x, r.gm, sm.rot, lane, y);
 #pragma unroll
     for (int e = 0; e < 4; ++e) x[e] = y[e];
   }
@@ -172,9 +185,11 @@ __global__ void __launch_bounds__(f8s::kThreads, 1) fp8_decode_small_kernel(cons
   const float* vsc = L.vs + g * (p.Smax / kScaleBlock + 1);
   const int blk0 = c / (kKeyTile / kKeys);
   float ks = c < c1 && blk0 < p.T - 1 ? ksc[blk0] : 0.f, vs = c < c1 && blk0 < p.T - 1 ? vsc[blk0] : 0.f;
-  const bool tail = j1 == p.T;
+  const bool appends = j1 == p.T && warp >= kWarps - 2;  // (the last two warps: K's new row, and V's)
+  NewRow fresh;
+  if (appends) load_new_row(p, L, g, warp - (kWarps - 2), lane, fresh);
   query_row(p, sm, L, g, warp, lane);
-  if (tail && warp >= kWarps - 2) new_row(p, sm, L, g, warp - (kWarps - 2), lane);
+  if (appends) new_row(p, sm, L, g, warp - (kWarps - 2), lane, fresh);
   __syncthreads();
   pdl_launch_dependents();
   // A fragments of step s: q's channels of this lane's word s, high (rows 0-7) and low (8-15)
@@ -305,7 +320,39 @@ __global__ void __launch_bounds__(f8s::kThreads, 1) fp8_decode_small_kernel(cons
     acc.z = fmaf(v.z, f, acc.z);
     acc.w = fmaf(v.w, f, acc.w);
   }
-  if (p.parts > 1) {
+  if (p.cluster) {
+    // a unit's parts are a cluster: their partials stay in shared memory, and the first one combines them
+    *reinterpret_cast<float4*>(&sm.part_o[h][4 * lane]) = acc;
+    if (lane == 0) sm.part_ml[h] = make_float2(M, sum);
+    cluster_sync();
+    if (part == 0) {
+      float4 v[kMaxCluster];
+      float2 ml[kMaxCluster];
+#pragma unroll
+      for (int k = 0; k < kMaxCluster; ++k)
+        if (k < p.parts) {
+          v[k] = ld_shared_cluster_v4(mapa_shared(smem_u32(&sm.part_o[h][4 * lane]), k));
+          ml[k] = ld_shared_cluster_v2(mapa_shared(smem_u32(&sm.part_ml[h]), k));
+        }
+#pragma unroll
+      for (int k = 0; k < kMaxCluster; ++k)
+        if (k < p.parts) M = fmaxf(M, ml[k].x);
+      sum = 0.f;
+      acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kMaxCluster; ++k)
+        if (k < p.parts) {
+          const float f = ex2_approx(ml[k].x - M);
+          sum = fmaf(ml[k].y, f, sum);
+          acc.x = fmaf(v[k].x, f, acc.x);
+          acc.y = fmaf(v[k].y, f, acc.y);
+          acc.z = fmaf(v[k].z, f, acc.z);
+          acc.w = fmaf(v[k].w, f, acc.w);
+        }
+    }
+    cluster_sync_exit();  // no CTA leaves while the first one reads its shared memory
+    if (part != 0) return;
+  } else if (p.parts > 1) {
     const size_t ps = static_cast<size_t>(blockIdx.x) * kRepText + h;
     __stcg(reinterpret_cast<float4*>(p.part_o + ps * kD) + lane, acc);
     if (lane == 0) __stcg(reinterpret_cast<float2*>(p.part_ml) + ps, make_float2(M, sum));
@@ -356,6 +403,13 @@ cudaError_t fp8_decode_small_set_attributes() {
 
 template <int CAP>
 cudaError_t launch_fp8_decode_small(const F8SmallParams<CAP>& p, cudaLaunchConfig_t cfg) {
+  cudaLaunchAttribute attr[2] = {cfg.attrs[0]};
+  if (p.cluster) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {static_cast<unsigned>(p.parts), 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+  }
   cfg.gridDim = dim3(p.n_layers * kHkv * p.parts);
   cfg.blockDim = dim3(f8s::kThreads);
   cfg.dynamicSmemBytes = sizeof(f8s::Smem);

@@ -399,6 +399,7 @@ struct F8SmallParams {
   float* scores;
   float* lse;
   int T, parts;        // CTAs to a unit, each with its share of the unit's tiles
+  int cluster;         // they are a cluster
   int pos, Smax, n_layers;
   float scale_log2;
 };

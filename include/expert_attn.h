@@ -437,11 +437,12 @@ int expert_attn_read_fp8(const ea_fp8_rows* layers, int n_layers, int row0, int 
  * expert_attn_write_fp8 (so earlier rows of its block can be rounded again), and every query head attends to the values
  * that rows [0, pos] then have. Rows after pos are never used and stay as they are. q_raw bf16 [64][128], k_raw and v_raw
  * bf16 [8][128], gains bf16 [128], out bf16 [64][128]; k_new and v_new, if not NULL, bf16 [8][128], receive the new row's
- * values. q rows are held to 2^-19 of their largest channel, softmax weights to 2^-14, K and V as stored; q_raw's and k_raw's
+ * values. q rows are held to 2^-19 of their largest channel, K and V as stored, softmax weights to 2^-10 of themselves down to 2^-13 of
+ * the largest among their row's block of 128, and to 2^-23 of that below; q_raw's and k_raw's
  * squares are summed in fp32 (values below 2^60).
  * weight_out, if not NULL (layer by layer): fp32 [8][Smax]; element (g, r), r < pos, becomes weight_in's (0 if weight_in is NULL) plus the
  * softmax weights of row r summed over the 8 query heads of KV head g, and element (g, pos) those of row pos alone; later
- * elements stay as they are. weight_in may be weight_out; otherwise it must not stand twice in a call either. Both
+ * elements stay as they are. weight_in may be weight_out; otherwise it must not overlap what the call writes, nor stand twice in it. Both
  * 16-byte aligned. 0 <= pos < Smax; |pos + rope_delta| < 2^24. */
 typedef struct {
   const void* q_raw;

@@ -100,7 +100,7 @@ def test_parts_of_little_work(h, device, sms):
                 assert decode(h, n, pos, 1 << 22, False) == OK, (n, pos)
                 if h.fake_fp8_kernel() == 1:
                     T = pos // 128 + 1
-                    assert 1 <= h.fake_fp8_parts() <= min(32, T) and (T <= 4) <= (h.fake_fp8_parts() == 1)
+                    assert 1 <= h.fake_fp8_parts() <= min(32, T) and (T <= 2) <= (h.fake_fp8_parts() == 1)
                     assert h.fake_fp8_parts() == 1 or h.fake_fp8_parts() * n * 8 <= sms
     finally:
         h.fake_sms(152)
