@@ -7,9 +7,9 @@
 //
 // The codes go to the tensor cores as they are, K's as the rows of one product and V's as the columns of the next, and no value is
 // ever widened. What they meet has more bits than a code: it comes in pieces. A number y, |y| <= 256, is c0 + c1 / 32 + c2 / 1024 + ..,
-// each c the e4m3 number next to 32 times what the pieces before left: a code is off by at most half of its last place,
-// 2^-5 of a number's power of two, so that four pieces hold a q row to 2^-20 of its largest channel (scores that weights come from:
-// fp32 would be 2^-24), two hold a softmax weight to 2^-10 of itself down to 2^-13 of the tile's largest, and to 2^-23 of that below (the output
+// each c the e4m3 number next to 32 times what the pieces before left. A code has four bits: what it leaves of a y in [2^e, 2^(e+1)) is at
+// most 2^(e-4), so that four pieces hold a q row to 2^-19 of its largest channel (scores that weights come from: fp32 would be
+// 2^-24), and two hold a softmax weight to 2^-9 of itself down to 2^-14 of the tile's largest, and to 2^-23 of that below (the output
 // is bf16, 2^-8). Products of codes are exact, sums are in fp32, and
 // pieces are columns that the MMA has to spare: 8 heads in 4 pieces are N = 32 (up to 64 columns an MMA takes the same 46 cycles).
 //   S^T  = K Q^T    M = 128 keys, N = 32 (half of the heads, piece, head), K = 128 channels; A = the K tile (K-major)

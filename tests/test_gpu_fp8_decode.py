@@ -1,7 +1,8 @@
 """The decode step over an 8-bit cache against the oracle in fp64 over the appended cache's values.
 
-Bars. The output is bf16: at most half a step off, 2^-8 of it; softmax weights are held to 2^-14 and q to 2^-19 of a row's
-largest channel, which add less than 2^-12: relative L2 <= REL = 2^-8 + 2^-12. A weight is fp32: its relative error is the
+Bars. The output is bf16: at most half a step off, 2^-8 of it, and 2^-8 / sqrt(3) of it in relative L2 over mantissas of every size; softmax
+weights are held to 2^-9 (rounded to nearest, of either sign), which adds no more than 2^-9 / sqrt(3) over keys whose V is random, and q to
+2^-19 of a row's largest channel: relative L2 <= REL = 2^-8 + 2^-12. A weight is fp32: its relative error is the
 error of its score and of the log-sum-exp, each at most (2^-18 + 2^-19) times sum |q k| / sqrt(128), which these inputs keep
 under 12: 2 x 12 x 1.5 x 2^-18 < 1.5e-4 = WREL. The stored rows are those of the rule, bit for bit."""
 import numpy as np
@@ -345,3 +346,36 @@ def test_workspace_too_small_is_refused():
     ws = ea.alloc_decode_fp8_workspace(1, 256, weights=False)
     with pytest.raises(ea.ExpertAttnError, match="workspace"):
         ea.text_decode_attention_fp8([b], 100, 256, 0, ws)
+
+
+@pytest.mark.parametrize("first", [True, False])
+@pytest.mark.parametrize("layers", [1, 20])
+def test_many_keys_far_below_one(layers, first):
+    """One key e^16.97 above the others, which all together weigh 2 % of it (2^19 keys), or 2^-9 (2^14 keys, twenty layers): a weight
+    that its own tile's largest outweighs by 2^24 may count as zero, those of the other tiles must not."""
+    n = 1 << (19 if layers == 1 else 14)
+    Smax, at = n + 128, 5 if first else n - 5
+    x = decode_inputs(1)
+    for name in ("q_gamma", "k_gamma"):
+        x[name].fill_(1.0)
+    x["q_raw"].zero_()
+    x["q_raw"][..., 63] = x["q_raw"][..., 127] = 1.0  # normed: 8 in both
+    x["k_raw"].zero_()
+    x["v_raw"].fill_(1.0)
+    bufs = []
+    for _ in range(layers):
+        cache = ea.alloc_fp8_cache(Smax)
+        cache.v_cache.fill_(0x38)        # 1 in every channel, under scales of 1
+        cache.k_cache[:, at, 63] = 0x58  # 16
+        cache.k_cache[:, at, 127] = 0x50  # 8: 8 * 24 / sqrt(128) = 16.97
+        cache.v_cache[:, at] = 0xB8      # -1
+        bufs.append(decode_buffers(x, cache, None, torch.zeros(8, Smax, device=DEV)))
+    ws = ea.alloc_decode_fp8_workspace(layers, Smax, weights=True)
+    ea.text_decode_attention_fp8(bufs, n, Smax, -n, ws)
+    check_status(ws)
+    big, rest = np.exp(8 * 24 / 128 ** 0.5), n
+    for b in bufs:
+        want = (rest - big) / (rest + big)
+        assert float((b.out.double() - want).abs().max()) <= (2.0 ** -8 + 2.0 ** -12) * abs(want)
+        w = f64(b.weight_out)
+        assert np.allclose(w[:, at], 8 * big / (rest + big), rtol=WREL) and np.allclose(w[:, at + 1:n + 1], 8 / (rest + big), rtol=WREL)
