@@ -28,10 +28,11 @@ constexpr int kLoads = 2;           // loads of four weights that a thread has i
 constexpr int kMoveThreads = 256;
 constexpr int kPieces = kScaleBlock * kD / 16 / kMoveThreads;  // 16-byte pieces of a block that a thread moves
 
-// Order-preserving bits: NaN above infinity, the zeros equal.
+// Order-preserving bits of a weight: NaN above infinity, the zeros equal. No weight has kAlways or 0.
+constexpr uint32_t kAlways = 0xFFFFFFFFu;  // a row that stays whatever its weight is (0: there is no such row)
 __device__ __forceinline__ uint32_t key_of(float w) {
-  const uint32_t u = __float_as_uint(w + 0.0f);
-  return w != w ? 0xFFFFFFFFu : (u & 0x80000000u) ? ~u : u | 0x80000000u;
+  const uint32_t u = __float_as_uint(w + 0.0f), key = u ^ (static_cast<uint32_t>(static_cast<int>(u) >> 31) | 0x80000000u);
+  return w != w ? kAlways - 1u : key;
 }
 __device__ __forceinline__ uint4 ld_cluster_v4(uint32_t a) {
   uint4 v;
@@ -65,8 +66,20 @@ __global__ void __launch_bounds__(kSelThreads, 2048 / kSelThreads) fp8_evict_sel
   uint32_t* before = p.before + static_cast<size_t>(u) * (p.blocks + 1);
   const int lo = p.n_first, hi = p.n_rows - p.n_recent;  // rows that are chosen among
   const int s0 = min(rank * p.slice, p.n_rows), s1 = min(s0 + p.slice, p.n_rows);  // this CTA's rows
+  const int groups = (s1 - s0 + kScaleBlock - 1) / kScaleBlock, pad = groups * kScaleBlock;  // (Smax is in blocks, too)
   const bool cached = p.slice <= kCached;
-  uint32_t need = p.n_keep - p.n_first - p.n_recent, bits = 0u;
+  // bits of the four rows from row s0 + j on
+  auto bits4 = [&](int j) {
+    const float4 x = *reinterpret_cast<const float4*>(w + s0 + j);
+    uint4 k = make_uint4(key_of(x.x), key_of(x.y), key_of(x.z), key_of(x.w));
+    const int i = s0 + j;
+    if (__builtin_expect(i < lo || i + 4 > hi, 0)) {
+      auto mark = [&](int r, uint32_t v) { return r >= p.n_rows ? 0u : r < lo || r >= hi ? kAlways : v; };
+      k = make_uint4(mark(i, k.x), mark(i + 1, k.y), mark(i + 2, k.z), mark(i + 3, k.w));
+    }
+    return k;
+  };
+  uint32_t need = p.n_keep, bits = 0u;
   for (int i = tid; i < 3 * kBins / 4; i += kSelThreads) reinterpret_cast<uint4*>(sm.hist)[i] = make_uint4(0u, 0u, 0u, 0u);
   __syncthreads();
   pdl_wait_primary();
@@ -80,30 +93,24 @@ __global__ void __launch_bounds__(kSelThreads, 2048 / kSelThreads) fp8_evict_sel
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, width = pass == 2 ? 10 : 11;
     uint32_t* hist = sm.hist[pass];
-    // (a load of four weights may end behind the last row, but not behind its block of the array)
     const bool load = pass == 0 || !cached;
 #pragma unroll 1
-    for (int i0 = s0 + 4 * tid; i0 < s1; i0 += 4 * kLoads * kSelThreads) {
+    for (int j0 = 4 * tid; j0 < pad; j0 += 4 * kLoads * kSelThreads) {
       uint4 k[kLoads];
 #pragma unroll
       for (int q = 0; q < kLoads; ++q) {
-        const int i = i0 + 4 * kSelThreads * q;
-        if (i < s1) k[q] = load ? *reinterpret_cast<const uint4*>(w + i) : *reinterpret_cast<const uint4*>(keys + (i - s0));
+        const int j = j0 + 4 * kSelThreads * q;
+        if (j < pad) k[q] = load ? bits4(j) : *reinterpret_cast<const uint4*>(keys + j);
       }
 #pragma unroll
       for (int q = 0; q < kLoads; ++q) {
-        const int i = i0 + 4 * kSelThreads * q;
-        if (i >= s1) break;
-        uint32_t v[4] = {k[q].x, k[q].y, k[q].z, k[q].w};
-        if (load) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = key_of(__uint_as_float(v[e]));
-          if (cached) *reinterpret_cast<uint4*>(keys + (i - s0)) = make_uint4(v[0], v[1], v[2], v[3]);
-        }
+        const int j = j0 + 4 * kSelThreads * q;
+        if (j >= pad) break;
+        if (pass == 0 && cached) *reinterpret_cast<uint4*>(keys + j) = k[q];
+        const uint32_t v[4] = {k[q].x - bits, k[q].y - bits, k[q].z - bits, k[q].w - bits};
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (i + e >= lo && i + e < hi && (pass == 0 || (v[e] >> (shift + width)) == (bits >> (shift + width))))
-            atomicAdd(&hist[(v[e] >> shift) & ((1u << width) - 1u)], 1u);
+          if (pass == 0 || v[e] >> (shift + width) == 0u) atomicAdd(&hist[v[e] >> shift], 1u);
       }
     }
     if (cs > 1) cluster_sync();
@@ -145,7 +152,7 @@ __global__ void __launch_bounds__(kSelThreads, 2048 / kSelThreads) fp8_evict_sel
     uint32_t above = sum - mine;
 #pragma unroll
     for (int k = 0; k < kSelWarps; ++k) above += k < warp ? sm.scan[k] : 0u;
-    if (above < need && need <= above + mine) {  // (one thread, unless nothing is needed)
+    if (above < need && need <= above + mine) {  // (one thread)
       uint32_t d = b0 + 3;
       if (above + c.w < need) { above += c.w; --d;
         if (above + c.z < need) { above += c.z; --d;
@@ -154,33 +161,27 @@ __global__ void __launch_bounds__(kSelThreads, 2048 / kSelThreads) fp8_evict_sel
       sm.found[1] = above;
     }
     __syncthreads();
-    if (need > 0) {
-      bits |= sm.found[0] << shift;
-      need -= sm.found[1];
-    }
+    bits |= sm.found[0] << shift;
+    need -= sm.found[1];
   }
-  if (p.n_keep == p.n_first + p.n_recent) bits = 0xFFFFFFFFu;  // none is chosen: nothing lies above, and need is 0
-  // Rows above the threshold (or kept anyway) and at it, by warp: a warp has 128-row blocks in a row, a lane four rows of each
-  const int groups = (s1 - s0 + kScaleBlock - 1) / kScaleBlock, per = (groups + kSelWarps - 1) / kSelWarps;
+  // Rows above the threshold and at it, by warp: a warp has 128-row blocks in a row, a lane four rows of each
+  const int per = (groups + kSelWarps - 1) / kSelWarps;
   const int g0 = min(warp * per, groups), g1 = min(g0 + per, groups);
-  // bit e: whether row s0 + 128 grp + 4 lane + e is above; bit 16 + e: at
+  // bit e: whether row s0 + 128 grp + 4 lane + e is above; bit 4 + e: at
   auto look = [&](int grp) {
-    const int j = kScaleBlock * grp + 4 * lane, i = s0 + j;
-    uint4 k = *reinterpret_cast<const uint4*>(cached ? keys + j : reinterpret_cast<const uint32_t*>(w) + i);
-    uint32_t v[4] = {k.x, k.y, k.z, k.w}, m = 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (!cached) v[e] = key_of(__uint_as_float(v[e]));
-      const bool chosen = i + e >= lo && i + e < hi;
-      if (i + e < s1) m |= (!chosen || v[e] > bits ? 1u : v[e] == bits ? 0x10000u : 0u) << e;
-    }
-    return m;
+    const int j = kScaleBlock * grp + 4 * lane;
+    const uint4 k = cached ? *reinterpret_cast<const uint4*>(keys + j) : bits4(j);
+    return (k.x > bits ? 1u : 0u) | (k.y > bits ? 2u : 0u) | (k.z > bits ? 4u : 0u) | (k.w > bits ? 8u : 0u) |
+           (k.x == bits ? 16u : 0u) | (k.y == bits ? 32u : 0u) | (k.z == bits ? 64u : 0u) | (k.w == bits ? 128u : 0u);
   };
+  static_assert(kCached / kScaleBlock / 32 <= 8 && kSlice / kScaleBlock / 16 <= 8, "eight blocks' bits in 64");
+  uint64_t seen = 0;  // of a cached slice
   uint32_t a = 0, e = 0;
   for (int grp = g0; grp < g1; ++grp) {
     const uint32_t m = look(grp);
-    a += __popc(m & 0xFFFFu);
-    e += __popc(m >> 16);
+    if (cached) seen |= static_cast<uint64_t>(m) << (8 * (grp - g0));
+    a += __popc(m & 15u);
+    e += __popc(m >> 4);
   }
   a = __reduce_add_sync(0xffffffffu, a);
   e = __reduce_add_sync(0xffffffffu, e);
@@ -209,7 +210,7 @@ __global__ void __launch_bounds__(kSelThreads, 2048 / kSelThreads) fp8_evict_sel
     cluster_sync_exit();  // no CTA leaves while another reads its shared memory
   }
   for (int grp = g0; grp < g1; ++grp) {
-    const uint32_t m = look(grp), c = __popc(m & 0xFFFFu) | __popc(m >> 16) << 16;
+    const uint32_t m = cached ? static_cast<uint32_t>(seen >> (8 * (grp - g0))) & 255u : look(grp), c = __popc(m & 15u) | __popc(m >> 4) << 16;
     uint32_t sum = c;  // of the lanes up to this one: rows above, and (from bit 16) at the threshold
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -221,7 +222,7 @@ __global__ void __launch_bounds__(kSelThreads, 2048 / kSelThreads) fp8_evict_sel
     if (lane == 0) before[i / kScaleBlock] = a1 + min(e1, need);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const bool gt = (m >> e) & 1u, eq = (m >> (16 + e)) & 1u;
+      const bool gt = (m >> e) & 1u, eq = (m >> (4 + e)) & 1u;
       if (gt || (eq && e1 < need)) kept[a1 + min(e1, need)] = i + e;
       a1 += gt;
       e1 += eq;
