@@ -34,6 +34,10 @@ __device__ __forceinline__ uint32_t key_of(float w) {
   const uint32_t u = __float_as_uint(w + 0.0f), key = u ^ (static_cast<uint32_t>(static_cast<int>(u) >> 31) | 0x80000000u);
   return w != w ? kAlways - 1u : key;
 }
+// One more in a counter in shared memory, if v <= most (with a branch: 64 layers of 4700 rows 184.7 us, not 182.1).
+__device__ __forceinline__ void count_up_to(uint32_t v, uint32_t most, uint32_t counter) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ls.u32 p, %0, %1;\n\t@p red.shared.add.u32 [%2], 1;\n\t}" ::"r"(v), "r"(most), "r"(counter) : "memory");
+}
 __device__ __forceinline__ uint4 ld_cluster_v4(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
@@ -91,8 +95,10 @@ __global__ void __launch_bounds__(kSelThreads, 2048 / kSelThreads) fp8_evict_sel
   // Of the least weight that stays: 11, then 11, then 10 bits. `need` rows stay among those that share the bits known so far.
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, width = pass == 2 ? 10 : 11;
-    uint32_t* hist = sm.hist[pass];
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const uint32_t most = pass == 0 ? 0xFFFFFFFFu : pass == 1 ? (1u << 21) - 1u : (1u << 10) - 1u;
+    const uint32_t* hist = sm.hist[pass];
+    const uint32_t bins = smem_u32(hist);
     const bool load = pass == 0 || !cached;
 #pragma unroll 1
     for (int j0 = 4 * tid; j0 < pad; j0 += 4 * kLoads * kSelThreads) {
@@ -109,8 +115,7 @@ __global__ void __launch_bounds__(kSelThreads, 2048 / kSelThreads) fp8_evict_sel
         if (pass == 0 && cached) *reinterpret_cast<uint4*>(keys + j) = k[q];
         const uint32_t v[4] = {k[q].x - bits, k[q].y - bits, k[q].z - bits, k[q].w - bits};
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (pass == 0 || v[e] >> (shift + width) == 0u) atomicAdd(&hist[v[e] >> shift], 1u);
+        for (int e = 0; e < 4; ++e) count_up_to(v[e], most, bins + 4 * (v[e] >> shift));
       }
     }
     if (cs > 1) cluster_sync();
@@ -149,9 +154,8 @@ __global__ void __launch_bounds__(kSelThreads, 2048 / kSelThreads) fp8_evict_sel
     }
     if (lane == 31) sm.scan[warp] = sum;
     __syncthreads();
-    uint32_t above = sum - mine;
-#pragma unroll
-    for (int k = 0; k < kSelWarps; ++k) above += k < warp ? sm.scan[k] : 0u;
+    const uint32_t above0 = __reduce_add_sync(0xffffffffu, lane < min(warp, kBins / 128) ? sm.scan[lane] : 0u);
+    uint32_t above = above0 + (sum - mine);
     if (above < need && need <= above + mine) {  // (one thread)
       uint32_t d = b0 + 3;
       if (above + c.w < need) { above += c.w; --d;
