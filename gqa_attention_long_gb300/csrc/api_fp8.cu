@@ -145,6 +145,16 @@ F8AttnLayer attn_layer(const ea_decode_fp8_args& x) {
           static_cast<__nv_bfloat16*>(x.k_new), static_cast<__nv_bfloat16*>(x.v_new), x.weight_in, x.weight_out};
 }
 
+// fp8_decode_kernel's CTAs, at most: one to an SM.
+int decode_ctas(int sm_count) { return sm_count < kMaxGridCtas ? sm_count : kMaxGridCtas; }
+
+// Whether fp8_decode_kernel forms the weights itself: units of at most kF8KeptTiles tiles, and one and a half of them to a CTA, so
+// that most are whole ones. With the second kernel and without it: 64 layers at pos 4700 132.5 and 120.3 us, at pos 2500 79.0 and 73.6, 32 layers at
+// pos 4900 (1.7 units) 76.3 and 74.0; 16 layers at pos 4700 (0.8) 44.2 and 47.0.
+bool forms_weights(int n, int pos, int sm_count) {
+  return n > kSmallCap && pos / kKeyTile + 1 <= kF8KeptTiles && 2 * n * kHkv >= 3 * decode_ctas(sm_count);
+}
+
 // Parameter blocks are large (24 KB at full capacity): kept off the stack, one per capacity, with a mutex of its own.
 template <int CAP>
 struct DecodeBlock {
@@ -170,6 +180,7 @@ int launch_decode_t(const ea_decode_fp8_args* a, int n, int pos, int Smax, long 
   p.status = reinterpret_cast<uint32_t*>(ws);
   p.scores = weights ? reinterpret_cast<float*>(ws + wl.scores_off) : nullptr;
   p.lse = reinterpret_cast<float*>(ws + wl.lse_off);
+  p.form = forms_weights(n, pos, sm_count);
   p.T = pos / kKeyTile + 1;
   p.W = static_cast<long long>(n) * kHkv * p.T;
   p.pos = pos;
@@ -178,9 +189,8 @@ int launch_decode_t(const ea_decode_fp8_args* a, int n, int pos, int Smax, long 
   p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(kD)));
   cudaLaunchAttribute attr[1];
   cudaLaunchConfig_t cfg = launch_config(st, attr, true);
-  int n_ctas = sm_count < kMaxGridCtas ? sm_count : kMaxGridCtas;
-  if (static_cast<long long>(n_ctas) > p.W) n_ctas = static_cast<int>(p.W);
-  cfg.gridDim = dim3(n_ctas);
+  const int most = decode_ctas(sm_count);
+  cfg.gridDim = dim3(most < p.W ? most : static_cast<int>(p.W));
   if (launch_fp8_decode<CAP>(p, cfg) != cudaSuccess) {
     cudaGetLastError();
     return EA_ERR_CUDA;
@@ -328,7 +338,7 @@ int text_decode_attention_fp8(const ea_decode_fp8_args* layers, int n_layers, in
          : parts > 0 ? launch_small<kDecodeMaxLayers>(layers + l0, n, pos, Smax, p0, weights, ws, wl, parts, st)
          : n <= kSmallCap ? launch_decode_t<kSmallCap>(layers + l0, n, pos, Smax, p0, weights, ws, wl, di.sm_count, st)
                           : launch_decode_t<kDecodeMaxLayers>(layers + l0, n, pos, Smax, p0, weights, ws, wl, di.sm_count, st);
-    if (rc == EA_OK && weights) rc = launch_weights(layers + l0, n, pos, Smax, ws, wl, st);
+    if (rc == EA_OK && weights && (parts > 0 || !forms_weights(n, pos, di.sm_count))) rc = launch_weights(layers + l0, n, pos, Smax, ws, wl, st);
     if (rc != EA_OK) return rc;
   }
   return EA_OK;

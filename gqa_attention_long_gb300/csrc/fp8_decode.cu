@@ -25,8 +25,13 @@
 // was what they waited for most (2.8 of 10 warp cycles an instruction): they are short, and what is rare is out of their way.
 // A unit cut over several CTAs is merged by the part that finishes last; a part that is not its CTA's last segment is counted by warp
 // 15, and merged at the CTA's end should it be the last after all, so that the output warps need not wait.
-// For layers whose weights are asked for, the scores go to the workspace (32 bytes a key) and a second kernel forms the weights
-// from them and the units' log2-sum-exps.
+// Weights that are asked for need a unit's scores once more when its log2-sum-exps are known: 32 bytes a key. They go to the workspace, and
+// a second kernel forms the weights; or, where most units are whole ones of one CTA, these stay in tensor memory, whose columns hold 44 tiles'
+// scores beside the accumulators, and the output warps form their weights between the next unit's tiles (64 layers at pos 4700: 120 us, not
+// 132.5); the cut ones' are formed by the CTA that merges them. What that takes is the loads' latency (sums before come through
+// prefetches and asynchronous copies: 10 us less) rather than the arithmetic.
+// Figures (64 layers at pos 4700; 4 layers at pos 131070): 99.5 and 160.5 us, 91.6 % and 98.5 % of the copy's rate; the former's 125 tiles
+// a CTA bear a start and an end of about 8 us.
 #include "fp8.cuh"
 
 namespace ea {
@@ -42,6 +47,7 @@ constexpr uint32_t kOpBytes = kCols * 128;          // Q: 32 rows of 128 bytes
 constexpr uint32_t kPBytes = kOutCols * 128;        // P: 16
 constexpr int kMaxParts = 160;                      // parts of one unit (at most one per CTA)
 constexpr int kMergeBatch = 4;
+constexpr int kWeigh = 4;  // tiles whose weights the output warps form at a time
 constexpr int kTails = 72;                          // units of one CTA, at most
 // Shared memory (offsets from the 1024-byte-aligned base)
 constexpr uint32_t SM_K = 0;
@@ -56,7 +62,9 @@ constexpr uint32_t SM_QF = SM_FIN + 8 * kRepText * 8;            // [8 segments]
 constexpr uint32_t SM_LRED = SM_QF + 8 * kRepText * 4;           // [8 warps][4 heads]
 constexpr uint32_t SM_TAILS = SM_LRED + 8 * 4 * 4;    // [K, V][kTails]: the appended block's scale
 constexpr uint32_t SM_SW = SM_TAILS + 2 * kTails * 4;            // merge weights [part][head]
-constexpr uint32_t SM_BAR = (SM_SW + kMaxParts * kRepText * 4 + 7) & ~7u;
+constexpr uint32_t SM_UNIT = SM_SW + kMaxParts * kRepText * 4;   // WeighUnit
+constexpr uint32_t SM_SUMS = SM_UNIT + 48;                       // sums before: [kWeigh][128]
+constexpr uint32_t SM_BAR = SM_SUMS + kWeigh * kKeyTile * 4;
 // PFULL, ODONE, OFREE: one barrier per parity of the tile count; SDONE: per S buffer; QFULL, QFREE: per Q buffer. The softmax warps
 // can be two tiles, and so three segments, ahead of the output warps: what those wait for from them has as many barriers (FAC by
 // tile, FIN by segment) as it takes for none to complete twice unseen. FAC also tells that a tile's S buffer has been read.
@@ -65,9 +73,15 @@ constexpr int B_KFULL = 0, B_KEMPTY = B_KFULL + kKRing, B_VFULL = B_KEMPTY + kKR
               B_DRAIN = B_FIN + 8, B_PART = B_DRAIN + 2, B_LATE = B_PART + 1, B_TAIL = B_LATE + 1, kNumBars = B_TAIL + 2 * kTails;  // TAIL: [K, V][unit], whose new row is in place
 constexpr uint32_t SM_TMEM = SM_BAR + kNumBars * 8;
 constexpr uint32_t SM_MERGE = SM_TMEM + 4;
-constexpr uint32_t kSmemBytes = SM_MERGE + 4 + 1024;  // + base alignment
+constexpr uint32_t SM_TODO = SM_MERGE + 4;  // [2]: merged units whose weights are still to be formed (or -1)
+constexpr uint32_t kSmemBytes = SM_TODO + 8 + 1024;  // + base alignment
 static_assert(kSmemBytes <= 232448, "shared memory budget of one sm_103 CTA");
-constexpr uint32_t kTmemCols = 256, TM_S = 0, TM_O = 128;  // 4 and 2 buffers of 32 columns
+// 4 and 2 buffers of 32 and 16 columns; then the scores of kKept tiles, 8 columns each
+constexpr uint32_t kTmemCols = 512, TM_S = 0, TM_O = 128, TM_X = 160, kKept = (kTmemCols - TM_X) / 8;
+// (kForm) Tile n's scores take the place of tile n - kKept's. Who writes them knows that output warps have read out O of tile n - 4, and have so
+// formed the weights that go with tile n - 5's. They form those of tiles 4 k .. 4 k + 3 of a unit of T tiles beside tile T + k, both counted from
+// its first: T + k <= 4 k + kKept - 5 for every k.
+static_assert(kF8KeptTiles + 5 <= static_cast<int>(kKept), "scores are read before others take their place");
 
 struct Seg {
   int u, j0, j1;  // unit and its key-tile range [j0, j1)
@@ -82,6 +96,15 @@ __device__ __forceinline__ bool next_seg(long long& t, long long end, int T, Seg
   s.j1 = static_cast<int>(j1 < T ? j1 : T);
   t += s.j1 - s.j0;
   return true;
+}
+
+// What becomes of the weights: none is asked for; scores go to the workspace, for a second kernel; or this one forms them, of whole units
+// from scores that it keeps in tensor memory.
+constexpr int kNoWeights = 0, kScores = 1, kForm = 2;
+// Whether the CTA whose segment s is keeps its unit's scores (kForm).
+template <class P>
+__device__ __forceinline__ bool kept_unit(const P& p, const Seg& s) {
+  return s.j0 == 0 && s.j1 == p.T;
 }
 
 __device__ __forceinline__ float warp_sum(float x) {
@@ -103,6 +126,15 @@ __device__ __forceinline__ uint32_t atom_add_acq_rel_gpu(uint32_t* a, uint32_t v
 __device__ __forceinline__ void st_shared_u8(uint32_t a, uint32_t v) {
   asm volatile("st.shared.u8 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
+__device__ __forceinline__ void st_shared_f32(uint32_t a, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory"); }
+__device__ __forceinline__ float ld_shared_f32(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const float* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
 // The waits of this file are a whole warp's and take little code: one look here, and the further ones (counted_wait, which gives up after a
 // number of them) out of the loops' way: 64 layers at pos 4700 107 -> 100 us. Who gives up notes it and leaves, and then so does, the
 // same number of looks later, who waits for it.
@@ -112,6 +144,11 @@ __device__ __forceinline__ bool short_wait(uint32_t bar, uint32_t parity) {
   return long_wait(bar, parity);
 }
 
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const float (&x)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(__float_as_uint(x[0])),
+               "r"(__float_as_uint(x[1])), "r"(__float_as_uint(x[2])), "r"(__float_as_uint(x[3]))
+               : "memory");
+}
 // 16 consecutive TMEM columns of this warp's 32 lanes -> 16 registers per thread.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
@@ -412,7 +449,7 @@ __device__ __noinline__ float last_tile(const F8DecodeParams<CAP>& p, uint32_t s
 }
 
 // One set of warps: heads 4 set .. 4 set + 3 of every tile.
-template <int CAP>
+template <int kMode, int CAP>
 __device__ __forceinline__ bool softmax(const F8DecodeParams<CAP>& p, uint32_t sbase, uint8_t* smem, uint32_t tmem, int set, long long start,
                                      long long end) {
   constexpr int H = kRepText / 2;
@@ -431,9 +468,10 @@ __device__ __forceinline__ bool softmax(const F8DecodeParams<CAP>& p, uint32_t s
     const int l = s.u / kHkv, g = s.u % kHkv;
     const F8AttnLayer& L = p.layer[l];
     const float* ks = L.ks + g * (p.Smax / kScaleBlock + 1);
-    float4* scores = p.scores != nullptr && L.w_out != nullptr
-                         ? reinterpret_cast<float4*>(p.scores) + static_cast<size_t>(2 * s.u + set) * p.T * kKeyTile + tid
-                         : nullptr;
+    // where scores go: tensor memory (keep), or the workspace
+    const bool weights = kMode != kNoWeights && L.w_out != nullptr, keep = kMode == kForm && weights && kept_unit(p, s);
+    float4* scores = weights && !keep ? reinterpret_cast<float4*>(p.scores) + static_cast<size_t>(2 * s.u + set) * p.T * kKeyTile + tid
+                                      : nullptr;
     const int last = s.j1 == p.T ? p.T - 1 : s.j1;  // the tile whose scale the appending warp hands over
     float k_next = s.j0 < last ? ks[s.j0] : 0.f;
     if (seg == 0) {
@@ -472,7 +510,11 @@ __device__ __forceinline__ bool softmax(const F8DecodeParams<CAP>& p, uint32_t s
         mine = lane == h ? mx : mine;
       }
       if (lane < H) red[(n & 1) * 32 + warp * H + lane] = mine;
-      if (__builtin_expect(scores != nullptr, 0) && live) scores[static_cast<size_t>(j) * kKeyTile] = make_float4(x[0], x[1], x[2], x[3]);
+      if (kMode != kNoWeights && scores != nullptr && live) scores[static_cast<size_t>(j) * kKeyTile] = make_float4(x[0], x[1], x[2], x[3]);
+      if (keep) {
+        tc_fence_after();
+        tmem_st4(s_cols + TM_X - TM_S - set * 12 + n % kKept * 8, x);
+      }
       if (__builtin_expect(!bar_sync_and(id, kGroup, ok), 0)) return false;
       const float4* r4 = reinterpret_cast<const float4*>(red + (n & 1) * 32);
       const float4 ra = r4[0], rb = r4[1], rc = r4[2], rd = r4[3];
@@ -505,6 +547,7 @@ __device__ __forceinline__ bool softmax(const F8DecodeParams<CAP>& p, uint32_t s
         to[1] = make_float4(fac[2].x, fac[2].y, fac[3].x, fac[3].y);
       }
       fence_proxy_async_smem();  // P, and zeroed V rows, are read by the tensor core
+      if (keep) tmem_wait_st();
       tc_fence_before();
       bar_sync(id, kGroup);
       if (tid == 0) {
@@ -532,9 +575,9 @@ __device__ __forceinline__ bool softmax(const F8DecodeParams<CAP>& p, uint32_t s
 }
 
 // ----------------------------------------------------------------------------- output warps
-// Merges unit u from its parts' partials: output thread = channel.
+// Merges unit u from its parts' partials: output thread = channel. The nth that this CTA merges, whose weights it forms, too.
 template <int CAP>
-__device__ __noinline__ void merge(const F8DecodeParams<CAP>& p, uint8_t* smem, int u) {
+__device__ __noinline__ void merge(const F8DecodeParams<CAP>& p, uint8_t* smem, int u, int nth) {
   const int tid = threadIdx.x - kOutWarp * 32, g = u % kHkv;
   const long long u0 = static_cast<long long>(u) * p.T;
   const int c0 = cta_of_tile(u0, p.W, gridDim.x), np = cta_of_tile(u0 + p.T - 1, p.W, gridDim.x) - c0 + 1;
@@ -602,7 +645,10 @@ __device__ __noinline__ void merge(const F8DecodeParams<CAP>& p, uint8_t* smem, 
   __nv_bfloat16* o = p.layer[u / kHkv].out + static_cast<size_t>(kRepText * g) * kD + tid;
 #pragma unroll
   for (int h = 0; h < kRepText; ++h) o[h * kD] = __float2bfloat16_rn(acc[h]);
-  if (tid == 0) p.unit_cnt[u] = 0u;  // every part has arrived: ready for the next call
+  if (tid == 0) {
+    p.unit_cnt[u] = 0u;  // every part has arrived: ready for the next call
+    if (p.layer[u / kHkv].w_out != nullptr) reinterpret_cast<int*>(smem + SM_TODO)[nth] = u;  // (read in kForm)
+  }
 }
 
 // What the output warps do before there is any output: the first segment's new rows, and the second segment's Q (its unit is the next one).
@@ -616,8 +662,73 @@ __device__ __noinline__ void early(const F8DecodeParams<CAP>& p, uint32_t sbase,
   if (threadIdx.x == kOutWarp * 32) mbar_arrive(sbase + SM_BAR + 8 * (B_QFULL + 1));
 }
 
-template <int CAP>
-__device__ __forceinline__ bool output(const F8DecodeParams<CAP>& p, uint32_t sbase, uint8_t* smem, uint32_t tmem, long long start, long long end) {
+__device__ __forceinline__ float4 as_float4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return make_float4(__uint_as_float(a), __uint_as_float(b), __uint_as_float(c), __uint_as_float(d));
+}
+// The sum of a key's eight softmax weights.
+__device__ __forceinline__ float weight_of(const float4& a, const float4& b, const float4& la, const float4& lb) {
+  return ((ex2_approx(a.x - la.x) + ex2_approx(a.y - la.y)) + (ex2_approx(a.z - la.z) + ex2_approx(a.w - la.w))) +
+         ((ex2_approx(b.x - lb.x) + ex2_approx(b.y - lb.y)) + (ex2_approx(b.z - lb.z) + ex2_approx(b.w - lb.w)));
+}
+// What the weights of a unit are formed with (the kernel's parameters are too far away to be looked up at every step).
+struct WeighUnit {
+  float lse[kRepText];
+  const float* w_in;
+  float* w_out;
+};
+// Its next tile's place in tensor memory, and that tile's first key.
+struct Weighing {
+  uint32_t slot;
+  int key;
+};
+// A key's sums so far, of the kWeigh tiles from its own on (0 for the new row's, and behind it), on their way to the thread's words of
+// shared memory: no register waits for them, which a call's return would do.
+__device__ __forceinline__ void fetch_sums(const float* w_in, uint32_t sums, int key, int pos) {
+#pragma unroll
+  for (int i = 0; i < kWeigh; ++i) {
+    const int k = key + i * kKeyTile;
+    if (w_in == nullptr || k >= pos) {
+      st_shared_f32(sums + i * kKeyTile * 4, 0.f);
+    } else {
+      cp_async4(sums + i * kKeyTile * 4, w_in + k);
+    }
+  }
+}
+// Weights of kWeigh tiles: cols is where tensor memory holds scores (what lies behind the last tile is not used), key the calling
+// thread's.
+__device__ __noinline__ void weigh(const uint8_t* smem, uint32_t cols, uint32_t slot, uint32_t sums, int key, int pos) {
+  const WeighUnit& unit = *reinterpret_cast<const WeighUnit*>(smem + SM_UNIT);
+  uint32_t x[kWeigh][8];
+#pragma unroll
+  for (int i = 0; i < kWeigh; ++i) {
+    tmem_ld8(cols + 8 * slot, x[i]);
+    slot = slot + 1 == kKept ? 0u : slot + 1;
+  }
+  const float4 la = *reinterpret_cast<const float4*>(unit.lse), lb = *reinterpret_cast<const float4*>(unit.lse + 4);
+  const float* w_in = unit.w_in;
+  float* w_out = unit.w_out;
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < kWeigh; ++i) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) asm volatile("" : "+r"(x[i][e])::"memory");  // (not before the wait)
+    const int k = key + i * kKeyTile;
+    if (k <= pos)
+      w_out[k] = ld_shared_f32(sums + i * kKeyTile * 4) +
+                 weight_of(as_float4(x[i][0], x[i][1], x[i][2], x[i][3]), as_float4(x[i][4], x[i][5], x[i][6], x[i][7]), la, lb);
+  }
+  fetch_sums(w_in, sums, key + kWeigh * kKeyTile, pos);
+}
+__device__ __forceinline__ void weigh_on(Weighing& w, const uint8_t* smem, uint32_t cols, uint32_t sbase, int tid, int pos) {
+  weigh(smem, cols, w.slot, sbase + SM_SUMS + 4 * tid, w.key + tid, pos);
+  w.key += kWeigh * kKeyTile;
+  w.slot = w.slot + kWeigh >= kKept ? w.slot + kWeigh - kKept : w.slot + kWeigh;
+}
+
+template <int kMode, int CAP>
+__device__ __forceinline__ bool output_segments(const F8DecodeParams<CAP>& p, uint32_t sbase, uint8_t* smem, uint32_t tmem, long long start, long long end,
+                                                Weighing& weighing) {
   const int tid = threadIdx.x - kOutWarp * 32, warp = tid >> 5;  // channel = TMEM lane
   const uint32_t o_cols = tmem + (static_cast<uint32_t>(warp * 32) << 16) + TM_O, bar0 = sbase + SM_BAR;
   volatile uint32_t* merge_flag = reinterpret_cast<volatile uint32_t*>(smem + SM_MERGE);
@@ -632,6 +743,8 @@ __device__ __forceinline__ bool output(const F8DecodeParams<CAP>& p, uint32_t sb
     if (seg == 0) early(p, sbase, smem, s.u, s.j1 == p.T, t < end, warp);
     const int last = s.j1 == p.T ? p.T - 1 : s.j1;  // the tile whose scale the appending warp hands over
     float v_next = s.j0 < last ? vs[s.j0] : 0.f;
+    if (kMode == kForm && tid == 0 && s.j0 == 0 && L.w_out != nullptr && L.w_in != nullptr)  // they are needed soon
+      prefetch_l2_bulk(L.w_in + static_cast<size_t>(g) * p.Smax, p.T * kKeyTile * 4);
     float acc[kRepText];
 #pragma unroll
     for (int h = 0; h < kRepText; ++h) acc[h] = 0.f;
@@ -659,6 +772,7 @@ __device__ __forceinline__ bool output(const F8DecodeParams<CAP>& p, uint32_t sb
         acc[h] = fmaf(acc[h], f[h / 2].x, fmaf(__uint_as_float(d[8 + h]), 0x1p-5f, __uint_as_float(d[h])) * (f[h / 2].y * vf));
         acc[h + 1] = fmaf(acc[h + 1], f[h / 2].z, fmaf(__uint_as_float(d[9 + h]), 0x1p-5f, __uint_as_float(d[h + 1])) * (f[h / 2].w * vf));
       }
+      if (kMode == kForm && weighing.key <= p.pos) weigh_on(weighing, smem, o_cols + TM_X - TM_O, sbase, tid, p.pos);
     }
     tails += s.j1 == p.T ? 1 : 0;
     // ---- the segment's end: its sums, then its output or its part of one
@@ -668,7 +782,23 @@ __device__ __forceinline__ bool output(const F8DecodeParams<CAP>& p, uint32_t sb
       __nv_bfloat16* o = L.out + static_cast<size_t>(kRepText * g) * kD + tid;
 #pragma unroll
       for (int h = 0; h < kRepText; ++h) o[h * kD] = __float2bfloat16_rn(__fdividef(acc[h], fin[h].y));
-      if (p.scores != nullptr && tid < kRepText) p.lse[s.u * kRepText + tid] = fin[tid].x + log2f(fin[tid].y);
+      if (kMode != kNoWeights && L.w_out != nullptr) {
+        if (kMode == kScores) {
+          if (tid < kRepText) p.lse[s.u * kRepText + tid] = fin[tid].x + log2f(fin[tid].y);
+        } else {  // (the unit before's are all formed: it had no more tiles than this one)
+          WeighUnit& unit = *reinterpret_cast<WeighUnit*>(smem + SM_UNIT);
+          const float* w_in = L.w_in != nullptr ? L.w_in + static_cast<size_t>(g) * p.Smax : nullptr;
+          if (tid < kRepText) unit.lse[tid] = fin[tid].x + log2f(fin[tid].y);
+          if (tid == 0) {
+            unit.w_in = w_in;
+            unit.w_out = L.w_out + static_cast<size_t>(g) * p.Smax;
+          }
+          weighing.slot = (n - p.T) % kKept;
+          weighing.key = 0;
+          fetch_sums(w_in, sbase + SM_SUMS + 4 * tid, tid, p.pos);
+          tc_fence_after();
+        }
+      }
       continue;
     }
     // Part index: 2 c + slot (a part is its CTA's first segment or its last). Layout [part][channel][8 heads].
@@ -686,23 +816,61 @@ __device__ __forceinline__ bool output(const F8DecodeParams<CAP>& p, uint32_t sb
     if (late >= 0) break;  // (SM_MERGE is the other part's until it has been read)
     if (tid == 0) *merge_flag = count_part(p, s.u) ? 1u : 0u;
     bar_sync(3, kGroup);
-    if (*merge_flag) merge(p, smem, s.u);
+    if (*merge_flag) merge(p, smem, s.u, 0);
     return true;
   }
   if (late < 0) return true;
   if (!bar_sync_and(3, kGroup, wait(B_LATE, 0))) return false;
-  if (*merge_flag) merge(p, smem, late);
+  if (*merge_flag) merge(p, smem, late, 0);
   if (s.j1 == p.T || s.u == late) return true;  // (a CTA's last segment is a part unless it ends its unit)
   bar_sync(3, kGroup);
   if (tid == 0) *merge_flag = count_part(p, s.u) ? 1u : 0u;
   bar_sync(3, kGroup);
-  if (*merge_flag) merge(p, smem, s.u);
+  if (*merge_flag) merge(p, smem, s.u, 1);
+  return true;
+}
+// The whole CTA: the weights of a unit that it has merged, from the parts' scores in the workspace.
+template <int CAP>
+__device__ __noinline__ void weigh_merged(const F8DecodeParams<CAP>& p, int u) {
+  constexpr int kBatch = (kF8KeptTiles * kKeyTile + kThreads - 1) / kThreads;  // all keys' loads are under way together
+  const F8AttnLayer& L = p.layer[u / kHkv];
+  const size_t half = static_cast<size_t>(p.T) * kKeyTile, at = static_cast<size_t>(u % kHkv) * p.Smax;
+  const float4* x = reinterpret_cast<const float4*>(p.scores) + 2 * u * half;
+  const float4* lse = reinterpret_cast<const float4*>(p.lse + u * kRepText);
+  const float4 la = __ldcg(lse), lb = __ldcg(lse + 1);
+  float4 a[kBatch], b[kBatch];
+  float w[kBatch];
+#pragma unroll
+  for (int i = 0; i < kBatch; ++i) {
+    const int k = threadIdx.x + i * kThreads;
+    w[i] = 0.f;
+    if (k <= p.pos) {
+      a[i] = __ldcg(x + k);
+      b[i] = __ldcg(x + half + k);
+      if (k < p.pos && L.w_in != nullptr) w[i] = L.w_in[at + k];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kBatch; ++i) {
+    const int k = threadIdx.x + i * kThreads;
+    if (k <= p.pos) L.w_out[at + k] = w[i] + weight_of(a[i], b[i], la, lb);
+  }
+}
+template <int kMode, int CAP>
+__device__ __forceinline__ bool output(const F8DecodeParams<CAP>& p, uint32_t sbase, uint8_t* smem, uint32_t tmem, long long start, long long end) {
+  const int tid = threadIdx.x - kOutWarp * 32;
+  Weighing weighing;
+  weighing.key = p.pos + 1;  // nothing yet
+  if (!output_segments<kMode>(p, sbase, smem, tmem, start, end, weighing)) return false;
+  if (kMode != kForm) return true;
+  bar_sync(3, kGroup);  // (the log2-sum-exps are there)
+  while (weighing.key <= p.pos) weigh_on(weighing, smem, tmem + (static_cast<uint32_t>((tid >> 5) * 32) << 16) + TM_X, sbase, tid, p.pos);
   return true;
 }
 
 }  // namespace f8d
 
-template <int CAP>
+template <int CAP, int kMode>
 __global__ void __launch_bounds__(f8d::kThreads, 1) fp8_decode_kernel(const __grid_constant__ F8DecodeParams<CAP> p) {
   using namespace f8d;
   extern __shared__ uint8_t smem_raw[];
@@ -715,6 +883,7 @@ __global__ void __launch_bounds__(f8d::kThreads, 1) fp8_decode_kernel(const __gr
     mbar_init(bar0 + 8 * b, (b >= B_PFULL && b < B_PFULL + 2) || (b >= B_FAC && b < B_FIN + 8) ? 2 : 1);
     fence_mbar_init();
   }
+  if (threadIdx.x < 2) reinterpret_cast<int*>(smem + SM_TODO)[threadIdx.x] = -1;
   if (threadIdx.x < kD / 2) reinterpret_cast<float4*>(smem + SM_ROT)[threadIdx.x] = p.rot[threadIdx.x];
   if (warp == 0) {
     tmem_alloc(sbase + SM_TMEM, kTmemCols);
@@ -743,9 +912,9 @@ __global__ void __launch_bounds__(f8d::kThreads, 1) fp8_decode_kernel(const __gr
   pdl_wait_primary();
   bool ok = true;
   if (warp < kOutWarp) {
-    ok = softmax(p, sbase, smem, tmem, warp >> 2, start, end);
+    ok = softmax<kMode>(p, sbase, smem, tmem, warp >> 2, start, end);
   } else if (warp < kOutWarp + 4) {
-    ok = output(p, sbase, smem, tmem, start, end);
+    ok = output<kMode>(p, sbase, smem, tmem, start, end);
   } else if (warp == 12) {
     ok = producer(p, sbase, start, end);
   } else if (warp == 13) {
@@ -760,6 +929,12 @@ __global__ void __launch_bounds__(f8d::kThreads, 1) fp8_decode_kernel(const __gr
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (kMode == kForm)
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+      const int u = reinterpret_cast<const int*>(smem + SM_TODO)[i];
+      if (u >= 0) weigh_merged(p, u);
+    }
   if (warp == 0) tmem_dealloc(tmem, kTmemCols);
 }
 
@@ -790,17 +965,19 @@ __global__ void __launch_bounds__(kWThreads) fp8_weights_kernel(const __grid_con
 #pragma unroll
   for (int i = 0; i < kWKeys; ++i)
     if (key0 + i * kWThreads <= p.pos)
-      L.w_out[at + i * kWThreads] =
-          w[i] + (((ex2_approx(a[i].x - c.x) + ex2_approx(a[i].y - c.y)) + (ex2_approx(a[i].z - c.z) + ex2_approx(a[i].w - c.w))) +
-                  ((ex2_approx(b[i].x - d.x) + ex2_approx(b[i].y - d.y)) + (ex2_approx(b[i].z - d.z) + ex2_approx(b[i].w - d.w))));
+      L.w_out[at + i * kWThreads] = w[i] + f8d::weight_of(a[i], b[i], c, d);
 }
 
 cudaError_t fp8_decode_set_attributes() {
-  cudaError_t e = cudaFuncSetAttribute(fp8_decode_kernel<kSmallCap>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(f8d::kSmemBytes));
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(fp8_decode_kernel<kDecodeMaxLayers>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(f8d::kSmemBytes));
+  cudaError_t e = cudaSuccess;
+  auto set = [&](auto kernel) {
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(f8d::kSmemBytes));
+  };
+  set(fp8_decode_kernel<kSmallCap, f8d::kNoWeights>);
+  set(fp8_decode_kernel<kSmallCap, f8d::kScores>);
+  set(fp8_decode_kernel<kDecodeMaxLayers, f8d::kNoWeights>);
+  set(fp8_decode_kernel<kDecodeMaxLayers, f8d::kScores>);
+  set(fp8_decode_kernel<kDecodeMaxLayers, f8d::kForm>);
   return e;
 }
 
@@ -809,7 +986,10 @@ cudaError_t launch_fp8_decode(const F8DecodeParams<CAP>& p, cudaLaunchConfig_t c
   if (p.n_layers * kHkv / static_cast<int>(cfg.gridDim.x) + 2 > f8d::kTails) return cudaErrorInvalidConfiguration;  // (a GPU of 7 SMs)
   cfg.blockDim = dim3(f8d::kThreads);
   cfg.dynamicSmemBytes = f8d::kSmemBytes;
-  return cudaLaunchKernelEx(&cfg, fp8_decode_kernel<CAP>, p);
+  if (p.scores == nullptr) return cudaLaunchKernelEx(&cfg, fp8_decode_kernel<CAP, f8d::kNoWeights>, p);
+  if constexpr (CAP == kDecodeMaxLayers)
+    if (p.form) return cudaLaunchKernelEx(&cfg, fp8_decode_kernel<CAP, f8d::kForm>, p);
+  return cudaLaunchKernelEx(&cfg, fp8_decode_kernel<CAP, f8d::kScores>, p);
 }
 template cudaError_t launch_fp8_decode<kSmallCap>(const F8DecodeParams<kSmallCap>&, cudaLaunchConfig_t);
 template cudaError_t launch_fp8_decode<kDecodeMaxLayers>(const F8DecodeParams<kDecodeMaxLayers>&, cudaLaunchConfig_t);

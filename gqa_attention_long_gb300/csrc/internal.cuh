@@ -381,11 +381,12 @@ struct F8DecodeParams {
   float* part_ml;      // [n_ctas][2 slots][8 heads][2]: reference (log2 units) and sum
   uint32_t* unit_cnt;  // [unit]: parts that have written their partial (zero between calls)
   uint32_t* status;
-  float* scores;       // [unit][heads 0-3, 4-7][128 T][4]: every key's scores in log2 units, if a layer's weights are asked for (else null)
+  float* scores;       // [unit][heads 0-3, 4-7][128 T][4]: the keys' scores in log2 units, if a layer's weights are asked for (else null)
   float* lse;          // [unit][8]: the heads' log2-sum-exp
   long long W;         // key tiles: n_layers * 8 * T
   int T;               // key tiles per unit: pos / 128 + 1
   int pos, Smax, n_layers;
+  int form;            // the kernel forms the weights that are asked for (more than kSmallCap layers only)
   float scale_log2;    // log2(e) / sqrt(128)
 };
 // The same step for little work (fp8_decode_small.cu), and the weights from either's scores (fp8_decode.cu).
@@ -409,6 +410,8 @@ struct F8WeightsParams {
   const float* lse;
   int T, pos, Smax, n_layers;
 };
+// Up to so many key tiles to a unit fp8_decode_kernel forms the weights itself.
+constexpr int kF8KeptTiles = 39;
 // Workspace: [0, 1024) status word; unit counters and log2-sum-exps of 64 layers, whatever the call's number; partials of at
 // most max_ctas CTAs; scores, for a call that asks for weights.
 struct F8DecodeWs {

@@ -111,7 +111,14 @@ def test_weights_are_formed_only_if_asked_for(h):
     n = h.fake_fp8_weights()
     assert decode(h, 3, weights=False) == OK and h.fake_fp8_weights() == n
     assert decode(h, 3) == OK and h.fake_fp8_weights() == n + 1
-    assert decode(h, 70, 4000, 4096) == OK and h.fake_fp8_weights() == n + 3
+    # of 70 layers 64 are one launch, which forms them itself (units of 32 tiles, 3.4 to a CTA), and 6 another
+    assert decode(h, 70, 4000, 4096) == OK and h.fake_fp8_weights() == n + 2
+    # beyond 39 tiles a unit's scores do not stay where they are
+    assert decode(h, 64, 39 * 128 - 1, 8192) == OK and h.fake_fp8_weights() == n + 2
+    assert decode(h, 64, 39 * 128, 8192) == OK and h.fake_fp8_weights() == n + 3
+    # and fewer than one and a half units to a CTA (28 layers on 152 SMs) are mostly cut
+    assert decode(h, 28, 4000, 4096) == OK and h.fake_fp8_weights() == n + 4
+    assert decode(h, 29, 4000, 4096) == OK and h.fake_fp8_weights() == n + 4
 
 
 def test_eviction_stays_in_its_workspace(h):

@@ -379,3 +379,30 @@ def test_many_keys_far_below_one(layers, first):
         assert float((b.out.double() - want).abs().max()) <= (2.0 ** -8 + 2.0 ** -12) * abs(want)
         w = f64(b.weight_out)
         assert np.allclose(w[:, at], 8 * big / (rest + big), rtol=WREL) and np.allclose(w[:, at + 1:n + 1], 8 / (rest + big), rtol=WREL)
+
+
+@pytest.mark.parametrize("layers,pos", [(29, 39 * 128 - 1), (29, 39 * 128), (30, 39 * 128 - 127), (64, 5 * 128 - 1), (64, 1300), (40, 2561),
+                                        (65, 38 * 128 + 77)])
+def test_weights_of_many_layers(layers, pos):
+    """One to three whole units and parts of two more to a CTA, with sums before in place, elsewhere, nowhere, and layers without weights."""
+    Smax = (pos // 128 + 1) * 128 + 128
+    x, h = decode_inputs(11), random_cache(5, Smax, pos)
+    g = torch.Generator(device=DEV).manual_seed(9)
+    base = torch.rand(8, Smax, generator=g, device=DEV)
+    bufs, kinds = [], []
+    for i in range(layers):
+        kind = ("in place", "elsewhere", "nowhere", "elsewhere", "none")[i % 5 if i < layers - 6 else 1]
+        wo = {"in place": base.clone(), "none": None}.get(kind, torch.full_like(base, -7.0))
+        wi = {"in place": wo, "elsewhere": base.clone()}.get(kind)
+        bufs.append(decode_buffers(x, h.device(), wi, wo))
+        kinds.append(kind)
+    ws = ea.alloc_decode_fp8_workspace(layers, Smax, weights=True)
+    ea.text_decode_attention_fp8(bufs, pos, Smax, 3, ws)
+    check_status(ws)
+    r = decode_oracle(x, h, pos, 3)
+    for b, kind in zip(bufs, kinds):
+        same_cache(b.cache, h, signs=False)
+        close(b.out, r["out"])
+        if kind != "none":
+            weights_close(b.weight_out, None if kind == "nowhere" else base, r["weight"], pos)
+            assert torch.equal(b.weight_out[:, pos + 1:], base[:, pos + 1:]) if kind == "in place" else (b.weight_out[:, pos + 1:] == -7.0).all()
