@@ -406,3 +406,33 @@ def test_weights_of_many_layers(layers, pos):
         if kind != "none":
             weights_close(b.weight_out, None if kind == "nowhere" else base, r["weight"], pos)
             assert torch.equal(b.weight_out[:, pos + 1:], base[:, pos + 1:]) if kind == "in place" else (b.weight_out[:, pos + 1:] == -7.0).all()
+
+
+def test_weights_of_many_layers_in_captured_steps():
+    """In place, thirty layers, a captured step replayed four times while another stream has calls of its own: each adds the same weights
+    (four fp32 additions, each off by at most half a step)."""
+    n, pos, Smax = 30, 1400, 1536
+    x, h = decode_inputs(21), random_cache(22, Smax, pos)
+    base = torch.rand(8, Smax, generator=torch.Generator(device=DEV).manual_seed(4), device=DEV)
+    mine, others = ([decode_buffers(x, h.device(), w, w) for w in (base.clone() for _ in range(n))] for _ in range(2))
+    ws, ws2 = (ea.alloc_decode_fp8_workspace(n, Smax, weights=True) for _ in range(2))
+    s, s2, graph = torch.cuda.Stream(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=s):
+        ea.text_decode_attention_fp8(mine, pos, Smax, 0, ws)
+    for _ in range(4):
+        with torch.cuda.stream(s):
+            graph.replay()
+        with torch.cuda.stream(s2):
+            ea.text_decode_attention_fp8(others, pos, Smax, 0, ws2)
+    torch.cuda.synchronize()
+    check_status(ws)
+    check_status(ws2)
+    r = decode_oracle(x, h, pos, 0)
+    want = f64(base)[:, :pos] + 4 * r["weight"][:, :pos]
+    for b in mine + others:
+        close(b.out, r["out"])
+        got = f64(b.weight_out)
+        assert (np.abs(got[:, :pos] - want) <= 4 * WREL * r["weight"][:, :pos] + 4 * 2.0 ** -24 * want).all()
+        assert (np.abs(got[:, pos] - r["weight"][:, pos]) <= WREL * r["weight"][:, pos]).all()
+        assert torch.equal(b.weight_out[:, pos + 1:], base[:, pos + 1:])
