@@ -205,6 +205,10 @@ int launch_decode_t(const ea_decode_fp8_args* a, int n, int pos, int Smax, long 
 // as many free SMs beside one another: 14.9 us, and 8.1).
 constexpr int kSmallTiles = 14, kOnePart = 2, kSmallParts = 32, kSmallCluster = 4;
 
+// Whether fp8_decode_small_kernel forms the weights itself: where a unit's CTAs can tell each other its log2-sum-exps. With a second kernel and without:
+// 1 layer at pos 1000 9.1 and 8.1 us, 4 layers at pos 4700 19.9 and 17.9, 8 layers at pos 1000 11.8 and 10.3, 32 layers at pos 500 21.7 and 19.2.
+bool small_forms(int parts, int T) { return parts <= kSmallCluster && (T + parts - 1) / parts <= kF8SmallKept; }
+
 template <int CAP>
 int launch_small(const ea_decode_fp8_args* a, int n, int pos, int Smax, long long p0, bool weights, uint8_t* ws, const F8DecodeWs& wl,
                  int parts, cudaStream_t st) {
@@ -219,6 +223,7 @@ int launch_small(const ea_decode_fp8_args* a, int n, int pos, int Smax, long lon
   p.T = pos / kKeyTile + 1;
   p.parts = parts;
   p.cluster = parts > 1 && parts <= kSmallCluster;
+  p.form = weights && small_forms(parts, p.T);
   p.pos = pos;
   p.Smax = Smax;
   p.n_layers = n;
@@ -338,7 +343,8 @@ int text_decode_attention_fp8(const ea_decode_fp8_args* layers, int n_layers, in
          : parts > 0 ? launch_small<kDecodeMaxLayers>(layers + l0, n, pos, Smax, p0, weights, ws, wl, parts, st)
          : n <= kSmallCap ? launch_decode_t<kSmallCap>(layers + l0, n, pos, Smax, p0, weights, ws, wl, di.sm_count, st)
                           : launch_decode_t<kDecodeMaxLayers>(layers + l0, n, pos, Smax, p0, weights, ws, wl, di.sm_count, st);
-    if (rc == EA_OK && weights && (parts > 0 || !forms_weights(n, pos, di.sm_count))) rc = launch_weights(layers + l0, n, pos, Smax, ws, wl, st);
+    const bool formed = parts > 0 ? small_forms(parts, pos / kKeyTile + 1) : forms_weights(n, pos, di.sm_count);
+    if (rc == EA_OK && weights && !formed) rc = launch_weights(layers + l0, n, pos, Smax, ws, wl, st);
     if (rc != EA_OK) return rc;
   }
   return EA_OK;

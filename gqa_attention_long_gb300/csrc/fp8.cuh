@@ -125,4 +125,9 @@ __device__ __forceinline__ void f8_norm_rope_pair(const float (&x)[4], const flo
   }
 }
 
+// The sum of a key's eight softmax weights, from its scores and the log2-sum-exps.
+__device__ __forceinline__ float f8_weight(const float4& a, const float4& b, const float4& la, const float4& lb) {
+  return ((ex2_approx(a.x - la.x) + ex2_approx(a.y - la.y)) + (ex2_approx(a.z - la.z) + ex2_approx(a.w - la.w))) +
+         ((ex2_approx(b.x - lb.x) + ex2_approx(b.y - lb.y)) + (ex2_approx(b.z - lb.z) + ex2_approx(b.w - lb.w)));
+}
 }  // namespace ea

@@ -665,11 +665,6 @@ __device__ __noinline__ void early(const F8DecodeParams<CAP>& p, uint32_t sbase,
 __device__ __forceinline__ float4 as_float4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return make_float4(__uint_as_float(a), __uint_as_float(b), __uint_as_float(c), __uint_as_float(d));
 }
-// The sum of a key's eight softmax weights.
-__device__ __forceinline__ float weight_of(const float4& a, const float4& b, const float4& la, const float4& lb) {
-  return ((ex2_approx(a.x - la.x) + ex2_approx(a.y - la.y)) + (ex2_approx(a.z - la.z) + ex2_approx(a.w - la.w))) +
-         ((ex2_approx(b.x - lb.x) + ex2_approx(b.y - lb.y)) + (ex2_approx(b.z - lb.z) + ex2_approx(b.w - lb.w)));
-}
 // What the weights of a unit are formed with (the kernel's parameters are too far away to be looked up at every step).
 struct WeighUnit {
   float lse[kRepText];
@@ -716,7 +711,7 @@ __device__ __noinline__ void weigh(const uint8_t* smem, uint32_t cols, uint32_t 
     const int k = key + i * kKeyTile;
     if (k <= pos)
       w_out[k] = ld_shared_f32(sums + i * kKeyTile * 4) +
-                 weight_of(as_float4(x[i][0], x[i][1], x[i][2], x[i][3]), as_float4(x[i][4], x[i][5], x[i][6], x[i][7]), la, lb);
+                 f8_weight(as_float4(x[i][0], x[i][1], x[i][2], x[i][3]), as_float4(x[i][4], x[i][5], x[i][6], x[i][7]), la, lb);
   }
   fetch_sums(w_in, sums, key + kWeigh * kKeyTile, pos);
 }
@@ -853,7 +848,7 @@ __device__ __noinline__ void weigh_merged(const F8DecodeParams<CAP>& p, int u) {
 #pragma unroll
   for (int i = 0; i < kBatch; ++i) {
     const int k = threadIdx.x + i * kThreads;
-    if (k <= p.pos) L.w_out[at + k] = w[i] + weight_of(a[i], b[i], la, lb);
+    if (k <= p.pos) L.w_out[at + k] = w[i] + f8_weight(a[i], b[i], la, lb);
   }
 }
 template <int kMode, int CAP>
@@ -965,7 +960,7 @@ __global__ void __launch_bounds__(kWThreads) fp8_weights_kernel(const __grid_con
 #pragma unroll
   for (int i = 0; i < kWKeys; ++i)
     if (key0 + i * kWThreads <= p.pos)
-      L.w_out[at + i * kWThreads] = w[i] + f8d::weight_of(a[i], b[i], c, d);
+      L.w_out[at + i * kWThreads] = w[i] + f8_weight(a[i], b[i], c, d);
 }
 
 cudaError_t fp8_decode_set_attributes() {

@@ -9,7 +9,8 @@
 //   V: it holds bytes [16 g, 16 g + 16) of keys 2t, 2t + 1, 2t + 8, 2t + 9 of each sixteen: byte i of two keys is a pair for columns of channel 16 g + i.
 // Scores come out in P's own fragment layout. A CTA has eight warps and whole 128-row blocks of one unit; the block of the new row is moved to a
 // larger scale in the registers of the four warps that hold it. Two to four parts of a unit are a cluster and meet in shared memory; more of
-// them are merged by the last one to finish.
+// them are merged by the last one to finish. Whole units and clusters form the weights that are asked for, too: their keys' scores wait in
+// shared memory until the parts have told each other their log2-sum-exps; else they go to the workspace, for a second kernel.
 //
 // What bounds it: latencies one after the other (launch, the rows' and the codes' loads, the norm and rotation, the merge); 1 layer at pos 300
 // 7.0 us, at pos 4700 (9.6 MB of cache) 9.0 us, 8 layers at pos 1000 9.8 us.
@@ -26,7 +27,7 @@ constexpr int kMaxParts = 32, kMaxCluster = 4;
 struct Smem {
   float4 rot[kD / 2];
   alignas(16) __half q[2][kRepText][kD];  // high and low halves
-  float qf[kRepText];                     // what a head's scores are multiplied by, beside K's scale
+  alignas(16) float qf[kRepText];         // what a head's scores are multiplied by, beside K's scale
   alignas(16) uint8_t fresh[2][kD];       // the new row's codes, K and V
   float scale[2];                         // its block's scale
   float shrink[2];                        // what the block's earlier codes are multiplied by (1: nothing)
@@ -34,8 +35,10 @@ struct Smem {
   uint32_t last;
   float2 part_ml[kRepText];               // this CTA's, read by its cluster
   alignas(16) float part_o[kRepText][kD];
+  alignas(16) float lse[kRepText];        // of the unit, if weights are formed
   alignas(16) float o[kWarps][kRepText][kD];
-};
+};  // then, if weights are formed, the scores of this CTA's keys: [key][8 heads]
+constexpr int kAhead = 4;  // sums before that a thread loads early
 
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -163,7 +166,7 @@ __device__ __forceinline__ void last_codes(Codes& c, Smem& sm, uint8_t* kc, uint
 
 }  // namespace f8s
 
-template <int CAP>
+template <int CAP, bool kForm>
 __global__ void __launch_bounds__(f8s::kThreads, 1) fp8_decode_small_kernel(const __grid_constant__ F8SmallParams<CAP> p) {
   using namespace f8s;
   extern __shared__ __align__(16) uint8_t f8s_smem[];
@@ -188,6 +191,14 @@ __global__ void __launch_bounds__(f8s::kThreads, 1) fp8_decode_small_kernel(cons
   const bool appends = j1 == p.T && warp >= kWarps - 2;  // (the last two warps: K's new row, and V's)
   NewRow fresh;
   if (appends) load_new_row(p, L, g, warp - (kWarps - 2), lane, fresh);
+  const bool form = kForm && L.w_out != nullptr;
+  float* xs = reinterpret_cast<float*>(f8s_smem + sizeof(Smem));
+  const int first = j0 * kKeyTile, keys = min(j1 * kKeyTile, p.pos + 1) - first;  // this CTA's
+  const float* w_in = form && L.w_in != nullptr ? L.w_in + static_cast<size_t>(g) * p.Smax + first : nullptr;
+  auto sum_before = [&](int k) { return w_in != nullptr && k < keys && first + k < p.pos ? w_in[k] : 0.f; };
+  float before[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) before[i] = sum_before(tid + kThreads * i);
   query_row(p, sm, L, g, warp, lane);
   if (appends) new_row(p, sm, L, g, warp - (kWarps - 2), lane, fresh);
   __syncthreads();
@@ -238,7 +249,13 @@ __global__ void __launch_bounds__(f8s::kThreads, 1) fp8_decode_small_kernel(cons
     }
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    if (p.scores != nullptr && L.w_out != nullptr) {
+    if (form) {
+      float* to = xs + (key0 - first + 2 * t) * kRepText + gk;
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) to[(8 * n + e) * kRepText] = x[n][e];
+    } else if (p.scores != nullptr && L.w_out != nullptr) {
       float* to = p.scores + (static_cast<size_t>(2 * u + (gk >> 2)) * p.T * kKeyTile + key0 + 2 * t) * 4 + (gk & 3);
 #pragma unroll
       for (int n = 0; n < 4; ++n)
@@ -325,13 +342,13 @@ __global__ void __launch_bounds__(f8s::kThreads, 1) fp8_decode_small_kernel(cons
     *reinterpret_cast<float4*>(&sm.part_o[h][4 * lane]) = acc;
     if (lane == 0) sm.part_ml[h] = make_float2(M, sum);
     cluster_sync();
-    if (part == 0) {
+    if (part == 0 || form) {
       float4 v[kMaxCluster];
       float2 ml[kMaxCluster];
 #pragma unroll
       for (int k = 0; k < kMaxCluster; ++k)
         if (k < p.parts) {
-          v[k] = ld_shared_cluster_v4(mapa_shared(smem_u32(&sm.part_o[h][4 * lane]), k));
+          v[k] = part == 0 ? ld_shared_cluster_v4(mapa_shared(smem_u32(&sm.part_o[h][4 * lane]), k)) : make_float4(0.f, 0.f, 0.f, 0.f);
           ml[k] = ld_shared_cluster_v2(mapa_shared(smem_u32(&sm.part_ml[h]), k));
         }
 #pragma unroll
@@ -350,8 +367,8 @@ __global__ void __launch_bounds__(f8s::kThreads, 1) fp8_decode_small_kernel(cons
           acc.w = fmaf(v[k].w, f, acc.w);
         }
     }
-    cluster_sync_exit();  // no CTA leaves while the first one reads its shared memory
-    if (part != 0) return;
+    cluster_sync_exit();  // no CTA leaves while another one reads its shared memory
+    if (part != 0 && !form) return;
   } else if (p.parts > 1) {
     const size_t ps = static_cast<size_t>(blockIdx.x) * kRepText + h;
     __stcg(reinterpret_cast<float4*>(p.part_o + ps * kD) + lane, acc);
@@ -389,16 +406,38 @@ __global__ void __launch_bounds__(f8s::kThreads, 1) fp8_decode_small_kernel(cons
     }
     if (tid == 0) p.unit_cnt[u] = 0u;  // ready for the next call
   }
+  if (form) {
+    if (lane == 0) sm.lse[h] = M + log2f(sum);
+    __syncthreads();
+    const float4 la = *reinterpret_cast<const float4*>(sm.lse), lb = *reinterpret_cast<const float4*>(sm.lse + 4);
+    float* w_out = L.w_out + static_cast<size_t>(g) * p.Smax + first;
+    auto put = [&](int k, float w) {
+      const float4 a = *reinterpret_cast<const float4*>(xs + k * kRepText), b = *reinterpret_cast<const float4*>(xs + k * kRepText + 4);
+      w_out[k] = w + f8_weight(a, b, la, lb);
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (tid + kThreads * i < keys) put(tid + kThreads * i, before[i]);
+    for (int k = tid + kThreads * kAhead; k < keys; k += kThreads) put(k, sum_before(k));
+    if (p.cluster && part != 0) return;
+  }
   const float inv = 1.0f / sum;
   *reinterpret_cast<uint2*>(L.out + (kRepText * g + h) * kD + 4 * lane) =
       make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-  if (p.scores != nullptr && lane == 0) p.lse[u * kRepText + h] = M + log2f(sum);
+  if (!form && p.scores != nullptr && lane == 0) p.lse[u * kRepText + h] = M + log2f(sum);
 }
 
 cudaError_t fp8_decode_small_set_attributes() {
-  const int bytes = static_cast<int>(sizeof(f8s::Smem));
-  const cudaError_t e = cudaFuncSetAttribute(fp8_decode_small_kernel<kSmallCap>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  return e != cudaSuccess ? e : cudaFuncSetAttribute(fp8_decode_small_kernel<kDecodeMaxLayers>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  const int bytes = static_cast<int>(sizeof(f8s::Smem)), kept = kF8SmallKept * kKeyTile * kRepText * static_cast<int>(sizeof(float));
+  cudaError_t e = cudaSuccess;
+  auto set = [&](auto kernel, int size) {
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, size);
+  };
+  set(fp8_decode_small_kernel<kSmallCap, false>, bytes);
+  set(fp8_decode_small_kernel<kSmallCap, true>, bytes + kept);
+  set(fp8_decode_small_kernel<kDecodeMaxLayers, false>, bytes);
+  set(fp8_decode_small_kernel<kDecodeMaxLayers, true>, bytes + kept);
+  return e;
 }
 
 template <int CAP>
@@ -413,7 +452,9 @@ cudaError_t launch_fp8_decode_small(const F8SmallParams<CAP>& p, cudaLaunchConfi
   cfg.gridDim = dim3(p.n_layers * kHkv * p.parts);
   cfg.blockDim = dim3(f8s::kThreads);
   cfg.dynamicSmemBytes = sizeof(f8s::Smem);
-  return cudaLaunchKernelEx(&cfg, fp8_decode_small_kernel<CAP>, p);
+  if (!p.form) return cudaLaunchKernelEx(&cfg, fp8_decode_small_kernel<CAP, false>, p);
+  cfg.dynamicSmemBytes += static_cast<size_t>((p.T + p.parts - 1) / p.parts) * kKeyTile * kRepText * sizeof(float);
+  return cudaLaunchKernelEx(&cfg, fp8_decode_small_kernel<CAP, true>, p);
 }
 template cudaError_t launch_fp8_decode_small<kSmallCap>(const F8SmallParams<kSmallCap>&, cudaLaunchConfig_t);
 template cudaError_t launch_fp8_decode_small<kDecodeMaxLayers>(const F8SmallParams<kDecodeMaxLayers>&, cudaLaunchConfig_t);

@@ -402,6 +402,7 @@ struct F8SmallParams {
   int T, parts;        // CTAs to a unit, each with its share of the unit's tiles
   int cluster;         // they are a cluster
   int pos, Smax, n_layers;
+  int form;            // the kernel forms the weights that are asked for: its scores stay in shared memory (parts == 1, or cluster)
   float scale_log2;
 };
 struct F8WeightsParams {
@@ -412,6 +413,8 @@ struct F8WeightsParams {
 };
 // Up to so many key tiles to a unit fp8_decode_kernel forms the weights itself.
 constexpr int kF8KeptTiles = 39;
+// So many tiles to a CTA fp8_decode_small_kernel can keep the scores of.
+constexpr int kF8SmallKept = 40;
 // Workspace: [0, 1024) status word; unit counters and log2-sum-exps of 64 layers, whatever the call's number; partials of at
 // most max_ctas CTAs; scores, for a call that asks for weights.
 struct F8DecodeWs {

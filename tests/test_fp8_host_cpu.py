@@ -109,16 +109,18 @@ def test_parts_of_little_work(h, device, sms):
 def test_weights_are_formed_only_if_asked_for(h):
     h.fake_device(0, -1)
     n = h.fake_fp8_weights()
-    assert decode(h, 3, weights=False) == OK and h.fake_fp8_weights() == n
+    assert decode(h, 1, 4000, 4096, weights=False) == OK and h.fake_fp8_weights() == n
+    # sixteen parts to a unit meet in the workspace, two (three layers, three tiles) in a cluster, which forms the weights itself
+    assert decode(h, 1, 4000, 4096) == OK and h.fake_fp8_weights() == n + 1
     assert decode(h, 3) == OK and h.fake_fp8_weights() == n + 1
-    # of 70 layers 64 are one launch, which forms them itself (units of 32 tiles, 3.4 to a CTA), and 6 another
-    assert decode(h, 70, 4000, 4096) == OK and h.fake_fp8_weights() == n + 2
+    # of 70 layers 64 are one launch, which forms them (units of 32 tiles, 3.4 to a CTA), and 6 another (three parts to a unit)
+    assert decode(h, 70, 4000, 4096) == OK and h.fake_fp8_weights() == n + 1
     # beyond 39 tiles a unit's scores do not stay where they are
-    assert decode(h, 64, 39 * 128 - 1, 8192) == OK and h.fake_fp8_weights() == n + 2
-    assert decode(h, 64, 39 * 128, 8192) == OK and h.fake_fp8_weights() == n + 3
+    assert decode(h, 64, 39 * 128 - 1, 8192) == OK and h.fake_fp8_weights() == n + 1
+    assert decode(h, 64, 39 * 128, 8192) == OK and h.fake_fp8_weights() == n + 2
     # and fewer than one and a half units to a CTA (28 layers on 152 SMs) are mostly cut
-    assert decode(h, 28, 4000, 4096) == OK and h.fake_fp8_weights() == n + 4
-    assert decode(h, 29, 4000, 4096) == OK and h.fake_fp8_weights() == n + 4
+    assert decode(h, 28, 4000, 4096) == OK and h.fake_fp8_weights() == n + 3
+    assert decode(h, 29, 4000, 4096) == OK and h.fake_fp8_weights() == n + 3
 
 
 def test_eviction_stays_in_its_workspace(h):

@@ -436,3 +436,25 @@ def test_weights_of_many_layers_in_captured_steps():
         assert (np.abs(got[:, :pos] - want) <= 4 * WREL * r["weight"][:, :pos] + 4 * 2.0 ** -24 * want).all()
         assert (np.abs(got[:, pos] - r["weight"][:, pos]) <= WREL * r["weight"][:, pos]).all()
         assert torch.equal(b.weight_out[:, pos + 1:], base[:, pos + 1:])
+
+
+@pytest.mark.parametrize("layers,pos", [(5, 700), (5, 127), (5, 128), (20, 200), (12, 1400), (10, 3327), (40, 640)])
+def test_weights_of_a_few_tiles(layers, pos):
+    """Units of one CTA and of a cluster, with sums before in place, elsewhere, nowhere, and layers without weights."""
+    Smax = (pos // 128 + 1) * 128
+    x, h = decode_inputs(31), random_cache(32, Smax, pos)
+    base = torch.rand(8, Smax, generator=torch.Generator(device=DEV).manual_seed(5), device=DEV)
+    bufs, kinds = [], [("in place", "none", "nowhere", "elsewhere", "elsewhere")[i % 5] for i in range(layers)]
+    for kind in kinds:
+        wo = {"in place": base.clone(), "none": None}.get(kind, torch.full_like(base, -7.0))
+        bufs.append(decode_buffers(x, h.device(), {"in place": wo, "elsewhere": base.clone()}.get(kind), wo))
+    ws = ea.alloc_decode_fp8_workspace(layers, Smax, weights=True)
+    ea.text_decode_attention_fp8(bufs, pos, Smax, 0, ws)
+    check_status(ws)
+    r = decode_oracle(x, h, pos, 0)
+    for b, kind in zip(bufs, kinds):
+        same_cache(b.cache, h, signs=False)
+        close(b.out, r["out"])
+        if kind != "none":
+            weights_close(b.weight_out, None if kind == "nowhere" else base, r["weight"], pos)
+            assert torch.equal(b.weight_out[:, pos + 1:], base[:, pos + 1:]) if kind == "in place" else (b.weight_out[:, pos + 1:] == -7.0).all()
