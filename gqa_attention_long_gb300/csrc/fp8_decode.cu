@@ -24,14 +24,15 @@
 // output warps, which have nothing else to do yet). S has four buffers, Q, P and O have two. Five loops run side by side on one scheduler's instruction cache, and fetching
 // was what they waited for most (2.8 of 10 warp cycles an instruction): they are short, and what is rare is out of their way.
 // A unit cut over several CTAs is merged by the part that finishes last; a part that is not its CTA's last segment is counted by warp
-// 15, and merged at the CTA's end should it be the last after all, so that the output warps need not wait.
+// 15, and merged at the CTA's end should it be the last after all, so that the output warps need not wait. A CTA's last part of a unit of
+// two whose other part has come adds that to its registers' sums: 3 us less at the end than through global memory.
 // Weights that are asked for need a unit's scores once more when its log2-sum-exps are known: 32 bytes a key. They go to the workspace, and
 // a second kernel forms the weights; or, where most units are whole ones of one CTA, these stay in tensor memory, whose columns hold 44 tiles'
 // scores beside the accumulators, and the output warps form their weights between the next unit's tiles (64 layers at pos 4700: 120 us, not
 // 132.5); the cut ones' are formed by the CTA that merges them. What that takes is the loads' latency (sums before come through
 // prefetches and asynchronous copies: 10 us less) rather than the arithmetic.
-// Figures (64 layers at pos 4700; 4 layers at pos 131070): 99.5 and 160.5 us, 91.6 % and 98.5 % of the copy's rate; the former's 125 tiles
-// a CTA bear a start and an end of about 8 us.
+// Figures (64 layers at pos 4700; 4 layers at pos 131070): 98 and 160.3 us, 93 % and 98.6 % of the copy's rate; the former's 125 tiles
+// a CTA bear a start and an end of about 6 us.
 #include "fp8.cuh"
 
 namespace ea {
@@ -74,7 +75,8 @@ constexpr int B_KFULL = 0, B_KEMPTY = B_KFULL + kKRing, B_VFULL = B_KEMPTY + kKR
 constexpr uint32_t SM_TMEM = SM_BAR + kNumBars * 8;
 constexpr uint32_t SM_MERGE = SM_TMEM + 4;
 constexpr uint32_t SM_TODO = SM_MERGE + 4;  // [2]: merged units whose weights are still to be formed (or -1)
-constexpr uint32_t kSmemBytes = SM_TODO + 8 + 1024;  // + base alignment
+constexpr uint32_t SM_LASTPART = SM_TODO + 8;  // whether the other part of the unit that the last segment begins is there already
+constexpr uint32_t kSmemBytes = SM_LASTPART + 4 + 1024;  // + base alignment
 static_assert(kSmemBytes <= 232448, "shared memory budget of one sm_103 CTA");
 // 4 and 2 buffers of 32 and 16 columns; then the scores of kKept tiles, 8 columns each
 constexpr uint32_t kTmemCols = 512, TM_S = 0, TM_O = 128, TM_X = 160, kKept = (kTmemCols - TM_X) / 8;
@@ -122,6 +124,11 @@ __device__ __forceinline__ uint32_t atom_add_acq_rel_gpu(uint32_t* a, uint32_t v
   uint32_t old;
   asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;" : "=r"(old) : "l"(a), "r"(v) : "memory");
   return old;
+}
+__device__ __forceinline__ uint32_t ld_acquire_gpu(const uint32_t* a) {
+  uint32_t v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(a) : "memory");
+  return v;
 }
 __device__ __forceinline__ void st_shared_u8(uint32_t a, uint32_t v) {
   asm volatile("st.shared.u8 [%0], %1;" ::"r"(a), "r"(v) : "memory");
@@ -268,20 +275,45 @@ __device__ __forceinline__ bool count_part(const P& p, int u) {
   return atom_add_acq_rel_gpu(p.unit_cnt + u, 1u) == static_cast<uint32_t>(parts - 1);
 }
 
+// Whether segment s, after which t is the next tile, is the first of a unit's two parts and the CTA's last segment, with a Q that warp 15
+// prepares: it then looks whether the other part, which its CTA began with, has arrived. If so nobody else will merge the unit, and this CTA
+// need not write its part, count it and read it again.
+template <class P>
+__device__ __forceinline__ bool last_part(const P& p, const Seg& s, uint32_t seg, long long t, long long end) {
+  return seg > 1 && t >= end && s.j0 == 0 && s.j1 < p.T &&
+         cta_tile_start(blockIdx.x + 2, p.W, gridDim.x) >= static_cast<long long>(s.u + 1) * p.T;
+}
+
 // One warp: the Q and the new rows of every segment but the first.
 template <int CAP>
 __device__ __forceinline__ bool prepare(const F8DecodeParams<CAP>& p, uint32_t sbase, uint8_t* smem, long long start, long long end) {
   const int lane = threadIdx.x & 31;
   const uint32_t bar0 = sbase + SM_BAR;
   uint32_t idx = 0, seg = 0;
+  int first = -1;  // the first segment's unit, if that is a part, and not the last segment: its partial is counted here
   Seg s;
-  for (long long t = start; next_seg(t, end, p.T, s); ++seg) {
+#pragma unroll 1
+  for (long long t = start;; ++seg) {
+    const bool more = next_seg(t, end, p.T, s);
+    if (first >= 0 && (seg > 2 || !more)) {  // (the third segment's Q was prepared when the first one's products were done)
+      const bool ok = counted_wait(bar0 + 8 * B_PART, 0);
+      if (lane == 0) {
+        *reinterpret_cast<volatile uint32_t*>(smem + SM_MERGE) = ok && count_part(p, first) ? 1u : 0u;
+        mbar_arrive(bar0 + 8 * B_LATE);
+      }
+      if (!ok) return false;
+      first = -1;
+    }
+    if (!more) return true;
+    if (seg == 0 && t < end && !(s.j0 == 0 && s.j1 == p.T)) first = s.u;
     if (seg > 0) {
       if (seg > 1) {  // (output warps have the second one's Q)
         const uint32_t buf = seg & 1;
         if (!counted_wait(bar0 + 8 * (B_QFREE + buf), ((seg - 2) >> 1) & 1)) return false;
 #pragma unroll 1
         for (int h = 0; h < kRepText; ++h) prepare_q(p, sbase, smem, s.u, h, seg);
+        if (lane == 0 && last_part(p, s, seg, t, end))
+          *reinterpret_cast<volatile uint32_t*>(smem + SM_LASTPART) = ld_acquire_gpu(p.unit_cnt + s.u);
         __syncwarp();
         if (lane == 0) mbar_arrive(bar0 + 8 * (B_QFULL + buf));
       }
@@ -292,15 +324,6 @@ __device__ __forceinline__ bool prepare(const F8DecodeParams<CAP>& p, uint32_t s
     }
     idx += s.j1 == p.T ? 1 : 0;
   }
-  long long t = start;
-  if (!next_seg(t, end, p.T, s) || t >= end || (s.j0 == 0 && s.j1 == p.T)) return true;
-  // the first segment is a part, and not the last segment: its partial is counted here
-  const bool ok = counted_wait(bar0 + 8 * B_PART, 0);
-  if (lane == 0) {
-    *reinterpret_cast<volatile uint32_t*>(smem + SM_MERGE) = ok && count_part(p, s.u) ? 1u : 0u;
-    mbar_arrive(bar0 + 8 * B_LATE);
-  }
-  return ok;
 }
 
 // ---------------------------------------------------------------- producer and MMA issuers
@@ -651,6 +674,33 @@ __device__ __noinline__ void merge(const F8DecodeParams<CAP>& p, uint8_t* smem, 
   }
 }
 
+// The same for a unit whose second part is there, the first being the calling thread's sums and `fin`. (The roundings are merge()'s, so that
+// results do not depend on when the other part came.)
+template <int CAP>
+__device__ __noinline__ void merge_two(const F8DecodeParams<CAP>& p, uint8_t* smem, int u, const float2* fin, float a0, float a1, float a2, float a3, float a4,
+                                       float a5, float a6, float a7) {
+  const int tid = threadIdx.x - kOutWarp * 32;
+  const size_t ps = static_cast<size_t>(blockIdx.x + 1) * 2;
+  const float4* po = reinterpret_cast<const float4*>(p.part_o + ps * kRepText * kD) + 2 * tid;
+  const float4* pm = reinterpret_cast<const float4*>(p.part_ml + ps * kRepText * 2);
+  const float4 o0 = __ldcg(po), o1 = __ldcg(po + 1), m[4] = {__ldcg(pm), __ldcg(pm + 1), __ldcg(pm + 2), __ldcg(pm + 3)};
+  const float acc[kRepText] = {a0, a1, a2, a3, a4, a5, a6, a7}, other[kRepText] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
+  const F8AttnLayer& L = p.layer[u / kHkv];
+  __nv_bfloat16* out = L.out + static_cast<size_t>(kRepText * (u % kHkv)) * kD + tid;
+#pragma unroll
+  for (int h = 0; h < kRepText; ++h) {
+    const float2 a = fin[h], b = h & 1 ? make_float2(m[h / 2].z, m[h / 2].w) : make_float2(m[h / 2].x, m[h / 2].y);
+    const float M = fmaxf(a.x, b.x), wa = ex2_approx(a.x - M), wb = ex2_approx(b.x - M);
+    const float sum = __fadd_rn(__fmul_rn(a.y, wa), __fmul_rn(b.y, wb)), inv = 1.0f / sum;
+    out[h * kD] = __float2bfloat16_rn(fmaf(wb * inv, other[h], __fmul_rn(wa * inv, acc[h])));
+    if (p.scores != nullptr && tid == h) p.lse[u * kRepText + h] = M + log2f(sum);
+  }
+  if (tid == 0) {
+    p.unit_cnt[u] = 0u;
+    if (L.w_out != nullptr) reinterpret_cast<int*>(smem + SM_TODO)[1] = u;  // (read in kForm)
+  }
+}
+
 // What the output warps do before there is any output: the first segment's new rows, and the second segment's Q (its unit is the next one).
 template <int CAP>
 __device__ __noinline__ void early(const F8DecodeParams<CAP>& p, uint32_t sbase, uint8_t* smem, int u, bool tail, bool more, int warp) {
@@ -796,6 +846,13 @@ __device__ __forceinline__ bool output_segments(const F8DecodeParams<CAP>& p, ui
       }
       continue;
     }
+    if (last_part(p, s, seg, t, end) && wait(B_QFULL + (seg & 1), (seg >> 1) & 1) &&
+        *reinterpret_cast<volatile uint32_t*>(smem + SM_LASTPART) == 1u) {
+      merge_two(p, smem, s.u, fin, acc[0], acc[1], acc[2], acc[3], acc[4], acc[5], acc[6], acc[7]);
+      if (late < 0) return true;
+      s.u = late;  // (nothing more to count)
+      break;
+    }
     // Part index: 2 c + slot (a part is its CTA's first segment or its last). Layout [part][channel][8 heads].
     const size_t ps = static_cast<size_t>(blockIdx.x) * 2 + (seg == 0 ? 0 : 1);
     float4* po = reinterpret_cast<float4*>(p.part_o + ps * kRepText * kD) + 2 * tid;
@@ -878,7 +935,7 @@ __global__ void __launch_bounds__(f8d::kThreads, 1) fp8_decode_kernel(const __gr
     mbar_init(bar0 + 8 * b, (b >= B_PFULL && b < B_PFULL + 2) || (b >= B_FAC && b < B_FIN + 8) ? 2 : 1);
     fence_mbar_init();
   }
-  if (threadIdx.x < 2) reinterpret_cast<int*>(smem + SM_TODO)[threadIdx.x] = -1;
+  if (threadIdx.x < 3) reinterpret_cast<int*>(smem + SM_TODO)[threadIdx.x] = threadIdx.x < 2 ? -1 : 0;  // (and SM_LASTPART)
   if (threadIdx.x < kD / 2) reinterpret_cast<float4*>(smem + SM_ROT)[threadIdx.x] = p.rot[threadIdx.x];
   if (warp == 0) {
     tmem_alloc(sbase + SM_TMEM, kTmemCols);
@@ -905,19 +962,20 @@ __global__ void __launch_bounds__(f8d::kThreads, 1) fp8_decode_kernel(const __gr
   }
   // everything below reads what earlier kernels in the stream wrote
   pdl_wait_primary();
+  // (the roles' order is the code's, and matters to the instruction caches: 64 layers at pos 4700 97.9 us with softmax last, 99.4 with it first)
   bool ok = true;
-  if (warp < kOutWarp) {
-    ok = softmax<kMode>(p, sbase, smem, tmem, warp >> 2, start, end);
-  } else if (warp < kOutWarp + 4) {
-    ok = output<kMode>(p, sbase, smem, tmem, start, end);
+  if (warp == 15) {
+    ok = prepare(p, sbase, smem, start, end);
   } else if (warp == 12) {
     ok = producer(p, sbase, start, end);
   } else if (warp == 13) {
     ok = qk_issuer(p, sbase, tmem, start, end);
   } else if (warp == 14) {
     ok = pv_issuer(p, sbase, tmem, static_cast<uint32_t>(end - start));
-  } else {
-    ok = prepare(p, sbase, smem, start, end);
+  } else if (warp >= kOutWarp && warp < kOutWarp + 4) {
+    ok = output<kMode>(p, sbase, smem, tmem, start, end);
+  } else if (warp < kOutWarp) {
+    ok = softmax<kMode>(p, sbase, smem, tmem, warp >> 2, start, end);
   }
   if (!ok && (threadIdx.x & 31) == 0) atomicOr(p.status, kErrF8DecodeWait);
   pdl_launch_dependents();
