@@ -28,10 +28,10 @@
 // two whose other part has come adds that to its registers' sums: 3 us less at the end than through global memory.
 // Weights that are asked for need a unit's scores once more when its log2-sum-exps are known: 32 bytes a key. They go to the workspace, and
 // a second kernel forms the weights; or, where most units are whole ones of one CTA, these stay in tensor memory, whose columns hold 44 tiles'
-// scores beside the accumulators, and the output warps form their weights between the next unit's tiles (64 layers at pos 4700: 120 us, not
+// scores beside the accumulators, and the output warps form their weights between the next unit's tiles (64 layers at pos 4700: 118 us, not
 // 132.5); the cut ones' are formed by the CTA that merges them. What that takes is the loads' latency (sums before come through
 // prefetches and asynchronous copies: 10 us less) rather than the arithmetic.
-// Figures (64 layers at pos 4700; 4 layers at pos 131070): 98 and 160.3 us, 93 % and 98.6 % of the copy's rate; the former's 125 tiles
+// Figures (64 layers at pos 4700; 4 layers at pos 131070): 98.2 and 161 us, 93 % and 98 % of the copy's rate; the former's 125 tiles
 // a CTA bear a start and an end of about 6 us.
 #include "fp8.cuh"
 
@@ -240,28 +240,35 @@ __device__ __noinline__ void append_row(const F8DecodeParams<CAP>& p, uint32_t s
   }
 }
 
-// q row h of segment seg's unit, as pieces, into its Q buffer: one warp.
+// q rows [h, h1) of segment seg's unit, as pieces, into its Q buffer: one warp, which loads a row ahead (64 layers at pos 1000, whose units are
+// eight tiles: 42.3 -> 39.6 us).
 template <int CAP>
-__device__ __noinline__ void prepare_q(const F8DecodeParams<CAP>& p, uint32_t sbase, uint8_t* smem, int u, int h, uint32_t seg) {
+__device__ __noinline__ void prepare_q(const F8DecodeParams<CAP>& p, uint32_t sbase, uint8_t* smem, int u, int h, int h1, uint32_t seg) {
   const int lane = threadIdx.x & 31;
   const F8AttnLayer& L = p.layer[u / kHkv];
-  float x[4], gm[4], y[4];
+  const __nv_bfloat16* q = L.q_raw + kRepText * (u % kHkv) * kD;
+  float next[4], gm[4];
   f8_load_row(L.q_gamma, lane, gm);
-  f8_load_row(L.q_raw + (kRepText * (u % kHkv) + h) * kD, lane, x);
-  f8_norm_rope(x, gm, reinterpret_cast<const float4*>(smem + SM_ROT), lane, y);
-  const int e = f16_exponent(f8_row_max(y));  // the row's largest magnitude is in [2^e, 2^(e + 1)): put it in [128, 256)
-  const float up = f8_pow2(min(7 - e, 126));
+  f8_load_row(q + h * kD, lane, next);
+#pragma unroll 1
+  for (; h < h1; ++h) {
+    float x[4] = {next[0], next[1], next[2], next[3]}, y[4];
+    if (h + 1 < h1) f8_load_row(q + (h + 1) * kD, lane, next);
+    f8_norm_rope(x, gm, reinterpret_cast<const float4*>(smem + SM_ROT), lane, y);
+    const int e = f16_exponent(f8_row_max(y));  // the row's largest magnitude is in [2^e, 2^(e + 1)): put it in [128, 256)
+    const float up = f8_pow2(min(7 - e, 126));
 #pragma unroll
-  for (int i = 0; i < 4; ++i) y[i] *= up;
-  if (lane == 0) reinterpret_cast<float*>(smem + SM_QF)[(seg & 7) * kRepText + h] = p.scale_log2 * f8_pow2(max(e - 7, -126));  // over up
-  // 16-byte chunk c of row r at chunk c ^ (r % 8)
-  const uint32_t r0 = (h >> 2) * 16 + (h & 3), c = lane >> 3;
-  uint32_t row = sbase + SM_QT + (seg & 1) * kOpBytes + r0 * 128 + ((2 * lane) & 15);
+    for (int i = 0; i < 4; ++i) y[i] *= up;
+    if (lane == 0) reinterpret_cast<float*>(smem + SM_QF)[(seg & 7) * kRepText + h] = p.scale_log2 * f8_pow2(max(e - 7, -126));  // over up
+    // 16-byte chunk c of row r at chunk c ^ (r % 8)
+    const uint32_t r0 = (h >> 2) * 16 + (h & 3), c = lane >> 3;
+    uint32_t row = sbase + SM_QT + (seg & 1) * kOpBytes + r0 * 128 + ((2 * lane) & 15);
 #pragma unroll
-  for (int piece = 0; piece < 4; ++piece, row += 4 * 128) {
-    const uint32_t r = (r0 + 4 * piece) & 7, lo = take_piece(y[0], y[1]), hi = take_piece(y[2], y[3]);
-    st_shared_u16(row + ((c ^ r) << 4), static_cast<uint16_t>(lo));
-    st_shared_u16(row + (((c + 4) ^ r) << 4), static_cast<uint16_t>(hi));
+    for (int piece = 0; piece < 4; ++piece, row += 4 * 128) {
+      const uint32_t r = (r0 + 4 * piece) & 7, lo = take_piece(y[0], y[1]), hi = take_piece(y[2], y[3]);
+      st_shared_u16(row + ((c ^ r) << 4), static_cast<uint16_t>(lo));
+      st_shared_u16(row + (((c + 4) ^ r) << 4), static_cast<uint16_t>(hi));
+    }
   }
   fence_proxy_async_smem();  // read by the tensor core
 }
@@ -310,8 +317,7 @@ __device__ __forceinline__ bool prepare(const F8DecodeParams<CAP>& p, uint32_t s
       if (seg > 1) {  // (output warps have the second one's Q)
         const uint32_t buf = seg & 1;
         if (!counted_wait(bar0 + 8 * (B_QFREE + buf), ((seg - 2) >> 1) & 1)) return false;
-#pragma unroll 1
-        for (int h = 0; h < kRepText; ++h) prepare_q(p, sbase, smem, s.u, h, seg);
+        prepare_q(p, sbase, smem, s.u, 0, kRepText, seg);
         if (lane == 0 && last_part(p, s, seg, t, end))
           *reinterpret_cast<volatile uint32_t*>(smem + SM_LASTPART) = ld_acquire_gpu(p.unit_cnt + s.u);
         __syncwarp();
@@ -498,7 +504,7 @@ __device__ __forceinline__ bool softmax(const F8DecodeParams<CAP>& p, uint32_t s
     const int last = s.j1 == p.T ? p.T - 1 : s.j1;  // the tile whose scale the appending warp hands over
     float k_next = s.j0 < last ? ks[s.j0] : 0.f;
     if (seg == 0) {
-      prepare_q(p, sbase, smem, s.u, 4 * set + warp, seg);
+      prepare_q(p, sbase, smem, s.u, 4 * set + warp, 4 * set + warp + 1, seg);
       bar_sync(4, 2 * kGroup);
       if (threadIdx.x == 0) mbar_arrive(bar0 + 8 * B_QFULL);
     }
@@ -706,8 +712,7 @@ template <int CAP>
 __device__ __noinline__ void early(const F8DecodeParams<CAP>& p, uint32_t sbase, uint8_t* smem, int u, bool tail, bool more, int warp) {
   if (tail && warp < 2) append_row(p, sbase, smem, warp, u, 0);
   if (!more) return;
-#pragma unroll 1
-  for (int h = 0; h < 2; ++h) prepare_q(p, sbase, smem, u + 1, 2 * warp + h, 1);
+  prepare_q(p, sbase, smem, u + 1, 2 * warp, 2 * warp + 2, 1);
   bar_sync(3, kGroup);
   if (threadIdx.x == kOutWarp * 32) mbar_arrive(sbase + SM_BAR + 8 * (B_QFULL + 1));
 }
@@ -962,7 +967,7 @@ __global__ void __launch_bounds__(f8d::kThreads, 1) fp8_decode_kernel(const __gr
   }
   // everything below reads what earlier kernels in the stream wrote
   pdl_wait_primary();
-  // (the roles' order is the code's, and matters to the instruction caches: 64 layers at pos 4700 97.9 us with softmax last, 99.4 with it first)
+  // (the roles' order is the code's, and matters to the instruction caches: 64 layers at pos 4700 98.2 us in this one, 98.7 to 100.7 in others)
   bool ok = true;
   if (warp == 15) {
     ok = prepare(p, sbase, smem, start, end);
