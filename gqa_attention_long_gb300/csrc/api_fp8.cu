@@ -198,12 +198,16 @@ int launch_decode_t(const ea_decode_fp8_args* a, int n, int pos, int Smax, long 
   return EA_OK;
 }
 
-// Little work (see fp8_decode_small.cu): at most kSmallTiles key tiles to an SM. Its kernel and the other one: 1 layer at pos 300 7.0 and 10.2 us, at
-// pos 4700 9.1 and 13.4, 4 layers 16.6 and 18.8, 8 layers (15.6 tiles) 26.8 and 24.7; 32 layers at pos 1000 (13.5) 26.6 and 29.4, 64 layers at
-// pos 500 (13.5) 35.9 and 44.3. Up to kOnePart tiles a unit is one CTA's (4 layers at pos 300, three tiles: 7.6 us whole, 7.0 in two parts). Up
+// Little work (see fp8_decode_small.cu): its kernel's CTAs, of `tiles` key tiles each, come in `waves` of one to an SM, and the start and the end of one
+// are about four tiles' time: waves x (kSmallEnds + tiles) <= kSmallWork + waves / 2 (more units take the other
+// kernel longer, too). Its kernel and the other one: 1 layer at pos 300 (1 x (4 + 2)) 6.8 and 10.4 us, at pos
+// 4700 (1 x 6) 9.1 and 13.4; 16 layers at pos 1000 (1 x 12) 13.3 and 18.1, at pos 1500 (1 x 16) 18.0 and 19.1; 5 layers at pos 4700 (1 x 17) 20.1 and 19.7;
+// 32 layers at pos 600 (2 x 9) 21.7 and 22.7; 12 layers at pos 2000 (1 x 20) 21.4 and 18.8; 32 layers at pos 800 (2 x 11) 25.1 and 23.4, 64 layers at pos
+// 100 (4 x 5) 21.1 and 22.5, at pos 380 (4 x 7) 34.3 and 27.3. Up to kOnePart tiles a unit is one CTA's (4 layers at pos 300, three tiles: 7.6 us whole, 7.0 in two parts). Up
 // to kSmallCluster parts are a cluster (1 layer at pos 1000: 7.6 us, 7.9 through global memory; in clusters of eight 2 layers at pos 2000 wait for
-// as many free SMs beside one another: 14.9 us, and 8.1).
-constexpr int kSmallTiles = 14, kOnePart = 2, kSmallParts = 32, kSmallCluster = 4;
+// as many free SMs beside one another: 14.9 us, and 8.1). Clusters of three and four do not fill every SM: 6 layers at pos 600 in 48 clusters of
+// three took 13.4 us, 7 layers in pairs 9.3; from seven eighths of the SMs on they are pairs.
+constexpr int kSmallEnds = 4, kSmallWork = 18, kOnePart = 2, kSmallParts = 32, kSmallCluster = 4;
 
 // Whether fp8_decode_small_kernel forms the weights itself: where a unit's CTAs can tell each other its log2-sum-exps. With a second kernel and without:
 // 1 layer at pos 1000 9.1 and 8.1 us, 4 layers at pos 4700 19.9 and 17.9, 8 layers at pos 1000 11.8 and 10.3, 32 layers at pos 500 21.7 and 19.2.
@@ -257,11 +261,13 @@ int launch_weights(const ea_decode_fp8_args* a, int n, int pos, int Smax, uint8_
 // CTA's.
 int small_parts(int n, int pos, int sm_count) {
   const int T = pos / kKeyTile + 1, units = n * kHkv;
-  if (static_cast<long long>(units) * T > static_cast<long long>(kSmallTiles) * sm_count) return 0;
   int parts = sm_count / units;
   if (parts > (T + 1) / 2) parts = (T + 1) / 2;  // (two tiles keep a CTA's eight warps busy)
   if (parts > kSmallParts) parts = kSmallParts;
-  return parts < 1 || T <= kOnePart ? 1 : parts;
+  if (parts > 2 && parts <= kSmallCluster && units * parts > sm_count / 8 * 7) parts = 2;
+  if (parts < 1 || T <= kOnePart) parts = 1;
+  const int waves = (units * parts + sm_count - 1) / sm_count, tiles = (T + parts - 1) / parts;
+  return static_cast<long long>(waves) * (kSmallEnds + tiles) <= kSmallWork + waves / 2 ? parts : 0;
 }
 
 // Whether [a, a + n) and [b, b + n) share bytes without being the same.

@@ -113,8 +113,8 @@ def test_weights_are_formed_only_if_asked_for(h):
     # sixteen parts to a unit meet in the workspace, two (three layers, three tiles) in a cluster, which forms the weights itself
     assert decode(h, 1, 4000, 4096) == OK and h.fake_fp8_weights() == n + 1
     assert decode(h, 3) == OK and h.fake_fp8_weights() == n + 1
-    # of 70 layers 64 are one launch, which forms them (units of 32 tiles, 3.4 to a CTA), and 6 another (three parts to a unit)
-    assert decode(h, 70, 4000, 4096) == OK and h.fake_fp8_weights() == n + 1
+    # of 68 layers 64 are one launch, which forms them (units of 32 tiles, 3.4 to a CTA), and 4 another (four parts to a unit)
+    assert decode(h, 68, 4000, 4096) == OK and h.fake_fp8_weights() == n + 1
     # beyond 39 tiles a unit's scores do not stay where they are
     assert decode(h, 64, 39 * 128 - 1, 8192) == OK and h.fake_fp8_weights() == n + 1
     assert decode(h, 64, 39 * 128, 8192) == OK and h.fake_fp8_weights() == n + 2
