@@ -9,11 +9,15 @@
 // ever widened. What they meet has more bits than a code: it comes in pieces. A number y, |y| <= 256, is c0 + c1 / 32 + c2 / 1024 + ..,
 // each c the e4m3 number next to 32 times what the pieces before left. A code has four bits: what it leaves of a y in [2^e, 2^(e+1)) is at
 // most 2^(e-4), so that four pieces hold a q row to 2^-19 of its largest channel (scores that weights come from: fp32 would be
-// 2^-24), and two hold a softmax weight to 2^-9 of itself down to 2^-14 of the tile's largest, and to 2^-23 of that below (the output
-// is bf16, 2^-8). Products of codes are exact, sums are in fp32, and
-// pieces are columns that the MMA has to spare: 8 heads in 4 pieces are N = 32 (up to 64 columns an MMA takes the same 46 cycles).
+// 2^-24). A softmax weight has three, c0 + (c1 + c2) / 32, the last of which is the e4m3 number next to what c1 leaves as it is: a weight is held
+// to 2^-14 of itself down to 2^-9 of the tile's largest, and to 2^-23 of that below. (With two, 2^-9 of itself, the
+// bf16 output's error was 1.71e-3 of it, not 1.66e-3, and outputs that cancel were off by up to 2^-10 of what they come from.) Products of
+// codes are exact, sums are in fp32, and pieces are columns that the MMA has to spare: 8 heads in 4 pieces are N = 32 (up to 64
+// columns an MMA takes the same 46 cycles).
 //   S^T  = K Q^T    M = 128 keys, N = 32 (half of the heads, piece, head), K = 128 channels; A = the K tile (K-major)
-//   O^T  = V^T P^T  M = 128 channels, N = 16 (piece, head), K = 128 keys; A = the V tile (MN-major)
+//   O^T  = V^T P^T  M = 128 channels, N = 32 (c0, c1, zeros, c2 by head), K = 128 keys; A = the V tile (MN-major). Where weights
+//                   are formed (below), which takes the columns, N = 16: c0 and c1, then zeros and c2 into the same ones (a second set of
+//                   MMAs, 2 us of 123 for 64 layers at pos 4700)
 // Each tile's weights are taken relative to its own largest score, and its O^T is read out and added, times its share and V's scale, in
 // fp32: whatever scales and maxima the other tiles have, none of it is rounded away.
 //
@@ -43,9 +47,10 @@ constexpr int kGroup = 128;  // threads of either set of softmax warps, and of t
 constexpr int kOutWarp = 8;  // the first of the output warps
 constexpr int kKRing = 4, kVRing = 8;
 constexpr uint32_t kTileBytes = kKeyTile * kD;      // a K or a V tile: 128 rows of 128 bytes, 128-byte swizzle
-constexpr int kCols = 32, kOutCols = 16;            // N of the two products
+constexpr int kCols = 32;                           // N of the first product
 constexpr uint32_t kOpBytes = kCols * 128;          // Q: 32 rows of 128 bytes
-constexpr uint32_t kPBytes = kOutCols * 128;        // P: 16
+constexpr uint32_t kPiece = kRepText * 128;         // a piece of P: a row for each head
+constexpr uint32_t kPBytes = 4 * kPiece;            // P: c0, c1, zeros, c2
 constexpr int kMaxParts = 160;                      // parts of one unit (at most one per CTA)
 constexpr int kMergeBatch = 4;
 constexpr int kWeigh = 4;  // tiles whose weights the output warps form at a time
@@ -78,7 +83,7 @@ constexpr uint32_t SM_TODO = SM_MERGE + 4;  // [2]: merged units whose weights a
 constexpr uint32_t SM_LASTPART = SM_TODO + 8;  // whether the other part of the unit that the last segment begins is there already
 constexpr uint32_t kSmemBytes = SM_LASTPART + 4 + 1024;  // + base alignment
 static_assert(kSmemBytes <= 232448, "shared memory budget of one sm_103 CTA");
-// 4 and 2 buffers of 32 and 16 columns; then the scores of kKept tiles, 8 columns each
+// 4 and 2 buffers of 32 columns (O: 16 in kForm); there, then, the scores of kKept tiles, 8 columns each
 constexpr uint32_t kTmemCols = 512, TM_S = 0, TM_O = 128, TM_X = 160, kKept = (kTmemCols - TM_X) / 8;
 // (kForm) Tile n's scores take the place of tile n - kKept's. Who writes them knows that output warps have read out O of tile n - 4, and have so
 // formed the weights that go with tile n - 5's. They form those of tiles 4 k .. 4 k + 3 of a unit of T tiles beside tile T + k, both counted from
@@ -103,6 +108,7 @@ __device__ __forceinline__ bool next_seg(long long& t, long long end, int T, Seg
 // What becomes of the weights: none is asked for; scores go to the workspace, for a second kernel; or this one forms them, of whole units
 // from scores that it keeps in tensor memory.
 constexpr int kNoWeights = 0, kScores = 1, kForm = 2;
+constexpr int out_cols(int mode) { return mode == kForm ? 16 : 32; }  // N of the second product
 // Whether the CTA whose segment s is keeps its unit's scores (kForm).
 template <class P>
 __device__ __forceinline__ bool kept_unit(const P& p, const Seg& s) {
@@ -174,13 +180,13 @@ __device__ __forceinline__ void tmem_landed16(uint32_t (&r)[16]) {
                : "memory");
 }
 
-// Two numbers' next piece: the pair of codes, and 32 times what it leaves.
-__device__ __forceinline__ uint32_t take_piece(float& a, float& b) {
+// Two numbers' next piece: the pair of codes, and what it leaves, times `finer`.
+__device__ __forceinline__ uint32_t take_piece(float& a, float& b, float finer = 32.0f) {
   uint16_t c;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(c) : "f"(a), "f"(b));
   const float2 f = unpack_f16x2(cvt_f16x2_e4m3x2(c));
-  a = (a - f.x) * 32.0f;
-  b = (b - f.y) * 32.0f;
+  a = (a - f.x) * finer;
+  b = (b - f.y) * finer;
   return c;
 }
 
@@ -428,8 +434,9 @@ __device__ __forceinline__ bool qk_issuer(const F8DecodeParams<CAP>& p, uint32_t
 }
 
 // PV(n) needs its tile, P(n), and O buffer n % 2 read out by the output warps.
-template <int CAP>
+template <int kMode, int CAP>
 __device__ __forceinline__ bool pv_issuer(const F8DecodeParams<CAP>& p, uint32_t sbase, uint32_t tmem, uint32_t total) {
+  constexpr int kOutCols = out_cols(kMode), kSteps = 4 * 32 / kOutCols;
   constexpr uint32_t kIdesc = umma_idesc_f16(128, kOutCols, false, true, false);  // A = V MN-major, B = P K-major
   const uint32_t bar0 = sbase + SM_BAR;
   const uint64_t vd = sw128_desc(sbase + SM_V, kTileBytes, 1024), pd = sw128_desc(sbase + SM_PT, 16, 1024);
@@ -445,7 +452,8 @@ __device__ __forceinline__ bool pv_issuer(const F8DecodeParams<CAP>& p, uint32_t
     const uint32_t d = tmem + TM_O + (n & 1) * kOutCols;
     if (elect_one()) {
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) umma_f8_ss(d, v0 + kk * (32 * 128 >> 4), p0 + 2 * kk, kIdesc, kk > 0);  // 32 keys per step
+      for (int kk = 0; kk < kSteps; ++kk)  // 32 keys per step
+        umma_f8_ss(d, v0 + (kk & 3) * (32 * 128 >> 4), p0 + (kk >> 2) * (2 * kPiece >> 4) + 2 * (kk & 3), kIdesc, kk > 0);
       umma_commit(bar0 + 8 * (B_ODONE + (n & 1)));
       umma_commit(bar0 + 8 * (B_VEMPTY + n % kVRing));
     }
@@ -486,7 +494,7 @@ __device__ __forceinline__ bool softmax(const F8DecodeParams<CAP>& p, uint32_t s
   const uint32_t bar0 = sbase + SM_BAR, id = 1 + set;
   const uint32_t s_cols = tmem + (static_cast<uint32_t>(warp * 32) << 16) + TM_S + set * 16;
   float* red = reinterpret_cast<float*>(smem + SM_RED) + set * 4 * H;  // [2][8 warps][4]
-  // P^T row piece * 8 + head, column tid: 16-byte chunk c of row r at chunk c ^ (r % 8)
+  // P^T row 8 piece + head (c2: 24 + head), column tid: 16-byte chunk c of row r at chunk c ^ (r % 8)
   uint32_t at[H];
 #pragma unroll
   for (int h = 0; h < H; ++h) at[h] = sbase + SM_PT + (4 * set + h) * 128 + (((tid >> 4) ^ (4 * set + h)) << 4) + (tid & 15);
@@ -549,7 +557,7 @@ __device__ __forceinline__ bool softmax(const F8DecodeParams<CAP>& p, uint32_t s
       const float4 ra = r4[0], rb = r4[1], rc = r4[2], rd = r4[3];
       const float m[H] = {fmaxf(fmaxf(ra.x, rb.x), fmaxf(rc.x, rd.x)), fmaxf(fmaxf(ra.y, rb.y), fmaxf(rc.y, rd.y)),
                           fmaxf(fmaxf(ra.z, rb.z), fmaxf(rc.z, rd.z)), fmaxf(fmaxf(ra.w, rb.w), fmaxf(rc.w, rd.w))};
-      // weights relative to the tile's largest, times 256, in two pieces
+      // weights relative to the tile's largest, times 256, in three pieces
       const uint32_t buf = (n & 1) * kPBytes;
       float y[H];
       float2 fac[H];  // (what the sums before are multiplied by, the tile's share)
@@ -563,12 +571,12 @@ __device__ __forceinline__ bool softmax(const F8DecodeParams<CAP>& p, uint32_t s
         lsum[h] = fmaf(lsum[h], fac[h].x, x[h] * fac[h].y);
       }
 #pragma unroll
-      for (int piece = 0; piece < 2; ++piece)
+      for (int piece = 0; piece < 3; ++piece)
 #pragma unroll
         for (int h = 0; h < H; h += 2) {
-          const uint32_t c = take_piece(y[h], y[h + 1]);
-          st_shared_u8(at[h] + buf + piece * kRepText * 128, c);
-          st_shared_u8(at[h + 1] + buf + piece * kRepText * 128, c >> 8);
+          const uint32_t c = take_piece(y[h], y[h + 1], piece == 0 ? 32.0f : 1.0f), to = buf + (piece < 2 ? piece : 3) * kPiece;
+          st_shared_u8(at[h] + to, c);
+          st_shared_u8(at[h + 1] + to, c >> 8);
         }
       if (tid == 0) {
         float4* to = reinterpret_cast<float4*>(smem + SM_FAC) + ((n & 3) * kRepText + set * H) / 2;
@@ -808,12 +816,19 @@ __device__ __forceinline__ bool output_segments(const F8DecodeParams<CAP>& p, ui
         v_scale = reinterpret_cast<const float*>(smem + SM_TAILS)[kTails + tails];
       }
       tc_fence_after();
-      uint32_t d[16];  // O^T row = channel tid, columns (piece, head)
-      tmem_ld16(o_cols + (n & 1) * kOutCols, d);
+      uint32_t d[16], d2[8];  // O^T row = channel tid, columns (piece, head)
+      tmem_ld16(o_cols + (n & 1) * out_cols(kMode), d);
+      if (kMode != kForm) tmem_ld8(o_cols + (n & 1) * out_cols(kMode) + 24, d2);
       const float4* fac = reinterpret_cast<const float4*>(smem + SM_FAC) + (n & 3) * (kRepText / 2);
       const float4 f[4] = {fac[0], fac[1], fac[2], fac[3]};
       const float vf = v_scale * 0x1p-8f;
       tmem_landed16(d);
+      if (kMode != kForm)
+#pragma unroll
+        for (int h = 0; h < kRepText; ++h) {
+          asm volatile("" : "+r"(d2[h])::"memory");  // (not before the wait)
+          d[8 + h] = __float_as_uint(__uint_as_float(d[8 + h]) + __uint_as_float(d2[h]));
+        }
       tc_fence_before();
       if (__builtin_expect(!bar_sync_and(3, kGroup, ok), 0)) return false;
       if (tid == 0) mbar_arrive(bar0 + 8 * (B_OFREE + (n & 1)));
@@ -942,6 +957,8 @@ __global__ void __launch_bounds__(f8d::kThreads, 1) fp8_decode_kernel(const __gr
   }
   if (threadIdx.x < 3) reinterpret_cast<int*>(smem + SM_TODO)[threadIdx.x] = threadIdx.x < 2 ? -1 : 0;  // (and SM_LASTPART)
   if (threadIdx.x < kD / 2) reinterpret_cast<float4*>(smem + SM_ROT)[threadIdx.x] = p.rot[threadIdx.x];
+  if (threadIdx.x < 128)  // P's rows of zeros, of both buffers
+    reinterpret_cast<uint4*>(smem + SM_PT + (threadIdx.x >> 6) * kPBytes + 2 * kPiece)[threadIdx.x & 63] = make_uint4(0u, 0u, 0u, 0u);
   if (warp == 0) {
     tmem_alloc(sbase + SM_TMEM, kTmemCols);
     tmem_relinquish();
@@ -976,7 +993,7 @@ __global__ void __launch_bounds__(f8d::kThreads, 1) fp8_decode_kernel(const __gr
   } else if (warp == 13) {
     ok = qk_issuer(p, sbase, tmem, start, end);
   } else if (warp == 14) {
-    ok = pv_issuer(p, sbase, tmem, static_cast<uint32_t>(end - start));
+    ok = pv_issuer<kMode>(p, sbase, tmem, static_cast<uint32_t>(end - start));
   } else if (warp >= kOutWarp && warp < kOutWarp + 4) {
     ok = output<kMode>(p, sbase, smem, tmem, start, end);
   } else if (warp < kOutWarp) {

@@ -437,7 +437,7 @@ int expert_attn_read_fp8(const ea_fp8_rows* layers, int n_layers, int row0, int 
  * expert_attn_write_fp8 (so earlier rows of its block can be rounded again), and every query head attends to the values
  * that rows [0, pos] then have. Rows after pos are never used and stay as they are. q_raw bf16 [64][128], k_raw and v_raw
  * bf16 [8][128], gains bf16 [128], out bf16 [64][128]; k_new and v_new, if not NULL, bf16 [8][128], receive the new row's
- * values. q rows are held to 2^-19 of their largest channel, K and V as stored, softmax weights to 2^-9 of themselves down to 2^-14 of
+ * values. q rows are held to 2^-19 of their largest channel, K and V as stored, softmax weights to 2^-14 of themselves down to 2^-9 of
  * the largest among their row's block of 128, and to 2^-23 of that below; q_raw's and k_raw's
  * squares are summed in fp32 (values below 2^60).
  * weight_out, if not NULL (layer by layer): fp32 [8][Smax]; element (g, r), r < pos, becomes weight_in's (0 if weight_in is NULL) plus the
