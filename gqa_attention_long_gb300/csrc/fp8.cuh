@@ -125,6 +125,17 @@ __device__ __forceinline__ void f8_norm_rope_pair(const float (&x)[4], const flo
   }
 }
 
+// Sums of weights (at most one each, of up to 2^22 rows) times V, codes of at most 448 under scales of up to 2^94, stay under 2^125. V under a larger
+// scale is counted times a power of two, `down`, which brings it there; sums that were formed under another one are multiplied by what it
+// changed by. At the end the weights' sum is multiplied by it, too, and their reference raised by as much: the sums then stand to each other as they should.
+constexpr float kF8TopSum = 0x1p94f;
+__device__ __forceinline__ float f8_lower(float scale) {  // scale > kF8TopSum: 2^93 over its power of two
+  return f8_pow2(93 + 127 - static_cast<int>(__float_as_uint(scale) >> 23));
+}
+__device__ __forceinline__ float2 f8_lowered(float2 ml, float down) {
+  return make_float2(ml.x + static_cast<float>(127 - static_cast<int>(__float_as_uint(down) >> 23)), ml.y * down);
+}
+
 // The sum of a key's eight softmax weights, from its scores and the log2-sum-exps.
 __device__ __forceinline__ float f8_weight(const float4& a, const float4& b, const float4& la, const float4& lb) {
   return ((ex2_approx(a.x - la.x) + ex2_approx(a.y - la.y)) + (ex2_approx(a.z - la.z) + ex2_approx(a.w - la.w))) +

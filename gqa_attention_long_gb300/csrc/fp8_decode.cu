@@ -688,10 +688,10 @@ __device__ __noinline__ void merge(const F8DecodeParams<CAP>& p, uint8_t* smem, 
   }
 }
 
-// The same for a unit whose second part is there, the first being the calling thread's sums and `fin`. (The roundings are merge()'s, so that
+// The same for a unit whose second part is there, the first being the calling thread's sums, `fin` and `down`. (The roundings are merge()'s, so that
 // results do not depend on when the other part came.)
 template <int CAP>
-__device__ __noinline__ void merge_two(const F8DecodeParams<CAP>& p, uint8_t* smem, int u, const float2* fin, float a0, float a1, float a2, float a3, float a4,
+__device__ __noinline__ void merge_two(const F8DecodeParams<CAP>& p, uint8_t* smem, int u, const float2* fin, float down, float a0, float a1, float a2, float a3, float a4,
                                        float a5, float a6, float a7) {
   const int tid = threadIdx.x - kOutWarp * 32;
   const size_t ps = static_cast<size_t>(blockIdx.x + 1) * 2;
@@ -703,7 +703,7 @@ __device__ __noinline__ void merge_two(const F8DecodeParams<CAP>& p, uint8_t* sm
   __nv_bfloat16* out = L.out + static_cast<size_t>(kRepText * (u % kHkv)) * kD + tid;
 #pragma unroll
   for (int h = 0; h < kRepText; ++h) {
-    const float2 a = fin[h], b = h & 1 ? make_float2(m[h / 2].z, m[h / 2].w) : make_float2(m[h / 2].x, m[h / 2].y);
+    const float2 a = f8_lowered(fin[h], down), b = h & 1 ? make_float2(m[h / 2].z, m[h / 2].w) : make_float2(m[h / 2].x, m[h / 2].y);
     const float M = fmaxf(a.x, b.x), wa = ex2_approx(a.x - M), wb = ex2_approx(b.x - M);
     const float sum = __fadd_rn(__fmul_rn(a.y, wa), __fmul_rn(b.y, wb)), inv = 1.0f / sum;
     out[h * kD] = __float2bfloat16_rn(fmaf(wb * inv, other[h], __fmul_rn(wa * inv, acc[h])));
@@ -803,7 +803,7 @@ __device__ __forceinline__ bool output_segments(const F8DecodeParams<CAP>& p, ui
     float v_next = s.j0 < last ? vs[s.j0] : 0.f;
     if (kMode == kForm && tid == 0 && s.j0 == 0 && L.w_out != nullptr && L.w_in != nullptr)  // they are needed soon
       prefetch_l2_bulk(L.w_in + static_cast<size_t>(g) * p.Smax, p.T * kKeyTile * 4);
-    float acc[kRepText];
+    float acc[kRepText], down = 1.0f;  // (down: see f8_lower)
 #pragma unroll
     for (int h = 0; h < kRepText; ++h) acc[h] = 0.f;
 #pragma unroll 1
@@ -821,7 +821,13 @@ __device__ __forceinline__ bool output_segments(const F8DecodeParams<CAP>& p, ui
       if (kMode != kForm) tmem_ld8(o_cols + (n & 1) * out_cols(kMode) + 24, d2);
       const float4* fac = reinterpret_cast<const float4*>(smem + SM_FAC) + (n & 3) * (kRepText / 2);
       const float4 f[4] = {fac[0], fac[1], fac[2], fac[3]};
-      const float vf = v_scale * 0x1p-8f;
+      if (__builtin_expect(v_scale * down > kF8TopSum, 0)) {
+        const float less = f8_lower(v_scale * down);
+        down *= less;
+#pragma unroll
+        for (int h = 0; h < kRepText; ++h) acc[h] *= less;
+      }
+      const float vf = v_scale * down * 0x1p-8f;
       tmem_landed16(d);
       if (kMode != kForm)
 #pragma unroll
@@ -846,7 +852,7 @@ __device__ __forceinline__ bool output_segments(const F8DecodeParams<CAP>& p, ui
     if (s.j0 == 0 && s.j1 == p.T) {
       __nv_bfloat16* o = L.out + static_cast<size_t>(kRepText * g) * kD + tid;
 #pragma unroll
-      for (int h = 0; h < kRepText; ++h) o[h * kD] = __float2bfloat16_rn(__fdividef(acc[h], fin[h].y));
+      for (int h = 0; h < kRepText; ++h) o[h * kD] = __float2bfloat16_rn(__fdividef(acc[h], fin[h].y * down));
       if (kMode != kNoWeights && L.w_out != nullptr) {
         if (kMode == kScores) {
           if (tid < kRepText) p.lse[s.u * kRepText + tid] = fin[tid].x + log2f(fin[tid].y);
@@ -868,7 +874,7 @@ __device__ __forceinline__ bool output_segments(const F8DecodeParams<CAP>& p, ui
     }
     if (last_part(p, s, seg, t, end) && wait(B_QFULL + (seg & 1), (seg >> 1) & 1) &&
         *reinterpret_cast<volatile uint32_t*>(smem + SM_LASTPART) == 1u) {
-      merge_two(p, smem, s.u, fin, acc[0], acc[1], acc[2], acc[3], acc[4], acc[5], acc[6], acc[7]);
+      merge_two(p, smem, s.u, fin, down, acc[0], acc[1], acc[2], acc[3], acc[4], acc[5], acc[6], acc[7]);
       if (late < 0) return true;
       s.u = late;  // (nothing more to count)
       break;
@@ -878,7 +884,7 @@ __device__ __forceinline__ bool output_segments(const F8DecodeParams<CAP>& p, ui
     float4* po = reinterpret_cast<float4*>(p.part_o + ps * kRepText * kD) + 2 * tid;
     po[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
     po[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-    if (tid < kRepText) *reinterpret_cast<float2*>(p.part_ml + (ps * kRepText + tid) * 2) = fin[tid];
+    if (tid < kRepText) *reinterpret_cast<float2*>(p.part_ml + (ps * kRepText + tid) * 2) = f8_lowered(fin[tid], down);
     bar_sync(3, kGroup);
     if (t < end) {  // (the first segment)
       late = s.u;

@@ -217,6 +217,7 @@ __global__ void __launch_bounds__(f8s::kThreads, 1) fp8_decode_small_kernel(cons
     }
   const float qf = sm.qf[gk];
   float m_run = -INFINITY, lsum = 0.f;  // head gk
+  float down = 1.0f;                    // see f8_lower
   float o[16][2];                       // head gk, channels 16 (2t) + i and 16 (2t + 1) + i
 #pragma unroll
   for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = 0.f;
@@ -275,7 +276,16 @@ __global__ void __launch_bounds__(f8s::kThreads, 1) fp8_decode_small_kernel(cons
       split_f16(e0, e1, pa[n >> 1][2 * (n & 1)], pa[n >> 1][2 * (n & 1) + 1]);
     }
     lsum = fmaf(lsum, fa, sum * fb);
-    const float fv = fb * vs;
+    if (__builtin_expect(vs * down > kF8TopSum, 0)) {
+      const float less = f8_lower(vs * down);
+      down *= less;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        o[i][0] *= less;
+        o[i][1] *= less;
+      }
+    }
+    const float fv = fb * (vs * down);
 #pragma unroll
     for (int w = 0; w < 4; ++w) {  // channels 16 g + 4 w .. + 3
       float d[4][4];
@@ -312,7 +322,7 @@ __global__ void __launch_bounds__(f8s::kThreads, 1) fp8_decode_small_kernel(cons
   // ---- the CTA's eight warps into one
   lsum += __shfl_xor_sync(0xffffffffu, lsum, 1);
   lsum += __shfl_xor_sync(0xffffffffu, lsum, 2);
-  if (t == 0) sm.ml[warp][gk] = make_float2(m_run, lsum);
+  if (t == 0) sm.ml[warp][gk] = f8_lowered(make_float2(m_run, lsum), down);
 #pragma unroll
   for (int i = 0; i < 16; i += 4) {
     *reinterpret_cast<float4*>(&sm.o[warp][gk][32 * t + i]) = make_float4(o[i][0], o[i + 1][0], o[i + 2][0], o[i + 3][0]);

@@ -439,7 +439,8 @@ int expert_attn_read_fp8(const ea_fp8_rows* layers, int n_layers, int row0, int 
  * bf16 [8][128], gains bf16 [128], out bf16 [64][128]; k_new and v_new, if not NULL, bf16 [8][128], receive the new row's
  * values. q rows are held to 2^-19 of their largest channel, K and V as stored, softmax weights to 2^-14 of themselves down to 2^-9 of
  * the largest among their row's block of 128, and to 2^-23 of that below; q_raw's and k_raw's
- * squares are summed in fp32 (values below 2^60).
+ * squares are summed in fp32 (values below 2^60), and
+ * scores have to be finite in fp32. V's sums are not limited so: out is finite wherever the weighted mean of V is.
  * weight_out, if not NULL (layer by layer): fp32 [8][Smax]; element (g, r), r < pos, becomes weight_in's (0 if weight_in is NULL) plus the
  * softmax weights of row r summed over the 8 query heads of KV head g, and element (g, pos) those of row pos alone; later
  * elements stay as they are. weight_in may be weight_out; otherwise it must not overlap what the call writes, nor stand twice in it. Both
