@@ -297,12 +297,16 @@ int validate_evict(const ea_evict_fp8_args* a, int n_layers, int n_rows, int n_k
         partly(x.v_scale, x.v_scale_dst, scales) || partly(x.weight, x.weight_dst, sums))
       return EA_ERR_INVALID_ARG;
   }
-  return mx_distinct<11>(a, n_layers, [](const ea_evict_fp8_args& x) {
-           const bool other = x.k_cache != x.k_dst;
-           auto src = [&](const void* q) { return other ? q : nullptr; };
-           return std::array<const void*, 11>{x.k_dst, x.v_dst, x.k_scale_dst, x.v_scale_dst, x.weight_dst, x.kept, src(x.k_cache),
-                                              src(x.v_cache), src(x.k_scale), src(x.v_scale), src(x.weight)};
-         })
+  return mx_distinct<6>(
+             a, n_layers,
+             [](const ea_evict_fp8_args& x) {
+               return std::array<const void*, 6>{x.k_dst, x.v_dst, x.k_scale_dst, x.v_scale_dst, x.weight_dst, x.kept};
+             },
+             [](const ea_evict_fp8_args& x) {  // (in place they are what is written)
+               const bool other = x.k_cache != x.k_dst;
+               auto src = [&](const void* q) { return other ? q : nullptr; };
+               return std::array<const void*, 5>{src(x.k_cache), src(x.v_cache), src(x.k_scale), src(x.v_scale), src(x.weight)};
+             })
              ? EA_OK
              : EA_ERR_INVALID_ARG;
 }

@@ -7,6 +7,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <array>
 #include <cmath>
 #include <mutex>
 
@@ -46,10 +47,17 @@ cudaLaunchConfig_t launch_config(cudaStream_t st, cudaLaunchAttribute* attr, boo
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Whether the arrays that one call writes, get(a[l])[0 .. N) of every layer, are all different: what stands twice
-// would be written twice, in any order. Null entries (outputs that are not asked for) are passed over.
-template <int N, class A, class Get>
-bool mx_distinct(const A* a, int n, Get get) {
+struct MxNone {
+  template <class A>
+  std::array<const void*, 0> operator()(const A&) const {
+    return {};
+  }
+};
+// Whether the arrays that one call writes, writes(a[l])[0 .. N) of every layer, are all different (what stands twice
+// would be written twice, in any order), and none of those that it only reads, reads(a[l]), is among them (which may stand in several
+// layers). Null entries (outputs that are not asked for) are passed over.
+template <int N, class A, class Writes, class Reads = MxNone>
+bool mx_distinct(const A* a, int n, Writes writes, Reads reads = {}) {
   constexpr int kBits = N <= 4 ? 9 : N <= 8 ? 10 : 11;
   constexpr uint32_t kSlots = 1u << kBits;
   static_assert(N * kMaxLayersPerLaunch <= kSlots / 2, "table");
@@ -62,12 +70,15 @@ bool mx_distinct(const A* a, int n, Get get) {
     };
     const int l1 = l0 + kMaxLayersPerLaunch < n ? l0 + kMaxLayersPerLaunch : n;
     for (int l = l0; l < n; ++l)  // 64 layers into the table, the later ones against it
-      for (const void* p : get(a[l])) {
+      for (const void* p : writes(a[l])) {
         if (p == nullptr) continue;
         const uint32_t h = find(p);
         if (seen[h] != nullptr) return false;
         if (l < l1) seen[h] = p;
       }
+    for (int l = 0; l < n; ++l)
+      for (const void* p : reads(a[l]))
+        if (p != nullptr && seen[find(p)] != nullptr) return false;
   }
   return true;
 }

@@ -476,7 +476,8 @@ int text_decode_attention_fp8(const ea_decode_fp8_args* layers, int n_layers, in
  * scale s' is rounded again: the fp32 product code * (s' / s) to nearest. What lies behind row n_keep in the destination, its scales
  * and weights among it, stays as it was. Heads choose for themselves, so that after a call row r of two heads can be different
  * tokens: keys keep the rotation of their own position, and later calls give the next token's position as pos + rope_delta.
- * In place (every destination is its source), or into other arrays (none is, nor overlaps one).
+ * In place (every destination is its source), or into other arrays (none is, nor overlaps one; sources that are not written may stand in
+ * several layers).
  * 0 <= n_first, 0 <= n_recent, n_first + n_recent <= n_keep <= n_rows <= Smax. Two launches per 64 layers. */
 typedef struct {
   const void* k_cache;
