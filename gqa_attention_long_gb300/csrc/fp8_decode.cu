@@ -264,7 +264,7 @@ __device__ __noinline__ void prepare_q(const F8DecodeParams<CAP>& p, uint32_t sb
     const int e = f16_exponent(f8_row_max(y));  // the row's largest magnitude is in [2^e, 2^(e + 1)): put it in [128, 256)
     const float up = f8_pow2(min(7 - e, 126));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] *= up;
+    for (int i = 0; i < 4; ++i) y[i] = fmaf(y[i], up, y[i] * 0.0f);  // (an infinity is NaN: as codes it would saturate)
     if (lane == 0) reinterpret_cast<float*>(smem + SM_QF)[(seg & 7) * kRepText + h] = p.scale_log2 * f8_pow2(max(e - 7, -126));  // over up
     // 16-byte chunk c of row r at chunk c ^ (r % 8)
     const uint32_t r0 = (h >> 2) * 16 + (h & 3), c = lane >> 3;
