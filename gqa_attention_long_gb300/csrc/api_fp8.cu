@@ -149,8 +149,14 @@ F8AttnLayer attn_layer(const ea_decode_fp8_args& x) {
 int decode_ctas(int sm_count) { return sm_count < kMaxGridCtas ? sm_count : kMaxGridCtas; }
 
 // Whether fp8_decode_kernel forms the weights itself: units of at most kF8KeptTiles tiles, and one and a half of them to a CTA, so
-// that most are whole ones. With the second kernel and without it: 64 layers at pos 4700 132.5 and 120.3 us, at pos 2500 79.0 and 73.6, 32 layers at
-// pos 4900 (1.7 units) 76.3 and 74.0; 16 layers at pos 4700 (0.8) 44.2 and 47.0.
+// that most are whole ones. us a call:
+//   layers x pos (units to a CTA)   second kernel   without it
+//   64 x 4700 (3.4)                 133.6           122.5
+//   64 x 2500 (3.4)                  79.8            74.8
+//   32 x 4900 (1.7)                  78.6            76.0
+//   29 x 4000 (1.5)                  63.3            61.6
+//   24 x 4700 (1.3)                  60.0            60.0
+//   16 x 4700 (0.8)                  45.3            47.3
 bool forms_weights(int n, int pos, int sm_count) {
   return n > kSmallCap && pos / kKeyTile + 1 <= kF8KeptTiles && 2 * n * kHkv >= 3 * decode_ctas(sm_count);
 }
@@ -198,20 +204,31 @@ int launch_decode_t(const ea_decode_fp8_args* a, int n, int pos, int Smax, long 
   return EA_OK;
 }
 
-// Little work (see fp8_decode_small.cu): its kernel's CTAs, of `tiles` key tiles each, come in `waves` of one to an SM, and the start and the end of one
-// are about four tiles' time: waves x (kSmallEnds + tiles) <= kSmallWork + waves / 2 (more units take the other
-// kernel longer, too). Its kernel and the other one: 1 layer at pos 300 (1 x (4 + 2)) 6.8 and 10.4 us, at pos
-// 4700 (1 x 6) 9.1 and 13.4; 16 layers at pos 1000 (1 x 12) 13.3 and 18.1, at pos 1500 (1 x 16) 18.0 and 19.1; 5 layers at pos 4700 (1 x 17) 20.1 and 19.7;
-// 32 layers at pos 600 (2 x 9) 21.7 and 22.7; 12 layers at pos 2000 (1 x 20) 21.4 and 18.8; 32 layers at pos 800 (2 x 11) 25.1 and 23.4, 64 layers at pos
-// 100 (4 x 5) 21.1 and 22.5, at pos 380 (4 x 7) 34.3 and 27.3. Up to kOnePart tiles a unit is one CTA's (4 layers at pos 300, three tiles: 7.6 us whole, 7.0 in two parts). Up
-// to kSmallCluster parts are a cluster (1 layer at pos 1000: 7.6 us, 7.9 through global memory; in clusters of eight 2 layers at pos 2000 wait for
-// as many free SMs beside one another: 14.9 us, and 8.1). Clusters of three and four do not fill every SM: 6 layers at pos 600 in 48 clusters of
-// three took 13.4 us, 7 layers in pairs 9.3; from seven eighths of the SMs on they are pairs.
-constexpr int kSmallEnds = 4, kSmallWork = 18, kOnePart = 2, kSmallParts = 32, kSmallCluster = 4;
+// Little work (see fp8_decode_small.cu): its kernel's CTAs, of `tiles` key tiles each, come in `waves` of one to an SM, and the start and
+// the end of one are about four tiles' time: waves x (kSmallEnds + tiles) <= kSmallWork + waves / 2 (more units take the other
+// kernel longer, too). us a call:
+//   layers x pos (waves x (4 + tiles))   its kernel   the other one
+//    1 x  300 (1 x  6)                    6.8         10.5
+//    1 x 4700 (1 x  6)                    9.2         13.6
+//   16 x 1000 (1 x 12)                   13.2         18.2
+//   16 x 1500 (1 x 16)                   18.0         19.2
+//    5 x 4700 (1 x 17)                   20.4         20.1
+//   12 x 2000 (1 x 20)                   21.5         19.1
+//   32 x  600 (2 x  9)                   21.7         23.4
+//   32 x  800 (2 x 11)                   25.2         24.0
+//   64 x  100 (4 x  5)                   21.8         22.9
+//   64 x  380 (4 x  7)                   33.7         28.3
+// Up to kOnePart tiles a unit is one CTA's (4 layers at pos 300, three tiles: 7.6 us whole, 7.0 in two parts). Up to kF8SmallCluster
+// parts are a cluster (1 layer at pos 1000: 7.6 us, 7.9 through global memory; in clusters of eight 2 layers at pos 2000 wait for as
+// many free SMs beside one another: 14.9 us, and 8.1). Clusters of three and four do not fill every SM: 6 layers at pos 600 in 48
+// clusters of three took 13.4 us, and 9.1 in pairs; from seven eighths of the SMs on they are pairs.
+constexpr int kSmallEnds = 4, kSmallWork = 18, kOnePart = 2;
+static_assert(kSmallWork - kSmallEnds <= kF8SmallTiles, "a CTA's tiles: as many in one wave, fewer in more");
 
-// Whether fp8_decode_small_kernel forms the weights itself: where a unit's CTAs can tell each other its log2-sum-exps. With a second kernel and without:
-// 1 layer at pos 1000 9.1 and 8.1 us, 4 layers at pos 4700 19.9 and 17.9, 8 layers at pos 1000 11.8 and 10.3, 32 layers at pos 500 21.7 and 19.2.
-bool small_forms(int parts, int T) { return parts <= kSmallCluster && (T + parts - 1) / parts <= kF8SmallKept; }
+// Whether fp8_decode_small_kernel forms the weights itself: where a unit's CTAs can tell each other its log2-sum-exps. With a second
+// kernel and without: 1 layer at pos 1000 9.1 and 8.1 us, 4 layers at pos 4700 19.9 and 17.9, 8 layers at pos 1000 11.8 and 10.3, 32 layers
+// at pos 500 21.7 and 19.2.
+bool small_forms(int parts) { return parts <= kF8SmallCluster; }
 
 template <int CAP>
 int launch_small(const ea_decode_fp8_args* a, int n, int pos, int Smax, long long p0, bool weights, uint8_t* ws, const F8DecodeWs& wl,
@@ -226,8 +243,8 @@ int launch_small(const ea_decode_fp8_args* a, int n, int pos, int Smax, long lon
   p.lse = reinterpret_cast<float*>(ws + wl.lse_off);
   p.T = pos / kKeyTile + 1;
   p.parts = parts;
-  p.cluster = parts > 1 && parts <= kSmallCluster;
-  p.form = weights && small_forms(parts, p.T);
+  p.cluster = parts > 1 && parts <= kF8SmallCluster;
+  p.form = weights && small_forms(parts);
   p.pos = pos;
   p.Smax = Smax;
   p.n_layers = n;
@@ -263,8 +280,8 @@ int small_parts(int n, int pos, int sm_count) {
   const int T = pos / kKeyTile + 1, units = n * kHkv;
   int parts = sm_count / units;
   if (parts > (T + 1) / 2) parts = (T + 1) / 2;  // (two tiles keep a CTA's eight warps busy)
-  if (parts > kSmallParts) parts = kSmallParts;
-  if (parts > 2 && parts <= kSmallCluster && units * parts > sm_count / 8 * 7) parts = 2;
+  if (parts > kF8SmallParts) parts = kF8SmallParts;
+  if (parts > 2 && parts <= kF8SmallCluster && units * parts > sm_count / 8 * 7) parts = 2;
   if (parts < 1 || T <= kOnePart) parts = 1;
   const int waves = (units * parts + sm_count - 1) / sm_count, tiles = (T + parts - 1) / parts;
   return static_cast<long long>(waves) * (kSmallEnds + tiles) <= kSmallWork + waves / 2 ? parts : 0;
@@ -353,7 +370,7 @@ int text_decode_attention_fp8(const ea_decode_fp8_args* layers, int n_layers, in
          : parts > 0 ? launch_small<kDecodeMaxLayers>(layers + l0, n, pos, Smax, p0, weights, ws, wl, parts, st)
          : n <= kSmallCap ? launch_decode_t<kSmallCap>(layers + l0, n, pos, Smax, p0, weights, ws, wl, di.sm_count, st)
                           : launch_decode_t<kDecodeMaxLayers>(layers + l0, n, pos, Smax, p0, weights, ws, wl, di.sm_count, st);
-    const bool formed = parts > 0 ? small_forms(parts, pos / kKeyTile + 1) : forms_weights(n, pos, di.sm_count);
+    const bool formed = parts > 0 ? small_forms(parts) : forms_weights(n, pos, di.sm_count);
     if (rc == EA_OK && weights && !formed) rc = launch_weights(layers + l0, n, pos, Smax, ws, wl, st);
     if (rc != EA_OK) return rc;
   }

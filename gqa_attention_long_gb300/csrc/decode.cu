@@ -93,13 +93,6 @@ struct Seg {
   int u, j0, j1;  // unit and its key-tile range [j0, j1)
 };
 
-// atomicAdd at GPU scope with acquire-release semantics; returns the old value
-__device__ __forceinline__ uint32_t atom_add_acq_rel_gpu(uint32_t* a, uint32_t v) {
-  uint32_t old;
-  asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;" : "=r"(old) : "l"(a), "r"(v) : "memory");
-  return old;
-}
-
 // Next segment of a CTA's tile range [t, end): unit u = t / T (tile indices stay below 2^31).
 __device__ __forceinline__ bool next_seg(long long& t, long long end, int T, Seg& s) {
   if (t >= end) return false;

@@ -22,7 +22,6 @@ namespace f8s {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kKeys = 32;  // of a warp's chunk
-constexpr int kMaxParts = 32, kMaxCluster = 4;
 
 struct Smem {
   float4 rot[kD / 2];
@@ -48,11 +47,6 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
 }
 __device__ __forceinline__ uint32_t codes_f16(uint32_t w, int half) {
   return cvt_f16x2_e4m3x2(static_cast<uint16_t>(half ? w >> 16 : w));
-}
-__device__ __forceinline__ uint32_t atom_add_acq_rel_gpu(uint32_t* a, uint32_t v) {
-  uint32_t old;
-  asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;" : "=r"(old) : "l"(a), "r"(v) : "memory");
-  return old;
 }
 // Two numbers as f16, and 2^11 times what that leaves.
 __device__ __forceinline__ void split_f16(float a, float b, uint32_t& hi, uint32_t& lo) {
@@ -353,21 +347,21 @@ __global__ void __launch_bounds__(f8s::kThreads, 1) fp8_decode_small_kernel(cons
     if (lane == 0) sm.part_ml[h] = make_float2(M, sum);
     cluster_sync();
     if (part == 0 || form) {
-      float4 v[kMaxCluster];
-      float2 ml[kMaxCluster];
+      float4 v[kF8SmallCluster];
+      float2 ml[kF8SmallCluster];
 #pragma unroll
-      for (int k = 0; k < kMaxCluster; ++k)
+      for (int k = 0; k < kF8SmallCluster; ++k)
         if (k < p.parts) {
           v[k] = part == 0 ? ld_shared_cluster_v4(mapa_shared(smem_u32(&sm.part_o[h][4 * lane]), k)) : make_float4(0.f, 0.f, 0.f, 0.f);
           ml[k] = ld_shared_cluster_v2(mapa_shared(smem_u32(&sm.part_ml[h]), k));
         }
 #pragma unroll
-      for (int k = 0; k < kMaxCluster; ++k)
+      for (int k = 0; k < kF8SmallCluster; ++k)
         if (k < p.parts) M = fmaxf(M, ml[k].x);
       sum = 0.f;
       acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int k = 0; k < kMaxCluster; ++k)
+      for (int k = 0; k < kF8SmallCluster; ++k)
         if (k < p.parts) {
           const float f = ex2_approx(ml[k].x - M);
           sum = fmaf(ml[k].y, f, sum);
@@ -390,7 +384,7 @@ __global__ void __launch_bounds__(f8s::kThreads, 1) fp8_decode_small_kernel(cons
     // every part of head h: a lane weighs one
     const size_t first = static_cast<size_t>(u) * p.parts;
     const float2 ml = lane < p.parts ? __ldcg(reinterpret_cast<const float2*>(p.part_ml) + (first + lane) * kRepText + h) : make_float2(-INFINITY, 0.f);
-    float4 v[kMaxParts / 2];  // half of the parts under way at a time
+    float4 v[kF8SmallParts / 2];  // half of the parts under way at a time
     M = ml.x;
 #pragma unroll
     for (int k = 16; k >= 1; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
@@ -399,12 +393,12 @@ __global__ void __launch_bounds__(f8s::kThreads, 1) fp8_decode_small_kernel(cons
 #pragma unroll
     for (int k = 16; k >= 1; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
     acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = 0; k0 < p.parts; k0 += kMaxParts / 2) {
+    for (int k0 = 0; k0 < p.parts; k0 += kF8SmallParts / 2) {
 #pragma unroll
-      for (int k = 0; k < kMaxParts / 2; ++k)
+      for (int k = 0; k < kF8SmallParts / 2; ++k)
         if (k0 + k < p.parts) v[k] = __ldcg(reinterpret_cast<const float4*>(p.part_o + ((first + k0 + k) * kRepText + h) * kD) + lane);
 #pragma unroll
-      for (int k = 0; k < kMaxParts / 2; ++k) {
+      for (int k = 0; k < kF8SmallParts / 2; ++k) {
         const float w = __shfl_sync(0xffffffffu, f, (k0 + k) & 31);
         if (k0 + k < p.parts) {
           acc.x = fmaf(v[k].x, w, acc.x);
@@ -438,7 +432,7 @@ __global__ void __launch_bounds__(f8s::kThreads, 1) fp8_decode_small_kernel(cons
 }
 
 cudaError_t fp8_decode_small_set_attributes() {
-  const int bytes = static_cast<int>(sizeof(f8s::Smem)), kept = kF8SmallKept * kKeyTile * kRepText * static_cast<int>(sizeof(float));
+  const int bytes = static_cast<int>(sizeof(f8s::Smem)), kept = kF8SmallTiles * kKeyTile * kRepText * static_cast<int>(sizeof(float));
   cudaError_t e = cudaSuccess;
   auto set = [&](auto kernel, int size) {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, size);

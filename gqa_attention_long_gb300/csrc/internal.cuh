@@ -413,8 +413,9 @@ struct F8WeightsParams {
 };
 // Up to so many key tiles to a unit fp8_decode_kernel forms the weights itself.
 constexpr int kF8KeptTiles = 39;
-// So many tiles to a CTA fp8_decode_small_kernel can keep the scores of.
-constexpr int kF8SmallKept = 40;
+// fp8_decode_small_kernel's CTAs: at most so many parts to a unit (a lane of one warp weighs one), of so many tiles (whose scores shared
+// memory can keep); up to kF8SmallCluster parts are a cluster.
+constexpr int kF8SmallParts = 32, kF8SmallCluster = 4, kF8SmallTiles = 14;
 // Workspace: [0, 1024) status word; unit counters and log2-sum-exps of 64 layers, whatever the call's number; partials of at
 // most max_ctas CTAs; scores, for a call that asks for weights.
 struct F8DecodeWs {
