@@ -370,6 +370,8 @@ __global__ void __launch_bounds__(f8s::kThreads, 1) fp8_decode_small_kernel(cons
           acc.z = fmaf(v[k].z, f, acc.z);
           acc.w = fmaf(v[k].w, f, acc.w);
         }
+      // (a store that needs every load's value)
+      *reinterpret_cast<volatile float*>(&sm.o[0][h][lane]) = ((acc.x + acc.y) + (acc.z + acc.w)) + sum;
     }
     cluster_sync_exit();  // no CTA leaves while another one reads its shared memory
     if (part != 0 && !form) return;

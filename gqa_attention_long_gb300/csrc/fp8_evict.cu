@@ -214,6 +214,7 @@ __global__ void __launch_bounds__(kSelThreads, 2048 / kSelThreads) fp8_evict_sel
       above += __float_as_uint(t.x);
       equal += __float_as_uint(t.y);
     }
+    if (lane == 0) *const_cast<volatile uint32_t*>(&sm.scan[warp]) = above + equal;  // (a store that needs every load's value)
     cluster_sync_exit();  // no CTA leaves while another reads its shared memory
   }
   for (int grp = g0; grp < g1; ++grp) {
