@@ -29,14 +29,15 @@
 // was what they waited for most (2.8 of 10 warp cycles an instruction): they are short, and what is rare is out of their way.
 // A unit cut over several CTAs is merged by the part that finishes last; a part that is not its CTA's last segment is counted by warp
 // 15, and merged at the CTA's end should it be the last after all, so that the output warps need not wait. A CTA's last part of a unit of
-// two whose other part has come adds that to its registers' sums: 3 us less at the end than through global memory.
+// two whose other part has come adds that to its registers' sums (64 layers at pos 4700: 1.6 us less than through global memory).
 // Weights that are asked for need a unit's scores once more when its log2-sum-exps are known: 32 bytes a key. They go to the workspace, and
 // a second kernel forms the weights; or, where most units are whole ones of one CTA, these stay in tensor memory, whose columns hold 44 tiles'
-// scores beside the accumulators, and the output warps form their weights between the next unit's tiles (64 layers at pos 4700: 118 us, not
-// 132.5); the cut ones' are formed by the CTA that merges them. What that takes is the loads' latency (sums before come through
+// scores beside the accumulators, and the output warps form their weights between the next unit's tiles (64 layers at pos 4700: 122.5 us, not
+// 133.6); the cut ones' are formed by the CTA that merges them. What that takes is the loads' latency (sums before come through
 // prefetches and asynchronous copies: 10 us less) rather than the arithmetic.
-// Figures (64 layers at pos 4700; 4 layers at pos 131070): 98.2 and 161 us, 93 % and 98 % of the copy's rate; the former's 125 tiles
-// a CTA bear a start and an end of about 6 us.
+// Figures (64 layers at pos 4700; 4 layers at pos 131070): 100.0 and 163 us, 91 % and 97 % of the copy's rate; the former's 125 tiles
+// a CTA bear a start and an end of about 6 us. A unit has a chain of its own (its Q from one warp, its first scores, its end) of about 5 us, which
+// the tiles of short units do not hide: 64 layers at pos 1000 40.1 us, at pos 380 28.1, two and three and a half times their bytes' time.
 #include "fp8.cuh"
 
 namespace ea {
@@ -984,7 +985,7 @@ __global__ void __launch_bounds__(f8d::kThreads, 1) fp8_decode_kernel(const __gr
   }
   // everything below reads what earlier kernels in the stream wrote
   pdl_wait_primary();
-  // (the roles' order is the code's, and matters to the instruction caches: 64 layers at pos 4700 98.2 us in this one, 98.7 to 100.7 in others)
+  // (the roles' order is the code's, and matters to the instruction caches: 64 layers at pos 4700 take up to 2 % longer in others)
   bool ok = true;
   if (warp == 15) {
     ok = prepare(p, sbase, smem, start, end);
